@@ -74,7 +74,9 @@ enum {
 /* device-side error bits (pnb_state_check) */
 enum {
   PNB_DEV_ERR_TOKEN = 1,   /* a token from device memory was out of range; id 0 was used */
-  PNB_DEV_ERR_TIMEOUT = 2  /* a bounded wait inside a kernel expired; results are invalid */
+  PNB_DEV_ERR_TIMEOUT = 2, /* a bounded wait inside a kernel expired; results are invalid */
+  PNB_DEV_ERR_FULL = 4,    /* pnb_kvq_append: rows past the cache's capacity were not stored */
+  PNB_DEV_ERR_RANGE = 8    /* pnb_kvq_append: a start or count from device memory was out of range */
 };
 
 /* Model dimensions: the config fields of the pages ("Engine Architecture",
@@ -411,6 +413,127 @@ int pnb_attention_decode_static(const float *q_dev, const void *k_dev, const voi
                                 int32_t dtype, int32_t n_head, int32_t n_kv_head, int32_t head_dim,
                                 int32_t cap, int32_t window, int32_t pos, float *out_dev,
                                 int32_t *err_dev, pnb_stream stream);
+
+/* ------------------------------------------------------- 4-bit KV cache
+   Decode attention over a KV cache held in GGUF Q4_0 blocks, for callers whose
+   contexts outgrow a bf16 cache: 4.5 bits per value, 144 bytes per position
+   and KV head at head_dim 128 where bf16 takes 512.  No counterpart in the
+   Pantheon pages; it stands beside pnb_attention_decode_static (attention over
+   a caller's cache, one layer per call) and takes K rows after RoPE as every
+   cache of this library does.
+
+   A cache holds n_layer layers of n_slot sequences.  Each K and V row is kept
+   in blocks of 32 consecutive head dimensions, one fp16 scale d and 32 codes
+   u: value = d (u - 8), d = fp16(max|x| / 7), u = clamp(rint(x / d), -8, 7) + 8
+   with correctly rounded quotients and ties to the even integer (the rule of
+   the PNB_Q4_0 weights); d = 0 gives u = 8.  A block with a NaN or an infinity
+   reads as NaN; a scale past 65504 saturates.
+
+   The entries of a slot are indexed 0 .. len - 1.  Beside the codes every
+   layer keeps, in the caller's buffer, each entry's original position (id) and
+   accumulated attention weight per KV head, and per slot its length and the
+   number of tokens ever appended (the next id).  The buffer holds everything
+   that outlives a call: a copy of it is a copy of the cache.
+
+   All calls are stream-ordered and may be captured into a CUDA graph (lengths
+   are read on the device).  The library allocates the cache's workspace in
+   pnb_kvq_new; calls on one cache share it, so at most one may be in flight
+   per cache, on any stream, graphs included.  Errors found on the device
+   (PNB_DEV_ERR_FULL, _RANGE, _TIMEOUT) set bits that pnb_kvq_check reads.
+   A length outside [0, cap] in the buffer is taken as the nearer of the two. */
+typedef struct {
+  int32_t n_layer, n_slot;    /* layers; sequences, at most 1024 */
+  int32_t n_head, n_kv_head;  /* n_head % n_kv_head == 0, at most 64 query heads per KV head */
+  int32_t head_dim;           /* 32, 64 or 128 */
+  int32_t cap;                /* entries per slot, a multiple of 32, at most 2^20 */
+  int32_t track;              /* most tokens per pnb_kvq_attention call that updates the weights (0: none);
+                                 the workspace holds n_slot * n_head * track * cap fp32 scores */
+} pnb_kvq_config;
+typedef struct pnb_kvq pnb_kvq;
+
+/* Rows [slot][token][head][head_dim] of a caller's device tensor, head_dim
+   contiguous, the other strides in elements (so rows may lie inside a fused
+   QKV projection or a state's KV cache).  dtype: PNB_F32 or PNB_BF16.  dev
+   and every stride must keep rows 16-byte aligned (PNB_E_ALIGN); strides are
+   not negative, and rows that a call writes must not overlap (PNB_E_INVAL). */
+typedef struct {
+  const void *dev;
+  int64_t slot, token, head;
+  int32_t dtype;
+} pnb_rows;
+
+/* Bytes of a cache's buffer; 0 for an invalid or unsupported config. */
+size_t pnb_kvq_bytes(const pnb_kvq_config *cfg);
+
+/* Create a cache over a caller-owned buffer (128-byte aligned) on the current
+   device.  The buffer is not touched: pnb_kvq_reset a new one, or attach to
+   one that a cache of the same config has filled. */
+int pnb_kvq_new(const pnb_kvq_config *cfg, void *buf_dev, size_t bytes, pnb_kvq **out);
+void pnb_kvq_free(pnb_kvq *c);
+
+/* Empty one slot, or all (slot = -1, which also clears the error bits), in
+   every layer. */
+int pnb_kvq_reset(pnb_kvq *c, int32_t slot, pnb_stream stream);
+
+/* Quantise and append up to T rows per slot (1 <= T <= cap): n_new_dev[b] of
+   them (device int32 [n_slot], 0 .. T; NULL: all T), from token 0 on, at
+   entries start_dev[b] .. (0 .. len; NULL: at the slot's length).  A start
+   below the length first takes back what lies behind it (rejected draft
+   tokens; not past an eviction, which reorders entries).  New entries get the
+   next ids and weight 0; the slot's length becomes start + n_new.  Rows past
+   the capacity are dropped (PNB_DEV_ERR_FULL); a slot whose start or count is
+   out of range stays as it was (PNB_DEV_ERR_RANGE).  k and v have one dtype. */
+int pnb_kvq_append(pnb_kvq *c, int32_t layer, const pnb_rows *k, const pnb_rows *v, int32_t T,
+                   const int32_t *n_new_dev, const int32_t *start_dev, pnb_stream stream);
+
+/* Write entries first .. first + T - 1 of every slot (first_dev int32
+   [n_slot], NULL: 0) as values to k and v (one dtype; bf16 rounds them).
+   Entries outside [0, len) are written as zero. */
+int pnb_kvq_read(pnb_kvq *c, int32_t layer, const int32_t *first_dev, int32_t T, const pnb_rows *k,
+                 const pnb_rows *v, pnb_stream stream);
+
+/* Attention of T query tokens per slot over the slot's entries: the T tokens
+   are the last T appended (T = 1: decode; T > 1: drafted tokens, or the last
+   rows of a prompt), so query t attends to entries [0, len - T + 1 + t).  A row
+   with nothing to attend to, an empty slot's among them, answers 0.
+     q    [n_slot][T][n_head][head_dim], already rotated
+     out  the same shape: softmax(q.k / sqrt(head_dim)) applied to V
+   T * n_head / n_kv_head <= 64 (PNB_E_UNSUPPORTED).  q and out may differ in
+   dtype; out may be q's own rows when they have the same strides and dtype.
+   fp32 outputs carry about 1e-6 of relative error against exact arithmetic on
+   the held values.
+   decay < 0: the weights stay as they are.  decay >= 0 (finite; T <= track,
+   else PNB_E_INVAL): weights[j] = decay * weights[j] + the sum over the T
+   tokens and the KV head's query heads of the softmax weight of entry j
+   (decay 1 accumulates, 0 keeps this call's weights only, without reading the
+   old ones).  Results do not depend on the run: no atomic sums. */
+int pnb_kvq_attention(pnb_kvq *c, int32_t layer, const pnb_rows *q, int32_t T, const pnb_rows *out,
+                      float decay, pnb_stream stream);
+
+/* Cut every slot that holds more than `budget` entries (1 <= budget <= dst's
+   cap) down to it, per KV head: entries with id < n_sink or among the last
+   n_recent ids stay (n_sink + n_recent <= budget), and of the others those
+   with the largest weights, the lower index first among equals (a NaN weight
+   counts by its sign bit as larger or smaller than every number).  The
+   entries that stay below index `budget` keep their index; those behind move,
+   in order, into the places of the dropped ones.  dst may be another cache or
+   layer of the same n_slot, n_kv_head and head_dim (shorter slots are copied
+   whole, src is not changed), or src itself in place.  src's cap is at most
+   2^18 (PNB_E_UNSUPPORTED). */
+int pnb_kvq_evict(pnb_kvq *src, int32_t src_layer, pnb_kvq *dst, int32_t dst_layer, int32_t budget,
+                  int32_t n_sink, int32_t n_recent, pnb_stream stream);
+
+/* Device pointers of one layer's bookkeeping inside the caller's buffer. */
+typedef struct {
+  int32_t *len, *seen;   /* [n_slot] */
+  int32_t *ids;          /* [n_slot][n_kv_head][cap] */
+  float *weights;        /* [n_slot][n_kv_head][cap] */
+} pnb_kvq_views;
+int pnb_kvq_layer_views(const pnb_kvq *c, int32_t layer, pnb_kvq_views *out);
+
+/* Synchronise and read the cache's device error bits (PNB_DEV_ERR_*); returns
+   PNB_E_DEVICE when any is set. */
+int pnb_kvq_check(pnb_kvq *c, int32_t *device_error);
 
 /* Diagnostics: have the step's kernels record globaltimer stamps (ns) into
    trace_dev, laid out [launch][256][8]: launch = 6 * layer + kernel kind

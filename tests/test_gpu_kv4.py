@@ -1,0 +1,680 @@
+"""The 4-bit KV cache on the GPU against a plain 64-bit implementation.
+
+Values held in the cache, ids, lengths and the eviction's choice must be equal
+to the reference's.  Attention tolerances follow the kernel's roundings:
+
+* a score x = q.k / sqrt(hd) is a sum of hd products whose fp32-side factor
+  keeps 22 bits, accumulated in fp32: |dx| <= A (2^-22 + 16 * 2^-24) with
+  A = sum |q_n k_n| / sqrt(hd);
+* a weight's relative error is then |dx| (natural units) + 2^-21 (exponential),
+  and an output, a weighted mean of values up to |v|, moves by at most twice
+  the largest relative error of a weight times |v|, plus the product's own
+  22-bit factor and fp32 sums (2^-20 |v|);
+* a bf16 output adds its rounding (eps / 2 = 2^-8 of the value) and the single
+  fp16 of its weights (2^-11 |v|).
+"""
+import numpy as np
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():
+    pytest.skip("needs a CUDA GPU", allow_module_level=True)
+
+import transformer_decode_step_gb300 as pnb  # noqa: E402
+
+F32, BF16 = torch.float32, torch.bfloat16
+
+
+def held(x):
+    """What the cache stands for after storing rows x [..., hd], in 64 bits."""
+    x = x.detach().double().cpu().numpy()
+    b = x.reshape(x.shape[:-1] + (-1, 32))
+    top = np.abs(b).max(-1, keepdims=True)
+    with np.errstate(over="ignore", invalid="ignore"):
+        d = np.minimum(top / 7.0, 65504.0).astype(np.float16).astype(np.float64)
+        u = np.clip(np.rint(b / np.where(d == 0, 1.0, d)), -8, 7)
+    y = u * d
+    y[~np.isfinite(top[..., 0])] = np.nan
+    return torch.from_numpy(y.reshape(x.shape)).cuda()
+
+
+class Ref:
+    """A plain cache: per slot and KV head the held rows, ids and weights (64 bits)."""
+
+    def __init__(self, n_slot, n_head, n_kv, hd, cap):
+        self.B, self.H, self.Hkv, self.hd, self.cap = n_slot, n_head, n_kv, hd, cap
+        z = lambda *s: torch.zeros(s, dtype=torch.float64, device="cuda")
+        self.k, self.v = z(n_slot, n_kv, cap, hd), z(n_slot, n_kv, cap, hd)
+        self.w = z(n_slot, n_kv, cap)
+        self.ids = torch.zeros((n_slot, n_kv, cap), dtype=torch.int64, device="cuda")
+        self.len, self.seen = [0] * n_slot, [0] * n_slot
+
+    def append(self, k, v, n_new=None, start=None):
+        hk, hv = held(k), held(v)
+        for b in range(self.B):
+            n = k.shape[1] if n_new is None else n_new[b]
+            s = self.len[b] if start is None else start[b]
+            seen = self.seen[b] - (self.len[b] - s)
+            n = min(n, self.cap - s)
+            self.k[b, :, s:s + n] = hk[b, :n].transpose(0, 1)
+            self.v[b, :, s:s + n] = hv[b, :n].transpose(0, 1)
+            self.w[b, :, s:s + n] = 0
+            self.ids[b, :, s:s + n] = torch.arange(seen, seen + n, device="cuda")
+            self.len[b], self.seen[b] = s + n, seen + n
+
+    def attention(self, q, decay=None):
+        """(output, tolerance without the output type's, weights' tolerance)"""
+        B, T, H, hd = q.shape
+        G = H // self.Hkv
+        out = torch.zeros((B, T, H, hd), dtype=torch.float64, device="cuda")
+        tol = torch.zeros((B, T, H, 1), dtype=torch.float64, device="cuda")
+        wtol = 0.0
+        new = torch.zeros_like(self.w)
+        for b in range(B):
+            for t in range(T):
+                m = self.len[b] - T + 1 + t
+                if m <= 0:
+                    continue
+                qq = q[b, t].double().reshape(self.Hkv, G, hd)
+                k, v = self.k[b, :, :m], self.v[b, :, :m]
+                x = torch.einsum("hgd,hnd->hgn", qq, k) / hd ** 0.5
+                p = torch.softmax(x, -1)
+                out[b, t] = torch.einsum("hgn,hnd->hgd", p, v).reshape(H, hd)
+                new[b, :, :m] += p.sum(1)
+                a = torch.einsum("hgd,hnd->hgn", qq.abs(), k.abs()).amax(-1) / hd ** 0.5
+                rel = a * (2.0 ** -22 + 16 * 2.0 ** -24) + 2.0 ** -21
+                big = v.abs().amax((1, 2))[:, None]
+                tol[b, t] = ((2 * rel + 2.0 ** -20) * big).reshape(H, 1)
+                wtol = max(wtol, float(2 * rel.max()) * G * T)
+        if decay is not None:
+            for b in range(B):
+                n = self.len[b]
+                self.w[b, :, :n] = decay * self.w[b, :, :n] + new[b, :, :n] if decay else new[b, :, :n]
+        return out, tol, wtol
+
+    def evict(self, budget, n_sink=0, n_recent=0, w=None):
+        """The new arrangement; w: the weights to choose by (the kernel's own fp32 ones)."""
+        w = self.w if w is None else w
+        for b in range(self.B):
+            n = self.len[b]
+            if n <= budget:
+                continue
+            for h in range(self.Hkv):
+                ids = self.ids[b, h, :n].cpu().numpy()
+                wt = w[b, h, :n].double().cpu().numpy()
+                stay = (ids < n_sink) | (ids >= self.seen[b] - n_recent)
+                rest = np.flatnonzero(~stay)
+                rest = rest[np.argsort(-wt[rest], kind="stable")][:budget - int(stay.sum())]
+                stay[rest] = True
+                src = np.arange(budget)
+                src[~stay[:budget]] = budget + np.flatnonzero(stay[budget:])
+                s = torch.from_numpy(src).cuda()
+                for a in (self.k, self.v, self.w, self.ids):
+                    a[b, h, :budget] = a[b, h, s]
+            self.len[b] = budget
+
+
+def make(n_slot, n_head, n_kv, hd, cap, n_layer=1, track=0):
+    """A cache whose buffer starts full of NaN scales and wild codes."""
+    c = pnb.Kv4Cache(n_layer, n_slot, n_head, n_kv, hd, cap, track=track)
+    c.buf.fill_(0xFF)
+    c.reset()
+    return c
+
+
+def rows(shape, seed, dtype=F32, scale=1.0):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return (torch.randn(shape, generator=g, device="cuda") * scale).to(dtype)
+
+
+def i32(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def check_content(c, ref, layer=0):
+    B, n = ref.B, max(ref.len + [1])
+    k = torch.full((B, n, ref.Hkv, ref.hd), 7.0, device="cuda")
+    v = torch.full_like(k, 7.0)
+    c.read(layer, k, v)
+    assert c.lengths(layer).tolist() == ref.len
+    assert c.seen(layer).tolist() == ref.seen
+    for b in range(B):
+        m = ref.len[b]
+        for got, want in ((k, ref.k), (v, ref.v)):
+            w = want[b, :, :m].transpose(0, 1)
+            g = got[b, :m].double()
+            assert torch.equal(torch.isnan(g), torch.isnan(w))
+            assert torch.equal(torch.nan_to_num(g), torch.nan_to_num(w))
+            assert not got[b, m:].any()
+        assert torch.equal(c.ids(layer)[b, :, :m].long(), ref.ids[b, :, :m])
+
+
+def check_attention(c, ref, q, out_dtype=None, decay=None, layer=0):
+    out = torch.full(q.shape, float("nan"), dtype=out_dtype or q.dtype, device="cuda")
+    c.attention(layer, q, out, decay=decay)
+    want, tol, wtol = ref.attention(q, decay)
+    if out.dtype == BF16:
+        tol = tol + want.abs() * 2.0 ** -8 + tol_fp16(ref)
+    err = (out.double() - want).abs()
+    assert bool((err <= tol).all()), f"max error {float((err - tol).max()):.3e} over tolerance"
+    if decay is not None:
+        w = c.weights(layer)
+        for b in range(ref.B):
+            n = ref.len[b]
+            d = (w[b, :, :n].double() - ref.w[b, :, :n]).abs()
+            assert n == 0 or float(d.max()) <= wtol + 2.0 ** -22 * float(ref.w[b, :, :n].max())
+    return out
+
+
+def tol_fp16(ref):
+    """A bf16 output's weights are single fp16 numbers: 2^-11 of the largest value."""
+    big = max(float(ref.v[b, :, :n].abs().max()) for b, n in enumerate(ref.len) if n) if any(ref.len) else 0.0
+    return 2.0 ** -11 * big
+
+
+# ------------------------------------------------------------ append / read
+@pytest.mark.parametrize("hd", [32, 64, 128])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("T", [1, 31, 33, 100])
+def test_append_holds_the_definition(hd, dtype, T):
+    c, ref = make(3, 6, 3, hd, 128), Ref(3, 6, 3, hd, 128)
+    k, v = rows((3, T, 3, hd), 1, dtype, 3.0), rows((3, T, 3, hd), 2, dtype, 0.1)
+    n = [T, 0, (T + 1) // 2]
+    c.append(0, k, v, n_new=i32(n))
+    ref.append(k, v, n)
+    check_content(c, ref)
+    assert c.device_error() == 0
+
+
+def test_append_piecewise_equals_at_once():
+    k, v = rows((2, 95, 2, 64), 3, BF16), rows((2, 95, 2, 64), 4, BF16)
+    whole = make(2, 2, 2, 64, 96)
+    whole.append(0, k, v)
+    c = make(2, 2, 2, 64, 96)
+    at = 0
+    for n in (1, 2, 5, 24, 31, 1, 31):
+        c.append(0, k[:, at:at + n], v[:, at:at + n])
+        at += n
+    assert at == 95
+    a, b = torch.empty(2, 2, 95, 2, 64, device="cuda"), torch.empty(2, 2, 95, 2, 64, device="cuda")
+    whole.read(0, a[0], a[1])
+    c.read(0, b[0], b[1])
+    assert torch.equal(a, b)
+    assert torch.equal(whole.ids(0)[..., :95], c.ids(0)[..., :95])
+
+
+def test_quantiser_borders():
+    """Quotients exactly between two codes, subnormal scales, zero, huge and non-finite rows."""
+    hd = 32
+    x = torch.zeros(1, 9, 1, hd, dtype=torch.float64)
+    d = 0.3017578125                                     # an fp16 number
+    x[0, 0, 0, :16] = (torch.arange(16) - 7.5) * d       # ties, the largest beyond 7 d
+    x[0, 0, 0, 16] = 7 * d
+    x[0, 0, 0, :16] = x[0, 0, 0, :16].clamp(-7 * d, 7 * d)
+    x[0, 1, 0] = torch.linspace(-1, 1, hd) * 7 * 2.0 ** -24 * 1.4   # scale rounds to a subnormal
+    x[0, 2, 0] = torch.linspace(-1, 1, hd) * 2.0 ** -26  # scale rounds to zero
+    x[0, 4, 0, 3] = 1e30                                 # scale saturates
+    x[0, 5, 0, 5] = float("nan")
+    x[0, 6, 0, 5] = float("inf")
+    x[0, 7, 0, 5] = -float("inf")
+    x[0, 8, 0, 0] = -1.0                                 # one negative entry: u = 8 - 7
+    x = x.float().cuda()
+    # ties a half ulp away in either direction are no ties
+    y = x.clone()
+    y[0, 0, 0, 1] = torch.nextafter(y[0, 0, 0, 1], torch.tensor(0.0, device="cuda"))
+    y[0, 0, 0, 2] = torch.nextafter(y[0, 0, 0, 2], torch.tensor(-9.0, device="cuda"))
+    c, ref = make(1, 1, 1, hd, 32), Ref(1, 1, 1, hd, 32)
+    c.append(0, x, y)
+    ref.append(x, y)
+    check_content(c, ref)
+
+
+def test_quantiser_many_values():
+    """Every quotient of 2^21 fp32 values, many of them near a border."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(5)
+    n = 1 << 9
+    top = torch.rand((1, n, 32, 4, 1), generator=g, device="cuda") * 4 + 0.01
+    d = (top / torch.full_like(top, 7.0)).half().float()
+    steps = torch.randint(-13, 14, (1, n, 32, 4, 32), generator=g, device="cuda").float() * 0.5
+    x = steps * d
+    x = torch.where(torch.rand(x.shape, generator=g, device="cuda") < 0.5, x,
+                    torch.nextafter(x, x * 2))
+    x[..., :1] = top
+    x = torch.minimum(x, top).reshape(1, n, 32, 128)
+    c, ref = make(1, 32, 32, 128, n), Ref(1, 32, 32, 128, n)
+    c.append(0, x, -x)
+    ref.append(x, -x)
+    check_content(c, ref)
+
+
+def test_append_reads_strided_rows():
+    """K and V inside a fused QKV projection, and in a state's [head][position][hd] cache layout."""
+    B, T, H, Hkv, hd = 2, 9, 4, 2, 64
+    fused = rows((B, T, (H + 2 * Hkv) * hd), 6, BF16)
+    k = fused[..., H * hd:(H + Hkv) * hd].view(B, T, Hkv, hd)
+    v = fused[..., (H + Hkv) * hd:].view(B, T, Hkv, hd)
+    c, ref = make(B, H, Hkv, hd, 64), Ref(B, H, Hkv, hd, 64)
+    c.append(0, k, v)
+    ref.append(k, v)
+    cache = rows((2, B, Hkv, 40, hd), 7)
+    k, v = cache[0].transpose(1, 2), cache[1].transpose(1, 2)
+    c.append(0, k, v, n_new=i32([40, 17]))
+    ref.append(k, v, [40, 17])
+    check_content(c, ref)
+    # and read back into that layout, rounded to bf16
+    back = torch.zeros((2, B, Hkv, 50, hd), dtype=BF16, device="cuda")
+    c.read(0, back[0].transpose(1, 2)[:, :30], back[1].transpose(1, 2)[:, :30], first=i32([4, 19]))
+    for b, f in enumerate((4, 19)):
+        n = min(30, ref.len[b] - f)
+        assert torch.equal(back[0, b, :, :n], ref.k[b, :, f:f + n].to(BF16))
+        assert torch.equal(back[1, b, :, :n], ref.v[b, :, f:f + n].to(BF16))
+        assert not back[:, b, :, n:].any()
+
+
+def test_rollback_and_capacity():
+    c, ref = make(2, 2, 1, 32, 64), Ref(2, 2, 1, 32, 64)
+    k, v = rows((2, 60, 1, 32), 8), rows((2, 60, 1, 32), 9)
+    c.append(0, k, v)
+    ref.append(k, v)
+    k2, v2 = rows((2, 5, 1, 32), 10), rows((2, 5, 1, 32), 11)
+    c.append(0, k2, v2, n_new=i32([5, 3]), start=i32([57, 60]))   # slot 0 takes back 3 drafts
+    ref.append(k2, v2, [5, 3], [57, 60])
+    check_content(c, ref)
+    assert c.device_error() == 0
+    c.append(0, k2, v2)                       # 62 + 5 and 63 + 5 pass the capacity
+    ref.append(k2, v2)
+    check_content(c, ref)
+    assert ref.len == [64, 64] and c.device_error() == pnb.PNB_DEV_ERR_FULL
+    c.reset()
+    assert c.device_error() == 0 and c.lengths(0).tolist() == [0, 0]
+    # starts and counts out of range leave the slot alone
+    c.append(0, k2, v2, start=i32([1, 0]))
+    assert c.lengths(0).tolist() == [0, 5] and c.device_error() == pnb.PNB_DEV_ERR_RANGE
+    c.append(0, k2, v2, n_new=i32([6, -1]))
+    assert c.lengths(0).tolist() == [0, 5] and c.seen(0).tolist() == [0, 5]
+
+
+def test_reset_of_one_slot_and_layers():
+    c = make(2, 2, 2, 32, 32, n_layer=2)
+    k = rows((2, 3, 2, 32), 12)
+    for layer in (0, 1):
+        c.append(layer, k, k)
+    c.append(1, k, k)
+    assert c.lengths(0).tolist() == [3, 3] and c.lengths(1).tolist() == [6, 6]
+    c.reset(1)
+    assert c.lengths(0).tolist() == [3, 0] and c.lengths(1).tolist() == [6, 0]
+
+
+# --------------------------------------------------------------- attention
+SHAPES = [  # n_kv, group, head_dim, T
+    (2, 1, 128, 1), (2, 4, 128, 1), (1, 8, 128, 1), (3, 3, 64, 1), (2, 7, 32, 1), (1, 16, 64, 1),
+    (2, 4, 128, 3), (4, 1, 64, 9), (1, 5, 32, 8), (1, 64, 128, 1), (1, 1, 32, 64),
+]
+
+
+@pytest.mark.parametrize("n_kv,G,hd,T", SHAPES)
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_attention_against_64_bits(n_kv, G, hd, T, dtype):
+    lens = [0, 1, 2, 31, 32, 33, 64, 65, 200, 257]
+    B, cap = len(lens), 288
+    c, ref = make(B, n_kv * G, n_kv, hd, cap), Ref(B, n_kv * G, n_kv, hd, cap)
+    k, v = rows((B, max(lens), n_kv, hd), 13, BF16, 2.0), rows((B, max(lens), n_kv, hd), 14, BF16)
+    c.append(0, k, v, n_new=i32(lens))
+    ref.append(k, v, lens)
+    check_attention(c, ref, rows((B, T, n_kv * G, hd), 15, dtype, 2.0))
+    assert c.device_error() == 0
+
+
+@pytest.mark.parametrize("q_dtype,out_dtype", [(F32, BF16), (BF16, F32)])
+def test_attention_types_may_differ(q_dtype, out_dtype):
+    c, ref = make(2, 4, 2, 64, 96), Ref(2, 4, 2, 64, 96)
+    k, v = rows((2, 90, 2, 64), 16), rows((2, 90, 2, 64), 17)
+    c.append(0, k, v, n_new=i32([90, 41]))
+    ref.append(k, v, [90, 41])
+    check_attention(c, ref, rows((2, 1, 4, 64), 18, q_dtype), out_dtype)
+
+
+@pytest.mark.parametrize("hd,n_kv,G,B,n", [(128, 1, 8, 1, 20011), (128, 8, 4, 2, 5003), (64, 2, 4, 1, 9001),
+                                           (32, 1, 1, 1, 40961), (128, 2, 1, 300, 70)])
+def test_attention_split_over_many_ctas(hd, n_kv, G, B, n):
+    cap = -(-n // 32) * 32
+    c, ref = make(B, n_kv * G, n_kv, hd, cap, track=1), Ref(B, n_kv * G, n_kv, hd, cap)
+    lens = [max(1, n - 17 * b) if B < 10 else 1 + (37 * b) % n for b in range(B)]
+    k, v = rows((B, n, n_kv, hd), 19, BF16, 1.5), rows((B, n, n_kv, hd), 20, BF16)
+    c.append(0, k, v, n_new=i32(lens))
+    ref.append(k, v, lens)
+    q = rows((B, 1, n_kv * G, hd), 21, F32, 2.0)
+    a = check_attention(c, ref, q, decay=0.0)
+    w = c.weights(0).clone()
+    for _ in range(3):                        # the same call gives the same bits
+        b = torch.empty_like(a)
+        c.attention(0, q, b, decay=0.0)
+        assert torch.equal(a, b)
+        for i, m in enumerate(lens):
+            assert torch.equal(w[i, :, :m], c.weights(0)[i, :, :m])
+
+
+def test_extreme_values():
+    """A score far above the others late in the sequence, V scales that grow by 2^20 along it
+    (the fp16 products' reference moves), large and tiny queries."""
+    B, n, hd = 4, 400, 64
+    k, v = rows((B, n, 1, hd), 22), rows((B, n, 1, hd), 23)
+    v = v * torch.logspace(-4, 2, n, device="cuda")[None, :, None, None]
+    k[1, 350] *= 40
+    q = rows((B, 1, 2, hd), 24)
+    q[2] *= 1e-20
+    q[3] *= 30
+    c, ref = make(B, 2, 1, hd, 416), Ref(B, 2, 1, hd, 416)
+    c.append(0, k, v)
+    ref.append(k, v)
+    check_attention(c, ref, q)
+    # values that shrink instead, and rows of zeros
+    v = v.flip(1).contiguous()
+    v[0, 100:] = 0
+    c.reset()
+    ref = Ref(B, 2, 1, hd, 416)
+    c.append(0, k, v)
+    ref.append(k, v)
+    check_attention(c, ref, q)
+
+
+def test_non_finite_rows_stay_where_they_are():
+    """A NaN in one slot's key, query row or value block poisons only what attends to it."""
+    B, n, hd = 4, 70, 64
+    k, v = rows((B, n, 1, hd), 25), rows((B, n, 1, hd), 26)
+    q = rows((B, 2, 2, hd), 27)
+    k[0, 69, 0, 3] = float("nan")             # the last entry: the first query does not see it
+    q[1, 1, 1, 7] = float("inf")
+    v[2, 69, 0, 40] = float("inf")            # block 1 (dims 32..63) of the last entry
+    c, ref = make(B, 2, 1, hd, 96), Ref(B, 2, 1, hd, 96)
+    c.append(0, k, v)
+    out = torch.empty_like(q)
+    c.attention(0, q, out)
+    nan = torch.isnan(out)
+    assert not nan[0, 0].any() and nan[0, 1].all()
+    assert not nan[1, 0].any() and not nan[1, 1, 0].any() and nan[1, 1, 1].all()
+    assert not nan[2, 0].any() and not nan[2, 1, :, :32].any() and nan[2, 1, :, 32:].all()
+    assert not nan[3].any()
+    k[0, 69] = 0
+    v[2, 69] = 0
+    q[1] = 0
+    c.reset()
+    ref = Ref(B, 2, 1, hd, 96)
+    c.append(0, k, v)
+    ref.append(k, v)
+    check_attention(c, ref, q)
+
+
+def test_attention_strided_rows_and_output_over_queries():
+    B, T, H, Hkv, hd = 3, 2, 4, 2, 128
+    c, ref = make(B, H, Hkv, hd, 128), Ref(B, H, Hkv, hd, 128)
+    k, v = rows((B, 120, Hkv, hd), 28), rows((B, 120, Hkv, hd), 29)
+    c.append(0, k, v, n_new=i32([120, 77, 1]))
+    ref.append(k, v, [120, 77, 1])
+    fused = rows((B, T, (H + 2 * Hkv) * hd), 30)
+    before = fused.clone()
+    q = fused[..., :H * hd].view(B, T, H, hd)
+    want, tol, _ = ref.attention(q)
+    c.attention(0, q, q)                      # in place
+    assert bool(((q.double() - want).abs() <= tol).all())
+    assert torch.equal(fused[..., H * hd:], before[..., H * hd:])
+
+
+# ------------------------------------------------------- weights, eviction
+@pytest.mark.parametrize("n_kv,G,hd,T", [(2, 4, 128, 1), (1, 1, 64, 1), (2, 3, 32, 1), (1, 4, 128, 16),
+                                         (2, 1, 64, 11)])
+def test_weights(n_kv, G, hd, T):
+    lens = [0, 1, 31, 100, 515, 1030]
+    B, cap = len(lens), 1056
+    c, ref = make(B, n_kv * G, n_kv, hd, cap, track=T), Ref(B, n_kv * G, n_kv, hd, cap)
+    k, v = rows((B, max(lens), n_kv, hd), 31), rows((B, max(lens), n_kv, hd), 32)
+    c.append(0, k, v, n_new=i32(lens))
+    ref.append(k, v, lens)
+    assert not any(c.weights(0)[b, :, :m].any() for b, m in enumerate(lens))
+    before = c.weights(0).clone()
+    for i, decay in enumerate((1.0, 1.0, 0.5, 0.0, 1.0)):
+        check_attention(c, ref, rows((B, T, n_kv * G, hd), 33 + i, F32, 1.5), decay=decay)
+    for b, m in enumerate(lens):              # nothing behind a sequence's end is written
+        assert torch.equal(before[b, :, m:].view(torch.int32), c.weights(0)[b, :, m:].view(torch.int32))
+
+
+def test_decay_zero_does_not_read_old_weights():
+    c = make(1, 1, 1, 32, 32, track=1)
+    k = rows((1, 20, 1, 32), 40)
+    c.append(0, k, k)
+    c.weights(0).fill_(float("nan"))
+    q, out = rows((1, 1, 1, 32), 41), torch.empty(1, 1, 1, 32, device="cuda")
+    c.attention(0, q, out, decay=0.0)
+    w = c.weights(0)[0, 0, :20]
+    assert abs(float(w.sum()) - 1) < 1e-5
+    assert torch.isnan(c.weights(0)[0, 0, 20:]).all()
+
+
+def fill(c, ref, lens, seed, tie=False):
+    B, n = len(lens), max(lens)
+    k, v = rows((B, n, ref.Hkv, ref.hd), seed), rows((B, n, ref.Hkv, ref.hd), seed + 1)
+    c.append(0, k, v, n_new=i32(lens))
+    ref.append(k, v, lens)
+    w = rows(tuple(ref.w.shape), seed + 2).abs()
+    if tie:
+        w = (w * 3).floor()
+    c.weights(0).copy_(w)
+    ref.w.copy_(w.double())
+
+
+@pytest.mark.parametrize("hd", [32, 64, 128])
+@pytest.mark.parametrize("budget,sink,recent", [(1, 0, 0), (33, 4, 10), (64, 0, 64), (100, 3, 0), (299, 4, 8)])
+@pytest.mark.parametrize("tie", [False, True])
+def test_evict(hd, budget, sink, recent, tie):
+    lens = [0, 1, budget, budget + 1, 300, 150, 299]
+    B = len(lens)
+    for in_place in (True, False):
+        c, ref = make(B, 2, 2, hd, 320), Ref(B, 2, 2, hd, 320)
+        fill(c, ref, [min(n, 300) for n in lens], 50, tie)
+        d = c if in_place else make(B, 6, 2, hd, 320 if budget > 288 else -(-budget // 32) * 32)
+        whole = c.buf.clone()
+        c.evict(0, budget, sink, recent, dst=d)
+        assert in_place or torch.equal(whole, c.buf)
+        ref.evict(budget, sink, recent)
+        check_content(d, ref)
+        for b, n in enumerate(ref.len):
+            assert torch.equal(d.weights(0)[b, :, :n].double(), ref.w[b, :, :n])
+
+
+@pytest.mark.parametrize("cap,n,budget", [(4096, 4096, 1000), (8192, 5000, 4999), (20000, 19999, 7000),
+                                          (40000, 39001, 20000), (140000, 139999, 33)])
+def test_evict_long(cap, n, budget):
+    """Capacities of one CTA, of clusters, and of the larger forms; weights exactly alike in places."""
+    cap = -(-cap // 32) * 32
+    c, ref = make(1, 1, 1, 32, cap), Ref(1, 1, 1, 32, cap)
+    fill(c, ref, [n], 60, tie=True)
+    c.evict(0, budget, 4, 16)
+    ref.evict(budget, 4, 16)
+    check_content(c, ref)
+
+
+def test_evict_odd_weights():
+    """Infinite, negative, signed-zero and NaN weights have a fixed order."""
+    c, ref = make(1, 1, 1, 32, 32), Ref(1, 1, 1, 32, 32)
+    fill(c, ref, [8], 70)
+    w = torch.tensor([0.0, -0.0, float("nan"), float("inf"), -1.0, 2.0, -float("inf"), 1.0], device="cuda")
+    c.weights(0)[0, 0, :8] = w
+    c.evict(0, 4)
+    assert c.ids(0)[0, 0, :4].tolist() == [5, 7, 2, 3]   # dropped 0 and 1: 5 and 7 move up
+    c.evict(0, 2)
+    assert c.ids(0)[0, 0, :2].tolist() == [2, 3]
+
+
+def test_decode_loop_as_used():
+    """Prompt, then steps of append, attention with accumulated weights and eviction, in place, on two
+    layers; checked against the reference at every step, then replayed from a CUDA graph."""
+    B, H, Hkv, hd, cap, budget = 3, 8, 2, 64, 96, 64
+    steps = 12
+    lens = [60, 5, 80]
+    kp, vp = rows((2, B, 80, Hkv, hd), 80), rows((2, B, 80, Hkv, hd), 81)
+    ks, vs = rows((steps, 2, B, 1, Hkv, hd), 82, BF16), rows((steps, 2, B, 1, Hkv, hd), 83, BF16)
+    qs = rows((steps, 2, B, 1, H, hd), 84, BF16, 2.0)
+
+    def begin(c):
+        c.reset()
+        for layer in (0, 1):
+            c.append(layer, kp[layer], vp[layer], n_new=i32(lens))
+
+    c = make(B, H, Hkv, hd, cap, n_layer=2, track=1)
+    refs = [Ref(B, H, Hkv, hd, cap) for _ in (0, 1)]
+    begin(c)
+    for layer in (0, 1):
+        refs[layer].append(kp[layer], vp[layer], lens)
+    outs = []
+    for i in range(steps):
+        for layer, ref in enumerate(refs):
+            c.append(layer, ks[i, layer], vs[i, layer])
+            ref.append(ks[i, layer], vs[i, layer])
+            outs.append(check_attention(c, ref, qs[i, layer], F32, decay=1.0, layer=layer))
+            ref.w.copy_(c.weights(layer).double().nan_to_num())   # choose by the kernel's own sums
+            c.evict(layer, budget, n_sink=4, n_recent=16)
+            ref.evict(budget, 4, 16)
+            check_content(c, ref, layer)
+    assert c.device_error() == 0
+
+    # the same loop from one captured step; a second cache keeps it apart from the first
+    g = make(B, H, Hkv, hd, cap, n_layer=2, track=1)
+    begin(g)
+    k, v, q = ks[0].clone(), vs[0].clone(), qs[0].clone()
+    out = torch.empty((2, B, 1, H, hd), device="cuda")
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for layer in (0, 1):
+            g.append(layer, k[layer], v[layer])
+            g.attention(layer, q[layer], out[layer], decay=1.0)
+            g.evict(layer, budget, n_sink=4, n_recent=16)
+    for i in range(steps):
+        k.copy_(ks[i]); v.copy_(vs[i]); q.copy_(qs[i])
+        graph.replay()
+        for layer in (0, 1):
+            assert torch.equal(out[layer], outs[2 * i + layer])
+    for layer in (0, 1):
+        check_content(g, refs[layer], layer)
+    assert g.device_error() == 0
+
+
+def test_two_caches_on_two_streams():
+    B, H, Hkv, hd, n = 4, 8, 2, 128, 700
+    caches, refs, qs, outs = [], [], [], []
+    for i in range(2):
+        c, ref = make(B, H, Hkv, hd, 704, track=1), Ref(B, H, Hkv, hd, 704)
+        k, v = rows((B, n, Hkv, hd), 90 + i), rows((B, n, Hkv, hd), 92 + i)
+        c.append(0, k, v)
+        ref.append(k, v)
+        caches.append(c); refs.append(ref)
+        qs.append(rows((B, 1, H, hd), 94 + i)); outs.append(torch.empty(B, 1, H, hd, device="cuda"))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(20):
+        for c, q, o, s in zip(caches, qs, outs, streams):
+            c.attention(0, q, o, decay=0.0, stream=s)
+    torch.cuda.synchronize()
+    for ref, q, o in zip(refs, qs, outs):
+        want, tol, _ = ref.attention(q)
+        assert bool(((o.double() - want).abs() <= tol).all())
+
+
+def test_a_copied_buffer_is_a_copied_cache():
+    c, ref = make(2, 4, 2, 64, 64), Ref(2, 4, 2, 64, 64)
+    k, v = rows((2, 50, 2, 64), 96), rows((2, 50, 2, 64), 97)
+    c.append(0, k, v, n_new=i32([50, 9]))
+    ref.append(k, v, [50, 9])
+    d = pnb.Kv4Cache(1, 2, 4, 2, 64, 64, buf=c.buf.clone())
+    c.reset()
+    check_content(d, ref)
+    check_attention(d, ref, rows((2, 1, 4, 64), 98))
+
+
+def test_wild_lengths_in_the_buffer_stay_inside_it():
+    c = make(2, 2, 1, 32, 32, track=1)
+    k = rows((2, 32, 1, 32), 99)
+    c.append(0, k, k)
+    c.lengths(0).copy_(i32([1 << 30, -5]))
+    q, out = rows((2, 1, 2, 32), 100), torch.empty(2, 1, 2, 32, device="cuda")
+    c.attention(0, q, out, decay=0.0)
+    assert torch.isfinite(out).all() and not out[1].any() and out[0].any()
+
+
+def test_after_a_models_prefill():
+    """A prefilled state's K / V of one layer moved into a 4-bit cache, and the step's own rotated
+    queries answered from it: the held values are the state's cache through the quantiser."""
+    import synth.workloads as wl
+    from synth import BF16 as SBF16
+
+    s = wl.Shape(n_vocab=1000, n_embd=1024, n_head=8, n_kv_head=2, n_layer=2, n_ff=1024, n_ctx=96,
+                 rope_theta=1e4, rms_norm_eps=1e-5, sliding_window=0, dtype=SBF16)
+    sm = pnb.SynthModel(s, 21, device="cuda")
+    st = sm.new_state()
+    prompt = torch.arange(1, 71, dtype=torch.int32, device="cuda")
+    st.prefill(prompt)
+    torch.cuda.synchronize()
+    kv = st.kv.view(torch.uint8)[:sm.model.kv_bytes()].view(BF16).view(2, 2, 1, 2, 96, 128)
+    c, ref = make(1, 8, 2, 128, 96, n_layer=2), Ref(1, 8, 2, 128, 96)
+    k, v = kv[1, 0].transpose(1, 2)[:, :70], kv[1, 1].transpose(1, 2)[:, :70]
+    c.append(1, k, v)
+    ref.append(k, v)
+    check_content(c, ref, layer=1)
+
+    class Holder:
+        __cuda_array_interface__ = {"shape": (1, 1, 8, 128), "typestr": "<f4",
+                                    "data": (st.activations()["q"], False), "version": 3}
+    st.run_kernel(pnb.PNB_KERNEL_QKV, 1)
+    q = torch.as_tensor(Holder(), device="cuda").clone()
+    check_attention(c, ref, q, layer=1)
+
+
+# ---------------------------------------------------------------- refusals
+def test_refusals():
+    c = make(2, 4, 2, 64, 64, n_layer=2, track=1)
+    k, q = rows((2, 3, 2, 64), 101), rows((2, 1, 4, 64), 102)
+    out = torch.empty_like(q)
+
+    def code(f, *a, **kw):
+        with pytest.raises(pnb.PnbError) as e:
+            f(*a, **kw)
+        return e.value.code
+
+    assert code(c.append, 2, k, k) == -1 and code(c.append, -1, k, k) == -1
+    assert code(c.append, 0, k[:, :, :1], k[:, :, :1]) == -1
+    assert code(c.append, 0, k, k[:, :2]) == -1
+    assert code(c.append, 0, k, k.to(BF16)) == -1
+    assert code(c.append, 0, k.half(), k.half()) == -1
+    assert code(c.append, 0, k.cpu(), k.cpu()) == -10
+    assert code(c.append, 0, k[..., ::2].expand(2, 3, 2, 32), k) == -1
+    odd = torch.empty(2, 3, 2 * 64 + 1, device="cuda")[..., :128].view(2, 3, 2, 64)
+    assert code(c.append, 0, odd, odd) == -3                      # rows not 16-byte aligned
+    assert code(c.append, 0, rows((2, 65, 2, 64), 1), rows((2, 65, 2, 64), 1)) == -1
+    assert code(c.append, 0, k, k, n_new=torch.zeros(2, device="cuda")) == -1
+    assert code(c.append, 0, k, k, start=i32([0])) == -1
+    assert code(c.read, 0, k[:1].expand(2, 3, 2, 64), k.clone()) == -1   # overlapping outputs
+    assert code(c.attention, 0, q, out, decay=-0.5) == -1
+    assert code(c.attention, 0, q, out, decay=float("nan")) == -1
+    assert code(c.attention, 0, q, out, decay=float("inf")) == -1
+    q2 = rows((2, 2, 4, 64), 103)
+    assert code(c.attention, 0, q2, q2.clone(), decay=1.0) == -1          # more tokens than `track`
+    q33 = rows((2, 33, 4, 64), 103)
+    assert code(c.attention, 0, q33, q33.clone()) == -5                   # 66 rows per KV head
+    assert code(c.attention, 0, q[:, :0], out[:, :0]) == -1
+    assert code(c.attention, 0, q, out[:1].expand(2, 1, 4, 64)) == -1
+    assert code(c.evict, 0, 0) == -1 and code(c.evict, 0, 65) == -1
+    assert code(c.evict, 0, 10, n_sink=6, n_recent=5) == -1
+    assert code(c.evict, 0, 10, n_sink=-1) == -1
+    assert code(c.evict, 0, 10, dst_layer=2) == -1
+    assert code(c.evict, 0, 10, dst=make(2, 4, 2, 32, 64)) == -1
+    assert code(c.evict, 0, 33, dst=make(2, 4, 2, 64, 32)) == -1
+    assert code(c.evict, 0, 10, dst=pnb.Kv4Cache(1, 2, 4, 2, 64, 32, buf=c.buf)) == -1
+    assert code(c.reset, 2) == -1
+    big = pnb.Kv4Cache(1, 1, 1, 1, 32, (1 << 18) + 32)
+    big.reset()
+    assert code(big.evict, 0, 10) == -5
+    assert c.device_error() == 0 and c.lengths(0).tolist() == [0, 0]

@@ -21,7 +21,7 @@ _lib = ctypes.CDLL(LIB)
 
 PNB_F32, PNB_BF16, PNB_Q8_0, PNB_Q4_0 = 0, 1, 2, 3
 PNB_TOKEN_PREV = -1
-PNB_DEV_ERR_TOKEN, PNB_DEV_ERR_TIMEOUT = 1, 2
+PNB_DEV_ERR_TOKEN, PNB_DEV_ERR_TIMEOUT, PNB_DEV_ERR_FULL, PNB_DEV_ERR_RANGE = 1, 2, 4, 8
 (PNB_KERNEL_QKV, PNB_KERNEL_ATTN, PNB_KERNEL_OPROJ, PNB_KERNEL_ROUTER, PNB_KERNEL_GATE_UP,
  PNB_KERNEL_DOWN, PNB_KERNEL_LM_HEAD) = range(7)
 ERRORS = {0: "PNB_OK", -1: "PNB_E_INVAL", -2: "PNB_E_NULL", -3: "PNB_E_ALIGN",
@@ -60,6 +60,20 @@ class pnb_activations(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("x", "q", "attn", "h")]
 
 
+class pnb_kvq_config(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in
+                ("n_layer", "n_slot", "n_head", "n_kv_head", "head_dim", "cap", "track")]
+
+
+class pnb_rows(ctypes.Structure):
+    _fields_ = [("dev", ctypes.c_void_p), ("slot", ctypes.c_int64), ("token", ctypes.c_int64),
+                ("head", ctypes.c_int64), ("dtype", ctypes.c_int32)]
+
+
+class pnb_kvq_views(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("len", "seen", "ids", "weights")]
+
+
 _p, _i32, _sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
 _SIGS = {
     "pnb_model_create": (_i32, [_p, _p, _p]),
@@ -92,6 +106,16 @@ _SIGS = {
     "pnb_attention_decode_static": (_i32, [_p, _p, _p, _i32, _i32, _i32, _i32, _i32, _i32, _i32,
                                            _p, _p, _p]),
     "pnb_state_wait_probe": (_i32, [_p, ctypes.c_uint64, _p]),
+    "pnb_kvq_bytes": (_sz, [_p]),
+    "pnb_kvq_new": (_i32, [_p, _p, _sz, _p]),
+    "pnb_kvq_free": (None, [_p]),
+    "pnb_kvq_reset": (_i32, [_p, _i32, _p]),
+    "pnb_kvq_append": (_i32, [_p, _i32, _p, _p, _i32, _p, _p, _p]),
+    "pnb_kvq_read": (_i32, [_p, _i32, _p, _i32, _p, _p, _p]),
+    "pnb_kvq_attention": (_i32, [_p, _i32, _p, _i32, _p, ctypes.c_float, _p]),
+    "pnb_kvq_evict": (_i32, [_p, _i32, _p, _i32, _i32, _i32, _i32, _p]),
+    "pnb_kvq_layer_views": (_i32, [_p, _i32, _p]),
+    "pnb_kvq_check": (_i32, [_p, _p]),
     "pnb_strerror": (ctypes.c_char_p, [_i32]),
 }
 for _name, (_res, _args) in _SIGS.items():
@@ -333,3 +357,4 @@ class State:
 
 
 from .synthetic import SynthModel  # noqa: E402  (generated-weight models for tests / bench)
+from .kv4 import Kv4Cache  # noqa: E402  (the 4-bit KV cache)

@@ -1,0 +1,198 @@
+// pnb_kv4.cuh - the 4-bit KV cache: layout, kernel arguments and launchers.
+//
+// Every K and V row is held in Q4_0 blocks of 32 consecutive head dimensions:
+// one fp16 scale d and 32 codes u, value = d * (u - 8).  A (layer, slot, KV
+// head) is a list of chunks of 32 positions, each one contiguous run of
+// 1152 * NG bytes (NG = head_dim / 32; 4608 at head_dim 128), so that a single
+// bulk copy brings the K and V of 32 positions into shared memory:
+//
+//   [K codes 512 NG][K scales 64 NG][V codes 512 NG][V scales 64 NG]
+//
+// The codes lie as the attention kernel's matrix instructions (m16n8k16, fp16)
+// want their B operand, so that one 32-bit word of 8 codes becomes four
+// registers of two fp16 each with four masks and one shift:
+//   - a word's nibbles n and n + 4 are a pair: (w >> 4 n) & 0x000f000f is the
+//     pair as two fp16 subnormals u * 2^-24, exactly; for odd n the shift is
+//     left out and the pair stands for u * 2^-20 (the other operand carries
+//     the 2^-4);
+//   - K: a lane (r = lane / 4, c = lane % 4) holds position 8 t + r and, per
+//     32-dim block j, the word of dims 32 j + 8 c + n;
+//   - V: the lane holds dim 32 J + 8 i + r and the word whose nibble t + 4 e
+//     is position 8 t + 2 c + e.
+// Scales of positions 8 t + 2 c and 8 t + 2 c + 1 are a half2 per block, next
+// to one another over the blocks: what a lane (r, c) multiplies its scores and
+// softmax weights of that position pair with.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "pnb.h"
+#include "pnb_device.cuh"
+
+namespace pnb {
+
+constexpr int kKv4Chunk = 32;              // positions per chunk
+constexpr int kKv4Rows = 8;                // query rows (tokens x heads of a group) per work item
+constexpr int kKv4Warps = 8;               // warps per attention CTA
+constexpr int kKv4Threads = kKv4Warps * 32;
+constexpr int kKv4CtasPerSm = 2;
+constexpr int kKv4MaxRows = 64;            // tokens x heads of a group in one call
+constexpr int kKv4MaxSlots = 1024;
+constexpr int kKv4MaxCap = 1 << 20;        // positions per slot
+constexpr int kKv4MaxEvictCap = 1 << 18;   // largest cache the eviction selects from
+constexpr int kErrFull = 4;                // mirror of PNB_DEV_ERR_FULL
+constexpr int kErrRange = 8;               // mirror of PNB_DEV_ERR_RANGE
+
+__host__ __device__ constexpr int kv4_chunk_bytes(int ng) { return 1152 * ng; }
+__host__ __device__ constexpr int kv4_kscale_off(int ng) { return 512 * ng; }
+__host__ __device__ constexpr int kv4_v_off(int ng) { return 576 * ng; }
+__host__ __device__ constexpr int kv4_vscale_off(int ng) { return 1088 * ng; }
+// K word of position p (0..31 in the chunk), block j, dims 8 c .. 8 c + 7 of it
+__host__ __device__ constexpr int kv4_kword(int ng, int p, int c, int j) {
+  return p * 16 * ng + c * 4 * ng + j * 4;
+}
+// scale of position p, block j, relative to the K or V scale area
+__host__ __device__ constexpr int kv4_scale(int ng, int p, int j) {
+  return (p >> 1) * 4 * ng + j * 4 + (p & 1) * 2;
+}
+// V words of dims 32 J + 8 i + r (i = 0..3, 16 bytes) for position class c
+__host__ __device__ constexpr int kv4_vunit(int J, int r, int c) { return J * 512 + (r * 4 + c) * 16; }
+// bit position of position p's nibble in its V word; its class is (p / 2) % 4
+__host__ __device__ constexpr int kv4_vshift(int p) { return 4 * ((p >> 3) + 4 * (p & 1)); }
+
+// rows of a caller's tensor [slot][token][head][head_dim], strides in elements
+struct Kv4Rows {
+  void *p;
+  int64_t slot, token, head;
+  int32_t dtype;
+};
+
+// one layer of a cache
+struct Kv4Layer {
+  uint8_t *codes;       // [n_slot][n_kv][cap / 32] chunks
+  int32_t *ids;         // [n_slot][n_kv][cap] original position of each entry
+  float *weights;       // [n_slot][n_kv][cap] accumulated attention weights
+  int32_t *len, *seen;  // [n_slot] entries held, tokens ever appended
+  int32_t cap;
+};
+
+struct Kv4AppendArgs {
+  Kv4Layer l;
+  Kv4Rows k, v;
+  const int32_t *n_new, *start;   // [n_slot] or NULL
+  int32_t n_slot, n_kv, T;
+  uint32_t *arrive;               // [n_slot]
+  int32_t *err;
+};
+
+struct Kv4ReadArgs {
+  Kv4Layer l;
+  Kv4Rows k, v;
+  const int32_t *first;           // [n_slot] or NULL
+  int32_t n_slot, n_kv, T;
+};
+
+struct Kv4AttnArgs {
+  Kv4Layer l;
+  Kv4Rows q, out;
+  int32_t n_slot, n_kv, G, T, rows, nrb;  // rows = T * G, nrb = row blocks of kKv4Rows
+  float qscale;                   // log2(e) / sqrt(head_dim)
+  float *part;                    // [2 grid][kKv4Rows][head_dim]
+  float *part_ml;                 // [2 grid][kKv4Rows][2]: reference, sum
+  unsigned *counter;              // [grid]
+  int32_t *err;
+  float *scores;                  // [n_slot][n_kv][rows][cap], log2 units (NULL: not tracked)
+  float *lse;                     // [n_slot][n_kv][rows]
+};
+
+struct Kv4WeightArgs {
+  Kv4Layer l;
+  const float *scores, *lse;
+  int32_t n_slot, n_kv, rows;
+  float decay;
+};
+
+struct Kv4EvictArgs {
+  Kv4Layer src, dst;
+  int32_t n_slot, n_kv, budget, n_sink, n_recent;
+  int32_t in_place;
+  int32_t *src_of, *movers;       // [n_slot][n_kv][src.cap]
+  int32_t *n_old;                 // [n_slot]
+  uint32_t *arrive;               // [n_slot]
+};
+
+cudaError_t prepare_kv4_kernels(int ng, int *attn_grid);
+cudaError_t launch_kv4_append(int ng, const Kv4AppendArgs &a, cudaStream_t st);
+cudaError_t launch_kv4_read(int ng, const Kv4ReadArgs &a, cudaStream_t st);
+cudaError_t launch_kv4_attn(int ng, const Kv4AttnArgs &a, int grid, cudaStream_t st);
+cudaError_t launch_kv4_weights(const Kv4WeightArgs &a, cudaStream_t st);
+cudaError_t launch_kv4_evict(int ng, const Kv4EvictArgs &a, cudaStream_t st);
+cudaError_t launch_kv4_reset(int32_t *len, int32_t *seen, int64_t layer_stride, int n_layer, int n_slot,
+                             int slot, cudaStream_t st);
+
+// launch with programmatic dependent launch: every kernel of the cache waits
+// (griddepcontrol.wait) before its first access to global memory
+template <typename K, typename A>
+inline cudaError_t kv4_launch(K kern, dim3 grid, dim3 block, size_t smem, int cluster, cudaStream_t st,
+                              const A &a) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  int na = 0;
+  attr[na].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[na].val.programmaticStreamSerializationAllowed = 1;
+  ++na;
+  if (cluster > 1) {
+    attr[na].id = cudaLaunchAttributeClusterDimension;
+    attr[na].val.clusterDim.x = cluster;
+    attr[na].val.clusterDim.y = 1;
+    attr[na].val.clusterDim.z = 1;
+    ++na;
+  }
+  cfg.attrs = attr;
+  cfg.numAttrs = na;
+  return cudaLaunchKernelEx(&cfg, kern, a);
+}
+
+// Entries of slot b as the kernels use them: a length outside [0, cap] (the
+// buffer is the caller's) never leads an access out of the cache.
+__device__ __forceinline__ int kv4_len(const Kv4Layer &l, int b) {
+  const int n = l.len[b];
+  return n < 0 ? 0 : (n > l.cap ? l.cap : n);
+}
+
+// Prefix sums over the slots of mult * ceil(len / unit) into pre[0 .. n_slot]
+// (shared memory), by the calling warp; the caller synchronises.
+__device__ __forceinline__ void kv4_prefix(const Kv4Layer &l, int n_slot, int unit, int mult, int *pre) {
+  const int lane = threadIdx.x & 31;
+  int base = 0;
+  for (int b0 = 0; b0 < n_slot; b0 += 32) {
+    const int b = b0 + lane;
+    int v = b < n_slot ? mult * ((kv4_len(l, b) + unit - 1) / unit) : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += u;
+    }
+    if (b < n_slot) pre[b + 1] = base + v;
+    base += __shfl_sync(0xffffffffu, v, 31);
+  }
+  if (lane == 0) pre[0] = 0;
+}
+
+// the slot whose range of the prefix sums holds x (0 <= x < pre[n_slot])
+__device__ __forceinline__ int kv4_find(const int *pre, int n_slot, int x) {
+  int lo = 0, hi = n_slot;   // pre[lo] <= x < pre[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (pre[mid] <= x) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+}  // namespace pnb

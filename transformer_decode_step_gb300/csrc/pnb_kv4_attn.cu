@@ -1,0 +1,628 @@
+// pnb_kv4_attn.cu - decode attention over the 4-bit KV cache, and the
+// accumulation of each cached position's attention weight.
+//
+// For the rows q_i of one KV head (the query heads of its group times the
+// call's tokens), with keys k_j = d_jg (u_j - 8) per 32-dim block g:
+//   x_ij = log2(e) / sqrt(hd) sum_g d_jg (sum_{n in g} q_in u_jn - 8 sum_{n in g} q_in)
+//   o_i  = sum_j p_ij v_j / l_i,  p_ij = 2^(x_ij - ref_i),  l_i = sum_j p_ij
+// and the same for the values: sum_j (p_ij d_jg) u_jn - 8 sum_j p_ij d_jg.
+// Codes never become scaled numbers: the matrix instructions multiply the
+// integers u (exact in fp16), so the only roundings are those of the fp32
+// operand's split into two fp16 (22 bits) and of the fp32 sums.
+#include <cuda_fp16.h>
+
+#include "pnb_kv4.cuh"
+
+namespace pnb {
+
+namespace {
+
+constexpr uint32_t kMaskEven = 0x000f000fu, kMaskOdd = 0x00f000f0u;
+// chunks a CTA takes at least (one per warp): below it a call uses fewer CTAs
+constexpr int kMinChunks = kKv4Warps;
+
+template <int NG>
+struct AttnSmem {
+  static constexpr int kHd = 32 * NG;
+  static constexpr int kStages = NG == 4 ? 2 : 4;
+  static constexpr int kChunk = kv4_chunk_bytes(NG);
+  static constexpr int kRing = kKv4Warps * kStages * kChunk;
+  static constexpr int kQ = kRing;                                  // uint4 [NG][2][32]
+  static constexpr int kO = kQ + NG * 2 * 32 * 16;                  // float [warps][8][kHd]
+  static constexpr int kMl = kO + kKv4Warps * kKv4Rows * kHd * 4;   // float2 [warps][8]
+  static constexpr int kBars = kMl + kKv4Warps * kKv4Rows * 8;
+  static constexpr int kRow = kBars + kKv4Warps * kStages * 8;      // float [8][NG + 1]
+  static constexpr int kFlag = kRow + kKv4Rows * (NG + 1) * 4;
+  static constexpr int kPre = kFlag + 16;                           // int [n_slot + 1]
+  static int bytes(int n_slot) { return kPre + (n_slot + 1) * 4; }
+};
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                        uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  unsigned long long d;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(d)
+      : "l"(*reinterpret_cast<unsigned long long *>(&a)), "l"(*reinterpret_cast<unsigned long long *>(&b)));
+  return *reinterpret_cast<float2 *>(&d);
+}
+
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  unsigned long long d;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(d)
+      : "l"(*reinterpret_cast<unsigned long long *>(&a)), "l"(*reinterpret_cast<unsigned long long *>(&b)));
+  return *reinterpret_cast<float2 *>(&d);
+}
+
+__device__ __forceinline__ float2 half2_pair(uint32_t w) {
+  return __half22float2(*reinterpret_cast<const __half2 *>(&w));
+}
+
+__device__ __forceinline__ uint32_t pack_half2(float2 v) {
+  const __half2 h = __floats2half2_rn(v.x, v.y);
+  return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+template <int NG>
+__device__ __forceinline__ void lds_words(const uint8_t *p, uint32_t (&w)[NG]) {
+  if constexpr (NG == 4) {
+    const uint4 v = *reinterpret_cast<const uint4 *>(p);
+    w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
+  } else if constexpr (NG == 2) {
+    const uint2 v = *reinterpret_cast<const uint2 *>(p);
+    w[0] = v.x; w[1] = v.y;
+  } else {
+    w[0] = *reinterpret_cast<const uint32_t *>(p);
+  }
+}
+
+// the larger finite half of a word, as its bits (0 when neither is finite)
+__device__ __forceinline__ uint32_t finite_half_max(uint32_t w) {
+  uint32_t a = w & 0xffffu, b = w >> 16;
+  a = a < 0x7c00u ? a : 0u;
+  b = b < 0x7c00u ? b : 0u;
+  return a > b ? a : b;
+}
+
+// A CTA's part of the flat chunk list that lies in one item (slot, KV head,
+// row block): chunks [c0, c1) of the item's nch.
+struct Segment {
+  int b, h, rb, c0, c1, nch;
+};
+
+__device__ __forceinline__ Segment segment_at(const int *pre, const Kv4AttnArgs &a, int x, int x1) {
+  Segment s;
+  s.b = kv4_find(pre, a.n_slot, x);
+  const int per = a.n_kv * a.nrb, rel = x - pre[s.b];
+  s.nch = (pre[s.b + 1] - pre[s.b]) / per;
+  const int it = rel / s.nch;
+  s.c0 = rel - it * s.nch;
+  s.h = it / a.nrb;
+  s.rb = it - s.h * a.nrb;
+  s.c1 = min(s.nch, s.c0 + (x1 - x));
+  return s;
+}
+
+template <int N>
+__device__ __forceinline__ void store_row(const Kv4Rows &o, int64_t at, const float (&v)[N]) {
+  if (o.dtype == PNB_F32) {
+    float *p = static_cast<float *>(o.p) + at;
+    if constexpr (N == 4) *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
+    else if constexpr (N == 2) *reinterpret_cast<float2 *>(p) = make_float2(v[0], v[1]);
+    else *p = v[0];
+  } else {
+    __nv_bfloat16 *p = static_cast<__nv_bfloat16 *>(o.p) + at;
+    if constexpr (N == 1) {
+      *p = __float2bfloat16_rn(v[0]);
+    } else {
+      __nv_bfloat162 h[N / 2];
+#pragma unroll
+      for (int i = 0; i < N / 2; ++i) h[i] = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+      if constexpr (N == 4) *reinterpret_cast<uint2 *>(p) = *reinterpret_cast<uint2 *>(h);
+      else *reinterpret_cast<uint32_t *>(p) = *reinterpret_cast<uint32_t *>(h);
+    }
+  }
+}
+
+// SPLIT: softmax weights keep 22 bits (two fp16) in the product with V, for
+// fp32 outputs; a bf16 output rounds to 8 bits, and one fp16 (11 bits, the
+// rounding errors of the positions independent) is enough for it.
+template <int NG, bool SPLIT, bool TRACK>
+__global__ void __launch_bounds__(kKv4Threads, kKv4CtasPerSm)
+    k_kv4_attn(const __grid_constant__ Kv4AttnArgs a) {
+  using L = AttnSmem<NG>;
+  constexpr int HD = L::kHd, ST = L::kStages;
+  extern __shared__ __align__(128) uint8_t smem[];
+  uint4 *qf = reinterpret_cast<uint4 *>(smem + L::kQ);
+  float *so = reinterpret_cast<float *>(smem + L::kO);
+  float2 *sml = reinterpret_cast<float2 *>(smem + L::kMl);
+  float *srow = reinterpret_cast<float *>(smem + L::kRow);
+  int *sflag = reinterpret_cast<int *>(smem + L::kFlag);
+  int *pre = reinterpret_cast<int *>(smem + L::kPre);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r = lane >> 2, c = lane & 3;
+  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::kBars) + warp * ST;
+  uint8_t *ring = smem + warp * ST * L::kChunk;
+
+  if (lane == 0) {
+    for (int s = 0; s < ST; ++s) mbar_init(bars + s, 1);
+    fence_barrier_init();
+  }
+  pdl_wait();
+  if (warp == 0) kv4_prefix(a.l, a.n_slot, kKv4Chunk, a.n_kv * a.nrb, pre);
+  __syncthreads();
+  const int total = pre[a.n_slot];
+  const int per_cta = max(kMinChunks, (total + (int)gridDim.x - 1) / (int)gridDim.x);
+  const int cta = blockIdx.x;
+  const int x0 = (int)min((int64_t)total, (int64_t)cta * per_cta);
+  const int x1 = (int)min((int64_t)total, (int64_t)x0 + per_cta);
+
+  // slots with nothing to attend to answer zero
+  for (int b = cta; b < a.n_slot; b += gridDim.x) {
+    if (pre[b + 1] != pre[b]) continue;
+    const float z[NG] = {};
+    for (int i = tid; i < a.T * a.n_kv * a.G * 32; i += kKv4Threads) {
+      const int row = i >> 5, t = row / (a.n_kv * a.G), hq = row - t * (a.n_kv * a.G);
+      store_row<NG>(a.out, b * a.out.slot + t * a.out.token + hq * a.out.head + (i & 31) * NG, z);
+    }
+    if (TRACK)
+      for (int i = tid; i < a.n_kv * a.rows; i += kKv4Threads)
+        a.lse[(int64_t)b * a.n_kv * a.rows + i] = INFINITY;
+  }
+  if (x0 >= x1) return;
+
+  // this warp's chunks are every eighth of each segment; its ring of bulk
+  // copies runs on across segments
+  const int64_t head_bytes = (int64_t)(a.l.cap / kKv4Chunk) * L::kChunk;
+  int px = x0, pc, pc1;            // producer: segment start, next chunk, segment end
+  const uint8_t *pbase;
+  Segment ps = segment_at(pre, a, px, x1);
+  auto enter = [&]() {
+    pc = ps.c0 + warp;
+    pc1 = ps.c1;
+    pbase = a.l.codes + ((int64_t)ps.b * a.n_kv + ps.h) * head_bytes;
+  };
+  enter();
+  int pstage = 0;
+  bool dead = false;
+  auto produce = [&]() {           // copy the warp's next chunk, if any, into stage pstage
+    while (pc >= pc1) {
+      px += ps.c1 - ps.c0;
+      if (px >= x1) return;
+      ps = segment_at(pre, a, px, x1);
+      enter();
+    }
+    if (lane == 0 && !dead) {
+      mbar_arrive_expect_tx(bars + pstage, L::kChunk);
+      bulk_g2s(ring + pstage * L::kChunk, pbase + (int64_t)pc * L::kChunk, L::kChunk, bars + pstage);
+    }
+    pc += kKv4Warps;
+    pstage = pstage + 1 == ST ? 0 : pstage + 1;
+  };
+#pragma unroll 1
+  for (int s = 0; s < ST; ++s) produce();
+
+  int stage = 0;
+  uint32_t phase = 0;
+  int x = x0;
+#pragma unroll 1
+  while (x < x1) {
+    const Segment sg = segment_at(pre, a, x, x1);
+    const int len = kv4_len(a.l, sg.b);
+
+    // queries of the row block: warp w takes row w.  Scaled to a largest
+    // magnitude of 2^10 (a power of two, undone in the scores), split into
+    // two fp16 and stored as the A operand: high parts in rows 0-7, low parts
+    // in rows 8-15.  The odd positions of each 8 dims carry 2^-4.
+    {
+      const int rr = sg.rb * kKv4Rows + warp;
+      float v[NG];
+      float mx = 0.f;
+      if (rr < a.rows) {
+        const int t = rr / a.G, hq = sg.h * a.G + (rr - t * a.G);
+        const int64_t at = sg.b * a.q.slot + t * a.q.token + hq * a.q.head + lane * NG;
+        if (a.q.dtype == PNB_F32) load_vals<float, NG>(static_cast<const float *>(a.q.p) + at, v);
+        else load_vals<__nv_bfloat16, NG>(static_cast<const __nv_bfloat16 *>(a.q.p) + at, v);
+      } else {
+#pragma unroll
+        for (int i = 0; i < NG; ++i) v[i] = 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < NG; ++i) {
+        v[i] *= a.qscale;
+        mx = fmaxf(mx, fabsf(v[i]));
+      }
+      mx = warp_max(mx);
+      int e = (int)(__float_as_uint(mx) >> 23) - 127;
+      e = min(max(e, -100), 100);
+      const float up = __uint_as_float((uint32_t)(10 - e + 127) << 23);
+      __half *qh = reinterpret_cast<__half *>(qf);
+      float sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < NG; ++i) {
+        const int d = lane * NG + i, g = d >> 5, cc = (d >> 3) & 3, n = d & 7;
+        const float s = (n & 1) ? 0.0625f : 1.f;
+        const float y = v[i] * up * s;
+        const __half hi = __float2half_rn(y);
+        const __half lo = __float2half_rn(y - __half2float(hi));
+        const int at = (((g * 2 + ((n & 3) >> 1)) * 32 + warp * 4 + cc) * 4 + (n & 1) * 2) * 2 + (n >> 2);
+        qh[at] = hi;
+        qh[at + 2] = lo;
+        sum += (__half2float(hi) + __half2float(lo)) * ((n & 1) ? 16.f : 1.f);
+      }
+#pragma unroll
+      for (int o = 1; o < 32 / NG; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      if ((lane & (32 / NG - 1)) == 0) srow[warp * (NG + 1) + lane / (32 / NG)] = sum * -0x1p-21f;
+      if (lane == 0) srow[warp * (NG + 1) + NG] = __uint_as_float((uint32_t)(24 + e - 10 + 127) << 23);
+    }
+    __syncthreads();
+    float nq[NG];   // -8 sum of the block's query entries, in units of the products (2^-24)
+#pragma unroll
+    for (int g = 0; g < NG; ++g) nq[g] = srow[r * (NG + 1) + g];
+    const float rs = srow[r * (NG + 1) + NG];
+    const int row = sg.rb * kKv4Rows + r;
+    const int limit_all = len - a.T + 1;                       // every row sees positions below it
+    const int limit = row < a.rows ? limit_all + row / a.G : 0;
+    float *score = nullptr;
+    if (TRACK && row < a.rows)
+      score = a.scores + (((int64_t)sg.b * a.n_kv + sg.h) * a.rows + row) * a.l.cap + 2 * c;
+
+    float o[NG * 4][4];
+#pragma unroll
+    for (int i = 0; i < NG * 4; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+    float2 acc[NG];                                            // sum of p d per block
+#pragma unroll
+    for (int g = 0; g < NG; ++g) acc[g] = make_float2(0.f, 0.f);
+    float2 l2 = make_float2(0.f, 0.f);
+    float m = -INFINITY;                                       // the row's reference maximum
+    int ev = -13;                                              // V scales seen are below 2^ev
+    float ref = -6.f - 13.f;
+
+#pragma unroll 1
+    for (int ch = sg.c0 + warp; ch < sg.c1; ch += kKv4Warps) {
+      if (!dead && !mbar_wait(bars + stage, phase)) {
+        // a wait that gave up: no more copies; those in flight get another
+        // bounded chance to land before the shared memory goes away
+        dead = true;
+        if (lane == 0) set_error(a.err, kErrTimeout);
+        for (int s = 0; s < ST; ++s)
+          mbar_wait(bars + (stage + s) % ST, stage + s < ST ? phase : phase ^ 1u);
+      }
+      const uint8_t *st = ring + stage * L::kChunk;
+      const int p0 = ch * kKv4Chunk;
+      const bool tail = p0 + kKv4Chunk > limit_all;
+
+      // scores of positions p0 + 8 t + 2 c + {0, 1}
+      float2 s2[4];
+      {
+        uint32_t kw[4][NG], ks[4][NG];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          lds_words<NG>(st + kv4_kword(NG, 8 * t + r, c, 0), kw[t]);
+          lds_words<NG>(st + kv4_kscale_off(NG) + (t * 4 + c) * 4 * NG, ks[t]);
+          s2[t] = make_float2(0.f, 0.f);
+        }
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+          const uint4 qa = qf[(g * 2) * 32 + lane], qb = qf[(g * 2 + 1) * 32 + lane];
+#pragma unroll
+          for (int t = 0; t < 4; ++t) {
+            float d[4] = {nq[g], nq[g], 0.f, 0.f};
+            uint32_t w = kw[t][g];
+            mma_f16(d, qa.x, qa.y, qa.z, qa.w, w & kMaskEven, w & kMaskOdd);
+            w >>= 8;
+            mma_f16(d, qb.x, qb.y, qb.z, qb.w, w & kMaskEven, w & kMaskOdd);
+            s2[t] = ffma2(add2(make_float2(d[0], d[1]), make_float2(d[2], d[3])), half2_pair(ks[t][g]),
+                          s2[t]);
+          }
+        }
+      }
+      // the largest V scale of the chunk (finite, inside the sequence) bounds
+      // what the fp16 products can reach
+      uint32_t hmax = 0;
+      {
+        constexpr int kWords = 16 * NG, kPer = (kWords + 31) / 32;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+          const int wi = lane * kPer + i;
+          if (wi < kWords) {
+            uint32_t w = *reinterpret_cast<const uint32_t *>(st + kv4_vscale_off(NG) + wi * 4);
+            if (tail) {
+              const int p = p0 + 2 * (wi / NG);
+              if (p >= len) w = 0;
+              else if (p + 1 >= len) w &= 0xffffu;
+            }
+            hmax = max(hmax, finite_half_max(w));
+          }
+        }
+        hmax = __reduce_max_sync(0xffffffffu, hmax);
+      }
+      if (tail) {
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          const int p = p0 + 8 * t + 2 * c;
+          if (p >= limit) s2[t].x = -INFINITY;
+          if (p + 1 >= limit) s2[t].y = -INFINITY;
+        }
+      }
+      float xm = -INFINITY;
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        if (TRACK && score)
+          *reinterpret_cast<float2 *>(score + p0 + 8 * t) = make_float2(s2[t].x * rs, s2[t].y * rs);
+        xm = fmaxf(xm, fmaxf(s2[t].x, s2[t].y));
+      }
+      xm = fmaxf(xm, __shfl_xor_sync(0xffffffffu, xm, 1));
+      xm = fmaxf(xm, __shfl_xor_sync(0xffffffffu, xm, 2)) * rs;
+      const int evc = (int)max(hmax >> 10, 1u) - 14;
+      // the reference moves only when a score exceeds it by 2^8 or a larger V
+      // scale arrives: p d stays below 2^14, inside fp16, and sums in fp32
+      // need no rescaling otherwise
+      if (__any_sync(0xffffffffu, xm > m + 8.f) || evc > ev) {
+        ev = max(ev, evc);
+        const float mn = fmaxf(m, xm);
+        const float nref = (mn == -INFINITY ? 0.f : mn) - 6.f + (float)ev;
+        const float al = m == -INFINITY ? 0.f : ex2(ref - nref);
+        m = mn;
+        ref = nref;
+        const float2 al2 = make_float2(al, al);
+        l2 = mul2(l2, al2);
+#pragma unroll
+        for (int g = 0; g < NG; ++g) acc[g] = mul2(acc[g], al2);
+#pragma unroll
+        for (int i = 0; i < NG * 4; ++i) {
+          o[i][0] *= al; o[i][1] *= al; o[i][2] *= al; o[i][3] *= al;
+        }
+      }
+      float2 p2[4];   // softmax weights; odd t carry 2^-4
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        const float rf = (t & 1) ? ref + 4.f : ref;
+        p2[t] = make_float2(ex2(fmaf(s2[t].x, rs, -rf)), ex2(fmaf(s2[t].y, rs, -rf)));
+        l2 = (t & 1) ? ffma2(p2[t], make_float2(16.f, 16.f), l2) : add2(l2, p2[t]);
+      }
+      uint32_t vs[4][NG];
+#pragma unroll
+      for (int t = 0; t < 4; ++t) lds_words<NG>(st + kv4_vscale_off(NG) + (t * 4 + c) * 4 * NG, vs[t]);
+#pragma unroll
+      for (int g = 0; g < NG; ++g) {
+        const uint4 vw = *reinterpret_cast<const uint4 *>(st + kv4_v_off(NG) + g * 512 + lane * 16);
+        const uint32_t w4[4] = {vw.x, vw.y, vw.z, vw.w};
+#pragma unroll
+        for (int kt = 0; kt < 2; ++kt) {
+          float2 w0 = mul2(p2[2 * kt], half2_pair(vs[2 * kt][g]));
+          float2 w1 = mul2(p2[2 * kt + 1], half2_pair(vs[2 * kt + 1][g]));
+          if (tail) {   // a masked position's scale is not the sequence's: it may be anything
+            const float2 q0 = p2[2 * kt], q1 = p2[2 * kt + 1];
+            w0 = make_float2(q0.x == 0.f ? 0.f : w0.x, q0.y == 0.f ? 0.f : w0.y);
+            w1 = make_float2(q1.x == 0.f ? 0.f : w1.x, q1.y == 0.f ? 0.f : w1.y);
+          }
+          acc[g] = add2(acc[g], w0);
+          acc[g] = ffma2(w1, make_float2(16.f, 16.f), acc[g]);
+          const uint32_t a0 = pack_half2(w0), a2 = pack_half2(w1);
+          uint32_t a1 = 0, a3 = 0;
+          if (SPLIT) {
+            const float2 h0 = half2_pair(a0), h1 = half2_pair(a2);
+            a1 = pack_half2(make_float2(w0.x - h0.x, w0.y - h0.y));
+            a3 = pack_half2(make_float2(w1.x - h1.x, w1.y - h1.y));
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t w = kt ? w4[i] >> 8 : w4[i];
+            mma_f16(o[g * 4 + i], a0, a1, a2, a3, w & kMaskEven, w & kMaskOdd);
+          }
+        }
+      }
+      __syncwarp();
+      produce();
+      stage = stage + 1 == ST ? 0 : stage + 1;
+      phase ^= stage == 0;
+    }
+
+    // this warp's rows: sum, reference and outputs (in units of 2^-24)
+    {
+      float l = l2.x + l2.y;
+      l += __shfl_xor_sync(0xffffffffu, l, 1);
+      l += __shfl_xor_sync(0xffffffffu, l, 2);
+      if (c == 0) sml[warp * kKv4Rows + r] = make_float2(ref, l);
+      float *od = so + (warp * kKv4Rows + r) * HD;
+#pragma unroll
+      for (int g = 0; g < NG; ++g) {
+        float s = acc[g].x + acc[g].y;
+        s += __shfl_xor_sync(0xffffffffu, s, 1);
+        s += __shfl_xor_sync(0xffffffffu, s, 2);
+        s *= 0x1p-21f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float *v = o[g * 4 + i];
+          // rows rotated by 8 floats each against bank conflicts
+          *reinterpret_cast<float2 *>(od + ((g * 32 + i * 8 + 2 * c + 8 * r) & (HD - 1))) =
+              make_float2(v[0] + v[2] - s, v[1] + v[3] - s);
+        }
+      }
+    }
+    __syncthreads();
+
+    // the CTA's rows: warp w adds up row w over the warps
+    const int my_row = sg.rb * kKv4Rows + warp;
+    float mref = -INFINITY, lsum = 0.f, os[NG];
+#pragma unroll
+    for (int i = 0; i < NG; ++i) os[i] = 0.f;
+#pragma unroll
+    for (int w = 0; w < kKv4Warps; ++w) {
+      const float2 ml = sml[w * kKv4Rows + warp];
+      if (ml.y != 0.f) mref = fmaxf(mref, ml.x);
+    }
+#pragma unroll
+    for (int w = 0; w < kKv4Warps; ++w) {
+      const float2 ml = sml[w * kKv4Rows + warp];
+      if (ml.y != 0.f) {
+        const float f = ex2(ml.x - mref);
+        lsum = fmaf(ml.y, f, lsum);
+        float v[NG];
+        load_vals<float, NG>(so + (w * kKv4Rows + warp) * HD + ((lane * NG + 8 * warp) & (HD - 1)), v);
+#pragma unroll
+        for (int i = 0; i < NG; ++i) os[i] = fmaf(v[i], f, os[i]);
+      }
+    }
+    auto finish = [&]() {   // the row's output, and its log-sum for the weights
+      if (my_row >= a.rows) return;
+      const int t = my_row / a.G, hq = sg.h * a.G + (my_row - t * a.G);
+      const float f = lsum != 0.f ? 0x1p24f / lsum : 0.f;
+#pragma unroll
+      for (int i = 0; i < NG; ++i) os[i] = lsum != 0.f ? os[i] * f : 0.f;
+      store_row<NG>(a.out, sg.b * a.out.slot + t * a.out.token + hq * a.out.head + lane * NG, os);
+      if (TRACK && lane == 0)
+        a.lse[((int64_t)sg.b * a.n_kv + sg.h) * a.rows + my_row] = lsum != 0.f ? mref + log2f(lsum) : INFINITY;
+    };
+    if (sg.c0 == 0 && sg.c1 == sg.nch) {
+      finish();
+    } else {
+      // the item is shared with other CTAs: leave the partial rows, and let
+      // the last CTA to arrive add them up in their order
+      const int item0 = x - sg.c0;                  // flat index of the item's first chunk
+      const int first = item0 / per_cta, last = (item0 + sg.nch - 1) / per_cta;
+      const int which = (cta == first && item0 != x0) ? 1 : 0;
+      const int64_t slot = (int64_t)(2 * cta + which) * kKv4Rows + warp;
+      float *pd = a.part + slot * HD + lane * NG;
+#pragma unroll
+      for (int i = 0; i < NG; ++i) pd[i] = os[i];
+      if (lane == 0) {
+        a.part_ml[slot * 2] = mref;
+        a.part_ml[slot * 2 + 1] = lsum;
+      }
+      __threadfence();
+      __syncthreads();
+      if (tid == 0) {
+        const unsigned n = atomicAdd(a.counter + first, 1u);
+        *sflag = n == (unsigned)(last - first);
+        if (*sflag) a.counter[first] = 0;
+      }
+      __syncthreads();
+      if (*sflag) {
+        __threadfence();
+        // item0 is the first CTA's first chunk or a later one: its partial is
+        // its first (0) or second (1) one; all others' is their first
+        const int which0 = item0 > first * per_cta ? 1 : 0;
+        auto at = [&](int i) {
+          return (int64_t)(2 * (first + i) + (i == 0 ? which0 : 0)) * kKv4Rows + warp;
+        };
+        const int n = last - first + 1;
+        float mr = -INFINITY;
+        for (int i = lane; i < n; i += 32) {
+          const float2 ml = __ldcg(reinterpret_cast<const float2 *>(a.part_ml + at(i) * 2));
+          if (ml.y != 0.f) mr = fmaxf(mr, ml.x);
+        }
+        mref = warp_max(mr);
+        lsum = 0.f;
+#pragma unroll
+        for (int i = 0; i < NG; ++i) os[i] = 0.f;
+#pragma unroll 4
+        for (int i = 0; i < n; ++i) {
+          const float2 ml = __ldcg(reinterpret_cast<const float2 *>(a.part_ml + at(i) * 2));
+          const float *pv = a.part + at(i) * HD + lane * NG;
+          float v[NG];
+#pragma unroll
+          for (int j = 0; j < NG; ++j) v[j] = __ldcg(pv + j);
+          if (ml.y != 0.f) {
+            const float f = ex2(ml.x - mref);
+            lsum = fmaf(ml.y, f, lsum);
+#pragma unroll
+            for (int j = 0; j < NG; ++j) os[j] = fmaf(v[j], f, os[j]);
+          }
+        }
+        finish();
+      }
+    }
+    x += sg.c1 - sg.c0;
+  }
+}
+
+// weights[j] = decay * weights[j] + sum over the rows of 2^(x_ij - lse_i): each
+// position has one owner that adds its rows in order.
+constexpr int kWeightThreads = 128, kWeightUnit = 4 * kWeightThreads;
+
+__global__ void __launch_bounds__(kWeightThreads) k_kv4_weights(const __grid_constant__ Kv4WeightArgs a) {
+  extern __shared__ int wpre[];
+  pdl_wait();
+  if (threadIdx.x < 32) kv4_prefix(a.l, a.n_slot, kWeightUnit, a.n_kv, wpre);
+  __syncthreads();
+  const int total = wpre[a.n_slot];
+  for (int u = blockIdx.x; u < total; u += gridDim.x) {
+    const int b = kv4_find(wpre, a.n_slot, u), rel = u - wpre[b];
+    const int per = (wpre[b + 1] - wpre[b]) / a.n_kv, h = rel / per;
+    const int len = kv4_len(a.l, b);
+    const int p = (rel - h * per) * kWeightUnit + 4 * (int)threadIdx.x;
+    if (p >= len) continue;
+    const int64_t bh = (int64_t)b * a.n_kv + h;
+    const float *x = a.scores + bh * a.rows * a.l.cap + p, *lse = a.lse + bh * a.rows;
+    float w[4] = {};
+#pragma unroll 4
+    for (int i = 0; i < a.rows; ++i) {
+      const float4 v = *reinterpret_cast<const float4 *>(x + (int64_t)i * a.l.cap);
+      const float z = lse[i];
+      w[0] += ex2(v.x - z); w[1] += ex2(v.y - z); w[2] += ex2(v.z - z); w[3] += ex2(v.w - z);
+    }
+    float *dst = a.l.weights + bh * a.l.cap + p;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (p + i < len) dst[i] = a.decay > 0.f ? fmaf(a.decay, dst[i], w[i]) : w[i];
+  }
+}
+
+template <int NG>
+cudaError_t prepare(int *grid) {
+  const int smem = AttnSmem<NG>::bytes(kKv4MaxSlots);
+  cudaError_t e = cudaSuccess;
+  auto set = [&](auto k) {
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  };
+  set(k_kv4_attn<NG, false, false>);
+  set(k_kv4_attn<NG, false, true>);
+  set(k_kv4_attn<NG, true, false>);
+  set(k_kv4_attn<NG, true, true>);
+  int dev = 0, sms = 0;
+  if (e == cudaSuccess) e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  *grid = sms * kKv4CtasPerSm;
+  return e;
+}
+
+template <int NG>
+cudaError_t run_attn(const Kv4AttnArgs &a, int grid, cudaStream_t st) {
+  const int smem = AttnSmem<NG>::bytes(a.n_slot);
+  const bool split = a.out.dtype == PNB_F32, track = a.scores != nullptr;
+  auto kern = split ? (track ? k_kv4_attn<NG, true, true> : k_kv4_attn<NG, true, false>)
+                    : (track ? k_kv4_attn<NG, false, true> : k_kv4_attn<NG, false, false>);
+  return kv4_launch(kern, dim3(grid), dim3(kKv4Threads), smem, 1, st, a);
+}
+
+}  // namespace
+
+cudaError_t prepare_kv4_kernels(int ng, int *attn_grid) {
+  return ng == 4 ? prepare<4>(attn_grid) : ng == 2 ? prepare<2>(attn_grid) : prepare<1>(attn_grid);
+}
+
+cudaError_t launch_kv4_attn(int ng, const Kv4AttnArgs &a, int grid, cudaStream_t st) {
+  return ng == 4 ? run_attn<4>(a, grid, st) : ng == 2 ? run_attn<2>(a, grid, st) : run_attn<1>(a, grid, st);
+}
+
+cudaError_t launch_kv4_weights(const Kv4WeightArgs &a, cudaStream_t st) {
+  const int64_t units = (int64_t)a.n_slot * a.n_kv * ((a.l.cap + kWeightUnit - 1) / kWeightUnit);
+  const int grid = (int)(units < 1216 ? units : 1216);   // 8 CTAs on each of 152 SMs
+  return kv4_launch(k_kv4_weights, dim3(grid), dim3(kWeightThreads), (a.n_slot + 1) * 4, 1, st, a);
+}
+
+}  // namespace pnb

@@ -1,0 +1,157 @@
+"""The 4-bit KV cache (pnb_kvq_*, include/pnb.h): append, read, attention, eviction.
+
+Like the rest of the binding it only marshals arguments.  The cache's buffer is
+a torch tensor; lengths, ids and weights are views of it.
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import Optional
+
+from . import (PNB_BF16, PNB_F32, PnbError, _ptr, _stream, check, pnb_kvq_append,
+               pnb_kvq_attention, pnb_kvq_bytes, pnb_kvq_check, pnb_kvq_config, pnb_kvq_evict,
+               pnb_kvq_free, pnb_kvq_layer_views, pnb_kvq_new, pnb_kvq_read, pnb_kvq_reset,
+               pnb_kvq_views, pnb_rows)
+
+
+class Kv4Cache:
+    """A pnb_kvq over a torch buffer (``buf``, allocated if None; reset() a new one).
+
+    Row tensors (k, v, q, out) are [n_slot][T][heads][head_dim], fp32 or bf16,
+    head_dim contiguous, other strides free as long as rows stay 16-byte aligned."""
+
+    def __init__(self, n_layer: int, n_slot: int, n_head: int, n_kv_head: int, head_dim: int,
+                 cap: int, track: int = 0, buf=None, device=None):
+        import torch
+
+        self._h = None
+        self.cfg = pnb_kvq_config(n_layer, n_slot, n_head, n_kv_head, head_dim, cap, track)
+        self._dtypes = {torch.float32: PNB_F32, torch.bfloat16: PNB_BF16}
+        nbytes = int(pnb_kvq_bytes(ctypes.byref(self.cfg)))
+        if buf is None:
+            buf = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=device or "cuda")
+        self.buf = buf
+        h = ctypes.c_void_p()
+        check(pnb_kvq_new(ctypes.byref(self.cfg), _ptr(buf), buf.numel() * buf.element_size(),
+                          ctypes.byref(h)), "pnb_kvq_new")
+        self._h = h.value
+        self._views = {}
+
+    def __del__(self):
+        if getattr(self, "_h", None):
+            pnb_kvq_free(self._h)
+            self._h = None
+
+    @property
+    def handle(self) -> int:
+        return self._h
+
+    def _rows(self, t, what: str, T: Optional[int], heads: int) -> pnb_rows:
+        g = self.cfg
+        shape = t.shape
+        if len(shape) != 4 or shape[0] != g.n_slot or shape[2] != heads or shape[3] != g.head_dim \
+                or (T is not None and shape[1] != T):
+            raise PnbError(-1, f"{what}: shape {tuple(shape)} is not [{g.n_slot}][{T or 'T'}]"
+                               f"[{heads}][{g.head_dim}]")
+        dt = self._dtypes.get(t.dtype)
+        s = t.stride()
+        if dt is None or s[3] != 1:
+            raise PnbError(-1, f"{what}: needs fp32 or bf16 rows with head_dim contiguous")
+        if t.device != self.buf.device:
+            raise PnbError(-10, f"{what}: on {t.device}, the cache is on {self.buf.device}")
+        # a dimension of one element has no stride of its own
+        return pnb_rows(t.data_ptr(), s[0] if shape[0] > 1 else 0, s[1] if shape[1] > 1 else 0,
+                        s[2] if heads > 1 else 0, dt)
+
+    def _ints(self, t, what: str):
+        if t is None:
+            return None
+        import torch
+        if t.dtype != torch.int32 or t.numel() != self.cfg.n_slot or not t.is_contiguous() \
+                or t.device != self.buf.device:
+            raise PnbError(-1, f"{what}: needs {self.cfg.n_slot} contiguous int32 on the cache's device")
+        return t.data_ptr()
+
+    def reset(self, slot: Optional[int] = None, stream=None):
+        """Empty one slot, or all of them (which also clears the error bits), in every layer."""
+        check(pnb_kvq_reset(self._h, -1 if slot is None else slot, _stream(stream)), "pnb_kvq_reset")
+
+    def append(self, layer: int, k, v, n_new=None, start=None, stream=None):
+        """Quantise and append n_new[b] (default: all T) rows of every slot b at entry
+        start[b] (default: its length).  n_new, start: device int32 [n_slot]."""
+        n = self.cfg.n_kv_head
+        rk = self._rows(k, "k", None, n)
+        rv = self._rows(v, "v", k.shape[1], n)
+        check(pnb_kvq_append(self._h, layer, ctypes.byref(rk), ctypes.byref(rv), k.shape[1],
+                             self._ints(n_new, "n_new"), self._ints(start, "start"),
+                             _stream(stream)), "pnb_kvq_append")
+
+    def read(self, layer: int, k, v, first=None, stream=None):
+        """Write the values of entries first[b] (default 0) .. + T - 1 into k and v."""
+        n = self.cfg.n_kv_head
+        rk = self._rows(k, "k", None, n)
+        rv = self._rows(v, "v", k.shape[1], n)
+        check(pnb_kvq_read(self._h, layer, self._ints(first, "first"), k.shape[1],
+                           ctypes.byref(rk), ctypes.byref(rv), _stream(stream)), "pnb_kvq_read")
+
+    def attention(self, layer: int, q, out, decay: Optional[float] = None, stream=None):
+        """Attention of the last T appended tokens' queries into ``out``; with ``decay``,
+        weights = decay * weights + this call's softmax weights."""
+        n = self.cfg.n_head
+        rq = self._rows(q, "q", None, n)
+        ro = self._rows(out, "out", q.shape[1], n)
+        if decay is None:
+            decay = -1.0
+        elif not decay >= 0.0:
+            raise PnbError(-1, f"decay {decay} is negative or not a number")
+        check(pnb_kvq_attention(self._h, layer, ctypes.byref(rq), q.shape[1], ctypes.byref(ro),
+                                decay, _stream(stream)), "pnb_kvq_attention")
+
+    def evict(self, layer: int, budget: int, n_sink: int = 0, n_recent: int = 0,
+              dst: Optional["Kv4Cache"] = None, dst_layer: Optional[int] = None, stream=None):
+        """Keep at most ``budget`` entries per slot and KV head, in place or into
+        (dst, dst_layer); see pnb_kvq_evict for which."""
+        d = self if dst is None else dst
+        check(pnb_kvq_evict(self._h, layer, d._h, layer if dst_layer is None else dst_layer, budget,
+                            n_sink, n_recent, _stream(stream)), "pnb_kvq_evict")
+
+    def _view(self, layer: int, name: str):
+        import torch
+
+        key = (layer, name)
+        if key not in self._views:
+            v = pnb_kvq_views()
+            check(pnb_kvq_layer_views(self._h, layer, ctypes.byref(v)), "pnb_kvq_layer_views")
+            g = self.cfg
+            shape = (g.n_slot,) if name in ("len", "seen") else (g.n_slot, g.n_kv_head, g.cap)
+            n = 1
+            for s in shape:
+                n *= s
+            at = getattr(v, name) - self.buf.data_ptr()
+            flat = self.buf.view(-1).view(torch.uint8)[at:at + 4 * n]
+            self._views[key] = flat.view(torch.float32 if name == "weights" else torch.int32).view(shape)
+        return self._views[key]
+
+    def lengths(self, layer: int):
+        """Entries held per slot (int32 [n_slot], a view of the buffer)."""
+        return self._view(layer, "len")
+
+    def seen(self, layer: int):
+        """Tokens ever appended per slot, the next entry's id (int32 [n_slot])."""
+        return self._view(layer, "seen")
+
+    def ids(self, layer: int):
+        """Original position of every entry (int32 [n_slot][n_kv_head][cap])."""
+        return self._view(layer, "ids")
+
+    def weights(self, layer: int):
+        """Accumulated attention weight of every entry (fp32 [n_slot][n_kv_head][cap])."""
+        return self._view(layer, "weights")
+
+    def device_error(self) -> int:
+        """Synchronise and read the device error bits (PNB_DEV_ERR_*)."""
+        e = ctypes.c_int32()
+        rc = pnb_kvq_check(self._h, ctypes.byref(e))
+        if rc not in (0, -8):
+            check(rc, "pnb_kvq_check")
+        return e.value
