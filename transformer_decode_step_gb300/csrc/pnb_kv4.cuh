@@ -10,11 +10,9 @@
 //
 // The codes lie as the attention kernel's matrix instructions (m16n8k16, fp16)
 // want their B operand, so that one 32-bit word of 8 codes becomes four
-// registers of two fp16 each with four masks and one shift:
-//   - a word's nibbles n and n + 4 are a pair: (w >> 4 n) & 0x000f000f is the
-//     pair as two fp16 subnormals u * 2^-24, exactly; for odd n the shift is
-//     left out and the pair stands for u * 2^-20 (the other operand carries
-//     the 2^-4);
+// registers of two fp16 each with four masks, one shift and four packed fp16
+// operations:
+//   - a word's nibbles n and n + 4 are a pair, in the two halves of the word;
 //   - K: a lane (r = lane / 4, c = lane % 4) holds position 8 t + r and, per
 //     32-dim block j, the word of dims 32 j + 8 c + n;
 //   - V: the lane holds dim 32 J + 8 i + r and the word whose nibble t + 4 e

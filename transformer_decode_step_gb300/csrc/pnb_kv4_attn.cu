@@ -3,11 +3,11 @@
 //
 // For the rows q_i of one KV head (the query heads of its group times the
 // call's tokens), with keys k_j = d_jg (u_j - 8) per 32-dim block g:
-//   x_ij = log2(e) / sqrt(hd) sum_g d_jg (sum_{n in g} q_in u_jn - 8 sum_{n in g} q_in)
+//   x_ij = log2(e) / sqrt(hd) sum_g d_jg sum_{n in g} q_in (u_jn - 8)
 //   o_i  = sum_j p_ij v_j / l_i,  p_ij = 2^(x_ij - ref_i),  l_i = sum_j p_ij
-// and the same for the values: sum_j (p_ij d_jg) u_jn - 8 sum_j p_ij d_jg.
+// and the same for the values: sum_j (p_ij d_jg) (u_jn - 8).
 // Codes never become scaled numbers: the matrix instructions multiply the
-// integers u (exact in fp16), so the only roundings are those of the fp32
+// integers u - 8 (exact in fp16), so the only roundings are those of the fp32
 // operand's split into two fp16 (22 bits) and of the fp32 sums.
 #include <cuda_fp16.h>
 
@@ -17,7 +17,6 @@ namespace pnb {
 
 namespace {
 
-constexpr uint32_t kMaskEven = 0x000f000fu, kMaskOdd = 0x00f000f0u;
 // chunks a CTA takes at least (one per warp): below it a call uses fewer CTAs
 constexpr int kMinChunks = kKv4Warps;
 
@@ -31,8 +30,8 @@ struct AttnSmem {
   static constexpr int kO = kQ + NG * 2 * 32 * 16;                  // float [warps][8][kHd]
   static constexpr int kMl = kO + kKv4Warps * kKv4Rows * kHd * 4;   // float2 [warps][8]
   static constexpr int kBars = kMl + kKv4Warps * kKv4Rows * 8;
-  static constexpr int kRow = kBars + kKv4Warps * kStages * 8;      // float [8][NG + 1]
-  static constexpr int kFlag = kRow + kKv4Rows * (NG + 1) * 4;
+  static constexpr int kRow = kBars + kKv4Warps * kStages * 8;      // float [8]
+  static constexpr int kFlag = kRow + kKv4Rows * 4;
   static constexpr int kPre = kFlag + 16;                           // int [n_slot + 1]
   static int bytes(int n_slot) { return kPre + (n_slot + 1) * 4; }
 };
@@ -43,6 +42,26 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
       "{%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// The code pairs of a word as fp16 pairs u - 8, exactly: nibbles 0 and 4
+// (b[0]), 1 and 5 (b[1]), 2 and 6 (b[2]), 3 and 7 (b[3]).  A masked nibble
+// under the exponent of 1024 is the number 1024 + u (or 1024 + 16 u), and one
+// packed operation takes the rest away.  (Left as subnormals u * 2^-24, which
+// saves that operation, the codes lose up to 10 bits in the matrix
+// instruction's alignment: outputs were 8e-5 off instead of 1e-6.)
+__device__ __forceinline__ void code_pairs(uint32_t w, uint32_t (&b)[4]) {
+  const __half2 off = __half2half2(__ushort_as_half(0x6408)), sixteenth = __half2half2(__ushort_as_half(0x2c00)),
+                m72 = __half2half2(__ushort_as_half(0xd480));
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t lo = (w & 0x000f000fu) | 0x64006400u, hi = (w & 0x00f000f0u) | 0x64006400u;
+    const __half2 l = __hsub2(*reinterpret_cast<const __half2 *>(&lo), off);
+    const __half2 h = __hfma2(*reinterpret_cast<const __half2 *>(&hi), sixteenth, m72);
+    b[2 * i] = *reinterpret_cast<const uint32_t *>(&l);
+    b[2 * i + 1] = *reinterpret_cast<const uint32_t *>(&h);
+    w >>= 8;
+  }
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -225,7 +244,7 @@ __global__ void __launch_bounds__(kKv4Threads, kKv4CtasPerSm)
     // queries of the row block: warp w takes row w.  Scaled to a largest
     // magnitude of 2^10 (a power of two, undone in the scores), split into
     // two fp16 and stored as the A operand: high parts in rows 0-7, low parts
-    // in rows 8-15.  The odd positions of each 8 dims carry 2^-4.
+    // in rows 8-15.
     {
       const int rr = sg.rb * kKv4Rows + warp;
       float v[NG];
@@ -249,29 +268,20 @@ __global__ void __launch_bounds__(kKv4Threads, kKv4CtasPerSm)
       e = min(max(e, -100), 100);
       const float up = __uint_as_float((uint32_t)(10 - e + 127) << 23);
       __half *qh = reinterpret_cast<__half *>(qf);
-      float sum = 0.f;
 #pragma unroll
       for (int i = 0; i < NG; ++i) {
         const int d = lane * NG + i, g = d >> 5, cc = (d >> 3) & 3, n = d & 7;
-        const float s = (n & 1) ? 0.0625f : 1.f;
-        const float y = v[i] * up * s;
+        const float y = v[i] * up;
         const __half hi = __float2half_rn(y);
         const __half lo = __float2half_rn(y - __half2float(hi));
         const int at = (((g * 2 + ((n & 3) >> 1)) * 32 + warp * 4 + cc) * 4 + (n & 1) * 2) * 2 + (n >> 2);
         qh[at] = hi;
         qh[at + 2] = lo;
-        sum += (__half2float(hi) + __half2float(lo)) * ((n & 1) ? 16.f : 1.f);
       }
-#pragma unroll
-      for (int o = 1; o < 32 / NG; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      if ((lane & (32 / NG - 1)) == 0) srow[warp * (NG + 1) + lane / (32 / NG)] = sum * -0x1p-21f;
-      if (lane == 0) srow[warp * (NG + 1) + NG] = __uint_as_float((uint32_t)(24 + e - 10 + 127) << 23);
+      if (lane == 0) srow[warp] = __uint_as_float((uint32_t)(e - 10 + 127) << 23);
     }
     __syncthreads();
-    float nq[NG];   // -8 sum of the block's query entries, in units of the products (2^-24)
-#pragma unroll
-    for (int g = 0; g < NG; ++g) nq[g] = srow[r * (NG + 1) + g];
-    const float rs = srow[r * (NG + 1) + NG];
+    const float rs = srow[r];
     const int row = sg.rb * kKv4Rows + r;
     const int limit_all = len - a.T + 1;                       // every row sees positions below it
     const int limit = row < a.rows ? limit_all + row / a.G : 0;
@@ -282,9 +292,6 @@ __global__ void __launch_bounds__(kKv4Threads, kKv4CtasPerSm)
     float o[NG * 4][4];
 #pragma unroll
     for (int i = 0; i < NG * 4; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-    float2 acc[NG];                                            // sum of p d per block
-#pragma unroll
-    for (int g = 0; g < NG; ++g) acc[g] = make_float2(0.f, 0.f);
     float2 l2 = make_float2(0.f, 0.f);
     float m = -INFINITY;                                       // the row's reference maximum
     int ev = -13;                                              // V scales seen are below 2^ev
@@ -319,11 +326,11 @@ __global__ void __launch_bounds__(kKv4Threads, kKv4CtasPerSm)
           const uint4 qa = qf[(g * 2) * 32 + lane], qb = qf[(g * 2 + 1) * 32 + lane];
 #pragma unroll
           for (int t = 0; t < 4; ++t) {
-            float d[4] = {nq[g], nq[g], 0.f, 0.f};
-            uint32_t w = kw[t][g];
-            mma_f16(d, qa.x, qa.y, qa.z, qa.w, w & kMaskEven, w & kMaskOdd);
-            w >>= 8;
-            mma_f16(d, qb.x, qb.y, qb.z, qb.w, w & kMaskEven, w & kMaskOdd);
+            float d[4] = {};
+            uint32_t u[4];
+            code_pairs(kw[t][g], u);
+            mma_f16(d, qa.x, qa.y, qa.z, qa.w, u[0], u[1]);
+            mma_f16(d, qb.x, qb.y, qb.z, qb.w, u[2], u[3]);
             s2[t] = ffma2(add2(make_float2(d[0], d[1]), make_float2(d[2], d[3])), half2_pair(ks[t][g]),
                           s2[t]);
           }
@@ -380,18 +387,15 @@ __global__ void __launch_bounds__(kKv4Threads, kKv4CtasPerSm)
         const float2 al2 = make_float2(al, al);
         l2 = mul2(l2, al2);
 #pragma unroll
-        for (int g = 0; g < NG; ++g) acc[g] = mul2(acc[g], al2);
-#pragma unroll
         for (int i = 0; i < NG * 4; ++i) {
           o[i][0] *= al; o[i][1] *= al; o[i][2] *= al; o[i][3] *= al;
         }
       }
-      float2 p2[4];   // softmax weights; odd t carry 2^-4
+      float2 p2[4];   // softmax weights
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
-        const float rf = (t & 1) ? ref + 4.f : ref;
-        p2[t] = make_float2(ex2(fmaf(s2[t].x, rs, -rf)), ex2(fmaf(s2[t].y, rs, -rf)));
-        l2 = (t & 1) ? ffma2(p2[t], make_float2(16.f, 16.f), l2) : add2(l2, p2[t]);
+        p2[t] = make_float2(ex2(fmaf(s2[t].x, rs, -ref)), ex2(fmaf(s2[t].y, rs, -ref)));
+        l2 = add2(l2, p2[t]);
       }
       uint32_t vs[4][NG];
 #pragma unroll
@@ -399,7 +403,11 @@ __global__ void __launch_bounds__(kKv4Threads, kKv4CtasPerSm)
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
         const uint4 vw = *reinterpret_cast<const uint4 *>(st + kv4_v_off(NG) + g * 512 + lane * 16);
-        const uint32_t w4[4] = {vw.x, vw.y, vw.z, vw.w};
+        uint32_t u[4][4];
+        code_pairs(vw.x, u[0]);
+        code_pairs(vw.y, u[1]);
+        code_pairs(vw.z, u[2]);
+        code_pairs(vw.w, u[3]);
 #pragma unroll
         for (int kt = 0; kt < 2; ++kt) {
           float2 w0 = mul2(p2[2 * kt], half2_pair(vs[2 * kt][g]));
@@ -409,8 +417,6 @@ __global__ void __launch_bounds__(kKv4Threads, kKv4CtasPerSm)
             w0 = make_float2(q0.x == 0.f ? 0.f : w0.x, q0.y == 0.f ? 0.f : w0.y);
             w1 = make_float2(q1.x == 0.f ? 0.f : w1.x, q1.y == 0.f ? 0.f : w1.y);
           }
-          acc[g] = add2(acc[g], w0);
-          acc[g] = ffma2(w1, make_float2(16.f, 16.f), acc[g]);
           const uint32_t a0 = pack_half2(w0), a2 = pack_half2(w1);
           uint32_t a1 = 0, a3 = 0;
           if (SPLIT) {
@@ -419,10 +425,7 @@ __global__ void __launch_bounds__(kKv4Threads, kKv4CtasPerSm)
             a3 = pack_half2(make_float2(w1.x - h1.x, w1.y - h1.y));
           }
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint32_t w = kt ? w4[i] >> 8 : w4[i];
-            mma_f16(o[g * 4 + i], a0, a1, a2, a3, w & kMaskEven, w & kMaskOdd);
-          }
+          for (int i = 0; i < 4; ++i) mma_f16(o[g * 4 + i], a0, a1, a2, a3, u[i][2 * kt], u[i][2 * kt + 1]);
         }
       }
       __syncwarp();
@@ -431,7 +434,7 @@ __global__ void __launch_bounds__(kKv4Threads, kKv4CtasPerSm)
       phase ^= stage == 0;
     }
 
-    // this warp's rows: sum, reference and outputs (in units of 2^-24)
+    // this warp's rows: sum, reference and outputs
     {
       float l = l2.x + l2.y;
       l += __shfl_xor_sync(0xffffffffu, l, 1);
@@ -439,19 +442,10 @@ __global__ void __launch_bounds__(kKv4Threads, kKv4CtasPerSm)
       if (c == 0) sml[warp * kKv4Rows + r] = make_float2(ref, l);
       float *od = so + (warp * kKv4Rows + r) * HD;
 #pragma unroll
-      for (int g = 0; g < NG; ++g) {
-        float s = acc[g].x + acc[g].y;
-        s += __shfl_xor_sync(0xffffffffu, s, 1);
-        s += __shfl_xor_sync(0xffffffffu, s, 2);
-        s *= 0x1p-21f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float *v = o[g * 4 + i];
-          // rows rotated by 8 floats each against bank conflicts
-          *reinterpret_cast<float2 *>(od + ((g * 32 + i * 8 + 2 * c + 8 * r) & (HD - 1))) =
-              make_float2(v[0] + v[2] - s, v[1] + v[3] - s);
-        }
-      }
+      for (int i = 0; i < NG * 4; ++i)
+        // rows rotated by 8 floats each against bank conflicts
+        *reinterpret_cast<float2 *>(od + ((i * 8 + 2 * c + 8 * r) & (HD - 1))) =
+            make_float2(o[i][0] + o[i][2], o[i][1] + o[i][3]);
     }
     __syncthreads();
 
@@ -480,7 +474,7 @@ __global__ void __launch_bounds__(kKv4Threads, kKv4CtasPerSm)
     auto finish = [&]() {   // the row's output, and its log-sum for the weights
       if (my_row >= a.rows) return;
       const int t = my_row / a.G, hq = sg.h * a.G + (my_row - t * a.G);
-      const float f = lsum != 0.f ? 0x1p24f / lsum : 0.f;
+      const float f = lsum != 0.f ? 1.f / lsum : 0.f;
 #pragma unroll
       for (int i = 0; i < NG; ++i) os[i] = lsum != 0.f ? os[i] * f : 0.f;
       store_row<NG>(a.out, sg.b * a.out.slot + t * a.out.token + hq * a.out.head + lane * NG, os);
