@@ -44,18 +44,35 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// the same with a zero accumulator
+__device__ __forceinline__ void mma_f16_new(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                            uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
 // The code pairs of a word as fp16 pairs u - 8, exactly: nibbles 0 and 4
 // (b[0]), 1 and 5 (b[1]), 2 and 6 (b[2]), 3 and 7 (b[3]).  A masked nibble
 // under the exponent of 1024 is the number 1024 + u (or 1024 + 16 u), and one
 // packed operation takes the rest away.  (Left as subnormals u * 2^-24, which
 // saves that operation, the codes lose up to 10 bits in the matrix
-// instruction's alignment: outputs were 8e-5 off instead of 1e-6.)
-__device__ __forceinline__ void code_pairs(uint32_t w, uint32_t (&b)[4]) {
+// instruction's alignment: outputs were 8e-5 off instead of 1e-6.)  `magic` is
+// 0x64006400 in a register: as a second immediate it would cost a second
+// logic instruction per mask.
+__device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t mask, uint32_t magic) {
+  uint32_t d;
+  asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(d) : "r"(w), "r"(mask), "r"(magic));
+  return d;
+}
+
+__device__ __forceinline__ void code_pairs(uint32_t w, uint32_t magic, uint32_t (&b)[4]) {
   const __half2 off = __half2half2(__ushort_as_half(0x6408)), sixteenth = __half2half2(__ushort_as_half(0x2c00)),
                 m72 = __half2half2(__ushort_as_half(0xd480));
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    const uint32_t lo = (w & 0x000f000fu) | 0x64006400u, hi = (w & 0x00f000f0u) | 0x64006400u;
+    const uint32_t lo = and_or(w, 0x000f000fu, magic), hi = and_or(w, 0x00f000f0u, magic);
     const __half2 l = __hsub2(*reinterpret_cast<const __half2 *>(&lo), off);
     const __half2 h = __hfma2(*reinterpret_cast<const __half2 *>(&hi), sixteenth, m72);
     b[2 * i] = *reinterpret_cast<const uint32_t *>(&l);
@@ -86,9 +103,9 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
   return *reinterpret_cast<float2 *>(&d);
 }
 
-__device__ __forceinline__ float2 half2_pair(uint32_t w) {
-  return __half22float2(*reinterpret_cast<const __half2 *>(&w));
-}
+__device__ __forceinline__ __half2 as_half2(uint32_t w) { return *reinterpret_cast<const __half2 *>(&w); }
+__device__ __forceinline__ uint32_t as_word(__half2 h) { return *reinterpret_cast<const uint32_t *>(&h); }
+__device__ __forceinline__ float2 half2_pair(uint32_t w) { return __half22float2(as_half2(w)); }
 
 __device__ __forceinline__ uint32_t pack_half2(float2 v) {
   const __half2 h = __floats2half2_rn(v.x, v.y);
@@ -236,6 +253,8 @@ __global__ void __launch_bounds__(kKv4Threads, kKv4CtasPerSm)
   int stage = 0;
   uint32_t phase = 0;
   int x = x0;
+  uint32_t magic = 0x64006400u;
+  asm volatile("" : "+r"(magic));
 #pragma unroll 1
   while (x < x1) {
     const Segment sg = segment_at(pre, a, x, x1);
@@ -294,8 +313,8 @@ __global__ void __launch_bounds__(kKv4Threads, kKv4CtasPerSm)
     for (int i = 0; i < NG * 4; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
     float2 l2 = make_float2(0.f, 0.f);
     float m = -INFINITY;                                       // the row's reference maximum
-    int ev = -13;                                              // V scales seen are below 2^ev
-    float ref = -6.f - 13.f;
+    int ev = -1;                                               // V scales seen are below 2^ev
+    float ref = -11.f;
 
 #pragma unroll 1
     for (int ch = sg.c0 + warp; ch < sg.c1; ch += kKv4Warps) {
@@ -326,10 +345,10 @@ __global__ void __launch_bounds__(kKv4Threads, kKv4CtasPerSm)
           const uint4 qa = qf[(g * 2) * 32 + lane], qb = qf[(g * 2 + 1) * 32 + lane];
 #pragma unroll
           for (int t = 0; t < 4; ++t) {
-            float d[4] = {};
+            float d[4];
             uint32_t u[4];
-            code_pairs(kw[t][g], u);
-            mma_f16(d, qa.x, qa.y, qa.z, qa.w, u[0], u[1]);
+            code_pairs(kw[t][g], magic, u);
+            mma_f16_new(d, qa.x, qa.y, qa.z, qa.w, u[0], u[1]);
             mma_f16(d, qb.x, qb.y, qb.z, qb.w, u[2], u[3]);
             s2[t] = ffma2(add2(make_float2(d[0], d[1]), make_float2(d[2], d[3])), half2_pair(ks[t][g]),
                           s2[t]);
@@ -373,14 +392,15 @@ __global__ void __launch_bounds__(kKv4Threads, kKv4CtasPerSm)
       }
       xm = fmaxf(xm, __shfl_xor_sync(0xffffffffu, xm, 1));
       xm = fmaxf(xm, __shfl_xor_sync(0xffffffffu, xm, 2)) * rs;
-      const int evc = (int)max(hmax >> 10, 1u) - 14;
-      // the reference moves only when a score exceeds it by 2^8 or a larger V
-      // scale arrives: p d stays below 2^14, inside fp16, and sums in fp32
-      // need no rescaling otherwise
-      if (__any_sync(0xffffffffu, xm > m + 8.f) || evc > ev) {
+      const int evc = (int)(hmax >> 10) - 14;
+      // The weights are scaled by 2^(10 - ev), V scales lying below 2^ev with
+      // ev >= -1, and the reference moves only when a score exceeds it by 2^4
+      // or a larger V scale arrives: p stays below 2^15 and p d below 2^14,
+      // inside fp16, and the fp32 sums need no rescaling otherwise.
+      if (__any_sync(0xffffffffu, xm > m + 4.f) || evc > ev) {
         ev = max(ev, evc);
         const float mn = fmaxf(m, xm);
-        const float nref = (mn == -INFINITY ? 0.f : mn) - 6.f + (float)ev;
+        const float nref = (mn == -INFINITY ? 0.f : mn) - 10.f + (float)ev;
         const float al = m == -INFINITY ? 0.f : ex2(ref - nref);
         m = mn;
         ref = nref;
@@ -397,35 +417,49 @@ __global__ void __launch_bounds__(kKv4Threads, kKv4CtasPerSm)
         p2[t] = make_float2(ex2(fmaf(s2[t].x, rs, -ref)), ex2(fmaf(s2[t].y, rs, -ref)));
         l2 = add2(l2, p2[t]);
       }
+      // p d as fp16: w = p_hi d, rounded, and for SPLIT the rest of the exact
+      // product, its residual (one fma) + p_lo d
+      uint32_t ph[4], pl[4];
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        ph[t] = pack_half2(p2[t]);
+        if (SPLIT) {
+          const float2 h = half2_pair(ph[t]);
+          pl[t] = pack_half2(make_float2(p2[t].x - h.x, p2[t].y - h.y));
+        }
+      }
       uint32_t vs[4][NG];
 #pragma unroll
-      for (int t = 0; t < 4; ++t) lds_words<NG>(st + kv4_vscale_off(NG) + (t * 4 + c) * 4 * NG, vs[t]);
+      for (int t = 0; t < 4; ++t) {
+        lds_words<NG>(st + kv4_vscale_off(NG) + (t * 4 + c) * 4 * NG, vs[t]);
+        if (tail) {   // a masked position's scale may be anything: its weight is 0, not 0 times it
+          const int p = p0 + 8 * t + 2 * c;
+          const uint32_t seen = p >= limit ? 0u : (p + 1 >= limit ? 0xffffu : 0xffffffffu);
+#pragma unroll
+          for (int g = 0; g < NG; ++g) vs[t][g] &= seen;
+        }
+      }
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
         const uint4 vw = *reinterpret_cast<const uint4 *>(st + kv4_v_off(NG) + g * 512 + lane * 16);
         uint32_t u[4][4];
-        code_pairs(vw.x, u[0]);
-        code_pairs(vw.y, u[1]);
-        code_pairs(vw.z, u[2]);
-        code_pairs(vw.w, u[3]);
+        code_pairs(vw.x, magic, u[0]);
+        code_pairs(vw.y, magic, u[1]);
+        code_pairs(vw.z, magic, u[2]);
+        code_pairs(vw.w, magic, u[3]);
 #pragma unroll
         for (int kt = 0; kt < 2; ++kt) {
-          float2 w0 = mul2(p2[2 * kt], half2_pair(vs[2 * kt][g]));
-          float2 w1 = mul2(p2[2 * kt + 1], half2_pair(vs[2 * kt + 1][g]));
-          if (tail) {   // a masked position's scale is not the sequence's: it may be anything
-            const float2 q0 = p2[2 * kt], q1 = p2[2 * kt + 1];
-            w0 = make_float2(q0.x == 0.f ? 0.f : w0.x, q0.y == 0.f ? 0.f : w0.y);
-            w1 = make_float2(q1.x == 0.f ? 0.f : w1.x, q1.y == 0.f ? 0.f : w1.y);
-          }
-          const uint32_t a0 = pack_half2(w0), a2 = pack_half2(w1);
-          uint32_t a1 = 0, a3 = 0;
-          if (SPLIT) {
-            const float2 h0 = half2_pair(a0), h1 = half2_pair(a2);
-            a1 = pack_half2(make_float2(w0.x - h0.x, w0.y - h0.y));
-            a3 = pack_half2(make_float2(w1.x - h1.x, w1.y - h1.y));
+          uint32_t hi[2], lo[2] = {0, 0};
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const __half2 d = as_half2(vs[2 * kt + e][g]), p = as_half2(ph[2 * kt + e]);
+            const __half2 w = __hmul2_rn(p, d);
+            hi[e] = as_word(w);
+            if (SPLIT) lo[e] = as_word(__hfma2(as_half2(pl[2 * kt + e]), d, __hfma2(p, d, __hneg2(w))));
           }
 #pragma unroll
-          for (int i = 0; i < 4; ++i) mma_f16(o[g * 4 + i], a0, a1, a2, a3, u[i][2 * kt], u[i][2 * kt + 1]);
+          for (int i = 0; i < 4; ++i)
+            mma_f16(o[g * 4 + i], hi[0], lo[0], hi[1], lo[1], u[i][2 * kt], u[i][2 * kt + 1]);
         }
       }
       __syncwarp();
