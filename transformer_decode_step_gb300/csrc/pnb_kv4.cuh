@@ -96,8 +96,9 @@ struct Kv4AttnArgs {
   Kv4Rows q, out;
   int32_t n_slot, n_kv, G, T, rows, nrb;  // rows = T * G, nrb = row blocks of kKv4Rows
   float qscale;                   // log2(e) / sqrt(head_dim)
-  float *part;                    // [2 grid][kKv4Rows][head_dim]
-  float *part_ml;                 // [2 grid][kKv4Rows][2]: reference, sum
+  float *warp_part;               // [grid][kKv4Warps][kKv4Rows][head_dim]: rows a warp puts aside
+  float *part;                    // [2 grid][kKv4Rows][head_dim]: a CTA's partial rows
+  float *part_ml;                 // [2 grid][kKv4Rows][2]: their reference and sum
   unsigned *counter;              // [grid]
   int32_t *err;
   float *scores;                  // [n_slot][n_kv][rows][cap], log2 units (NULL: not tracked)
@@ -163,14 +164,18 @@ __device__ __forceinline__ int kv4_len(const Kv4Layer &l, int b) {
   return n < 0 ? 0 : (n > l.cap ? l.cap : n);
 }
 
-// Prefix sums over the slots of mult * ceil(len / unit) into pre[0 .. n_slot]
-// (shared memory), by the calling warp; the caller synchronises.
-__device__ __forceinline__ void kv4_prefix(const Kv4Layer &l, int n_slot, int unit, int mult, int *pre) {
+// Prefix sums over the slots of mult * (ceil(len / unit) + extra), 0 for an
+// empty slot, into pre[0 .. n_slot] (shared memory), and the lengths into lens
+// when given, by the calling warp; the caller synchronises.
+__device__ __forceinline__ void kv4_prefix(const Kv4Layer &l, int n_slot, int unit, int extra, int mult, int *pre,
+                                           int *lens) {
   const int lane = threadIdx.x & 31;
   int base = 0;
   for (int b0 = 0; b0 < n_slot; b0 += 32) {
     const int b = b0 + lane;
-    int v = b < n_slot ? mult * ((kv4_len(l, b) + unit - 1) / unit) : 0;
+    const int n = b < n_slot ? kv4_len(l, b) : 0;
+    if (lens && b < n_slot) lens[b] = n;
+    int v = n > 0 ? mult * ((n + unit - 1) / unit + extra) : 0;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int u = __shfl_up_sync(0xffffffffu, v, o);

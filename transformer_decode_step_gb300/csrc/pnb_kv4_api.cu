@@ -17,7 +17,7 @@ struct pnb_kvq {
   // byte offsets within a layer, and a layer's bytes
   size_t o_ids = 0, o_weights = 0, o_len = 0, o_seen = 0, layer_bytes = 0;
   uint8_t *ws = nullptr;
-  float *part = nullptr, *part_ml = nullptr, *scores = nullptr, *lse = nullptr;
+  float *part = nullptr, *part_ml = nullptr, *warp_part = nullptr, *scores = nullptr, *lse = nullptr;
   unsigned *counter = nullptr;
   uint32_t *arrive = nullptr;
   int32_t *err = nullptr, *n_old = nullptr, *src_of = nullptr, *movers = nullptr;
@@ -39,7 +39,7 @@ int check_config(const pnb_kvq_config &c) {
       c.n_kv_head > 1024 || c.n_layer > 4096 || c.cap > kKv4MaxCap)
     return PNB_E_UNSUPPORTED;
   // the flat list of work chunks is indexed with 32 bits
-  const int64_t chunks = (int64_t)c.n_slot * c.n_kv_head * (c.cap / kKv4Chunk);
+  const int64_t chunks = (int64_t)c.n_slot * c.n_kv_head * (c.cap / kKv4Chunk + 1);
   if (chunks * (kKv4MaxRows / kKv4Rows) >= (int64_t)1 << 31) return PNB_E_UNSUPPORTED;
   return PNB_OK;
 }
@@ -151,6 +151,7 @@ int pnb_kvq_new(const pnb_kvq_config *cfg, void *buf_dev, size_t bytes, pnb_kvq 
   const size_t zeroed = at;
   const size_t o_nold = take(4 * (size_t)c.n_slot), o_ml = take(part_rows * 8);
   const size_t o_part = take(part_rows * c.head_dim * 4);
+  const size_t o_wpart = take(part_rows / 2 * kKv4Warps * c.head_dim * 4);
   const size_t o_src = take(entries * 4), o_mov = take(entries * 4);
   const size_t o_lse = take(rows * 4), o_scores = take(rows * c.cap * 4);
   cudaError_t e = cudaMalloc(&k->ws, at);
@@ -167,6 +168,7 @@ int pnb_kvq_new(const pnb_kvq_config *cfg, void *buf_dev, size_t bytes, pnb_kvq 
   k->n_old = reinterpret_cast<int32_t *>(k->ws + o_nold);
   k->part_ml = reinterpret_cast<float *>(k->ws + o_ml);
   k->part = reinterpret_cast<float *>(k->ws + o_part);
+  k->warp_part = reinterpret_cast<float *>(k->ws + o_wpart);
   k->src_of = reinterpret_cast<int32_t *>(k->ws + o_src);
   k->movers = reinterpret_cast<int32_t *>(k->ws + o_mov);
   k->lse = reinterpret_cast<float *>(k->ws + o_lse);
@@ -265,6 +267,7 @@ int pnb_kvq_attention(pnb_kvq *c, int32_t layer, const pnb_rows *q, int32_t T, c
   a.qscale = (float)(1.4426950408889634 / std::sqrt((double)g.head_dim));
   a.part = c->part;
   a.part_ml = c->part_ml;
+  a.warp_part = c->warp_part;
   a.counter = c->counter;
   a.err = c->err;
   a.scores = track ? c->scores : nullptr;

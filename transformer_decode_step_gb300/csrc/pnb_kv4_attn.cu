@@ -17,8 +17,11 @@ namespace pnb {
 
 namespace {
 
-// chunks a CTA takes at least (one per warp): below it a call uses fewer CTAs
-constexpr int kMinChunks = kKv4Warps;
+// Work units: an item (slot, KV head, block of 8 query rows) takes one per
+// chunk of 32 positions and kItemUnits more for its queries and its end.
+constexpr int kItemUnits = 1;
+// units a warp takes at least: below it a call uses fewer warps
+constexpr int kMinUnits = 2;
 
 template <int NG>
 struct AttnSmem {
@@ -26,14 +29,13 @@ struct AttnSmem {
   static constexpr int kStages = NG == 4 ? 2 : 4;
   static constexpr int kChunk = kv4_chunk_bytes(NG);
   static constexpr int kRing = kKv4Warps * kStages * kChunk;
-  static constexpr int kQ = kRing;                                  // uint4 [NG][2][32]
-  static constexpr int kO = kQ + NG * 2 * 32 * 16;                  // float [warps][8][kHd]
-  static constexpr int kMl = kO + kKv4Warps * kKv4Rows * kHd * 4;   // float2 [warps][8]
-  static constexpr int kBars = kMl + kKv4Warps * kKv4Rows * 8;
-  static constexpr int kRow = kBars + kKv4Warps * kStages * 8;      // float [8]
-  static constexpr int kFlag = kRow + kKv4Rows * 4;
+  static constexpr int kQ = kRing;                                  // uint4 [warps][NG][2][32]
+  static constexpr int kBars = kQ + kKv4Warps * NG * 2 * 32 * 16;
+  static constexpr int kPart = kBars + kKv4Warps * kStages * 8;     // int [2 warps]: item of each partial
+  static constexpr int kMl = kPart + kKv4Warps * 2 * 4;             // float2 [2 warps][8]: reference, sum
+  static constexpr int kFlag = kMl + kKv4Warps * 2 * kKv4Rows * 8;
   static constexpr int kPre = kFlag + 16;                           // int [n_slot + 1]
-  static int bytes(int n_slot) { return kPre + (n_slot + 1) * 4; }
+  static int bytes(int n_slot) { return kPre + (2 * n_slot + 1) * 4; }   // and the lengths
 };
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -133,22 +135,26 @@ __device__ __forceinline__ uint32_t finite_half_max(uint32_t w) {
   return a > b ? a : b;
 }
 
-// A CTA's part of the flat chunk list that lies in one item (slot, KV head,
-// row block): chunks [c0, c1) of the item's nch.
+// The part of a warp's units [x, x1) that lies in one item: chunks [c0, c1) of
+// the item's nch (none when only its extra units do), `units` units.
+// first is the unit of the item's chunk 0: it identifies the item.
 struct Segment {
-  int b, h, rb, c0, c1, nch;
+  int b, h, rb, c0, c1, nch, units, first;
 };
 
 __device__ __forceinline__ Segment segment_at(const int *pre, const Kv4AttnArgs &a, int x, int x1) {
   Segment s;
   s.b = kv4_find(pre, a.n_slot, x);
-  const int per = a.n_kv * a.nrb, rel = x - pre[s.b];
-  s.nch = (pre[s.b + 1] - pre[s.b]) / per;
-  const int it = rel / s.nch;
-  s.c0 = rel - it * s.nch;
+  const int items = a.n_kv * a.nrb, rel = x - pre[s.b];
+  const int per = (pre[s.b + 1] - pre[s.b]) / items;
+  s.nch = per - kItemUnits;
+  const int it = rel / per, off = rel - it * per;
   s.h = it / a.nrb;
   s.rb = it - s.h * a.nrb;
-  s.c1 = min(s.nch, s.c0 + (x1 - x));
+  s.units = min(x1 - x, per - off);
+  s.c0 = max(0, off - kItemUnits);
+  s.c1 = max(0, off + s.units - kItemUnits);
+  s.first = x - off + kItemUnits;
   return s;
 }
 
@@ -173,37 +179,74 @@ __device__ __forceinline__ void store_row(const Kv4Rows &o, int64_t at, const fl
   }
 }
 
+template <int N>
+__device__ __forceinline__ void ldcg_row(const float *p, float (&v)[N]) {
+  if constexpr (N == 4) {
+    const float4 u = __ldcg(reinterpret_cast<const float4 *>(p));
+    v[0] = u.x; v[1] = u.y; v[2] = u.z; v[3] = u.w;
+  } else if constexpr (N == 2) {
+    const float2 u = __ldcg(reinterpret_cast<const float2 *>(p));
+    v[0] = u.x; v[1] = u.y;
+  } else {
+    v[0] = __ldcg(p);
+  }
+}
+
+// a row's output from its sums (lane: dims NG lane ..), and its log-sum for the weights
+template <int NG, bool TRACK>
+__device__ __forceinline__ void finish_row(const Kv4AttnArgs &a, const Segment &sg, int row, int lane, float mref,
+                                           float lsum, float (&os)[NG]) {
+  const int t = row / a.G, hq = sg.h * a.G + (row - t * a.G);
+  const float f = lsum != 0.f ? 1.f / lsum : 0.f;
+#pragma unroll
+  for (int i = 0; i < NG; ++i) os[i] = lsum != 0.f ? os[i] * f : 0.f;
+  store_row<NG>(a.out, sg.b * a.out.slot + t * a.out.token + hq * a.out.head + lane * NG, os);
+  if (TRACK && lane == 0)
+    a.lse[((int64_t)sg.b * a.n_kv + sg.h) * a.rows + row] = lsum != 0.f ? mref + log2f(lsum) : INFINITY;
+}
+
 // SPLIT: softmax weights keep 22 bits (two fp16) in the product with V, for
 // fp32 outputs; a bf16 output rounds to 8 bits, and one fp16 (11 bits, the
 // rounding errors of the positions independent) is enough for it.
+//
+// Every warp takes an equal, contiguous run of the units and works alone: its
+// own ring of bulk copies (one chunk of K and V each, running on across
+// items), its own queries and softmax state.  Items that lie in one warp are
+// finished by it; the others leave partial rows, which the CTA adds up at its
+// end, and for items shared by CTAs the last CTA to arrive does, all in the
+// order of the units, so that results do not depend on the run.  (With the
+// CTA's warps on one item at a time, the two barriers and the queries' load at
+// each item cost 3.5 us: 64 ragged slots took 79 us and short slots beside long
+// ones 41.)
 template <int NG, bool SPLIT, bool TRACK>
 __global__ void __launch_bounds__(kKv4Threads, kKv4CtasPerSm)
     k_kv4_attn(const __grid_constant__ Kv4AttnArgs a) {
   using L = AttnSmem<NG>;
   constexpr int HD = L::kHd, ST = L::kStages;
   extern __shared__ __align__(128) uint8_t smem[];
-  uint4 *qf = reinterpret_cast<uint4 *>(smem + L::kQ);
-  float *so = reinterpret_cast<float *>(smem + L::kO);
+  int *spart = reinterpret_cast<int *>(smem + L::kPart);
   float2 *sml = reinterpret_cast<float2 *>(smem + L::kMl);
-  float *srow = reinterpret_cast<float *>(smem + L::kRow);
   int *sflag = reinterpret_cast<int *>(smem + L::kFlag);
-  int *pre = reinterpret_cast<int *>(smem + L::kPre);
+  int *pre = reinterpret_cast<int *>(smem + L::kPre), *lens = pre + a.n_slot + 1;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r = lane >> 2, c = lane & 3;
+  uint4 *qf = reinterpret_cast<uint4 *>(smem + L::kQ) + warp * NG * 2 * 32;
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::kBars) + warp * ST;
   uint8_t *ring = smem + warp * ST * L::kChunk;
 
   if (lane == 0) {
     for (int s = 0; s < ST; ++s) mbar_init(bars + s, 1);
     fence_barrier_init();
+    spart[2 * warp] = spart[2 * warp + 1] = -1;
   }
   pdl_wait();
-  if (warp == 0) kv4_prefix(a.l, a.n_slot, kKv4Chunk, a.n_kv * a.nrb, pre);
+  if (warp == 0) kv4_prefix(a.l, a.n_slot, kKv4Chunk, kItemUnits, a.n_kv * a.nrb, pre, lens);
   __syncthreads();
-  const int total = pre[a.n_slot];
-  const int per_cta = max(kMinChunks, (total + (int)gridDim.x - 1) / (int)gridDim.x);
-  const int cta = blockIdx.x;
-  const int x0 = (int)min((int64_t)total, (int64_t)cta * per_cta);
-  const int x1 = (int)min((int64_t)total, (int64_t)x0 + per_cta);
+  const int total = pre[a.n_slot], cta = blockIdx.x;
+  const int ctas = max(1, min((int)gridDim.x, total / (kKv4Warps * kMinUnits)));
+  const int64_t warps = (int64_t)ctas * kKv4Warps, my_warp = (int64_t)cta * kKv4Warps + warp;
+  // warp i takes units [total i / warps, total (i + 1) / warps), CTA i accordingly
+  const int x0 = (int)(my_warp * total / warps), x1 = (int)((my_warp + 1) * total / warps);
+  auto cta_of = [&](int unit) { return (int)((((int64_t)unit + 1) * ctas - 1) / total); };
 
   // slots with nothing to attend to answer zero
   for (int b = cta; b < a.n_slot; b += gridDim.x) {
@@ -213,95 +256,108 @@ __global__ void __launch_bounds__(kKv4Threads, kKv4CtasPerSm)
       const int row = i >> 5, t = row / (a.n_kv * a.G), hq = row - t * (a.n_kv * a.G);
       store_row<NG>(a.out, b * a.out.slot + t * a.out.token + hq * a.out.head + (i & 31) * NG, z);
     }
-    if (TRACK)
-      for (int i = tid; i < a.n_kv * a.rows; i += kKv4Threads)
-        a.lse[(int64_t)b * a.n_kv * a.rows + i] = INFINITY;
   }
-  if (x0 >= x1) return;
+  if (cta >= ctas || total == 0) return;
 
-  // this warp's chunks are every eighth of each segment; its ring of bulk
-  // copies runs on across segments
   const int64_t head_bytes = (int64_t)(a.l.cap / kKv4Chunk) * L::kChunk;
-  int px = x0, pc, pc1;            // producer: segment start, next chunk, segment end
-  const uint8_t *pbase;
-  Segment ps = segment_at(pre, a, px, x1);
-  auto enter = [&]() {
-    pc = ps.c0 + warp;
-    pc1 = ps.c1;
-    pbase = a.l.codes + ((int64_t)ps.b * a.n_kv + ps.h) * head_bytes;
-  };
-  enter();
+  int px = x0, pc = 0, pc1 = 0;    // producer: next segment's first unit, next chunk, segment's end
+  const uint8_t *pbase = nullptr;
   int pstage = 0;
   bool dead = false;
   auto produce = [&]() {           // copy the warp's next chunk, if any, into stage pstage
     while (pc >= pc1) {
-      px += ps.c1 - ps.c0;
       if (px >= x1) return;
-      ps = segment_at(pre, a, px, x1);
-      enter();
+      const Segment ps = segment_at(pre, a, px, x1);
+      px += ps.units;
+      pc = ps.c0;
+      pc1 = ps.c1;
+      pbase = a.l.codes + ((int64_t)ps.b * a.n_kv + ps.h) * head_bytes;
     }
     if (lane == 0 && !dead) {
       mbar_arrive_expect_tx(bars + pstage, L::kChunk);
       bulk_g2s(ring + pstage * L::kChunk, pbase + (int64_t)pc * L::kChunk, L::kChunk, bars + pstage);
     }
-    pc += kKv4Warps;
+    ++pc;
     pstage = pstage + 1 == ST ? 0 : pstage + 1;
   };
-#pragma unroll 1
-  for (int s = 0; s < ST; ++s) produce();
 
   int stage = 0;
   uint32_t phase = 0;
-  int x = x0;
+  bool primed = false, early = false;
+  float2 *early_part = reinterpret_cast<float2 *>(a.warp_part) + ((int64_t)cta * kKv4Warps + warp) * NG * 4 * 32 + lane;
   uint32_t magic = 0x64006400u;
   asm volatile("" : "+r"(magic));
 #pragma unroll 1
-  while (x < x1) {
+  for (int x = x0; x < x1;) {
     const Segment sg = segment_at(pre, a, x, x1);
-    const int len = kv4_len(a.l, sg.b);
+    x += sg.units;
+    if (sg.c0 >= sg.c1) continue;
+    const int len = lens[sg.b];
+    const int row = sg.rb * kKv4Rows + r;
 
-    // queries of the row block: warp w takes row w.  Scaled to a largest
-    // magnitude of 2^10 (a power of two, undone in the scores), split into
-    // two fp16 and stored as the A operand: high parts in rows 0-7, low parts
-    // in rows 8-15.
+    // Queries: lane (r, c) holds dims 32 g + 8 c .. + 7 of row r, which are its
+    // own entries of the A operand (high parts in rows 0-7, low parts in rows
+    // 8-15).  Scaled to a largest magnitude of 2^10 by a power of two that the
+    // scores undo, split into two fp16, kept in shared memory (32 registers).
+    float rs;
     {
-      const int rr = sg.rb * kKv4Rows + warp;
-      float v[NG];
-      float mx = 0.f;
-      if (rr < a.rows) {
-        const int t = rr / a.G, hq = sg.h * a.G + (rr - t * a.G);
-        const int64_t at = sg.b * a.q.slot + t * a.q.token + hq * a.q.head + lane * NG;
-        if (a.q.dtype == PNB_F32) load_vals<float, NG>(static_cast<const float *>(a.q.p) + at, v);
-        else load_vals<__nv_bfloat16, NG>(static_cast<const __nv_bfloat16 *>(a.q.p) + at, v);
+      float v[NG][8];
+      if (row < a.rows) {
+        const int t = row / a.G, hq = sg.h * a.G + (row - t * a.G);
+        const int64_t at = sg.b * a.q.slot + t * a.q.token + hq * a.q.head + 8 * c;
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+          if (a.q.dtype == PNB_F32) {
+            const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(a.q.p) + at + 32 * g);
+            const float4 u = p[0], w = p[1];
+            v[g][0] = u.x; v[g][1] = u.y; v[g][2] = u.z; v[g][3] = u.w;
+            v[g][4] = w.x; v[g][5] = w.y; v[g][6] = w.z; v[g][7] = w.w;
+          } else {
+            load_vals<__nv_bfloat16, 8>(static_cast<const __nv_bfloat16 *>(a.q.p) + at + 32 * g, v[g]);
+          }
+        }
       } else {
 #pragma unroll
-        for (int i = 0; i < NG; ++i) v[i] = 0.f;
-      }
+        for (int g = 0; g < NG; ++g)
 #pragma unroll
-      for (int i = 0; i < NG; ++i) {
-        v[i] *= a.qscale;
-        mx = fmaxf(mx, fabsf(v[i]));
+          for (int i = 0; i < 8; ++i) v[g][i] = 0.f;
       }
-      mx = warp_max(mx);
+      // the first copies go out behind the first queries' loads, which would
+      // otherwise wait in their queue
+      if (!primed) {
+        primed = true;
+#pragma unroll 1
+        for (int s = 0; s < ST; ++s) produce();
+      }
+      float mx = 0.f;
+#pragma unroll
+      for (int g = 0; g < NG; ++g)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          v[g][i] *= a.qscale;
+          mx = fmaxf(mx, fabsf(v[g][i]));
+        }
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
       int e = (int)(__float_as_uint(mx) >> 23) - 127;
       e = min(max(e, -100), 100);
       const float up = __uint_as_float((uint32_t)(10 - e + 127) << 23);
-      __half *qh = reinterpret_cast<__half *>(qf);
+      rs = __uint_as_float((uint32_t)(e - 10 + 127) << 23);
 #pragma unroll
-      for (int i = 0; i < NG; ++i) {
-        const int d = lane * NG + i, g = d >> 5, cc = (d >> 3) & 3, n = d & 7;
-        const float y = v[i] * up;
-        const __half hi = __float2half_rn(y);
-        const __half lo = __float2half_rn(y - __half2float(hi));
-        const int at = (((g * 2 + ((n & 3) >> 1)) * 32 + warp * 4 + cc) * 4 + (n & 1) * 2) * 2 + (n >> 2);
-        qh[at] = hi;
-        qh[at + 2] = lo;
-      }
-      if (lane == 0) srow[warp] = __uint_as_float((uint32_t)(e - 10 + 127) << 23);
+      for (int g = 0; g < NG; ++g)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {   // dims n, n + 4 with n = 2 h (a0, a1) and 2 h + 1 (a2, a3)
+          uint32_t w[4];
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const float2 y = make_float2(v[g][2 * h + k] * up, v[g][2 * h + k + 4] * up);
+            w[2 * k] = pack_half2(y);
+            const float2 z = half2_pair(w[2 * k]);
+            w[2 * k + 1] = pack_half2(make_float2(y.x - z.x, y.y - z.y));
+          }
+          qf[(g * 2 + h) * 32 + lane] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
     }
-    __syncthreads();
-    const float rs = srow[r];
-    const int row = sg.rb * kKv4Rows + r;
     const int limit_all = len - a.T + 1;                       // every row sees positions below it
     const int limit = row < a.rows ? limit_all + row / a.G : 0;
     float *score = nullptr;
@@ -317,7 +373,7 @@ __global__ void __launch_bounds__(kKv4Threads, kKv4CtasPerSm)
     float ref = -11.f;
 
 #pragma unroll 1
-    for (int ch = sg.c0 + warp; ch < sg.c1; ch += kKv4Warps) {
+    for (int ch = sg.c0; ch < sg.c1; ++ch) {
       if (!dead && !mbar_wait(bars + stage, phase)) {
         // a wait that gave up: no more copies; those in flight get another
         // bounded chance to land before the shared memory goes away
@@ -468,113 +524,161 @@ __global__ void __launch_bounds__(kKv4Threads, kKv4CtasPerSm)
       phase ^= stage == 0;
     }
 
-    // this warp's rows: sum, reference and outputs
-    {
-      float l = l2.x + l2.y;
-      l += __shfl_xor_sync(0xffffffffu, l, 1);
-      l += __shfl_xor_sync(0xffffffffu, l, 2);
-      if (c == 0) sml[warp * kKv4Rows + r] = make_float2(ref, l);
-      float *od = so + (warp * kKv4Rows + r) * HD;
+    // the warp's rows: row r's sum over its four lanes, outputs of dims 8 i + 2 c
+    float l = l2.x + l2.y;
+    l += __shfl_xor_sync(0xffffffffu, l, 1);
+    l += __shfl_xor_sync(0xffffffffu, l, 2);
+    if (sg.c0 == 0 && sg.c1 == sg.nch) {
+      if (row < a.rows) {
+        const int t = row / a.G, hq = sg.h * a.G + (row - t * a.G);
+        const int64_t at = sg.b * a.out.slot + t * a.out.token + hq * a.out.head + 2 * c;
+        const float f = l != 0.f ? 1.f / l : 0.f;
 #pragma unroll
-      for (int i = 0; i < NG * 4; ++i)
-        // rows rotated by 8 floats each against bank conflicts
-        *reinterpret_cast<float2 *>(od + ((i * 8 + 2 * c + 8 * r) & (HD - 1))) =
-            make_float2(o[i][0] + o[i][2], o[i][1] + o[i][3]);
+        for (int i = 0; i < NG * 4; ++i) {
+          float v[2] = {(o[i][0] + o[i][2]) * f, (o[i][1] + o[i][3]) * f};
+          if (l == 0.f) v[0] = v[1] = 0.f;
+          store_row<2>(a.out, at + 8 * i, v);
+        }
+        if (TRACK && c == 0)
+          a.lse[((int64_t)sg.b * a.n_kv + sg.h) * a.rows + row] = l != 0.f ? ref + log2f(l) : INFINITY;
+      }
+    } else {
+      const int which = sg.c0 == 0 ? 1 : 0;    // 1: the item starts here and goes on behind
+      if (c == 0) sml[(2 * warp + which) * kKv4Rows + r] = make_float2(ref, l);
+      if (lane == 0) spart[2 * warp + which] = sg.first;
+      // the rows, rotated by 8 floats each against bank conflicts, into the
+      // warp's ring once its last chunk is used; before that to global memory
+      if (x >= x1) {
+        float *pd = reinterpret_cast<float *>(ring) + (which * kKv4Rows + r) * HD;
+#pragma unroll
+        for (int i = 0; i < NG * 4; ++i)
+          *reinterpret_cast<float2 *>(pd + ((8 * i + 2 * c + 8 * r) & (HD - 1))) =
+              make_float2(o[i][0] + o[i][2], o[i][1] + o[i][3]);
+      } else {
+        early = true;
+#pragma unroll
+        for (int i = 0; i < NG * 4; ++i)
+          early_part[i * 32] = make_float2(o[i][0] + o[i][2], o[i][1] + o[i][3]);
+      }
     }
-    __syncthreads();
+  }
+  if (early) {
+    float *pd = reinterpret_cast<float *>(ring) + r * HD;
+#pragma unroll
+    for (int i = 0; i < NG * 4; ++i)
+      *reinterpret_cast<float2 *>(pd + ((8 * i + 2 * c + 8 * r) & (HD - 1))) = early_part[i * 32];
+  }
+  __syncthreads();
 
-    // the CTA's rows: warp w adds up row w over the warps
+  // The CTA's partial rows, in the units' order: entry 2 w is warp w's item
+  // from before, 2 w + 1 the one that it starts.  Consecutive entries of one
+  // item form a group; the warps share out the groups' rows.
+  const int mine = lane < 2 * kKv4Warps ? spart[lane] : -1;
+  const uint32_t valid = __ballot_sync(0xffffffffu, mine >= 0), below = valid & ((1u << lane) - 1u);
+  const int before = __shfl_sync(0xffffffffu, mine, below ? 31 - __clz(below) : 0);
+  const uint32_t starts = __ballot_sync(0xffffffffu, mine >= 0 && (!below || before != mine));
+  const int groups = __popc(starts), rows = min(kKv4Rows, a.rows);
+#pragma unroll 1
+  for (int task = warp; task < groups * rows; task += kKv4Warps) {
+    const int gi = task / rows, i = task - gi * rows;
+    uint32_t m = starts;
+    for (int k = 0; k < gi; ++k) m &= m - 1u;
+    const uint32_t rest = m & (m - 1u), begin = m & -m;          // begin: the group's first bit
+    const uint32_t members = valid & ((rest & -rest) - begin);   // up to the next group's
+    const int first = __shfl_sync(0xffffffffu, mine, __ffs(begin) - 1);
+    const Segment sg = segment_at(pre, a, first, total);
+    const int my_row = sg.rb * kKv4Rows + i;
+    if (my_row >= a.rows) continue;
+    const int c0 = cta_of(first), c1 = cta_of(first + sg.nch - 1);
+    // lane e holds entry e's factor
+    const float2 ml = (members >> lane) & 1u ? sml[lane * kKv4Rows + i] : make_float2(0.f, 0.f);
+    const float mref = warp_max(ml.y != 0.f ? ml.x : -INFINITY);
+    const float fac = ml.y != 0.f ? ex2(ml.x - mref) : 0.f;
+    const float lsum = warp_sum(ml.y * fac);
+    float os[NG] = {};
+#pragma unroll
+    for (int e = 0; e < 2 * kKv4Warps; ++e) {
+      const float f = __shfl_sync(0xffffffffu, fac, e);
+      if (f == 0.f) continue;
+      float v[NG];
+      load_vals<float, NG>(reinterpret_cast<const float *>(smem + (e >> 1) * ST * L::kChunk) +
+                               ((e & 1) * kKv4Rows + i) * HD + ((lane * NG + 8 * i) & (HD - 1)), v);
+#pragma unroll
+      for (int j = 0; j < NG; ++j) os[j] = fmaf(v[j], f, os[j]);
+    }
+    if (c0 == cta && c1 == cta) {
+      finish_row<NG, TRACK>(a, sg, my_row, lane, mref, lsum, os);
+    } else {
+      const int64_t at = (int64_t)(2 * cta + (c0 == cta ? 1 : 0)) * kKv4Rows + i;
+#pragma unroll
+      for (int j = 0; j < NG; ++j) a.part[at * HD + lane * NG + j] = os[j];
+      if (lane == 0) reinterpret_cast<float2 *>(a.part_ml)[at] = make_float2(mref, lsum);
+    }
+  }
+
+  // items shared with other CTAs (the CTA's first and last at most): the last
+  // CTA to arrive adds them up
+  int shared_first[2] = {-1, -1};
+  if (groups > 0) {
+    const int f0 = __shfl_sync(0xffffffffu, mine, __ffs(starts) - 1);
+    const int f1 = __shfl_sync(0xffffffffu, mine, 31 - __clz(starts));
+    if (cta_of(f0) != cta) shared_first[0] = f0;
+    const Segment sg = segment_at(pre, a, f1, total);
+    if (cta_of(f1 + sg.nch - 1) != cta && (f1 != f0 || shared_first[0] < 0)) shared_first[1] = f1;
+  }
+  if (shared_first[0] < 0 && shared_first[1] < 0) return;
+
+  __threadfence();
+  __syncthreads();
+  if (tid < 2) {
+    const int first = shared_first[tid];
+    int last = 0;
+    if (first >= 0) {
+      const int c0 = cta_of(first), c1 = cta_of(first + segment_at(pre, a, first, total).nch - 1);
+      last = atomicAdd(a.counter + c0, 1u) == (unsigned)(c1 - c0);
+      if (last) a.counter[c0] = 0;
+    }
+    sflag[tid] = last;
+  }
+  __syncthreads();
+#pragma unroll 1
+  for (int i = 0; i < 2; ++i) {
+    if (!sflag[i]) continue;
+    __threadfence();
+    const int first = shared_first[i];
+    const Segment sg = segment_at(pre, a, first, total);
     const int my_row = sg.rb * kKv4Rows + warp;
-    float mref = -INFINITY, lsum = 0.f, os[NG];
-#pragma unroll
-    for (int i = 0; i < NG; ++i) os[i] = 0.f;
-#pragma unroll
-    for (int w = 0; w < kKv4Warps; ++w) {
-      const float2 ml = sml[w * kKv4Rows + warp];
+    if (my_row >= a.rows) continue;
+    const int c0 = cta_of(first), n = cta_of(first + sg.nch - 1) - c0 + 1;
+    // the first CTA's partial is its second one, all others' their first
+    auto at = [&](int k) { return (int64_t)(2 * (c0 + k) + (k == 0 ? 1 : 0)) * kKv4Rows + warp; };
+    float mref = -INFINITY, lsum = 0.f, os[NG] = {};
+    for (int k = lane; k < n; k += 32) {
+      const float2 ml = __ldcg(reinterpret_cast<const float2 *>(a.part_ml) + at(k));
       if (ml.y != 0.f) mref = fmaxf(mref, ml.x);
     }
-#pragma unroll
-    for (int w = 0; w < kKv4Warps; ++w) {
-      const float2 ml = sml[w * kKv4Rows + warp];
-      if (ml.y != 0.f) {
-        const float f = ex2(ml.x - mref);
-        lsum = fmaf(ml.y, f, lsum);
+    mref = warp_max(mref);
+    for (int k0 = 0; k0 < n; k0 += 32) {   // lane k: the factor of partial k0 + k
+      float fac = 0.f, l = 0.f;
+      if (k0 + lane < n) {
+        const float2 ml = __ldcg(reinterpret_cast<const float2 *>(a.part_ml) + at(k0 + lane));
+        if (ml.y != 0.f) {
+          fac = ex2(ml.x - mref);
+          l = ml.y * fac;
+        }
+      }
+      lsum += warp_sum(l);
+      const int m = min(32, n - k0);
+#pragma unroll 8
+      for (int k = 0; k < m; ++k) {
         float v[NG];
-        load_vals<float, NG>(so + (w * kKv4Rows + warp) * HD + ((lane * NG + 8 * warp) & (HD - 1)), v);
+        ldcg_row<NG>(a.part + at(k0 + k) * HD + lane * NG, v);
+        const float f = __shfl_sync(0xffffffffu, fac, k);
 #pragma unroll
-        for (int i = 0; i < NG; ++i) os[i] = fmaf(v[i], f, os[i]);
+        for (int j = 0; j < NG; ++j) os[j] = fmaf(v[j], f, os[j]);
       }
     }
-    auto finish = [&]() {   // the row's output, and its log-sum for the weights
-      if (my_row >= a.rows) return;
-      const int t = my_row / a.G, hq = sg.h * a.G + (my_row - t * a.G);
-      const float f = lsum != 0.f ? 1.f / lsum : 0.f;
-#pragma unroll
-      for (int i = 0; i < NG; ++i) os[i] = lsum != 0.f ? os[i] * f : 0.f;
-      store_row<NG>(a.out, sg.b * a.out.slot + t * a.out.token + hq * a.out.head + lane * NG, os);
-      if (TRACK && lane == 0)
-        a.lse[((int64_t)sg.b * a.n_kv + sg.h) * a.rows + my_row] = lsum != 0.f ? mref + log2f(lsum) : INFINITY;
-    };
-    if (sg.c0 == 0 && sg.c1 == sg.nch) {
-      finish();
-    } else {
-      // the item is shared with other CTAs: leave the partial rows, and let
-      // the last CTA to arrive add them up in their order
-      const int item0 = x - sg.c0;                  // flat index of the item's first chunk
-      const int first = item0 / per_cta, last = (item0 + sg.nch - 1) / per_cta;
-      const int which = (cta == first && item0 != x0) ? 1 : 0;
-      const int64_t slot = (int64_t)(2 * cta + which) * kKv4Rows + warp;
-      float *pd = a.part + slot * HD + lane * NG;
-#pragma unroll
-      for (int i = 0; i < NG; ++i) pd[i] = os[i];
-      if (lane == 0) {
-        a.part_ml[slot * 2] = mref;
-        a.part_ml[slot * 2 + 1] = lsum;
-      }
-      __threadfence();
-      __syncthreads();
-      if (tid == 0) {
-        const unsigned n = atomicAdd(a.counter + first, 1u);
-        *sflag = n == (unsigned)(last - first);
-        if (*sflag) a.counter[first] = 0;
-      }
-      __syncthreads();
-      if (*sflag) {
-        __threadfence();
-        // item0 is the first CTA's first chunk or a later one: its partial is
-        // its first (0) or second (1) one; all others' is their first
-        const int which0 = item0 > first * per_cta ? 1 : 0;
-        auto at = [&](int i) {
-          return (int64_t)(2 * (first + i) + (i == 0 ? which0 : 0)) * kKv4Rows + warp;
-        };
-        const int n = last - first + 1;
-        float mr = -INFINITY;
-        for (int i = lane; i < n; i += 32) {
-          const float2 ml = __ldcg(reinterpret_cast<const float2 *>(a.part_ml + at(i) * 2));
-          if (ml.y != 0.f) mr = fmaxf(mr, ml.x);
-        }
-        mref = warp_max(mr);
-        lsum = 0.f;
-#pragma unroll
-        for (int i = 0; i < NG; ++i) os[i] = 0.f;
-#pragma unroll 4
-        for (int i = 0; i < n; ++i) {
-          const float2 ml = __ldcg(reinterpret_cast<const float2 *>(a.part_ml + at(i) * 2));
-          const float *pv = a.part + at(i) * HD + lane * NG;
-          float v[NG];
-#pragma unroll
-          for (int j = 0; j < NG; ++j) v[j] = __ldcg(pv + j);
-          if (ml.y != 0.f) {
-            const float f = ex2(ml.x - mref);
-            lsum = fmaf(ml.y, f, lsum);
-#pragma unroll
-            for (int j = 0; j < NG; ++j) os[j] = fmaf(v[j], f, os[j]);
-          }
-        }
-        finish();
-      }
-    }
-    x += sg.c1 - sg.c0;
+    finish_row<NG, TRACK>(a, sg, my_row, lane, mref, lsum, os);
   }
 }
 
@@ -585,7 +689,7 @@ constexpr int kWeightThreads = 128, kWeightUnit = 4 * kWeightThreads;
 __global__ void __launch_bounds__(kWeightThreads) k_kv4_weights(const __grid_constant__ Kv4WeightArgs a) {
   extern __shared__ int wpre[];
   pdl_wait();
-  if (threadIdx.x < 32) kv4_prefix(a.l, a.n_slot, kWeightUnit, a.n_kv, wpre);
+  if (threadIdx.x < 32) kv4_prefix(a.l, a.n_slot, kWeightUnit, 0, a.n_kv, wpre, nullptr);
   __syncthreads();
   const int total = wpre[a.n_slot];
   for (int u = blockIdx.x; u < total; u += gridDim.x) {
