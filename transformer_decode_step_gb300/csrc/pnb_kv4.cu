@@ -120,7 +120,8 @@ __global__ void __launch_bounds__(kAppendThreads) k_kv4_append(const __grid_cons
       const uint32_t w = q4_word(x[i], &d);
       if (is_v) vcode[p][sub] = w;
       else if (live) *reinterpret_cast<uint32_t *>(chunk + kv4_kword(NG, p, cc, j)) = w;
-      if (live && cc == 0) *reinterpret_cast<__half *>(scales + kv4_scale(NG, p, j)) = d;
+      if (live && cc == 0)
+        *reinterpret_cast<__half *>(scales + (is_v ? kv4_vscale(NG, p, j) : kv4_kscale(NG, p, j))) = d;
     }
     if (tid < kKv4Chunk && p0 + tid >= lo && p0 + tid < hi) {
       a.l.ids[bh * a.l.cap + p0 + tid] = seen0 + (p0 + tid - start);
@@ -212,12 +213,12 @@ __global__ void __launch_bounds__(kReadThreads) k_kv4_read(const __grid_constant
     float x[8] = {};
     if (pos < len) {
       if (!is_v) {
-        const float d = __half2float(*reinterpret_cast<const __half *>(sm + kv4_kscale_off(NG) + kv4_scale(NG, p, j)));
+        const float d = __half2float(*reinterpret_cast<const __half *>(sm + kv4_kscale_off(NG) + kv4_kscale(NG, p, j)));
         const uint32_t w = *reinterpret_cast<const uint32_t *>(sm + kv4_kword(NG, p, sub, j));
 #pragma unroll
         for (int e = 0; e < 8; ++e) x[e] = d * (float)((int)((w >> (4 * e)) & 15u) - 8);
       } else {
-        const float d = __half2float(*reinterpret_cast<const __half *>(sm + kv4_vscale_off(NG) + kv4_scale(NG, p, j)));
+        const float d = __half2float(*reinterpret_cast<const __half *>(sm + kv4_vscale_off(NG) + kv4_vscale(NG, p, j)));
         const int c = (p >> 1) & 3, sh = kv4_vshift(p);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
@@ -451,9 +452,10 @@ __global__ void __launch_bounds__(kMoveThreads) k_kv4_move(const __grid_constant
     *reinterpret_cast<uint32_t *>(to + p * 16 * NG + w * 4) =
         *reinterpret_cast<const uint32_t *>(chunk + q * 16 * NG + w * 4);
     if (w < 2 * NG) {
-      const int off = w < NG ? kv4_kscale_off(NG) : kv4_vscale_off(NG), j = w % NG;
-      *reinterpret_cast<uint16_t *>(to + off + kv4_scale(NG, p, j)) =
-          *reinterpret_cast<const uint16_t *>(chunk + off + kv4_scale(NG, q, j));
+      const int j = w % NG;
+      const int into = w < NG ? kv4_kscale_off(NG) + kv4_kscale(NG, p, j) : kv4_vscale_off(NG) + kv4_vscale(NG, p, j);
+      const int out_of = w < NG ? kv4_kscale_off(NG) + kv4_kscale(NG, q, j) : kv4_vscale_off(NG) + kv4_vscale(NG, q, j);
+      *reinterpret_cast<uint16_t *>(to + into) = *reinterpret_cast<const uint16_t *>(chunk + out_of);
     }
   }
   // V codes: unit (J, r, c) holds 4 dims of 8 positions

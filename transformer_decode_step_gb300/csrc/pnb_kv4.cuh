@@ -9,7 +9,7 @@
 //   [K codes 512 NG][K scales 64 NG][V codes 512 NG][V scales 64 NG]
 //
 // The codes lie as the attention kernel's matrix instructions (m16n8k16, fp16)
-// want their B operand, so that one 32-bit word of 8 codes becomes four
+// want their A operand, so that one 32-bit word of 8 codes becomes four
 // registers of two fp16 each with four masks, one shift and four packed fp16
 // operations:
 //   - a word's nibbles n and n + 4 are a pair, in the two halves of the word;
@@ -17,9 +17,10 @@
 //     32-dim block j, the word of dims 32 j + 8 c + n;
 //   - V: the lane holds dim 32 J + 8 i + r and the word whose nibble t + 4 e
 //     is position 8 t + 2 c + e.
-// Scales of positions 8 t + 2 c and 8 t + 2 c + 1 are a half2 per block, next
-// to one another over the blocks: what a lane (r, c) multiplies its scores and
-// softmax weights of that position pair with.
+// A position's K scales are its blocks' fp16 in a row: what a lane multiplies
+// its position's partial scores with.  The V scales of positions 8 t + 2 c and
+// 8 t + 2 c + 1 are a half2 per block, next to one another over the blocks: what
+// a lane (r, c) multiplies its softmax weights of that position pair with.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -31,7 +32,7 @@
 namespace pnb {
 
 constexpr int kKv4Chunk = 32;              // positions per chunk
-constexpr int kKv4Rows = 8;                // query rows (tokens x heads of a group) per work item
+constexpr int kKv4Rows = 8;                // most query rows (tokens x heads of a group) per work item
 constexpr int kKv4Warps = 8;               // warps per attention CTA
 constexpr int kKv4Threads = kKv4Warps * 32;
 constexpr int kKv4CtasPerSm = 2;
@@ -50,8 +51,9 @@ __host__ __device__ constexpr int kv4_vscale_off(int ng) { return 1088 * ng; }
 __host__ __device__ constexpr int kv4_kword(int ng, int p, int c, int j) {
   return p * 16 * ng + c * 4 * ng + j * 4;
 }
-// scale of position p, block j, relative to the K or V scale area
-__host__ __device__ constexpr int kv4_scale(int ng, int p, int j) {
+// scale of position p, block j, relative to the K and to the V scale area
+__host__ __device__ constexpr int kv4_kscale(int ng, int p, int j) { return p * 2 * ng + j * 2; }
+__host__ __device__ constexpr int kv4_vscale(int ng, int p, int j) {
   return (p >> 1) * 4 * ng + j * 4 + (p & 1) * 2;
 }
 // V words of dims 32 J + 8 i + r (i = 0..3, 16 bytes) for position class c
@@ -94,7 +96,8 @@ struct Kv4ReadArgs {
 struct Kv4AttnArgs {
   Kv4Layer l;
   Kv4Rows q, out;
-  int32_t n_slot, n_kv, G, T, rows, nrb;  // rows = T * G, nrb = row blocks of kKv4Rows
+  int32_t n_slot, n_kv, G, T, rows;  // rows = T * G
+  int32_t nrb;                    // items per KV head (set by the launcher)
   float qscale;                   // log2(e) / sqrt(head_dim)
   float *warp_part;               // [grid][kKv4Warps][kKv4Rows][head_dim]: rows a warp puts aside
   float *part;                    // [2 grid][kKv4Rows][head_dim]: a CTA's partial rows

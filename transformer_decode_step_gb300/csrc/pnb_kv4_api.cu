@@ -40,7 +40,7 @@ int check_config(const pnb_kvq_config &c) {
     return PNB_E_UNSUPPORTED;
   // the flat list of work chunks is indexed with 32 bits
   const int64_t chunks = (int64_t)c.n_slot * c.n_kv_head * (c.cap / kKv4Chunk + 1);
-  if (chunks * (kKv4MaxRows / kKv4Rows) >= (int64_t)1 << 31) return PNB_E_UNSUPPORTED;
+  if (chunks * (kKv4MaxRows / 4) >= (int64_t)1 << 31) return PNB_E_UNSUPPORTED;
   return PNB_OK;
 }
 
@@ -263,7 +263,6 @@ int pnb_kvq_attention(pnb_kvq *c, int32_t layer, const pnb_rows *q, int32_t T, c
   a.G = G;
   a.T = T;
   a.rows = T * G;
-  a.nrb = (a.rows + kKv4Rows - 1) / kKv4Rows;
   a.qscale = (float)(1.4426950408889634 / std::sqrt((double)g.head_dim));
   a.part = c->part;
   a.part_ml = c->part_ml;

@@ -9,6 +9,17 @@
 // Codes never become scaled numbers: the matrix instructions multiply the
 // integers u - 8 (exact in fp16), so the only roundings are those of the fp32
 // operand's split into two fp16 (22 bits) and of the fp32 sums.
+//
+// Both products take the codes as the A operand (m16n8k16: 16 positions of K by
+// 16 dims, 16 dims of V by 16 positions) and the few rows as B's 8 columns.
+// FINE (queries or outputs in fp32): columns 2 q and 2 q + 1 are the high and
+// low fp16 parts of row q, four rows per column block.  Otherwise (bf16 queries,
+// exact in one fp16, and bf16 outputs, whose rounding to 8 bits hides that of
+// the softmax weights to 11): a row per column, eight per block.  Scores come
+// out with a position per lane group r = lane / 4 and rows by c = lane % 4; a
+// transposition of 8 x 8 fp16 turns them into B operands of the second product.
+// (With the rows as A's 16 rows, high parts over low parts, both products took
+// twice the matrix instructions and the outputs twice the registers.)
 #include <cuda_fp16.h>
 
 #include "pnb_kv4.cuh"
@@ -23,14 +34,14 @@ constexpr int kItemUnits = 1;
 // units a warp takes at least: below it a call uses fewer warps
 constexpr int kMinUnits = 2;
 
-template <int NG>
+template <int NG, int NT>
 struct AttnSmem {
   static constexpr int kHd = 32 * NG;
   static constexpr int kStages = NG == 4 ? 2 : 4;
   static constexpr int kChunk = kv4_chunk_bytes(NG);
   static constexpr int kRing = kKv4Warps * kStages * kChunk;
-  static constexpr int kQ = kRing;                                  // uint4 [warps][NG][2][32]
-  static constexpr int kBars = kQ + kKv4Warps * NG * 2 * 32 * 16;
+  static constexpr int kQ = kRing;                                  // uint2 [warps][NT][2 NG][32], NT > 1
+  static constexpr int kBars = kQ + (NT > 1 ? kKv4Warps * NT * 2 * NG * 32 * 8 : 0);
   static constexpr int kPart = kBars + kKv4Warps * kStages * 8;     // int [2 warps]: item of each partial
   static constexpr int kMl = kPart + kKv4Warps * 2 * 4;             // float2 [2 warps][8]: reference, sum
   static constexpr int kFlag = kMl + kKv4Warps * 2 * kKv4Rows * 8;
@@ -114,6 +125,13 @@ __device__ __forceinline__ uint32_t pack_half2(float2 v) {
   return *reinterpret_cast<const uint32_t *>(&h);
 }
 
+// the 8 x 8 matrix of fp16 whose row r lane (r, c) holds columns 2 c, 2 c + 1 of, transposed
+__device__ __forceinline__ uint32_t transpose8(uint32_t w) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(w));
+  return d;
+}
+
 template <int NG>
 __device__ __forceinline__ void lds_words(const uint8_t *p, uint32_t (&w)[NG]) {
   if constexpr (NG == 4) {
@@ -179,6 +197,21 @@ __device__ __forceinline__ void store_row(const Kv4Rows &o, int64_t at, const fl
   }
 }
 
+// N consecutive fp16 as fp32
+template <int N>
+__device__ __forceinline__ void lds_halves(const uint8_t *p, float (&v)[N]) {
+  if constexpr (N == 4) {
+    const uint2 w = *reinterpret_cast<const uint2 *>(p);
+    const float2 x = half2_pair(w.x), y = half2_pair(w.y);
+    v[0] = x.x; v[1] = x.y; v[2] = y.x; v[3] = y.y;
+  } else if constexpr (N == 2) {
+    const float2 x = half2_pair(*reinterpret_cast<const uint32_t *>(p));
+    v[0] = x.x; v[1] = x.y;
+  } else {
+    v[0] = __half2float(*reinterpret_cast<const __half *>(p));
+  }
+}
+
 template <int N>
 __device__ __forceinline__ void ldcg_row(const float *p, float (&v)[N]) {
   if constexpr (N == 4) {
@@ -205,10 +238,6 @@ __device__ __forceinline__ void finish_row(const Kv4AttnArgs &a, const Segment &
     a.lse[((int64_t)sg.b * a.n_kv + sg.h) * a.rows + row] = lsum != 0.f ? mref + log2f(lsum) : INFINITY;
 }
 
-// SPLIT: softmax weights keep 22 bits (two fp16) in the product with V, for
-// fp32 outputs; a bf16 output rounds to 8 bits, and one fp16 (11 bits, the
-// rounding errors of the positions independent) is enough for it.
-//
 // Every warp takes an equal, contiguous run of the units and works alone: its
 // own ring of bulk copies (one chunk of K and V each, running on across
 // items), its own queries and softmax state.  Items that lie in one warp are
@@ -218,18 +247,22 @@ __device__ __forceinline__ void finish_row(const Kv4AttnArgs &a, const Segment &
 // CTA's warps on one item at a time, the two barriers and the queries' load at
 // each item cost 3.5 us: 64 ragged slots took 79 us and short slots beside long
 // ones 41.)
-template <int NG, bool SPLIT, bool TRACK>
+template <int NG, bool FINE, int NT, bool TRACK>
 __global__ void __launch_bounds__(kKv4Threads, kKv4CtasPerSm)
     k_kv4_attn(const __grid_constant__ Kv4AttnArgs a) {
-  using L = AttnSmem<NG>;
+  using L = AttnSmem<NG, NT>;
   constexpr int HD = L::kHd, ST = L::kStages;
+  constexpr int RPB = FINE ? 4 : 8;           // rows per block of 8 columns
+  constexpr int RPI = RPB * NT;               // rows per item
+  constexpr int RL = (FINE ? 1 : 2) * NT;     // rows whose scores and outputs a lane holds
+  static_assert(RPI <= kKv4Rows, "partial rows");
   extern __shared__ __align__(128) uint8_t smem[];
   int *spart = reinterpret_cast<int *>(smem + L::kPart);
   float2 *sml = reinterpret_cast<float2 *>(smem + L::kMl);
   int *sflag = reinterpret_cast<int *>(smem + L::kFlag);
   int *pre = reinterpret_cast<int *>(smem + L::kPre), *lens = pre + a.n_slot + 1;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r = lane >> 2, c = lane & 3;
-  uint4 *qf = reinterpret_cast<uint4 *>(smem + L::kQ) + warp * NG * 2 * 32;
+  uint2 *qs = reinterpret_cast<uint2 *>(smem + L::kQ) + warp * NT * 2 * NG * 32 + lane;
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::kBars) + warp * ST;
   uint8_t *ring = smem + warp * ST * L::kChunk;
 
@@ -284,7 +317,7 @@ __global__ void __launch_bounds__(kKv4Threads, kKv4CtasPerSm)
   int stage = 0;
   uint32_t phase = 0;
   bool primed = false, early = false;
-  float2 *early_part = reinterpret_cast<float2 *>(a.warp_part) + ((int64_t)cta * kKv4Warps + warp) * NG * 4 * 32 + lane;
+  float *early_part = a.warp_part + ((int64_t)cta * kKv4Warps + warp) * kKv4Rows * HD + lane;
   uint32_t magic = 0x64006400u;
   asm volatile("" : "+r"(magic));
 #pragma unroll 1
@@ -293,84 +326,116 @@ __global__ void __launch_bounds__(kKv4Threads, kKv4CtasPerSm)
     x += sg.units;
     if (sg.c0 >= sg.c1) continue;
     const int len = lens[sg.b];
-    const int row = sg.rb * kKv4Rows + r;
+    const int row0 = sg.rb * RPI;
+    // the lane's score rows are row0 + lane_row(k), k < RL; its column's row in
+    // block t (queries, weights) is row0 + col_row + RPB t
+    auto lane_row = [&](int k) { return FINE ? c + 4 * k : 2 * c + k; };
+    const int col_row = FINE ? r >> 1 : r;
 
-    // Queries: lane (r, c) holds dims 32 g + 8 c .. + 7 of row r, which are its
-    // own entries of the A operand (high parts in rows 0-7, low parts in rows
-    // 8-15).  Scaled to a largest magnitude of 2^10 by a power of two that the
-    // scores undo, split into two fp16, kept in shared memory (32 registers).
-    float rs;
+    // Queries: lane (r, c) holds dims 32 g + 8 c .. + 7 of its column, which are
+    // its own entries of the B operand.  Scaled to a largest magnitude of 2^10 by
+    // a power of two that the scores undo; FINE: split, high part in even columns.
+    uint2 qf[NT == 1 ? 2 * NG : 1];
+    float rs[RL];
     {
-      float v[NG][8];
-      if (row < a.rows) {
-        const int t = row / a.G, hq = sg.h * a.G + (row - t * a.G);
-        const int64_t at = sg.b * a.q.slot + t * a.q.token + hq * a.q.head + 8 * c;
+      float scale[NT];
 #pragma unroll
-        for (int g = 0; g < NG; ++g) {
-          if (a.q.dtype == PNB_F32) {
-            const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(a.q.p) + at + 32 * g);
-            const float4 u = p[0], w = p[1];
-            v[g][0] = u.x; v[g][1] = u.y; v[g][2] = u.z; v[g][3] = u.w;
-            v[g][4] = w.x; v[g][5] = w.y; v[g][6] = w.z; v[g][7] = w.w;
-          } else {
-            load_vals<__nv_bfloat16, 8>(static_cast<const __nv_bfloat16 *>(a.q.p) + at + 32 * g, v[g]);
+      for (int nt = 0; nt < NT; ++nt) {
+        const int row = row0 + col_row + RPB * nt;
+        float v[NG][8];
+        if (row < a.rows) {
+          const int t = row / a.G, hq = sg.h * a.G + (row - t * a.G);
+          const int64_t at = sg.b * a.q.slot + t * a.q.token + hq * a.q.head + 8 * c;
+#pragma unroll
+          for (int g = 0; g < NG; ++g) {
+            if (FINE && a.q.dtype == PNB_F32) {
+              const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(a.q.p) + at + 32 * g);
+              const float4 u = p[0], w = p[1];
+              v[g][0] = u.x; v[g][1] = u.y; v[g][2] = u.z; v[g][3] = u.w;
+              v[g][4] = w.x; v[g][5] = w.y; v[g][6] = w.z; v[g][7] = w.w;
+            } else {
+              load_vals<__nv_bfloat16, 8>(static_cast<const __nv_bfloat16 *>(a.q.p) + at + 32 * g, v[g]);
+            }
           }
+        } else {
+#pragma unroll
+          for (int g = 0; g < NG; ++g)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[g][i] = 0.f;
         }
-      } else {
+        // the first copies go out behind the first queries' loads, which would
+        // otherwise wait in their queue
+        if (!primed) {
+          primed = true;
+#pragma unroll 1
+          for (int s = 0; s < ST; ++s) produce();
+        }
+        float mx = 0.f;
 #pragma unroll
         for (int g = 0; g < NG; ++g)
 #pragma unroll
-          for (int i = 0; i < 8; ++i) v[g][i] = 0.f;
-      }
-      // the first copies go out behind the first queries' loads, which would
-      // otherwise wait in their queue
-      if (!primed) {
-        primed = true;
-#pragma unroll 1
-        for (int s = 0; s < ST; ++s) produce();
-      }
-      float mx = 0.f;
+          for (int i = 0; i < 8; ++i) mx = fmaxf(mx, fabsf(v[g][i]));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        int e = (int)(__float_as_uint(mx) >> 23) - 127;
+        e = min(max(e, -100), 100);
+        const float up = __uint_as_float((uint32_t)(10 - e + 127) << 23);
+        scale[nt] = __uint_as_float((uint32_t)(e - 10 + 127) << 23) * a.qscale;
 #pragma unroll
-      for (int g = 0; g < NG; ++g)
+        for (int g = 0; g < NG; ++g)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          v[g][i] *= a.qscale;
-          mx = fmaxf(mx, fabsf(v[g][i]));
-        }
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-      int e = (int)(__float_as_uint(mx) >> 23) - 127;
-      e = min(max(e, -100), 100);
-      const float up = __uint_as_float((uint32_t)(10 - e + 127) << 23);
-      rs = __uint_as_float((uint32_t)(e - 10 + 127) << 23);
+          for (int h = 0; h < 2; ++h) {   // dims n, n + 4 with n = 2 h (b0) and 2 h + 1 (b1)
+            uint32_t w[2];
 #pragma unroll
-      for (int g = 0; g < NG; ++g)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {   // dims n, n + 4 with n = 2 h (a0, a1) and 2 h + 1 (a2, a3)
-          uint32_t w[4];
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const float2 y = make_float2(v[g][2 * h + k] * up, v[g][2 * h + k + 4] * up);
-            w[2 * k] = pack_half2(y);
-            const float2 z = half2_pair(w[2 * k]);
-            w[2 * k + 1] = pack_half2(make_float2(y.x - z.x, y.y - z.y));
+            for (int k = 0; k < 2; ++k) {
+              const float2 y = make_float2(v[g][2 * h + k] * up, v[g][2 * h + k + 4] * up);
+              w[k] = pack_half2(y);
+              if (FINE) {
+                const float2 z = half2_pair(w[k]);
+                const uint32_t lo = pack_half2(make_float2(y.x - z.x, y.y - z.y));
+                w[k] = (r & 1) ? lo : w[k];
+              }
+            }
+            if (NT == 1) qf[g * 2 + h] = make_uint2(w[0], w[1]);
+            else qs[(nt * 2 * NG + g * 2 + h) * 32] = make_uint2(w[0], w[1]);
           }
-          qf[(g * 2 + h) * 32 + lane] = make_uint4(w[0], w[1], w[2], w[3]);
-        }
+      }
+      // the score rows' factors from the lanes of their columns
+#pragma unroll
+      for (int k = 0; k < RL; ++k)
+        rs[k] = __shfl_sync(0xffffffffu, scale[FINE ? k : 0], FINE ? 8 * c : 4 * (2 * c + k));
     }
     const int limit_all = len - a.T + 1;                       // every row sees positions below it
-    const int limit = row < a.rows ? limit_all + row / a.G : 0;
-    float *score = nullptr;
-    if (TRACK && row < a.rows)
-      score = a.scores + (((int64_t)sg.b * a.n_kv + sg.h) * a.rows + row) * a.l.cap + 2 * c;
-
-    float o[NG * 4][4];
+    int limit[RL], limit_col[NT];
+    float *score[RL];
 #pragma unroll
-    for (int i = 0; i < NG * 4; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-    float2 l2 = make_float2(0.f, 0.f);
-    float m = -INFINITY;                                       // the row's reference maximum
+    for (int k = 0; k < RL; ++k) {
+      const int row = row0 + lane_row(k);
+      limit[k] = row < a.rows ? limit_all + row / a.G : 0;
+      if (TRACK)
+        score[k] = row < a.rows
+                       ? a.scores + (((int64_t)sg.b * a.n_kv + sg.h) * a.rows + row) * a.l.cap + r
+                       : nullptr;
+    }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int row = row0 + col_row + RPB * nt;
+      limit_col[nt] = row < a.rows ? limit_all + row / a.G : 0;
+    }
+
+    float o[NT][NG * 2][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < NG * 2; ++i) o[nt][i][0] = o[nt][i][1] = o[nt][i][2] = o[nt][i][3] = 0.f;
+    float l[RL], m[RL], ref[RL];                               // sum, reference maximum, reference
     int ev = -1;                                               // V scales seen are below 2^ev
-    float ref = -11.f;
+#pragma unroll
+    for (int k = 0; k < RL; ++k) {
+      l[k] = 0.f;
+      m[k] = -INFINITY;
+      ref[k] = -11.f;
+    }
 
 #pragma unroll 1
     for (int ch = sg.c0; ch < sg.c1; ++ch) {
@@ -386,28 +451,41 @@ __global__ void __launch_bounds__(kKv4Threads, kKv4CtasPerSm)
       const int p0 = ch * kKv4Chunk;
       const bool tail = p0 + kKv4Chunk > limit_all;
 
-      // scores of positions p0 + 8 t + 2 c + {0, 1}
-      float2 s2[4];
-      {
-        uint32_t kw[4][NG], ks[4][NG];
+      // scores of position p0 + 8 t + r, row lane_row(k)
+      float s[4][RL];
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          lds_words<NG>(st + kv4_kword(NG, 8 * t + r, c, 0), kw[t]);
-          lds_words<NG>(st + kv4_kscale_off(NG) + (t * 4 + c) * 4 * NG, ks[t]);
-          s2[t] = make_float2(0.f, 0.f);
+      for (int mt = 0; mt < 2; ++mt) {
+        uint32_t kw[2][NG];
+        float kd[2][NG];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int p = 8 * (2 * mt + h) + r;
+          lds_words<NG>(st + kv4_kword(NG, p, c, 0), kw[h]);
+          lds_halves<NG>(st + kv4_kscale_off(NG) + kv4_kscale(NG, p, 0), kd[h]);
+#pragma unroll
+          for (int k = 0; k < RL; ++k) s[2 * mt + h][k] = 0.f;
         }
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
-          const uint4 qa = qf[(g * 2) * 32 + lane], qb = qf[(g * 2 + 1) * 32 + lane];
+          uint32_t u0[4], u1[4];
+          code_pairs(kw[0][g], magic, u0);
+          code_pairs(kw[1][g], magic, u1);
 #pragma unroll
-          for (int t = 0; t < 4; ++t) {
+          for (int nt = 0; nt < NT; ++nt) {
+            const uint2 qa = NT == 1 ? qf[g * 2] : qs[(nt * 2 * NG + g * 2) * 32];
+            const uint2 qb = NT == 1 ? qf[g * 2 + 1] : qs[(nt * 2 * NG + g * 2 + 1) * 32];
             float d[4];
-            uint32_t u[4];
-            code_pairs(kw[t][g], magic, u);
-            mma_f16_new(d, qa.x, qa.y, qa.z, qa.w, u[0], u[1]);
-            mma_f16(d, qb.x, qb.y, qb.z, qb.w, u[2], u[3]);
-            s2[t] = ffma2(add2(make_float2(d[0], d[1]), make_float2(d[2], d[3])), half2_pair(ks[t][g]),
-                          s2[t]);
+            mma_f16_new(d, u0[0], u1[0], u0[1], u1[1], qa.x, qa.y);
+            mma_f16(d, u0[2], u1[2], u0[3], u1[3], qb.x, qb.y);
+            if (FINE) {
+              s[2 * mt][nt] = fmaf(d[0] + d[1], kd[0][g], s[2 * mt][nt]);
+              s[2 * mt + 1][nt] = fmaf(d[2] + d[3], kd[1][g], s[2 * mt + 1][nt]);
+            } else {
+              s[2 * mt][0] = fmaf(d[0], kd[0][g], s[2 * mt][0]);
+              s[2 * mt][1] = fmaf(d[1], kd[0][g], s[2 * mt][1]);
+              s[2 * mt + 1][0] = fmaf(d[2], kd[1][g], s[2 * mt + 1][0]);
+              s[2 * mt + 1][1] = fmaf(d[3], kd[1][g], s[2 * mt + 1][1]);
+            }
           }
         }
       }
@@ -433,68 +511,77 @@ __global__ void __launch_bounds__(kKv4Threads, kKv4CtasPerSm)
       }
       if (tail) {
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          const int p = p0 + 8 * t + 2 * c;
-          if (p >= limit) s2[t].x = -INFINITY;
-          if (p + 1 >= limit) s2[t].y = -INFINITY;
-        }
-      }
-      float xm = -INFINITY;
+        for (int t = 0; t < 4; ++t)
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        if (TRACK && score)
-          *reinterpret_cast<float2 *>(score + p0 + 8 * t) = make_float2(s2[t].x * rs, s2[t].y * rs);
-        xm = fmaxf(xm, fmaxf(s2[t].x, s2[t].y));
+          for (int k = 0; k < RL; ++k)
+            if (p0 + 8 * t + r >= limit[k]) s[t][k] = -INFINITY;
       }
-      xm = fmaxf(xm, __shfl_xor_sync(0xffffffffu, xm, 1));
-      xm = fmaxf(xm, __shfl_xor_sync(0xffffffffu, xm, 2)) * rs;
+      float xm[RL];
+      bool move = false;
+#pragma unroll
+      for (int k = 0; k < RL; ++k) {
+        if (TRACK && score[k]) {
+#pragma unroll
+          for (int t = 0; t < 4; ++t) score[k][p0 + 8 * t] = s[t][k] * rs[k];
+        }
+        xm[k] = fmaxf(fmaxf(s[0][k], s[1][k]), fmaxf(s[2][k], s[3][k]));
+        xm[k] = fmaxf(xm[k], __shfl_xor_sync(0xffffffffu, xm[k], 4));
+        xm[k] = fmaxf(xm[k], __shfl_xor_sync(0xffffffffu, xm[k], 8));
+        xm[k] = fmaxf(xm[k], __shfl_xor_sync(0xffffffffu, xm[k], 16)) * rs[k];
+        move |= xm[k] > m[k] + 4.f;
+      }
       const int evc = (int)(hmax >> 10) - 14;
       // The weights are scaled by 2^(10 - ev), V scales lying below 2^ev with
       // ev >= -1, and the reference moves only when a score exceeds it by 2^4
       // or a larger V scale arrives: p stays below 2^15 and p d below 2^14,
       // inside fp16, and the fp32 sums need no rescaling otherwise.
-      if (__any_sync(0xffffffffu, xm > m + 4.f) || evc > ev) {
+      if (__any_sync(0xffffffffu, move) || evc > ev) {
         ev = max(ev, evc);
-        const float mn = fmaxf(m, xm);
-        const float nref = (mn == -INFINITY ? 0.f : mn) - 10.f + (float)ev;
-        const float al = m == -INFINITY ? 0.f : ex2(ref - nref);
-        m = mn;
-        ref = nref;
-        const float2 al2 = make_float2(al, al);
-        l2 = mul2(l2, al2);
 #pragma unroll
-        for (int i = 0; i < NG * 4; ++i) {
-          o[i][0] *= al; o[i][1] *= al; o[i][2] *= al; o[i][3] *= al;
+        for (int k = 0; k < RL; ++k) {
+          const float mn = fmaxf(m[k], xm[k]);
+          const float nref = (mn == -INFINITY ? 0.f : mn) - 10.f + (float)ev;
+          const float al = m[k] == -INFINITY ? 0.f : ex2(ref[k] - nref);
+          m[k] = mn;
+          ref[k] = nref;
+          l[k] *= al;
+#pragma unroll
+          for (int i = 0; i < NG * 2; ++i) {
+            if (FINE) {
+              o[k][i][0] *= al; o[k][i][1] *= al; o[k][i][2] *= al; o[k][i][3] *= al;
+            } else {
+              o[0][i][k] *= al; o[0][i][2 + k] *= al;
+            }
+          }
         }
       }
-      float2 p2[4];   // softmax weights
+      // softmax weights as columns: x[nt][t] holds positions 8 t + 2 c, + 1 of the lane's column
+      uint32_t xc[NT][4], xh[NT][4];
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
-        p2[t] = make_float2(ex2(fmaf(s2[t].x, rs, -ref)), ex2(fmaf(s2[t].y, rs, -ref)));
-        l2 = add2(l2, p2[t]);
-      }
-      // p d as fp16: w = p_hi d, rounded, and for SPLIT the rest of the exact
-      // product, its residual (one fma) + p_lo d
-      uint32_t ph[4], pl[4];
+        float p[RL];
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        ph[t] = pack_half2(p2[t]);
-        if (SPLIT) {
-          const float2 h = half2_pair(ph[t]);
-          pl[t] = pack_half2(make_float2(p2[t].x - h.x, p2[t].y - h.y));
+        for (int k = 0; k < RL; ++k) {
+          p[k] = ex2(fmaf(s[t][k], rs[k], -ref[k]));
+          l[k] += p[k];
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          if (FINE) {
+            const float h = __half2float(__float2half_rn(p[nt]));
+            xc[nt][t] = transpose8(pack_half2(make_float2(h, p[nt] - h)));
+            const uint32_t other = __shfl_xor_sync(0xffffffffu, xc[nt][t], 4);
+            xh[nt][t] = (r & 1) ? other : xc[nt][t];   // the high parts, in both of a row's columns
+            xc[nt][t] = (r & 1) ? xc[nt][t] : 0u;      // the low parts, in the odd one
+          } else {
+            xc[nt][t] = transpose8(pack_half2(make_float2(p[0], p[1])));
+          }
         }
       }
       uint32_t vs[4][NG];
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        lds_words<NG>(st + kv4_vscale_off(NG) + (t * 4 + c) * 4 * NG, vs[t]);
-        if (tail) {   // a masked position's scale may be anything: its weight is 0, not 0 times it
-          const int p = p0 + 8 * t + 2 * c;
-          const uint32_t seen = p >= limit ? 0u : (p + 1 >= limit ? 0xffffu : 0xffffffffu);
-#pragma unroll
-          for (int g = 0; g < NG; ++g) vs[t][g] &= seen;
-        }
-      }
+      for (int t = 0; t < 4; ++t) lds_words<NG>(st + kv4_vscale_off(NG) + (t * 4 + c) * 4 * NG, vs[t]);
+      const uint32_t odd = (r & 1) ? 0xffffffffu : 0u;
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
         const uint4 vw = *reinterpret_cast<const uint4 *>(st + kv4_v_off(NG) + g * 512 + lane * 16);
@@ -504,18 +591,32 @@ __global__ void __launch_bounds__(kKv4Threads, kKv4CtasPerSm)
         code_pairs(vw.z, magic, u[2]);
         code_pairs(vw.w, magic, u[3]);
 #pragma unroll
-        for (int kt = 0; kt < 2; ++kt) {
-          uint32_t hi[2], lo[2] = {0, 0};
+        for (int nt = 0; nt < NT; ++nt) {
+          // p d in fp16; FINE: even columns its rounding, odd columns the rest of the
+          // exact product, the rounding's residual (one fma) + p_lo d
+          uint32_t w[4];
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const __half2 d = as_half2(vs[2 * kt + e][g]), p = as_half2(ph[2 * kt + e]);
-            const __half2 w = __hmul2_rn(p, d);
-            hi[e] = as_word(w);
-            if (SPLIT) lo[e] = as_word(__hfma2(as_half2(pl[2 * kt + e]), d, __hfma2(p, d, __hneg2(w))));
+          for (int t = 0; t < 4; ++t) {
+            uint32_t dw = vs[t][g];
+            if (tail) {   // a masked position's scale may be anything: its weight is 0, not 0 times it
+              const int p = p0 + 8 * t + 2 * c;
+              dw &= p >= limit_col[nt] ? 0u : (p + 1 >= limit_col[nt] ? 0xffffu : 0xffffffffu);
+            }
+            const __half2 d = as_half2(dw);
+            if (FINE) {
+              const __half2 h = as_half2(xh[nt][t]);
+              const uint32_t first = as_word(__hmul2_rn(h, d)) & odd;
+              w[t] = as_word(__hfma2(as_half2(xc[nt][t]), d, __hfma2(h, d, __hneg2(as_half2(first)))));
+            } else {
+              w[t] = as_word(__hmul2_rn(as_half2(xc[nt][t]), d));
+            }
           }
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            mma_f16(o[g * 4 + i], hi[0], lo[0], hi[1], lo[1], u[i][2 * kt], u[i][2 * kt + 1]);
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int kt = 0; kt < 2; ++kt)
+              mma_f16(o[nt][g * 2 + j], u[2 * j][2 * kt], u[2 * j + 1][2 * kt], u[2 * j][2 * kt + 1],
+                      u[2 * j + 1][2 * kt + 1], w[2 * kt], w[2 * kt + 1]);
         }
       }
       __syncwarp();
@@ -524,49 +625,60 @@ __global__ void __launch_bounds__(kKv4Threads, kKv4CtasPerSm)
       phase ^= stage == 0;
     }
 
-    // the warp's rows: row r's sum over its four lanes, outputs of dims 8 i + 2 c
-    float l = l2.x + l2.y;
-    l += __shfl_xor_sync(0xffffffffu, l, 1);
-    l += __shfl_xor_sync(0xffffffffu, l, 2);
+    // the lane's outputs: row lane_row(k), dim 8 i + r
+    auto out_of = [&](int k, int i) {
+      return FINE ? o[k][i >> 1][2 * (i & 1)] + o[k][i >> 1][2 * (i & 1) + 1] : o[0][i >> 1][2 * (i & 1) + k];
+    };
+#pragma unroll
+    for (int k = 0; k < RL; ++k) {
+      l[k] += __shfl_xor_sync(0xffffffffu, l[k], 4);
+      l[k] += __shfl_xor_sync(0xffffffffu, l[k], 8);
+      l[k] += __shfl_xor_sync(0xffffffffu, l[k], 16);
+    }
     if (sg.c0 == 0 && sg.c1 == sg.nch) {
-      if (row < a.rows) {
+#pragma unroll
+      for (int k = 0; k < RL; ++k) {
+        const int row = row0 + lane_row(k);
+        if (row >= a.rows) continue;
         const int t = row / a.G, hq = sg.h * a.G + (row - t * a.G);
-        const int64_t at = sg.b * a.out.slot + t * a.out.token + hq * a.out.head + 2 * c;
-        const float f = l != 0.f ? 1.f / l : 0.f;
+        const int64_t at = sg.b * a.out.slot + t * a.out.token + hq * a.out.head + r;
+        const float f = l[k] != 0.f ? 1.f / l[k] : 0.f;
 #pragma unroll
         for (int i = 0; i < NG * 4; ++i) {
-          float v[2] = {(o[i][0] + o[i][2]) * f, (o[i][1] + o[i][3]) * f};
-          if (l == 0.f) v[0] = v[1] = 0.f;
-          store_row<2>(a.out, at + 8 * i, v);
+          const float v[1] = {l[k] != 0.f ? out_of(k, i) * f : 0.f};
+          store_row<1>(a.out, at + 8 * i, v);
         }
-        if (TRACK && c == 0)
-          a.lse[((int64_t)sg.b * a.n_kv + sg.h) * a.rows + row] = l != 0.f ? ref + log2f(l) : INFINITY;
+        if (TRACK && r == 0)
+          a.lse[((int64_t)sg.b * a.n_kv + sg.h) * a.rows + row] = l[k] != 0.f ? ref[k] + log2f(l[k]) : INFINITY;
       }
     } else {
       const int which = sg.c0 == 0 ? 1 : 0;    // 1: the item starts here and goes on behind
-      if (c == 0) sml[(2 * warp + which) * kKv4Rows + r] = make_float2(ref, l);
       if (lane == 0) spart[2 * warp + which] = sg.first;
       // the rows, rotated by 8 floats each against bank conflicts, into the
       // warp's ring once its last chunk is used; before that to global memory
-      if (x >= x1) {
-        float *pd = reinterpret_cast<float *>(ring) + (which * kKv4Rows + r) * HD;
+      float *pd = x >= x1 ? reinterpret_cast<float *>(ring) + which * RPI * HD : nullptr;
+      early |= x < x1;
 #pragma unroll
-        for (int i = 0; i < NG * 4; ++i)
-          *reinterpret_cast<float2 *>(pd + ((8 * i + 2 * c + 8 * r) & (HD - 1))) =
-              make_float2(o[i][0] + o[i][2], o[i][1] + o[i][3]);
-      } else {
-        early = true;
+      for (int k = 0; k < RL; ++k) {
+        const int i0 = lane_row(k);
+        if (r == 0) sml[(2 * warp + which) * kKv4Rows + i0] = make_float2(ref[k], l[k]);
 #pragma unroll
-        for (int i = 0; i < NG * 4; ++i)
-          early_part[i * 32] = make_float2(o[i][0] + o[i][2], o[i][1] + o[i][3]);
+        for (int i = 0; i < NG * 4; ++i) {
+          if (pd) pd[i0 * HD + ((8 * i + r + 8 * i0) & (HD - 1))] = out_of(k, i);
+          else early_part[(k * NG * 4 + i) * 32] = out_of(k, i);
+        }
       }
     }
   }
   if (early) {
-    float *pd = reinterpret_cast<float *>(ring) + r * HD;
 #pragma unroll
-    for (int i = 0; i < NG * 4; ++i)
-      *reinterpret_cast<float2 *>(pd + ((8 * i + 2 * c + 8 * r) & (HD - 1))) = early_part[i * 32];
+    for (int k = 0; k < RL; ++k) {
+      const int i0 = FINE ? c + 4 * k : 2 * c + k;
+#pragma unroll
+      for (int i = 0; i < NG * 4; ++i)
+        reinterpret_cast<float *>(ring)[i0 * HD + ((8 * i + r + 8 * i0) & (HD - 1))] =
+            early_part[(k * NG * 4 + i) * 32];
+    }
   }
   __syncthreads();
 
@@ -577,7 +689,7 @@ __global__ void __launch_bounds__(kKv4Threads, kKv4CtasPerSm)
   const uint32_t valid = __ballot_sync(0xffffffffu, mine >= 0), below = valid & ((1u << lane) - 1u);
   const int before = __shfl_sync(0xffffffffu, mine, below ? 31 - __clz(below) : 0);
   const uint32_t starts = __ballot_sync(0xffffffffu, mine >= 0 && (!below || before != mine));
-  const int groups = __popc(starts), rows = min(kKv4Rows, a.rows);
+  const int groups = __popc(starts), rows = min(RPI, a.rows);
 #pragma unroll 1
   for (int task = warp; task < groups * rows; task += kKv4Warps) {
     const int gi = task / rows, i = task - gi * rows;
@@ -587,7 +699,7 @@ __global__ void __launch_bounds__(kKv4Threads, kKv4CtasPerSm)
     const uint32_t members = valid & ((rest & -rest) - begin);   // up to the next group's
     const int first = __shfl_sync(0xffffffffu, mine, __ffs(begin) - 1);
     const Segment sg = segment_at(pre, a, first, total);
-    const int my_row = sg.rb * kKv4Rows + i;
+    const int my_row = sg.rb * RPI + i;
     if (my_row >= a.rows) continue;
     const int c0 = cta_of(first), c1 = cta_of(first + sg.nch - 1);
     // lane e holds entry e's factor
@@ -602,7 +714,7 @@ __global__ void __launch_bounds__(kKv4Threads, kKv4CtasPerSm)
       if (f == 0.f) continue;
       float v[NG];
       load_vals<float, NG>(reinterpret_cast<const float *>(smem + (e >> 1) * ST * L::kChunk) +
-                               ((e & 1) * kKv4Rows + i) * HD + ((lane * NG + 8 * i) & (HD - 1)), v);
+                               ((e & 1) * RPI + i) * HD + ((lane * NG + 8 * i) & (HD - 1)), v);
 #pragma unroll
       for (int j = 0; j < NG; ++j) os[j] = fmaf(v[j], f, os[j]);
     }
@@ -647,8 +759,8 @@ __global__ void __launch_bounds__(kKv4Threads, kKv4CtasPerSm)
     __threadfence();
     const int first = shared_first[i];
     const Segment sg = segment_at(pre, a, first, total);
-    const int my_row = sg.rb * kKv4Rows + warp;
-    if (my_row >= a.rows) continue;
+    const int my_row = sg.rb * RPI + warp;
+    if (warp >= RPI || my_row >= a.rows) continue;
     const int c0 = cta_of(first), n = cta_of(first + sg.nch - 1) - c0 + 1;
     // the first CTA's partial is its second one, all others' their first
     auto at = [&](int k) { return (int64_t)(2 * (c0 + k) + (k == 0 ? 1 : 0)) * kKv4Rows + warp; };
@@ -716,15 +828,17 @@ __global__ void __launch_bounds__(kWeightThreads) k_kv4_weights(const __grid_con
 
 template <int NG>
 cudaError_t prepare(int *grid) {
-  const int smem = AttnSmem<NG>::bytes(kKv4MaxSlots);
   cudaError_t e = cudaSuccess;
-  auto set = [&](auto k) {
+  auto set = [&](auto k, int smem) {
     if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   };
-  set(k_kv4_attn<NG, false, false>);
-  set(k_kv4_attn<NG, false, true>);
-  set(k_kv4_attn<NG, true, false>);
-  set(k_kv4_attn<NG, true, true>);
+  const int s1 = AttnSmem<NG, 1>::bytes(kKv4MaxSlots), s2 = AttnSmem<NG, 2>::bytes(kKv4MaxSlots);
+  set(k_kv4_attn<NG, false, 1, false>, s1);
+  set(k_kv4_attn<NG, false, 1, true>, s1);
+  set(k_kv4_attn<NG, true, 1, false>, s1);
+  set(k_kv4_attn<NG, true, 1, true>, s1);
+  set(k_kv4_attn<NG, true, 2, false>, s2);
+  set(k_kv4_attn<NG, true, 2, true>, s2);
   int dev = 0, sms = 0;
   if (e == cudaSuccess) e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
@@ -732,13 +846,19 @@ cudaError_t prepare(int *grid) {
   return e;
 }
 
+template <int NG, bool FINE, int NT>
+cudaError_t run_attn(Kv4AttnArgs a, int grid, cudaStream_t st) {
+  constexpr int rows = (FINE ? 4 : 8) * NT;
+  a.nrb = (a.rows + rows - 1) / rows;
+  const int smem = AttnSmem<NG, NT>::bytes(a.n_slot);
+  auto kern = a.scores ? k_kv4_attn<NG, FINE, NT, true> : k_kv4_attn<NG, FINE, NT, false>;
+  return kv4_launch(kern, dim3(grid), dim3(kKv4Threads), smem, 1, st, a);
+}
+
 template <int NG>
 cudaError_t run_attn(const Kv4AttnArgs &a, int grid, cudaStream_t st) {
-  const int smem = AttnSmem<NG>::bytes(a.n_slot);
-  const bool split = a.out.dtype == PNB_F32, track = a.scores != nullptr;
-  auto kern = split ? (track ? k_kv4_attn<NG, true, true> : k_kv4_attn<NG, true, false>)
-                    : (track ? k_kv4_attn<NG, false, true> : k_kv4_attn<NG, false, false>);
-  return kv4_launch(kern, dim3(grid), dim3(kKv4Threads), smem, 1, st, a);
+  if (a.q.dtype == PNB_BF16 && a.out.dtype == PNB_BF16) return run_attn<NG, false, 1>(a, grid, st);
+  return a.rows <= 4 ? run_attn<NG, true, 1>(a, grid, st) : run_attn<NG, true, 2>(a, grid, st);
 }
 
 }  // namespace
