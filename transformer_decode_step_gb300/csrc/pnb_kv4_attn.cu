@@ -32,7 +32,7 @@ namespace {
 // chunk of 32 positions and kItemUnits more for its queries and its end.
 constexpr int kItemUnits = 1;
 // units a warp takes at least: below it a call uses fewer warps
-constexpr int kMinUnits = 2;
+constexpr int kMinUnits = 1;
 
 template <int NG, int NT>
 struct AttnSmem {
@@ -42,8 +42,8 @@ struct AttnSmem {
   static constexpr int kRing = kKv4Warps * kStages * kChunk;
   static constexpr int kQ = kRing;                                  // uint2 [warps][NT][2 NG][32], NT > 1
   static constexpr int kBars = kQ + (NT > 1 ? kKv4Warps * NT * 2 * NG * 32 * 8 : 0);
-  static constexpr int kPart = kBars + kKv4Warps * kStages * 8;     // int [2 warps]: item of each partial
-  static constexpr int kMl = kPart + kKv4Warps * 2 * 4;             // float2 [2 warps][8]: reference, sum
+  static constexpr int kPart = kBars + kKv4Warps * kStages * 8;     // int4 [2 warps]: item of each partial
+  static constexpr int kMl = kPart + kKv4Warps * 2 * 16;            // float2 [2 warps][8]: reference, sum
   static constexpr int kFlag = kMl + kKv4Warps * 2 * kKv4Rows * 8;
   static constexpr int kPre = kFlag + 16;                           // int [n_slot + 1]
   static int bytes(int n_slot) { return kPre + (2 * n_slot + 1) * 4; }   // and the lengths
@@ -160,21 +160,44 @@ struct Segment {
   int b, h, rb, c0, c1, nch, units, first;
 };
 
-__device__ __forceinline__ Segment segment_at(const int *pre, const Kv4AttnArgs &a, int x, int x1) {
+__device__ __forceinline__ Segment segment_at(const int *pre, const int *lens, const Kv4AttnArgs &a, int x, int x1) {
   Segment s;
   s.b = kv4_find(pre, a.n_slot, x);
-  const int items = a.n_kv * a.nrb, rel = x - pre[s.b];
-  const int per = (pre[s.b + 1] - pre[s.b]) / items;
-  s.nch = per - kItemUnits;
-  const int it = rel / per, off = rel - it * per;
-  s.h = it / a.nrb;
-  s.rb = it - s.h * a.nrb;
+  const int rel = x - pre[s.b];
+  s.nch = (lens[s.b] + kKv4Chunk - 1) / kKv4Chunk;
+  const int per = s.nch + kItemUnits;
+  const int it = (int)((unsigned)rel / (unsigned)per), off = rel - it * per;
+  s.h = it;
+  s.rb = 0;
+  if (a.nrb > 1) {
+    s.h = (int)((unsigned)it / (unsigned)a.nrb);
+    s.rb = it - s.h * a.nrb;
+  }
   s.units = min(x1 - x, per - off);
   s.c0 = max(0, off - kItemUnits);
   s.c1 = max(0, off + s.units - kItemUnits);
   s.first = x - off + kItemUnits;
   return s;
 }
+
+// The equal split of `total` units: part i of n takes [start(i), start(i + 1)),
+// start(i) = floor(i total / n), in 32 bits (n < 2^13).
+struct Split {
+  int n, base, rem;
+  __device__ __forceinline__ Split(int total, int parts) : n(parts) {
+    base = (int)((unsigned)total / (unsigned)parts);
+    rem = total - base * parts;
+  }
+  __device__ __forceinline__ int start(int i) const { return i * base + (int)((unsigned)(i * rem) / (unsigned)n); }
+  // the part that holds unit u
+  __device__ __forceinline__ int part_of(int u) const {
+    int i = (int)((float)u * ((float)n / ((float)base * (float)n + (float)rem)));
+    i = min(max(i, 0), n - 1);
+    while (i > 0 && start(i) > u) --i;
+    while (i + 1 < n && start(i + 1) <= u) ++i;
+    return i;
+  }
+};
 
 template <int N>
 __device__ __forceinline__ void store_row(const Kv4Rows &o, int64_t at, const float (&v)[N]) {
@@ -227,15 +250,15 @@ __device__ __forceinline__ void ldcg_row(const float *p, float (&v)[N]) {
 
 // a row's output from its sums (lane: dims NG lane ..), and its log-sum for the weights
 template <int NG, bool TRACK>
-__device__ __forceinline__ void finish_row(const Kv4AttnArgs &a, const Segment &sg, int row, int lane, float mref,
+__device__ __forceinline__ void finish_row(const Kv4AttnArgs &a, int b, int h, int row, int lane, float mref,
                                            float lsum, float (&os)[NG]) {
-  const int t = row / a.G, hq = sg.h * a.G + (row - t * a.G);
+  const int t = row / a.G, hq = h * a.G + (row - t * a.G);
   const float f = lsum != 0.f ? 1.f / lsum : 0.f;
 #pragma unroll
   for (int i = 0; i < NG; ++i) os[i] = lsum != 0.f ? os[i] * f : 0.f;
-  store_row<NG>(a.out, sg.b * a.out.slot + t * a.out.token + hq * a.out.head + lane * NG, os);
+  store_row<NG>(a.out, b * a.out.slot + t * a.out.token + hq * a.out.head + lane * NG, os);
   if (TRACK && lane == 0)
-    a.lse[((int64_t)sg.b * a.n_kv + sg.h) * a.rows + row] = lsum != 0.f ? mref + log2f(lsum) : INFINITY;
+    a.lse[((int64_t)b * a.n_kv + h) * a.rows + row] = lsum != 0.f ? mref + log2f(lsum) : INFINITY;
 }
 
 // Every warp takes an equal, contiguous run of the units and works alone: its
@@ -257,7 +280,7 @@ __global__ void __launch_bounds__(kKv4Threads, kKv4CtasPerSm)
   constexpr int RL = (FINE ? 1 : 2) * NT;     // rows whose scores and outputs a lane holds
   static_assert(RPI <= kKv4Rows, "partial rows");
   extern __shared__ __align__(128) uint8_t smem[];
-  int *spart = reinterpret_cast<int *>(smem + L::kPart);
+  int4 *spart = reinterpret_cast<int4 *>(smem + L::kPart);
   float2 *sml = reinterpret_cast<float2 *>(smem + L::kMl);
   int *sflag = reinterpret_cast<int *>(smem + L::kFlag);
   int *pre = reinterpret_cast<int *>(smem + L::kPre), *lens = pre + a.n_slot + 1;
@@ -269,17 +292,16 @@ __global__ void __launch_bounds__(kKv4Threads, kKv4CtasPerSm)
   if (lane == 0) {
     for (int s = 0; s < ST; ++s) mbar_init(bars + s, 1);
     fence_barrier_init();
-    spart[2 * warp] = spart[2 * warp + 1] = -1;
+    spart[2 * warp].x = spart[2 * warp + 1].x = -1;
   }
   pdl_wait();
   if (warp == 0) kv4_prefix(a.l, a.n_slot, kKv4Chunk, kItemUnits, a.n_kv * a.nrb, pre, lens);
   __syncthreads();
   const int total = pre[a.n_slot], cta = blockIdx.x;
   const int ctas = max(1, min((int)gridDim.x, total / (kKv4Warps * kMinUnits)));
-  const int64_t warps = (int64_t)ctas * kKv4Warps, my_warp = (int64_t)cta * kKv4Warps + warp;
-  // warp i takes units [total i / warps, total (i + 1) / warps), CTA i accordingly
-  const int x0 = (int)(my_warp * total / warps), x1 = (int)((my_warp + 1) * total / warps);
-  auto cta_of = [&](int unit) { return (int)((((int64_t)unit + 1) * ctas - 1) / total); };
+  const Split by_cta(total, ctas);   // and each CTA's part is split over its warps the same way
+  const int u0 = by_cta.start(cta), u1 = by_cta.start(cta + 1);
+  const int x0 = u0 + (u1 - u0) * warp / kKv4Warps, x1 = u0 + (u1 - u0) * (warp + 1) / kKv4Warps;
 
   // slots with nothing to attend to answer zero
   for (int b = cta; b < a.n_slot; b += gridDim.x) {
@@ -293,18 +315,21 @@ __global__ void __launch_bounds__(kKv4Threads, kKv4CtasPerSm)
   if (cta >= ctas || total == 0) return;
 
   const int64_t head_bytes = (int64_t)(a.l.cap / kKv4Chunk) * L::kChunk;
-  int px = x0, pc = 0, pc1 = 0;    // producer: next segment's first unit, next chunk, segment's end
+  // producer: next segment's first unit, next chunk, segment's end
+  int px = x0, pc = 0, pc1 = 0;
   const uint8_t *pbase = nullptr;
+  auto enter = [&](const Segment &ps) {
+    px += ps.units;
+    pc = ps.c0;
+    pc1 = ps.c1;
+    pbase = a.l.codes + ((int64_t)ps.b * a.n_kv + ps.h) * head_bytes;
+  };
   int pstage = 0;
   bool dead = false;
   auto produce = [&]() {           // copy the warp's next chunk, if any, into stage pstage
     while (pc >= pc1) {
       if (px >= x1) return;
-      const Segment ps = segment_at(pre, a, px, x1);
-      px += ps.units;
-      pc = ps.c0;
-      pc1 = ps.c1;
-      pbase = a.l.codes + ((int64_t)ps.b * a.n_kv + ps.h) * head_bytes;
+      enter(segment_at(pre, lens, a, px, x1));
     }
     if (lane == 0 && !dead) {
       mbar_arrive_expect_tx(bars + pstage, L::kChunk);
@@ -322,7 +347,8 @@ __global__ void __launch_bounds__(kKv4Threads, kKv4CtasPerSm)
   asm volatile("" : "+r"(magic));
 #pragma unroll 1
   for (int x = x0; x < x1;) {
-    const Segment sg = segment_at(pre, a, x, x1);
+    const Segment sg = segment_at(pre, lens, a, x, x1);
+    if (x == x0) enter(sg);
     x += sg.units;
     if (sg.c0 >= sg.c1) continue;
     const int len = lens[sg.b];
@@ -653,7 +679,7 @@ __global__ void __launch_bounds__(kKv4Threads, kKv4CtasPerSm)
       }
     } else {
       const int which = sg.c0 == 0 ? 1 : 0;    // 1: the item starts here and goes on behind
-      if (lane == 0) spart[2 * warp + which] = sg.first;
+      if (lane == 0) spart[2 * warp + which] = make_int4(sg.first, sg.nch, sg.b, sg.h * a.nrb + sg.rb);
       // the rows, rotated by 8 floats each against bank conflicts, into the
       // warp's ring once its last chunk is used; before that to global memory
       float *pd = x >= x1 ? reinterpret_cast<float *>(ring) + which * RPI * HD : nullptr;
@@ -685,11 +711,22 @@ __global__ void __launch_bounds__(kKv4Threads, kKv4CtasPerSm)
   // The CTA's partial rows, in the units' order: entry 2 w is warp w's item
   // from before, 2 w + 1 the one that it starts.  Consecutive entries of one
   // item form a group; the warps share out the groups' rows.
-  const int mine = lane < 2 * kKv4Warps ? spart[lane] : -1;
+  const int mine = lane < 2 * kKv4Warps ? spart[lane].x : -1;
   const uint32_t valid = __ballot_sync(0xffffffffu, mine >= 0), below = valid & ((1u << lane) - 1u);
   const int before = __shfl_sync(0xffffffffu, mine, below ? 31 - __clz(below) : 0);
   const uint32_t starts = __ballot_sync(0xffffffffu, mine >= 0 && (!below || before != mine));
   const int groups = __popc(starts), rows = min(RPI, a.rows);
+  struct Item {
+    int first, nch, b, h, rb;
+  };
+  auto item_of = [&](int4 e) {
+    Item it = {e.x, e.y, e.z, e.w, 0};
+    if (a.nrb > 1) {
+      it.h = e.w / a.nrb;
+      it.rb = e.w - it.h * a.nrb;
+    }
+    return it;
+  };
 #pragma unroll 1
   for (int task = warp; task < groups * rows; task += kKv4Warps) {
     const int gi = task / rows, i = task - gi * rows;
@@ -697,11 +734,9 @@ __global__ void __launch_bounds__(kKv4Threads, kKv4CtasPerSm)
     for (int k = 0; k < gi; ++k) m &= m - 1u;
     const uint32_t rest = m & (m - 1u), begin = m & -m;          // begin: the group's first bit
     const uint32_t members = valid & ((rest & -rest) - begin);   // up to the next group's
-    const int first = __shfl_sync(0xffffffffu, mine, __ffs(begin) - 1);
-    const Segment sg = segment_at(pre, a, first, total);
-    const int my_row = sg.rb * RPI + i;
+    const Item it = item_of(spart[__ffs(begin) - 1]);
+    const int my_row = it.rb * RPI + i;
     if (my_row >= a.rows) continue;
-    const int c0 = cta_of(first), c1 = cta_of(first + sg.nch - 1);
     // lane e holds entry e's factor
     const float2 ml = (members >> lane) & 1u ? sml[lane * kKv4Rows + i] : make_float2(0.f, 0.f);
     const float mref = warp_max(ml.y != 0.f ? ml.x : -INFINITY);
@@ -718,10 +753,10 @@ __global__ void __launch_bounds__(kKv4Threads, kKv4CtasPerSm)
 #pragma unroll
       for (int j = 0; j < NG; ++j) os[j] = fmaf(v[j], f, os[j]);
     }
-    if (c0 == cta && c1 == cta) {
-      finish_row<NG, TRACK>(a, sg, my_row, lane, mref, lsum, os);
+    if (it.first >= u0 && it.first + it.nch <= u1) {
+      finish_row<NG, TRACK>(a, it.b, it.h, my_row, lane, mref, lsum, os);
     } else {
-      const int64_t at = (int64_t)(2 * cta + (c0 == cta ? 1 : 0)) * kKv4Rows + i;
+      const int64_t at = (int64_t)(2 * cta + (it.first >= u0 ? 1 : 0)) * kKv4Rows + i;
 #pragma unroll
       for (int j = 0; j < NG; ++j) a.part[at * HD + lane * NG + j] = os[j];
       if (lane == 0) reinterpret_cast<float2 *>(a.part_ml)[at] = make_float2(mref, lsum);
@@ -730,67 +765,76 @@ __global__ void __launch_bounds__(kKv4Threads, kKv4CtasPerSm)
 
   // items shared with other CTAs (the CTA's first and last at most): the last
   // CTA to arrive adds them up
-  int shared_first[2] = {-1, -1};
+  Item front = {}, back = {};
+  bool at_front = false, at_back = false;
   if (groups > 0) {
-    const int f0 = __shfl_sync(0xffffffffu, mine, __ffs(starts) - 1);
-    const int f1 = __shfl_sync(0xffffffffu, mine, 31 - __clz(starts));
-    if (cta_of(f0) != cta) shared_first[0] = f0;
-    const Segment sg = segment_at(pre, a, f1, total);
-    if (cta_of(f1 + sg.nch - 1) != cta && (f1 != f0 || shared_first[0] < 0)) shared_first[1] = f1;
+    front = item_of(spart[__ffs(starts) - 1]);
+    back = item_of(spart[31 - __clz(starts)]);
+    at_front = front.first < u0;
+    at_back = back.first + back.nch > u1 && !(at_front && back.first == front.first);
   }
-  if (shared_first[0] < 0 && shared_first[1] < 0) return;
-
-  __threadfence();
+  if (!at_front && !at_back) return;
   __syncthreads();
   if (tid < 2) {
-    const int first = shared_first[tid];
-    int last = 0;
-    if (first >= 0) {
-      const int c0 = cta_of(first), c1 = cta_of(first + segment_at(pre, a, first, total).nch - 1);
-      last = atomicAdd(a.counter + c0, 1u) == (unsigned)(c1 - c0);
-      if (last) a.counter[c0] = 0;
+    const Item it = tid ? back : front;
+    int n = 0, c0 = 0;
+    if (tid ? at_back : at_front) {
+      c0 = by_cta.part_of(it.first);
+      n = by_cta.part_of(it.first + it.nch - 1) - c0 + 1;
+      __threadfence();             // the CTA's partial rows, ordered by the barrier before it
+      if (atomicAdd(a.counter + c0, 1u) == (unsigned)(n - 1)) a.counter[c0] = 0;
+      else n = 0;
+      __threadfence();
     }
-    sflag[tid] = last;
+    sflag[2 * tid] = n;
+    sflag[2 * tid + 1] = c0;
   }
   __syncthreads();
 #pragma unroll 1
   for (int i = 0; i < 2; ++i) {
-    if (!sflag[i]) continue;
-    __threadfence();
-    const int first = shared_first[i];
-    const Segment sg = segment_at(pre, a, first, total);
-    const int my_row = sg.rb * RPI + warp;
-    if (warp >= RPI || my_row >= a.rows) continue;
-    const int c0 = cta_of(first), n = cta_of(first + sg.nch - 1) - c0 + 1;
+    const int n = sflag[2 * i], c0 = sflag[2 * i + 1];
+    const Item it = i ? back : front;
+    const int my_row = it.rb * RPI + warp;
+    if (n == 0 || warp >= RPI || my_row >= a.rows) continue;
     // the first CTA's partial is its second one, all others' their first
     auto at = [&](int k) { return (int64_t)(2 * (c0 + k) + (k == 0 ? 1 : 0)) * kKv4Rows + warp; };
-    float mref = -INFINITY, lsum = 0.f, os[NG] = {};
-    for (int k = lane; k < n; k += 32) {
-      const float2 ml = __ldcg(reinterpret_cast<const float2 *>(a.part_ml) + at(k));
-      if (ml.y != 0.f) mref = fmaxf(mref, ml.x);
+    auto ml_of = [&](int k) {
+      return k < n ? __ldcg(reinterpret_cast<const float2 *>(a.part_ml) + at(k)) : make_float2(0.f, 0.f);
+    };
+    float2 ml = ml_of(lane);               // lane k: partial k0 + k
+    float mref = ml.y != 0.f ? ml.x : -INFINITY, lsum = 0.f, os[NG] = {};
+    for (int k = lane + 32; k < n; k += 32) {
+      const float2 x = ml_of(k);
+      if (x.y != 0.f) mref = fmaxf(mref, x.x);
     }
     mref = warp_max(mref);
-    for (int k0 = 0; k0 < n; k0 += 32) {   // lane k: the factor of partial k0 + k
-      float fac = 0.f, l = 0.f;
-      if (k0 + lane < n) {
-        const float2 ml = __ldcg(reinterpret_cast<const float2 *>(a.part_ml) + at(k0 + lane));
-        if (ml.y != 0.f) {
-          fac = ex2(ml.x - mref);
-          l = ml.y * fac;
-        }
-      }
+    for (int k0 = 0; k0 < n; k0 += 32) {
+      if (k0 > 0) ml = ml_of(k0 + lane);
+      const float fac = ml.y != 0.f ? ex2(ml.x - mref) : 0.f, l = ml.y != 0.f ? ml.y * fac : 0.f;
       lsum += warp_sum(l);
       const int m = min(32, n - k0);
-#pragma unroll 8
-      for (int k = 0; k < m; ++k) {
-        float v[NG];
-        ldcg_row<NG>(a.part + at(k0 + k) * HD + lane * NG, v);
-        const float f = __shfl_sync(0xffffffffu, fac, k);
+      for (int k = 0; k < m; k += 8) {     // eight rows' loads in flight
+        float v[8][NG];
 #pragma unroll
-        for (int j = 0; j < NG; ++j) os[j] = fmaf(v[j], f, os[j]);
+        for (int q = 0; q < 8; ++q) {
+          if (k + q < m) {
+            ldcg_row<NG>(a.part + at(k0 + k + q) * HD + lane * NG, v[q]);
+          } else {
+#pragma unroll
+            for (int j = 0; j < NG; ++j) v[q][j] = 0.f;
+          }
+        }
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          const float f = __shfl_sync(0xffffffffu, fac, (k + q) & 31);
+          if (k + q < m) {
+#pragma unroll
+            for (int j = 0; j < NG; ++j) os[j] = fmaf(v[q][j], f, os[j]);
+          }
+        }
       }
     }
-    finish_row<NG, TRACK>(a, sg, my_row, lane, mref, lsum, os);
+    finish_row<NG, TRACK>(a, it.b, it.h, my_row, lane, mref, lsum, os);
   }
 }
 

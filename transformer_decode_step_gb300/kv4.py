@@ -6,12 +6,16 @@ a torch tensor; lengths, ids and weights are views of it.
 from __future__ import annotations
 
 import ctypes
+import struct
 from typing import Optional
 
-from . import (PNB_BF16, PNB_F32, PnbError, _ptr, _stream, check, pnb_kvq_append,
-               pnb_kvq_attention, pnb_kvq_bytes, pnb_kvq_check, pnb_kvq_config, pnb_kvq_evict,
-               pnb_kvq_free, pnb_kvq_layer_views, pnb_kvq_new, pnb_kvq_read, pnb_kvq_reset,
-               pnb_kvq_views, pnb_rows)
+from . import (PNB_BF16, PNB_F32, PnbError, _ptr, check, pnb_kvq_append, pnb_kvq_attention,
+               pnb_kvq_bytes, pnb_kvq_check, pnb_kvq_config, pnb_kvq_evict, pnb_kvq_free,
+               pnb_kvq_layer_views, pnb_kvq_new, pnb_kvq_read, pnb_kvq_reset, pnb_kvq_views)
+
+# a pnb_rows as bytes (a ctypes.Structure takes three times as long to fill, and a
+# short attention call is bound by the host)
+_pack_rows = struct.Struct("@Pqqqi4x").pack
 
 
 class Kv4Cache:
@@ -27,6 +31,8 @@ class Kv4Cache:
         self._h = None
         self.cfg = pnb_kvq_config(n_layer, n_slot, n_head, n_kv_head, head_dim, cap, track)
         self._dtypes = {torch.float32: PNB_F32, torch.bfloat16: PNB_BF16}
+        self._int32 = torch.int32
+        self._raw_stream = torch._C._cuda_getCurrentRawStream
         nbytes = int(pnb_kvq_bytes(ctypes.byref(self.cfg)))
         if buf is None:
             buf = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=device or "cuda")
@@ -35,6 +41,7 @@ class Kv4Cache:
         check(pnb_kvq_new(ctypes.byref(self.cfg), _ptr(buf), buf.numel() * buf.element_size(),
                           ctypes.byref(h)), "pnb_kvq_new")
         self._h = h.value
+        self._device = buf.get_device()
         self._views = {}
 
     def __del__(self):
@@ -46,66 +53,70 @@ class Kv4Cache:
     def handle(self) -> int:
         return self._h
 
-    def _rows(self, t, what: str, T: Optional[int], heads: int) -> pnb_rows:
+    def _stream(self, stream) -> int:
+        """A stream's handle; by default the current one of the cache's device."""
+        if stream is None:
+            return self._raw_stream(self._device)
+        return stream if isinstance(stream, int) else stream.cuda_stream
+
+    def _rows(self, t, what: str, T: int, heads: int) -> bytes:
         g = self.cfg
-        shape = t.shape
-        if len(shape) != 4 or shape[0] != g.n_slot or shape[2] != heads or shape[3] != g.head_dim \
-                or (T is not None and shape[1] != T):
-            raise PnbError(-1, f"{what}: shape {tuple(shape)} is not [{g.n_slot}][{T or 'T'}]"
+        if tuple(t.shape) != (g.n_slot, T, heads, g.head_dim):
+            raise PnbError(-1, f"{what}: shape {tuple(t.shape)} is not [{g.n_slot}][{T}]"
                                f"[{heads}][{g.head_dim}]")
         dt = self._dtypes.get(t.dtype)
-        s = t.stride()
-        if dt is None or s[3] != 1:
+        slot, token, head, one = t.stride()
+        if dt is None or one != 1:
             raise PnbError(-1, f"{what}: needs fp32 or bf16 rows with head_dim contiguous")
-        if t.device != self.buf.device:
+        if t.get_device() != self._device:
             raise PnbError(-10, f"{what}: on {t.device}, the cache is on {self.buf.device}")
         # a dimension of one element has no stride of its own
-        return pnb_rows(t.data_ptr(), s[0] if shape[0] > 1 else 0, s[1] if shape[1] > 1 else 0,
-                        s[2] if heads > 1 else 0, dt)
+        return _pack_rows(t.data_ptr(), slot if g.n_slot > 1 else 0, token if T > 1 else 0,
+                          head if heads > 1 else 0, dt)
 
     def _ints(self, t, what: str):
         if t is None:
             return None
-        import torch
-        if t.dtype != torch.int32 or t.numel() != self.cfg.n_slot or not t.is_contiguous() \
-                or t.device != self.buf.device:
+        if t.dtype != self._int32 or t.numel() != self.cfg.n_slot or not t.is_contiguous() \
+                or t.get_device() != self._device:
             raise PnbError(-1, f"{what}: needs {self.cfg.n_slot} contiguous int32 on the cache's device")
         return t.data_ptr()
 
+    @staticmethod
+    def _tokens(t, what: str) -> int:
+        if t.dim() != 4:
+            raise PnbError(-1, f"{what}: needs rows [n_slot][T][heads][head_dim]")
+        return t.size(1)
+
     def reset(self, slot: Optional[int] = None, stream=None):
         """Empty one slot, or all of them (which also clears the error bits), in every layer."""
-        check(pnb_kvq_reset(self._h, -1 if slot is None else slot, _stream(stream)), "pnb_kvq_reset")
+        check(pnb_kvq_reset(self._h, -1 if slot is None else slot, self._stream(stream)), "pnb_kvq_reset")
 
     def append(self, layer: int, k, v, n_new=None, start=None, stream=None):
         """Quantise and append n_new[b] (default: all T) rows of every slot b at entry
         start[b] (default: its length).  n_new, start: device int32 [n_slot]."""
-        n = self.cfg.n_kv_head
-        rk = self._rows(k, "k", None, n)
-        rv = self._rows(v, "v", k.shape[1], n)
-        check(pnb_kvq_append(self._h, layer, ctypes.byref(rk), ctypes.byref(rv), k.shape[1],
+        n, T = self.cfg.n_kv_head, self._tokens(k, "k")
+        check(pnb_kvq_append(self._h, layer, self._rows(k, "k", T, n), self._rows(v, "v", T, n), T,
                              self._ints(n_new, "n_new"), self._ints(start, "start"),
-                             _stream(stream)), "pnb_kvq_append")
+                             self._stream(stream)), "pnb_kvq_append")
 
     def read(self, layer: int, k, v, first=None, stream=None):
         """Write the values of entries first[b] (default 0) .. + T - 1 into k and v."""
-        n = self.cfg.n_kv_head
-        rk = self._rows(k, "k", None, n)
-        rv = self._rows(v, "v", k.shape[1], n)
-        check(pnb_kvq_read(self._h, layer, self._ints(first, "first"), k.shape[1],
-                           ctypes.byref(rk), ctypes.byref(rv), _stream(stream)), "pnb_kvq_read")
+        n, T = self.cfg.n_kv_head, self._tokens(k, "k")
+        check(pnb_kvq_read(self._h, layer, self._ints(first, "first"), T, self._rows(k, "k", T, n),
+                           self._rows(v, "v", T, n), self._stream(stream)), "pnb_kvq_read")
 
     def attention(self, layer: int, q, out, decay: Optional[float] = None, stream=None):
         """Attention of the last T appended tokens' queries into ``out``; with ``decay``,
         weights = decay * weights + this call's softmax weights."""
-        n = self.cfg.n_head
-        rq = self._rows(q, "q", None, n)
-        ro = self._rows(out, "out", q.shape[1], n)
+        n, T = self.cfg.n_head, self._tokens(q, "q")
         if decay is None:
             decay = -1.0
         elif not decay >= 0.0:
             raise PnbError(-1, f"decay {decay} is negative or not a number")
-        check(pnb_kvq_attention(self._h, layer, ctypes.byref(rq), q.shape[1], ctypes.byref(ro),
-                                decay, _stream(stream)), "pnb_kvq_attention")
+        check(pnb_kvq_attention(self._h, layer, self._rows(q, "q", T, n), T,
+                                self._rows(out, "out", T, n), decay, self._stream(stream)),
+              "pnb_kvq_attention")
 
     def evict(self, layer: int, budget: int, n_sink: int = 0, n_recent: int = 0,
               dst: Optional["Kv4Cache"] = None, dst_layer: Optional[int] = None, stream=None):
@@ -113,7 +124,7 @@ class Kv4Cache:
         (dst, dst_layer); see pnb_kvq_evict for which."""
         d = self if dst is None else dst
         check(pnb_kvq_evict(self._h, layer, d._h, layer if dst_layer is None else dst_layer, budget,
-                            n_sink, n_recent, _stream(stream)), "pnb_kvq_evict")
+                            n_sink, n_recent, self._stream(stream)), "pnb_kvq_evict")
 
     def _view(self, layer: int, name: str):
         import torch
