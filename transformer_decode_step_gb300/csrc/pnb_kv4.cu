@@ -11,6 +11,33 @@ namespace pnb {
 
 namespace {
 
+// 8 x 8 nibbles transposed: nibble j of word i becomes nibble i of word j.
+__device__ __forceinline__ void transpose_nibbles(uint32_t (&w)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {          // halves of rows i and i + 4
+    const uint32_t a = w[i], b = w[i + 4];
+    w[i] = __byte_perm(a, b, 0x5410);
+    w[i + 4] = __byte_perm(a, b, 0x7632);
+  }
+#pragma unroll
+  for (int g = 0; g < 8; g += 4)
+#pragma unroll
+    for (int i = g; i < g + 2; ++i) {    // bytes of rows i and i + 2
+      const uint32_t a = w[i], b = w[i + 2];
+      w[i] = __byte_perm(a, b, 0x6240);
+      w[i + 2] = __byte_perm(a, b, 0x7351);
+    }
+#pragma unroll
+  for (int i = 0; i < 8; i += 2) {       // nibbles of rows i and i + 1
+    const uint32_t a = w[i], b = w[i + 1];
+    w[i] = (a & 0x0f0f0f0fu) | ((b << 4) & 0xf0f0f0f0u);
+    w[i + 1] = ((a >> 4) & 0x0f0f0f0fu) | (b & 0xf0f0f0f0u);
+  }
+}
+
+// position (0..31 in a chunk) of nibble n of a V word of class c
+__device__ __forceinline__ int vpos(int c, int n) { return 8 * (n & 3) + 2 * c + (n >> 2); }
+
 // ------------------------------------------------------------------ append
 // One Q4_0 block is held by 4 neighbouring lanes, 8 dims each:
 //   d = fp16(max|x| / 7), u = clamp(rint(x / d), -8, 7) + 8
@@ -18,151 +45,269 @@ namespace {
 // which can be off by one next to a border, and put right from the residual
 // x - k d (one fma, exact there: x lies within a factor of two of k d, or k is
 // 0): a residual beyond d / 2, or of exactly d / 2 with k odd (ties go to the
-// even integer), moves k by one.
+// even integer), moves k by one.  Few blocks have such a value, or a scale so
+// coarse (subnormal) that a quotient leaves [-7.5, 7.5].
 // NaN and infinities make the block's scale NaN; a scale past fp16's range
 // saturates.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+
 __device__ __forceinline__ uint32_t q4_word(const float (&x)[8], __half *scale) {
-  uint32_t top = 0;   // as integers, magnitudes order like floats, NaN on top
+  float top = 0.f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(x[i]) & 0x7fffffffu);
-  top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-  top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-  if (top >= 0x7f800000u) {
-    *scale = __ushort_as_half((unsigned short)0x7fffu);
-    return 0x88888888u;
-  }
-  const __half d = __float2half_rn(fminf(__fdiv_rn(__uint_as_float(top), 7.f), 65504.f));
-  *scale = d;
+  for (int i = 0; i < 8; ++i) top = max_nan(top, fabsf(x[i]));
+  top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, 1));
+  top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, 2));
+  const bool finite = top < INFINITY;    // false for NaN too
+  const __half d = __float2half_rn(fminf(__fdiv_rn(top, 7.f), 65504.f));
   const float df = __half2float(d);
-  if (df == 0.f) return 0x88888888u;
+  *scale = finite ? d : __ushort_as_half((unsigned short)0x7fffu);
+  if (!finite || df == 0.f) return 0x88888888u;
+  const float big = 12582912.f;          // 1.5 * 2^23: adding it rounds to an integer, in the low bits
   const float inv = __frcp_rn(df), half_d = 0.5f * df;
   uint32_t w = 0;
+  float off = 0.f;
 #pragma unroll
   for (int i = 7; i >= 0; --i) {
-    const float big = 12582912.f;                 // 1.5 * 2^23: adding it rounds to an integer
-    float k = __fadd_rn(__fmaf_rn(x[i], inv, big), -big);
-    const float e = __fmaf_rn(-k, df, x[i]);
-    if (fabsf(e) >= half_d && (fabsf(e) > half_d || (__float_as_uint(k + big) & 1u))) k += copysignf(1.f, e);
-    k = fminf(fmaxf(k, -8.f), 7.f);
-    w = (w << 4) | (__float_as_uint(k + (big + 8.f)) & 15u);
+    const float t = __fmaf_rn(x[i], inv, big);
+    off = fmaxf(off, fabsf(__fmaf_rn(-__fadd_rn(t, -big), df, x[i])));
+    w = (w << 4) | (__float_as_uint(t) & 15u);
   }
-  return w;
+  if (off >= half_d || top > 7.5f * df) {
+    w = 0;
+#pragma unroll 1
+    for (int i = 7; i >= 0; --i) {
+      float v = x[0];
+#pragma unroll
+      for (int j = 1; j < 8; ++j) v = i == j ? x[j] : v;
+      float k = __fadd_rn(__fmaf_rn(v, inv, big), -big);
+      const float e = __fmaf_rn(-k, df, v);
+      if (fabsf(e) > half_d || (fabsf(e) == half_d && (__float_as_uint(k + big) & 1u))) k += copysignf(1.f, e);
+      k = fminf(fmaxf(k, -8.f), 7.f);
+      w = (w << 4) | (__float_as_uint(k + big) & 15u);
+    }
+  }
+  return w ^ 0x88888888u;                // + 8 modulo 16
 }
 
+// 8 consecutive elements, as loaded
 template <typename T>
-__device__ __forceinline__ void load8(const void *p, int64_t at, float (&x)[8]) {
-  if constexpr (sizeof(T) == 2) {
-    load_vals<__nv_bfloat16, 8>(static_cast<const __nv_bfloat16 *>(p) + at, x);
-  } else {
-    const float4 *q = reinterpret_cast<const float4 *>(static_cast<const float *>(p) + at);
-    const float4 u = q[0], v = q[1];
-    x[0] = u.x; x[1] = u.y; x[2] = u.z; x[3] = u.w;
-    x[4] = v.x; x[5] = v.y; x[6] = v.z; x[7] = v.w;
+struct Raw8 {
+  uint4 v[sizeof(T) / 2];
+  __device__ __forceinline__ void load(const void *p, int64_t at) {
+    const uint4 *q = reinterpret_cast<const uint4 *>(static_cast<const T *>(p) + at);
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) v[i] = q[i];
   }
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) v[i] = make_uint4(0, 0, 0, 0);
+  }
+  __device__ __forceinline__ void floats(float (&x)[8]) const {
+    if constexpr (sizeof(T) == 2) {
+      load_vals<__nv_bfloat16, 8>(reinterpret_cast<const __nv_bfloat16 *>(v), x);
+    } else {
+      x[0] = __uint_as_float(v[0].x); x[1] = __uint_as_float(v[0].y);
+      x[2] = __uint_as_float(v[0].z); x[3] = __uint_as_float(v[0].w);
+      x[4] = __uint_as_float(v[1].x); x[5] = __uint_as_float(v[1].y);
+      x[6] = __uint_as_float(v[1].z); x[7] = __uint_as_float(v[1].w);
+    }
+  }
+};
+
+// What a slot's append does, from the device's counts.
+struct AppendRange {
+  int start, end, seen0, bad;   // entries [start, end), id of the first
+  __device__ __forceinline__ AppendRange(const Kv4AppendArgs &a, int b) {
+    const int len = kv4_len(a.l, b), seen = a.l.seen[b];
+    int n = a.n_new ? a.n_new[b] : a.T;
+    start = a.start ? a.start[b] : len;
+    bad = 0;
+    if (start < 0 || start > len || n < 0 || n > a.T) {
+      bad = kErrRange;          // the slot stays as it was
+      start = len;
+      n = 0;
+    }
+    if (n > a.l.cap - start) {
+      bad = kErrFull;           // rows past the capacity are not stored
+      n = a.l.cap - start;
+    }
+    end = start + n;
+    seen0 = seen - (len - start);
+  }
+  __device__ __forceinline__ void commit(const Kv4AppendArgs &a, int b) const {
+    if (bad) set_error(a.err, bad);
+    if (bad != kErrRange) {
+      a.l.len[b] = end;
+      a.l.seen[b] = seen0 + (end - start);
+    }
+  }
+};
+
+// Few tokens: one CTA per slot, so that it alone reads and moves the length.
+// First every (token, head, K or V) row is quantised, TPR threads each; then
+// each 16-byte unit of V words (8 positions of 4 dims) that holds a new
+// position is read, completed and written by one thread.  Bound by its four
+// dependent trips to memory.
+constexpr int kStepThreads = 512, kStepTokens = 8;
+
+template <int NG, typename T>
+__global__ void __launch_bounds__(kStepThreads) k_kv4_append_step(const __grid_constant__ Kv4AppendArgs a) {
+  constexpr int TPR = 4 * NG, CH = kv4_chunk_bytes(NG);
+  extern __shared__ __align__(16) uint32_t vrow[];       // [T][n_kv][TPR] V codes
+  const int tid = threadIdx.x, b = blockIdx.x;
+  pdl_wait();
+  const AppendRange r(a, b);
+  const int n = r.end - r.start, rows = n * a.n_kv;
+  uint8_t *slot = a.l.codes + (int64_t)b * a.n_kv * (a.l.cap / kKv4Chunk) * CH;
+  auto chunk_of = [&](int h, int pos) { return slot + ((int64_t)h * (a.l.cap / kKv4Chunk) + pos / kKv4Chunk) * CH; };
+  // whole warps run the block maximum's shuffles: 2 rows TPR is a multiple of 32 only by padding
+  const int work = (2 * rows * TPR + 31) / 32 * 32;
+  for (int i = tid; i < work; i += kStepThreads) {
+    const int row = i / TPR, sub = i % TPR, rr = row >> 1, h = rr % a.n_kv, t = rr / a.n_kv;
+    const bool live = rr < rows, is_v = row & 1;
+    const Kv4Rows &src = is_v ? a.v : a.k;
+    Raw8<T> raw;
+    if (live) raw.load(src.p, b * src.slot + t * src.token + h * src.head + sub * 8);
+    else raw.clear();
+    float x[8];
+    raw.floats(x);
+    __half d;
+    const uint32_t w = q4_word(x, &d);
+    if (!live) continue;
+    const int pos = r.start + t, p = pos % kKv4Chunk, j = sub >> 2, cc = sub & 3;
+    uint8_t *chunk = chunk_of(h, pos);
+    if (is_v) vrow[(t * a.n_kv + h) * TPR + sub] = w;
+    else *reinterpret_cast<uint32_t *>(chunk + kv4_kword(NG, p, cc, j)) = w;
+    if (cc == 0)
+      *reinterpret_cast<__half *>(chunk + (is_v ? kv4_vscale_off(NG) + kv4_vscale(NG, p, j)
+                                                : kv4_kscale_off(NG) + kv4_kscale(NG, p, j))) = d;
+    if (sub == 0 && !is_v) {
+      const int64_t at = ((int64_t)b * a.n_kv + h) * a.l.cap + pos;
+      a.l.ids[at] = r.seen0 + t;
+      a.l.weights[at] = 0.f;
+    }
+  }
+  __syncthreads();
+  // units (h, J, rr, token): the first token of its chunk and class does the unit's work
+  for (int i = tid; i < rows * 8 * NG; i += kStepThreads) {
+    const int rr = i % 8, J = (i / 8) % NG, h = (i / (8 * NG)) % a.n_kv, t0 = i / (8 * NG * a.n_kv);
+    const int pos = r.start + t0, c = (pos >> 1) & 3;
+    bool first = true;
+    for (int t = 0; t < t0; ++t) {
+      const int q = r.start + t;
+      first &= q / kKv4Chunk != pos / kKv4Chunk || ((q >> 1) & 3) != c;
+    }
+    if (!first) continue;
+    uint4 *unit = reinterpret_cast<uint4 *>(chunk_of(h, pos) + kv4_v_off(NG) + kv4_vunit(J, rr, c));
+    uint4 u = *unit;
+    for (int t = t0; t < n; ++t) {
+      const int q = r.start + t;
+      if (q / kKv4Chunk != pos / kKv4Chunk || ((q >> 1) & 3) != c) continue;
+      const int sh = kv4_vshift(q % kKv4Chunk);
+      const uint4 w = *reinterpret_cast<const uint4 *>(vrow + (t * a.n_kv + h) * TPR + 4 * J);
+      const uint32_t keep = ~(15u << sh);
+      u.x = (u.x & keep) | (((w.x >> (4 * rr)) & 15u) << sh);
+      u.y = (u.y & keep) | (((w.y >> (4 * rr)) & 15u) << sh);
+      u.z = (u.z & keep) | (((w.z >> (4 * rr)) & 15u) << sh);
+      u.w = (u.w & keep) | (((w.w >> (4 * rr)) & 15u) << sh);
+    }
+    *unit = u;
+  }
+  if (tid == 0) r.commit(a, b);
 }
 
-constexpr int kAppendThreads = 256;
+// Many tokens: CTAs of kAppendChunks chunks of one (slot, KV head).  128
+// threads quantise a chunk's new K rows, 128 its V rows, 16 bytes of a row (32
+// for fp32) per thread and pass, the next chunk's rows on their way meanwhile.
+// K words go straight to their place; V words hold 8 positions of one dim, so
+// 8 x 8 nibbles are transposed by one thread each through shared memory, and a
+// chunk that already holds entries keeps their nibbles.  The slot's last CTA
+// moves its length.  Bound by the rows' bytes.
+constexpr int kAppendThreads = 256, kAppendChunks = 4;
 
-// One CTA per (chunk, KV head, slot): 128 threads quantise the chunk's new K
-// rows, 128 its new V rows (16 bytes or 32 of a row per thread).  K words go
-// straight to their place; V words hold 8 positions of one dim, so the codes
-// cross shared memory, and a chunk that already holds entries keeps their
-// nibbles.  Bound by the rows' bytes; a single token by its dependent loads.
 template <int NG, typename T>
 __global__ void __launch_bounds__(kAppendThreads) k_kv4_append(const __grid_constant__ Kv4AppendArgs a) {
   constexpr int TPR = 4 * NG;                     // threads (words) per row
   constexpr int RPP = 128 / TPR;                  // rows per pass: 8, 16, 32
   constexpr int PASSES = kKv4Chunk / RPP;
-  __shared__ __align__(16) uint32_t vcode[kKv4Chunk][TPR];
+  constexpr int VP = TPR + 4;                     // V row pitch in words, against bank conflicts
+  __shared__ __align__(16) uint32_t vcode[2][kKv4Chunk * VP];
   const int tid = threadIdx.x, b = blockIdx.z, h = blockIdx.y;
   pdl_wait();
-  const int len = kv4_len(a.l, b), seen = a.l.seen[b];
-  int start = a.start ? a.start[b] : len;
-  int n = a.n_new ? a.n_new[b] : a.T;
-  int bad = 0;
-  if (start < 0 || start > len || n < 0 || n > a.T) {
-    bad = kErrRange;                              // the slot stays as it was
-    start = len;
-    n = 0;
-  }
-  if (n > a.l.cap - start) {
-    bad = kErrFull;                               // rows past the capacity are not stored
-    n = a.l.cap - start;
-  }
-  const int end = start + n;
-  const int seen0 = seen - (len - start);         // id of the first new entry
-  const int ch = start / kKv4Chunk + (int)blockIdx.x, p0 = ch * kKv4Chunk;
-  const int lo = max(start, p0), hi = min(end, p0 + kKv4Chunk);
-  if (lo < hi) {
-    const int64_t bh = (int64_t)b * a.n_kv + h;
-    uint8_t *chunk = a.l.codes + (bh * (a.l.cap / kKv4Chunk) + ch) * kv4_chunk_bytes(NG);
-    const bool is_v = tid >= 128;
-    const int th = tid & 127, sub = th % TPR, j = sub >> 2, cc = sub & 3, r0 = th / TPR;
-    const Kv4Rows &rows = is_v ? a.v : a.k;
-    uint8_t *scales = chunk + (is_v ? kv4_vscale_off(NG) : kv4_kscale_off(NG));
-    const int64_t base = b * rows.slot + h * rows.head + sub * 8 + (int64_t)(p0 - start) * rows.token;
-    float x[PASSES][8];
+  const AppendRange rg(a, b);
+  const int64_t bh = (int64_t)b * a.n_kv + h;
+  const bool is_v = tid >= 128;
+  const int th = tid & 127, sub = th % TPR, j = sub >> 2, cc = sub & 3, r0 = th / TPR;
+  const Kv4Rows &rows = is_v ? a.v : a.k;
+  const int ch0 = rg.start / kKv4Chunk + (int)blockIdx.x * kAppendChunks;
+  const int ch1 = min(ch0 + kAppendChunks, (rg.end + kKv4Chunk - 1) / kKv4Chunk);
+  const char *src = static_cast<const char *>(rows.p) + (b * rows.slot + h * rows.head + sub * 8) * sizeof(T);
+  Raw8<T> raw[PASSES];
+  auto fetch = [&](int ch) {
 #pragma unroll
     for (int i = 0; i < PASSES; ++i) {
-      const int p = r0 + i * RPP;
-      if (p0 + p >= lo && p0 + p < hi) {
-        load8<T>(rows.p, base + p * rows.token, x[i]);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[i][e] = 0.f;
-      }
+      const int pos = ch * kKv4Chunk + r0 + i * RPP;
+      if (pos >= rg.start && pos < rg.end) raw[i].load(src, (int64_t)(pos - rg.start) * rows.token);
+      else raw[i].clear();
     }
+  };
+  if (ch0 < ch1) fetch(ch0);
+  for (int ch = ch0; ch < ch1; ++ch) {
+    const int p0 = ch * kKv4Chunk, lo = max(rg.start, p0), hi = min(rg.end, p0 + kKv4Chunk);
+    uint8_t *chunk = a.l.codes + (bh * (a.l.cap / kKv4Chunk) + ch) * kv4_chunk_bytes(NG);
+    uint8_t *scales = chunk + (is_v ? kv4_vscale_off(NG) : kv4_kscale_off(NG));
+    uint32_t *vc = vcode[ch & 1];
+    uint32_t w[PASSES];
+    __half d[PASSES];
+#pragma unroll
+    for (int i = 0; i < PASSES; ++i) {
+      float x[8];
+      raw[i].floats(x);
+      w[i] = q4_word(x, &d[i]);
+    }
+    if (ch + 1 < ch1) fetch(ch + 1);
 #pragma unroll
     for (int i = 0; i < PASSES; ++i) {
       const int p = r0 + i * RPP;
       const bool live = p0 + p >= lo && p0 + p < hi;
-      __half d;
-      const uint32_t w = q4_word(x[i], &d);
-      if (is_v) vcode[p][sub] = w;
-      else if (live) *reinterpret_cast<uint32_t *>(chunk + kv4_kword(NG, p, cc, j)) = w;
+      if (is_v) vc[p * VP + sub] = w[i];
+      else if (live) *reinterpret_cast<uint32_t *>(chunk + kv4_kword(NG, p, cc, j)) = w[i];
       if (live && cc == 0)
-        *reinterpret_cast<__half *>(scales + (is_v ? kv4_vscale(NG, p, j) : kv4_kscale(NG, p, j))) = d;
+        *reinterpret_cast<__half *>(scales + (is_v ? kv4_vscale(NG, p, j) : kv4_kscale(NG, p, j))) = d[i];
     }
     if (tid < kKv4Chunk && p0 + tid >= lo && p0 + tid < hi) {
-      a.l.ids[bh * a.l.cap + p0 + tid] = seen0 + (p0 + tid - start);
+      a.l.ids[bh * a.l.cap + p0 + tid] = rg.seen0 + (p0 + tid - rg.start);
       a.l.weights[bh * a.l.cap + p0 + tid] = 0.f;
     }
     __syncthreads();
-    if (tid < 32 * NG) {                          // unit (J, r, c): 4 dims of 8 positions
-      const int J = tid >> 5, r = (tid >> 2) & 7, c = tid & 3;
-      uint32_t w[4] = {}, fresh = 0;
+    if (tid < 16 * NG) {                          // (J, c, i): 8 dims 32 J + 8 i .. of 8 positions
+      const int i = tid & 3, c = (tid >> 2) & 3, J = tid >> 4;
+      uint32_t n[8], fresh = 0;
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        const int p = 8 * (k >> 1) + 2 * c + (k & 1), sh = 4 * ((k >> 1) + 4 * (k & 1));
-        const uint4 q = *reinterpret_cast<const uint4 *>(&vcode[p][J * 4]);
-        if (p0 + p >= lo && p0 + p < hi) fresh |= 15u << sh;
-        w[0] |= ((q.x >> (4 * r)) & 15u) << sh;
-        w[1] |= ((q.y >> (4 * r)) & 15u) << sh;
-        w[2] |= ((q.z >> (4 * r)) & 15u) << sh;
-        w[3] |= ((q.w >> (4 * r)) & 15u) << sh;
+        const int p = vpos(c, k);
+        n[k] = vc[p * VP + J * 4 + i];
+        if (p0 + p >= lo && p0 + p < hi) fresh |= 15u << (4 * k);
       }
-      uint4 *dst = reinterpret_cast<uint4 *>(chunk + kv4_v_off(NG) + kv4_vunit(J, r, c));
-      if (fresh == 0xffffffffu) {
-        *dst = make_uint4(w[0], w[1], w[2], w[3]);
-      } else if (fresh) {
-        const uint4 old = *dst;
-        *dst = make_uint4((old.x & ~fresh) | (w[0] & fresh), (old.y & ~fresh) | (w[1] & fresh),
-                          (old.z & ~fresh) | (w[2] & fresh), (old.w & ~fresh) | (w[3] & fresh));
+      transpose_nibbles(n);
+      uint8_t *to = chunk + kv4_v_off(NG) + kv4_vunit(J, 0, c) + 4 * i;
+#pragma unroll
+      for (int r = 0; r < 8; ++r) {               // dim r of the eight
+        uint32_t *p = reinterpret_cast<uint32_t *>(to + kv4_vunit(0, r, 0));
+        if (fresh == 0xffffffffu) *p = n[r];
+        else if (fresh) *p = (*p & ~fresh) | (n[r] & fresh);
       }
     }
   }
-  // the slot's last CTA moves its length: all have read the old one
   __syncthreads();
-  if (tid == 0) {
+  if (tid == 0) {                                 // all the CTA's threads have read the old length
     __threadfence();
     const unsigned ctas = gridDim.x * gridDim.y;
-    if (atomicInc(a.arrive + b, ctas - 1) == ctas - 1) {
-      if (bad) set_error(a.err, bad);
-      if (bad != kErrRange) {
-        a.l.len[b] = end;
-        a.l.seen[b] = seen0 + n;
-      }
-    }
+    if (atomicInc(a.arrive + b, ctas - 1) == ctas - 1) rg.commit(a, b);
   }
 }
 
@@ -181,75 +326,150 @@ __device__ __forceinline__ void store8(void *p, int64_t at, const float (&x)[8])
   }
 }
 
-constexpr int kReadThreads = 256;
+// d (u - 8) of a word's 8 codes: a code under the exponent of 2^23 is 2^23 + u
+__device__ __forceinline__ void q4_values(uint32_t w, float d, float (&x)[8]) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    x[e] = d * (__uint_as_float(((w >> (4 * e)) & 15u) | 0x4b000000u) - 8388616.f);
+}
 
-// One CTA per (chunk, KV head, slot): the chunk through shared memory, then 8
-// dims of one position per thread and store (one word of K codes; one nibble
-// of each of 8 V words).  Bound by the values' bytes.
+__device__ __forceinline__ float half_at(const uint8_t *p) {
+  return __half2float(*reinterpret_cast<const __half *>(p));
+}
+
+// Few tokens: a thread per 8 dims of a row, straight from the cache.
+template <int NG, typename T>
+__global__ void __launch_bounds__(256) k_kv4_read_step(const __grid_constant__ Kv4ReadArgs a) {
+  constexpr int TPR = 4 * NG, CH = kv4_chunk_bytes(NG);
+  pdl_wait();
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= (int64_t)a.n_slot * a.T * a.n_kv * 2 * TPR) return;
+  const int sub = (int)(i % TPR), j = sub >> 2, cc = sub & 3;
+  const bool is_v = (i / TPR) & 1;
+  int64_t k = i / (2 * TPR);
+  const int h = (int)(k % a.n_kv);
+  k /= a.n_kv;
+  const int t = (int)(k % a.T), b = (int)(k / a.T);
+  const int first = a.first ? a.first[b] : 0;
+  const int64_t pos = first < 0 ? -1 : (int64_t)first + t;
+  float x[8] = {};
+  if (pos >= 0 && pos < kv4_len(a.l, b)) {
+    const int p = (int)(pos % kKv4Chunk);
+    const uint8_t *chunk = a.l.codes + (((int64_t)b * a.n_kv + h) * (a.l.cap / kKv4Chunk) + pos / kKv4Chunk) * CH;
+    if (!is_v) {
+      q4_values(*reinterpret_cast<const uint32_t *>(chunk + kv4_kword(NG, p, cc, j)),
+                half_at(chunk + kv4_kscale_off(NG) + kv4_kscale(NG, p, j)), x);
+    } else {
+      const float d = half_at(chunk + kv4_vscale_off(NG) + kv4_vscale(NG, p, j));
+      const int sh = kv4_vshift(p);
+      uint32_t w = 0;
+#pragma unroll
+      for (int r = 0; r < 8; ++r)
+        w |= ((*reinterpret_cast<const uint32_t *>(chunk + kv4_v_off(NG) + kv4_vunit(j, r, (p >> 1) & 3) + 4 * cc) >>
+               sh) & 15u) << (4 * r);
+      q4_values(w, d, x);
+    }
+  }
+  const Kv4Rows &o = is_v ? a.v : a.k;
+  store8<T>(o.p, b * o.slot + t * o.token + h * o.head + sub * 8, x);
+}
+
+// Many tokens: CTAs of kReadChunks chunks of one (slot, KV head), which one
+// bulk copy brings into shared memory; then 8 dims of a K position per thread,
+// and 8 x 8 nibbles of V (8 positions, 8 dims) per thread.  Bound by the
+// values' bytes.
+constexpr int kReadThreads = 256, kReadChunks = 4;
+
 template <int NG, typename T>
 __global__ void __launch_bounds__(kReadThreads) k_kv4_read(const __grid_constant__ Kv4ReadArgs a) {
-  constexpr int CH = kv4_chunk_bytes(NG);
-  __shared__ __align__(16) uint8_t sm[CH];
+  constexpr int CH = kv4_chunk_bytes(NG), TPR = 4 * NG;
+  __shared__ __align__(128) uint8_t sm[kReadChunks * CH];
+  __shared__ __align__(8) uint64_t bar;
   const int tid = threadIdx.x, b = blockIdx.z, h = blockIdx.y;
+  if (tid == 0) {
+    mbar_init(&bar, 1);
+    fence_barrier_init();
+  }
   pdl_wait();
   const int len = kv4_len(a.l, b);
   int first = a.first ? a.first[b] : 0;
   first = first < 0 || first > a.l.cap ? a.l.cap : first;   // outside the cache: nothing but zeros
-  const int ch = first / kKv4Chunk + (int)blockIdx.x, p0 = ch * kKv4Chunk;
-  const int64_t last = (int64_t)first + a.T;
-  const int lo = max(first, p0), hi = (int)min(last, (int64_t)p0 + kKv4Chunk);
+  const int ch0 = first / kKv4Chunk + (int)blockIdx.x * kReadChunks;
+  const int64_t p0 = (int64_t)ch0 * kKv4Chunk, lo = max((int64_t)first, p0);
+  const int64_t hi = min((int64_t)first + a.T, p0 + kReadChunks * kKv4Chunk);
   if (lo >= hi) return;
-  if (p0 < len) {
-    const uint4 *src = reinterpret_cast<const uint4 *>(
-        a.l.codes + (((int64_t)b * a.n_kv + h) * (a.l.cap / kKv4Chunk) + ch) * CH);
-    for (int i = tid; i < CH / 16; i += kReadThreads) reinterpret_cast<uint4 *>(sm)[i] = src[i];
-  }
+  // chunks that hold entries to be read
+  const int held = (int)max((int64_t)0, (min(hi, (int64_t)len) - p0 + kKv4Chunk - 1) / kKv4Chunk);
   __syncthreads();
-  for (int i = tid; i < 2 * kKv4Chunk * 4 * NG; i += kReadThreads) {
-    const bool is_v = i >= kKv4Chunk * 4 * NG;
-    const int k = is_v ? i - kKv4Chunk * 4 * NG : i;
-    const int p = k / (4 * NG), w8 = k % (4 * NG), j = w8 >> 2, sub = w8 & 3, pos = p0 + p;
-    if (pos < lo || pos >= hi) continue;
-    float x[8] = {};
-    if (pos < len) {
-      if (!is_v) {
-        const float d = __half2float(*reinterpret_cast<const __half *>(sm + kv4_kscale_off(NG) + kv4_kscale(NG, p, j)));
-        const uint32_t w = *reinterpret_cast<const uint32_t *>(sm + kv4_kword(NG, p, sub, j));
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = d * (float)((int)((w >> (4 * e)) & 15u) - 8);
-      } else {
-        const float d = __half2float(*reinterpret_cast<const __half *>(sm + kv4_vscale_off(NG) + kv4_vscale(NG, p, j)));
-        const int c = (p >> 1) & 3, sh = kv4_vshift(p);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const uint32_t w = *reinterpret_cast<const uint32_t *>(sm + kv4_v_off(NG) + kv4_vunit(j, e, c) + 4 * sub);
-          x[e] = d * (float)((int)((w >> sh) & 15u) - 8);
-        }
-      }
+  bool ok = true;
+  if (held > 0) {
+    if (tid == 0) {
+      mbar_arrive_expect_tx(&bar, held * CH);
+      bulk_g2s(sm, a.l.codes + (((int64_t)b * a.n_kv + h) * (a.l.cap / kKv4Chunk) + ch0) * CH, held * CH, &bar);
     }
-    const Kv4Rows &o = is_v ? a.v : a.k;
-    store8<T>(o.p, b * o.slot + (int64_t)(pos - first) * o.token + h * o.head + w8 * 8, x);
+    ok = mbar_wait(&bar, 0);
+    if (!ok && tid == 0) {
+      set_error(a.err, kErrTimeout);
+      mbar_wait(&bar, 0);          // another bounded chance to land before the shared memory goes away
+    }
+  }
+  const int64_t slot_k = b * a.k.slot + h * a.k.head, slot_v = b * a.v.slot + h * a.v.head;
+  for (int i = tid; i < kReadChunks * kKv4Chunk * TPR; i += kReadThreads) {
+    const int q = i / TPR, sub = i % TPR, j = sub >> 2, cc = sub & 3, p = q % kKv4Chunk;
+    const int64_t pos = p0 + q;
+    if (pos < lo || pos >= hi) continue;
+    const uint8_t *chunk = sm + (q / kKv4Chunk) * CH;
+    float x[8] = {};
+    if (pos < len)
+      q4_values(*reinterpret_cast<const uint32_t *>(chunk + kv4_kword(NG, p, cc, j)),
+                half_at(chunk + kv4_kscale_off(NG) + kv4_kscale(NG, p, j)), x);
+    store8<T>(a.k.p, slot_k + (pos - first) * a.k.token + sub * 8, x);
+  }
+  for (int i = tid; i < kReadChunks * 4 * TPR; i += kReadThreads) {
+    const int sub = i % TPR, j = sub >> 2, cc = sub & 3, c = (i / TPR) & 3, q = i / (4 * TPR);
+    const uint8_t *chunk = sm + q * CH;
+    uint32_t w[8];
+#pragma unroll
+    for (int r = 0; r < 8; ++r)
+      w[r] = *reinterpret_cast<const uint32_t *>(chunk + kv4_v_off(NG) + kv4_vunit(j, r, c) + 4 * cc);
+    transpose_nibbles(w);
+#pragma unroll
+    for (int n = 0; n < 8; ++n) {
+      const int p = vpos(c, n);
+      const int64_t pos = p0 + q * kKv4Chunk + p;
+      if (pos < lo || pos >= hi) continue;
+      float x[8] = {};
+      if (pos < len) q4_values(w[n], half_at(chunk + kv4_vscale_off(NG) + kv4_vscale(NG, p, j)), x);
+      store8<T>(a.v.p, slot_v + (pos - first) * a.v.token + sub * 8, x);
+    }
   }
 }
 
 // ---------------------------------------------------------------- eviction
 // Selection, one thread-block cluster per (slot, KV head), the entries' keys
-// in registers: entries that must stay have the largest key, the others an
-// order-preserving image of their weight.  A radix descent (four 8-bit levels)
-// finds the key of rank `budget`; of the entries with exactly that key the
-// first ones stay.  Then the kept entries behind the budget ("movers") fill
-// the dropped ones' places below it ("holes"), both in index order:
-// src_of[hole r] = mover r.
+// (order-preserving images of their weights) in registers.  Entries that must
+// stay are set apart; a radix descent, eight bits at a time from the highest
+// bit in which the others differ, finds the key of the rank that is left, and
+// ends as soon as a bin is kept whole; of the entries with exactly that key the
+// first ones stay.  Then the kept entries behind the budget ("movers") fill the
+// dropped ones' places below it ("holes"), both in index order:
+// src_of[hole r] = mover r.  Bound by the latency of its barriers.
 template <int THREADS, int K>
 __global__ void __launch_bounds__(THREADS) k_kv4_select(const __grid_constant__ Kv4EvictArgs a) {
   constexpr int WARPS = THREADS / 32, COPIES = 8;
+  static_assert(THREADS >= 256, "a bin per thread");
   __shared__ uint32_t hist[COPIES][256];
-  __shared__ uint32_t merged[2][256];
-  __shared__ uint32_t warp_sum[WARPS], totals[4];
-  __shared__ uint32_t s_bin, s_need;
+  __shared__ uint32_t merged[2][256], sums[256];
+  __shared__ uint32_t warp_sum[WARPS], warp_min[WARPS], warp_max_[WARPS], totals[4];
+  __shared__ uint32_t range[3];                    // the CTA's smallest and largest loose key, entries that stay
+  __shared__ uint32_t s_bin, s_need, s_equal;
   cg::cluster_group cluster = cg::this_cluster();
   const int CL = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, h = blockIdx.y, b = blockIdx.z;
+  auto sync_all = [&]() {
+    if (CL > 1) cluster.sync();
+    else __syncthreads();
+  };
   pdl_wait();
   const int n = kv4_len(a.src, b), seen = a.src.seen[b], m = a.budget;
   const int64_t bh = (int64_t)b * a.n_kv + h;
@@ -259,7 +479,7 @@ __global__ void __launch_bounds__(THREADS) k_kv4_select(const __grid_constant__ 
   // (uniform over the cluster)
   if (n > m) {
     const int base = rank * THREADS * K + warp * 32 * K + lane;   // this lane's entries: base + 32 k
-    uint32_t key[K];
+    uint32_t key[K], loose = 0, lo = 0xffffffffu, hi = 0, stay = 0;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       const int i = base + 32 * k;
@@ -267,41 +487,88 @@ __global__ void __launch_bounds__(THREADS) k_kv4_select(const __grid_constant__ 
       if (i < n) {
         const int id = ids[i];
         const uint32_t u = __float_as_uint(wt[i]);
-        const bool stays = id < a.n_sink || (int64_t)id >= (int64_t)seen - a.n_recent;
-        key[k] = stays ? 0xffffffffu : ((u & 0x80000000u) ? ~u : (u | 0x80000000u));
+        key[k] = (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+        if (id < a.n_sink || (int64_t)id >= (int64_t)seen - a.n_recent) {
+          ++stay;
+        } else {
+          loose |= 1u << k;
+          lo = min(lo, key[k]);
+          hi = max(hi, key[k]);
+        }
       }
     }
-    uint32_t prefix = 0, need = (uint32_t)m;   // the need-th largest among keys with this prefix
-    uint32_t equal = 0;
+    for (int i = tid; i < COPIES * 256; i += THREADS) (&hist[0][0])[i] = 0;
+    lo = __reduce_min_sync(0xffffffffu, lo);
+    hi = __reduce_max_sync(0xffffffffu, hi);
+    stay = __reduce_add_sync(0xffffffffu, stay);
+    if (lane == 0) {
+      warp_min[warp] = lo;
+      warp_max_[warp] = hi;
+      warp_sum[warp] = stay;
+    }
+    __syncthreads();
+    if (warp == 0) {
+      lo = __reduce_min_sync(0xffffffffu, lane < WARPS ? warp_min[lane] : 0xffffffffu);
+      hi = __reduce_max_sync(0xffffffffu, lane < WARPS ? warp_max_[lane] : 0u);
+      stay = __reduce_add_sync(0xffffffffu, lane < WARPS ? warp_sum[lane] : 0u);
+      if (lane == 0) {
+        range[0] = lo;
+        range[1] = hi;
+        range[2] = stay;
+      }
+    }
+    sync_all();
+    lo = 0xffffffffu;
+    hi = stay = 0;
+    for (int c = 0; c < CL; ++c) {
+      const uint32_t *r = CL > 1 ? cluster.map_shared_rank(range, c) : range;
+      lo = min(lo, r[0]);
+      hi = max(hi, r[1]);
+      stay += r[2];
+    }
+    // loose keys agree above bit `shift - 1`; the need-th largest of them is sought
+    const int top = lo < hi ? 31 - __clz(lo ^ hi) : 7;
+    int shift = top + 1;
+    uint32_t prefix = (uint32_t)((uint64_t)hi >> shift), equal = 0xffffffffu;
+    uint32_t need = (uint32_t)m > stay ? (uint32_t)m - stay : 0u;
 #pragma unroll 1
-    for (int level = 0; level < 4; ++level) {
-      const int sh = 24 - 8 * level;
-      for (int i = tid; i < COPIES * 256; i += THREADS) (&hist[0][0])[i] = 0;
-      __syncthreads();
+    for (int level = 0; need > 0 && shift > 0 && need != equal; ++level) {
+      const int width = min(8, shift);
+      shift -= width;
+      const uint32_t digit = (1u << width) - 1u;
 #pragma unroll
       for (int k = 0; k < K; ++k) {
-        const bool in = base + 32 * k < n && (level == 0 || (key[k] >> (sh + 8)) == prefix);
-        if (in) atomicAdd(&hist[warp % COPIES][(key[k] >> sh) & 255u], 1u);
+        const bool in = ((loose >> k) & 1u) && (uint32_t)((uint64_t)key[k] >> (shift + width)) == prefix;
+        if (in) atomicAdd(&hist[warp % COPIES][(key[k] >> shift) & digit], 1u);
       }
       __syncthreads();
       uint32_t *mine = merged[level & 1];
-      for (int i = tid; i < 256; i += THREADS) {
+      if (tid < 256) {
         uint32_t s = 0;
 #pragma unroll
-        for (int q = 0; q < COPIES; ++q) s += hist[q][i];
-        mine[i] = s;
+        for (int q = 0; q < COPIES; ++q) {
+          s += hist[q][tid];
+          hist[q][tid] = 0;
+        }
+        mine[tid] = s;
+        if (CL == 1) sums[tid] = s;
       }
-      if (CL > 1) cluster.sync();
-      else __syncthreads();
-      // warp 0: totals over the cluster, then the bin in which the running
-      // count from the top reaches `need` (lane l holds bins 255 - 8 l - 7 ..)
+      if (CL > 1) {
+        cluster.sync();
+        if (tid < 256) {
+          uint32_t s = 0;
+          for (int c = 0; c < CL; ++c) s += *cluster.map_shared_rank(mine + tid, c);
+          sums[tid] = s;
+        }
+      }
+      __syncthreads();
+      // warp 0: the bin in which the running count from the top reaches `need`
+      // (lane l holds bins 255 - 8 l - 7 ..)
       if (warp == 0) {
         uint32_t v[8], sum = 0;
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
-          v[q] = 0;
-          for (int c = 0; c < CL; ++c)
-            v[q] += CL > 1 ? *cluster.map_shared_rank(mine + 255 - 8 * lane - q, c) : mine[255 - 8 * lane - q];
+          v[q] = sums[255 - 8 * lane - q];
           sum += v[q];
         }
         uint32_t inc = sum;
@@ -317,19 +584,18 @@ __global__ void __launch_bounds__(THREADS) k_kv4_select(const __grid_constant__ 
             if (above < need && need <= above + v[q]) {
               s_bin = 255 - 8 * lane - q;
               s_need = need - above;
-              totals[0] = v[q];
+              s_equal = v[q];
             }
             above += v[q];
           }
         }
       }
       __syncthreads();
-      prefix = (prefix << 8) | s_bin;
+      prefix = (prefix << width) | s_bin;
       need = s_need;
-      equal = totals[0];
-      __syncthreads();
+      equal = s_equal;
     }
-    // the first `need` of the `equal` entries with key == prefix stay
+    // the first `need` of the `equal` entries with key == prefix stay (shift is 0 unless all do)
     auto ranks = [&](uint32_t mine, int slot) -> uint32_t {
       // exclusive base of this warp's count over the cluster, in index order
       if (lane == 0) warp_sum[warp] = mine;
@@ -349,23 +615,23 @@ __global__ void __launch_bounds__(THREADS) k_kv4_select(const __grid_constant__ 
       return before;
     };
     uint32_t kept = 0;                             // bit k: entry base + 32 k stays
-    if (need == equal) {
+    if (need == 0 || need == equal) {
 #pragma unroll
       for (int k = 0; k < K; ++k)
-        if (base + 32 * k < n && key[k] >= prefix) kept |= 1u << k;
+        if (base + 32 * k < n && (!((loose >> k) & 1u) || (need > 0 && (key[k] >> shift) >= prefix))) kept |= 1u << k;
     } else {
       uint32_t mine = 0;
 #pragma unroll
       for (int k = 0; k < K; ++k)
-        mine += __popc(__ballot_sync(0xffffffffu, base + 32 * k < n && key[k] == prefix));
+        mine += __popc(__ballot_sync(0xffffffffu, ((loose >> k) & 1u) && key[k] == prefix));
       uint32_t at = ranks(mine, 1);
 #pragma unroll
       for (int k = 0; k < K; ++k) {
-        const bool eq = base + 32 * k < n && key[k] == prefix;
+        const bool is_loose = (loose >> k) & 1u, eq = is_loose && key[k] == prefix;
         const uint32_t vote = __ballot_sync(0xffffffffu, eq);
         const bool first = eq && at + __popc(vote & ((1u << lane) - 1u)) < need;
         at += __popc(vote);
-        if (base + 32 * k < n && (key[k] > prefix || first)) kept |= 1u << k;
+        if (base + 32 * k < n && (!is_loose || key[k] > prefix || first)) kept |= 1u << k;
       }
     }
     uint32_t holes = 0, moves = 0;
@@ -386,8 +652,7 @@ __global__ void __launch_bounds__(THREADS) k_kv4_select(const __grid_constant__ 
       move_at += __popc(vote);
     }
     __threadfence();
-    if (CL > 1) cluster.sync();
-    else __syncthreads();
+    sync_all();
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       const int i = base + 32 * k;
@@ -410,73 +675,107 @@ __global__ void __launch_bounds__(THREADS) k_kv4_select(const __grid_constant__ 
   }
 }
 
-constexpr int kMoveThreads = 128;
+constexpr int kMoveThreads = 128, kMoveChunks = 4;
 
-// The moves, one CTA per (destination chunk, KV head, slot).  Sources of moves
-// lie at or behind the budget and destinations below it, so the CTAs do not
-// depend on one another; in the chunk that holds the budget's border a V word
-// may be read by others while its owner replaces it, with the nibbles that they
-// read unchanged (32-bit accesses).
+// The moves, one CTA per (kMoveChunks destination chunks, KV head, slot).
+// Sources of moves lie at or behind the budget and destinations below it, so
+// the CTAs do not depend on one another; in the chunk that holds the budget's
+// border a V word may be read by others while its owner replaces it, with the
+// nibbles that they read unchanged (32-bit accesses).
 template <int NG>
 __global__ void __launch_bounds__(kMoveThreads) k_kv4_move(const __grid_constant__ Kv4EvictArgs a) {
-  constexpr int CH = kv4_chunk_bytes(NG);
-  __shared__ int src[kKv4Chunk];
-  const int tid = threadIdx.x, h = blockIdx.y, b = blockIdx.z, p0 = blockIdx.x * kKv4Chunk;
+  constexpr int CH = kv4_chunk_bytes(NG), POS = kMoveChunks * kKv4Chunk;
+  static_assert(POS == kMoveThreads, "a position per thread");
+  __shared__ int src[POS];
+  __shared__ int moved_chunk[kMoveChunks];
+  const int tid = threadIdx.x, h = blockIdx.y, b = blockIdx.z, p0 = blockIdx.x * POS;
   pdl_wait();
   const int n = a.n_old[b], out = min(n, a.budget);
   if (p0 >= out || (a.in_place && n <= a.budget)) return;
   const int64_t bh = (int64_t)b * a.n_kv + h;
   const uint8_t *from = a.src.codes + bh * (a.src.cap / kKv4Chunk) * CH;
-  uint8_t *to = a.dst.codes + (bh * (a.dst.cap / kKv4Chunk) + blockIdx.x) * CH;
-  int moved = 0;
-  if (tid < kKv4Chunk) {
+  uint8_t *to = a.dst.codes + (bh * (a.dst.cap / kKv4Chunk) + blockIdx.x * kMoveChunks) * CH;
+  {
     const int p = p0 + tid;
     int s = -1;
     if (p < out) {
       s = n > a.budget ? a.src_of[bh * a.src.cap + p] : p;
-      moved = s != p;
-      if (!a.in_place || moved) {
+      if (!a.in_place || s != p) {
         a.dst.ids[bh * a.dst.cap + p] = a.src.ids[bh * a.src.cap + s];
         a.dst.weights[bh * a.dst.cap + p] = a.src.weights[bh * a.src.cap + s];
       }
     }
     src[tid] = s;
+    const bool any = __any_sync(0xffffffffu, s >= 0 && s != p);
+    if ((tid & 31) == 0) moved_chunk[tid >> 5] = any;
   }
-  if (!__syncthreads_or(moved) && a.in_place) return;
-  // K codes and both kinds of scales, row by row
-  for (int i = tid; i < kKv4Chunk * 4 * NG; i += kMoveThreads) {
-    const int p = i / (4 * NG), w = i % (4 * NG), s = src[p];
-    if (s < 0 || (a.in_place && s == p0 + p)) continue;
-    const uint8_t *chunk = from + (int64_t)(s / kKv4Chunk) * CH;
-    const int q = s % kKv4Chunk;
-    *reinterpret_cast<uint32_t *>(to + p * 16 * NG + w * 4) =
-        *reinterpret_cast<const uint32_t *>(chunk + q * 16 * NG + w * 4);
-    if (w < 2 * NG) {
-      const int j = w % NG;
-      const int into = w < NG ? kv4_kscale_off(NG) + kv4_kscale(NG, p, j) : kv4_vscale_off(NG) + kv4_vscale(NG, p, j);
-      const int out_of = w < NG ? kv4_kscale_off(NG) + kv4_kscale(NG, q, j) : kv4_vscale_off(NG) + kv4_vscale(NG, q, j);
-      *reinterpret_cast<uint16_t *>(to + into) = *reinterpret_cast<const uint16_t *>(chunk + out_of);
-    }
-  }
-  // V codes: unit (J, r, c) holds 4 dims of 8 positions
-  for (int u = tid; u < 32 * NG; u += kMoveThreads) {
-    const int J = u >> 5, r = (u >> 2) & 7, c = u & 3;
-    const uint4 old = *reinterpret_cast<const uint4 *>(from + (int64_t)blockIdx.x * CH + kv4_v_off(NG) +
-                                                       kv4_vunit(J, r, c));
-    uint32_t w[4] = {old.x, old.y, old.z, old.w};
+  __syncthreads();
+  // K rows, NG 16-byte vectors each; all loads before the stores
+  {
+    uint4 v[NG];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const int p = 8 * (k >> 1) + 2 * c + (k & 1), s = src[p];
-      if (s < 0 || s == p0 + p) continue;
-      const int q = s % kKv4Chunk, from_sh = kv4_vshift(q), sh = kv4_vshift(p);
-      const uint4 v = *reinterpret_cast<const uint4 *>(from + (int64_t)(s / kKv4Chunk) * CH + kv4_v_off(NG) +
-                                                       kv4_vunit(J, r, (q >> 1) & 3));
-      w[0] = (w[0] & ~(15u << sh)) | (((v.x >> from_sh) & 15u) << sh);
-      w[1] = (w[1] & ~(15u << sh)) | (((v.y >> from_sh) & 15u) << sh);
-      w[2] = (w[2] & ~(15u << sh)) | (((v.z >> from_sh) & 15u) << sh);
-      w[3] = (w[3] & ~(15u << sh)) | (((v.w >> from_sh) & 15u) << sh);
+    for (int i = 0; i < NG; ++i) {
+      const int p = (i * kMoveThreads + tid) / NG, s = src[p];
+      if (s >= 0 && !(a.in_place && s == p0 + p))
+        v[i] = reinterpret_cast<const uint4 *>(from + (int64_t)(s / kKv4Chunk) * CH + (s % kKv4Chunk) * 16 * NG)[tid % NG];
     }
-    *reinterpret_cast<uint4 *>(to + kv4_v_off(NG) + kv4_vunit(J, r, c)) = make_uint4(w[0], w[1], w[2], w[3]);
+#pragma unroll
+    for (int i = 0; i < NG; ++i) {
+      const int p = (i * kMoveThreads + tid) / NG, s = src[p];
+      if (s >= 0 && !(a.in_place && s == p0 + p))
+        reinterpret_cast<uint4 *>(to + (p / kKv4Chunk) * CH + (p % kKv4Chunk) * 16 * NG)[tid % NG] = v[i];
+    }
+  }
+  // both kinds of scales, a position per thread
+  if (src[tid] >= 0 && !(a.in_place && src[tid] == p0 + tid)) {
+    const int s = src[tid], p = tid % kKv4Chunk, q = s % kKv4Chunk;
+    const uint8_t *f = from + (int64_t)(s / kKv4Chunk) * CH;
+    uint8_t *t = to + (tid / kKv4Chunk) * CH;
+#pragma unroll
+    for (int j = 0; j < NG; ++j) {
+      *reinterpret_cast<uint16_t *>(t + kv4_kscale_off(NG) + kv4_kscale(NG, p, j)) =
+          *reinterpret_cast<const uint16_t *>(f + kv4_kscale_off(NG) + kv4_kscale(NG, q, j));
+      *reinterpret_cast<uint16_t *>(t + kv4_vscale_off(NG) + kv4_vscale(NG, p, j)) =
+          *reinterpret_cast<const uint16_t *>(f + kv4_vscale_off(NG) + kv4_vscale(NG, q, j));
+    }
+  }
+  // V codes: unit (J, r, c) holds 4 dims of 8 positions; thread: NG units in all
+  constexpr int UNITS = 32 * NG, PER = kMoveChunks * UNITS / kMoveThreads;
+  auto live = [&](int k) { return p0 + k * kKv4Chunk < out && (!a.in_place || moved_chunk[k]); };
+  uint4 w[PER];
+#pragma unroll
+  for (int x = 0; x < PER; ++x) {
+    const int i = x * kMoveThreads + tid, k = i / UNITS, u = i % UNITS;
+    if (live(k))
+      w[x] = *reinterpret_cast<const uint4 *>(from + (int64_t)(p0 / kKv4Chunk + k) * CH + kv4_v_off(NG) + u * 16);
+  }
+#pragma unroll
+  for (int x = 0; x < PER; ++x) {
+    const int i = x * kMoveThreads + tid, k = i / UNITS, u = i % UNITS, c = u & 3;
+    if (!live(k)) continue;
+    if (moved_chunk[k]) {
+      uint4 v[8];
+      int s[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int p = vpos(c, e);
+        s[e] = src[k * kKv4Chunk + p];
+        if (s[e] == p0 + k * kKv4Chunk + p) s[e] = -1;
+        if (s[e] >= 0)
+          v[e] = *reinterpret_cast<const uint4 *>(from + (int64_t)(s[e] / kKv4Chunk) * CH + kv4_v_off(NG) +
+                                                  ((u & ~3) + ((s[e] >> 1) & 3)) * 16);
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        if (s[e] < 0) continue;
+        const int from_sh = kv4_vshift(s[e] % kKv4Chunk), sh = 4 * e;
+        w[x].x = (w[x].x & ~(15u << sh)) | (((v[e].x >> from_sh) & 15u) << sh);
+        w[x].y = (w[x].y & ~(15u << sh)) | (((v[e].y >> from_sh) & 15u) << sh);
+        w[x].z = (w[x].z & ~(15u << sh)) | (((v[e].z >> from_sh) & 15u) << sh);
+        w[x].w = (w[x].w & ~(15u << sh)) | (((v[e].w >> from_sh) & 15u) << sh);
+      }
+    }
+    *reinterpret_cast<uint4 *>(to + k * CH + kv4_v_off(NG) + u * 16) = w[x];
   }
 }
 
@@ -491,25 +790,43 @@ __global__ void k_kv4_reset(int32_t *len, int32_t *seen, int64_t stride, int n_l
   }
 }
 
+// chunks that T rows from any position touch at most, in groups
+int chunk_groups(int T, int group) { return ((T + kKv4Chunk - 2) / kKv4Chunk + group) / group; }
+
+template <int NG, typename T>
+cudaError_t run_append(const Kv4AppendArgs &a, cudaStream_t st) {
+  // measured on 64 slots x 8 heads at head_dim 128 (bf16), step against chunks: see kStepTokens
+  const size_t smem = (size_t)a.T * a.n_kv * 4 * NG * 4;
+  if (a.T <= kStepTokens && smem <= 48 * 1024)
+    return kv4_launch(k_kv4_append_step<NG, T>, dim3(a.n_slot), dim3(kStepThreads), smem, 1, st, a);
+  const dim3 grid(chunk_groups(a.T, kAppendChunks), a.n_kv, a.n_slot);
+  return kv4_launch(k_kv4_append<NG, T>, grid, dim3(kAppendThreads), 0, 1, st, a);
+}
+
+template <int NG, typename T>
+cudaError_t run_read(const Kv4ReadArgs &a, cudaStream_t st) {
+  if (a.T <= kStepTokens) {
+    const int64_t threads = (int64_t)a.n_slot * a.T * a.n_kv * 8 * NG;
+    return kv4_launch(k_kv4_read_step<NG, T>, dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, 1, st, a);
+  }
+  const dim3 grid(chunk_groups(a.T, kReadChunks), a.n_kv, a.n_slot);
+  return kv4_launch(k_kv4_read<NG, T>, grid, dim3(kReadThreads), 0, 1, st, a);
+}
+
 template <int NG>
 cudaError_t run_append(const Kv4AppendArgs &a, cudaStream_t st) {
-  // T rows from any position touch at most this many chunks
-  const dim3 grid((a.T + kKv4Chunk - 2) / kKv4Chunk + 1, a.n_kv, a.n_slot);
-  return a.k.dtype == PNB_F32 ? kv4_launch(k_kv4_append<NG, float>, grid, dim3(kAppendThreads), 0, 1, st, a)
-                              : kv4_launch(k_kv4_append<NG, __nv_bfloat16>, grid, dim3(kAppendThreads), 0, 1, st, a);
+  return a.k.dtype == PNB_F32 ? run_append<NG, float>(a, st) : run_append<NG, __nv_bfloat16>(a, st);
 }
 
 template <int NG>
 cudaError_t run_read(const Kv4ReadArgs &a, cudaStream_t st) {
-  const dim3 grid((a.T + kKv4Chunk - 2) / kKv4Chunk + 1, a.n_kv, a.n_slot);
-  return a.k.dtype == PNB_F32 ? kv4_launch(k_kv4_read<NG, float>, grid, dim3(kReadThreads), 0, 1, st, a)
-                              : kv4_launch(k_kv4_read<NG, __nv_bfloat16>, grid, dim3(kReadThreads), 0, 1, st, a);
+  return a.k.dtype == PNB_F32 ? run_read<NG, float>(a, st) : run_read<NG, __nv_bfloat16>(a, st);
 }
 
 template <int NG>
 cudaError_t run_move(const Kv4EvictArgs &a, cudaStream_t st) {
-  const int most = a.budget < a.src.cap ? a.budget : a.src.cap;
-  const dim3 grid((most + kKv4Chunk - 1) / kKv4Chunk, a.n_kv, a.n_slot);
+  const int most = a.budget < a.src.cap ? a.budget : a.src.cap, pos = kMoveChunks * kKv4Chunk;
+  const dim3 grid((most + pos - 1) / pos, a.n_kv, a.n_slot);
   return kv4_launch(k_kv4_move<NG>, grid, dim3(kMoveThreads), 0, 1, st, a);
 }
 
@@ -524,14 +841,19 @@ cudaError_t launch_kv4_read(int ng, const Kv4ReadArgs &a, cudaStream_t st) {
 }
 
 cudaError_t launch_kv4_evict(int ng, const Kv4EvictArgs &a, cudaStream_t st) {
-  // entries per CTA and CTAs per cluster that hold the whole capacity in registers
-  const int per = a.src.cap <= 8 * 256 * 16 ? 256 * 16 : a.src.cap <= 8 * 1024 * 16 ? 1024 * 16 : 1024 * 32;
+  // entries per CTA and CTAs per cluster that hold the whole capacity in
+  // registers; up to 4096 entries in one CTA, then in growing clusters of such
+  // CTAs (which keep many SMs busy when there are few rows), then larger CTAs
+  const int cap = a.src.cap;
+  const int per = cap <= 1024 ? 1024 : cap <= 2048 ? 2048 : cap <= 8 * 4096 ? 4096 : cap <= 8 * 16384 ? 16384 : 32768;
   int cl = 1;
-  while (cl * per < a.src.cap) cl *= 2;
+  while (cl * per < cap) cl *= 2;
   const dim3 grid(cl, a.n_kv, a.n_slot);
   cudaError_t e;
-  if (per == 256 * 16) e = kv4_launch(k_kv4_select<256, 16>, grid, dim3(256), 0, cl, st, a);
-  else if (per == 1024 * 16) e = kv4_launch(k_kv4_select<1024, 16>, grid, dim3(1024), 0, cl, st, a);
+  if (per == 1024) e = kv4_launch(k_kv4_select<256, 4>, grid, dim3(256), 0, cl, st, a);
+  else if (per == 2048) e = kv4_launch(k_kv4_select<256, 8>, grid, dim3(256), 0, cl, st, a);
+  else if (per == 4096) e = kv4_launch(k_kv4_select<256, 16>, grid, dim3(256), 0, cl, st, a);
+  else if (per == 16384) e = kv4_launch(k_kv4_select<1024, 16>, grid, dim3(1024), 0, cl, st, a);
   else e = kv4_launch(k_kv4_select<1024, 32>, grid, dim3(1024), 0, cl, st, a);
   if (e != cudaSuccess) return e;
   return ng == 4 ? run_move<4>(a, st) : ng == 2 ? run_move<2>(a, st) : run_move<1>(a, st);

@@ -91,6 +91,7 @@ struct Kv4ReadArgs {
   Kv4Rows k, v;
   const int32_t *first;           // [n_slot] or NULL
   int32_t n_slot, n_kv, T;
+  int32_t *err;
 };
 
 struct Kv4AttnArgs {

@@ -236,6 +236,7 @@ int pnb_kvq_read(pnb_kvq *c, int32_t layer, const int32_t *first_dev, int32_t T,
   if (rc != PNB_OK) return rc;
   a.l = layer_of(c, layer);
   a.first = first_dev;
+  a.err = c->err;
   a.n_slot = g.n_slot;
   a.n_kv = g.n_kv_head;
   a.T = T;
