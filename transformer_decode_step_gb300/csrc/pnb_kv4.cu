@@ -39,60 +39,6 @@ __device__ __forceinline__ void transpose_nibbles(uint32_t (&w)[8]) {
 __device__ __forceinline__ int vpos(int c, int n) { return 8 * (n & 3) + 2 * c + (n >> 2); }
 
 // ------------------------------------------------------------------ append
-// One Q4_0 block is held by 4 neighbouring lanes, 8 dims each:
-//   d = fp16(max|x| / 7), u = clamp(rint(x / d), -8, 7) + 8
-// with correctly rounded quotients.  rint(x / d) is taken as rint(x * (1 / d)),
-// which can be off by one next to a border, and put right from the residual
-// x - k d (one fma, exact there: x lies within a factor of two of k d, or k is
-// 0): a residual beyond d / 2, or of exactly d / 2 with k odd (ties go to the
-// even integer), moves k by one.  Few blocks have such a value, or a scale so
-// coarse (subnormal) that a quotient leaves [-7.5, 7.5].
-// NaN and infinities make the block's scale NaN; a scale past fp16's range
-// saturates.
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float d;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
-  return d;
-}
-
-__device__ __forceinline__ uint32_t q4_word(const float (&x)[8], __half *scale) {
-  float top = 0.f;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) top = max_nan(top, fabsf(x[i]));
-  top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, 1));
-  top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, 2));
-  const bool finite = top < INFINITY;    // false for NaN too
-  const __half d = __float2half_rn(fminf(__fdiv_rn(top, 7.f), 65504.f));
-  const float df = __half2float(d);
-  *scale = finite ? d : __ushort_as_half((unsigned short)0x7fffu);
-  if (!finite || df == 0.f) return 0x88888888u;
-  const float big = 12582912.f;          // 1.5 * 2^23: adding it rounds to an integer, in the low bits
-  const float inv = __frcp_rn(df), half_d = 0.5f * df;
-  uint32_t w = 0;
-  float off = 0.f;
-#pragma unroll
-  for (int i = 7; i >= 0; --i) {
-    const float t = __fmaf_rn(x[i], inv, big);
-    off = fmaxf(off, fabsf(__fmaf_rn(-__fadd_rn(t, -big), df, x[i])));
-    w = (w << 4) | (__float_as_uint(t) & 15u);
-  }
-  if (off >= half_d || top > 7.5f * df) {
-    w = 0;
-#pragma unroll 1
-    for (int i = 7; i >= 0; --i) {
-      float v = x[0];
-#pragma unroll
-      for (int j = 1; j < 8; ++j) v = i == j ? x[j] : v;
-      float k = __fadd_rn(__fmaf_rn(v, inv, big), -big);
-      const float e = __fmaf_rn(-k, df, v);
-      if (fabsf(e) > half_d || (fabsf(e) == half_d && (__float_as_uint(k + big) & 1u))) k += copysignf(1.f, e);
-      k = fminf(fmaxf(k, -8.f), 7.f);
-      w = (w << 4) | (__float_as_uint(k + big) & 15u);
-    }
-  }
-  return w ^ 0x88888888u;                // + 8 modulo 16
-}
-
 // 8 consecutive elements, as loaded
 template <typename T>
 struct Raw8 {
@@ -117,6 +63,89 @@ struct Raw8 {
     }
   }
 };
+
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+
+// largest magnitude of the 8, NaN when one is
+__device__ __forceinline__ float top8(const Raw8<float> &, const float (&x)[8]) {
+  float top = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) top = max_nan(top, fabsf(x[i]));
+  return top;
+}
+__device__ __forceinline__ float top8(const Raw8<__nv_bfloat16> &r, const float (&)[8]) {
+  const __nv_bfloat162 *h = reinterpret_cast<const __nv_bfloat162 *>(r.v);
+  const __nv_bfloat162 m = __hmax2_nan(__hmax2_nan(__habs2(h[0]), __habs2(h[1])), __hmax2_nan(__habs2(h[2]), __habs2(h[3])));
+  return max_nan(__low2float(m), __high2float(m));
+}
+
+// The codes, where they are hard to round: from the residual x - k d (one fma,
+// exact near a border: x lies within a factor of two of k d, or k is 0), one
+// beyond d / 2, or of exactly d / 2 with k odd (ties go to the even integer),
+// moves k by one; and quotients outside [-8, 7] (a subnormal scale is coarse).
+__device__ __noinline__ uint32_t q4_word_checked(float4 a, float4 b, float df, float inv) {
+  const float x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}, big = 12582912.f;
+  uint32_t w = 0;
+#pragma unroll
+  for (int i = 7; i >= 0; --i) {
+    float k = __fadd_rn(__fmaf_rn(x[i], inv, big), -big);
+    const float e = __fmaf_rn(-k, df, x[i]), half_d = 0.5f * df;
+    if (fabsf(e) > half_d || (fabsf(e) == half_d && (__float_as_uint(k + big) & 1u))) k += copysignf(1.f, e);
+    k = fminf(fmaxf(k, -8.f), 7.f);
+    w = (w << 4) | (__float_as_uint(k + big) & 15u);
+  }
+  return w ^ 0x88888888u;                // + 8 modulo 16
+}
+
+// One Q4_0 block is held by 4 neighbouring lanes, 8 dims each:
+//   d = fp16(max|x| / 7), u = clamp(rint(x / d), -8, 7) + 8
+// with correctly rounded quotients: max|x| / 7 by one residual step, and
+// rint(x / d) from x * (1 / d), whose error of a few units matters next to a
+// border only.
+//  - bf16: x has 8 bits and d 11, so x / d is exactly half an integer or at
+//    least 2^-12 away from one; rounded to a multiple of 2^-13 first, the
+//    approximate quotient then rounds as the exact one does, ties included.
+//  - fp32: blocks with a residual of d / 2 or more are done again, checked.
+// Four codes are packed as the number k0 + 16 k1 + 256 k2 + 4096 k3, exact in
+// fp32.  NaN and infinities make the block's scale NaN; a scale past fp16's
+// range saturates.
+template <typename T>
+__device__ __forceinline__ uint32_t q4_word(const Raw8<T> &raw, __half *scale) {
+  float x[8];
+  raw.floats(x);
+  float top = top8(raw, x);
+  top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, 1));
+  top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, 2));
+  const float seventh = 1.f / 7.f, q0 = __fmul_rn(top, seventh);
+  const float quot = __fmaf_rn(__fmaf_rn(-q0, 7.f, top), seventh, q0);
+  const __half d = __float2half_rn(fminf(quot, 65504.f));
+  const float df = __half2float(d);
+  const bool finite = top < INFINITY;    // false for NaN too
+  *scale = finite ? d : __ushort_as_half((unsigned short)0x7fffu);
+  if (!finite || df == 0.f) return 0x88888888u;
+  const float big = 12582912.f;          // 1.5 * 2^23: adding it rounds to an integer
+  const float inv = __fdividef(1.f, df);
+  float off = 0.f, k[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if (sizeof(T) == 2) {
+      k[i] = __fadd_rn(__fadd_rn(__fadd_rn(__fmaf_rn(x[i], inv, 1536.f), -1536.f), big), -big);
+    } else {
+      k[i] = __fadd_rn(__fmaf_rn(x[i], inv, big), -big);
+      off = fmaxf(off, fabsf(__fmaf_rn(-k[i], df, x[i])));
+    }
+  }
+  if ((sizeof(T) == 4 && off >= 0.5f * df) || top > 7.5f * df)
+    return q4_word_checked(make_float4(x[0], x[1], x[2], x[3]), make_float4(x[4], x[5], x[6], x[7]), df, inv);
+  const float lo = __fmaf_rn(__fmaf_rn(__fmaf_rn(k[3], 16.f, k[2]), 16.f, k[1]), 16.f, k[0]);
+  const float hi = __fmaf_rn(__fmaf_rn(__fmaf_rn(k[7], 16.f, k[6]), 16.f, k[5]), 16.f, k[4]);
+  // + 0x8888: every code + 8, in the low 16 bits
+  return __byte_perm(__float_as_uint(lo + (big + 34952.f)), __float_as_uint(hi + (big + 34952.f)), 0x5410);
+}
 
 // What a slot's append does, from the device's counts.
 struct AppendRange {
@@ -173,10 +202,8 @@ __global__ void __launch_bounds__(kStepThreads) k_kv4_append_step(const __grid_c
     Raw8<T> raw;
     if (live) raw.load(src.p, b * src.slot + t * src.token + h * src.head + sub * 8);
     else raw.clear();
-    float x[8];
-    raw.floats(x);
     __half d;
-    const uint32_t w = q4_word(x, &d);
+    const uint32_t w = q4_word(raw, &d);
     if (!live) continue;
     const int pos = r.start + t, p = pos % kKv4Chunk, j = sub >> 2, cc = sub & 3;
     uint8_t *chunk = chunk_of(h, pos);
@@ -245,53 +272,61 @@ __global__ void __launch_bounds__(kAppendThreads) k_kv4_append(const __grid_cons
   const Kv4Rows &rows = is_v ? a.v : a.k;
   const int ch0 = rg.start / kKv4Chunk + (int)blockIdx.x * kAppendChunks;
   const int ch1 = min(ch0 + kAppendChunks, (rg.end + kKv4Chunk - 1) / kKv4Chunk);
-  const char *src = static_cast<const char *>(rows.p) + (b * rows.slot + h * rows.head + sub * 8) * sizeof(T);
+  const T *src = static_cast<const T *>(rows.p) + b * rows.slot + h * rows.head + sub * 8;
   Raw8<T> raw[PASSES];
   auto fetch = [&](int ch) {
+    const int first = ch * kKv4Chunk + r0 - rg.start, count = rg.end - rg.start;
+    const T *at = src + first * rows.token;
+    if (ch * kKv4Chunk >= rg.start && (ch + 1) * kKv4Chunk <= rg.end) {
 #pragma unroll
-    for (int i = 0; i < PASSES; ++i) {
-      const int pos = ch * kKv4Chunk + r0 + i * RPP;
-      if (pos >= rg.start && pos < rg.end) raw[i].load(src, (int64_t)(pos - rg.start) * rows.token);
-      else raw[i].clear();
+      for (int i = 0; i < PASSES; ++i) raw[i].load(at + i * (RPP * rows.token), 0);
+    } else {
+#pragma unroll
+      for (int i = 0; i < PASSES; ++i) {
+        const int t = first + i * RPP;
+        if (t >= 0 && t < count) raw[i].load(at + i * (RPP * rows.token), 0);
+        else raw[i].clear();
+      }
     }
   };
   if (ch0 < ch1) fetch(ch0);
   for (int ch = ch0; ch < ch1; ++ch) {
-    const int p0 = ch * kKv4Chunk, lo = max(rg.start, p0), hi = min(rg.end, p0 + kKv4Chunk);
+    const int p0 = ch * kKv4Chunk, lo = max(rg.start, p0) - p0, hi = min(rg.end - p0, kKv4Chunk);
     uint8_t *chunk = a.l.codes + (bh * (a.l.cap / kKv4Chunk) + ch) * kv4_chunk_bytes(NG);
     uint8_t *scales = chunk + (is_v ? kv4_vscale_off(NG) : kv4_kscale_off(NG));
     uint32_t *vc = vcode[ch & 1];
     uint32_t w[PASSES];
     __half d[PASSES];
 #pragma unroll
-    for (int i = 0; i < PASSES; ++i) {
-      float x[8];
-      raw[i].floats(x);
-      w[i] = q4_word(x, &d[i]);
-    }
+    for (int i = 0; i < PASSES; ++i) w[i] = q4_word(raw[i], &d[i]);
     if (ch + 1 < ch1) fetch(ch + 1);
+    if (is_v) {
+#pragma unroll
+      for (int i = 0; i < PASSES; ++i) vc[(r0 + i * RPP) * VP + sub] = w[i];
+    }
 #pragma unroll
     for (int i = 0; i < PASSES; ++i) {
       const int p = r0 + i * RPP;
-      const bool live = p0 + p >= lo && p0 + p < hi;
-      if (is_v) vc[p * VP + sub] = w[i];
-      else if (live) *reinterpret_cast<uint32_t *>(chunk + kv4_kword(NG, p, cc, j)) = w[i];
-      if (live && cc == 0)
+      if (p < lo || p >= hi) continue;
+      if (!is_v) *reinterpret_cast<uint32_t *>(chunk + kv4_kword(NG, p, cc, j)) = w[i];
+      if (cc == 0)
         *reinterpret_cast<__half *>(scales + (is_v ? kv4_vscale(NG, p, j) : kv4_kscale(NG, p, j))) = d[i];
     }
-    if (tid < kKv4Chunk && p0 + tid >= lo && p0 + tid < hi) {
+    if (tid >= lo && tid < hi) {
       a.l.ids[bh * a.l.cap + p0 + tid] = rg.seen0 + (p0 + tid - rg.start);
       a.l.weights[bh * a.l.cap + p0 + tid] = 0.f;
     }
     __syncthreads();
-    if (tid < 16 * NG) {                          // (J, c, i): 8 dims 32 J + 8 i .. of 8 positions
-      const int i = tid & 3, c = (tid >> 2) & 3, J = tid >> 4;
+    // (J, c, i): 8 dims 32 J + 8 i .. of 8 positions; another pair of warps for each chunk
+    const int u = tid - 64 * (ch & 3);
+    if (u >= 0 && u < 16 * NG) {
+      const int i = u & 3, c = (u >> 2) & 3, J = u >> 4;
       uint32_t n[8], fresh = 0;
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         const int p = vpos(c, k);
         n[k] = vc[p * VP + J * 4 + i];
-        if (p0 + p >= lo && p0 + p < hi) fresh |= 15u << (4 * k);
+        if (p >= lo && p < hi) fresh |= 15u << (4 * k);
       }
       transpose_nibbles(n);
       uint8_t *to = chunk + kv4_v_off(NG) + kv4_vunit(J, 0, c) + 4 * i;
@@ -326,11 +361,32 @@ __device__ __forceinline__ void store8(void *p, int64_t at, const float (&x)[8])
   }
 }
 
-// d (u - 8) of a word's 8 codes: a code under the exponent of 2^23 is 2^23 + u
+// 16 bytes of the 8: all of them as bf16, or four (part 0 or 1) as fp32
+template <typename T>
+__device__ __forceinline__ void store16(void *p, int64_t at, int part, const float (&x)[8]) {
+  if constexpr (sizeof(T) == 2)
+    store8<T>(p, at, x);
+  else
+    *reinterpret_cast<float4 *>(static_cast<float *>(p) + at + 4 * part) =
+        part ? make_float4(x[4], x[5], x[6], x[7]) : make_float4(x[0], x[1], x[2], x[3]);
+}
+
+// d (u - 8) of a word's 8 codes: nibbles n and n + 4 under fp16 exponents are
+// 1024 + u (or 1024 + 16 u), u - 8 is exact in fp16 and its product in fp32
 __device__ __forceinline__ void q4_values(uint32_t w, float d, float (&x)[8]) {
+  const __half2 off = __half2half2(__ushort_as_half(0x6408)), sixteenth = __half2half2(__ushort_as_half(0x2c00)),
+                m72 = __half2half2(__ushort_as_half(0xd480));
 #pragma unroll
-  for (int e = 0; e < 8; ++e)
-    x[e] = d * (__uint_as_float(((w >> (4 * e)) & 15u) | 0x4b000000u) - 8388616.f);
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t lo = (w & 0x000f000fu) | 0x64006400u, hi = (w & 0x00f000f0u) | 0x64006400u;
+    const float2 l = __half22float2(__hsub2(*reinterpret_cast<const __half2 *>(&lo), off));
+    const float2 h = __half22float2(__hfma2(*reinterpret_cast<const __half2 *>(&hi), sixteenth, m72));
+    x[2 * i] = d * l.x;
+    x[2 * i + 4] = d * l.y;
+    x[2 * i + 1] = d * h.x;
+    x[2 * i + 5] = d * h.y;
+    w >>= 8;
+  }
 }
 
 __device__ __forceinline__ float half_at(const uint8_t *p) {
@@ -413,9 +469,12 @@ __global__ void __launch_bounds__(kReadThreads) k_kv4_read(const __grid_constant
       mbar_wait(&bar, 0);          // another bounded chance to land before the shared memory goes away
     }
   }
+  // a row's threads: one per 16 bytes, 8 dims of bf16 or 4 of fp32, so that
+  // every store of a warp is contiguous
+  constexpr int HALF = sizeof(T) == 4 ? 2 : 1, LPR = TPR * HALF;
   const int64_t slot_k = b * a.k.slot + h * a.k.head, slot_v = b * a.v.slot + h * a.v.head;
-  for (int i = tid; i < kReadChunks * kKv4Chunk * TPR; i += kReadThreads) {
-    const int q = i / TPR, sub = i % TPR, j = sub >> 2, cc = sub & 3, p = q % kKv4Chunk;
+  for (int i = tid; i < kReadChunks * kKv4Chunk * LPR; i += kReadThreads) {
+    const int q = i / LPR, sub = (i % LPR) / HALF, part = i % HALF, j = sub >> 2, cc = sub & 3, p = q % kKv4Chunk;
     const int64_t pos = p0 + q;
     if (pos < lo || pos >= hi) continue;
     const uint8_t *chunk = sm + (q / kKv4Chunk) * CH;
@@ -423,10 +482,10 @@ __global__ void __launch_bounds__(kReadThreads) k_kv4_read(const __grid_constant
     if (pos < len)
       q4_values(*reinterpret_cast<const uint32_t *>(chunk + kv4_kword(NG, p, cc, j)),
                 half_at(chunk + kv4_kscale_off(NG) + kv4_kscale(NG, p, j)), x);
-    store8<T>(a.k.p, slot_k + (pos - first) * a.k.token + sub * 8, x);
+    store16<T>(a.k.p, slot_k + (pos - first) * a.k.token + sub * 8, part, x);
   }
-  for (int i = tid; i < kReadChunks * 4 * TPR; i += kReadThreads) {
-    const int sub = i % TPR, j = sub >> 2, cc = sub & 3, c = (i / TPR) & 3, q = i / (4 * TPR);
+  for (int i = tid; i < kReadChunks * 4 * LPR; i += kReadThreads) {
+    const int sub = (i % LPR) / HALF, part = i % HALF, j = sub >> 2, cc = sub & 3, c = (i / LPR) & 3, q = i / (4 * LPR);
     const uint8_t *chunk = sm + q * CH;
     uint32_t w[8];
 #pragma unroll
@@ -440,7 +499,7 @@ __global__ void __launch_bounds__(kReadThreads) k_kv4_read(const __grid_constant
       if (pos < lo || pos >= hi) continue;
       float x[8] = {};
       if (pos < len) q4_values(w[n], half_at(chunk + kv4_vscale_off(NG) + kv4_vscale(NG, p, j)), x);
-      store8<T>(a.v.p, slot_v + (pos - first) * a.v.token + sub * 8, x);
+      store16<T>(a.v.p, slot_v + (pos - first) * a.v.token + sub * 8, part, x);
     }
   }
 }
@@ -460,7 +519,8 @@ __global__ void __launch_bounds__(THREADS) k_kv4_select(const __grid_constant__ 
   static_assert(THREADS >= 256, "a bin per thread");
   __shared__ uint32_t hist[COPIES][256];
   __shared__ uint32_t merged[2][256], sums[256];
-  __shared__ uint32_t warp_sum[WARPS], warp_min[WARPS], warp_max_[WARPS], totals[4];
+  __shared__ uint32_t warp_sum[WARPS], warp_min[WARPS], warp_max_[WARPS];
+  __shared__ uint2 warp_pair[WARPS], totals[2];
   __shared__ uint32_t range[3];                    // the CTA's smallest and largest loose key, entries that stay
   __shared__ uint32_t s_bin, s_need, s_equal;
   cg::cluster_group cluster = cg::this_cluster();
@@ -518,13 +578,11 @@ __global__ void __launch_bounds__(THREADS) k_kv4_select(const __grid_constant__ 
       }
     }
     sync_all();
-    lo = 0xffffffffu;
-    hi = stay = 0;
-    for (int c = 0; c < CL; ++c) {
-      const uint32_t *r = CL > 1 ? cluster.map_shared_rank(range, c) : range;
-      lo = min(lo, r[0]);
-      hi = max(hi, r[1]);
-      stay += r[2];
+    {   // over the cluster: a CTA per lane
+      const uint32_t *r = CL > 1 ? cluster.map_shared_rank(range, min(lane, CL - 1)) : range;
+      lo = __reduce_min_sync(0xffffffffu, r[0]);
+      hi = __reduce_max_sync(0xffffffffu, r[1]);
+      stay = __reduce_add_sync(0xffffffffu, lane < CL ? r[2] : 0u);
     }
     // loose keys agree above bit `shift - 1`; the need-th largest of them is sought
     const int top = lo < hi ? 31 - __clz(lo ^ hi) : 7;
@@ -556,8 +614,11 @@ __global__ void __launch_bounds__(THREADS) k_kv4_select(const __grid_constant__ 
       if (CL > 1) {
         cluster.sync();
         if (tid < 256) {
-          uint32_t s = 0;
-          for (int c = 0; c < CL; ++c) s += *cluster.map_shared_rank(mine + tid, c);
+          uint32_t v[8], s = 0;
+#pragma unroll
+          for (int c = 0; c < 8; ++c) v[c] = c < CL ? *cluster.map_shared_rank(mine + tid, c) : 0u;
+#pragma unroll
+          for (int c = 0; c < 8; ++c) s += v[c];
           sums[tid] = s;
         }
       }
@@ -596,20 +657,20 @@ __global__ void __launch_bounds__(THREADS) k_kv4_select(const __grid_constant__ 
       equal = s_equal;
     }
     // the first `need` of the `equal` entries with key == prefix stay (shift is 0 unless all do)
-    auto ranks = [&](uint32_t mine, int slot) -> uint32_t {
-      // exclusive base of this warp's count over the cluster, in index order
-      if (lane == 0) warp_sum[warp] = mine;
+    // exclusive bases of this warp's two counts over the cluster, in index order
+    auto ranks = [&](uint32_t first, uint32_t second, int slot) -> uint2 {
+      if (lane == 0) warp_pair[warp] = make_uint2(first, second);
       __syncthreads();
-      uint32_t before = 0, all = 0;
-      for (int w = 0; w < WARPS; ++w) {
-        const uint32_t s = warp_sum[w];
-        before += w < warp ? s : 0;
-        all += s;
-      }
+      const uint2 w = lane < WARPS ? warp_pair[lane] : make_uint2(0, 0);
+      uint2 before = make_uint2(__reduce_add_sync(0xffffffffu, lane < warp ? w.x : 0u),
+                                __reduce_add_sync(0xffffffffu, lane < warp ? w.y : 0u));
       if (CL > 1) {
+        const uint2 all = make_uint2(__reduce_add_sync(0xffffffffu, w.x), __reduce_add_sync(0xffffffffu, w.y));
         if (tid == 0) totals[slot] = all;
         cluster.sync();
-        for (int c = 0; c < rank; ++c) before += *cluster.map_shared_rank(&totals[slot], c);
+        const uint2 t = lane < rank ? *cluster.map_shared_rank(&totals[slot], lane) : make_uint2(0, 0);
+        before.x += __reduce_add_sync(0xffffffffu, t.x);
+        before.y += __reduce_add_sync(0xffffffffu, t.y);
       }
       __syncthreads();
       return before;
@@ -624,7 +685,7 @@ __global__ void __launch_bounds__(THREADS) k_kv4_select(const __grid_constant__ 
 #pragma unroll
       for (int k = 0; k < K; ++k)
         mine += __popc(__ballot_sync(0xffffffffu, ((loose >> k) & 1u) && key[k] == prefix));
-      uint32_t at = ranks(mine, 1);
+      uint32_t at = ranks(mine, 0, 0).x;
 #pragma unroll
       for (int k = 0; k < K; ++k) {
         const bool is_loose = (loose >> k) & 1u, eq = is_loose && key[k] == prefix;
@@ -642,7 +703,8 @@ __global__ void __launch_bounds__(THREADS) k_kv4_select(const __grid_constant__ 
       holes += __popc(__ballot_sync(0xffffffffu, i < m && !s));
       moves += __popc(__ballot_sync(0xffffffffu, i >= m && s));
     }
-    uint32_t hole_at = ranks(holes, 2), move_at = ranks(moves, 3);
+    const uint2 at = ranks(holes, moves, 1);
+    uint32_t hole_at = at.x, move_at = at.y;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       const int i = base + 32 * k;
@@ -651,8 +713,7 @@ __global__ void __launch_bounds__(THREADS) k_kv4_select(const __grid_constant__ 
       if (go) movers[move_at + __popc(vote & ((1u << lane) - 1u))] = i;
       move_at += __popc(vote);
     }
-    __threadfence();
-    sync_all();
+    sync_all();   // the cluster's barrier orders its writes of `movers` too
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       const int i = base + 32 * k;
