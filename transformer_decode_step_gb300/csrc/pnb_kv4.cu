@@ -744,7 +744,7 @@ constexpr int kMoveThreads = 128, kMoveChunks = 4;
 // border a V word may be read by others while its owner replaces it, with the
 // nibbles that they read unchanged (32-bit accesses).
 template <int NG>
-__global__ void __launch_bounds__(kMoveThreads) k_kv4_move(const __grid_constant__ Kv4EvictArgs a) {
+__global__ void __launch_bounds__(kMoveThreads, 8) k_kv4_move(const __grid_constant__ Kv4EvictArgs a) {
   constexpr int CH = kv4_chunk_bytes(NG), POS = kMoveChunks * kKv4Chunk;
   static_assert(POS == kMoveThreads, "a position per thread");
   __shared__ int src[POS];
@@ -756,23 +756,40 @@ __global__ void __launch_bounds__(kMoveThreads) k_kv4_move(const __grid_constant
   const int64_t bh = (int64_t)b * a.n_kv + h;
   const uint8_t *from = a.src.codes + bh * (a.src.cap / kKv4Chunk) * CH;
   uint8_t *to = a.dst.codes + (bh * (a.dst.cap / kKv4Chunk) + blockIdx.x * kMoveChunks) * CH;
+  // V units (J, r, c), 4 dims of 8 positions, NG per thread: those of the same
+  // place, at once unless most chunks will not be touched
+  constexpr int UNITS = 32 * NG, PER = kMoveChunks * UNITS / kMoveThreads;
+  uint4 w[PER];
+  auto same_place = [&](int k, int u) {
+    return *reinterpret_cast<const uint4 *>(from + (int64_t)(p0 / kKv4Chunk + k) * CH + kv4_v_off(NG) + u * 16);
+  };
+  if (!a.in_place) {
+#pragma unroll
+    for (int x = 0; x < PER; ++x) {
+      const int i = x * kMoveThreads + tid, k = i / UNITS;
+      if (p0 + k * kKv4Chunk < out) w[x] = same_place(k, i % UNITS);
+    }
+  }
+  int my_src = -1;
   {
     const int p = p0 + tid;
     int s = -1;
-    if (p < out) {
-      s = n > a.budget ? a.src_of[bh * a.src.cap + p] : p;
-      if (!a.in_place || s != p) {
-        a.dst.ids[bh * a.dst.cap + p] = a.src.ids[bh * a.src.cap + s];
-        a.dst.weights[bh * a.dst.cap + p] = a.src.weights[bh * a.src.cap + s];
-      }
-    }
+    if (p < out) s = n > a.budget ? a.src_of[bh * a.src.cap + p] : p;
+    my_src = s;
     src[tid] = s;
     const bool any = __any_sync(0xffffffffu, s >= 0 && s != p);
     if ((tid & 31) == 0) moved_chunk[tid >> 5] = any;
   }
   __syncthreads();
-  // K rows, NG 16-byte vectors each; all loads before the stores
+  // K rows, NG 16-byte vectors each, ids and weights; all loads before the stores
   {
+    const bool mine = my_src >= 0 && !(a.in_place && my_src == p0 + tid);
+    int32_t id = 0;
+    float weight = 0.f;
+    if (mine) {
+      id = a.src.ids[bh * a.src.cap + my_src];
+      weight = a.src.weights[bh * a.src.cap + my_src];
+    }
     uint4 v[NG];
 #pragma unroll
     for (int i = 0; i < NG; ++i) {
@@ -786,10 +803,14 @@ __global__ void __launch_bounds__(kMoveThreads) k_kv4_move(const __grid_constant
       if (s >= 0 && !(a.in_place && s == p0 + p))
         reinterpret_cast<uint4 *>(to + (p / kKv4Chunk) * CH + (p % kKv4Chunk) * 16 * NG)[tid % NG] = v[i];
     }
+    if (mine) {
+      a.dst.ids[bh * a.dst.cap + p0 + tid] = id;
+      a.dst.weights[bh * a.dst.cap + p0 + tid] = weight;
+    }
   }
   // both kinds of scales, a position per thread
-  if (src[tid] >= 0 && !(a.in_place && src[tid] == p0 + tid)) {
-    const int s = src[tid], p = tid % kKv4Chunk, q = s % kKv4Chunk;
+  if (my_src >= 0 && !(a.in_place && my_src == p0 + tid)) {
+    const int s = my_src, p = tid % kKv4Chunk, q = s % kKv4Chunk;
     const uint8_t *f = from + (int64_t)(s / kKv4Chunk) * CH;
     uint8_t *t = to + (tid / kKv4Chunk) * CH;
 #pragma unroll
@@ -800,15 +821,13 @@ __global__ void __launch_bounds__(kMoveThreads) k_kv4_move(const __grid_constant
           *reinterpret_cast<const uint16_t *>(f + kv4_vscale_off(NG) + kv4_vscale(NG, q, j));
     }
   }
-  // V codes: unit (J, r, c) holds 4 dims of 8 positions; thread: NG units in all
-  constexpr int UNITS = 32 * NG, PER = kMoveChunks * UNITS / kMoveThreads;
   auto live = [&](int k) { return p0 + k * kKv4Chunk < out && (!a.in_place || moved_chunk[k]); };
-  uint4 w[PER];
+  if (a.in_place) {
 #pragma unroll
-  for (int x = 0; x < PER; ++x) {
-    const int i = x * kMoveThreads + tid, k = i / UNITS, u = i % UNITS;
-    if (live(k))
-      w[x] = *reinterpret_cast<const uint4 *>(from + (int64_t)(p0 / kKv4Chunk + k) * CH + kv4_v_off(NG) + u * 16);
+    for (int x = 0; x < PER; ++x) {
+      const int i = x * kMoveThreads + tid, k = i / UNITS;
+      if (live(k)) w[x] = same_place(k, i % UNITS);
+    }
   }
 #pragma unroll
   for (int x = 0; x < PER; ++x) {
