@@ -181,7 +181,7 @@ struct AppendRange {
 // each 16-byte unit of V words (8 positions of 4 dims) that holds a new
 // position is read, completed and written by one thread.  Bound by its four
 // dependent trips to memory.
-constexpr int kStepThreads = 512, kStepTokens = 8;
+constexpr int kStepThreads = 512;
 
 template <int NG, typename T>
 __global__ void __launch_bounds__(kStepThreads) k_kv4_append_step(const __grid_constant__ Kv4AppendArgs a) {
@@ -329,12 +329,17 @@ __global__ void __launch_bounds__(kAppendThreads) k_kv4_append(const __grid_cons
         if (p >= lo && p < hi) fresh |= 15u << (4 * k);
       }
       transpose_nibbles(n);
-      uint8_t *to = chunk + kv4_v_off(NG) + kv4_vunit(J, 0, c) + 4 * i;
+      uint32_t *to = reinterpret_cast<uint32_t *>(chunk + kv4_v_off(NG) + kv4_vunit(J, 0, c) + 4 * i);
+      if (fresh != 0xffffffffu && fresh != 0) {   // dim r of the eight: word 16 r; all loads first
+        uint32_t old[8];
 #pragma unroll
-      for (int r = 0; r < 8; ++r) {               // dim r of the eight
-        uint32_t *p = reinterpret_cast<uint32_t *>(to + kv4_vunit(0, r, 0));
-        if (fresh == 0xffffffffu) *p = n[r];
-        else if (fresh) *p = (*p & ~fresh) | (n[r] & fresh);
+        for (int r = 0; r < 8; ++r) old[r] = to[16 * r];
+#pragma unroll
+        for (int r = 0; r < 8; ++r) n[r] = (old[r] & ~fresh) | (n[r] & fresh);
+      }
+      if (fresh != 0) {
+#pragma unroll
+        for (int r = 0; r < 8; ++r) to[16 * r] = n[r];
       }
     }
   }
@@ -434,7 +439,7 @@ __global__ void __launch_bounds__(256) k_kv4_read_step(const __grid_constant__ K
 // bulk copy brings into shared memory; then 8 dims of a K position per thread,
 // and 8 x 8 nibbles of V (8 positions, 8 dims) per thread.  Bound by the
 // values' bytes.
-constexpr int kReadThreads = 256, kReadChunks = 4;
+constexpr int kReadThreads = 256, kReadChunks = 4, kReadStepTokens = 16;
 
 template <int NG, typename T>
 __global__ void __launch_bounds__(kReadThreads) k_kv4_read(const __grid_constant__ Kv4ReadArgs a) {
@@ -875,17 +880,24 @@ int chunk_groups(int T, int group) { return ((T + kKv4Chunk - 2) / kKv4Chunk + g
 
 template <int NG, typename T>
 cudaError_t run_append(const Kv4AppendArgs &a, cudaStream_t st) {
-  // measured on 64 slots x 8 heads at head_dim 128 (bf16), step against chunks: see kStepTokens
-  const size_t smem = (size_t)a.T * a.n_kv * 4 * NG * 4;
-  if (a.T <= kStepTokens && smem <= 48 * 1024)
-    return kv4_launch(k_kv4_append_step<NG, T>, dim3(a.n_slot), dim3(kStepThreads), smem, 1, st, a);
+  // One CTA per slot (2.4 us and 0.6 for every 2048 values of a slot's rows)
+  // against one per chunk and head (3.2 us while all are resident, 12 us for
+  // 2048 of them); bf16, head_dim 128, us, step form first:
+  //   64 slots x 8 heads: 1 token 3.0, 4.7; 2 tokens 3.3, 4.5; 8 tokens 8.2, 4.5
+  //   1 x 32: 1 token 4.8, 3.2     256 x 8: 1 token 3.6, 11.8; 4 tokens 6.4, 12.2
+  const int64_t values = (int64_t)a.T * a.n_kv * 32 * NG;
+  if (values <= 2048 || (values <= 8192 && (int64_t)a.n_slot * a.n_kv > 1024))
+    return kv4_launch(k_kv4_append_step<NG, T>, dim3(a.n_slot), dim3(kStepThreads), (size_t)values / 2, 1, st, a);
   const dim3 grid(chunk_groups(a.T, kAppendChunks), a.n_kv, a.n_slot);
   return kv4_launch(k_kv4_append<NG, T>, grid, dim3(kAppendThreads), 0, 1, st, a);
 }
 
 template <int NG, typename T>
 cudaError_t run_read(const Kv4ReadArgs &a, cudaStream_t st) {
-  if (a.T <= kStepTokens) {
+  // few rows per chunk: straight from the cache, or through whole chunks (64
+  // slots x 8 heads at head_dim 128, fp32, us: 1 token 2.3, 4.8; 16 tokens 4.6, 6.0;
+  // 32 tokens 7.0 both)
+  if (a.T <= kReadStepTokens) {
     const int64_t threads = (int64_t)a.n_slot * a.T * a.n_kv * 8 * NG;
     return kv4_launch(k_kv4_read_step<NG, T>, dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, 1, st, a);
   }

@@ -30,7 +30,7 @@ namespace {
 
 // Work units: an item (slot, KV head, block of 8 query rows) takes one per
 // chunk of 32 positions and kItemUnits more for its queries and its end.
-constexpr int kItemUnits = 1;
+constexpr int kItemUnits = 2;
 // units a warp takes at least: below it a call uses fewer warps
 constexpr int kMinUnits = 1;
 

@@ -42,6 +42,8 @@ class Kv4Cache:
                           ctypes.byref(h)), "pnb_kvq_new")
         self._h = h.value
         self._device = buf.get_device()
+        self._n_slot, self._head_dim, self._slots = n_slot, head_dim, (n_slot,)
+        self._n_head, self._n_kv = n_head, n_kv_head
         self._views = {}
 
     def __del__(self):
@@ -59,11 +61,16 @@ class Kv4Cache:
             return self._raw_stream(self._device)
         return stream if isinstance(stream, int) else stream.cuda_stream
 
-    def _rows(self, t, what: str, T: int, heads: int) -> bytes:
-        g = self.cfg
-        if tuple(t.shape) != (g.n_slot, T, heads, g.head_dim):
-            raise PnbError(-1, f"{what}: shape {tuple(t.shape)} is not [{g.n_slot}][{T}]"
-                               f"[{heads}][{g.head_dim}]")
+    def _shape(self, t, what: str, heads: int) -> tuple:
+        """[n_slot][T][heads][head_dim] with T from the tensor."""
+        shape = t.shape
+        if len(shape) != 4:
+            raise PnbError(-1, f"{what}: needs rows [n_slot][T][heads][head_dim]")
+        return (self._n_slot, shape[1], heads, self._head_dim)
+
+    def _rows(self, t, what: str, shape: tuple) -> bytes:
+        if t.shape != shape:
+            raise PnbError(-1, f"{what}: shape {tuple(t.shape)} is not {shape}")
         dt = self._dtypes.get(t.dtype)
         slot, token, head, one = t.stride()
         if dt is None or one != 1:
@@ -71,22 +78,17 @@ class Kv4Cache:
         if t.get_device() != self._device:
             raise PnbError(-10, f"{what}: on {t.device}, the cache is on {self.buf.device}")
         # a dimension of one element has no stride of its own
-        return _pack_rows(t.data_ptr(), slot if g.n_slot > 1 else 0, token if T > 1 else 0,
+        n, T, heads, _ = shape
+        return _pack_rows(t.data_ptr(), slot if n > 1 else 0, token if T > 1 else 0,
                           head if heads > 1 else 0, dt)
 
     def _ints(self, t, what: str):
         if t is None:
             return None
-        if t.dtype != self._int32 or t.numel() != self.cfg.n_slot or not t.is_contiguous() \
+        if t.dtype != self._int32 or t.shape != self._slots or not t.is_contiguous() \
                 or t.get_device() != self._device:
-            raise PnbError(-1, f"{what}: needs {self.cfg.n_slot} contiguous int32 on the cache's device")
+            raise PnbError(-1, f"{what}: needs {self._n_slot} contiguous int32 on the cache's device")
         return t.data_ptr()
-
-    @staticmethod
-    def _tokens(t, what: str) -> int:
-        if t.dim() != 4:
-            raise PnbError(-1, f"{what}: needs rows [n_slot][T][heads][head_dim]")
-        return t.size(1)
 
     def reset(self, slot: Optional[int] = None, stream=None):
         """Empty one slot, or all of them (which also clears the error bits), in every layer."""
@@ -95,27 +97,28 @@ class Kv4Cache:
     def append(self, layer: int, k, v, n_new=None, start=None, stream=None):
         """Quantise and append n_new[b] (default: all T) rows of every slot b at entry
         start[b] (default: its length).  n_new, start: device int32 [n_slot]."""
-        n, T = self.cfg.n_kv_head, self._tokens(k, "k")
-        check(pnb_kvq_append(self._h, layer, self._rows(k, "k", T, n), self._rows(v, "v", T, n), T,
-                             self._ints(n_new, "n_new"), self._ints(start, "start"),
+        shape = self._shape(k, "k", self._n_kv)
+        check(pnb_kvq_append(self._h, layer, self._rows(k, "k", shape), self._rows(v, "v", shape),
+                             shape[1], self._ints(n_new, "n_new"), self._ints(start, "start"),
                              self._stream(stream)), "pnb_kvq_append")
 
     def read(self, layer: int, k, v, first=None, stream=None):
         """Write the values of entries first[b] (default 0) .. + T - 1 into k and v."""
-        n, T = self.cfg.n_kv_head, self._tokens(k, "k")
-        check(pnb_kvq_read(self._h, layer, self._ints(first, "first"), T, self._rows(k, "k", T, n),
-                           self._rows(v, "v", T, n), self._stream(stream)), "pnb_kvq_read")
+        shape = self._shape(k, "k", self._n_kv)
+        check(pnb_kvq_read(self._h, layer, self._ints(first, "first"), shape[1],
+                           self._rows(k, "k", shape), self._rows(v, "v", shape),
+                           self._stream(stream)), "pnb_kvq_read")
 
     def attention(self, layer: int, q, out, decay: Optional[float] = None, stream=None):
         """Attention of the last T appended tokens' queries into ``out``; with ``decay``,
         weights = decay * weights + this call's softmax weights."""
-        n, T = self.cfg.n_head, self._tokens(q, "q")
+        shape = self._shape(q, "q", self._n_head)
         if decay is None:
             decay = -1.0
         elif not decay >= 0.0:
             raise PnbError(-1, f"decay {decay} is negative or not a number")
-        check(pnb_kvq_attention(self._h, layer, self._rows(q, "q", T, n), T,
-                                self._rows(out, "out", T, n), decay, self._stream(stream)),
+        check(pnb_kvq_attention(self._h, layer, self._rows(q, "q", shape), shape[1],
+                                self._rows(out, "out", shape), decay, self._stream(stream)),
               "pnb_kvq_attention")
 
     def evict(self, layer: int, budget: int, n_sink: int = 0, n_recent: int = 0,
