@@ -70,6 +70,17 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return d;
 }
 
+__device__ __forceinline__ float2 dup(float v) { return make_float2(v, v); }
+
+// a + b on packed pairs of fp32
+__device__ __forceinline__ float2 fadd2(float2 a, float2 b) {
+  unsigned long long d;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(d)
+      : "l"(*reinterpret_cast<unsigned long long *>(&a)), "l"(*reinterpret_cast<unsigned long long *>(&b)));
+  return *reinterpret_cast<float2 *>(&d);
+}
+
 // largest magnitude of the 8, NaN when one is
 __device__ __forceinline__ float top8(const Raw8<float> &, const float (&x)[8]) {
   float top = 0.f;
@@ -128,23 +139,28 @@ __device__ __forceinline__ uint32_t q4_word(const Raw8<T> &raw, __half *scale) {
   *scale = finite ? d : __ushort_as_half((unsigned short)0x7fffu);
   if (!finite || df == 0.f) return 0x88888888u;
   const float big = 12582912.f;          // 1.5 * 2^23: adding it rounds to an integer
-  const float inv = __fdividef(1.f, df);
-  float off = 0.f, k[8];
+  float inv;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(df));
+  float off = 0.f;
+  float2 k[4];                           // dims i and i + 4, two at a time
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < 4; ++i) {
+    const float2 v = make_float2(x[i], x[i + 4]);
     if (sizeof(T) == 2) {
-      k[i] = __fadd_rn(__fadd_rn(__fadd_rn(__fmaf_rn(x[i], inv, 1536.f), -1536.f), big), -big);
+      const float2 q = fadd2(ffma2(v, dup(inv), dup(1536.f)), dup(-1536.f));
+      k[i] = fadd2(fadd2(q, dup(big)), dup(-big));
     } else {
-      k[i] = __fadd_rn(__fmaf_rn(x[i], inv, big), -big);
-      off = fmaxf(off, fabsf(__fmaf_rn(-k[i], df, x[i])));
+      k[i] = fadd2(ffma2(v, dup(inv), dup(big)), dup(-big));
+      const float2 e = ffma2(k[i], dup(-df), v);
+      off = fmaxf(off, fmaxf(fabsf(e.x), fabsf(e.y)));
     }
   }
   if ((sizeof(T) == 4 && off >= 0.5f * df) || top > 7.5f * df)
     return q4_word_checked(make_float4(x[0], x[1], x[2], x[3]), make_float4(x[4], x[5], x[6], x[7]), df, inv);
-  const float lo = __fmaf_rn(__fmaf_rn(__fmaf_rn(k[3], 16.f, k[2]), 16.f, k[1]), 16.f, k[0]);
-  const float hi = __fmaf_rn(__fmaf_rn(__fmaf_rn(k[7], 16.f, k[6]), 16.f, k[5]), 16.f, k[4]);
+  const float2 four = ffma2(ffma2(ffma2(k[3], dup(16.f), k[2]), dup(16.f), k[1]), dup(16.f), k[0]);
   // + 0x8888: every code + 8, in the low 16 bits
-  return __byte_perm(__float_as_uint(lo + (big + 34952.f)), __float_as_uint(hi + (big + 34952.f)), 0x5410);
+  const float2 bits = fadd2(four, dup(big + 34952.f));
+  return __byte_perm(__float_as_uint(bits.x), __float_as_uint(bits.y), 0x5410);
 }
 
 // What a slot's append does, from the device's counts.
