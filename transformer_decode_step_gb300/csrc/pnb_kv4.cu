@@ -268,8 +268,8 @@ __global__ void __launch_bounds__(kStepThreads) k_kv4_append_step(const __grid_c
 // for fp32) per thread and pass, the next chunk's rows on their way meanwhile.
 // K words go straight to their place; V words hold 8 positions of one dim, so
 // 8 x 8 nibbles are transposed by one thread each through shared memory, and a
-// chunk that already holds entries keeps their nibbles.  The slot's last CTA
-// moves its length.  Bound by the rows' bytes.
+// chunk that already holds entries keeps their nibbles.  The last of the slot's
+// CTAs to have read the length moves it.  Bound by the rows' bytes.
 constexpr int kAppendThreads = 256, kAppendChunks = 4;
 
 template <int NG, typename T>
@@ -282,6 +282,12 @@ __global__ void __launch_bounds__(kAppendThreads) k_kv4_append(const __grid_cons
   const int tid = threadIdx.x, b = blockIdx.z, h = blockIdx.y;
   pdl_wait();
   const AppendRange rg(a, b);
+  __syncthreads();
+  if (tid == 0) {                                 // all the CTA's threads have read the old length
+    __threadfence();
+    const unsigned ctas = gridDim.x * gridDim.y;
+    if (atomicInc(a.arrive + b, ctas - 1) == ctas - 1) rg.commit(a, b);
+  }
   const int64_t bh = (int64_t)b * a.n_kv + h;
   const bool is_v = tid >= 128;
   const int th = tid & 127, sub = th % TPR, j = sub >> 2, cc = sub & 3, r0 = th / TPR;
@@ -345,25 +351,20 @@ __global__ void __launch_bounds__(kAppendThreads) k_kv4_append(const __grid_cons
         if (p >= lo && p < hi) fresh |= 15u << (4 * k);
       }
       transpose_nibbles(n);
-      uint32_t *to = reinterpret_cast<uint32_t *>(chunk + kv4_v_off(NG) + kv4_vunit(J, 0, c) + 4 * i);
-      if (fresh != 0xffffffffu && fresh != 0) {   // dim r of the eight: word 16 r; all loads first
+      uint8_t *unit = chunk + kv4_v_off(NG) + 4 * i;
+      auto to = [&](int r) { return reinterpret_cast<uint32_t *>(unit + kv4_vunit(J, r, c)); };   // dim r of the eight
+      if (fresh != 0xffffffffu && fresh != 0) {   // all loads first
         uint32_t old[8];
 #pragma unroll
-        for (int r = 0; r < 8; ++r) old[r] = to[16 * r];
+        for (int r = 0; r < 8; ++r) old[r] = *to(r);
 #pragma unroll
         for (int r = 0; r < 8; ++r) n[r] = (old[r] & ~fresh) | (n[r] & fresh);
       }
       if (fresh != 0) {
 #pragma unroll
-        for (int r = 0; r < 8; ++r) to[16 * r] = n[r];
+        for (int r = 0; r < 8; ++r) *to(r) = n[r];
       }
     }
-  }
-  __syncthreads();
-  if (tid == 0) {                                 // all the CTA's threads have read the old length
-    __threadfence();
-    const unsigned ctas = gridDim.x * gridDim.y;
-    if (atomicInc(a.arrive + b, ctas - 1) == ctas - 1) rg.commit(a, b);
   }
 }
 
@@ -528,18 +529,19 @@ __global__ void __launch_bounds__(kReadThreads) k_kv4_read(const __grid_constant
 // ---------------------------------------------------------------- eviction
 // Selection, one thread-block cluster per (slot, KV head), the entries' keys
 // (order-preserving images of their weights) in registers.  Entries that must
-// stay are set apart; a radix descent, eight bits at a time from the highest
-// bit in which the others differ, finds the key of the rank that is left, and
-// ends as soon as a bin is kept whole; of the entries with exactly that key the
+// stay are set apart; a radix descent over the others' distances from their
+// smallest key, ten bits at a time, finds the key of the rank that is left, and
+// ends as soon as a bin is kept whole (mostly after two levels); of the entries with exactly that key the
 // first ones stay.  Then the kept entries behind the budget ("movers") fill the
-// dropped ones' places below it ("holes"), both in index order:
-// src_of[hole r] = mover r.  Bound by the latency of its barriers.
+// dropped ones' places below it ("holes"), both in index order: src_of[p] is p
+// or, for hole r, -1 - r, and movers[r] what goes there.  Bound by the latency
+// of its barriers.
 template <int THREADS, int K>
-__global__ void __launch_bounds__(THREADS) k_kv4_select(const __grid_constant__ Kv4EvictArgs a) {
-  constexpr int WARPS = THREADS / 32, COPIES = 8;
-  static_assert(THREADS >= 256, "a bin per thread");
-  __shared__ uint32_t hist[COPIES][256];
-  __shared__ uint32_t merged[2][256], sums[256];
+__global__ void __launch_bounds__(THREADS, THREADS >= 1024 ? 1 : 3) k_kv4_select(const __grid_constant__ Kv4EvictArgs a) {
+  constexpr int WARPS = THREADS / 32, COPIES = 4, BITS = 10, BINS = 1 << BITS;
+  static_assert(THREADS >= BINS / 4, "four bins per thread");
+  __shared__ __align__(16) uint32_t hist[COPIES][BINS];
+  __shared__ __align__(16) uint32_t merged[2][BINS];
   __shared__ uint32_t warp_sum[WARPS], warp_min[WARPS], warp_max_[WARPS];
   __shared__ uint2 warp_pair[WARPS], totals[2];
   __shared__ uint32_t range[3];                    // the CTA's smallest and largest loose key, entries that stay
@@ -557,6 +559,16 @@ __global__ void __launch_bounds__(THREADS) k_kv4_select(const __grid_constant__ 
   const int32_t *ids = a.src.ids + bh * a.src.cap;
   const float *wt = a.src.weights + bh * a.src.cap;
   int32_t *src_of = a.src_of + bh * a.src.cap, *movers = a.movers + bh * a.src.cap;
+  __syncthreads();
+  if (tid == 0) {                 // the last of the slot's CTAs to have read the length moves it
+    if (h == 0 && rank == 0) a.n_old[b] = n;
+    __threadfence();
+    const unsigned ctas = gridDim.x * gridDim.y;
+    if (atomicInc(a.arrive + b, ctas - 1) == ctas - 1) {
+      a.dst.len[b] = min(n, m);
+      a.dst.seen[b] = seen;
+    }
+  }
   // (uniform over the cluster)
   if (n > m) {
     const int base = rank * THREADS * K + warp * 32 * K + lane;   // this lane's entries: base + 32 k
@@ -578,7 +590,7 @@ __global__ void __launch_bounds__(THREADS) k_kv4_select(const __grid_constant__ 
         }
       }
     }
-    for (int i = tid; i < COPIES * 256; i += THREADS) (&hist[0][0])[i] = 0;
+    for (int i = tid; i < COPIES * BINS; i += THREADS) (&hist[0][0])[i] = 0;
     lo = __reduce_min_sync(0xffffffffu, lo);
     hi = __reduce_max_sync(0xffffffffu, hi);
     stay = __reduce_add_sync(0xffffffffu, stay);
@@ -605,71 +617,72 @@ __global__ void __launch_bounds__(THREADS) k_kv4_select(const __grid_constant__ 
       hi = __reduce_max_sync(0xffffffffu, r[1]);
       stay = __reduce_add_sync(0xffffffffu, lane < CL ? r[2] : 0u);
     }
-    // loose keys agree above bit `shift - 1`; the need-th largest of them is sought
-    const int top = lo < hi ? 31 - __clz(lo ^ hi) : 7;
-    int shift = top + 1;
-    uint32_t prefix = (uint32_t)((uint64_t)hi >> shift), equal = 0xffffffffu;
+    // distances from the smallest loose key; the need-th largest is sought.
+    // prefix: its bits from `shift` up
+#pragma unroll
+    for (int k = 0; k < K; ++k) key[k] -= lo;
+    int shift = hi > lo ? 32 - __clz(hi - lo) : 1;
+    uint32_t prefix = 0, equal = 0xffffffffu;
     uint32_t need = (uint32_t)m > stay ? (uint32_t)m - stay : 0u;
 #pragma unroll 1
     for (int level = 0; need > 0 && shift > 0 && need != equal; ++level) {
-      const int width = min(8, shift);
+      const int width = min(BITS, shift);
       shift -= width;
       const uint32_t digit = (1u << width) - 1u;
 #pragma unroll
       for (int k = 0; k < K; ++k) {
-        const bool in = ((loose >> k) & 1u) && (uint32_t)((uint64_t)key[k] >> (shift + width)) == prefix;
-        if (in) atomicAdd(&hist[warp % COPIES][(key[k] >> shift) & digit], 1u);
+        const uint32_t d = key[k] >> shift;
+        if (((loose >> k) & 1u) && (level == 0 || (d >> width) == prefix)) atomicAdd(&hist[warp % COPIES][d & digit], 1u);
       }
       __syncthreads();
+      // thread t: the four bins 1023 - 4 t - 3 .. 1023 - 4 t, over the copies and the cluster
+      const int first = BINS - 4 - 4 * tid;
+      uint4 v = make_uint4(0, 0, 0, 0);
+      auto add = [&](uint4 x) { v.x += x.x; v.y += x.y; v.z += x.z; v.w += x.w; };
       uint32_t *mine = merged[level & 1];
-      if (tid < 256) {
-        uint32_t s = 0;
+      if (tid < BINS / 4) {
 #pragma unroll
         for (int q = 0; q < COPIES; ++q) {
-          s += hist[q][tid];
-          hist[q][tid] = 0;
+          uint4 *h4 = reinterpret_cast<uint4 *>(&hist[q][first]);
+          add(*h4);
+          *h4 = make_uint4(0, 0, 0, 0);
         }
-        mine[tid] = s;
-        if (CL == 1) sums[tid] = s;
+        if (CL > 1) *reinterpret_cast<uint4 *>(mine + first) = v;
       }
       if (CL > 1) {
         cluster.sync();
-        if (tid < 256) {
-          uint32_t v[8], s = 0;
+        if (tid < BINS / 4) {
+          uint4 x[8];
 #pragma unroll
-          for (int c = 0; c < 8; ++c) v[c] = c < CL ? *cluster.map_shared_rank(mine + tid, c) : 0u;
+          for (int c = 0; c < 8; ++c)
+            x[c] = c < CL ? *reinterpret_cast<const uint4 *>(cluster.map_shared_rank(mine + first, c)) : make_uint4(0, 0, 0, 0);
+          v = make_uint4(0, 0, 0, 0);
 #pragma unroll
-          for (int c = 0; c < 8; ++c) s += v[c];
-          sums[tid] = s;
+          for (int c = 0; c < 8; ++c) add(x[c]);
         }
       }
+      // the bin in which the running count from the top reaches `need`
+      const uint32_t sum = v.x + v.y + v.z + v.w;
+      uint32_t inc = sum;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t u = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += u;
+      }
+      if (lane == 31) warp_sum[warp] = inc;
       __syncthreads();
-      // warp 0: the bin in which the running count from the top reaches `need`
-      // (lane l holds bins 255 - 8 l - 7 ..)
-      if (warp == 0) {
-        uint32_t v[8], sum = 0;
+      const uint32_t before = __reduce_add_sync(0xffffffffu, lane < warp ? warp_sum[lane] : 0u);
+      uint32_t above = before + inc - sum;
+      if (above < need && need <= above + sum) {
+        const uint32_t four[4] = {v.w, v.z, v.y, v.x};
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          v[q] = sums[255 - 8 * lane - q];
-          sum += v[q];
-        }
-        uint32_t inc = sum;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const uint32_t u = __shfl_up_sync(0xffffffffu, inc, o);
-          if (lane >= o) inc += u;
-        }
-        uint32_t above = inc - sum;
-        if (above < need && need <= inc) {
-#pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            if (above < need && need <= above + v[q]) {
-              s_bin = 255 - 8 * lane - q;
-              s_need = need - above;
-              s_equal = v[q];
-            }
-            above += v[q];
+        for (int q = 0; q < 4; ++q) {
+          if (above < need && need <= above + four[q]) {
+            s_bin = first + 3 - q;
+            s_need = need - above;
+            s_equal = four[q];
           }
+          above += four[q];
         }
       }
       __syncthreads();
@@ -734,26 +747,15 @@ __global__ void __launch_bounds__(THREADS) k_kv4_select(const __grid_constant__ 
       if (go) movers[move_at + __popc(vote & ((1u << lane) - 1u))] = i;
       move_at += __popc(vote);
     }
-    sync_all();   // the cluster's barrier orders its writes of `movers` too
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       const int i = base + 32 * k;
       const bool hole = i < m && !((kept >> k) & 1u);
       const uint32_t vote = __ballot_sync(0xffffffffu, hole);
-      if (i < m) src_of[i] = hole ? __ldcg(movers + hole_at + __popc(vote & ((1u << lane) - 1u))) : i;
+      if (i < m) src_of[i] = hole ? -1 - (int)(hole_at + __popc(vote & ((1u << lane) - 1u))) : i;
       hole_at += __popc(vote);
     }
     if (CL > 1) cluster.sync();   // no CTA leaves while a peer may read its shared memory
-  }
-  __syncthreads();                // every thread has read the old length
-  if (tid == 0) {
-    if (h == 0 && rank == 0) a.n_old[b] = n;
-    __threadfence();
-    const unsigned ctas = gridDim.x * gridDim.y;
-    if (atomicInc(a.arrive + b, ctas - 1) == ctas - 1) {
-      a.dst.len[b] = min(n, m);
-      a.dst.seen[b] = seen;
-    }
   }
 }
 
@@ -781,7 +783,7 @@ __global__ void __launch_bounds__(kMoveThreads, 8) k_kv4_move(const __grid_const
   // place, at once unless most chunks will not be touched
   constexpr int UNITS = 32 * NG, PER = kMoveChunks * UNITS / kMoveThreads;
   uint4 w[PER];
-  auto same_place = [&](int k, int u) {
+  auto same_place = [&](int k, int u) {   // unit u in their order in memory
     return *reinterpret_cast<const uint4 *>(from + (int64_t)(p0 / kKv4Chunk + k) * CH + kv4_v_off(NG) + u * 16);
   };
   if (!a.in_place) {
@@ -795,7 +797,10 @@ __global__ void __launch_bounds__(kMoveThreads, 8) k_kv4_move(const __grid_const
   {
     const int p = p0 + tid;
     int s = -1;
-    if (p < out) s = n > a.budget ? a.src_of[bh * a.src.cap + p] : p;
+    if (p < out) {
+      s = n > a.budget ? a.src_of[bh * a.src.cap + p] : p;
+      if (s < 0) s = a.movers[bh * a.src.cap - 1 - s];
+    }
     my_src = s;
     src[tid] = s;
     const bool any = __any_sync(0xffffffffu, s >= 0 && s != p);
@@ -852,7 +857,7 @@ __global__ void __launch_bounds__(kMoveThreads, 8) k_kv4_move(const __grid_const
   }
 #pragma unroll
   for (int x = 0; x < PER; ++x) {
-    const int i = x * kMoveThreads + tid, k = i / UNITS, u = i % UNITS, c = u & 3;
+    const int i = x * kMoveThreads + tid, k = i / UNITS, u = i % UNITS, J = u >> 5, c = (u >> 3) & 3, r = (u - 2 * c) & 7;
     if (!live(k)) continue;
     if (moved_chunk[k]) {
       uint4 v[8];
@@ -864,7 +869,7 @@ __global__ void __launch_bounds__(kMoveThreads, 8) k_kv4_move(const __grid_const
         if (s[e] == p0 + k * kKv4Chunk + p) s[e] = -1;
         if (s[e] >= 0)
           v[e] = *reinterpret_cast<const uint4 *>(from + (int64_t)(s[e] / kKv4Chunk) * CH + kv4_v_off(NG) +
-                                                  ((u & ~3) + ((s[e] >> 1) & 3)) * 16);
+                                                  kv4_vunit(J, r, (s[e] >> 1) & 3));
       }
 #pragma unroll
       for (int e = 0; e < 8; ++e) {

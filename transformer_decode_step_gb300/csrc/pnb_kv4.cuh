@@ -56,8 +56,12 @@ __host__ __device__ constexpr int kv4_kscale(int ng, int p, int j) { return p * 
 __host__ __device__ constexpr int kv4_vscale(int ng, int p, int j) {
   return (p >> 1) * 4 * ng + j * 4 + (p & 1) * 2;
 }
-// V words of dims 32 J + 8 i + r (i = 0..3, 16 bytes) for position class c
-__host__ __device__ constexpr int kv4_vunit(int J, int r, int c) { return J * 512 + (r * 4 + c) * 16; }
+// V words of dims 32 J + 8 i + r (i = 0..3, 16 bytes) for position class c: a
+// position's 32 dims lie in 128 contiguous bytes, the units rotated so that the
+// attention's lanes (r, c) read them without bank conflicts
+__host__ __device__ constexpr int kv4_vunit(int J, int r, int c) {
+  return J * 512 + c * 128 + ((r + 2 * c) & 7) * 16;
+}
 // bit position of position p's nibble in its V word; its class is (p / 2) % 4
 __host__ __device__ constexpr int kv4_vshift(int p) { return 4 * ((p >> 3) + 4 * (p & 1)); }
 
@@ -169,16 +173,18 @@ __device__ __forceinline__ int kv4_len(const Kv4Layer &l, int b) {
 }
 
 // Prefix sums over the slots of mult * (ceil(len / unit) + extra), 0 for an
-// empty slot, into pre[0 .. n_slot] (shared memory), and the lengths into lens
-// when given, by the calling warp; the caller synchronises.
+// empty slot, into pre[0 .. n_slot] (shared memory), and when lens is given the
+// lengths and, behind them, the number of slots that are not empty, by the
+// calling warp; the caller synchronises.
 __device__ __forceinline__ void kv4_prefix(const Kv4Layer &l, int n_slot, int unit, int extra, int mult, int *pre,
                                            int *lens) {
   const int lane = threadIdx.x & 31;
-  int base = 0;
+  int base = 0, live = 0;
   for (int b0 = 0; b0 < n_slot; b0 += 32) {
     const int b = b0 + lane;
     const int n = b < n_slot ? kv4_len(l, b) : 0;
     if (lens && b < n_slot) lens[b] = n;
+    live += __popc(__ballot_sync(0xffffffffu, n > 0));
     int v = n > 0 ? mult * ((n + unit - 1) / unit + extra) : 0;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -189,6 +195,7 @@ __device__ __forceinline__ void kv4_prefix(const Kv4Layer &l, int n_slot, int un
     base += __shfl_sync(0xffffffffu, v, 31);
   }
   if (lane == 0) pre[0] = 0;
+  if (lens && lane == 0) lens[n_slot] = live;
 }
 
 // the slot whose range of the prefix sums holds x (0 <= x < pre[n_slot])

@@ -31,8 +31,9 @@ namespace {
 // Work units: an item (slot, KV head, block of 8 query rows) takes one per
 // chunk of 32 positions and kItemUnits more for its queries and its end.
 constexpr int kItemUnits = 2;
-// units a warp takes at least: below it a call uses fewer warps
-constexpr int kMinUnits = 1;
+// items of at most this many units on average are not split over CTAs while
+// there are enough CTAs for them
+constexpr int kWholeUnits = 24;
 
 template <int NG, int NT>
 struct AttnSmem {
@@ -46,7 +47,7 @@ struct AttnSmem {
   static constexpr int kMl = kPart + kKv4Warps * 2 * 16;            // float2 [2 warps][8]: reference, sum
   static constexpr int kFlag = kMl + kKv4Warps * 2 * kKv4Rows * 8;
   static constexpr int kPre = kFlag + 16;                           // int [n_slot + 1]
-  static int bytes(int n_slot) { return kPre + (2 * n_slot + 1) * 4; }   // and the lengths
+  static int bytes(int n_slot) { return kPre + (2 * n_slot + 2) * 4; }   // and the lengths, and a count
 };
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -298,7 +299,12 @@ __global__ void __launch_bounds__(kKv4Threads, kKv4CtasPerSm)
   if (warp == 0) kv4_prefix(a.l, a.n_slot, kKv4Chunk, kItemUnits, a.n_kv * a.nrb, pre, lens);
   __syncthreads();
   const int total = pre[a.n_slot], cta = blockIdx.x;
-  const int ctas = max(1, min((int)gridDim.x, total / (kKv4Warps * kMinUnits)));
+  // One unit per warp, except that short items (a CTA's warps take a unit in
+  // about 1.2 us, and rows shared by CTAs cost 3 us more) get a CTA each.
+  const int items = lens[a.n_slot] * a.n_kv * a.nrb;
+  const int ctas = items <= (int)gridDim.x && total <= items * kWholeUnits
+                       ? max(1, items)
+                       : max(1, min((int)gridDim.x, total / kKv4Warps));
   const Split by_cta(total, ctas);   // and each CTA's part is split over its warps the same way
   const int u0 = by_cta.start(cta), u1 = by_cta.start(cta + 1);
   const int x0 = u0 + (u1 - u0) * warp / kKv4Warps, x1 = u0 + (u1 - u0) * (warp + 1) / kKv4Warps;
@@ -343,6 +349,7 @@ __global__ void __launch_bounds__(kKv4Threads, kKv4CtasPerSm)
   uint32_t phase = 0;
   bool primed = false, early = false;
   float *early_part = a.warp_part + ((int64_t)cta * kKv4Warps + warp) * kKv4Rows * HD + lane;
+  const int vunit_off = kv4_vunit(0, r, c);
   uint32_t magic = 0x64006400u;
   asm volatile("" : "+r"(magic));
 #pragma unroll 1
@@ -610,7 +617,7 @@ __global__ void __launch_bounds__(kKv4Threads, kKv4CtasPerSm)
       const uint32_t odd = (r & 1) ? 0xffffffffu : 0u;
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
-        const uint4 vw = *reinterpret_cast<const uint4 *>(st + kv4_v_off(NG) + g * 512 + lane * 16);
+        const uint4 vw = *reinterpret_cast<const uint4 *>(st + kv4_v_off(NG) + g * 512 + vunit_off);
         uint32_t u[4][4];
         code_pairs(vw.x, magic, u[0]);
         code_pairs(vw.y, magic, u[1]);
