@@ -559,8 +559,9 @@ __global__ void __launch_bounds__(THREADS, THREADS >= 1024 ? 1 : 3) k_kv4_select
   const int32_t *ids = a.src.ids + bh * a.src.cap;
   const float *wt = a.src.weights + bh * a.src.cap;
   int32_t *src_of = a.src_of + bh * a.src.cap, *movers = a.movers + bh * a.src.cap;
-  __syncthreads();
-  if (tid == 0) {                 // the last of the slot's CTAs to have read the length moves it
+  auto arrive = [&]() {           // the last of the slot's CTAs to have read the length moves it
+    __syncthreads();
+    if (tid != 0) return;
     if (h == 0 && rank == 0) a.n_old[b] = n;
     __threadfence();
     const unsigned ctas = gridDim.x * gridDim.y;
@@ -568,25 +569,34 @@ __global__ void __launch_bounds__(THREADS, THREADS >= 1024 ? 1 : 3) k_kv4_select
       a.dst.len[b] = min(n, m);
       a.dst.seen[b] = seen;
     }
-  }
+  };
   // (uniform over the cluster)
   if (n > m) {
     const int base = rank * THREADS * K + warp * 32 * K + lane;   // this lane's entries: base + 32 k
     uint32_t key[K], loose = 0, lo = 0xffffffffu, hi = 0, stay = 0;
+    constexpr int LOADS = K < 16 ? K : 16;        // in flight at once
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const int i = base + 32 * k;
-      key[k] = 0;
-      if (i < n) {
-        const int id = ids[i];
-        const uint32_t u = __float_as_uint(wt[i]);
-        key[k] = (u & 0x80000000u) ? ~u : (u | 0x80000000u);
-        if (id < a.n_sink || (int64_t)id >= (int64_t)seen - a.n_recent) {
+    for (int k0 = 0; k0 < K; k0 += LOADS) {
+      int id[LOADS];
+      float w[LOADS];
+#pragma unroll
+      for (int k = 0; k < LOADS; ++k) {
+        const int i = min(base + 32 * (k0 + k), n - 1);
+        id[k] = ids[i];
+        w[k] = wt[i];
+      }
+      if (k0 == 0) arrive();
+#pragma unroll
+      for (int k = 0; k < LOADS; ++k) {
+        const uint32_t u = __float_as_uint(w[k]);
+        key[k0 + k] = (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+        if (base + 32 * (k0 + k) >= n) continue;
+        if (id[k] < a.n_sink || (int64_t)id[k] >= (int64_t)seen - a.n_recent) {
           ++stay;
         } else {
-          loose |= 1u << k;
-          lo = min(lo, key[k]);
-          hi = max(hi, key[k]);
+          loose |= 1u << (k0 + k);
+          lo = min(lo, key[k0 + k]);
+          hi = max(hi, key[k0 + k]);
         }
       }
     }
@@ -756,6 +766,8 @@ __global__ void __launch_bounds__(THREADS, THREADS >= 1024 ? 1 : 3) k_kv4_select
       hole_at += __popc(vote);
     }
     if (CL > 1) cluster.sync();   // no CTA leaves while a peer may read its shared memory
+  } else {
+    arrive();
   }
 }
 
