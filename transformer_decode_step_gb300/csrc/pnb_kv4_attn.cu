@@ -524,23 +524,26 @@ __global__ void __launch_bounds__(kKv4Threads, kKv4CtasPerSm)
       }
       // the largest V scale of the chunk (finite, inside the sequence) bounds
       // what the fp16 products can reach
-      uint32_t hmax = 0;
+      uint32_t hmax;
       {
         constexpr int kWords = 16 * NG, kPer = (kWords + 31) / 32;
+        uint32_t w[kPer];
+        lds_words<kPer>(st + kv4_vscale_off(NG) + (lane * kPer % kWords) * 4, w);
+        if (tail) {
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-          const int wi = lane * kPer + i;
-          if (wi < kWords) {
-            uint32_t w = *reinterpret_cast<const uint32_t *>(st + kv4_vscale_off(NG) + wi * 4);
-            if (tail) {
-              const int p = p0 + 2 * (wi / NG);
-              if (p >= len) w = 0;
-              else if (p + 1 >= len) w &= 0xffffu;
-            }
-            hmax = max(hmax, finite_half_max(w));
+          for (int i = 0; i < kPer; ++i) {
+            const int p = p0 + 2 * ((lane * kPer + i) % kWords / NG);
+            w[i] &= p >= len ? 0u : (p + 1 >= len ? 0xffffu : 0xffffffffu);
           }
         }
-        hmax = __reduce_max_sync(0xffffffffu, hmax);
+        const uint32_t both = kPer == 2 ? as_word(__hmax2(as_half2(w[0]), as_half2(w[kPer - 1]))) : w[0];
+        hmax = __reduce_max_sync(0xffffffffu, max(both & 0xffffu, both >> 16));
+        if (hmax >= 0x7c00u) {   // a block of NaN: only the finite scales count
+          hmax = 0;
+#pragma unroll
+          for (int i = 0; i < kPer; ++i) hmax = max(hmax, finite_half_max(w[i]));
+          hmax = __reduce_max_sync(0xffffffffu, hmax);
+        }
       }
       if (tail) {
 #pragma unroll
@@ -557,10 +560,7 @@ __global__ void __launch_bounds__(kKv4Threads, kKv4CtasPerSm)
 #pragma unroll
           for (int t = 0; t < 4; ++t) score[k][p0 + 8 * t] = s[t][k] * rs[k];
         }
-        xm[k] = fmaxf(fmaxf(s[0][k], s[1][k]), fmaxf(s[2][k], s[3][k]));
-        xm[k] = fmaxf(xm[k], __shfl_xor_sync(0xffffffffu, xm[k], 4));
-        xm[k] = fmaxf(xm[k], __shfl_xor_sync(0xffffffffu, xm[k], 8));
-        xm[k] = fmaxf(xm[k], __shfl_xor_sync(0xffffffffu, xm[k], 16)) * rs[k];
+        xm[k] = fmaxf(fmaxf(s[0][k], s[1][k]), fmaxf(s[2][k], s[3][k])) * rs[k];
         move |= xm[k] > m[k] + 4.f;
       }
       const int evc = (int)(hmax >> 10) - 14;
@@ -572,6 +572,9 @@ __global__ void __launch_bounds__(kKv4Threads, kKv4CtasPerSm)
         ev = max(ev, evc);
 #pragma unroll
         for (int k = 0; k < RL; ++k) {
+          xm[k] = fmaxf(xm[k], __shfl_xor_sync(0xffffffffu, xm[k], 4));
+          xm[k] = fmaxf(xm[k], __shfl_xor_sync(0xffffffffu, xm[k], 8));
+          xm[k] = fmaxf(xm[k], __shfl_xor_sync(0xffffffffu, xm[k], 16));
           const float mn = fmaxf(m[k], xm[k]);
           const float nref = (mn == -INFINITY ? 0.f : mn) - 10.f + (float)ev;
           const float al = m[k] == -INFINITY ? 0.f : ex2(ref[k] - nref);
