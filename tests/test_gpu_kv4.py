@@ -251,6 +251,68 @@ def test_quantiser_many_values():
     check_content(c, ref)
 
 
+@pytest.mark.parametrize("hd", [32, 128])
+def test_quantiser_bf16_ties(hd):
+    """bf16 quotients that are half an integer exactly (scales that are powers of two and seven
+    times them), and every bf16 magnitude against a fixed scale."""
+    n = 1 << 10
+    g = torch.Generator(device="cuda")
+    g.manual_seed(6)
+    e = torch.randint(-12, 9, (1, n, 2, hd // 32, 1), generator=g, device="cuda").float()
+    d = torch.exp2(e) * torch.where(torch.rand(e.shape, generator=g, device="cuda") < 0.5, 1.0, 1.25)
+    x = torch.randint(-13, 14, (1, n, 2, hd // 32, 32), generator=g, device="cuda").float() * 0.5 * d
+    x[..., 0:1] = 7 * d
+    ties = x.to(BF16)
+    assert torch.equal(ties.float(), x)      # halves of the scale are bf16 numbers
+    # magnitudes from 2^-32 up to 7, all bf16 numbers among them, in blocks whose largest is 7
+    every = torch.arange(0x2f80, 0x40e0, dtype=torch.int16, device="cuda").view(BF16)
+    blocks = n * 2 * (hd // 32)
+    y = torch.full((blocks, 32), 7.0, dtype=BF16, device="cuda")
+    at = torch.arange(blocks * 31, device="cuda") % every.numel()
+    y[:, 1:] = every[at].view(blocks, 31)
+    c, ref = make(1, 2, 2, hd, n), Ref(1, 2, 2, hd, n)
+    v = y.reshape(1, n, 2, hd)
+    c.append(0, ties.reshape(1, n, 2, hd), v)
+    ref.append(ties.reshape(1, n, 2, hd), v)
+    check_content(c, ref)
+    c.reset()
+    c.append(0, -v, v * -0.5)                # the other sign, and a scale of one half
+    ref = Ref(1, 2, 2, hd, n)
+    ref.append(-v, v * -0.5)
+    check_content(c, ref)
+
+
+@pytest.mark.parametrize("n_slot,n_kv,hd,T", [(3, 2, 128, 8), (300, 4, 128, 8), (300, 4, 128, 3), (5, 40, 32, 2),
+                                              (2, 1, 64, 16), (2, 1, 64, 17), (1, 64, 128, 1), (4, 3, 128, 9)])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_append_and_read_forms(n_slot, n_kv, hd, T, dtype):
+    """The one-CTA-per-slot and the chunked forms, from starts inside and at the ends of chunks, with
+    neighbouring entries kept, and reads that begin inside, at and behind a slot's end."""
+    cap = 96
+    c, ref = make(n_slot, n_kv, n_kv, hd, cap), Ref(n_slot, n_kv, n_kv, hd, cap)
+    lens = [(29 + 13 * b) % 64 for b in range(n_slot)]
+    k, v = rows((n_slot, 64, n_kv, hd), 300, dtype), rows((n_slot, 64, n_kv, hd), 301, dtype)
+    c.append(0, k, v, n_new=i32(lens))
+    ref.append(k, v, lens)
+    n = [T - b % 2 for b in range(n_slot)]
+    start = [max(0, m - b % 4) for b, m in enumerate(lens)]
+    k, v = rows((n_slot, T, n_kv, hd), 302, dtype), rows((n_slot, T, n_kv, hd), 303, dtype)
+    c.append(0, k, v, n_new=i32(n), start=i32(start))
+    ref.append(k, v, n, start)
+    check_content(c, ref)
+    assert c.device_error() == 0
+    first = [(m + b % 3 - 1) if b % 5 else (-1, cap, cap + 40, 1 << 30)[b // 5 % 4] for b, m in enumerate(start)]
+    yk, yv = torch.full_like(k, 9.0), torch.full_like(v, 9.0)
+    c.read(0, yk, yv, first=i32(first))
+    for b, f in enumerate(first):
+        for got, want in ((yk, ref.k), (yv, ref.v)):
+            w = torch.zeros((T, n_kv, hd), dtype=torch.float64, device="cuda")
+            m = min(T, ref.len[b] - f) if f >= 0 else 0
+            if m > 0:
+                w[:m] = want[b, :, f:f + m].transpose(0, 1)
+            assert torch.equal(got[b], w.to(dtype))
+
+
 def test_append_reads_strided_rows():
     """K and V inside a fused QKV projection, and in a state's [head][position][hd] cache layout."""
     B, T, H, Hkv, hd = 2, 9, 4, 2, 64
@@ -358,6 +420,25 @@ def test_attention_split_over_many_ctas(hd, n_kv, G, B, n):
             assert torch.equal(w[i, :, :m], c.weights(0)[i, :, :m])
 
 
+@pytest.mark.parametrize("B,n_kv,G,hd,lo,hi", [
+    (1024, 1, 1, 32, 0, 40),       # the most slots
+    (1024, 2, 4, 128, 5, 5),       # more items than CTAs, all alike
+    (3, 4, 2, 128, 99, 99),        # items of equal, short length: a CTA each
+    (5, 3, 8, 64, 1, 300),         # ragged and short
+    (2, 64, 1, 128, 700, 1000),
+])
+def test_attention_work_splits(B, n_kv, G, hd, lo, hi):
+    cap = -(-hi // 32) * 32
+    c, ref = make(B, n_kv * G, n_kv, hd, cap, track=1), Ref(B, n_kv * G, n_kv, hd, cap)
+    lens = [lo + (37 * b) % (hi - lo + 1) for b in range(B)]
+    k, v = rows((B, hi, n_kv, hd), 310, BF16, 1.5), rows((B, hi, n_kv, hd), 311, BF16)
+    c.append(0, k, v, n_new=i32(lens))
+    ref.append(k, v, lens)
+    for dtype in (F32, BF16):
+        check_attention(c, ref, rows((B, 1, n_kv * G, hd), 312, dtype, 2.0), decay=0.0)
+    assert c.device_error() == 0
+
+
 def test_extreme_values():
     """A score far above the others late in the sequence, V scales that grow by 2^20 along it
     (the fp16 products' reference moves), large and tiny queries."""
@@ -407,6 +488,30 @@ def test_non_finite_rows_stay_where_they_are():
     c.append(0, k, v)
     ref.append(k, v)
     check_attention(c, ref, q)
+
+
+@pytest.mark.parametrize("n_kv,G,hd,T", [(2, 4, 128, 1), (2, 8, 64, 1), (4, 1, 32, 1), (1, 4, 128, 4)])
+def test_attention_is_as_exact_as_plain_fp32(n_kv, G, hd, T):
+    """fp32 outputs and weights are no further from the 64-bit result than a plain fp32 computation on
+    the same held values is (both errors are random sums: twice the norm, plus one rounding)."""
+    B, n = 4, 1500
+    c, ref = make(B, n_kv * G, n_kv, hd, 1504, track=T), Ref(B, n_kv * G, n_kv, hd, 1504)
+    k, v = rows((B, n, n_kv, hd), 330, BF16), rows((B, n, n_kv, hd), 331, BF16)
+    c.append(0, k, v)
+    ref.append(k, v)
+    q = rows((B, T, n_kv * G, hd), 332, F32, 1.5)
+    out = check_attention(c, ref, q, decay=0.0)
+    want = ref.attention(q)[0]
+    kk, vv = ref.k[:, :, :n].float(), ref.v[:, :, :n].float()
+    qq = q.view(B, T, n_kv, G, hd).permute(0, 2, 1, 3, 4)
+    x = torch.einsum("bhtgd,bhnd->bhtgn", qq, kk) * hd ** -0.5
+    seen = torch.arange(n, device="cuda") < torch.arange(n - T + 1, n + 1, device="cuda")[:, None, None]
+    p = torch.softmax(torch.where(seen, x, -torch.inf), -1)
+    plain = torch.einsum("bhtgn,bhnd->bhtgd", p, vv).permute(0, 2, 1, 3, 4).reshape(out.shape)
+    norm = lambda a: float(a.double().norm())
+    assert norm(out - want) <= 2 * norm(plain - want) + 2.0 ** -23 * norm(want)
+    w = ref.w[:, :, :n]
+    assert norm(c.weights(0)[:, :, :n] - w) <= 2 * norm(p.sum((2, 3)) - w) + 2.0 ** -23 * norm(w)
 
 
 def test_attention_strided_rows_and_output_over_queries():
@@ -485,7 +590,26 @@ def test_evict(hd, budget, sink, recent, tie):
             assert torch.equal(d.weights(0)[b, :, :n].double(), ref.w[b, :, :n])
 
 
-@pytest.mark.parametrize("cap,n,budget", [(4096, 4096, 1000), (8192, 5000, 4999), (20000, 19999, 7000),
+def test_evict_between_layers_and_equal_weights():
+    """Into another layer of the same cache; all weights zero: the first entries stay."""
+    c, ref = make(2, 2, 2, 64, 128, n_layer=2), Ref(2, 2, 2, 64, 128)
+    k, v = rows((2, 100, 2, 64), 320), rows((2, 100, 2, 64), 321)
+    c.append(0, k, v, n_new=i32([100, 70]))
+    ref.append(k, v, [100, 70])
+    c.evict(0, 64, n_sink=2, n_recent=8, dst_layer=1)
+    check_content(c, ref, layer=0)
+    ref.evict(64, 2, 8)
+    check_content(c, ref, layer=1)
+    want = list(range(56)) + list(range(92, 100))
+    assert sorted(c.ids(1)[0, 1, :64].tolist()) == want
+    # appending goes on behind, with the ids that follow
+    c.append(1, k[:, :3], v[:, :3])
+    ref.append(k[:, :3], v[:, :3])
+    check_content(c, ref, layer=1)
+    assert c.ids(1)[0, 0, 64:67].tolist() == [100, 101, 102]
+
+
+@pytest.mark.parametrize("cap,n,budget", [(1024, 1000, 999), (1056, 1056, 500), (2048, 2048, 31), (4096, 4096, 1000), (8192, 5000, 4999), (20000, 19999, 7000),
                                           (40000, 39001, 20000), (140000, 139999, 33)])
 def test_evict_long(cap, n, budget):
     """Capacities of one CTA, of clusters, and of the larger forms; weights exactly alike in places."""

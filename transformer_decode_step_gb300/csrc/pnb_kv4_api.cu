@@ -39,7 +39,7 @@ int check_config(const pnb_kvq_config &c) {
       c.n_kv_head > 1024 || c.n_layer > 4096 || c.cap > kKv4MaxCap)
     return PNB_E_UNSUPPORTED;
   // the flat list of work chunks is indexed with 32 bits
-  const int64_t chunks = (int64_t)c.n_slot * c.n_kv_head * (c.cap / kKv4Chunk + 1);
+  const int64_t chunks = (int64_t)c.n_slot * c.n_kv_head * (c.cap / kKv4Chunk + 2);
   if (chunks * (kKv4MaxRows / 4) >= (int64_t)1 << 31) return PNB_E_UNSUPPORTED;
   return PNB_OK;
 }

@@ -791,10 +791,11 @@ __global__ void __launch_bounds__(kKv4Threads, kKv4CtasPerSm)
     if (tid ? at_back : at_front) {
       c0 = by_cta.part_of(it.first);
       n = by_cta.part_of(it.first + it.nch - 1) - c0 + 1;
-      __threadfence();             // the CTA's partial rows, ordered by the barrier before it
-      if (atomicAdd(a.counter + c0, 1u) == (unsigned)(n - 1)) a.counter[c0] = 0;
+      // releases the CTA's partial rows (ordered by the barrier before), acquires the others'
+      unsigned seen;
+      asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(seen) : "l"(a.counter + c0) : "memory");
+      if (seen == (unsigned)(n - 1)) a.counter[c0] = 0;
       else n = 0;
-      __threadfence();
     }
     sflag[2 * tid] = n;
     sflag[2 * tid + 1] = c0;
@@ -867,16 +868,28 @@ __global__ void __launch_bounds__(kWeightThreads) k_kv4_weights(const __grid_con
     const int64_t bh = (int64_t)b * a.n_kv + h;
     const float *x = a.scores + bh * a.rows * a.l.cap + p, *lse = a.lse + bh * a.rows;
     float w[4] = {};
-#pragma unroll 4
-    for (int i = 0; i < a.rows; ++i) {
-      const float4 v = *reinterpret_cast<const float4 *>(x + (int64_t)i * a.l.cap);
-      const float z = lse[i];
-      w[0] += ex2(v.x - z); w[1] += ex2(v.y - z); w[2] += ex2(v.z - z); w[3] += ex2(v.w - z);
-    }
     float *dst = a.l.weights + bh * a.l.cap + p;
+    float4 old = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (a.decay > 0.f) old = *reinterpret_cast<const float4 *>(dst);
+    for (int i0 = 0; i0 < a.rows; i0 += 8) {     // eight rows' loads in flight
+      float4 v[8];
+      float z[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int row = min(i0 + i, a.rows - 1);
+        v[i] = *reinterpret_cast<const float4 *>(x + (int64_t)row * a.l.cap);
+        z[i] = i0 + i < a.rows ? lse[row] : INFINITY;
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        w[0] += ex2(v[i].x - z[i]); w[1] += ex2(v[i].y - z[i]);
+        w[2] += ex2(v[i].z - z[i]); w[3] += ex2(v[i].w - z[i]);
+      }
+    }
+    const float held[4] = {old.x, old.y, old.z, old.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      if (p + i < len) dst[i] = a.decay > 0.f ? fmaf(a.decay, dst[i], w[i]) : w[i];
+      if (p + i < len) dst[i] = a.decay > 0.f ? fmaf(a.decay, held[i], w[i]) : w[i];
   }
 }
 
