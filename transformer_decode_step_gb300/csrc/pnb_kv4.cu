@@ -263,7 +263,7 @@ __global__ void __launch_bounds__(kStepThreads) k_kv4_append_step(const __grid_c
   if (tid == 0) r.commit(a, b);
 }
 
-// Many tokens: CTAs of kAppendChunks chunks of one (slot, KV head).  128
+// Many tokens: CTAs of up to kAppendChunks chunks of one (slot, KV head).  128
 // threads quantise a chunk's new K rows, 128 its V rows, 16 bytes of a row (32
 // for fp32) per thread and pass, the next chunk's rows on their way meanwhile.
 // K words go straight to their place; V words hold 8 positions of one dim, so
@@ -292,8 +292,8 @@ __global__ void __launch_bounds__(kAppendThreads) k_kv4_append(const __grid_cons
   const bool is_v = tid >= 128;
   const int th = tid & 127, sub = th % TPR, j = sub >> 2, cc = sub & 3, r0 = th / TPR;
   const Kv4Rows &rows = is_v ? a.v : a.k;
-  const int ch0 = rg.start / kKv4Chunk + (int)blockIdx.x * kAppendChunks;
-  const int ch1 = min(ch0 + kAppendChunks, (rg.end + kKv4Chunk - 1) / kKv4Chunk);
+  const int ch0 = rg.start / kKv4Chunk + (int)blockIdx.x * a.group;
+  const int ch1 = min(ch0 + a.group, (rg.end + kKv4Chunk - 1) / kKv4Chunk);
   const T *src = static_cast<const T *>(rows.p) + b * rows.slot + h * rows.head + sub * 8;
   Raw8<T> raw[PASSES];
   auto fetch = [&](int ch) {
@@ -452,7 +452,7 @@ __global__ void __launch_bounds__(256) k_kv4_read_step(const __grid_constant__ K
   store8<T>(o.p, b * o.slot + t * o.token + h * o.head + sub * 8, x);
 }
 
-// Many tokens: CTAs of kReadChunks chunks of one (slot, KV head), which one
+// Many tokens: CTAs of up to kReadChunks chunks of one (slot, KV head), which one
 // bulk copy brings into shared memory; then 8 dims of a K position per thread,
 // and 8 x 8 nibbles of V (8 positions, 8 dims) per thread.  Bound by the
 // values' bytes.
@@ -472,9 +472,9 @@ __global__ void __launch_bounds__(kReadThreads) k_kv4_read(const __grid_constant
   const int len = kv4_len(a.l, b);
   int first = a.first ? a.first[b] : 0;
   first = first < 0 || first > a.l.cap ? a.l.cap : first;   // outside the cache: nothing but zeros
-  const int ch0 = first / kKv4Chunk + (int)blockIdx.x * kReadChunks;
+  const int ch0 = first / kKv4Chunk + (int)blockIdx.x * a.group;
   const int64_t p0 = (int64_t)ch0 * kKv4Chunk, lo = max((int64_t)first, p0);
-  const int64_t hi = min((int64_t)first + a.T, p0 + kReadChunks * kKv4Chunk);
+  const int64_t hi = min((int64_t)first + a.T, p0 + a.group * kKv4Chunk);
   if (lo >= hi) return;
   // chunks that hold entries to be read
   const int held = (int)max((int64_t)0, (min(hi, (int64_t)len) - p0 + kKv4Chunk - 1) / kKv4Chunk);
@@ -495,7 +495,7 @@ __global__ void __launch_bounds__(kReadThreads) k_kv4_read(const __grid_constant
   // every store of a warp is contiguous
   constexpr int HALF = sizeof(T) == 4 ? 2 : 1, LPR = TPR * HALF;
   const int64_t slot_k = b * a.k.slot + h * a.k.head, slot_v = b * a.v.slot + h * a.v.head;
-  for (int i = tid; i < kReadChunks * kKv4Chunk * LPR; i += kReadThreads) {
+  for (int i = tid; i < a.group * kKv4Chunk * LPR; i += kReadThreads) {
     const int q = i / LPR, sub = (i % LPR) / HALF, part = i % HALF, j = sub >> 2, cc = sub & 3, p = q % kKv4Chunk;
     const int64_t pos = p0 + q;
     if (pos < lo || pos >= hi) continue;
@@ -506,7 +506,7 @@ __global__ void __launch_bounds__(kReadThreads) k_kv4_read(const __grid_constant
                 half_at(chunk + kv4_kscale_off(NG) + kv4_kscale(NG, p, j)), x);
     store16<T>(a.k.p, slot_k + (pos - first) * a.k.token + sub * 8, part, x);
   }
-  for (int i = tid; i < kReadChunks * 4 * LPR; i += kReadThreads) {
+  for (int i = tid; i < a.group * 4 * LPR; i += kReadThreads) {
     const int sub = (i % LPR) / HALF, part = i % HALF, j = sub >> 2, cc = sub & 3, c = (i / LPR) & 3, q = i / (4 * LPR);
     const uint8_t *chunk = sm + q * CH;
     uint32_t w[8];
@@ -911,8 +911,21 @@ __global__ void k_kv4_reset(int32_t *len, int32_t *seen, int64_t stride, int n_l
 // chunks that T rows from any position touch at most, in groups
 int chunk_groups(int T, int group) { return ((T + kKv4Chunk - 2) / kKv4Chunk + group) / group; }
 
+// Chunks per CTA: up to `most`, fewer while all CTAs fit the GPU at once (four
+// on each of 152 SMs).  bf16 append / fp32 read, us, always four chunks against
+// this rule and against always one: 1 sequence x 8 heads x 256 tokens 6.1 / 5.9,
+// 3.1 / 3.0, 3.0 / 3.1; 4 x 8 x 1031 7.8 / 8.4, 6.6 / 8.1, 7.2 / 8.4; 1 x 32 x
+// 8191 35.4 / 49.5, 35.3 / 49.6, 43.6 / 53.8.
+constexpr int kResidentCtas = 608;
+
+int chunk_group(int T, int n_kv, int n_slot, int most) {
+  const int64_t chunks = (int64_t)chunk_groups(T, 1) * n_kv * n_slot;
+  const int64_t per = (chunks + kResidentCtas - 1) / kResidentCtas;
+  return (int)(per < 1 ? 1 : per > most ? most : per);
+}
+
 template <int NG, typename T>
-cudaError_t run_append(const Kv4AppendArgs &a, cudaStream_t st) {
+cudaError_t run_append(Kv4AppendArgs a, cudaStream_t st) {
   // One CTA per slot (2.4 us and 0.6 for every 2048 values of a slot's rows)
   // against one per chunk and head (3.2 us while all are resident, 12 us for
   // 2048 of them); bf16, head_dim 128, us, step form first:
@@ -921,12 +934,13 @@ cudaError_t run_append(const Kv4AppendArgs &a, cudaStream_t st) {
   const int64_t values = (int64_t)a.T * a.n_kv * 32 * NG;
   if (values <= 2048 || (values <= 8192 && (int64_t)a.n_slot * a.n_kv > 1024))
     return kv4_launch(k_kv4_append_step<NG, T>, dim3(a.n_slot), dim3(kStepThreads), (size_t)values / 2, 1, st, a);
-  const dim3 grid(chunk_groups(a.T, kAppendChunks), a.n_kv, a.n_slot);
+  a.group = chunk_group(a.T, a.n_kv, a.n_slot, kAppendChunks);
+  const dim3 grid(chunk_groups(a.T, a.group), a.n_kv, a.n_slot);
   return kv4_launch(k_kv4_append<NG, T>, grid, dim3(kAppendThreads), 0, 1, st, a);
 }
 
 template <int NG, typename T>
-cudaError_t run_read(const Kv4ReadArgs &a, cudaStream_t st) {
+cudaError_t run_read(Kv4ReadArgs a, cudaStream_t st) {
   // few rows per chunk: straight from the cache, or through whole chunks (64
   // slots x 8 heads at head_dim 128, fp32, us: 1 token 2.3, 4.8; 16 tokens 4.6, 6.0;
   // 32 tokens 7.0 both)
@@ -934,7 +948,8 @@ cudaError_t run_read(const Kv4ReadArgs &a, cudaStream_t st) {
     const int64_t threads = (int64_t)a.n_slot * a.T * a.n_kv * 8 * NG;
     return kv4_launch(k_kv4_read_step<NG, T>, dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, 1, st, a);
   }
-  const dim3 grid(chunk_groups(a.T, kReadChunks), a.n_kv, a.n_slot);
+  a.group = chunk_group(a.T, a.n_kv, a.n_slot, kReadChunks);
+  const dim3 grid(chunk_groups(a.T, a.group), a.n_kv, a.n_slot);
   return kv4_launch(k_kv4_read<NG, T>, grid, dim3(kReadThreads), 0, 1, st, a);
 }
 

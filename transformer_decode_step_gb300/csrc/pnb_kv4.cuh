@@ -86,6 +86,7 @@ struct Kv4AppendArgs {
   Kv4Rows k, v;
   const int32_t *n_new, *start;   // [n_slot] or NULL
   int32_t n_slot, n_kv, T;
+  int32_t group;                  // chunks per CTA (set by the launcher)
   uint32_t *arrive;               // [n_slot]
   int32_t *err;
 };
@@ -95,6 +96,7 @@ struct Kv4ReadArgs {
   Kv4Rows k, v;
   const int32_t *first;           // [n_slot] or NULL
   int32_t n_slot, n_kv, T;
+  int32_t group;                  // chunks per CTA (set by the launcher)
   int32_t *err;
 };
 
