@@ -553,6 +553,7 @@ __global__ void __launch_bounds__(THREADS, THREADS >= 1024 ? 1 : 3) k_kv4_select
     if (CL > 1) cluster.sync();
     else __syncthreads();
   };
+  pdl_trigger();                  // the moves' CTAs may settle beside these, and wait
   pdl_wait();
   const int n = kv4_len(a.src, b), seen = a.src.seen[b], m = a.budget;
   const int64_t bh = (int64_t)b * a.n_kv + h;
@@ -819,14 +820,22 @@ __global__ void __launch_bounds__(kMoveThreads, 8) k_kv4_move(const __grid_const
     if ((tid & 31) == 0) moved_chunk[tid >> 5] = any;
   }
   __syncthreads();
-  // K rows, NG 16-byte vectors each, ids and weights; all loads before the stores
+  // K rows, NG 16-byte vectors each, and a position per thread its scales, id and
+  // weight; all loads before the stores
   {
     const bool mine = my_src >= 0 && !(a.in_place && my_src == p0 + tid);
     int32_t id = 0;
     float weight = 0.f;
+    uint16_t ks[NG] = {}, vs[NG] = {};
     if (mine) {
       id = a.src.ids[bh * a.src.cap + my_src];
       weight = a.src.weights[bh * a.src.cap + my_src];
+      const uint8_t *f = from + (int64_t)(my_src / kKv4Chunk) * CH;
+#pragma unroll
+      for (int j = 0; j < NG; ++j) {
+        ks[j] = *reinterpret_cast<const uint16_t *>(f + kv4_kscale_off(NG) + kv4_kscale(NG, my_src % kKv4Chunk, j));
+        vs[j] = *reinterpret_cast<const uint16_t *>(f + kv4_vscale_off(NG) + kv4_vscale(NG, my_src % kKv4Chunk, j));
+      }
     }
     uint4 v[NG];
 #pragma unroll
@@ -844,19 +853,12 @@ __global__ void __launch_bounds__(kMoveThreads, 8) k_kv4_move(const __grid_const
     if (mine) {
       a.dst.ids[bh * a.dst.cap + p0 + tid] = id;
       a.dst.weights[bh * a.dst.cap + p0 + tid] = weight;
-    }
-  }
-  // both kinds of scales, a position per thread
-  if (my_src >= 0 && !(a.in_place && my_src == p0 + tid)) {
-    const int s = my_src, p = tid % kKv4Chunk, q = s % kKv4Chunk;
-    const uint8_t *f = from + (int64_t)(s / kKv4Chunk) * CH;
-    uint8_t *t = to + (tid / kKv4Chunk) * CH;
+      uint8_t *t = to + (tid / kKv4Chunk) * CH;
 #pragma unroll
-    for (int j = 0; j < NG; ++j) {
-      *reinterpret_cast<uint16_t *>(t + kv4_kscale_off(NG) + kv4_kscale(NG, p, j)) =
-          *reinterpret_cast<const uint16_t *>(f + kv4_kscale_off(NG) + kv4_kscale(NG, q, j));
-      *reinterpret_cast<uint16_t *>(t + kv4_vscale_off(NG) + kv4_vscale(NG, p, j)) =
-          *reinterpret_cast<const uint16_t *>(f + kv4_vscale_off(NG) + kv4_vscale(NG, q, j));
+      for (int j = 0; j < NG; ++j) {
+        *reinterpret_cast<uint16_t *>(t + kv4_kscale_off(NG) + kv4_kscale(NG, tid % kKv4Chunk, j)) = ks[j];
+        *reinterpret_cast<uint16_t *>(t + kv4_vscale_off(NG) + kv4_vscale(NG, tid % kKv4Chunk, j)) = vs[j];
+      }
     }
   }
   auto live = [&](int k) { return p0 + k * kKv4Chunk < out && (!a.in_place || moved_chunk[k]); };
