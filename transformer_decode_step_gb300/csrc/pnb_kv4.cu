@@ -772,7 +772,7 @@ __global__ void __launch_bounds__(THREADS, THREADS >= 1024 ? 1 : 3) k_kv4_select
   }
 }
 
-constexpr int kMoveThreads = 128, kMoveChunks = 4;
+constexpr int kMoveThreads = 128, kMoveChunks = 2;
 
 // The moves, one CTA per (kMoveChunks destination chunks, KV head, slot).
 // Sources of moves lie at or behind the budget and destinations below it, so
@@ -782,7 +782,7 @@ constexpr int kMoveThreads = 128, kMoveChunks = 4;
 template <int NG>
 __global__ void __launch_bounds__(kMoveThreads, 8) k_kv4_move(const __grid_constant__ Kv4EvictArgs a) {
   constexpr int CH = kv4_chunk_bytes(NG), POS = kMoveChunks * kKv4Chunk;
-  static_assert(POS == kMoveThreads, "a position per thread");
+  static_assert(POS <= kMoveThreads, "a position per thread");
   __shared__ int src[POS];
   __shared__ int moved_chunk[kMoveChunks];
   const int tid = threadIdx.x, h = blockIdx.y, b = blockIdx.z, p0 = blockIdx.x * POS;
@@ -792,9 +792,10 @@ __global__ void __launch_bounds__(kMoveThreads, 8) k_kv4_move(const __grid_const
   const int64_t bh = (int64_t)b * a.n_kv + h;
   const uint8_t *from = a.src.codes + bh * (a.src.cap / kKv4Chunk) * CH;
   uint8_t *to = a.dst.codes + (bh * (a.dst.cap / kKv4Chunk) + blockIdx.x * kMoveChunks) * CH;
-  // V units (J, r, c), 4 dims of 8 positions, NG per thread: those of the same
-  // place, at once unless most chunks will not be touched
-  constexpr int UNITS = 32 * NG, PER = kMoveChunks * UNITS / kMoveThreads;
+  // V units (J, r, c), 4 dims of 8 positions: those of the same place,
+  // at once unless most chunks will not be touched
+  constexpr int UNITS = 32 * NG, PER = (kMoveChunks * UNITS + kMoveThreads - 1) / kMoveThreads;
+  constexpr int VECS = (POS * NG + kMoveThreads - 1) / kMoveThreads;
   uint4 w[PER];
   auto same_place = [&](int k, int u) {   // unit u in their order in memory
     return *reinterpret_cast<const uint4 *>(from + (int64_t)(p0 / kKv4Chunk + k) * CH + kv4_v_off(NG) + u * 16);
@@ -803,11 +804,11 @@ __global__ void __launch_bounds__(kMoveThreads, 8) k_kv4_move(const __grid_const
 #pragma unroll
     for (int x = 0; x < PER; ++x) {
       const int i = x * kMoveThreads + tid, k = i / UNITS;
-      if (p0 + k * kKv4Chunk < out) w[x] = same_place(k, i % UNITS);
+      if (k < kMoveChunks && p0 + k * kKv4Chunk < out) w[x] = same_place(k, i % UNITS);
     }
   }
   int my_src = -1;
-  {
+  if (tid < POS) {
     const int p = p0 + tid;
     int s = -1;
     if (p < out) {
@@ -837,16 +838,16 @@ __global__ void __launch_bounds__(kMoveThreads, 8) k_kv4_move(const __grid_const
         vs[j] = *reinterpret_cast<const uint16_t *>(f + kv4_vscale_off(NG) + kv4_vscale(NG, my_src % kKv4Chunk, j));
       }
     }
-    uint4 v[NG];
+    uint4 v[VECS];
 #pragma unroll
-    for (int i = 0; i < NG; ++i) {
-      const int p = (i * kMoveThreads + tid) / NG, s = src[p];
+    for (int i = 0; i < VECS; ++i) {
+      const int p = (i * kMoveThreads + tid) / NG, s = p < POS ? src[p] : -1;
       if (s >= 0 && !(a.in_place && s == p0 + p))
         v[i] = reinterpret_cast<const uint4 *>(from + (int64_t)(s / kKv4Chunk) * CH + (s % kKv4Chunk) * 16 * NG)[tid % NG];
     }
 #pragma unroll
-    for (int i = 0; i < NG; ++i) {
-      const int p = (i * kMoveThreads + tid) / NG, s = src[p];
+    for (int i = 0; i < VECS; ++i) {
+      const int p = (i * kMoveThreads + tid) / NG, s = p < POS ? src[p] : -1;
       if (s >= 0 && !(a.in_place && s == p0 + p))
         reinterpret_cast<uint4 *>(to + (p / kKv4Chunk) * CH + (p % kKv4Chunk) * 16 * NG)[tid % NG] = v[i];
     }
@@ -861,7 +862,7 @@ __global__ void __launch_bounds__(kMoveThreads, 8) k_kv4_move(const __grid_const
       }
     }
   }
-  auto live = [&](int k) { return p0 + k * kKv4Chunk < out && (!a.in_place || moved_chunk[k]); };
+  auto live = [&](int k) { return k < kMoveChunks && p0 + k * kKv4Chunk < out && (!a.in_place || moved_chunk[k]); };
   if (a.in_place) {
 #pragma unroll
     for (int x = 0; x < PER; ++x) {
