@@ -41,8 +41,8 @@ struct AttnSmem {
   static constexpr int kStages = NG == 4 ? 2 : 4;
   static constexpr int kChunk = kv4_chunk_bytes(NG);
   static constexpr int kRing = kKv4Warps * kStages * kChunk;
-  static constexpr int kQ = kRing;                                  // uint2 [warps][NT][2 NG][32], NT > 1
-  static constexpr int kBars = kQ + (NT > 1 ? kKv4Warps * NT * 2 * NG * 32 * 8 : 0);
+  static constexpr int kQ = kRing;                                  // uint2 [warps][NT][2 NG][32]
+  static constexpr int kBars = kQ + kKv4Warps * NT * 2 * NG * 32 * 8;
   static constexpr int kPart = kBars + kKv4Warps * kStages * 8;     // int4 [2 warps]: item of each partial
   static constexpr int kMl = kPart + kKv4Warps * 2 * 16;            // float2 [2 warps][8]: reference, sum
   static constexpr int kFlag = kMl + kKv4Warps * 2 * kKv4Rows * 8;
@@ -368,7 +368,6 @@ __global__ void __launch_bounds__(kKv4Threads, kKv4CtasPerSm)
     // Queries: lane (r, c) holds dims 32 g + 8 c .. + 7 of its column, which are
     // its own entries of the B operand.  Scaled to a largest magnitude of 2^10 by
     // a power of two that the scores undo; FINE: split, high part in even columns.
-    uint2 qf[NT == 1 ? 2 * NG : 1];
     float rs[RL];
     {
       float scale[NT];
@@ -429,8 +428,7 @@ __global__ void __launch_bounds__(kKv4Threads, kKv4CtasPerSm)
                 w[k] = (r & 1) ? lo : w[k];
               }
             }
-            if (NT == 1) qf[g * 2 + h] = make_uint2(w[0], w[1]);
-            else qs[(nt * 2 * NG + g * 2 + h) * 32] = make_uint2(w[0], w[1]);
+            qs[(nt * 2 * NG + g * 2 + h) * 32] = make_uint2(w[0], w[1]);
           }
       }
       // the score rows' factors from the lanes of their columns
@@ -505,8 +503,8 @@ __global__ void __launch_bounds__(kKv4Threads, kKv4CtasPerSm)
           code_pairs(kw[1][g], magic, u1);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            const uint2 qa = NT == 1 ? qf[g * 2] : qs[(nt * 2 * NG + g * 2) * 32];
-            const uint2 qb = NT == 1 ? qf[g * 2 + 1] : qs[(nt * 2 * NG + g * 2 + 1) * 32];
+            const uint2 qa = qs[(nt * 2 * NG + g * 2) * 32];
+            const uint2 qb = qs[(nt * 2 * NG + g * 2 + 1) * 32];
             float d[4];
             mma_f16_new(d, u0[0], u1[0], u0[1], u1[1], qa.x, qa.y);
             mma_f16(d, u0[2], u1[2], u0[3], u1[3], qb.x, qb.y);
@@ -614,9 +612,6 @@ __global__ void __launch_bounds__(kKv4Threads, kKv4CtasPerSm)
           }
         }
       }
-      uint32_t vs[4][NG];
-#pragma unroll
-      for (int t = 0; t < 4; ++t) lds_words<NG>(st + kv4_vscale_off(NG) + (t * 4 + c) * 4 * NG, vs[t]);
       const uint32_t odd = (r & 1) ? 0xffffffffu : 0u;
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
@@ -633,7 +628,7 @@ __global__ void __launch_bounds__(kKv4Threads, kKv4CtasPerSm)
           uint32_t w[4];
 #pragma unroll
           for (int t = 0; t < 4; ++t) {
-            uint32_t dw = vs[t][g];
+            uint32_t dw = *reinterpret_cast<const uint32_t *>(st + kv4_vscale_off(NG) + (t * 4 + c) * 4 * NG + 4 * g);
             if (tail) {   // a masked position's scale may be anything: its weight is 0, not 0 times it
               const int p = p0 + 8 * t + 2 * c;
               dw &= p >= limit_col[nt] ? 0u : (p + 1 >= limit_col[nt] ? 0xffffu : 0xffffffffu);
