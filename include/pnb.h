@@ -498,6 +498,7 @@ int pnb_kvq_read(pnb_kvq *c, int32_t layer, const int32_t *first_dev, int32_t T,
    with nothing to attend to, an empty slot's among them, answers 0.
      q    [n_slot][T][n_head][head_dim], already rotated
      out  the same shape: softmax(q.k / sqrt(head_dim)) applied to V
+   Drafted tokens are attended before an eviction, which reorders entries.
    T * n_head / n_kv_head <= 64 (PNB_E_UNSUPPORTED).  q and out may differ in
    dtype; out may be q's own rows when they have the same strides and dtype.
    fp32 outputs carry about 1e-6 of relative error against exact arithmetic on

@@ -798,6 +798,13 @@ def test_refusals():
     assert code(c.evict, 0, 33, dst=make(2, 4, 2, 64, 32)) == -1
     assert code(c.evict, 0, 10, dst=pnb.Kv4Cache(1, 2, 4, 2, 64, 32, buf=c.buf)) == -1
     assert code(c.reset, 2) == -1
+    cfg = dict(n_layer=1, n_slot=1, n_head=1, n_kv_head=1, head_dim=32, cap=32)
+    assert code(pnb.Kv4Cache, **cfg, buf=torch.zeros(1 << 16, dtype=torch.uint8)) == -10   # host memory
+    dev = torch.zeros(1 << 16, dtype=torch.uint8, device="cuda")
+    assert code(pnb.Kv4Cache, **cfg, buf=dev.view(-1, 2)[:, 0]) == -1
+    assert code(pnb.Kv4Cache, **cfg, buf=dev[:1024]) == -1                # too small
+    assert code(pnb.Kv4Cache, **cfg, buf=dev[64:]) == -3                  # not 128-byte aligned
+    assert code(pnb.Kv4Cache, **{**cfg, "head_dim": 48}) == -5
     big = pnb.Kv4Cache(1, 1, 1, 1, 32, (1 << 18) + 32)
     big.reset()
     assert code(big.evict, 0, 10) == -5

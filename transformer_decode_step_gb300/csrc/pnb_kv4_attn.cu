@@ -29,7 +29,9 @@ namespace pnb {
 namespace {
 
 // Work units: an item (slot, KV head, block of 8 query rows) takes one per
-// chunk of 32 positions and kItemUnits more for its queries and its end.
+// chunk of 32 positions and kItemUnits more for its queries and its end (5
+// drafted tokens over ragged slots 16.9 us with one, 15.3 with two, 15.9 with
+// three).
 constexpr int kItemUnits = 2;
 // items of at most this many units on average are not split over CTAs while
 // there are enough CTAs for them
@@ -99,22 +101,6 @@ __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
-}
-
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-  unsigned long long d;
-  asm("add.rn.f32x2 %0, %1, %2;"
-      : "=l"(d)
-      : "l"(*reinterpret_cast<unsigned long long *>(&a)), "l"(*reinterpret_cast<unsigned long long *>(&b)));
-  return *reinterpret_cast<float2 *>(&d);
-}
-
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-  unsigned long long d;
-  asm("mul.rn.f32x2 %0, %1, %2;"
-      : "=l"(d)
-      : "l"(*reinterpret_cast<unsigned long long *>(&a)), "l"(*reinterpret_cast<unsigned long long *>(&b)));
-  return *reinterpret_cast<float2 *>(&d);
 }
 
 __device__ __forceinline__ __half2 as_half2(uint32_t w) { return *reinterpret_cast<const __half2 *>(&w); }

@@ -36,6 +36,10 @@ class Kv4Cache:
         nbytes = int(pnb_kvq_bytes(ctypes.byref(self.cfg)))
         if buf is None:
             buf = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=device or "cuda")
+        if not buf.is_cuda or buf.get_device() != torch.cuda.current_device():
+            raise PnbError(-10, f"Kv4Cache: the buffer is on {buf.device}, not on the current CUDA device")
+        if not buf.is_contiguous():
+            raise PnbError(-1, "Kv4Cache: the buffer is not contiguous")
         self.buf = buf
         h = ctypes.c_void_p()
         check(pnb_kvq_new(ctypes.byref(self.cfg), _ptr(buf), buf.numel() * buf.element_size(),
