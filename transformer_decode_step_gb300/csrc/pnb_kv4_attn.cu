@@ -40,6 +40,7 @@ constexpr int kWholeUnits = 24;
 template <int NG, int NT>
 struct AttnSmem {
   static constexpr int kHd = 32 * NG;
+  static constexpr int kPitch = kHd + 8;      // floats between partial rows: lanes (r, c) write row c, dims 8 i + r
   static constexpr int kStages = NG == 4 ? 2 : 4;
   static constexpr int kChunk = kv4_chunk_bytes(NG);
   static constexpr int kRing = kKv4Warps * kStages * kChunk;
@@ -261,11 +262,11 @@ template <int NG, bool FINE, int NT, bool TRACK>
 __global__ void __launch_bounds__(kKv4Threads, kKv4CtasPerSm)
     k_kv4_attn(const __grid_constant__ Kv4AttnArgs a) {
   using L = AttnSmem<NG, NT>;
-  constexpr int HD = L::kHd, ST = L::kStages;
+  constexpr int HD = L::kHd, ST = L::kStages, PITCH = L::kPitch;
   constexpr int RPB = FINE ? 4 : 8;           // rows per block of 8 columns
   constexpr int RPI = RPB * NT;               // rows per item
   constexpr int RL = (FINE ? 1 : 2) * NT;     // rows whose scores and outputs a lane holds
-  static_assert(RPI <= kKv4Rows, "partial rows");
+  static_assert(RPI <= kKv4Rows && 2 * RPI * PITCH * 4 <= ST * L::kChunk, "partial rows, in a warp's ring");
   extern __shared__ __align__(128) uint8_t smem[];
   int4 *spart = reinterpret_cast<int4 *>(smem + L::kPart);
   float2 *sml = reinterpret_cast<float2 *>(smem + L::kMl);
@@ -276,13 +277,16 @@ __global__ void __launch_bounds__(kKv4Threads, kKv4CtasPerSm)
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::kBars) + warp * ST;
   uint8_t *ring = smem + warp * ST * L::kChunk;
 
-  if (lane == 0) {
-    for (int s = 0; s < ST; ++s) mbar_init(bars + s, 1);
-    fence_barrier_init();
-    spart[2 * warp].x = spart[2 * warp + 1].x = -1;
-  }
   pdl_wait();
-  if (warp == 0) kv4_prefix(a.l, a.n_slot, kKv4Chunk, kItemUnits, a.n_kv * a.nrb, pre, lens);
+  if (warp == 0) {
+    kv4_prefix(a.l, a.n_slot, kKv4Chunk, kItemUnits, a.n_kv * a.nrb, pre, lens);
+  } else {                                    // meanwhile
+    if (warp == 1 && lane == 0) {
+      for (int s = 0; s < kKv4Warps * ST; ++s) mbar_init(reinterpret_cast<uint64_t *>(smem + L::kBars) + s, 1);
+      fence_barrier_init();
+    }
+    if (warp == 2 && lane < 2 * kKv4Warps) spart[lane].x = -1;
+  }
   __syncthreads();
   const int total = pre[a.n_slot], cta = blockIdx.x;
   // One unit per warp, except that short items (a CTA's warps take a unit in
@@ -671,9 +675,9 @@ __global__ void __launch_bounds__(kKv4Threads, kKv4CtasPerSm)
     } else {
       const int which = sg.c0 == 0 ? 1 : 0;    // 1: the item starts here and goes on behind
       if (lane == 0) spart[2 * warp + which] = make_int4(sg.first, sg.nch, sg.b, sg.h * a.nrb + sg.rb);
-      // the rows, rotated by 8 floats each against bank conflicts, into the
-      // warp's ring once its last chunk is used; before that to global memory
-      float *pd = x >= x1 ? reinterpret_cast<float *>(ring) + which * RPI * HD : nullptr;
+      // the rows into the warp's ring once its last chunk is used; before that to
+      // global memory
+      float *pd = x >= x1 ? reinterpret_cast<float *>(ring) + which * RPI * PITCH : nullptr;
       early |= x < x1;
 #pragma unroll
       for (int k = 0; k < RL; ++k) {
@@ -681,7 +685,7 @@ __global__ void __launch_bounds__(kKv4Threads, kKv4CtasPerSm)
         if (r == 0) sml[(2 * warp + which) * kKv4Rows + i0] = make_float2(ref[k], l[k]);
 #pragma unroll
         for (int i = 0; i < NG * 4; ++i) {
-          if (pd) pd[i0 * HD + ((8 * i + r + 8 * i0) & (HD - 1))] = out_of(k, i);
+          if (pd) pd[i0 * PITCH + r + 8 * i] = out_of(k, i);
           else early_part[(k * NG * 4 + i) * 32] = out_of(k, i);
         }
       }
@@ -693,8 +697,7 @@ __global__ void __launch_bounds__(kKv4Threads, kKv4CtasPerSm)
       const int i0 = FINE ? c + 4 * k : 2 * c + k;
 #pragma unroll
       for (int i = 0; i < NG * 4; ++i)
-        reinterpret_cast<float *>(ring)[i0 * HD + ((8 * i + r + 8 * i0) & (HD - 1))] =
-            early_part[(k * NG * 4 + i) * 32];
+        reinterpret_cast<float *>(ring)[i0 * PITCH + r + 8 * i] = early_part[(k * NG * 4 + i) * 32];
     }
   }
   __syncthreads();
@@ -740,7 +743,7 @@ __global__ void __launch_bounds__(kKv4Threads, kKv4CtasPerSm)
       if (f == 0.f) continue;
       float v[NG];
       load_vals<float, NG>(reinterpret_cast<const float *>(smem + (e >> 1) * ST * L::kChunk) +
-                               ((e & 1) * RPI + i) * HD + ((lane * NG + 8 * i) & (HD - 1)), v);
+                               ((e & 1) * RPI + i) * PITCH + lane * NG, v);
 #pragma unroll
       for (int j = 0; j < NG; ++j) os[j] = fmaf(v[j], f, os[j]);
     }
@@ -765,64 +768,70 @@ __global__ void __launch_bounds__(kKv4Threads, kKv4CtasPerSm)
     at_back = back.first + back.nch > u1 && !(at_front && back.first == front.first);
   }
   if (!at_front && !at_back) return;
-  __syncthreads();
-  if (tid < 2) {
-    const Item it = tid ? back : front;
-    int n = 0, c0 = 0;
-    if (tid ? at_back : at_front) {
+  const int slot = tid - (kKv4Threads - 32);   // lanes 0 and 1 of the last warp: front and back
+  int n = 0, c0 = 0;
+  if (slot == 0 || slot == 1) {
+    const Item it = slot ? back : front;
+    if (slot ? at_back : at_front) {
       c0 = by_cta.part_of(it.first);
       n = by_cta.part_of(it.first + it.nch - 1) - c0 + 1;
+    }
+  }
+  __syncthreads();
+  if (slot == 0 || slot == 1) {
+    if (n > 0) {
       // releases the CTA's partial rows (ordered by the barrier before), acquires the others'
       unsigned seen;
       asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(seen) : "l"(a.counter + c0) : "memory");
       if (seen == (unsigned)(n - 1)) a.counter[c0] = 0;
       else n = 0;
     }
-    sflag[2 * tid] = n;
-    sflag[2 * tid + 1] = c0;
+    sflag[2 * slot] = n;
+    sflag[2 * slot + 1] = c0;
   }
   __syncthreads();
+  // front and back at once where the warps suffice
+  constexpr bool BOTH = 2 * RPI <= kKv4Warps;
 #pragma unroll 1
-  for (int i = 0; i < 2; ++i) {
-    const int n = sflag[2 * i], c0 = sflag[2 * i + 1];
+  for (int i = BOTH ? warp / RPI : 0; i < 2; i += BOTH ? 2 : 1) {
+    n = sflag[2 * i];
+    c0 = sflag[2 * i + 1];
     const Item it = i ? back : front;
-    const int my_row = it.rb * RPI + warp;
-    if (n == 0 || warp >= RPI || my_row >= a.rows) continue;
+    const int w = BOTH ? warp % RPI : warp, my_row = it.rb * RPI + w;
+    if (n == 0 || w >= RPI || my_row >= a.rows) continue;
     // the first CTA's partial is its second one, all others' their first
-    auto at = [&](int k) { return (int64_t)(2 * (c0 + k) + (k == 0 ? 1 : 0)) * kKv4Rows + warp; };
+    auto at = [&](int k) { return (int64_t)(2 * (c0 + k) + (k == 0 ? 1 : 0)) * kKv4Rows + w; };
     auto ml_of = [&](int k) {
       return k < n ? __ldcg(reinterpret_cast<const float2 *>(a.part_ml) + at(k)) : make_float2(0.f, 0.f);
     };
-    float2 ml = ml_of(lane);               // lane k: partial k0 + k
-    float mref = ml.y != 0.f ? ml.x : -INFINITY, lsum = 0.f, os[NG] = {};
+    constexpr int AHEAD = 16;                // rows' loads in flight
+    float v[AHEAD][NG];
+    auto fetch = [&](int k0) {
+#pragma unroll
+      for (int q = 0; q < AHEAD; ++q)
+        if (k0 + q < n) ldcg_row<NG>(a.part + at(k0 + q) * HD + lane * NG, v[q]);
+    };
+    float2 ml = ml_of(lane);                 // lane k: partial k
+    fetch(0);
+    float mref = ml.y != 0.f ? ml.x : -INFINITY, lsum = 0.f, fac = 0.f, os[NG] = {};
     for (int k = lane + 32; k < n; k += 32) {
       const float2 x = ml_of(k);
       if (x.y != 0.f) mref = fmaxf(mref, x.x);
     }
     mref = warp_max(mref);
-    for (int k0 = 0; k0 < n; k0 += 32) {
-      if (k0 > 0) ml = ml_of(k0 + lane);
-      const float fac = ml.y != 0.f ? ex2(ml.x - mref) : 0.f, l = ml.y != 0.f ? ml.y * fac : 0.f;
-      lsum += warp_sum(l);
-      const int m = min(32, n - k0);
-      for (int k = 0; k < m; k += 8) {     // eight rows' loads in flight
-        float v[8][NG];
+    for (int k0 = 0; k0 < n; k0 += AHEAD) {
+      if (k0 > 0) fetch(k0);
+      if (k0 % 32 == 0) {                    // the factors of the next 32
+        if (k0 > 0) ml = ml_of(k0 + lane);
+        fac = ml.y != 0.f ? ex2(ml.x - mref) : 0.f;
+        lsum += warp_sum(ml.y != 0.f ? ml.y * fac : 0.f);
+      }
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          if (k + q < m) {
-            ldcg_row<NG>(a.part + at(k0 + k + q) * HD + lane * NG, v[q]);
-          } else {
+      for (int q = 0; q < AHEAD; ++q) {
+        const float f = __shfl_sync(0xffffffffu, fac, (k0 + q) & 31);
+        if (k0 + q < n) {
 #pragma unroll
-            for (int j = 0; j < NG; ++j) v[q][j] = 0.f;
-          }
-        }
-#pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          const float f = __shfl_sync(0xffffffffu, fac, (k + q) & 31);
-          if (k + q < m) {
-#pragma unroll
-            for (int j = 0; j < NG; ++j) os[j] = fmaf(v[q][j], f, os[j]);
-          }
+          for (int j = 0; j < NG; ++j) os[j] = fmaf(v[q][j], f, os[j]);
         }
       }
     }
