@@ -11,13 +11,15 @@
 // operand's split into two fp16 (22 bits) and of the fp32 sums.
 //
 // Both products take the codes as the A operand (m16n8k16: 16 positions of K by
-// 16 dims, 16 dims of V by 16 positions) and the few rows as B's 8 columns.
-// FINE (queries or outputs in fp32): columns 2 q and 2 q + 1 are the high and
-// low fp16 parts of row q, four rows per column block.  Otherwise (bf16 queries,
-// exact in one fp16, and bf16 outputs, whose rounding to 8 bits hides that of
-// the softmax weights to 11): a row per column, eight per block.  Scores come
-// out with a position per lane group r = lane / 4 and rows by c = lane % 4; a
-// transposition of 8 x 8 fp16 turns them into B operands of the second product.
+// 16 dims, 16 dims of V by 16 positions) and the few rows as B's 8 columns:
+//  - PAIR (up to four rows, queries or outputs in fp32): columns 2 q and 2 q + 1
+//    are the high and low fp16 parts of row q;
+//  - otherwise a row per column, and SPLIT (fp32) a second product with the low
+//    parts onto the same sums; bf16 queries are exact in one fp16, and a bf16
+//    output's rounding to 8 bits hides that of the softmax weights to 11.
+// Scores come out with a position per lane group r = lane / 4 and rows by c =
+// lane % 4; a transposition of 8 x 8 fp16 turns them into B operands of the
+// second product.
 // (With the rows as A's 16 rows, high parts over low parts, both products took
 // twice the matrix instructions and the outputs twice the registers.)
 #include <cuda_fp16.h>
@@ -37,15 +39,16 @@ constexpr int kItemUnits = 2;
 // there are enough CTAs for them
 constexpr int kWholeUnits = 24;
 
-template <int NG, int NT>
+template <int NG, bool PAIR, bool SPLIT>
 struct AttnSmem {
   static constexpr int kHd = 32 * NG;
   static constexpr int kPitch = kHd + 8;      // floats between partial rows: lanes (r, c) write row c, dims 8 i + r
   static constexpr int kStages = NG == 4 ? 2 : 4;
   static constexpr int kChunk = kv4_chunk_bytes(NG);
   static constexpr int kRing = kKv4Warps * kStages * kChunk;
-  static constexpr int kQ = kRing;                                  // uint2 [warps][NT][2 NG][32]
-  static constexpr int kBars = kQ + kKv4Warps * NT * 2 * NG * 32 * 8;
+  static constexpr int kQSets = SPLIT && !PAIR ? 2 : 1;             // high and low parts apart
+  static constexpr int kQ = kRing;                                  // uint2 [warps][sets][2 NG][32]
+  static constexpr int kBars = kQ + kKv4Warps * kQSets * 2 * NG * 32 * 8;
   static constexpr int kPart = kBars + kKv4Warps * kStages * 8;     // int4 [2 warps]: item of each partial
   static constexpr int kMl = kPart + kKv4Warps * 2 * 16;            // float2 [2 warps][8]: reference, sum
   static constexpr int kFlag = kMl + kKv4Warps * 2 * kKv4Rows * 8;
@@ -258,14 +261,14 @@ __device__ __forceinline__ void finish_row(const Kv4AttnArgs &a, int b, int h, i
 // CTA's warps on one item at a time, the two barriers and the queries' load at
 // each item cost 3.5 us: 64 ragged slots took 79 us and short slots beside long
 // ones 41.)
-template <int NG, bool FINE, int NT, bool TRACK>
+template <int NG, bool PAIR, bool SPLIT, bool TRACK>
 __global__ void __launch_bounds__(kKv4Threads, kKv4CtasPerSm)
     k_kv4_attn(const __grid_constant__ Kv4AttnArgs a) {
-  using L = AttnSmem<NG, NT>;
+  static_assert(SPLIT || !PAIR, "pairs are split");
+  using L = AttnSmem<NG, PAIR, SPLIT>;
   constexpr int HD = L::kHd, ST = L::kStages, PITCH = L::kPitch;
-  constexpr int RPB = FINE ? 4 : 8;           // rows per block of 8 columns
-  constexpr int RPI = RPB * NT;               // rows per item
-  constexpr int RL = (FINE ? 1 : 2) * NT;     // rows whose scores and outputs a lane holds
+  constexpr int RPI = PAIR ? 4 : 8;           // rows per item
+  constexpr int RL = PAIR ? 1 : 2;            // rows whose scores and outputs a lane holds
   static_assert(RPI <= kKv4Rows && 2 * RPI * PITCH * 4 <= ST * L::kChunk, "partial rows, in a warp's ring");
   extern __shared__ __align__(128) uint8_t smem[];
   int4 *spart = reinterpret_cast<int4 *>(smem + L::kPart);
@@ -273,7 +276,7 @@ __global__ void __launch_bounds__(kKv4Threads, kKv4CtasPerSm)
   int *sflag = reinterpret_cast<int *>(smem + L::kFlag);
   int *pre = reinterpret_cast<int *>(smem + L::kPre), *lens = pre + a.n_slot + 1;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r = lane >> 2, c = lane & 3;
-  uint2 *qs = reinterpret_cast<uint2 *>(smem + L::kQ) + warp * NT * 2 * NG * 32 + lane;
+  uint2 *qs = reinterpret_cast<uint2 *>(smem + L::kQ) + warp * L::kQSets * 2 * NG * 32 + lane;
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::kBars) + warp * ST;
   uint8_t *ring = smem + warp * ST * L::kChunk;
 
@@ -350,84 +353,80 @@ __global__ void __launch_bounds__(kKv4Threads, kKv4CtasPerSm)
     if (sg.c0 >= sg.c1) continue;
     const int len = lens[sg.b];
     const int row0 = sg.rb * RPI;
-    // the lane's score rows are row0 + lane_row(k), k < RL; its column's row in
-    // block t (queries, weights) is row0 + col_row + RPB t
-    auto lane_row = [&](int k) { return FINE ? c + 4 * k : 2 * c + k; };
-    const int col_row = FINE ? r >> 1 : r;
+    // the lane's score rows are row0 + lane_row(k), k < RL; its column's row
+    // (queries, weights) is row_col
+    auto lane_row = [&](int k) { return PAIR ? c : 2 * c + k; };
+    const int row_col = row0 + (PAIR ? r >> 1 : r);
 
     // Queries: lane (r, c) holds dims 32 g + 8 c .. + 7 of its column, which are
     // its own entries of the B operand.  Scaled to a largest magnitude of 2^10 by
-    // a power of two that the scores undo; FINE: split, high part in even columns.
+    // a power of two that the scores undo; PAIR: high part in even columns.
     float rs[RL];
     {
-      float scale[NT];
+      float v[NG][8];
+      if (row_col < a.rows) {
+        const int t = row_col / a.G, hq = sg.h * a.G + (row_col - t * a.G);
+        const int64_t at = sg.b * a.q.slot + t * a.q.token + hq * a.q.head + 8 * c;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const int row = row0 + col_row + RPB * nt;
-        float v[NG][8];
-        if (row < a.rows) {
-          const int t = row / a.G, hq = sg.h * a.G + (row - t * a.G);
-          const int64_t at = sg.b * a.q.slot + t * a.q.token + hq * a.q.head + 8 * c;
-#pragma unroll
-          for (int g = 0; g < NG; ++g) {
-            if (FINE && a.q.dtype == PNB_F32) {
-              const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(a.q.p) + at + 32 * g);
-              const float4 u = p[0], w = p[1];
-              v[g][0] = u.x; v[g][1] = u.y; v[g][2] = u.z; v[g][3] = u.w;
-              v[g][4] = w.x; v[g][5] = w.y; v[g][6] = w.z; v[g][7] = w.w;
-            } else {
-              load_vals<__nv_bfloat16, 8>(static_cast<const __nv_bfloat16 *>(a.q.p) + at + 32 * g, v[g]);
-            }
+        for (int g = 0; g < NG; ++g) {
+          if (SPLIT && a.q.dtype == PNB_F32) {
+            const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(a.q.p) + at + 32 * g);
+            const float4 u = p[0], w = p[1];
+            v[g][0] = u.x; v[g][1] = u.y; v[g][2] = u.z; v[g][3] = u.w;
+            v[g][4] = w.x; v[g][5] = w.y; v[g][6] = w.z; v[g][7] = w.w;
+          } else {
+            load_vals<__nv_bfloat16, 8>(static_cast<const __nv_bfloat16 *>(a.q.p) + at + 32 * g, v[g]);
           }
-        } else {
-#pragma unroll
-          for (int g = 0; g < NG; ++g)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[g][i] = 0.f;
         }
-        // the first copies go out behind the first queries' loads, which would
-        // otherwise wait in their queue
-        if (!primed) {
-          primed = true;
-#pragma unroll 1
-          for (int s = 0; s < ST; ++s) produce();
-        }
-        float mx = 0.f;
+      } else {
 #pragma unroll
         for (int g = 0; g < NG; ++g)
 #pragma unroll
-          for (int i = 0; i < 8; ++i) mx = fmaxf(mx, fabsf(v[g][i]));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        int e = (int)(__float_as_uint(mx) >> 23) - 127;
-        e = min(max(e, -100), 100);
-        const float up = __uint_as_float((uint32_t)(10 - e + 127) << 23);
-        scale[nt] = __uint_as_float((uint32_t)(e - 10 + 127) << 23) * a.qscale;
-#pragma unroll
-        for (int g = 0; g < NG; ++g)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {   // dims n, n + 4 with n = 2 h (b0) and 2 h + 1 (b1)
-            uint32_t w[2];
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const float2 y = make_float2(v[g][2 * h + k] * up, v[g][2 * h + k + 4] * up);
-              w[k] = pack_half2(y);
-              if (FINE) {
-                const float2 z = half2_pair(w[k]);
-                const uint32_t lo = pack_half2(make_float2(y.x - z.x, y.y - z.y));
-                w[k] = (r & 1) ? lo : w[k];
-              }
-            }
-            qs[(nt * 2 * NG + g * 2 + h) * 32] = make_uint2(w[0], w[1]);
-          }
+          for (int i = 0; i < 8; ++i) v[g][i] = 0.f;
       }
+      // the first copies go out behind the first queries' loads, which would
+      // otherwise wait in their queue
+      if (!primed) {
+        primed = true;
+#pragma unroll 1
+        for (int s = 0; s < ST; ++s) produce();
+      }
+      float mx = 0.f;
+#pragma unroll
+      for (int g = 0; g < NG; ++g)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) mx = fmaxf(mx, fabsf(v[g][i]));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+      int e = (int)(__float_as_uint(mx) >> 23) - 127;
+      e = min(max(e, -100), 100);
+      const float up = __uint_as_float((uint32_t)(10 - e + 127) << 23);
+      const float scale = __uint_as_float((uint32_t)(e - 10 + 127) << 23) * a.qscale;
+#pragma unroll
+      for (int g = 0; g < NG; ++g)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {   // dims n, n + 4 with n = 2 h (b0) and 2 h + 1 (b1)
+          uint32_t hi[2], lo[2] = {};
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const float2 y = make_float2(v[g][2 * h + k] * up, v[g][2 * h + k + 4] * up);
+            hi[k] = pack_half2(y);
+            if (SPLIT) {
+              const float2 z = half2_pair(hi[k]);
+              lo[k] = pack_half2(make_float2(y.x - z.x, y.y - z.y));
+            }
+          }
+          const bool low = PAIR && (r & 1);
+          qs[(g * 2 + h) * 32] = make_uint2(low ? lo[0] : hi[0], low ? lo[1] : hi[1]);
+          if (SPLIT && !PAIR) qs[(2 * NG + g * 2 + h) * 32] = make_uint2(lo[0], lo[1]);
+        }
       // the score rows' factors from the lanes of their columns
 #pragma unroll
-      for (int k = 0; k < RL; ++k)
-        rs[k] = __shfl_sync(0xffffffffu, scale[FINE ? k : 0], FINE ? 8 * c : 4 * (2 * c + k));
+      for (int k = 0; k < RL; ++k) rs[k] = __shfl_sync(0xffffffffu, scale, PAIR ? 8 * c : 4 * (2 * c + k));
     }
     const int limit_all = len - a.T + 1;                       // every row sees positions below it
-    int limit[RL], limit_col[NT];
+    int limit[RL];
+    const int limit_col = row_col < a.rows ? limit_all + row_col / a.G : 0;
     float *score[RL];
 #pragma unroll
     for (int k = 0; k < RL; ++k) {
@@ -438,17 +437,10 @@ __global__ void __launch_bounds__(kKv4Threads, kKv4CtasPerSm)
                        ? a.scores + (((int64_t)sg.b * a.n_kv + sg.h) * a.rows + row) * a.l.cap + r
                        : nullptr;
     }
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const int row = row0 + col_row + RPB * nt;
-      limit_col[nt] = row < a.rows ? limit_all + row / a.G : 0;
-    }
 
-    float o[NT][NG * 2][4];
+    float o[NG * 2][4];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int i = 0; i < NG * 2; ++i) o[nt][i][0] = o[nt][i][1] = o[nt][i][2] = o[nt][i][3] = 0.f;
+    for (int i = 0; i < NG * 2; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
     float l[RL], m[RL], ref[RL];                               // sum, reference maximum, reference
     int ev = -1;                                               // V scales seen are below 2^ev
 #pragma unroll
@@ -491,21 +483,25 @@ __global__ void __launch_bounds__(kKv4Threads, kKv4CtasPerSm)
           uint32_t u0[4], u1[4];
           code_pairs(kw[0][g], magic, u0);
           code_pairs(kw[1][g], magic, u1);
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            const uint2 qa = qs[(nt * 2 * NG + g * 2) * 32];
-            const uint2 qb = qs[(nt * 2 * NG + g * 2 + 1) * 32];
-            float d[4];
+          float d[4];
+          {
+            const uint2 qa = qs[(g * 2) * 32], qb = qs[(g * 2 + 1) * 32];
             mma_f16_new(d, u0[0], u1[0], u0[1], u1[1], qa.x, qa.y);
             mma_f16(d, u0[2], u1[2], u0[3], u1[3], qb.x, qb.y);
-            if (FINE) {
-              s[2 * mt][nt] = fmaf(d[0] + d[1], kd[0][g], s[2 * mt][nt]);
-              s[2 * mt + 1][nt] = fmaf(d[2] + d[3], kd[1][g], s[2 * mt + 1][nt]);
-            } else {
-              s[2 * mt][0] = fmaf(d[0], kd[0][g], s[2 * mt][0]);
-              s[2 * mt][1] = fmaf(d[1], kd[0][g], s[2 * mt][1]);
-              s[2 * mt + 1][0] = fmaf(d[2], kd[1][g], s[2 * mt + 1][0]);
-              s[2 * mt + 1][1] = fmaf(d[3], kd[1][g], s[2 * mt + 1][1]);
+          }
+          if (SPLIT && !PAIR) {
+            const uint2 qa = qs[(2 * NG + g * 2) * 32], qb = qs[(2 * NG + g * 2 + 1) * 32];
+            mma_f16(d, u0[0], u1[0], u0[1], u1[1], qa.x, qa.y);
+            mma_f16(d, u0[2], u1[2], u0[3], u1[3], qb.x, qb.y);
+          }
+          if (PAIR) {
+            s[2 * mt][0] = fmaf(d[0] + d[1], kd[0][g], s[2 * mt][0]);
+            s[2 * mt + 1][0] = fmaf(d[2] + d[3], kd[1][g], s[2 * mt + 1][0]);
+          } else {
+#pragma unroll
+            for (int k = 0; k < RL; ++k) {
+              s[2 * mt][k] = fmaf(d[k], kd[0][g], s[2 * mt][k]);
+              s[2 * mt + 1][k] = fmaf(d[2 + k], kd[1][g], s[2 * mt + 1][k]);
             }
           }
         }
@@ -571,16 +567,17 @@ __global__ void __launch_bounds__(kKv4Threads, kKv4CtasPerSm)
           l[k] *= al;
 #pragma unroll
           for (int i = 0; i < NG * 2; ++i) {
-            if (FINE) {
-              o[k][i][0] *= al; o[k][i][1] *= al; o[k][i][2] *= al; o[k][i][3] *= al;
+            if (PAIR) {
+              o[i][0] *= al; o[i][1] *= al; o[i][2] *= al; o[i][3] *= al;
             } else {
-              o[0][i][k] *= al; o[0][i][2 + k] *= al;
+              o[i][k] *= al; o[i][2 + k] *= al;
             }
           }
         }
       }
-      // softmax weights as columns: x[nt][t] holds positions 8 t + 2 c, + 1 of the lane's column
-      uint32_t xc[NT][4], xh[NT][4];
+      // softmax weights as columns: xh[t] holds the high parts of positions 8 t + 2 c,
+      // + 1 of the lane's column's row, xl[t] the low parts (PAIR: 0 in even columns)
+      uint32_t xh[4], xl[4];
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
         float p[RL];
@@ -589,16 +586,18 @@ __global__ void __launch_bounds__(kKv4Threads, kKv4CtasPerSm)
           p[k] = ex2(fmaf(s[t][k], rs[k], -ref[k]));
           l[k] += p[k];
         }
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          if (FINE) {
-            const float h = __half2float(__float2half_rn(p[nt]));
-            xc[nt][t] = transpose8(pack_half2(make_float2(h, p[nt] - h)));
-            const uint32_t other = __shfl_xor_sync(0xffffffffu, xc[nt][t], 4);
-            xh[nt][t] = (r & 1) ? other : xc[nt][t];   // the high parts, in both of a row's columns
-            xc[nt][t] = (r & 1) ? xc[nt][t] : 0u;      // the low parts, in the odd one
-          } else {
-            xc[nt][t] = transpose8(pack_half2(make_float2(p[0], p[1])));
+        if (PAIR) {
+          const float h = __half2float(__float2half_rn(p[0]));
+          const uint32_t mine = transpose8(pack_half2(make_float2(h, p[0] - h)));
+          const uint32_t other = __shfl_xor_sync(0xffffffffu, mine, 4);
+          xh[t] = (r & 1) ? other : mine;
+          xl[t] = (r & 1) ? mine : 0u;
+        } else {
+          const uint32_t h = pack_half2(make_float2(p[0], p[RL - 1]));
+          xh[t] = transpose8(h);
+          if (SPLIT) {
+            const float2 z = half2_pair(h);
+            xl[t] = transpose8(pack_half2(make_float2(p[0] - z.x, p[RL - 1] - z.y)));
           }
         }
       }
@@ -611,34 +610,36 @@ __global__ void __launch_bounds__(kKv4Threads, kKv4CtasPerSm)
         code_pairs(vw.y, magic, u[1]);
         code_pairs(vw.z, magic, u[2]);
         code_pairs(vw.w, magic, u[3]);
+        // p d in fp16: its rounding, and the rest of the exact product, the
+        // rounding's residual (one fma) + p_lo d.  PAIR: the one in even columns,
+        // the other in odd ones.
+        uint32_t w[4], wl[4];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          // p d in fp16; FINE: even columns its rounding, odd columns the rest of the
-          // exact product, the rounding's residual (one fma) + p_lo d
-          uint32_t w[4];
-#pragma unroll
-          for (int t = 0; t < 4; ++t) {
-            uint32_t dw = *reinterpret_cast<const uint32_t *>(st + kv4_vscale_off(NG) + (t * 4 + c) * 4 * NG + 4 * g);
-            if (tail) {   // a masked position's scale may be anything: its weight is 0, not 0 times it
-              const int p = p0 + 8 * t + 2 * c;
-              dw &= p >= limit_col[nt] ? 0u : (p + 1 >= limit_col[nt] ? 0xffffu : 0xffffffffu);
-            }
-            const __half2 d = as_half2(dw);
-            if (FINE) {
-              const __half2 h = as_half2(xh[nt][t]);
-              const uint32_t first = as_word(__hmul2_rn(h, d)) & odd;
-              w[t] = as_word(__hfma2(as_half2(xc[nt][t]), d, __hfma2(h, d, __hneg2(as_half2(first)))));
-            } else {
-              w[t] = as_word(__hmul2_rn(as_half2(xc[nt][t]), d));
-            }
+        for (int t = 0; t < 4; ++t) {
+          uint32_t dw = *reinterpret_cast<const uint32_t *>(st + kv4_vscale_off(NG) + (t * 4 + c) * 4 * NG + 4 * g);
+          if (tail) {   // a masked position's scale may be anything: its weight is 0, not 0 times it
+            const int p = p0 + 8 * t + 2 * c;
+            dw &= p >= limit_col ? 0u : (p + 1 >= limit_col ? 0xffffu : 0xffffffffu);
           }
-#pragma unroll
-          for (int j = 0; j < 2; ++j)
-#pragma unroll
-            for (int kt = 0; kt < 2; ++kt)
-              mma_f16(o[nt][g * 2 + j], u[2 * j][2 * kt], u[2 * j + 1][2 * kt], u[2 * j][2 * kt + 1],
-                      u[2 * j + 1][2 * kt + 1], w[2 * kt], w[2 * kt + 1]);
+          const __half2 d = as_half2(dw), h = as_half2(xh[t]);
+          const uint32_t first = as_word(__hmul2_rn(h, d));
+          w[t] = first;
+          if (SPLIT) {
+            const uint32_t taken = PAIR ? first & odd : first;
+            wl[t] = as_word(__hfma2(as_half2(xl[t]), d, __hfma2(h, d, __hneg2(as_half2(taken)))));
+            if (PAIR) w[t] = wl[t];
+          }
         }
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int kt = 0; kt < 2; ++kt) {
+            mma_f16(o[g * 2 + j], u[2 * j][2 * kt], u[2 * j + 1][2 * kt], u[2 * j][2 * kt + 1], u[2 * j + 1][2 * kt + 1],
+                    w[2 * kt], w[2 * kt + 1]);
+            if (SPLIT && !PAIR)
+              mma_f16(o[g * 2 + j], u[2 * j][2 * kt], u[2 * j + 1][2 * kt], u[2 * j][2 * kt + 1],
+                      u[2 * j + 1][2 * kt + 1], wl[2 * kt], wl[2 * kt + 1]);
+          }
       }
       __syncwarp();
       produce();
@@ -648,7 +649,7 @@ __global__ void __launch_bounds__(kKv4Threads, kKv4CtasPerSm)
 
     // the lane's outputs: row lane_row(k), dim 8 i + r
     auto out_of = [&](int k, int i) {
-      return FINE ? o[k][i >> 1][2 * (i & 1)] + o[k][i >> 1][2 * (i & 1) + 1] : o[0][i >> 1][2 * (i & 1) + k];
+      return PAIR ? o[i >> 1][2 * (i & 1)] + o[i >> 1][2 * (i & 1) + 1] : o[i >> 1][2 * (i & 1) + k];
     };
 #pragma unroll
     for (int k = 0; k < RL; ++k) {
@@ -694,7 +695,7 @@ __global__ void __launch_bounds__(kKv4Threads, kKv4CtasPerSm)
   if (early) {
 #pragma unroll
     for (int k = 0; k < RL; ++k) {
-      const int i0 = FINE ? c + 4 * k : 2 * c + k;
+      const int i0 = PAIR ? c : 2 * c + k;
 #pragma unroll
       for (int i = 0; i < NG * 4; ++i)
         reinterpret_cast<float *>(ring)[i0 * PITCH + r + 8 * i] = early_part[(k * NG * 4 + i) * 32];
@@ -889,13 +890,16 @@ cudaError_t prepare(int *grid) {
   auto set = [&](auto k, int smem) {
     if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   };
-  const int s1 = AttnSmem<NG, 1>::bytes(kKv4MaxSlots), s2 = AttnSmem<NG, 2>::bytes(kKv4MaxSlots);
-  set(k_kv4_attn<NG, false, 1, false>, s1);
-  set(k_kv4_attn<NG, false, 1, true>, s1);
-  set(k_kv4_attn<NG, true, 1, false>, s1);
-  set(k_kv4_attn<NG, true, 1, true>, s1);
-  set(k_kv4_attn<NG, true, 2, false>, s2);
-  set(k_kv4_attn<NG, true, 2, true>, s2);
+  auto set_both = [&](auto plain, auto track, int smem) {
+    set(plain, smem);
+    set(track, smem);
+  };
+  set_both(k_kv4_attn<NG, false, false, false>, k_kv4_attn<NG, false, false, true>,
+           AttnSmem<NG, false, false>::bytes(kKv4MaxSlots));
+  set_both(k_kv4_attn<NG, false, true, false>, k_kv4_attn<NG, false, true, true>,
+           AttnSmem<NG, false, true>::bytes(kKv4MaxSlots));
+  set_both(k_kv4_attn<NG, true, true, false>, k_kv4_attn<NG, true, true, true>,
+           AttnSmem<NG, true, true>::bytes(kKv4MaxSlots));
   int dev = 0, sms = 0;
   if (e == cudaSuccess) e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
@@ -903,19 +907,19 @@ cudaError_t prepare(int *grid) {
   return e;
 }
 
-template <int NG, bool FINE, int NT>
+template <int NG, bool PAIR, bool SPLIT>
 cudaError_t run_attn(Kv4AttnArgs a, int grid, cudaStream_t st) {
-  constexpr int rows = (FINE ? 4 : 8) * NT;
+  constexpr int rows = PAIR ? 4 : 8;
   a.nrb = (a.rows + rows - 1) / rows;
-  const int smem = AttnSmem<NG, NT>::bytes(a.n_slot);
-  auto kern = a.scores ? k_kv4_attn<NG, FINE, NT, true> : k_kv4_attn<NG, FINE, NT, false>;
+  const int smem = AttnSmem<NG, PAIR, SPLIT>::bytes(a.n_slot);
+  auto kern = a.scores ? k_kv4_attn<NG, PAIR, SPLIT, true> : k_kv4_attn<NG, PAIR, SPLIT, false>;
   return kv4_launch(kern, dim3(grid), dim3(kKv4Threads), smem, 1, st, a);
 }
 
 template <int NG>
 cudaError_t run_attn(const Kv4AttnArgs &a, int grid, cudaStream_t st) {
-  if (a.q.dtype == PNB_BF16 && a.out.dtype == PNB_BF16) return run_attn<NG, false, 1>(a, grid, st);
-  return a.rows <= 4 ? run_attn<NG, true, 1>(a, grid, st) : run_attn<NG, true, 2>(a, grid, st);
+  if (a.q.dtype == PNB_BF16 && a.out.dtype == PNB_BF16) return run_attn<NG, false, false>(a, grid, st);
+  return a.rows <= 4 ? run_attn<NG, true, true>(a, grid, st) : run_attn<NG, false, true>(a, grid, st);
 }
 
 }  // namespace
