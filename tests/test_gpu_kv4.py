@@ -439,6 +439,39 @@ def test_attention_work_splits(B, n_kv, G, hd, lo, hi):
     assert c.device_error() == 0
 
 
+def test_offsets_past_32_bits():
+    """A cache of 10 GB and 2^32 tracked scores: the last slot's entries, scores and moves lie behind
+    4 GiB.  Rows of all slots are one tensor's (slot stride 0); the other slots stay empty."""
+    B, n_kv, G, hd, T, cap = 64, 8, 8, 128, 8, 1 << 17
+    n = cap - 5
+    c = make(B, n_kv * G, n_kv, hd, cap, track=T)
+    assert c.buf.numel() > 9 << 30 and B * n_kv * G * T * cap >= 1 << 32
+    k, v = rows((1, n, n_kv, hd), 340, BF16), rows((1, n, n_kv, hd), 341, BF16)
+    c.append(0, k.expand(B, n, n_kv, hd), v.expand(B, n, n_kv, hd), n_new=i32([0] * (B - 1) + [n]))
+    q = rows((B, T, n_kv * G, hd), 342, BF16, 2.0)
+    out = torch.empty((B, T, n_kv * G, hd), device="cuda")
+    c.attention(0, q, out, decay=0.0)
+    assert not out[:-1].any() and c.device_error() == 0
+    ref = Ref(1, n_kv * G, n_kv, hd, cap)     # the last slot alone
+    ref.append(k, v)
+    want, tol, wtol = ref.attention(q[-1:], 0.0)
+    assert bool(((out[-1:].double() - want).abs() <= tol).all())
+    w = c.weights(0)[-1]
+    assert float((w[:, :n].double() - ref.w[0, :, :n]).abs().max()) <= wtol
+    ref.w[0].copy_(w.double())
+    c.evict(0, 60000, 4, 100)
+    ref.evict(60000, 4, 100)
+    assert c.lengths(0).tolist() == [0] * (B - 1) + [60000]
+    assert torch.equal(c.ids(0)[-1, :, :60000].long(), ref.ids[0, :, :60000])
+    first = i32([0] * (B - 1) + [59990])
+    yk = torch.empty((B, 20, n_kv, hd), device="cuda")
+    yv = torch.empty_like(yk)
+    c.read(0, yk, yv, first=first)
+    for got, held_rows in ((yk, ref.k), (yv, ref.v)):
+        assert torch.equal(got[-1, :10].double(), held_rows[0, :, 59990:60000].transpose(0, 1))
+        assert not got[-1, 10:].any() and not got[:-1].any()
+
+
 def test_extreme_values():
     """A score far above the others late in the sequence, V scales that grow by 2^20 along it
     (the fp16 products' reference moves), large and tiny queries."""
