@@ -33,9 +33,9 @@ namespace pnb {
 
 constexpr int kKv4Chunk = 32;              // positions per chunk
 constexpr int kKv4Rows = 8;                // most query rows (tokens x heads of a group) per work item
-constexpr int kKv4Warps = 8;               // warps per attention CTA
+constexpr int kKv4Warps = 16;              // warps per attention CTA
 constexpr int kKv4Threads = kKv4Warps * 32;
-constexpr int kKv4CtasPerSm = 2;
+constexpr int kKv4CtasPerSm = 1;
 constexpr int kKv4MaxRows = 64;            // tokens x heads of a group in one call
 constexpr int kKv4MaxSlots = 1024;
 constexpr int kKv4MaxCap = 1 << 20;        // positions per slot

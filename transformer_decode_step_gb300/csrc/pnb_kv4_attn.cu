@@ -37,9 +37,9 @@ namespace {
 constexpr int kItemUnits = 2;
 // items of at most this many units on average are not split over CTAs while
 // there are enough CTAs for them (8 KV heads of one sequence, head_dim 128, whole
-// against split, us: 6 units 5.5, 7.3; 14 units 6.7, 7.5; 22 units 8.0, 8.1; 26
-// units 9.4, 8.1; 34 units 10.7, 8.1)
-constexpr int kWholeUnits = 24;
+// against split, us: 6 units 5.8, 8.6; 10 units 6.4, 9.3; 18 units 8.2, 9.3; 26
+// units 9.1, 9.4; 34 units 10.2, 9.5; 50 units 12.3, 9.6)
+constexpr int kWholeUnits = 28;
 
 template <int NG, bool PAIR, bool SPLIT>
 struct AttnSmem {
@@ -263,6 +263,15 @@ __device__ __forceinline__ void finish_row(const Kv4AttnArgs &a, int b, int h, i
 // CTA's warps on one item at a time, the two barriers and the queries' load at
 // each item cost 3.5 us: 64 ragged slots took 79 us and short slots beside long
 // ones 41.)
+// The registers (128) leave 16 warps on an SM.  As one CTA of 16 they share fewer
+// items between CTAs than as two of 8: 128k positions 56.4 us against 59.3, 64
+// ragged slots 41.4 against 42.4, 8 KV heads at 8192 positions 10.2 against 11.6,
+// at 32768 15.4 against 16.9; 32 MHA heads at 2048 9.8 against 9.2, at 4096 11.4
+// against 11.3.
+// Bound by the latency of a warp's dependent steps (copy, scores, maximum,
+// weights, products) rather than by memory: 128k positions of 8 KV heads
+// (head_dim 128, fp32 rows) are read at 4.7 TB/s, 64 slots at 3.8, start, merge
+// and launch included; with few units the start and the merges are all there is.
 template <int NG, bool PAIR, bool SPLIT, bool TRACK>
 __global__ void __launch_bounds__(kKv4Threads, kKv4CtasPerSm)
     k_kv4_attn(const __grid_constant__ Kv4AttnArgs a) {
@@ -294,8 +303,8 @@ __global__ void __launch_bounds__(kKv4Threads, kKv4CtasPerSm)
   }
   __syncthreads();
   const int total = pre[a.n_slot], cta = blockIdx.x;
-  // One unit per warp, except that short items (a CTA's warps take a unit in
-  // about 1.2 us, and rows shared by CTAs cost 3 us more) get a CTA each.
+  // One unit per warp at least, except that short items get a CTA each: rows
+  // shared by CTAs cost about 3 us more.
   const int items = lens[a.n_slot] * a.n_kv * a.nrb;
   const int ctas = items <= (int)gridDim.x && total <= items * kWholeUnits
                        ? max(1, items)
