@@ -523,6 +523,23 @@ def test_non_finite_rows_stay_where_they_are():
     check_attention(c, ref, q)
 
 
+@pytest.mark.parametrize("n", [30, 200, 1500, 9000])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_a_nan_value_under_a_weight_of_zero(n, dtype):
+    """The first half's weights underflow to 0; 0 times its NaN block is NaN however the work is split."""
+    hd = 128
+    k, v, q = torch.ones(1, n, 1, hd, device="cuda"), rows((1, n, 1, hd), 31), torch.ones(1, 1, 4, hd, device="cuda")
+    k[:, :n // 2] = -1
+    v[0, n // 4, 0, 70] = float("nan")        # block 2 (dims 64..95)
+    c = make(1, 4, 1, hd, 9024)
+    c.append(0, k, v)
+    q = (10 * q).to(dtype)
+    out = torch.empty_like(q)
+    c.attention(0, q, out)
+    nan = torch.isnan(out)
+    assert nan[..., 64:96].all() and not nan[..., :64].any() and not nan[..., 96:].any()
+
+
 @pytest.mark.parametrize("n_kv,G,hd,T", [(2, 4, 128, 1), (2, 8, 64, 1), (4, 1, 32, 1), (1, 4, 128, 4)])
 def test_attention_is_as_exact_as_plain_fp32(n_kv, G, hd, T):
     """fp32 outputs and weights are no further from the 64-bit result than a plain fp32 computation on

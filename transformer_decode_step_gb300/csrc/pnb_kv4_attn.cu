@@ -746,13 +746,15 @@ __global__ void __launch_bounds__(kKv4Threads, kKv4CtasPerSm)
     // lane e holds entry e's factor
     const float2 ml = (members >> lane) & 1u ? sml[lane * kKv4Rows + i] : make_float2(0.f, 0.f);
     const float mref = warp_max(ml.y != 0.f ? ml.x : -INFINITY);
-    const float fac = ml.y != 0.f ? ex2(ml.x - mref) : 0.f;
+    float fac = ml.y != 0.f ? ex2(ml.x - mref) : 0.f;
     const float lsum = warp_sum(ml.y * fac);
+    // 0 stands for no entry; an entry's factor of 0 is -0, which hands on a NaN
+    if (fac == 0.f && ((members >> lane) & 1u)) fac = -0.f;
     float os[NG] = {};
 #pragma unroll
     for (int e = 0; e < 2 * kKv4Warps; ++e) {
       const float f = __shfl_sync(0xffffffffu, fac, e);
-      if (f == 0.f) continue;
+      if (__float_as_uint(f) == 0u) continue;
       float v[NG];
       load_vals<float, NG>(reinterpret_cast<const float *>(smem + (e >> 1) * ST * L::kChunk) +
                                ((e & 1) * RPI + i) * PITCH + lane * NG, v);
