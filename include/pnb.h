@@ -455,7 +455,9 @@ typedef struct pnb_kvq pnb_kvq;
    contiguous, the other strides in elements (so rows may lie inside a fused
    QKV projection or a state's KV cache).  dtype: PNB_F32 or PNB_BF16.  dev
    and every stride must keep rows 16-byte aligned (PNB_E_ALIGN); strides are
-   not negative, and rows that a call writes must not overlap (PNB_E_INVAL). */
+   not negative, and rows that a call writes overlap neither one another nor
+   the call's other rows; rows that lie between one another have the same
+   strides and dtype (PNB_E_INVAL). */
 typedef struct {
   const void *dev;
   int64_t slot, token, head;
@@ -519,8 +521,9 @@ int pnb_kvq_attention(pnb_kvq *c, int32_t layer, const pnb_rows *q, int32_t T, c
    entries that stay below index `budget` keep their index; those behind move,
    in order, into the places of the dropped ones.  dst may be another cache or
    layer of the same n_slot, n_kv_head and head_dim (shorter slots are copied
-   whole, src is not changed), or src itself in place.  src's cap is at most
-   2^18 (PNB_E_UNSUPPORTED). */
+   whole, src is not changed), or src itself in place; their buffers are the
+   same or do not overlap (PNB_E_INVAL).  src's cap is at most 2^18
+   (PNB_E_UNSUPPORTED). */
 int pnb_kvq_evict(pnb_kvq *src, int32_t src_layer, pnb_kvq *dst, int32_t dst_layer, int32_t budget,
                   int32_t n_sink, int32_t n_recent, pnb_stream stream);
 

@@ -859,3 +859,52 @@ def test_refusals():
     big.reset()
     assert code(big.evict, 0, 10) == -5
     assert c.device_error() == 0 and c.lengths(0).tolist() == [0, 0]
+
+
+def test_rows_over_one_another_are_refused():
+    """read's K over its V, attention's output over others' queries, eviction between overlapping buffers."""
+    B, T, H, Hkv, hd = 2, 3, 4, 2, 64
+    c = make(B, H, Hkv, hd, 64)
+    c.append(0, rows((B, 40, Hkv, hd), 104), rows((B, 40, Hkv, hd), 105))
+    want = torch.empty(2, B, T, Hkv, hd, device="cuda")
+    c.read(0, want[0], want[1])
+
+    def refused(f, *a, **kw):
+        with pytest.raises(pnb.PnbError) as e:
+            f(*a, **kw)
+        return e.value.code == -1
+
+    flat = torch.zeros(1 << 14, device="cuda")
+    at = lambda off, s, dtype=F32: flat.view(dtype)[off:].as_strided((B, T, Hkv, hd), s)
+    plain = (T * Hkv * hd, Hkv * hd, hd, 1)
+    n = B * T * Hkv * hd
+    for off in (0, 16, hd, hd * Hkv, n - hd, n - 4):          # rows over rows, whole or in part
+        assert refused(c.read, 0, at(0, plain), at(off, plain))
+        assert refused(c.read, 0, at(off, plain), at(0, plain))
+    side = (2 * T * Hkv * hd, 2 * Hkv * hd, hd, 1)             # K and V of a token side by side
+    pair = (2 * T * Hkv * hd, 2 * Hkv * hd, 2 * hd, 1)         # of a head
+    by_head = (Hkv * 2 * T * hd, hd, 2 * T * hd, 1)            # tokens inside heads
+    for s, off in ((plain, n), (side, Hkv * hd), (pair, hd), (by_head, T * hd)):
+        for a, b in ((0, off), (off, 0)):
+            k, v = at(a, s), at(b, s)
+            flat.zero_()
+            c.read(0, k, v)
+            assert torch.equal(k, want[0]) and torch.equal(v, want[1])
+    for s, off in ((side, hd), (pair, hd // 2), (pair, 2 * hd), (by_head, hd), (by_head, 2 * T * hd)):
+        assert refused(c.read, 0, at(0, s), at(off, s)) and refused(c.read, 0, at(off, s), at(0, s))
+    assert refused(c.read, 0, at(0, pair), at(hd, side))       # between one another, strides differ
+
+    q = flat[:B * T * H * hd].view(B, T, H, hd)
+    shifted = flat[hd:hd + B * T * H * hd].view(B, T, H, hd)
+    assert refused(c.attention, 0, q, shifted) and refused(c.attention, 0, shifted, q)
+    assert refused(c.attention, 0, q, flat.view(BF16)[:q.numel()].view(B, T, H, hd))
+    assert refused(c.attention, 0, q, flat.as_strided((B, T, H, hd), (H * hd, B * H * hd, hd, 1)))
+    c.attention(0, q, q)
+
+    nbytes = c.buf.numel()
+    two = torch.empty(2 * nbytes, dtype=torch.uint8, device="cuda")
+    over = [pnb.Kv4Cache(1, B, H, Hkv, hd, 64, buf=two[o:o + nbytes]) for o in (0, 128, nbytes)]
+    over[0].reset()
+    assert refused(over[0].evict, 0, 8, dst=over[1]) and refused(over[1].evict, 0, 8, dst=over[0])
+    over[0].evict(0, 8, dst=over[2])
+    assert over[2].lengths(0).tolist() == [0, 0]

@@ -2,8 +2,10 @@
 // caller's buffer, the library's workspace.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <new>
+#include <utility>
 
 #include "pnb.h"
 #include "pnb_kv4.cuh"
@@ -106,6 +108,46 @@ int check_rows(const pnb_rows *r, int T, int n_slot, int heads, int head_dim, bo
   out->head = r->head;
   out->dtype = r->dtype;
   return PNB_OK;
+}
+
+// Whether rows x, already checked as written rows, and rows y are apart in
+// memory: far from one another, or with the same type and strides (K and V side
+// by side in one tensor).  `same` answers for x and y being the same rows.
+bool apart(const Kv4Rows &x, const Kv4Rows &y, int T, int n_slot, int heads, int head_dim, bool same) {
+  int64_t s[3] = {x.slot, x.token, x.head}, n[3] = {n_slot, T, heads};
+  const int64_t sy[3] = {y.slot, y.token, y.head};
+  const int64_t ex = x.dtype == PNB_F32 ? 4 : 2, ey = y.dtype == PNB_F32 ? 4 : 2;
+  int64_t bx = head_dim, by = head_dim;
+  bool alike = x.dtype == y.dtype;
+  for (int i = 0; i < 3; ++i) {
+    bx += s[i] * (n[i] - 1);
+    by += sy[i] * (n[i] - 1);
+    alike &= n[i] == 1 || s[i] == sy[i];
+  }
+  const int64_t diff = static_cast<uint8_t *>(y.p) - static_cast<uint8_t *>(x.p);
+  if (diff >= bx * ex || -diff >= by * ey) return true;
+  if (!alike) return false;
+  if (diff == 0) return same;
+  for (int i = 0; i < 2; ++i)          // strides in descending order
+    for (int j = 0; j < 2 - i; ++j)
+      if (s[j] < s[j + 1]) {
+        std::swap(s[j], s[j + 1]);
+        std::swap(n[j], n[j + 1]);
+      }
+  // Do steps i_d, |i_d| < n_d, lead from a row of x to within a row of one of y?
+  // A stride is no shorter than what lies below it, so that only the two steps
+  // about the distance can.
+  for (int c = 0; c < 8; ++c) {
+    int64_t left = diff / ex;
+    for (int d = 0; d < 3; ++d) {
+      if (n[d] <= 1) continue;
+      int64_t i = left / s[d] - (left % s[d] < 0) + (c >> d & 1);
+      i = std::min(std::max(i, 1 - n[d]), n[d] - 1);
+      left -= i * s[d];
+    }
+    if (left < head_dim && left > -head_dim) return false;
+  }
+  return true;
 }
 
 }  // namespace
@@ -231,7 +273,7 @@ int pnb_kvq_read(pnb_kvq *c, int32_t layer, const int32_t *first_dev, int32_t T,
   int rc = check_rows(k, T, g.n_slot, g.n_kv_head, g.head_dim, true, &a.k);
   if (rc == PNB_OK) rc = check_rows(v, T, g.n_slot, g.n_kv_head, g.head_dim, true, &a.v);
   if (rc != PNB_OK) return rc;
-  if (k->dtype != v->dtype) return PNB_E_INVAL;
+  if (k->dtype != v->dtype || !apart(a.k, a.v, T, g.n_slot, g.n_kv_head, g.head_dim, false)) return PNB_E_INVAL;
   rc = check_call(c, layer);
   if (rc != PNB_OK) return rc;
   a.l = layer_of(c, layer);
@@ -256,6 +298,7 @@ int pnb_kvq_attention(pnb_kvq *c, int32_t layer, const pnb_rows *q, int32_t T, c
   int rc = check_rows(q, T, g.n_slot, g.n_head, g.head_dim, false, &a.q);
   if (rc == PNB_OK) rc = check_rows(out, T, g.n_slot, g.n_head, g.head_dim, true, &a.out);
   if (rc != PNB_OK) return rc;
+  if (!apart(a.out, a.q, T, g.n_slot, g.n_head, g.head_dim, true)) return PNB_E_INVAL;
   rc = check_call(c, layer);
   if (rc != PNB_OK) return rc;
   a.l = layer_of(c, layer);
@@ -295,7 +338,11 @@ int pnb_kvq_evict(pnb_kvq *src, int32_t src_layer, pnb_kvq *dst, int32_t dst_lay
   if (budget < 1 || n_sink < 0 || n_recent < 0 || (int64_t)n_sink + n_recent > budget) return PNB_E_INVAL;
   if (s.n_slot != d.n_slot || s.n_kv_head != d.n_kv_head || s.head_dim != d.head_dim) return PNB_E_INVAL;
   if (budget > d.cap) return PNB_E_INVAL;
-  if (src->buf == dst->buf && (s.cap != d.cap || src->layer_bytes != dst->layer_bytes)) return PNB_E_INVAL;
+  // one buffer, or two that are apart
+  if (src->buf == dst->buf ? s.cap != d.cap
+                           : src->buf < dst->buf + dst->layer_bytes * d.n_layer &&
+                                 dst->buf < src->buf + src->layer_bytes * s.n_layer)
+    return PNB_E_INVAL;
   if (s.cap > kKv4MaxEvictCap) return PNB_E_UNSUPPORTED;
   int rc = check_call(src, src_layer);
   if (rc == PNB_OK) rc = check_call(dst, dst_layer);
