@@ -82,13 +82,14 @@ __device__ __forceinline__ float2 fadd2(float2 a, float2 b) {
 }
 
 // largest magnitude of the 8, NaN when one is
-__device__ __forceinline__ float top8(const Raw8<float> &, const float (&x)[8]) {
-  float top = 0.f;
+__device__ __forceinline__ float top8(const Raw8<float> &r) {
+  float x[8], top = 0.f;
+  r.floats(x);
 #pragma unroll
   for (int i = 0; i < 8; ++i) top = max_nan(top, fabsf(x[i]));
   return top;
 }
-__device__ __forceinline__ float top8(const Raw8<__nv_bfloat16> &r, const float (&)[8]) {
+__device__ __forceinline__ float top8(const Raw8<__nv_bfloat16> &r) {
   const __nv_bfloat162 *h = reinterpret_cast<const __nv_bfloat162 *>(r.v);
   const __nv_bfloat162 m = __hmax2_nan(__hmax2_nan(__habs2(h[0]), __habs2(h[1])), __hmax2_nan(__habs2(h[2]), __habs2(h[3])));
   return max_nan(__low2float(m), __high2float(m));
@@ -112,55 +113,106 @@ __device__ __noinline__ uint32_t q4_word_checked(float4 a, float4 b, float df, f
   return w ^ 0x88888888u;                // + 8 modulo 16
 }
 
-// One Q4_0 block is held by 4 neighbouring lanes, 8 dims each:
-//   d = fp16(max|x| / 7), u = clamp(rint(x / d), -8, 7) + 8
-// with correctly rounded quotients: max|x| / 7 by one residual step, and
-// rint(x / d) from x * (1 / d), whose error of a few units matters next to a
-// border only.
+// A block's scale from its largest magnitude: d = fp16(max|x| / 7), the quotient
+// correctly rounded by one residual step.  NaN and infinities make it NaN; a
+// scale past fp16's range saturates.
+struct Q4Scale {
+  __half d;
+  float df;      // d, or 0 where all codes are 8
+  bool hard;     // some quotients lie outside [-8, 7]
+  __device__ __forceinline__ explicit Q4Scale(float top) {
+    const float seventh = 1.f / 7.f, q0 = __fmul_rn(top, seventh);
+    const float quot = __fmaf_rn(__fmaf_rn(-q0, 7.f, top), seventh, q0);
+    const bool finite = top < INFINITY;  // false for NaN too
+    d = __float2half_rn(fminf(quot, 65504.f));
+    df = finite ? __half2float(d) : 0.f;
+    hard = df != 0.f && top > 7.5f * df;
+    if (!finite) d = __ushort_as_half((unsigned short)0x7fffu);
+  }
+};
+
+// u = clamp(rint(x / d), -8, 7) + 8 of 8 elements, from x * (1 / d), whose error
+// of a few units matters next to a border only:
 //  - bf16: x has 8 bits and d 11, so x / d is exactly half an integer or at
 //    least 2^-12 away from one; rounded to a multiple of 2^-13 first, the
 //    approximate quotient then rounds as the exact one does, ties included.
 //  - fp32: blocks with a residual of d / 2 or more are done again, checked.
-// Four codes are packed as the number k0 + 16 k1 + 256 k2 + 4096 k3, exact in
-// fp32.  NaN and infinities make the block's scale NaN; a scale past fp16's
-// range saturates.
+// Adding 1.5 * 2^23 rounds to an integer and leaves it in the sum's low bits;
+// the codes are added up from those modulo 2^32.
 template <typename T>
-__device__ __forceinline__ uint32_t q4_word(const Raw8<T> &raw, __half *scale) {
+__device__ __forceinline__ uint32_t q4_codes(const Raw8<T> &raw, float df, bool hard) {
   float x[8];
   raw.floats(x);
-  float top = top8(raw, x);
-  top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, 1));
-  top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, 2));
-  const float seventh = 1.f / 7.f, q0 = __fmul_rn(top, seventh);
-  const float quot = __fmaf_rn(__fmaf_rn(-q0, 7.f, top), seventh, q0);
-  const __half d = __float2half_rn(fminf(quot, 65504.f));
-  const float df = __half2float(d);
-  const bool finite = top < INFINITY;    // false for NaN too
-  *scale = finite ? d : __ushort_as_half((unsigned short)0x7fffu);
-  if (!finite || df == 0.f) return 0x88888888u;
-  const float big = 12582912.f;          // 1.5 * 2^23: adding it rounds to an integer
+  const float big = 12582912.f;          // 1.5 * 2^23
+  constexpr uint32_t kBits = 0x4b400000u, kBias = 0x88888888u - kBits * 0x11111111u;
   float inv;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(df));
   float off = 0.f;
-  float2 k[4];                           // dims i and i + 4, two at a time
+  uint32_t b[8];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float2 v = make_float2(x[i], x[i + 4]);
+    const float2 v = make_float2(x[2 * i], x[2 * i + 1]);
+    float2 k;
     if (sizeof(T) == 2) {
-      const float2 q = fadd2(ffma2(v, dup(inv), dup(1536.f)), dup(-1536.f));
-      k[i] = fadd2(fadd2(q, dup(big)), dup(-big));
+      k = fadd2(ffma2(v, dup(inv), dup(1536.f)), dup(big - 1536.f));
     } else {
-      k[i] = fadd2(ffma2(v, dup(inv), dup(big)), dup(-big));
-      const float2 e = ffma2(k[i], dup(-df), v);
+      k = ffma2(v, dup(inv), dup(big));
+      const float2 e = ffma2(fadd2(k, dup(-big)), dup(-df), v);
       off = fmaxf(off, fmaxf(fabsf(e.x), fabsf(e.y)));
     }
+    b[2 * i] = __float_as_uint(k.x);
+    b[2 * i + 1] = __float_as_uint(k.y);
   }
-  if ((sizeof(T) == 4 && off >= 0.5f * df) || top > 7.5f * df)
+  if (df == 0.f) return 0x88888888u;
+  if ((sizeof(T) == 4 && off >= 0.5f * df) || hard)
     return q4_word_checked(make_float4(x[0], x[1], x[2], x[3]), make_float4(x[4], x[5], x[6], x[7]), df, inv);
-  const float2 four = ffma2(ffma2(ffma2(k[3], dup(16.f), k[2]), dup(16.f), k[1]), dup(16.f), k[0]);
-  // + 0x8888: every code + 8, in the low 16 bits
-  const float2 bits = fadd2(four, dup(big + 34952.f));
-  return __byte_perm(__float_as_uint(bits.x), __float_as_uint(bits.y), 0x5410);
+#pragma unroll
+  for (int o = 1; o < 8; o *= 2)
+#pragma unroll
+    for (int i = 0; i < 8; i += 2 * o) b[i] += b[i + o] << (4 * o);
+  return b[0] + kBias;
+}
+
+// One Q4_0 block is held by 4 neighbouring lanes, 8 dims each.
+template <typename T>
+__device__ __forceinline__ uint32_t q4_word(const Raw8<T> &raw, __half *scale) {
+  float top = top8(raw);
+  top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, 1));
+  top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, 2));
+  const Q4Scale q(top);
+  *scale = q.d;
+  return q4_codes(raw, q.df, q.hard);
+}
+
+// N blocks at once: the four lanes share out the blocks' scales; lane cc < N
+// answers that of block cc.
+template <int N, typename T>
+__device__ __forceinline__ __half q4_words(const Raw8<T> (&raw)[N], uint32_t (&w)[N]) {
+  static_assert(N == 1 || N == 2 || N == 4, "blocks per four lanes");
+  const int lane = threadIdx.x & 31;
+  float t[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) t[i] = top8(raw[i]);
+  if constexpr (N == 4) {
+    const bool up = lane & 2;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float theirs = __shfl_xor_sync(0xffffffffu, up ? t[i] : t[i + 2], 2);
+      t[i] = max_nan(up ? t[i + 2] : t[i], theirs);
+    }
+  }
+  if constexpr (N >= 2) {
+    const float theirs = __shfl_xor_sync(0xffffffffu, (lane & 1) ? t[0] : t[1], 1);
+    t[0] = max_nan((lane & 1) ? t[1] : t[0], theirs);
+  } else {
+    t[0] = max_nan(t[0], __shfl_xor_sync(0xffffffffu, t[0], 1));
+  }
+  if constexpr (N < 4) t[0] = max_nan(t[0], __shfl_xor_sync(0xffffffffu, t[0], 2));
+  const Q4Scale q(t[0]);
+  const bool hard = __any_sync(0xffffffffu, q.hard);
+#pragma unroll
+  for (int i = 0; i < N; ++i) w[i] = q4_codes(raw[i], __shfl_sync(0xffffffffu, q.df, (lane & ~3) | i), hard);
+  return q.d;
 }
 
 // What a slot's append does, from the device's counts.
@@ -269,11 +321,15 @@ __global__ void __launch_bounds__(kStepThreads) k_kv4_append_step(const __grid_c
 // K words go straight to their place; V words hold 8 positions of one dim, so
 // 8 x 8 nibbles are transposed by one thread each through shared memory, and a
 // chunk that already holds entries keeps their nibbles.  The last of the slot's
-// CTAs to have read the length moves it.  Bound by the rows' bytes.
-constexpr int kAppendThreads = 256, kAppendChunks = 4;
+// CTAs to have read the length moves it.  Bound by the rows' bytes in fp32
+// (8191 tokens of 32 heads at head_dim 128 in 48.9 us, 6.3 TB/s) and by the
+// quantiser's instructions in bf16 (32.8 us, 5.2 TB/s; at head_dim 64 4.2 TB/s).
+// Four CTAs per SM: fp32 with the 71 registers that it would take 50.4 -> 52.3 us,
+// bf16 at 48 registers 33.4 -> 32.6 us but four short prompts 5.7 -> 6.1 us.
+constexpr int kAppendThreads = 256, kAppendChunks = 8;
 
 template <int NG, typename T>
-__global__ void __launch_bounds__(kAppendThreads) k_kv4_append(const __grid_constant__ Kv4AppendArgs a) {
+__global__ void __launch_bounds__(kAppendThreads, sizeof(T) == 4 ? 4 : 0) k_kv4_append(const __grid_constant__ Kv4AppendArgs a) {
   constexpr int TPR = 4 * NG;                     // threads (words) per row
   constexpr int RPP = 128 / TPR;                  // rows per pass: 8, 16, 32
   constexpr int PASSES = kKv4Chunk / RPP;
@@ -318,9 +374,7 @@ __global__ void __launch_bounds__(kAppendThreads) k_kv4_append(const __grid_cons
     uint8_t *scales = chunk + (is_v ? kv4_vscale_off(NG) : kv4_kscale_off(NG));
     uint32_t *vc = vcode[ch & 1];
     uint32_t w[PASSES];
-    __half d[PASSES];
-#pragma unroll
-    for (int i = 0; i < PASSES; ++i) w[i] = q4_word(raw[i], &d[i]);
+    const __half d = q4_words(raw, w);            // the scale of row r0 + cc RPP
     if (ch + 1 < ch1) fetch(ch + 1);
     if (is_v) {
 #pragma unroll
@@ -329,11 +383,10 @@ __global__ void __launch_bounds__(kAppendThreads) k_kv4_append(const __grid_cons
 #pragma unroll
     for (int i = 0; i < PASSES; ++i) {
       const int p = r0 + i * RPP;
-      if (p < lo || p >= hi) continue;
-      if (!is_v) *reinterpret_cast<uint32_t *>(chunk + kv4_kword(NG, p, cc, j)) = w[i];
-      if (cc == 0)
-        *reinterpret_cast<__half *>(scales + (is_v ? kv4_vscale(NG, p, j) : kv4_kscale(NG, p, j))) = d[i];
+      if (!is_v && p >= lo && p < hi) *reinterpret_cast<uint32_t *>(chunk + kv4_kword(NG, p, cc, j)) = w[i];
     }
+    if (const int p = r0 + cc * RPP; cc < PASSES && p >= lo && p < hi)
+      *reinterpret_cast<__half *>(scales + (is_v ? kv4_vscale(NG, p, j) : kv4_kscale(NG, p, j))) = d;
     if (tid >= lo && tid < hi) {
       a.l.ids[bh * a.l.cap + p0 + tid] = rg.seen0 + (p0 + tid - rg.start);
       a.l.weights[bh * a.l.cap + p0 + tid] = 0.f;
@@ -914,8 +967,9 @@ __global__ void k_kv4_reset(int32_t *len, int32_t *seen, int64_t stride, int n_l
 // chunks that T rows from any position touch at most, in groups
 int chunk_groups(int T, int group) { return ((T + kKv4Chunk - 2) / kKv4Chunk + group) / group; }
 
-// Chunks per CTA: up to `most`, fewer while all CTAs fit the GPU at once (four
-// on each of 152 SMs).  bf16 append / fp32 read, us, always four chunks against
+// Chunks per CTA: up to `most` (append 8: one prompt of 8191 in fp32 48.9 us against
+// 50.4 with four and 57.0 with two; 8 x 4096 at head_dim 32 in fp32 15.0, 16.9,
+// 20.5), fewer while all CTAs fit the GPU at once (four on each of 152 SMs).  bf16 append / fp32 read, us, always four chunks against
 // this rule and against always one: 1 sequence x 8 heads x 256 tokens 6.1 / 5.9,
 // 3.1 / 3.0, 3.0 / 3.1; 4 x 8 x 1031 7.8 / 8.4, 6.6 / 8.1, 7.2 / 8.4; 1 x 32 x
 // 8191 35.4 / 49.5, 35.3 / 49.6, 43.6 / 53.8.
