@@ -598,11 +598,9 @@ __global__ void __launch_bounds__(kKv4Threads, kKv4CtasPerSm)
           l[k] += p[k];
         }
         if (PAIR) {
-          const float h = __half2float(__float2half_rn(p[0]));
-          const uint32_t mine = transpose8(pack_half2(make_float2(h, p[0] - h)));
-          const uint32_t other = __shfl_xor_sync(0xffffffffu, mine, 4);
-          xh[t] = (r & 1) ? other : mine;
-          xl[t] = (r & 1) ? mine : 0u;
+          const uint32_t h = pack_half2(make_float2(p[0], p[0]));
+          xh[t] = transpose8(h);
+          xl[t] = transpose8(pack_half2(make_float2(0.f, p[0] - __low2float(as_half2(h)))));
         } else {
           const uint32_t h = pack_half2(make_float2(p[0], p[RL - 1]));
           xh[t] = transpose8(h);
