@@ -248,7 +248,7 @@ struct AppendRange {
 // First every (token, head, K or V) row is quantised, TPR threads each; then
 // each 16-byte unit of V words (8 positions of 4 dims) that holds a new
 // position is read, completed and written by one thread.  Bound by its four
-// dependent trips to memory.
+// dependent trips to memory (one token of 64 slots x 8 heads, bf16: 3.0 us).
 constexpr int kStepThreads = 512;
 
 template <int NG, typename T>
@@ -468,7 +468,8 @@ __device__ __forceinline__ float half_at(const uint8_t *p) {
   return __half2float(*reinterpret_cast<const __half *>(p));
 }
 
-// Few tokens: a thread per 8 dims of a row, straight from the cache.
+// Few tokens: a thread per 8 dims of a row, straight from the cache.  Bound by
+// latency (one token of 64 slots x 8 heads 2.3 us).
 template <int NG, typename T>
 __global__ void __launch_bounds__(256) k_kv4_read_step(const __grid_constant__ Kv4ReadArgs a) {
   constexpr int TPR = 4 * NG, CH = kv4_chunk_bytes(NG);
@@ -508,7 +509,8 @@ __global__ void __launch_bounds__(256) k_kv4_read_step(const __grid_constant__ K
 // Many tokens: CTAs of up to kReadChunks chunks of one (slot, KV head), which one
 // bulk copy brings into shared memory; then 8 dims of a K position per thread,
 // and 8 x 8 nibbles of V (8 positions, 8 dims) per thread.  Bound by the
-// values' bytes.
+// values' bytes (8191 tokens of 32 heads at head_dim 128: bf16 28.0 us, fp32 49.3
+// us, 6.2 TB/s).
 constexpr int kReadThreads = 256, kReadChunks = 4, kReadStepTokens = 16;
 
 template <int NG, typename T>
@@ -588,7 +590,9 @@ __global__ void __launch_bounds__(kReadThreads) k_kv4_read(const __grid_constant
 // first ones stay.  Then the kept entries behind the budget ("movers") fill the
 // dropped ones' places below it ("holes"), both in index order: src_of[p] is p
 // or, for hole r, -1 - r, and movers[r] what goes there.  Bound by the latency
-// of its barriers.
+// of its barriers (8 heads each: 64 slots at 1000 entries 8 us, four at 32k in
+// clusters of eight CTAs 17 us; CTAs of 512 or 1024 threads with as many entries
+// 8.9 and 13 us, 17 and 25 us).
 template <int THREADS, int K>
 __global__ void __launch_bounds__(THREADS, THREADS >= 1024 ? 1 : 3) k_kv4_select(const __grid_constant__ Kv4EvictArgs a) {
   constexpr int WARPS = THREADS / 32, COPIES = 4, BITS = 10, BINS = 1 << BITS;
@@ -831,7 +835,9 @@ constexpr int kMoveThreads = 128, kMoveChunks = 2;
 // Sources of moves lie at or behind the budget and destinations below it, so
 // the CTAs do not depend on one another; in the chunk that holds the budget's
 // border a V word may be read by others while its owner replaces it, with the
-// nibbles that they read unchanged (32-bit accesses).
+// nibbles that they read unchanged (32-bit accesses).  Bound by the gathered V
+// words, which hold 8 positions each (8 heads, head_dim 128: four slots of 32k to
+// 8192 29 us, 130 MB; copies of 64 slots at 1000 entries 25.5 us, 157 MB, 6.2 TB/s).
 template <int NG>
 __global__ void __launch_bounds__(kMoveThreads, 8) k_kv4_move(const __grid_constant__ Kv4EvictArgs a) {
   constexpr int CH = kv4_chunk_bytes(NG), POS = kMoveChunks * kKv4Chunk;

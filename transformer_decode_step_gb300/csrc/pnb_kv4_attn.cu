@@ -268,10 +268,15 @@ __device__ __forceinline__ void finish_row(const Kv4AttnArgs &a, int b, int h, i
 // ragged slots 41.4 against 42.4, 8 KV heads at 8192 positions 10.2 against 11.6,
 // at 32768 15.4 against 16.9; 32 MHA heads at 2048 9.8 against 9.2, at 4096 11.4
 // against 11.3.
-// Bound by the latency of a warp's dependent steps (copy, scores, maximum,
-// weights, products) rather than by memory: 128k positions of 8 KV heads
-// (head_dim 128, fp32 rows) are read at 4.7 TB/s, 64 slots at 3.8, start, merge
-// and launch included; with few units the start and the merges are all there is.
+// 64 slots at 512..4096 positions (8 x 4 heads, head_dim 128, fp32) take 41.4 us
+// (3.8 TB/s), two contexts of 100k and 128k (bf16) 56.8 us (4.7 TB/s).  With the
+// copies alone, no products, they take 34.2 and 45.2: about 23 and 39 for the
+// bytes, the rest for launch, start (lengths, queries and first chunk in turn)
+// and merges, which is all that short caches have.  What the products add is
+// bound by the unpacking, 9 instructions for 8 codes, on the integer pipe (56 to
+// 59 % busy over the launch).  No gain from: queries or V scales in wider shared
+// loads, the shift of a code word as a multiplication (64 slots 43.7 us), the
+// masks of odd columns as multiplications, the next entries of the merge ahead.
 template <int NG, bool PAIR, bool SPLIT, bool TRACK>
 __global__ void __launch_bounds__(kKv4Threads, kKv4CtasPerSm)
     k_kv4_attn(const __grid_constant__ Kv4AttnArgs a) {
@@ -852,7 +857,9 @@ __global__ void __launch_bounds__(kKv4Threads, kKv4CtasPerSm)
 }
 
 // weights[j] = decay * weights[j] + sum over the rows of 2^(x_ij - lse_i): each
-// position has one owner that adds its rows in order.
+// position has one owner that adds its rows in order.  Bound by latency (8 slots
+// at 512..4096, 8 x 4 heads: 4 us behind the attention's 14) and, with many rows,
+// by the scores' bytes (16 rows of 32 heads at 6007 positions, 12 MB: 6 us).
 constexpr int kWeightThreads = 128, kWeightUnit = 4 * kWeightThreads;
 
 __global__ void __launch_bounds__(kWeightThreads) k_kv4_weights(const __grid_constant__ Kv4WeightArgs a) {
