@@ -439,6 +439,23 @@ def test_attention_work_splits(B, n_kv, G, hd, lo, hi):
     assert c.device_error() == 0
 
 
+@pytest.mark.parametrize("longest", [31, 832, 833])      # below, at and past what one CTA keeps whole
+@pytest.mark.parametrize("B,n_kv,G,hd,T", [(2, 3, 2, 128, 1), (37, 4, 8, 64, 3), (70, 3, 1, 128, 2), (9, 32, 4, 32, 5)])
+def test_attention_ragged_slots_some_empty(B, n_kv, G, hd, T, longest):
+    c, ref = make(B, n_kv * G, n_kv, hd, 864, track=T), Ref(B, n_kv * G, n_kv, hd, 864)
+    lens = [longest if b == B // 2 else 0 if b % 5 == 4 else (53 * b * b) % (longest + 1) for b in range(B)]
+    k, v = rows((B, longest, n_kv, hd), 313, BF16, 1.5), rows((B, longest, n_kv, hd), 314, BF16)
+    c.append(0, k, v, n_new=i32(lens))
+    ref.append(k, v, lens)
+    q = rows((B, T, n_kv * G, hd), 315, F32, 2.0)
+    a = check_attention(c, ref, q, decay=0.0)
+    check_attention(c, ref, q.to(BF16))
+    b = torch.empty_like(a)
+    c.attention(0, q, b)
+    assert torch.equal(a, b)                  # the same bits, tracked or not
+    assert c.device_error() == 0
+
+
 def test_offsets_past_32_bits():
     """A cache of 10 GB and 2^32 tracked scores: the last slot's entries, scores and moves lie behind
     4 GiB.  Rows of all slots are one tensor's (slot stride 0); the other slots stay empty."""

@@ -35,10 +35,11 @@ namespace {
 // drafted tokens over ragged slots 16.9 us with one, 15.3 with two, 15.9 with
 // three).
 constexpr int kItemUnits = 2;
-// items of at most this many units on average are not split over CTAs while
-// there are enough CTAs for them (8 KV heads of one sequence, head_dim 128, whole
-// against split, us: 6 units 5.8, 8.6; 10 units 6.4, 9.3; 18 units 8.2, 9.3; 26
-// units 9.1, 9.4; 34 units 10.2, 9.5; 50 units 12.3, 9.6)
+// While no item has more units than this, none is split over CTAs (head_dim 128,
+// us, whole against split: 8 KV heads of one sequence 6 units 5.8, 8.6; 18 units
+// 8.2, 9.3; 26 units 9.1, 9.4; 34 units 10.2, 9.5.  21 slots x 4 heads x 3 blocks
+// of rows, lengths up to 200 10.6, 16.2; all 800 17.7, 20.1.  64 x 8 heads, all
+// 100 10.9, 12.7; all 600 19.1, 18.3; all 1200 27.3, 26.5)
 constexpr int kWholeUnits = 28;
 
 template <int NG, bool PAIR, bool SPLIT>
@@ -54,8 +55,9 @@ struct AttnSmem {
   static constexpr int kPart = kBars + kKv4Warps * kStages * 8;     // int4 [2 warps]: item of each partial
   static constexpr int kMl = kPart + kKv4Warps * 2 * 16;            // float2 [2 warps][8]: reference, sum
   static constexpr int kFlag = kMl + kKv4Warps * 2 * kKv4Rows * 8;
-  static constexpr int kPre = kFlag + 16;                           // int [n_slot + 1]
-  static int bytes(int n_slot) { return kPre + (2 * n_slot + 2) * 4; }   // and the lengths, and a count
+  static constexpr int kSpan = kFlag + 16;                          // the CTA's units, the number of CTAs
+  static constexpr int kPre = kSpan + 16;                           // int [n_slot + 1]
+  static int bytes(int n_slot) { return kPre + (2 * n_slot + 3) * 4; }   // and the lengths, their count and largest
 };
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -171,6 +173,13 @@ __device__ __forceinline__ Segment segment_at(const int *pre, const int *lens, c
   s.c1 = max(0, off + s.units - kItemUnits);
   s.first = x - off + kItemUnits;
   return s;
+}
+
+// The first unit of the item that unit x belongs to.  Out of line: inlined, its
+// code on the way of all calls cost 0.1 to 0.3 us each.
+__device__ __noinline__ int item_start(const int *pre, const int *lens, int n_slot, int x) {
+  const int b = kv4_find(pre, n_slot, x), per = (lens[b] + kKv4Chunk - 1) / kKv4Chunk + kItemUnits;
+  return x - (int)((unsigned)(x - pre[b]) % (unsigned)per);
 }
 
 // The equal split of `total` units: part i of n takes [start(i), start(i + 1)),
@@ -290,6 +299,7 @@ __global__ void __launch_bounds__(kKv4Threads, kKv4CtasPerSm)
   int4 *spart = reinterpret_cast<int4 *>(smem + L::kPart);
   float2 *sml = reinterpret_cast<float2 *>(smem + L::kMl);
   int *sflag = reinterpret_cast<int *>(smem + L::kFlag);
+  int4 *sspan = reinterpret_cast<int4 *>(smem + L::kSpan);
   int *pre = reinterpret_cast<int *>(smem + L::kPre), *lens = pre + a.n_slot + 1;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r = lane >> 2, c = lane & 3;
   uint2 *qs = reinterpret_cast<uint2 *>(smem + L::kQ) + warp * L::kQSets * 2 * NG * 32 + lane;
@@ -308,15 +318,25 @@ __global__ void __launch_bounds__(kKv4Threads, kKv4CtasPerSm)
   }
   __syncthreads();
   const int total = pre[a.n_slot], cta = blockIdx.x;
-  // One unit per warp at least, except that short items get a CTA each: rows
+  // One unit per warp at least, except that short items stay in one CTA: rows
   // shared by CTAs cost about 3 us more.
   const int items = lens[a.n_slot] * a.n_kv * a.nrb;
-  const int ctas = items <= (int)gridDim.x && total <= items * kWholeUnits
-                       ? max(1, items)
-                       : max(1, min((int)gridDim.x, total / kKv4Warps));
-  const Split by_cta(total, ctas);   // and each CTA's part is split over its warps the same way
-  const int u0 = by_cta.start(cta), u1 = by_cta.start(cta + 1);
-  const int x0 = u0 + (u1 - u0) * warp / kKv4Warps, x1 = u0 + (u1 - u0) * (warp + 1) / kKv4Warps;
+  const int longest = (lens[a.n_slot + 1] + kKv4Chunk - 1) / kKv4Chunk + kItemUnits;
+  const bool whole = longest <= kWholeUnits;
+  const bool each = total == items * longest && items <= (int)gridDim.x;   // a CTA each
+  const int ctas = max(1, min((int)gridDim.x, !whole ? total / kKv4Warps : each ? items : total));
+  int x0, x1;
+  {
+    const Split by_cta(total, ctas);   // and each CTA's part is split over its warps the same way
+    int u0 = by_cta.start(cta), u1 = by_cta.start(cta + 1);
+    if (whole && !each) {              // the items that begin in it
+      if (u0 < total) u0 = item_start(pre, lens, a.n_slot, u0);
+      if (u1 < total) u1 = item_start(pre, lens, a.n_slot, u1);
+    }
+    x0 = u0 + (u1 - u0) * warp / kKv4Warps;
+    x1 = u0 + (u1 - u0) * (warp + 1) / kKv4Warps;
+    if (tid == 0) *sspan = make_int4(u0, u1, ctas, 0);   // for the end: the loop needs the registers
+  }
 
   // slots with nothing to attend to answer zero
   for (int b = cta; b < a.n_slot; b += gridDim.x) {
@@ -329,7 +349,6 @@ __global__ void __launch_bounds__(kKv4Threads, kKv4CtasPerSm)
   }
   if (cta >= ctas || total == 0) return;
 
-  const int64_t head_bytes = (int64_t)(a.l.cap / kKv4Chunk) * L::kChunk;
   // producer: next segment's first unit, next chunk, segment's end
   int px = x0, pc = 0, pc1 = 0;
   const uint8_t *pbase = nullptr;
@@ -337,7 +356,7 @@ __global__ void __launch_bounds__(kKv4Threads, kKv4CtasPerSm)
     px += ps.units;
     pc = ps.c0;
     pc1 = ps.c1;
-    pbase = a.l.codes + ((int64_t)ps.b * a.n_kv + ps.h) * head_bytes;
+    pbase = a.l.codes + ((int64_t)ps.b * a.n_kv + ps.h) * (a.l.cap / kKv4Chunk) * L::kChunk;
   };
   int pstage = 0;
   bool dead = false;
@@ -357,7 +376,7 @@ __global__ void __launch_bounds__(kKv4Threads, kKv4CtasPerSm)
   int stage = 0;
   uint32_t phase = 0;
   bool primed = false, early = false;
-  float *early_part = a.warp_part + ((int64_t)cta * kKv4Warps + warp) * kKv4Rows * HD + lane;
+  auto early_part = [&]() { return a.warp_part + ((int64_t)blockIdx.x * kKv4Warps + warp) * kKv4Rows * HD + lane; };
   const int vunit_off = kv4_vunit(0, r, c);
   uint32_t magic = 0x64006400u;
   asm volatile("" : "+r"(magic));
@@ -701,7 +720,7 @@ __global__ void __launch_bounds__(kKv4Threads, kKv4CtasPerSm)
 #pragma unroll
         for (int i = 0; i < NG * 4; ++i) {
           if (pd) pd[i0 * PITCH + r + 8 * i] = out_of(k, i);
-          else early_part[(k * NG * 4 + i) * 32] = out_of(k, i);
+          else early_part()[(k * NG * 4 + i) * 32] = out_of(k, i);
         }
       }
     }
@@ -712,11 +731,13 @@ __global__ void __launch_bounds__(kKv4Threads, kKv4CtasPerSm)
       const int i0 = PAIR ? c : 2 * c + k;
 #pragma unroll
       for (int i = 0; i < NG * 4; ++i)
-        reinterpret_cast<float *>(ring)[i0 * PITCH + r + 8 * i] = early_part[(k * NG * 4 + i) * 32];
+        reinterpret_cast<float *>(ring)[i0 * PITCH + r + 8 * i] = early_part()[(k * NG * 4 + i) * 32];
     }
   }
   __syncthreads();
 
+  const int4 span = *sspan;
+  const int u0 = span.x, u1 = span.y;
   // The CTA's partial rows, in the units' order: entry 2 w is warp w's item
   // from before, 2 w + 1 the one that it starts.  Consecutive entries of one
   // item form a group; the warps share out the groups' rows.
@@ -788,6 +809,7 @@ __global__ void __launch_bounds__(kKv4Threads, kKv4CtasPerSm)
   const int slot = tid - (kKv4Threads - 32);   // lanes 0 and 1 of the last warp: front and back
   int n = 0, c0 = 0;
   if (slot == 0 || slot == 1) {
+    const Split by_cta(pre[a.n_slot], span.z);
     const Item it = slot ? back : front;
     if (slot ? at_back : at_front) {
       c0 = by_cta.part_of(it.first);
