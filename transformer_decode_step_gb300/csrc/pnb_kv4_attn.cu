@@ -882,34 +882,43 @@ __global__ void __launch_bounds__(kKv4Threads, kKv4CtasPerSm)
 // position has one owner that adds its rows in order.  Bound by latency (8 slots
 // at 512..4096, 8 x 4 heads: 4 us behind the attention's 14) and, with many rows,
 // by the scores' bytes (16 rows of 32 heads at 6007 positions, 12 MB: 6 us).
-constexpr int kWeightThreads = 128, kWeightUnit = 4 * kWeightThreads;
+// Each thread has four positions; PARTS groups of threads share out the rows of
+// the same positions, and the first adds up the groups' sums in order.
+constexpr int kWeightThreads = 128;
 
+template <int PARTS>
 __global__ void __launch_bounds__(kWeightThreads) k_kv4_weights(const __grid_constant__ Kv4WeightArgs a) {
-  extern __shared__ int wpre[];
+  constexpr int GROUP = kWeightThreads / PARTS, UNIT = 4 * GROUP;
+  extern __shared__ __align__(16) uint8_t wsmem[];
+  float4 *sums = reinterpret_cast<float4 *>(wsmem);       // [PARTS - 1][GROUP]
+  int *wpre = reinterpret_cast<int *>(sums + (PARTS - 1) * GROUP);
+  const int part = PARTS == 1 ? 0 : threadIdx.x / GROUP, at = threadIdx.x % GROUP;
   pdl_wait();
-  if (threadIdx.x < 32) kv4_prefix(a.l, a.n_slot, kWeightUnit, 0, a.n_kv, wpre, nullptr);
+  if (threadIdx.x < 32) kv4_prefix(a.l, a.n_slot, UNIT, 0, a.n_kv, wpre, nullptr);
   __syncthreads();
-  const int total = wpre[a.n_slot];
+  const int total = wpre[a.n_slot], per_part = (a.rows + PARTS - 1) / PARTS;
   for (int u = blockIdx.x; u < total; u += gridDim.x) {
     const int b = kv4_find(wpre, a.n_slot, u), rel = u - wpre[b];
     const int per = (wpre[b + 1] - wpre[b]) / a.n_kv, h = rel / per;
     const int len = kv4_len(a.l, b);
-    const int p = (rel - h * per) * kWeightUnit + 4 * (int)threadIdx.x;
-    if (p >= len) continue;
+    const int p = (rel - h * per) * UNIT + 4 * at;
+    if (PARTS == 1 && p >= len) continue;
     const int64_t bh = (int64_t)b * a.n_kv + h;
     const float *x = a.scores + bh * a.rows * a.l.cap + p, *lse = a.lse + bh * a.rows;
     float w[4] = {};
     float *dst = a.l.weights + bh * a.l.cap + p;
     float4 old = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (a.decay > 0.f) old = *reinterpret_cast<const float4 *>(dst);
-    for (int i0 = 0; i0 < a.rows; i0 += 8) {     // eight rows' loads in flight
+    const bool live = PARTS == 1 || p < len;
+    if (live && part == 0 && a.decay > 0.f) old = *reinterpret_cast<const float4 *>(dst);
+    const int end = PARTS == 1 ? a.rows : live ? min((part + 1) * per_part, a.rows) : 0;
+    for (int i0 = PARTS == 1 ? 0 : part * per_part; i0 < end; i0 += 8) {     // eight rows' loads in flight
       float4 v[8];
       float z[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const int row = min(i0 + i, a.rows - 1);
+        const int row = min(i0 + i, end - 1);
         v[i] = *reinterpret_cast<const float4 *>(x + (int64_t)row * a.l.cap);
-        z[i] = i0 + i < a.rows ? lse[row] : INFINITY;
+        z[i] = i0 + i < end ? lse[row] : INFINITY;
       }
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
@@ -917,6 +926,19 @@ __global__ void __launch_bounds__(kWeightThreads) k_kv4_weights(const __grid_con
         w[2] += ex2(v[i].z - z[i]); w[3] += ex2(v[i].w - z[i]);
       }
     }
+    if constexpr (PARTS > 1) {
+      if (part > 0) sums[(part - 1) * GROUP + at] = make_float4(w[0], w[1], w[2], w[3]);
+      __syncthreads();
+      if (part == 0) {
+#pragma unroll
+        for (int k = 0; k < PARTS - 1; ++k) {
+          const float4 s = sums[k * GROUP + at];
+          w[0] += s.x; w[1] += s.y; w[2] += s.z; w[3] += s.w;
+        }
+      }
+      __syncthreads();
+    }
+    if (part > 0) continue;
     const float held[4] = {old.x, old.y, old.z, old.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -972,10 +994,20 @@ cudaError_t launch_kv4_attn(int ng, const Kv4AttnArgs &a, int grid, cudaStream_t
   return ng == 4 ? run_attn<4>(a, grid, st) : ng == 2 ? run_attn<2>(a, grid, st) : run_attn<1>(a, grid, st);
 }
 
-cudaError_t launch_kv4_weights(const Kv4WeightArgs &a, cudaStream_t st) {
-  const int64_t units = (int64_t)a.n_slot * a.n_kv * ((a.l.cap + kWeightUnit - 1) / kWeightUnit);
+template <int PARTS>
+cudaError_t run_weights(const Kv4WeightArgs &a, cudaStream_t st) {
+  constexpr int unit = 4 * kWeightThreads / PARTS;
+  const int64_t units = (int64_t)a.n_slot * a.n_kv * ((a.l.cap + unit - 1) / unit);
   const int grid = (int)(units < 1216 ? units : 1216);   // 8 CTAs on each of 152 SMs
-  return kv4_launch(k_kv4_weights, dim3(grid), dim3(kWeightThreads), (a.n_slot + 1) * 4, 1, st, a);
+  const int smem = (PARTS - 1) * (kWeightThreads / PARTS) * 16 + (a.n_slot + 1) * 4;
+  return kv4_launch(k_kv4_weights<PARTS>, dim3(grid), dim3(kWeightThreads), smem, 1, st, a);
+}
+
+cudaError_t launch_kv4_weights(const Kv4WeightArgs &a, cudaStream_t st) {
+  // rows in one or four parts, tracked attention at head_dim 64, us: 64 rows, 2
+  // slots at 367 16.3, 12.4; 56 rows, 14 at 958 24.1, 18.5; 64 rows, 8 x 32768 72.0,
+  // 68.7; 24 rows, 15 x 20000 35.5, 36.4; 16 rows, 64 x 8 at 1000 42.6, 47.3
+  return a.rows < 32 ? run_weights<1>(a, st) : run_weights<4>(a, st);
 }
 
 }  // namespace pnb
