@@ -277,14 +277,14 @@ __device__ __forceinline__ void finish_row(const Kv4AttnArgs &a, int b, int h, i
 // ragged slots 41.4 against 42.4, 8 KV heads at 8192 positions 10.2 against 11.6,
 // at 32768 15.4 against 16.9; 32 MHA heads at 2048 9.8 against 9.2, at 4096 11.4
 // against 11.3.
-// 64 slots at 512..4096 positions (8 x 4 heads, head_dim 128, fp32) take 41.4 us
-// (3.8 TB/s), two contexts of 100k and 128k (bf16) 56.8 us (4.7 TB/s).  With the
+// 64 slots at 512..4096 positions (8 x 4 heads, head_dim 128, fp32) take 40.3 us
+// (3.9 TB/s), two contexts of 100k and 128k (bf16) 56.5 us (4.7 TB/s).  With the
 // copies alone, no products, they take 34.2 and 45.2: about 23 and 39 for the
 // bytes, the rest for launch, start (lengths, queries and first chunk in turn)
 // and merges, which is all that short caches have.  What the products add is
 // bound by the unpacking, 9 instructions for 8 codes, on the integer pipe (56 to
-// 59 % busy over the launch).  No gain from: queries or V scales in wider shared
-// loads, the shift of a code word as a multiplication (64 slots 43.7 us), the
+// 59 % busy over the launch).  No gain from: queries in wider shared
+// loads, the shift of a code word as a multiplication (64 slots 41.6 -> 43.7 us), the
 // masks of odd columns as multiplications, the next entries of the merge ahead.
 template <int NG, bool PAIR, bool SPLIT, bool TRACK>
 __global__ void __launch_bounds__(kKv4Threads, kKv4CtasPerSm)
@@ -323,7 +323,7 @@ __global__ void __launch_bounds__(kKv4Threads, kKv4CtasPerSm)
   const int items = lens[a.n_slot] * a.n_kv * a.nrb;
   const int longest = (lens[a.n_slot + 1] + kKv4Chunk - 1) / kKv4Chunk + kItemUnits;
   const bool whole = longest <= kWholeUnits;
-  const bool each = total == items * longest && items <= (int)gridDim.x;   // a CTA each
+  const bool each = whole && total == items * longest && items <= (int)gridDim.x;   // a CTA each
   const int ctas = max(1, min((int)gridDim.x, !whole ? total / kKv4Warps : each ? items : total));
   int x0, x1;
   {
