@@ -775,6 +775,32 @@ def test_two_caches_on_two_streams():
         assert bool(((o.double() - want).abs() <= tol).all())
 
 
+def test_a_cache_made_and_used_on_a_side_stream():
+    """Creation leaves the workspace ready for any stream: the default one is busy meanwhile, and a
+    torch side stream does not wait for it."""
+    B, H, Hkv, hd, n = 3, 8, 2, 64, 1500
+    ref = Ref(B, H, Hkv, hd, 1504)
+    k, v, q = rows((B, n, Hkv, hd), 350), rows((B, n, Hkv, hd), 351), rows((B, 1, H, hd), 352)
+    ref.append(k, v)
+    want, tol, wtol = ref.attention(q, 0.0)
+    a = torch.randn(4096, 4096, device="cuda")
+    s = torch.cuda.Stream()
+    out = torch.empty_like(q)
+    torch.cuda.synchronize()
+    for _ in range(100):
+        a = (a @ a).clamp(-1, 1)
+    with torch.cuda.stream(s):
+        c = pnb.Kv4Cache(1, B, H, Hkv, hd, 1504, track=1)
+        c.reset()
+        c.append(0, k, v)
+        c.attention(0, q, out, decay=0.0)
+        c.evict(0, 1000, 4, 100)
+    torch.cuda.synchronize()
+    assert bool(((out.double() - want).abs() <= tol).all())
+    assert c.lengths(0).tolist() == [1000] * B and c.device_error() == 0
+    assert float(c.weights(0)[:, :, :1000].sum()) <= B * H * (1 + wtol)
+
+
 def test_a_copied_buffer_is_a_copied_cache():
     c, ref = make(2, 4, 2, 64, 64), Ref(2, 4, 2, 64, 64)
     k, v = rows((2, 50, 2, 64), 96), rows((2, 50, 2, 64), 97)

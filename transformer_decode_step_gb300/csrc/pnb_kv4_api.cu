@@ -69,6 +69,19 @@ Kv4Layer layer_of(const pnb_kvq *k, int layer) {
   return l;
 }
 
+// Zeroes device memory before it returns: the first call that reads it may be on
+// any stream, and a non-blocking one does not wait for a clear on the default
+// stream (which may itself be behind other work there).
+cudaError_t clear_now(void *p, size_t n) {
+  cudaStream_t st;
+  cudaError_t e = cudaStreamCreateWithFlags(&st, cudaStreamNonBlocking);
+  if (e != cudaSuccess) return e;
+  e = cudaMemsetAsync(p, 0, n, st);
+  const cudaError_t done = cudaStreamSynchronize(st);
+  cudaStreamDestroy(st);
+  return e != cudaSuccess ? e : done;
+}
+
 int check_call(const pnb_kvq *k, int layer) {
   int dev = -1;
   if (cudaGetDevice(&dev) != cudaSuccess) return PNB_E_CUDA;
@@ -197,7 +210,7 @@ int pnb_kvq_new(const pnb_kvq_config *cfg, void *buf_dev, size_t bytes, pnb_kvq 
   const size_t o_src = take(entries * 4), o_mov = take(entries * 4);
   const size_t o_lse = take(rows * 4), o_scores = take(rows * c.cap * 4);
   cudaError_t e = cudaMalloc(&k->ws, at);
-  if (e == cudaSuccess) e = cudaMemset(k->ws, 0, zeroed);
+  if (e == cudaSuccess) e = clear_now(k->ws, zeroed);
   if (e != cudaSuccess) {
     cudaGetLastError();
     if (k->ws) cudaFree(k->ws);
