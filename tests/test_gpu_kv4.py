@@ -282,6 +282,35 @@ def test_quantiser_bf16_ties(hd):
     check_content(c, ref)
 
 
+@pytest.mark.parametrize("T", [64, 96])      # the one-CTA-per-slot form and the chunked one
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("hard", [False, True])
+def test_quantiser_quotient_of_seven_and_a_half(T, dtype, hard):
+    """Blocks whose largest magnitude is 7.5 d exactly (d subnormal: n 2^-24, n = 1..6, the fp16 number
+    next to 7.5 n 2^-24 / 7): +7.5 rounds to the even 8 and is held as 7, at each place of a code
+    word, whatever other blocks (``hard``: a quotient above 7.5) share the warp."""
+    n = torch.arange(T) % 6 + 1
+    sign, at = 1.0 - 2.0 * (torch.arange(T) // 6 % 2), torch.arange(T) // 6 % 8
+    g = torch.Generator()
+    g.manual_seed(360)
+    d = n[:, None] * 2.0 ** -24
+    x = torch.randint(-6, 7, (T, 32), generator=g) * d
+    x[torch.arange(T), at + 8 * (torch.arange(T) % 4)] = 7.5 * sign * d[:, 0]
+    other = torch.randint(-6, 7, (T, 32), generator=g) * d
+    if hard:
+        other = torch.where(torch.arange(32) % 5 == 0, 8 * 2.0 ** -24, other.clamp(-6 * 2.0 ** -24, 6 * 2.0 ** -24))
+    x, other = (t.view(1, T, 1, 32).cuda().to(dtype) for t in (x, other))
+    assert float(x.double().abs().max()) == 45 * 2.0 ** -24 and not torch.equal(x, other)
+    assert torch.equal(held(x).abs().amax(-1)[0, :, 0].cpu(), (7.0 + (sign < 0)) * d[:, 0].double())
+    c = make(1, 1, 1, 32, 96)
+    for k, v in ((x, other), (other, x)):
+        c.reset()
+        ref = Ref(1, 1, 1, 32, 96)
+        c.append(0, k, v)
+        ref.append(k, v)
+        check_content(c, ref)
+
+
 @pytest.mark.parametrize("n_slot,n_kv,hd,T", [(3, 2, 128, 8), (300, 4, 128, 8), (300, 4, 128, 3), (5, 40, 32, 2),
                                               (2, 1, 64, 16), (2, 1, 64, 17), (1, 64, 128, 1), (4, 3, 128, 9)])
 @pytest.mark.parametrize("dtype", [F32, BF16])

@@ -119,14 +119,14 @@ __device__ __noinline__ uint32_t q4_word_checked(float4 a, float4 b, float df, f
 struct Q4Scale {
   __half d;
   float df;      // d, or 0 where all codes are 8
-  bool hard;     // some quotients lie outside [-8, 7]
+  bool hard;     // some quotients round outside [-8, 7] (7.5 itself to the even 8)
   __device__ __forceinline__ explicit Q4Scale(float top) {
     const float seventh = 1.f / 7.f, q0 = __fmul_rn(top, seventh);
     const float quot = __fmaf_rn(__fmaf_rn(-q0, 7.f, top), seventh, q0);
     const bool finite = top < INFINITY;  // false for NaN too
     d = __float2half_rn(fminf(quot, 65504.f));
     df = finite ? __half2float(d) : 0.f;
-    hard = df != 0.f && top > 7.5f * df;
+    hard = df != 0.f && top >= 7.5f * df;
     if (!finite) d = __ushort_as_half((unsigned short)0x7fffu);
   }
 };
