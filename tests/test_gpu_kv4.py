@@ -542,6 +542,46 @@ def test_extreme_values():
     check_attention(c, ref, q)
 
 
+@pytest.mark.parametrize("exponent", [20, 27, 28, 31, 60, 106, 119, 123])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("n_kv,G,T,n", [(2, 1, 1, 300), (1, 4, 2, 300), (2, 2, 1, 5000)])
+def test_attention_at_very_large_scores(n_kv, G, T, n, dtype, exponent):
+    """Queries up to 2^124 along one dim in which the keys hold whole numbers c <= 7: the scores of
+    the largest c lie above all others by far more than 100, so the answer is the mean of those entries'
+    values and they share the weight.  fp32 sums of equal terms: 2^-20 of the values covers them."""
+    B, hd = 3, 64
+    cap = -(-n // 32) * 32
+    g = torch.Generator(device="cuda")
+    g.manual_seed(370)
+    c = torch.randint(-7, 7, (B, n, n_kv), generator=g, device="cuda")
+    c[torch.rand((B, n, n_kv), generator=g, device="cuda") < 0.02] = 7
+    c[:, 0] = 7                                   # every query token sees it
+    k = torch.zeros((B, n, n_kv, hd), device="cuda")
+    k[..., 5] = c
+    k[..., 6] = 7                                 # the block's scale is 1
+    v = rows((B, n, n_kv, hd), 371)
+    q = torch.zeros((B, T, n_kv * G, hd), device="cuda")
+    q[..., 5] = (1 + torch.rand(q.shape[:3], generator=g, device="cuda")) * 2.0 ** exponent
+    q = q.to(dtype)
+    cache, ref = make(B, n_kv * G, n_kv, hd, cap, track=T), Ref(B, n_kv * G, n_kv, hd, cap)
+    cache.append(0, k, v)
+    ref.append(k, v)
+    assert torch.equal(ref.k[:, :, :n, 5], c.permute(0, 2, 1).double())
+    out = torch.empty_like(q)
+    cache.attention(0, q, out, decay=0.0)
+    weights = torch.zeros((B, n_kv, n), dtype=torch.float64, device="cuda")
+    for t in range(T):
+        m = n - T + 1 + t
+        p = (c[:, :m] == 7).permute(0, 2, 1).double()
+        p /= p.sum(-1, keepdim=True)
+        weights[..., :m] += G * p
+        want = torch.einsum("bhn,bhnd->bhd", p, ref.v[:, :, :m]).repeat_interleave(G, 1)
+        tol = 2.0 ** -20 * ref.v.abs().max() + (0 if dtype == F32 else 2.0 ** -8 * want.abs() + 2.0 ** -11 * ref.v.abs().max())
+        assert bool(((out[:, t].double() - want).abs() <= tol).all())
+    # roundings of an exponential (2^-22), a sum, its reciprocal and a product, over G T rows
+    assert bool(((cache.weights(0)[..., :n].double() - weights).abs() <= 2.0 ** -19 * weights + 1e-30).all())
+
+
 def test_non_finite_rows_stay_where_they_are():
     """A NaN in one slot's key, query row or value block poisons only what attends to it."""
     B, n, hd = 4, 70, 64

@@ -112,12 +112,13 @@ struct Kv4AttnArgs {
   unsigned *counter;              // [grid]
   int32_t *err;
   float *scores;                  // [n_slot][n_kv][rows][cap], log2 units (NULL: not tracked)
-  float *lse;                     // [n_slot][n_kv][rows]
+  float2 *wscale;                 // [n_slot][n_kv][rows] reference, reciprocal of the sum
 };
 
 struct Kv4WeightArgs {
   Kv4Layer l;
-  const float *scores, *lse;
+  const float *scores;
+  const float2 *wscale;
   int32_t n_slot, n_kv, rows;
   float decay;
 };

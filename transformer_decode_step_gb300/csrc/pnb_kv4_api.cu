@@ -19,7 +19,8 @@ struct pnb_kvq {
   // byte offsets within a layer, and a layer's bytes
   size_t o_ids = 0, o_weights = 0, o_len = 0, o_seen = 0, layer_bytes = 0;
   uint8_t *ws = nullptr;
-  float *part = nullptr, *part_ml = nullptr, *warp_part = nullptr, *scores = nullptr, *lse = nullptr;
+  float *part = nullptr, *part_ml = nullptr, *warp_part = nullptr, *scores = nullptr;
+  float2 *wscale = nullptr;
   unsigned *counter = nullptr;
   uint32_t *arrive = nullptr;
   int32_t *err = nullptr, *n_old = nullptr, *src_of = nullptr, *movers = nullptr;
@@ -208,7 +209,7 @@ int pnb_kvq_new(const pnb_kvq_config *cfg, void *buf_dev, size_t bytes, pnb_kvq 
   const size_t o_part = take(part_rows * c.head_dim * 4);
   const size_t o_wpart = take(part_rows / 2 * kKv4Warps * c.head_dim * 4);
   const size_t o_src = take(entries * 4), o_mov = take(entries * 4);
-  const size_t o_lse = take(rows * 4), o_scores = take(rows * c.cap * 4);
+  const size_t o_wscale = take(rows * 8), o_scores = take(rows * c.cap * 4);
   cudaError_t e = cudaMalloc(&k->ws, at);
   if (e == cudaSuccess) e = clear_now(k->ws, zeroed);
   if (e != cudaSuccess) {
@@ -226,7 +227,7 @@ int pnb_kvq_new(const pnb_kvq_config *cfg, void *buf_dev, size_t bytes, pnb_kvq 
   k->warp_part = reinterpret_cast<float *>(k->ws + o_wpart);
   k->src_of = reinterpret_cast<int32_t *>(k->ws + o_src);
   k->movers = reinterpret_cast<int32_t *>(k->ws + o_mov);
-  k->lse = reinterpret_cast<float *>(k->ws + o_lse);
+  k->wscale = reinterpret_cast<float2 *>(k->ws + o_wscale);
   k->scores = reinterpret_cast<float *>(k->ws + o_scores);
   *out = k;
   return PNB_OK;
@@ -327,14 +328,14 @@ int pnb_kvq_attention(pnb_kvq *c, int32_t layer, const pnb_rows *q, int32_t T, c
   a.counter = c->counter;
   a.err = c->err;
   a.scores = track ? c->scores : nullptr;
-  a.lse = track ? c->lse : nullptr;
+  a.wscale = track ? c->wscale : nullptr;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (launch_kv4_attn(c->ng, a, c->grid, st) != cudaSuccess) return PNB_E_CUDA;
   if (track) {
     Kv4WeightArgs w{};
     w.l = a.l;
     w.scores = a.scores;
-    w.lse = a.lse;
+    w.wscale = a.wscale;
     w.n_slot = a.n_slot;
     w.n_kv = a.n_kv;
     w.rows = a.rows;

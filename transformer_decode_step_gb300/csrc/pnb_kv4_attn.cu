@@ -250,7 +250,14 @@ __device__ __forceinline__ void ldcg_row(const float *p, float (&v)[N]) {
   }
 }
 
-// a row's output from its sums (lane: dims NG lane ..), and its log-sum for the weights
+// What turns a row's scores into weights: 2^(x - ref) times the sum's reciprocal
+// (as one number, ref + log2(sum) would round, most where scores are large).  A
+// row with nothing to attend to gets weights of 0.
+__device__ __forceinline__ float2 weight_scale(float ref, float sum) {
+  return sum != 0.f ? make_float2(ref, 1.f / sum) : make_float2(INFINITY, 0.f);
+}
+
+// a row's output from its sums (lane: dims NG lane ..), and what its weights are scaled with
 template <int NG, bool TRACK>
 __device__ __forceinline__ void finish_row(const Kv4AttnArgs &a, int b, int h, int row, int lane, float mref,
                                            float lsum, float (&os)[NG]) {
@@ -259,8 +266,7 @@ __device__ __forceinline__ void finish_row(const Kv4AttnArgs &a, int b, int h, i
 #pragma unroll
   for (int i = 0; i < NG; ++i) os[i] = lsum != 0.f ? os[i] * f : 0.f;
   store_row<NG>(a.out, b * a.out.slot + t * a.out.token + hq * a.out.head + lane * NG, os);
-  if (TRACK && lane == 0)
-    a.lse[((int64_t)b * a.n_kv + h) * a.rows + row] = lsum != 0.f ? mref + log2f(lsum) : INFINITY;
+  if (TRACK && lane == 0) a.wscale[((int64_t)b * a.n_kv + h) * a.rows + row] = weight_scale(mref, lsum);
 }
 
 // Every warp takes an equal, contiguous run of the units and works alone: its
@@ -434,7 +440,7 @@ __global__ void __launch_bounds__(kKv4Threads, kKv4CtasPerSm)
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
       int e = (int)(__float_as_uint(mx) >> 23) - 127;
-      e = min(max(e, -100), 100);
+      e = min(max(e, -100), 127);
       const float up = __uint_as_float((uint32_t)(10 - e + 127) << 23);
       const float scale = __uint_as_float((uint32_t)(e - 10 + 127) << 23) * a.qscale;
 #pragma unroll
@@ -564,6 +570,12 @@ __global__ void __launch_bounds__(kKv4Threads, kKv4CtasPerSm)
           hmax = __reduce_max_sync(0xffffffffu, hmax);
         }
       }
+      // The scores, rounded once: the maximum, the weights and what is stored come
+      // from the same numbers, so that at any size none lies above the maximum.
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int k = 0; k < RL; ++k) s[t][k] = __fmul_rn(s[t][k], rs[k]);
       if (tail) {
 #pragma unroll
         for (int t = 0; t < 4; ++t)
@@ -577,16 +589,17 @@ __global__ void __launch_bounds__(kKv4Threads, kKv4CtasPerSm)
       for (int k = 0; k < RL; ++k) {
         if (TRACK && score[k]) {
 #pragma unroll
-          for (int t = 0; t < 4; ++t) score[k][p0 + 8 * t] = s[t][k] * rs[k];
+          for (int t = 0; t < 4; ++t) score[k][p0 + 8 * t] = s[t][k];
         }
-        xm[k] = fmaxf(fmaxf(s[0][k], s[1][k]), fmaxf(s[2][k], s[3][k])) * rs[k];
+        xm[k] = fmaxf(fmaxf(s[0][k], s[1][k]), fmaxf(s[2][k], s[3][k]));
         move |= xm[k] > m[k] + 4.f;
       }
       const int evc = (int)(hmax >> 10) - 14;
       // The weights are scaled by 2^(10 - ev), V scales lying below 2^ev with
       // ev >= -1, and the reference moves only when a score exceeds it by 2^4
       // or a larger V scale arrives: p stays below 2^15 and p d below 2^14,
-      // inside fp16, and the fp32 sums need no rescaling otherwise.
+      // inside fp16, and the fp32 sums need no rescaling otherwise.  The reference is
+      // rounded up: where scores are so large that it rounds, p only gets smaller.
       if (__any_sync(0xffffffffu, move) || evc > ev) {
         ev = max(ev, evc);
 #pragma unroll
@@ -595,7 +608,7 @@ __global__ void __launch_bounds__(kKv4Threads, kKv4CtasPerSm)
           xm[k] = fmaxf(xm[k], __shfl_xor_sync(0xffffffffu, xm[k], 8));
           xm[k] = fmaxf(xm[k], __shfl_xor_sync(0xffffffffu, xm[k], 16));
           const float mn = fmaxf(m[k], xm[k]);
-          const float nref = (mn == -INFINITY ? 0.f : mn) - 10.f + (float)ev;
+          const float nref = __fadd_ru(mn == -INFINITY ? 0.f : mn, (float)(ev - 10));
           const float al = m[k] == -INFINITY ? 0.f : ex2(ref[k] - nref);
           m[k] = mn;
           ref[k] = nref;
@@ -618,7 +631,7 @@ __global__ void __launch_bounds__(kKv4Threads, kKv4CtasPerSm)
         float p[RL];
 #pragma unroll
         for (int k = 0; k < RL; ++k) {
-          p[k] = ex2(fmaf(s[t][k], rs[k], -ref[k]));
+          p[k] = ex2(__fadd_rn(s[t][k], -ref[k]));
           l[k] += p[k];
         }
         if (PAIR) {
@@ -703,8 +716,7 @@ __global__ void __launch_bounds__(kKv4Threads, kKv4CtasPerSm)
           const float v[1] = {l[k] != 0.f ? out_of(k, i) * f : 0.f};
           store_row<1>(a.out, at + 8 * i, v);
         }
-        if (TRACK && r == 0)
-          a.lse[((int64_t)sg.b * a.n_kv + sg.h) * a.rows + row] = l[k] != 0.f ? ref[k] + log2f(l[k]) : INFINITY;
+        if (TRACK && r == 0) a.wscale[((int64_t)sg.b * a.n_kv + sg.h) * a.rows + row] = weight_scale(ref[k], l[k]);
       }
     } else {
       const int which = sg.c0 == 0 ? 1 : 0;    // 1: the item starts here and goes on behind
@@ -878,7 +890,7 @@ __global__ void __launch_bounds__(kKv4Threads, kKv4CtasPerSm)
   }
 }
 
-// weights[j] = decay * weights[j] + sum over the rows of 2^(x_ij - lse_i): each
+// weights[j] = decay * weights[j] + sum over the rows of 2^(x_ij - ref_i) / l_i: each
 // position has one owner that adds its rows in order.  Bound by latency (8 slots
 // at 512..4096, 8 x 4 heads: 4 us behind the attention's 14) and, with many rows,
 // by the scores' bytes (16 rows of 32 heads at 6007 positions, 12 MB: 6 us).
@@ -904,7 +916,8 @@ __global__ void __launch_bounds__(kWeightThreads) k_kv4_weights(const __grid_con
     const int p = (rel - h * per) * UNIT + 4 * at;
     if (PARTS == 1 && p >= len) continue;
     const int64_t bh = (int64_t)b * a.n_kv + h;
-    const float *x = a.scores + bh * a.rows * a.l.cap + p, *lse = a.lse + bh * a.rows;
+    const float *x = a.scores + bh * a.rows * a.l.cap + p;
+    const float2 *scale = a.wscale + bh * a.rows;
     float w[4] = {};
     float *dst = a.l.weights + bh * a.l.cap + p;
     float4 old = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -913,17 +926,17 @@ __global__ void __launch_bounds__(kWeightThreads) k_kv4_weights(const __grid_con
     const int end = PARTS == 1 ? a.rows : live ? min((part + 1) * per_part, a.rows) : 0;
     for (int i0 = PARTS == 1 ? 0 : part * per_part; i0 < end; i0 += 8) {     // eight rows' loads in flight
       float4 v[8];
-      float z[8];
+      float2 z[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const int row = min(i0 + i, end - 1);
         v[i] = *reinterpret_cast<const float4 *>(x + (int64_t)row * a.l.cap);
-        z[i] = i0 + i < end ? lse[row] : INFINITY;
+        z[i] = i0 + i < end ? scale[row] : make_float2(INFINITY, 0.f);
       }
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        w[0] += ex2(v[i].x - z[i]); w[1] += ex2(v[i].y - z[i]);
-        w[2] += ex2(v[i].z - z[i]); w[3] += ex2(v[i].w - z[i]);
+        w[0] = fmaf(ex2(v[i].x - z[i].x), z[i].y, w[0]); w[1] = fmaf(ex2(v[i].y - z[i].x), z[i].y, w[1]);
+        w[2] = fmaf(ex2(v[i].z - z[i].x), z[i].y, w[2]); w[3] = fmaf(ex2(v[i].w - z[i].x), z[i].y, w[3]);
       }
     }
     if constexpr (PARTS > 1) {
