@@ -582,6 +582,97 @@ def test_attention_at_very_large_scores(n_kv, G, T, n, dtype, exponent):
     assert bool(((cache.weights(0)[..., :n].double() - weights).abs() <= 2.0 ** -19 * weights + 1e-30).all())
 
 
+def plain_fp32(ref, q):
+    """Outputs and weights of a plain fp32 computation on the held values, and the largest score."""
+    B, T, H, hd = q.shape
+    n, G = max(ref.len), H // ref.Hkv
+    kk, vv = ref.k[:, :, :n].float(), ref.v[:, :, :n].float()
+    qq = q.float().view(B, T, ref.Hkv, G, hd).permute(0, 2, 1, 3, 4).reshape(B, ref.Hkv, T * G, hd)
+    x = torch.matmul(qq, kk.transpose(2, 3)) * hd ** -0.5
+    limit = torch.arange(n - T + 1, n + 1, device="cuda").repeat_interleave(G)[:, None]
+    p = torch.softmax(torch.where(torch.arange(n, device="cuda") < limit, x, -torch.inf), -1)
+    out = torch.matmul(p, vv).view(B, ref.Hkv, T, G, hd).permute(0, 2, 1, 3, 4).reshape(B, T, H, hd)
+    return out, p.sum(2), float(x.abs().max())
+
+
+def check_as_exact_as_plain(c, ref, q):
+    """The fp32 output's error, in the norm over each 32-dim block, is at most twice that of plain fp32
+    (both are random sums over the rows and entries), plus one rounding, plus what is not random: an entry
+    that holds most of a row's weight moves the whole row by its score's error.  A score x of this cache is
+    rounded where its halves' sums meet (2^-24 of it, 2^-23 if cut off), by its block's scale and by the
+    softmax's scale (2^-24 each), 4 * 2^-24 |x| in all; plain fp32 has one or two of these."""
+    out = torch.empty(q.shape, device="cuda")
+    c.attention(0, q, out, decay=0.0)
+    want = ref.attention(q, 0.0)[0]
+    plain, pw, top = plain_fp32(ref, q)
+    one = 2.0 ** -23 + 4 * 2.0 ** -24 * top
+    norm = lambda a: a.double().unflatten(-1, (-1, 32)).transpose(-1, -2).reshape(-1, a.shape[-1] // 32).norm(dim=0)
+    assert bool((norm(out - want) <= 2 * norm(plain - want) + one * norm(want)).all()), \
+        (norm(out - want) / norm(want), norm(plain - want) / norm(want))
+    n = max(ref.len)
+    w, err = ref.w[:, :, :n], lambda a: float((a.double() - ref.w[:, :, :n]).norm())
+    assert err(c.weights(0)[:, :, :n]) <= 2 * err(pw) + one * float(w.norm())
+
+
+@pytest.mark.parametrize("n_kv,G,hd,T", [(4, 1, 64, 1), (2, 4, 128, 1), (1, 8, 32, 1), (1, 4, 128, 3)])
+@pytest.mark.parametrize("n", [60, 2304, 20000])
+@pytest.mark.parametrize("above,size", [(0.0, 0.4), (4.0, 0.4), (6.0, 0.08), (8.0, 1e-3), (8.0, 30.0)])
+def test_attention_beside_a_sink(n_kv, G, hd, T, n, above, size):
+    """The first entry's value is 0 and it holds 1 - e^-above of the weight or more (above 0: about half);
+    the others' small shares make the output."""
+    B = 4
+    cap = -(-n // 32) * 32
+    k, v = rows((B, n, n_kv, hd), 380), rows((B, n, n_kv, hd), 381, F32, size)
+    q = rows((B, T, n_kv * G, hd), 382)
+    q[..., 0] = 4.0
+    k[..., 0] = 0
+    k[:, 0] = 0
+    k[:, 0, :, 0] = (np.log(n) + 0.5 + above) * hd ** 0.5 / 4
+    v[:, 0] = 0
+    c, ref = make(B, n_kv * G, n_kv, hd, cap, track=T), Ref(B, n_kv * G, n_kv, hd, cap)
+    c.append(0, k, v)
+    ref.append(k, v)
+    check_as_exact_as_plain(c, ref, q)
+    ref.attention(q, 0.0)
+    share = ref.w[:, :, 0] / (T * G)
+    assert bool((share > 1 - 4 * np.exp(-above)).all()) and (above or 0.2 < float(share.mean()) < 0.8)
+
+
+@pytest.mark.parametrize("G", [1, 8])
+def test_attention_values_of_unlike_size(G):
+    """A block of 32 dims whose values are 100 times the others', single entries whose values are, and
+    scores spread so that far entries weigh 2^-20 of near ones."""
+    B, n, n_kv, hd = 4, 3000, 2, 128
+    k, v = rows((B, n, n_kv, hd), 383), rows((B, n, n_kv, hd), 384, F32, 0.05)
+    q = rows((B, 1, n_kv * G, hd), 385)
+    v[0, :, :, 32:64] *= 100
+    v[1, ::97] *= 100
+    q[..., 0] = 4.0
+    k[2:, :, :, 0] = torch.linspace(-14, 0, n, device="cuda")[:, None] * hd ** 0.5 / 4
+    k[3] = k[3].flip(0)
+    c, ref = make(B, n_kv * G, n_kv, hd, 3008, track=1), Ref(B, n_kv * G, n_kv, hd, 3008)
+    c.append(0, k, v)
+    ref.append(k, v)
+    check_as_exact_as_plain(c, ref, q)
+
+
+@pytest.mark.parametrize("G", [1, 8])
+def test_attention_values_with_a_mean_over_long_runs(G):
+    """Thousands of entries per warp whose values do not cancel: the sums' roundings must not add up."""
+    B, n, n_kv, hd = 32, 131072, 1, 32
+    k, v = rows((1, n, n_kv, hd), 386, BF16), rows((1, n, n_kv, hd), 387, BF16, 0.1) + 1
+    q = rows((B, 1, n_kv * G, hd), 388)
+    c, ref = make(B, G, n_kv, hd, n), Ref(1, G, n_kv, hd, n)
+    c.append(0, k.expand(B, n, n_kv, hd), v.expand(B, n, n_kv, hd))
+    ref.append(k, v)
+    out = torch.empty_like(q)
+    c.attention(0, q, out)
+    x = torch.einsum("bgd,nd->bgn", q[:, 0].double(), ref.k[0, 0]) / hd ** 0.5
+    want = torch.einsum("bgn,nd->bgd", torch.softmax(x, -1), ref.v[0, 0])
+    # of a mean near 1: the fp32 rounding of 2^-24 of each partial sum and of the result, a few of each
+    assert float((out[:, 0].double() - want).norm() / want.norm()) <= 4 * 2.0 ** -24
+
+
 def test_non_finite_rows_stay_where_they_are():
     """A NaN in one slot's key, query row or value block poisons only what attends to it."""
     B, n, hd = 4, 70, 64
@@ -607,6 +698,40 @@ def test_non_finite_rows_stay_where_they_are():
     c.append(0, k, v)
     ref.append(k, v)
     check_attention(c, ref, q)
+
+
+@pytest.mark.parametrize("n_kv,G,hd,T", [(2, 1, 128, 4), (1, 2, 64, 30), (2, 8, 32, 3), (1, 1, 128, 64)])
+@pytest.mark.parametrize("n", [7, 70, 1100])
+@pytest.mark.parametrize("small", [False, True])
+def test_nan_values_of_the_last_tokens(n_kv, G, hd, T, n, small):
+    """NaN blocks among the call's own tokens reach the query tokens behind them, in their 32 dims alone;
+    ``small``: beside values of zero and of very unlike sizes."""
+    B, cap = 3, 1120
+    g = torch.Generator()
+    g.manual_seed(396)
+    k, v = rows((B, n, n_kv, hd), 397), rows((B, n, n_kv, hd), 398)
+    if small:
+        v[:, ::3] *= 1e-4
+        v[:, 1::5] = 0
+    bad = torch.zeros((B, n, n_kv, hd // 32), dtype=torch.bool)
+    for b in range(1, B):
+        for _ in range(b):
+            at = max(0, n - T + int(torch.randint(0, T, (1,), generator=g)))
+            bad[b, at, int(torch.randint(0, n_kv, (1,), generator=g)), int(torch.randint(0, hd // 32, (1,), generator=g))] = True
+    bad = bad.cuda().repeat_interleave(32, -1)
+    c, ref = make(B, n_kv * G, n_kv, hd, cap), Ref(B, n_kv * G, n_kv, hd, cap)
+    c.append(0, k, v.masked_fill(bad, float("inf")))
+    ref.append(k, v.masked_fill(bad, 0.0))
+    for dtype in (F32, BF16):
+        q = rows((B, T, n_kv * G, hd), 399, dtype)
+        out = torch.empty_like(q)
+        c.attention(0, q, out)
+        want, tol, _ = ref.attention(q)
+        if dtype == BF16:
+            tol = tol + want.abs() * 2.0 ** -8 + tol_fp16(ref)
+        seen = torch.cumsum(torch.cat([bad.new_zeros((B, T, n_kv, hd)), bad], 1).int(), 1)[:, -T:] > 0   # by query t
+        assert torch.equal(torch.isnan(out), seen.repeat_interleave(G, 2))
+        assert bool(((out.double() - want).abs() <= tol).logical_or(torch.isnan(out)).all())
 
 
 @pytest.mark.parametrize("n", [30, 200, 1500, 9000])

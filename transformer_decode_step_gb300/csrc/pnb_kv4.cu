@@ -72,15 +72,6 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 
 __device__ __forceinline__ float2 dup(float v) { return make_float2(v, v); }
 
-// a + b on packed pairs of fp32
-__device__ __forceinline__ float2 fadd2(float2 a, float2 b) {
-  unsigned long long d;
-  asm("add.rn.f32x2 %0, %1, %2;"
-      : "=l"(d)
-      : "l"(*reinterpret_cast<unsigned long long *>(&a)), "l"(*reinterpret_cast<unsigned long long *>(&b)));
-  return *reinterpret_cast<float2 *>(&d);
-}
-
 // largest magnitude of the 8, NaN when one is
 __device__ __forceinline__ float top8(const Raw8<float> &r) {
   float x[8], top = 0.f;

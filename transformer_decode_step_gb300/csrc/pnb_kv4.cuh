@@ -168,6 +168,15 @@ inline cudaError_t kv4_launch(K kern, dim3 grid, dim3 block, size_t smem, int cl
   return cudaLaunchKernelEx(&cfg, kern, a);
 }
 
+// a + b on packed pairs of fp32
+__device__ __forceinline__ float2 fadd2(float2 a, float2 b) {
+  unsigned long long d;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(d)
+      : "l"(*reinterpret_cast<unsigned long long *>(&a)), "l"(*reinterpret_cast<unsigned long long *>(&b)));
+  return *reinterpret_cast<float2 *>(&d);
+}
+
 // Entries of slot b as the kernels use them: a length outside [0, cap] (the
 // buffer is the caller's) never leads an access out of the cache.
 __device__ __forceinline__ int kv4_len(const Kv4Layer &l, int b) {

@@ -24,6 +24,8 @@
 // twice the matrix instructions and the outputs twice the registers.)
 #include <cuda_fp16.h>
 
+#include <cfloat>
+
 #include "pnb_kv4.cuh"
 
 namespace pnb {
@@ -140,12 +142,12 @@ __device__ __forceinline__ void lds_words(const uint8_t *p, uint32_t (&w)[NG]) {
   }
 }
 
-// the larger finite half of a word, as its bits (0 when neither is finite)
-__device__ __forceinline__ uint32_t finite_half_max(uint32_t w) {
-  uint32_t a = w & 0xffffu, b = w >> 16;
-  a = a < 0x7c00u ? a : 0u;
-  b = b < 0x7c00u ? b : 0u;
-  return a > b ? a : b;
+// what V scales below 2^ev are multiplied with, as a power of two
+__device__ __forceinline__ int up_of(int ev) { return ev < -3 || ev > 0 ? -ev : 0; }
+
+// the halves of a word that are finite, as a mask (scales have no sign)
+__device__ __forceinline__ uint32_t finite_halves(uint32_t w) {
+  return ((w & 0xffffu) < 0x7c00u ? 0xffffu : 0u) | ((w >> 16) < 0x7c00u ? 0xffff0000u : 0u);
 }
 
 // The part of a warp's units [x, x1) that lies in one item: chunks [c0, c1) of
@@ -467,7 +469,6 @@ __global__ void __launch_bounds__(kKv4Threads, kKv4CtasPerSm)
     }
     const int limit_all = len - a.T + 1;                       // every row sees positions below it
     int limit[RL];
-    const int limit_col = row_col < a.rows ? limit_all + row_col / a.G : 0;
     float *score[RL];
 #pragma unroll
     for (int k = 0; k < RL; ++k) {
@@ -479,18 +480,16 @@ __global__ void __launch_bounds__(kKv4Threads, kKv4CtasPerSm)
                        : nullptr;
     }
 
-    float o[NG * 2][4];
+    float2 o[NG * 2][2];                                       // the products' accumulators, in 2^(ref - up_of(ev))
 #pragma unroll
-    for (int i = 0; i < NG * 2; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-    float l[RL], m[RL], ref[RL];                               // sum, reference maximum, reference
-    int ev = -1;                                               // V scales seen are below 2^ev
+    for (int i = 0; i < NG * 2; ++i) o[i][0] = o[i][1] = make_float2(0.f, 0.f);
+    float l[RL], ref[RL];                                      // sum (in 2^ref), reference
 #pragma unroll
     for (int k = 0; k < RL; ++k) {
       l[k] = 0.f;
-      m[k] = -INFINITY;
-      ref[k] = -11.f;
+      ref[k] = -FLT_MAX;
     }
-
+    int ev = 0;
 #pragma unroll 1
     for (int ch = sg.c0; ch < sg.c1; ++ch) {
       if (!dead && !mbar_wait(bars + stage, phase)) {
@@ -547,35 +546,12 @@ __global__ void __launch_bounds__(kKv4Threads, kKv4CtasPerSm)
           }
         }
       }
-      // the largest V scale of the chunk (finite, inside the sequence) bounds
-      // what the fp16 products can reach
-      uint32_t hmax;
-      {
-        constexpr int kWords = 16 * NG, kPer = (kWords + 31) / 32;
-        uint32_t w[kPer];
-        lds_words<kPer>(st + kv4_vscale_off(NG) + (lane * kPer % kWords) * 4, w);
-        if (tail) {
-#pragma unroll
-          for (int i = 0; i < kPer; ++i) {
-            const int p = p0 + 2 * ((lane * kPer + i) % kWords / NG);
-            w[i] &= p >= len ? 0u : (p + 1 >= len ? 0xffffu : 0xffffffffu);
-          }
-        }
-        const uint32_t both = kPer == 2 ? as_word(__hmax2(as_half2(w[0]), as_half2(w[kPer - 1]))) : w[0];
-        hmax = __reduce_max_sync(0xffffffffu, max(both & 0xffffu, both >> 16));
-        if (hmax >= 0x7c00u) {   // a block of NaN: only the finite scales count
-          hmax = 0;
-#pragma unroll
-          for (int i = 0; i < kPer; ++i) hmax = max(hmax, finite_half_max(w[i]));
-          hmax = __reduce_max_sync(0xffffffffu, hmax);
-        }
-      }
       // The scores, rounded once: the maximum, the weights and what is stored come
       // from the same numbers, so that at any size none lies above the maximum.
 #pragma unroll
-      for (int t = 0; t < 4; ++t)
+      for (int k = 0; k < RL; ++k)
 #pragma unroll
-        for (int k = 0; k < RL; ++k) s[t][k] = __fmul_rn(s[t][k], rs[k]);
+        for (int t = 0; t < 4; ++t) s[t][k] = __fmul_rn(s[t][k], rs[k]);
       if (tail) {
 #pragma unroll
         for (int t = 0; t < 4; ++t)
@@ -583,44 +559,160 @@ __global__ void __launch_bounds__(kKv4Threads, kKv4CtasPerSm)
           for (int k = 0; k < RL; ++k)
             if (p0 + 8 * t + r >= limit[k]) s[t][k] = -INFINITY;
       }
-      float xm[RL];
-      bool move = false;
+      if (TRACK) {
+#pragma unroll
+        for (int k = 0; k < RL; ++k)
+          if (score[k]) {
+#pragma unroll
+            for (int t = 0; t < 4; ++t) score[k][p0 + 8 * t] = s[t][k];
+          }
+      }
+      // The chunk's V scales lie below 2^evc (the finite ones, inside the sequence).
+      // ev follows within a factor of 2^3; scales above 1, or all below 2^-3, are
+      // brought to just below 1, in the chunk itself.
+      constexpr int kWords = 16 * NG, kPer = (kWords + 31) / 32;
+      uint32_t vw[kPer], both;          // the lane's words of V scales, and its two positions' largest
+      bool uneven;                      // one of them has far smaller values than another position
+      uint8_t *vscales = ring + stage * L::kChunk + kv4_vscale_off(NG) + (lane * kPer % kWords) * 4;
+      auto scale_words = [&](uint32_t by) {
+#pragma unroll
+        for (int i = 0; i < kPer; ++i)
+          reinterpret_cast<uint32_t *>(vscales)[i] = as_word(__hmul2_rn(as_half2(vw[i]), as_half2(by)));
+        // ahead of the copy that fills the stage again
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+      };
+      {
+        lds_words<kPer>(vscales, vw);
+        uint32_t outside = 0;           // the halves behind the sequence
+        const int p = p0 + 2 * (lane * kPer % kWords / NG);
+        if (tail) {
+          outside = p >= len ? 0xffffffffu : (p + 1 >= len ? 0xffff0000u : 0u);
+#pragma unroll
+          for (int i = 0; i < kPer; ++i) vw[i] &= ~outside;
+        }
+        auto largest = [&](const uint32_t (&w)[kPer]) {
+          const __half2 m = kPer == 2 ? __hmax2_nan(as_half2(w[0]), as_half2(w[kPer - 1])) : as_half2(w[0]);
+          return NG == 1 ? as_word(m) : as_word(__hmax2_nan(m, as_half2(__shfl_xor_sync(0xffffffffu, as_word(m), 1))));
+        };
+        auto over_warp = [](uint32_t w) { return __reduce_max_sync(0xffffffffu, max(w & 0xffffu, w >> 16)); };
+        both = largest(vw);
+        uint32_t hmax = over_warp(both);
+        if (hmax >= 0x7c00u) {          // a block of NaN: only the finite scales count
+          uint32_t finite[kPer];
+#pragma unroll
+          for (int i = 0; i < kPer; ++i) finite[i] = vw[i] & finite_halves(vw[i]);
+          both = largest(finite);
+          hmax = over_warp(both);
+          if (tail && a.T > 1) {
+            // A weight of 0 times NaN is NaN: entries that not all rows see lose
+            // their NaN here, and the rows that see them have it from now on.
+            for (int q = max(limit_all, p0); q < min(len, p0 + kKv4Chunk); ++q) {
+#pragma unroll
+              for (int g = 0; g < NG; ++g) {
+                const uint32_t d = *reinterpret_cast<const uint16_t *>(st + kv4_vscale_off(NG) + kv4_vscale(NG, q - p0, g));
+                if (d < 0x7c00u) continue;
+#pragma unroll
+                for (int i = 2 * g; i < 2 * g + 2; ++i)
+#pragma unroll
+                  for (int h = 0; h < 2; ++h) {
+                    if (q < limit[0]) o[i][h].x = NAN;
+                    if (q < limit[RL - 1]) o[i][h].y = NAN;
+                  }
+              }
+            }
+            __syncwarp();
+            const uint32_t some = (p >= limit_all ? 0xffffu : 0u) | (p + 1 >= limit_all ? 0xffff0000u : 0u);
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) vw[i] = (vw[i] & ~some) | (finite[i] & some);
+          }
+        }
+        const uint32_t in = both | outside;
+        const __half least = __ushort_as_half((unsigned short)min(in & 0xffffu, in >> 16));
+        uneven = __hlt(__hmul(least, __ushort_as_half(0x5400)), __ushort_as_half((unsigned short)hmax));   // 64 times
+        const int evc = (int)(hmax >> 10) - 14;
+        if ((unsigned)(ev - evc) > 3u && hmax != 0) {
+          const float more = __uint_as_float((uint32_t)(127 + up_of(evc) - up_of(ev)) << 23);
+          ev = evc;
+#pragma unroll
+          for (int i = 0; i < NG * 2; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) o[i][h] = make_float2(o[i][h].x * more, o[i][h].y * more);
+        }
+        if (up_of(ev) != 0 || tail) {   // and what lies behind the sequence becomes 0
+          const float f = __uint_as_float((uint32_t)(127 + up_of(ev)) << 23);
+          scale_words(pack_half2(make_float2(f, f)));
+        }
+      }
+      // p = 2^(x - ref) and p d in fp16: the reference follows the chunks' largest
+      // scores in whole powers of two, with some play, so that a chunk's largest p lies
+      // in 2^2 .. 2^15 whatever the chunks before it held (a first entry that takes
+      // nearly all the weight, say).  Products keep 22 bits down to 2^-3 and lose one
+      // per power of two from there.  (One reference for all chunks, that of the
+      // largest score, left 2 % of error beside such an entry.  New references by
+      // every chunk's own largest scores, with the sums' factors: 64 slots 47.5 us.)
+      bool off = uneven;                // some row's reference does not fit
+      float xmax[RL], lmul = 1.f;
 #pragma unroll
       for (int k = 0; k < RL; ++k) {
-        if (TRACK && score[k]) {
-#pragma unroll
-          for (int t = 0; t < 4; ++t) score[k][p0 + 8 * t] = s[t][k];
-        }
-        xm[k] = fmaxf(fmaxf(s[0][k], s[1][k]), fmaxf(s[2][k], s[3][k]));
-        move |= xm[k] > m[k] + 4.f;
+        xmax[k] = fmaxf(fmaxf(s[0][k], s[1][k]), fmaxf(s[2][k], s[3][k]));
+        const float d = xmax[k] - ref[k];
+        const uint32_t near = __ballot_sync(0xffffffffu, !(d < 2.f));
+        off |= d > 15.f;
+        off |= (near & (0x11111111u << c)) == 0;
       }
-      const int evc = (int)(hmax >> 10) - 14;
-      // The weights are scaled by 2^(10 - ev), V scales lying below 2^ev with
-      // ev >= -1, and the reference moves only when a score exceeds it by 2^4
-      // or a larger V scale arrives: p stays below 2^15 and p d below 2^14,
-      // inside fp16, and the fp32 sums need no rescaling otherwise.  The reference is
-      // rounded up: where scores are so large that it rounds, p only gets smaller.
-      if (__any_sync(0xffffffffu, move) || evc > ev) {
-        ev = max(ev, evc);
+      if (__any_sync(0xffffffffu, off)) {
+        // Where positions' values are uneven (next to a first entry with a value of
+        // zero), each position's V scales are brought to just below 1/2 and its
+        // weight takes the power of two: the reference then goes by what the
+        // positions add to the outputs.  The sum takes the weights as they are.
+        const bool spread = __any_sync(0xffffffffu, uneven);
+        float adj[4];
+        if (spread) {
+          auto field = [](uint32_t h) { return min(max(28 - (int)(h >> 10), 1), 28); };   // of 2^(field - 15)
+          scale_words((uint32_t)field(both & 0xffffu) << 10 | (uint32_t)field(both >> 16) << 26);
+#pragma unroll
+          for (int t = 0; t < 4; ++t) {
+            const uint32_t w = __shfl_sync(0xffffffffu, both, (4 * t + (r >> 1)) * (NG > 1 ? 2 : 1));
+            const uint32_t h = (r & 1) ? w >> 16 : w & 0xffffu;
+            adj[t] = h == 0 ? -INFINITY : (float)(up_of(ev) + 15 - field(h));
+          }
+        }
+        const float room = spread ? 13.f : 15.f;
+        float al[RL];
 #pragma unroll
         for (int k = 0; k < RL; ++k) {
-          xm[k] = fmaxf(xm[k], __shfl_xor_sync(0xffffffffu, xm[k], 4));
-          xm[k] = fmaxf(xm[k], __shfl_xor_sync(0xffffffffu, xm[k], 8));
-          xm[k] = fmaxf(xm[k], __shfl_xor_sync(0xffffffffu, xm[k], 16));
-          const float mn = fmaxf(m[k], xm[k]);
-          const float nref = __fadd_ru(mn == -INFINITY ? 0.f : mn, (float)(ev - 10));
-          const float al = m[k] == -INFINITY ? 0.f : ex2(ref[k] - nref);
-          m[k] = mn;
-          ref[k] = nref;
-          l[k] *= al;
+          auto over_rows = [](float x) {
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+            return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+          };
+          float xm = over_rows(xmax[k]), to = ref[k];
+          // the sums stay below 2^80 or so, which bounds how far a reference falls
+          const float lm = over_rows(l[k]);
+          const float least = fmaxf(ceilf(__fadd_ru(xm, -60.f)), ref[k] + (float)((int)(__float_as_uint(lm) >> 23) - 187));
+          if (spread)
+            xm = over_rows(fmaxf(fmaxf(s[0][k] + adj[0], s[1][k] + adj[1]), fmaxf(s[2][k] + adj[2], s[3][k] + adj[3])));
+          // (where scores are so large that the reference rounds, it rounds up)
+          if (xm - to > room || (xm - to < room - 13.f && xm > -INFINITY)) to = ceilf(__fadd_ru(xm, 6.f - room));
+          to = fmaxf(to, least);
+          al[k] = ex2(ref[k] - to);
+          ref[k] = to;
+          l[k] *= al[k];
+        }
 #pragma unroll
-          for (int i = 0; i < NG * 2; ++i) {
-            if (PAIR) {
-              o[i][0] *= al; o[i][1] *= al; o[i][2] *= al; o[i][3] *= al;
-            } else {
-              o[i][k] *= al; o[i][2 + k] *= al;
+        for (int i = 0; i < NG * 2; ++i)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) o[i][h] = make_float2(o[i][h].x * al[0], o[i][h].y * al[RL - 1]);
+        if (spread) {
+          lmul = 0.f;
+#pragma unroll
+          for (int k = 0; k < RL; ++k)
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+              l[k] += ex2(__fadd_rn(s[t][k], -ref[k]));
+              s[t][k] += adj[t];
             }
-          }
         }
       }
       // softmax weights as columns: xh[t] holds the high parts of positions 8 t + 2 c,
@@ -632,7 +724,7 @@ __global__ void __launch_bounds__(kKv4Threads, kKv4CtasPerSm)
 #pragma unroll
         for (int k = 0; k < RL; ++k) {
           p[k] = ex2(__fadd_rn(s[t][k], -ref[k]));
-          l[k] += p[k];
+          l[k] = fmaf(p[k], lmul, l[k]);
         }
         if (PAIR) {
           const uint32_t h = pack_half2(make_float2(p[0], p[0]));
@@ -662,11 +754,7 @@ __global__ void __launch_bounds__(kKv4Threads, kKv4CtasPerSm)
         uint32_t w[4], wl[4];
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
-          uint32_t dw = *reinterpret_cast<const uint32_t *>(st + kv4_vscale_off(NG) + (t * 4 + c) * 4 * NG + 4 * g);
-          if (tail) {   // a masked position's scale may be anything: its weight is 0, not 0 times it
-            const int p = p0 + 8 * t + 2 * c;
-            dw &= p >= limit_col ? 0u : (p + 1 >= limit_col ? 0xffffu : 0xffffffffu);
-          }
+          const uint32_t dw = *reinterpret_cast<const uint32_t *>(st + kv4_vscale_off(NG) + (t * 4 + c) * 4 * NG + 4 * g);
           const __half2 d = as_half2(dw), h = as_half2(xh[t]);
           const uint32_t first = as_word(__hmul2_rn(h, d));
           w[t] = first;
@@ -677,15 +765,19 @@ __global__ void __launch_bounds__(kKv4Threads, kKv4CtasPerSm)
           }
         }
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-          for (int kt = 0; kt < 2; ++kt) {
-            mma_f16(o[g * 2 + j], u[2 * j][2 * kt], u[2 * j + 1][2 * kt], u[2 * j][2 * kt + 1], u[2 * j + 1][2 * kt + 1],
-                    w[2 * kt], w[2 * kt + 1]);
-            if (SPLIT && !PAIR)
-              mma_f16(o[g * 2 + j], u[2 * j][2 * kt], u[2 * j + 1][2 * kt], u[2 * j][2 * kt + 1],
-                      u[2 * j + 1][2 * kt + 1], wl[2 * kt], wl[2 * kt + 1]);
+        for (int j = 0; j < 2; ++j) {
+          float d[4];
+          mma_f16_new(d, u[2 * j][0], u[2 * j + 1][0], u[2 * j][1], u[2 * j + 1][1], w[0], w[1]);
+          mma_f16(d, u[2 * j][2], u[2 * j + 1][2], u[2 * j][3], u[2 * j + 1][3], w[2], w[3]);
+          if (SPLIT && !PAIR) {
+            mma_f16(d, u[2 * j][0], u[2 * j + 1][0], u[2 * j][1], u[2 * j + 1][1], wl[0], wl[1]);
+            mma_f16(d, u[2 * j][2], u[2 * j + 1][2], u[2 * j][3], u[2 * j + 1][3], wl[2], wl[3]);
           }
+          // fp32 sums by rounding additions (the matrix instruction cuts off: thousands
+          // of entries with a common mean were 2e-6 too small)
+          o[2 * g + j][0] = fadd2(o[2 * g + j][0], make_float2(d[0], d[1]));
+          o[2 * g + j][1] = fadd2(o[2 * g + j][1], make_float2(d[2], d[3]));
+        }
       }
       __syncwarp();
       produce();
@@ -694,8 +786,10 @@ __global__ void __launch_bounds__(kKv4Threads, kKv4CtasPerSm)
     }
 
     // the lane's outputs: row lane_row(k), dim 8 i + r
+    const float vs = __uint_as_float((uint32_t)(127 - up_of(ev)) << 23);
     auto out_of = [&](int k, int i) {
-      return PAIR ? o[i >> 1][2 * (i & 1)] + o[i >> 1][2 * (i & 1) + 1] : o[i >> 1][2 * (i & 1) + k];
+      const float2 v = o[i >> 1][i & 1];
+      return (PAIR ? v.x + v.y : k ? v.y : v.x) * vs;
     };
 #pragma unroll
     for (int k = 0; k < RL; ++k) {
