@@ -505,7 +505,8 @@ int pnb_kvq_read(pnb_kvq *c, int32_t layer, const int32_t *first_dev, int32_t T,
    dtype; out may be q's own rows when they have the same strides and dtype.
    fp32 outputs carry about 1e-6 of relative error (of a row of one head, and
    beside what fp32 scores of the row's size are rounded by) against exact
-   arithmetic on the held values, however the weight is spread over them.
+   arithmetic on the held values, however the weight is spread over them; bf16
+   outputs are the rounding of the same numbers.
    decay < 0: the weights stay as they are.  decay >= 0 (finite; T <= track,
    else PNB_E_INVAL): weights[j] = decay * weights[j] + the sum over the T
    tokens and the KV head's query heads of the softmax weight of entry j

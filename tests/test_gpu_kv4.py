@@ -775,6 +775,27 @@ def test_attention_is_as_exact_as_plain_fp32(n_kv, G, hd, T):
     assert norm(c.weights(0)[:, :, :n] - w) <= 2 * norm(p.sum((2, 3)) - w) + 2.0 ** -23 * norm(w)
 
 
+@pytest.mark.parametrize("n_kv,G,hd,T", [(2, 4, 128, 1), (2, 8, 64, 1), (4, 1, 32, 1), (1, 4, 128, 3), (2, 1, 64, 16)])
+@pytest.mark.parametrize("n", [40, 1500, 20000])
+def test_bf16_outputs_are_rounded_once(n_kv, G, hd, T, n):
+    """A bf16 output is the rounding of a number as near the 64-bit one as an fp32 output's tolerance says,
+    and tracked weights have that of fp32 queries."""
+    B = 3
+    cap = -(-n // 32) * 32
+    c, ref = make(B, n_kv * G, n_kv, hd, cap, track=T), Ref(B, n_kv * G, n_kv, hd, cap)
+    k, v = rows((B, n, n_kv, hd), 390, BF16), rows((B, n, n_kv, hd), 391, BF16)
+    c.append(0, k, v, n_new=i32([n, n // 2, n - 1]))
+    ref.append(k, v, [n, n // 2, n - 1])
+    q = rows((B, T, n_kv * G, hd), 392, BF16)
+    out = check_attention(c, ref, q, decay=0.0)
+    want, tol, _ = ref.attention(q)
+    assert bool(((out >= (want - tol).to(BF16)) & (out <= (want + tol).to(BF16))).all())
+    # an fp32 output of the same queries rounds to the same numbers, but for those next to a border
+    full = torch.empty(q.shape, device="cuda")
+    c.attention(0, q, full)
+    assert float((full.to(BF16) != out).double().mean()) < 1e-2
+
+
 def test_attention_strided_rows_and_output_over_queries():
     B, T, H, Hkv, hd = 3, 2, 4, 2, 128
     c, ref = make(B, H, Hkv, hd, 128), Ref(B, H, Hkv, hd, 128)

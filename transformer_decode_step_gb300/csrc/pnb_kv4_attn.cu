@@ -12,11 +12,12 @@
 //
 // Both products take the codes as the A operand (m16n8k16: 16 positions of K by
 // 16 dims, 16 dims of V by 16 positions) and the few rows as B's 8 columns:
-//  - PAIR (up to four rows, queries or outputs in fp32): columns 2 q and 2 q + 1
-//    are the high and low fp16 parts of row q;
-//  - otherwise a row per column, and SPLIT (fp32) a second product with the low
-//    parts onto the same sums; bf16 queries are exact in one fp16, and a bf16
-//    output's rounding to 8 bits hides that of the softmax weights to 11.
+//  - PAIR (up to four rows): columns 2 q and 2 q + 1 are the high and low fp16
+//    parts of row q;
+//  - otherwise a row per column, and a second product with the low parts onto the
+//    same sums, SPLIT for the queries too: bf16 ones are exact in one fp16.
+// Softmax weights are in two parts whatever the outputs' type, so that a bf16
+// output is the rounding of what an fp32 one would be.
 // Scores come out with a position per lane group r = lane / 4 and rows by c =
 // lane % 4; a transposition of 8 x 8 fp16 turns them into B operands of the
 // second product.
@@ -733,10 +734,8 @@ __global__ void __launch_bounds__(kKv4Threads, kKv4CtasPerSm)
         } else {
           const uint32_t h = pack_half2(make_float2(p[0], p[RL - 1]));
           xh[t] = transpose8(h);
-          if (SPLIT) {
-            const float2 z = half2_pair(h);
-            xl[t] = transpose8(pack_half2(make_float2(p[0] - z.x, p[RL - 1] - z.y)));
-          }
+          const float2 z = half2_pair(h);
+          xl[t] = transpose8(pack_half2(make_float2(p[0] - z.x, p[RL - 1] - z.y)));
         }
       }
       const uint32_t odd = (r & 1) ? 0xffffffffu : 0u;
@@ -758,18 +757,16 @@ __global__ void __launch_bounds__(kKv4Threads, kKv4CtasPerSm)
           const __half2 d = as_half2(dw), h = as_half2(xh[t]);
           const uint32_t first = as_word(__hmul2_rn(h, d));
           w[t] = first;
-          if (SPLIT) {
-            const uint32_t taken = PAIR ? first & odd : first;
-            wl[t] = as_word(__hfma2(as_half2(xl[t]), d, __hfma2(h, d, __hneg2(as_half2(taken)))));
-            if (PAIR) w[t] = wl[t];
-          }
+          const uint32_t taken = PAIR ? first & odd : first;
+          wl[t] = as_word(__hfma2(as_half2(xl[t]), d, __hfma2(h, d, __hneg2(as_half2(taken)))));
+          if (PAIR) w[t] = wl[t];
         }
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           float d[4];
           mma_f16_new(d, u[2 * j][0], u[2 * j + 1][0], u[2 * j][1], u[2 * j + 1][1], w[0], w[1]);
           mma_f16(d, u[2 * j][2], u[2 * j + 1][2], u[2 * j][3], u[2 * j + 1][3], w[2], w[3]);
-          if (SPLIT && !PAIR) {
+          if (!PAIR) {
             mma_f16(d, u[2 * j][0], u[2 * j + 1][0], u[2 * j][1], u[2 * j + 1][1], wl[0], wl[1]);
             mma_f16(d, u[2 * j][2], u[2 * j + 1][2], u[2 * j][3], u[2 * j + 1][3], wl[2], wl[3]);
           }
@@ -1087,8 +1084,8 @@ cudaError_t run_attn(Kv4AttnArgs a, int grid, cudaStream_t st) {
 
 template <int NG>
 cudaError_t run_attn(const Kv4AttnArgs &a, int grid, cudaStream_t st) {
-  if (a.q.dtype == PNB_BF16 && a.out.dtype == PNB_BF16) return run_attn<NG, false, false>(a, grid, st);
-  return a.rows <= 4 ? run_attn<NG, true, true>(a, grid, st) : run_attn<NG, false, true>(a, grid, st);
+  if (a.rows <= 4) return run_attn<NG, true, true>(a, grid, st);
+  return a.q.dtype == PNB_BF16 ? run_attn<NG, false, false>(a, grid, st) : run_attn<NG, false, true>(a, grid, st);
 }
 
 }  // namespace
