@@ -872,6 +872,29 @@ def test_evict(hd, budget, sink, recent, tie):
             assert torch.equal(d.weights(0)[b, :, :n].double(), ref.w[b, :, :n])
 
 
+@pytest.mark.parametrize("hd", [32, 64, 128])
+@pytest.mark.parametrize("budget", [1, 33, 79, 95, 96])
+def test_evict_in_place_around_the_border(hd, budget):
+    """Entries that move within the chunk that holds the budget's border, into it and out of it: in
+    place the same as into another cache, and the same each time."""
+    B, n_kv = 40, 3
+    lens = [min(300, budget + (1, 5, 17, 40, 200)[b % 5]) for b in range(B)]
+    c, ref = make(B, n_kv, n_kv, hd, 320), Ref(B, n_kv, n_kv, hd, 320)
+    fill(c, ref, lens, 400)
+    for b, n in enumerate(lens):              # what lies behind the budget mostly stays
+        c.weights(0)[b, :, budget:n] += 2.0 * (b % 3)
+        ref.w[b, :, :n].copy_(c.weights(0)[b, :, :n])
+    start, d = c.buf.clone(), make(B, n_kv, n_kv, hd, 96)
+    c.evict(0, budget, dst=d)
+    ref.evict(budget)
+    check_content(d, ref)
+    for _ in range(3):
+        c.buf.copy_(start)
+        c.evict(0, budget)
+        check_content(c, ref)
+        assert torch.equal(c.weights(0)[..., :budget], d.weights(0)[..., :budget])
+
+
 def test_evict_between_layers_and_equal_weights():
     """Into another layer of the same cache; all weights zero: the first entries stay."""
     c, ref = make(2, 2, 2, 64, 128, n_layer=2), Ref(2, 2, 2, 64, 128)

@@ -621,6 +621,12 @@ __global__ void __launch_bounds__(THREADS, THREADS >= 1024 ? 1 : 3) k_kv4_select
   };
   // (uniform over the cluster)
   if (n > m) {
+    // The chunk that holds the budget's border gives entries and takes some, in
+    // one V word even: in place, its V codes are read from a copy.
+    if (a.in_place && rank == 0 && tid < 32 * a.ng) {
+      const uint8_t *from = a.src.codes + (bh * (a.src.cap / kKv4Chunk) + m / kKv4Chunk) * kv4_chunk_bytes(a.ng) + kv4_v_off(a.ng);
+      reinterpret_cast<uint4 *>(a.border + bh * (512 * a.ng))[tid] = reinterpret_cast<const uint4 *>(from)[tid];
+    }
     const int base = rank * THREADS * K + warp * 32 * K + lane;   // this lane's entries: base + 32 k
     uint32_t key[K], loose = 0, lo = 0xffffffffu, hi = 0, stay = 0;
     constexpr int LOADS = K < 16 ? K : 16;        // in flight at once
@@ -824,9 +830,8 @@ constexpr int kMoveThreads = 128, kMoveChunks = 2;
 
 // The moves, one CTA per (kMoveChunks destination chunks, KV head, slot).
 // Sources of moves lie at or behind the budget and destinations below it, so
-// the CTAs do not depend on one another; in the chunk that holds the budget's
-// border a V word may be read by others while its owner replaces it, with the
-// nibbles that they read unchanged (32-bit accesses).  Bound by the gathered V
+// the CTAs do not depend on one another; V words of the chunk that holds both
+// are read from the selection's copy.  Bound by the gathered V
 // words, which hold 8 positions each (8 heads, head_dim 128: four slots of 32k to
 // 8192 29 us, 130 MB; copies of 64 slots at 1000 entries 25.5 us, 157 MB, 6.2 TB/s).
 template <int NG>
@@ -834,6 +839,7 @@ __global__ void __launch_bounds__(kMoveThreads, 8) k_kv4_move(const __grid_const
   constexpr int CH = kv4_chunk_bytes(NG), POS = kMoveChunks * kKv4Chunk;
   static_assert(POS <= kMoveThreads, "a position per thread");
   __shared__ int src[POS];
+  __shared__ const uint8_t *vfrom[POS];     // the V codes of a source's chunk
   __shared__ int moved_chunk[kMoveChunks];
   const int tid = threadIdx.x, h = blockIdx.y, b = blockIdx.z, p0 = blockIdx.x * POS;
   pdl_wait();
@@ -867,6 +873,9 @@ __global__ void __launch_bounds__(kMoveThreads, 8) k_kv4_move(const __grid_const
     }
     my_src = s;
     src[tid] = s;
+    vfrom[tid] = a.in_place && s >= a.budget && s / kKv4Chunk == a.budget / kKv4Chunk
+                     ? a.border + bh * (512 * NG)
+                     : from + (int64_t)(s / kKv4Chunk) * CH + kv4_v_off(NG);
     const bool any = __any_sync(0xffffffffu, s >= 0 && s != p);
     if ((tid & 31) == 0) moved_chunk[tid >> 5] = any;
   }
@@ -933,8 +942,7 @@ __global__ void __launch_bounds__(kMoveThreads, 8) k_kv4_move(const __grid_const
         s[e] = src[k * kKv4Chunk + p];
         if (s[e] == p0 + k * kKv4Chunk + p) s[e] = -1;
         if (s[e] >= 0)
-          v[e] = *reinterpret_cast<const uint4 *>(from + (int64_t)(s[e] / kKv4Chunk) * CH + kv4_v_off(NG) +
-                                                  kv4_vunit(J, r, (s[e] >> 1) & 3));
+          v[e] = *reinterpret_cast<const uint4 *>(vfrom[k * kKv4Chunk + p] + kv4_vunit(J, r, (s[e] >> 1) & 3));
       }
 #pragma unroll
       for (int e = 0; e < 8; ++e) {

@@ -126,9 +126,10 @@ struct Kv4WeightArgs {
 struct Kv4EvictArgs {
   Kv4Layer src, dst;
   int32_t n_slot, n_kv, budget, n_sink, n_recent;
-  int32_t in_place;
+  int32_t in_place, ng;
   int32_t *src_of, *movers;       // [n_slot][n_kv][src.cap]
   int32_t *n_old;                 // [n_slot]
+  uint8_t *border;                // [n_slot][n_kv][512 ng] V codes of the chunk that holds the budget's border
   uint32_t *arrive;               // [n_slot]
 };
 

@@ -24,6 +24,7 @@ struct pnb_kvq {
   unsigned *counter = nullptr;
   uint32_t *arrive = nullptr;
   int32_t *err = nullptr, *n_old = nullptr, *src_of = nullptr, *movers = nullptr;
+  uint8_t *border = nullptr;
 };
 
 namespace {
@@ -209,6 +210,7 @@ int pnb_kvq_new(const pnb_kvq_config *cfg, void *buf_dev, size_t bytes, pnb_kvq 
   const size_t o_part = take(part_rows * c.head_dim * 4);
   const size_t o_wpart = take(part_rows / 2 * kKv4Warps * c.head_dim * 4);
   const size_t o_src = take(entries * 4), o_mov = take(entries * 4);
+  const size_t o_border = take((size_t)c.n_slot * c.n_kv_head * 512 * k->ng);
   const size_t o_wscale = take(rows * 8), o_scores = take(rows * c.cap * 4);
   cudaError_t e = cudaMalloc(&k->ws, at);
   if (e == cudaSuccess) e = clear_now(k->ws, zeroed);
@@ -227,6 +229,7 @@ int pnb_kvq_new(const pnb_kvq_config *cfg, void *buf_dev, size_t bytes, pnb_kvq 
   k->warp_part = reinterpret_cast<float *>(k->ws + o_wpart);
   k->src_of = reinterpret_cast<int32_t *>(k->ws + o_src);
   k->movers = reinterpret_cast<int32_t *>(k->ws + o_mov);
+  k->border = k->ws + o_border;
   k->wscale = reinterpret_cast<float2 *>(k->ws + o_wscale);
   k->scores = reinterpret_cast<float *>(k->ws + o_scores);
   *out = k;
@@ -372,6 +375,8 @@ int pnb_kvq_evict(pnb_kvq *src, int32_t src_layer, pnb_kvq *dst, int32_t dst_lay
   a.in_place = a.src.codes == a.dst.codes;
   a.src_of = src->src_of;
   a.movers = src->movers;
+  a.border = src->border;
+  a.ng = src->ng;
   a.n_old = src->n_old;
   a.arrive = src->arrive;
   return launch_kv4_evict(src->ng, a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? PNB_OK : PNB_E_CUDA;
