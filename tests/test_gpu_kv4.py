@@ -938,6 +938,23 @@ def test_evict_odd_weights():
     assert c.ids(0)[0, 0, :2].tolist() == [2, 3]
 
 
+@pytest.mark.parametrize("cap,n", [(64, 50), (1504, 1500), (9024, 9000)])
+def test_evict_takes_zeros_of_both_signs_as_equal(cap, n):
+    """0 and -0 are equal weights: the lower index stays, whatever its sign."""
+    c, ref = make(2, 2, 2, 32, cap), Ref(2, 2, 2, 32, cap)
+    fill(c, ref, [n, n - 3], 410)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(413)
+    u = torch.rand(c.weights(0).shape, generator=g, device="cuda")
+    w = torch.where(u < 0.4, 0.0, torch.where(u < 0.9, -0.0, u))
+    w[1] = torch.where(u[1] < 0.1, -u[1], w[1])
+    c.weights(0).copy_(w)
+    ref.w.copy_(w.double())
+    c.evict(0, n // 2, 2, 5)
+    ref.evict(n // 2, 2, 5)
+    check_content(c, ref)
+
+
 def test_decode_loop_as_used():
     """Prompt, then steps of append, attention with accumulated weights and eviction, in place, on two
     layers; checked against the reference at every step, then replayed from a CUDA graph."""

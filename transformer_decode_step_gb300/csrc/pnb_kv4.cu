@@ -643,7 +643,7 @@ __global__ void __launch_bounds__(THREADS, THREADS >= 1024 ? 1 : 3) k_kv4_select
       if (k0 == 0) arrive();
 #pragma unroll
       for (int k = 0; k < LOADS; ++k) {
-        const uint32_t u = __float_as_uint(w[k]);
+        const uint32_t u = w[k] == 0.f ? 0u : __float_as_uint(w[k]);   // -0 and 0 are equal
         key[k0 + k] = (u & 0x80000000u) ? ~u : (u | 0x80000000u);
         if (base + 32 * (k0 + k) >= n) continue;
         if (id[k] < a.n_sink || (int64_t)id[k] >= (int64_t)seen - a.n_recent) {
