@@ -974,15 +974,15 @@ int chunk_groups(int T, int group) { return ((T + kKv4Chunk - 2) / kKv4Chunk + g
 
 // Chunks per CTA: up to `most` (append 8: one prompt of 8191 in fp32 48.9 us against
 // 50.4 with four and 57.0 with two; 8 x 4096 at head_dim 32 in fp32 15.0, 16.9,
-// 20.5), fewer while all CTAs fit the GPU at once (four on each of 152 SMs).  bf16 append / fp32 read, us, always four chunks against
+// 20.5), fewer while all CTAs fit the GPU at once (four on each SM).  bf16 append / fp32 read, us, always four chunks against
 // this rule and against always one: 1 sequence x 8 heads x 256 tokens 6.1 / 5.9,
 // 3.1 / 3.0, 3.0 / 3.1; 4 x 8 x 1031 7.8 / 8.4, 6.6 / 8.1, 7.2 / 8.4; 1 x 32 x
 // 8191 35.4 / 49.5, 35.3 / 49.6, 43.6 / 53.8.
-constexpr int kResidentCtas = 608;
+constexpr int kChunkCtasPerSm = 4;
 
-int chunk_group(int T, int n_kv, int n_slot, int most) {
-  const int64_t chunks = (int64_t)chunk_groups(T, 1) * n_kv * n_slot;
-  const int64_t per = (chunks + kResidentCtas - 1) / kResidentCtas;
+int chunk_group(int T, int n_kv, int n_slot, int sms, int most) {
+  const int64_t chunks = (int64_t)chunk_groups(T, 1) * n_kv * n_slot, at_once = (int64_t)kChunkCtasPerSm * sms;
+  const int64_t per = (chunks + at_once - 1) / at_once;
   return (int)(per < 1 ? 1 : per > most ? most : per);
 }
 
@@ -996,7 +996,7 @@ cudaError_t run_append(Kv4AppendArgs a, cudaStream_t st) {
   const int64_t values = (int64_t)a.T * a.n_kv * 32 * NG;
   if (values <= 2048 || (values <= 8192 && (int64_t)a.n_slot * a.n_kv > 1024))
     return kv4_launch(k_kv4_append_step<NG, T>, dim3(a.n_slot), dim3(kStepThreads), (size_t)values / 2, 1, st, a);
-  a.group = chunk_group(a.T, a.n_kv, a.n_slot, kAppendChunks);
+  a.group = chunk_group(a.T, a.n_kv, a.n_slot, a.sms, kAppendChunks);
   const dim3 grid(chunk_groups(a.T, a.group), a.n_kv, a.n_slot);
   return kv4_launch(k_kv4_append<NG, T>, grid, dim3(kAppendThreads), 0, 1, st, a);
 }
@@ -1010,7 +1010,7 @@ cudaError_t run_read(Kv4ReadArgs a, cudaStream_t st) {
     const int64_t threads = (int64_t)a.n_slot * a.T * a.n_kv * 8 * NG;
     return kv4_launch(k_kv4_read_step<NG, T>, dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, 1, st, a);
   }
-  a.group = chunk_group(a.T, a.n_kv, a.n_slot, kReadChunks);
+  a.group = chunk_group(a.T, a.n_kv, a.n_slot, a.sms, kReadChunks);
   const dim3 grid(chunk_groups(a.T, a.group), a.n_kv, a.n_slot);
   return kv4_launch(k_kv4_read<NG, T>, grid, dim3(kReadThreads), 0, 1, st, a);
 }

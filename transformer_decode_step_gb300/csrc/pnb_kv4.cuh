@@ -85,7 +85,7 @@ struct Kv4AppendArgs {
   Kv4Layer l;
   Kv4Rows k, v;
   const int32_t *n_new, *start;   // [n_slot] or NULL
-  int32_t n_slot, n_kv, T;
+  int32_t n_slot, n_kv, T, sms;   // (sms: the device's SM count)
   int32_t group;                  // chunks per CTA (set by the launcher)
   uint32_t *arrive;               // [n_slot]
   int32_t *err;
@@ -95,7 +95,7 @@ struct Kv4ReadArgs {
   Kv4Layer l;
   Kv4Rows k, v;
   const int32_t *first;           // [n_slot] or NULL
-  int32_t n_slot, n_kv, T;
+  int32_t n_slot, n_kv, T, sms;   // (sms: the device's SM count)
   int32_t group;                  // chunks per CTA (set by the launcher)
   int32_t *err;
 };
@@ -119,7 +119,7 @@ struct Kv4WeightArgs {
   Kv4Layer l;
   const float *scores;
   const float2 *wscale;
-  int32_t n_slot, n_kv, rows;
+  int32_t n_slot, n_kv, rows, sms;
   float decay;
 };
 
@@ -133,7 +133,7 @@ struct Kv4EvictArgs {
   uint32_t *arrive;               // [n_slot]
 };
 
-cudaError_t prepare_kv4_kernels(int ng, int *attn_grid);
+cudaError_t prepare_kv4_kernels(int ng, int *sms);
 cudaError_t launch_kv4_append(int ng, const Kv4AppendArgs &a, cudaStream_t st);
 cudaError_t launch_kv4_read(int ng, const Kv4ReadArgs &a, cudaStream_t st);
 cudaError_t launch_kv4_attn(int ng, const Kv4AttnArgs &a, int grid, cudaStream_t st);

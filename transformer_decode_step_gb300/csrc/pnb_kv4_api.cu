@@ -14,7 +14,7 @@ using namespace pnb;
 
 struct pnb_kvq {
   pnb_kvq_config cfg;
-  int device = 0, ng = 0, grid = 0;
+  int device = 0, ng = 0, sms = 0, grid = 0;   // grid: the attention's CTAs
   uint8_t *buf = nullptr;
   // byte offsets within a layer, and a layer's bytes
   size_t o_ids = 0, o_weights = 0, o_len = 0, o_seen = 0, layer_bytes = 0;
@@ -189,11 +189,12 @@ int pnb_kvq_new(const pnb_kvq_config *cfg, void *buf_dev, size_t bytes, pnb_kvq 
   k->cfg = *cfg;
   lay_out(k);
   k->buf = static_cast<uint8_t *>(buf_dev);
-  if (cudaGetDevice(&k->device) != cudaSuccess || prepare_kv4_kernels(k->ng, &k->grid) != cudaSuccess) {
+  if (cudaGetDevice(&k->device) != cudaSuccess || prepare_kv4_kernels(k->ng, &k->sms) != cudaSuccess) {
     cudaGetLastError();
     delete k;
     return PNB_E_CUDA;
   }
+  k->grid = k->sms * kKv4CtasPerSm;
   const pnb_kvq_config &c = *cfg;
   const size_t entries = (size_t)c.n_slot * c.n_kv_head * c.cap;
   const size_t part_rows = (size_t)2 * k->grid * kKv4Rows;
@@ -275,6 +276,7 @@ int pnb_kvq_append(pnb_kvq *c, int32_t layer, const pnb_rows *k, const pnb_rows 
   a.n_slot = g.n_slot;
   a.n_kv = g.n_kv_head;
   a.T = T;
+  a.sms = c->sms;
   a.arrive = c->arrive;
   a.err = c->err;
   return launch_kv4_append(c->ng, a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? PNB_OK : PNB_E_CUDA;
@@ -299,6 +301,7 @@ int pnb_kvq_read(pnb_kvq *c, int32_t layer, const int32_t *first_dev, int32_t T,
   a.n_slot = g.n_slot;
   a.n_kv = g.n_kv_head;
   a.T = T;
+  a.sms = c->sms;
   return launch_kv4_read(c->ng, a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? PNB_OK : PNB_E_CUDA;
 }
 
@@ -342,6 +345,7 @@ int pnb_kvq_attention(pnb_kvq *c, int32_t layer, const pnb_rows *q, int32_t T, c
     w.n_slot = a.n_slot;
     w.n_kv = a.n_kv;
     w.rows = a.rows;
+    w.sms = c->sms;
     w.decay = decay;
     if (launch_kv4_weights(w, st) != cudaSuccess) return PNB_E_CUDA;
   }

@@ -987,7 +987,7 @@ __global__ void __launch_bounds__(kKv4Threads, kKv4CtasPerSm)
 // by the scores' bytes (16 rows of 32 heads at 6007 positions, 12 MB: 6 us).
 // Each thread has four positions; PARTS groups of threads share out the rows of
 // the same positions, and the first adds up the groups' sums in order.
-constexpr int kWeightThreads = 128;
+constexpr int kWeightThreads = 128, kWeightCtasPerSm = 8;
 
 template <int PARTS>
 __global__ void __launch_bounds__(kWeightThreads) k_kv4_weights(const __grid_constant__ Kv4WeightArgs a) {
@@ -1051,7 +1051,7 @@ __global__ void __launch_bounds__(kWeightThreads) k_kv4_weights(const __grid_con
 }
 
 template <int NG>
-cudaError_t prepare(int *grid) {
+cudaError_t prepare(int *sms) {
   cudaError_t e = cudaSuccess;
   auto set = [&](auto k, int smem) {
     if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
@@ -1066,10 +1066,9 @@ cudaError_t prepare(int *grid) {
            AttnSmem<NG, false, true>::bytes(kKv4MaxSlots));
   set_both(k_kv4_attn<NG, true, true, false>, k_kv4_attn<NG, true, true, true>,
            AttnSmem<NG, true, true>::bytes(kKv4MaxSlots));
-  int dev = 0, sms = 0;
+  int dev = 0;
   if (e == cudaSuccess) e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  *grid = sms * kKv4CtasPerSm;
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
   return e;
 }
 
@@ -1090,8 +1089,8 @@ cudaError_t run_attn(const Kv4AttnArgs &a, int grid, cudaStream_t st) {
 
 }  // namespace
 
-cudaError_t prepare_kv4_kernels(int ng, int *attn_grid) {
-  return ng == 4 ? prepare<4>(attn_grid) : ng == 2 ? prepare<2>(attn_grid) : prepare<1>(attn_grid);
+cudaError_t prepare_kv4_kernels(int ng, int *sms) {
+  return ng == 4 ? prepare<4>(sms) : ng == 2 ? prepare<2>(sms) : prepare<1>(sms);
 }
 
 cudaError_t launch_kv4_attn(int ng, const Kv4AttnArgs &a, int grid, cudaStream_t st) {
@@ -1102,7 +1101,8 @@ template <int PARTS>
 cudaError_t run_weights(const Kv4WeightArgs &a, cudaStream_t st) {
   constexpr int unit = 4 * kWeightThreads / PARTS;
   const int64_t units = (int64_t)a.n_slot * a.n_kv * ((a.l.cap + unit - 1) / unit);
-  const int grid = (int)(units < 1216 ? units : 1216);   // 8 CTAs on each of 152 SMs
+  const int64_t most = (int64_t)kWeightCtasPerSm * a.sms;
+  const int grid = (int)(units < most ? units : most);
   const int smem = (PARTS - 1) * (kWeightThreads / PARTS) * 16 + (a.n_slot + 1) * 4;
   return kv4_launch(k_kv4_weights<PARTS>, dim3(grid), dim3(kWeightThreads), smem, 1, st, a);
 }
