@@ -1159,6 +1159,28 @@ def test_refusals():
     assert c.device_error() == 0 and c.lengths(0).tolist() == [0, 0]
 
 
+def test_numbers_past_32_bits_are_refused():
+    """They would reach the library modulo 2^32: another layer, a budget of 5, a small cache."""
+    c, k, q = make(2, 2, 1, 32, 64, n_layer=2, track=1), rows((2, 40, 1, 32), 420), rows((2, 1, 2, 32), 421)
+    c.append(0, k, k)
+    before, wrap = c.buf.clone(), 1 << 32
+
+    def refused(f, *a, **kw):
+        with pytest.raises(pnb.PnbError) as e:
+            f(*a, **kw)
+        return e.value.code == -1
+
+    assert refused(c.append, wrap, k, k) and refused(c.read, wrap, k.clone(), k.clone())
+    assert refused(c.attention, wrap, q, q.clone(), decay=1.0) and refused(c.lengths, wrap)
+    assert refused(c.evict, wrap, 5) and refused(c.evict, 0, wrap + 5) and refused(c.evict, 0, 5, dst_layer=wrap + 1)
+    assert refused(c.evict, 0, 5, n_sink=wrap) and refused(c.evict, 0, 5, n_recent=wrap)
+    assert refused(c.reset, wrap) and refused(c.reset, -1) and refused(c.reset, 2)
+    assert torch.equal(before, c.buf)
+    cfg = dict(n_layer=1, n_slot=1, n_head=1, n_kv_head=1, head_dim=32, cap=32)
+    for name in cfg:
+        assert refused(pnb.Kv4Cache, **{**cfg, name: cfg[name] + wrap})
+
+
 def test_rows_over_one_another_are_refused():
     """read's K over its V, attention's output over others' queries, eviction between overlapping buffers."""
     B, T, H, Hkv, hd = 2, 3, 4, 2, 64

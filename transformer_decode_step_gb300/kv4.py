@@ -18,6 +18,13 @@ from . import (PNB_BF16, PNB_F32, PnbError, _ptr, check, pnb_kvq_append, pnb_kvq
 _pack_rows = struct.Struct("@Pqqqi4x").pack
 
 
+def _i32(v, what: str) -> int:
+    """v itself, refused where ctypes would cut it down to 32 bits."""
+    if not -(1 << 31) <= v < 1 << 31:
+        raise PnbError(-1, f"{what} {v} does not fit 32 bits")
+    return v
+
+
 class Kv4Cache:
     """A pnb_kvq over a torch buffer (``buf``, allocated if None; reset() a new one).
 
@@ -29,7 +36,9 @@ class Kv4Cache:
         import torch
 
         self._h = None
-        self.cfg = pnb_kvq_config(n_layer, n_slot, n_head, n_kv_head, head_dim, cap, track)
+        self.cfg = pnb_kvq_config(*(_i32(v, f"Kv4Cache: {n}") for v, n in zip(
+            (n_layer, n_slot, n_head, n_kv_head, head_dim, cap, track),
+            ("n_layer", "n_slot", "n_head", "n_kv_head", "head_dim", "cap", "track"))))
         self._dtypes = {torch.float32: PNB_F32, torch.bfloat16: PNB_BF16}
         self._int32 = torch.int32
         self._raw_stream = torch._C._cuda_getCurrentRawStream
@@ -96,20 +105,22 @@ class Kv4Cache:
 
     def reset(self, slot: Optional[int] = None, stream=None):
         """Empty one slot, or all of them (which also clears the error bits), in every layer."""
+        if slot is not None and not 0 <= slot < self._n_slot:
+            raise PnbError(-1, f"reset: slot {slot} of {self._n_slot}")
         check(pnb_kvq_reset(self._h, -1 if slot is None else slot, self._stream(stream)), "pnb_kvq_reset")
 
     def append(self, layer: int, k, v, n_new=None, start=None, stream=None):
         """Quantise and append n_new[b] (default: all T) rows of every slot b at entry
         start[b] (default: its length).  n_new, start: device int32 [n_slot]."""
         shape = self._shape(k, "k", self._n_kv)
-        check(pnb_kvq_append(self._h, layer, self._rows(k, "k", shape), self._rows(v, "v", shape),
+        check(pnb_kvq_append(self._h, _i32(layer, "layer"), self._rows(k, "k", shape), self._rows(v, "v", shape),
                              shape[1], self._ints(n_new, "n_new"), self._ints(start, "start"),
                              self._stream(stream)), "pnb_kvq_append")
 
     def read(self, layer: int, k, v, first=None, stream=None):
         """Write the values of entries first[b] (default 0) .. + T - 1 into k and v."""
         shape = self._shape(k, "k", self._n_kv)
-        check(pnb_kvq_read(self._h, layer, self._ints(first, "first"), shape[1],
+        check(pnb_kvq_read(self._h, _i32(layer, "layer"), self._ints(first, "first"), shape[1],
                            self._rows(k, "k", shape), self._rows(v, "v", shape),
                            self._stream(stream)), "pnb_kvq_read")
 
@@ -121,7 +132,7 @@ class Kv4Cache:
             decay = -1.0
         elif not decay >= 0.0:
             raise PnbError(-1, f"decay {decay} is negative or not a number")
-        check(pnb_kvq_attention(self._h, layer, self._rows(q, "q", shape), shape[1],
+        check(pnb_kvq_attention(self._h, _i32(layer, "layer"), self._rows(q, "q", shape), shape[1],
                                 self._rows(out, "out", shape), decay, self._stream(stream)),
               "pnb_kvq_attention")
 
@@ -130,8 +141,10 @@ class Kv4Cache:
         """Keep at most ``budget`` entries per slot and KV head, in place or into
         (dst, dst_layer); see pnb_kvq_evict for which."""
         d = self if dst is None else dst
-        check(pnb_kvq_evict(self._h, layer, d._h, layer if dst_layer is None else dst_layer, budget,
-                            n_sink, n_recent, self._stream(stream)), "pnb_kvq_evict")
+        check(pnb_kvq_evict(self._h, _i32(layer, "layer"), d._h,
+                            layer if dst_layer is None else _i32(dst_layer, "dst_layer"), _i32(budget, "budget"),
+                            _i32(n_sink, "n_sink"), _i32(n_recent, "n_recent"), self._stream(stream)),
+              "pnb_kvq_evict")
 
     def _view(self, layer: int, name: str):
         import torch
@@ -139,7 +152,7 @@ class Kv4Cache:
         key = (layer, name)
         if key not in self._views:
             v = pnb_kvq_views()
-            check(pnb_kvq_layer_views(self._h, layer, ctypes.byref(v)), "pnb_kvq_layer_views")
+            check(pnb_kvq_layer_views(self._h, _i32(layer, "layer"), ctypes.byref(v)), "pnb_kvq_layer_views")
             g = self.cfg
             shape = (g.n_slot,) if name in ("len", "seen") else (g.n_slot, g.n_kv_head, g.cap)
             n = 1
