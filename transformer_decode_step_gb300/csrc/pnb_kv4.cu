@@ -1,7 +1,6 @@
 // pnb_kv4.cu - the 4-bit KV cache's append (quantisation), read-back and
 // eviction kernels.  Layout: pnb_kv4.cuh.
 #include <cooperative_groups.h>
-#include <cuda_fp16.h>
 
 #include "pnb_kv4.cuh"
 
@@ -437,21 +436,15 @@ __device__ __forceinline__ void store16(void *p, int64_t at, int part, const flo
         part ? make_float4(x[4], x[5], x[6], x[7]) : make_float4(x[0], x[1], x[2], x[3]);
 }
 
-// d (u - 8) of a word's 8 codes: nibbles n and n + 4 under fp16 exponents are
-// 1024 + u (or 1024 + 16 u), u - 8 is exact in fp16 and its product in fp32
+// d (u - 8) of a word's 8 codes
 __device__ __forceinline__ void q4_values(uint32_t w, float d, float (&x)[8]) {
-  const __half2 off = __half2half2(__ushort_as_half(0x6408)), sixteenth = __half2half2(__ushort_as_half(0x2c00)),
-                m72 = __half2half2(__ushort_as_half(0xd480));
+  uint32_t b[4];
+  code_pairs(w, 0x64006400u, b);
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const uint32_t lo = (w & 0x000f000fu) | 0x64006400u, hi = (w & 0x00f000f0u) | 0x64006400u;
-    const float2 l = __half22float2(__hsub2(*reinterpret_cast<const __half2 *>(&lo), off));
-    const float2 h = __half22float2(__hfma2(*reinterpret_cast<const __half2 *>(&hi), sixteenth, m72));
-    x[2 * i] = d * l.x;
-    x[2 * i + 4] = d * l.y;
-    x[2 * i + 1] = d * h.x;
-    x[2 * i + 5] = d * h.y;
-    w >>= 8;
+  for (int n = 0; n < 4; ++n) {
+    const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&b[n]));
+    x[n] = d * v.x;
+    x[n + 4] = d * v.y;
   }
 }
 

@@ -23,6 +23,7 @@
 // a lane (r, c) multiplies its softmax weights of that position pair with.
 #pragma once
 
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -167,6 +168,34 @@ inline cudaError_t kv4_launch(K kern, dim3 grid, dim3 block, size_t smem, int cl
   cfg.attrs = attr;
   cfg.numAttrs = na;
   return cudaLaunchKernelEx(&cfg, kern, a);
+}
+
+// The code pairs of a word as fp16 pairs u - 8, exactly: nibbles 0 and 4
+// (b[0]), 1 and 5 (b[1]), 2 and 6 (b[2]), 3 and 7 (b[3]).  As published for 4-bit
+// weights: a masked nibble under the exponent of 1024 is the number 1024 + u (or
+// 1024 + 16 u), and one packed operation takes the rest away.  (Left as subnormals u * 2^-24, which
+// saves that operation, the codes lose up to 10 bits in the matrix
+// instruction's alignment: outputs were 8e-5 off instead of 1e-6.)  `magic` is
+// 0x64006400 in a register: as a second immediate it would cost a second
+// logic instruction per mask.
+__device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t mask, uint32_t magic) {
+  uint32_t d;
+  asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(d) : "r"(w), "r"(mask), "r"(magic));
+  return d;
+}
+
+__device__ __forceinline__ void code_pairs(uint32_t w, uint32_t magic, uint32_t (&b)[4]) {
+  const __half2 off = __half2half2(__ushort_as_half(0x6408)), sixteenth = __half2half2(__ushort_as_half(0x2c00)),
+                m72 = __half2half2(__ushort_as_half(0xd480));
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t lo = and_or(w, 0x000f000fu, magic), hi = and_or(w, 0x00f000f0u, magic);
+    const __half2 l = __hsub2(*reinterpret_cast<const __half2 *>(&lo), off);
+    const __half2 h = __hfma2(*reinterpret_cast<const __half2 *>(&hi), sixteenth, m72);
+    b[2 * i] = *reinterpret_cast<const uint32_t *>(&l);
+    b[2 * i + 1] = *reinterpret_cast<const uint32_t *>(&h);
+    w >>= 8;
+  }
 }
 
 // a + b on packed pairs of fp32

@@ -23,8 +23,6 @@
 // second product.
 // (With the rows as A's 16 rows, high parts over low parts, both products took
 // twice the matrix instructions and the outputs twice the registers.)
-#include <cuda_fp16.h>
-
 #include <cfloat>
 
 #include "pnb_kv4.cuh"
@@ -78,34 +76,6 @@ __device__ __forceinline__ void mma_f16_new(float (&d)[4], uint32_t a0, uint32_t
       "{%10,%10,%10,%10};"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
-}
-
-// The code pairs of a word as fp16 pairs u - 8, exactly: nibbles 0 and 4
-// (b[0]), 1 and 5 (b[1]), 2 and 6 (b[2]), 3 and 7 (b[3]).  A masked nibble
-// under the exponent of 1024 is the number 1024 + u (or 1024 + 16 u), and one
-// packed operation takes the rest away.  (Left as subnormals u * 2^-24, which
-// saves that operation, the codes lose up to 10 bits in the matrix
-// instruction's alignment: outputs were 8e-5 off instead of 1e-6.)  `magic` is
-// 0x64006400 in a register: as a second immediate it would cost a second
-// logic instruction per mask.
-__device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t mask, uint32_t magic) {
-  uint32_t d;
-  asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(d) : "r"(w), "r"(mask), "r"(magic));
-  return d;
-}
-
-__device__ __forceinline__ void code_pairs(uint32_t w, uint32_t magic, uint32_t (&b)[4]) {
-  const __half2 off = __half2half2(__ushort_as_half(0x6408)), sixteenth = __half2half2(__ushort_as_half(0x2c00)),
-                m72 = __half2half2(__ushort_as_half(0xd480));
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const uint32_t lo = and_or(w, 0x000f000fu, magic), hi = and_or(w, 0x00f000f0u, magic);
-    const __half2 l = __hsub2(*reinterpret_cast<const __half2 *>(&lo), off);
-    const __half2 h = __hfma2(*reinterpret_cast<const __half2 *>(&hi), sixteenth, m72);
-    b[2 * i] = *reinterpret_cast<const uint32_t *>(&l);
-    b[2 * i + 1] = *reinterpret_cast<const uint32_t *>(&h);
-    w >>= 8;
-  }
 }
 
 __device__ __forceinline__ float ex2(float x) {
