@@ -417,7 +417,8 @@ int pnb_attention_decode_static(const float *q_dev, const void *k_dev, const voi
 /* ------------------------------------------------------- 4-bit KV cache
    Decode attention over a KV cache held in GGUF Q4_0 blocks, for callers whose
    contexts outgrow a bf16 cache: 4.5 bits per value, 144 bytes per position
-   and KV head at head_dim 128 where bf16 takes 512.  No counterpart in the
+   and KV head at head_dim 128 where bf16 takes 512, and 8 more for the entry's
+   id and weight.  No counterpart in the
    Pantheon pages; it stands beside pnb_attention_decode_static (attention over
    a caller's cache, one layer per call) and takes K rows after RoPE as every
    cache of this library does.
@@ -437,9 +438,11 @@ int pnb_attention_decode_static(const float *q_dev, const void *k_dev, const voi
 
    All calls are stream-ordered and may be captured into a CUDA graph (lengths
    are read on the device).  The library allocates the cache's workspace in
-   pnb_kvq_new; calls on one cache share it, so at most one may be in flight
-   per cache, on any stream, graphs included.  Errors found on the device
-   (PNB_DEV_ERR_FULL, _RANGE, _TIMEOUT) set bits that pnb_kvq_check reads.
+   pnb_kvq_new (for evictions 8 bytes per entry of one layer, for tracked weights
+   4 bytes per entry and row, and partial sums of up to 80 KB per SM); calls on
+   one cache share it, so at most one may be in flight per cache, on any stream,
+   graphs included.  Errors found on the device (PNB_DEV_ERR_FULL, _RANGE,
+   _TIMEOUT) set bits that pnb_kvq_check reads.
    A length outside [0, cap] in the buffer is taken as the nearer of the two. */
 typedef struct {
   int32_t n_layer, n_slot;    /* layers; sequences, at most 1024 */
@@ -503,10 +506,11 @@ int pnb_kvq_read(pnb_kvq *c, int32_t layer, const int32_t *first_dev, int32_t T,
    Drafted tokens are attended before an eviction, which reorders entries.
    T * n_head / n_kv_head <= 64 (PNB_E_UNSUPPORTED).  q and out may differ in
    dtype; out may be q's own rows when they have the same strides and dtype.
-   fp32 outputs carry about 1e-6 of relative error (of a row of one head, and
-   beside what fp32 scores of the row's size are rounded by) against exact
-   arithmetic on the held values, however the weight is spread over them; bf16
-   outputs are the rounding of the same numbers.
+   fp32 outputs carry about 1e-6 of relative error (in the norm of a head's row)
+   against exact arithmetic on the held values, and what the rounding of large
+   scores adds (a few 2^-23 of the sum of their terms' magnitudes); entries whose
+   weight lies below 2^-60 of the row's largest may count as 0.  bf16 outputs are
+   the rounding of the same numbers.
    decay < 0: the weights stay as they are.  decay >= 0 (finite; T <= track,
    else PNB_E_INVAL): weights[j] = decay * weights[j] + the sum over the T
    tokens and the KV head's query heads of the softmax weight of entry j
@@ -518,14 +522,14 @@ int pnb_kvq_attention(pnb_kvq *c, int32_t layer, const pnb_rows *q, int32_t T, c
 /* Cut every slot that holds more than `budget` entries (1 <= budget <= dst's
    cap) down to it, per KV head: entries with id < n_sink or among the last
    n_recent ids stay (n_sink + n_recent <= budget), and of the others those
-   with the largest weights, the lower index first among equals (a NaN weight
-   counts by its sign bit as larger or smaller than every number).  The
-   entries that stay below index `budget` keep their index; those behind move,
-   in order, into the places of the dropped ones.  dst may be another cache or
-   layer of the same n_slot, n_kv_head and head_dim (shorter slots are copied
-   whole, src is not changed), or src itself in place; their buffers are the
-   same or do not overlap (PNB_E_INVAL).  src's cap is at most 2^18
-   (PNB_E_UNSUPPORTED). */
+   with the largest weights, the lower index first among equals, 0 and -0 among
+   them (a NaN weight counts by its sign bit as larger or smaller than every
+   number).  The entries that stay below index `budget` keep their index; those
+   behind move, in order, into the places of the dropped ones.  dst may be
+   another cache or layer of the same n_slot, n_kv_head and head_dim (shorter
+   slots are copied whole, src is not changed), or src itself in place; their
+   buffers are the same or do not overlap (PNB_E_INVAL).  src's cap is at most
+   2^18 (PNB_E_UNSUPPORTED). */
 int pnb_kvq_evict(pnb_kvq *src, int32_t src_layer, pnb_kvq *dst, int32_t dst_layer, int32_t budget,
                   int32_t n_sink, int32_t n_recent, pnb_stream stream);
 

@@ -104,7 +104,7 @@ __device__ __noinline__ uint32_t q4_word_checked(float4 a, float4 b, float df, f
 }
 
 // A block's scale from its largest magnitude: d = fp16(max|x| / 7), the quotient
-// correctly rounded by one residual step.  NaN and infinities make it NaN; a
+// correctly rounded by one residual step (Markstein's correction).  NaN and infinities make it NaN; a
 // scale past fp16's range saturates.
 struct Q4Scale {
   __half d;
@@ -238,7 +238,7 @@ struct AppendRange {
 // First every (token, head, K or V) row is quantised, TPR threads each; then
 // each 16-byte unit of V words (8 positions of 4 dims) that holds a new
 // position is read, completed and written by one thread.  Bound by its four
-// dependent trips to memory (one token of 64 slots x 8 heads, bf16: 3.0 us).
+// dependent trips to memory (one token of 64 slots x 8 heads, bf16: 2.6 us).
 constexpr int kStepThreads = 512;
 
 template <int NG, typename T>
@@ -314,8 +314,7 @@ __global__ void __launch_bounds__(kStepThreads) k_kv4_append_step(const __grid_c
 // CTAs to have read the length moves it.  Bound by the rows' bytes in fp32
 // (8191 tokens of 32 heads at head_dim 128 in 48.9 us, 6.3 TB/s) and by the
 // quantiser's instructions in bf16 (32.8 us, 5.2 TB/s; at head_dim 64 4.2 TB/s).
-// Four CTAs per SM: fp32 with the 71 registers that it would take 50.4 -> 52.3 us,
-// bf16 at 48 registers 33.4 -> 32.6 us but four short prompts 5.7 -> 6.1 us.
+// Four CTAs per SM: fp32 would take 71 registers and 52.3 us instead of 50.4.
 constexpr int kAppendThreads = 256, kAppendChunks = 8;
 
 template <int NG, typename T>
@@ -575,8 +574,7 @@ __global__ void __launch_bounds__(kReadThreads) k_kv4_read(const __grid_constant
 // dropped ones' places below it ("holes"), both in index order: src_of[p] is p
 // or, for hole r, -1 - r, and movers[r] what goes there.  Bound by the latency
 // of its barriers (8 heads each: 64 slots at 1000 entries 8 us, four at 32k in
-// clusters of eight CTAs 17 us; CTAs of 512 or 1024 threads with as many entries
-// 8.9 and 13 us, 17 and 25 us).
+// clusters of eight CTAs 17 us, of 1024 threads each 25 us).
 template <int THREADS, int K>
 __global__ void __launch_bounds__(THREADS, THREADS >= 1024 ? 1 : 3) k_kv4_select(const __grid_constant__ Kv4EvictArgs a) {
   constexpr int WARPS = THREADS / 32, COPIES = 4, BITS = 10, BINS = 1 << BITS;
@@ -967,8 +965,8 @@ int chunk_groups(int T, int group) { return ((T + kKv4Chunk - 2) / kKv4Chunk + g
 
 // Chunks per CTA: up to `most` (append 8: one prompt of 8191 in fp32 48.9 us against
 // 50.4 with four and 57.0 with two; 8 x 4096 at head_dim 32 in fp32 15.0, 16.9,
-// 20.5), fewer while all CTAs fit the GPU at once (four on each SM).  bf16 append / fp32 read, us, always four chunks against
-// this rule and against always one: 1 sequence x 8 heads x 256 tokens 6.1 / 5.9,
+// 20.5), fewer while all CTAs fit the GPU at once (four on each SM).  bf16 append /
+// fp32 read, us, always four chunks against this rule and against always one: 1 sequence x 8 heads x 256 tokens 6.1 / 5.9,
 // 3.1 / 3.0, 3.0 / 3.1; 4 x 8 x 1031 7.8 / 8.4, 6.6 / 8.1, 7.2 / 8.4; 1 x 32 x
 // 8191 35.4 / 49.5, 35.3 / 49.6, 43.6 / 53.8.
 constexpr int kChunkCtasPerSm = 4;
@@ -981,11 +979,15 @@ int chunk_group(int T, int n_kv, int n_slot, int sms, int most) {
 
 template <int NG, typename T>
 cudaError_t run_append(Kv4AppendArgs a, cudaStream_t st) {
-  // One CTA per slot (2.4 us and 0.6 for every 2048 values of a slot's rows)
-  // against one per chunk and head (3.2 us while all are resident, 12 us for
-  // 2048 of them); bf16, head_dim 128, us, step form first:
-  //   64 slots x 8 heads: 1 token 3.0, 4.7; 2 tokens 3.3, 4.5; 8 tokens 8.2, 4.5
-  //   1 x 32: 1 token 4.8, 3.2     256 x 8: 1 token 3.6, 11.8; 4 tokens 6.4, 12.2
+  // One CTA per slot against one per chunk and head, us, step form first, at
+  // head_dim 128 bf16, then 64 fp32, then 32 fp32 (the types differ by less than
+  // a tenth):
+  //   64 slots x 8 heads, 1 token    2.6, 3.8    2.6, 3.6    2.5, 3.6
+  //   64 x 8, 8 tokens               7.3, 4.0    4.8, 3.4    3.3, 3.8
+  //   1 x 32, 1 token                3.9, 2.8    2.9, 2.9    2.6, 2.9
+  //   256 x 8, 4 tokens              5.8, 11.8   3.9, 9.9    3.2, 10.1
+  //   1024 x 1, 8 tokens             7.9, 6.6    7.4, 5.7    7.9, 5.9
+  // (the last, many tokens of few heads, is where the rule picks the slower form)
   const int64_t values = (int64_t)a.T * a.n_kv * 32 * NG;
   if (values <= 2048 || (values <= 8192 && (int64_t)a.n_slot * a.n_kv > 1024))
     return kv4_launch(k_kv4_append_step<NG, T>, dim3(a.n_slot), dim3(kStepThreads), (size_t)values / 2, 1, st, a);

@@ -248,9 +248,8 @@ __device__ __forceinline__ void kv4_prefix(const Kv4Layer &l, int n_slot, int un
 }
 
 // The slot whose range of the prefix sums holds x (0 <= x < pre[n_slot]; the same
-// x in all lanes): the number of ranges that end at or before it.  (As a binary
-// search, six dependent loads for 64 slots, attention over 64 slots took 41.4 us
-// instead of 40.5.)
+// x in all lanes): the number of ranges that end at or before it.  (A binary
+// search, six dependent loads for 64 slots, adds 1 us to attention over them.)
 __device__ __forceinline__ int kv4_find(const int *pre, int n_slot, int x) {
   const int lane = threadIdx.x & 31;
   int n = 0;

@@ -32,15 +32,15 @@ namespace pnb {
 namespace {
 
 // Work units: an item (slot, KV head, block of 8 query rows) takes one per
-// chunk of 32 positions and kItemUnits more for its queries and its end (5
-// drafted tokens over ragged slots 16.9 us with one, 15.3 with two, 15.9 with
-// three).
+// chunk of 32 positions and kItemUnits more for its queries and its end (21 slots x
+// 4 heads x 3 blocks of rows, lengths up to 200, 10.9 us with one, 10.8 with two,
+// 13.3 with three; 64 x 8 heads at 1200 27.6, 26.6, 27.3).
 constexpr int kItemUnits = 2;
 // While no item has more units than this, none is split over CTAs (head_dim 128,
-// us, whole against split: 8 KV heads of one sequence 6 units 5.8, 8.6; 18 units
-// 8.2, 9.3; 26 units 9.1, 9.4; 34 units 10.2, 9.5.  21 slots x 4 heads x 3 blocks
-// of rows, lengths up to 200 10.6, 16.2; all 800 17.7, 20.1.  64 x 8 heads, all
-// 100 10.9, 12.7; all 600 19.1, 18.3; all 1200 27.3, 26.5)
+// us, whole against split: 8 KV heads of one sequence 6 units 6.3, 9.2; 18 units
+// 8.7, 9.4; 26 units 9.4, 9.5; 34 units 10.6, 9.6.  21 slots x 4 heads x 3 blocks
+// of rows, lengths up to 200 10.8, 13.6; all 800 18.4, 18.9.  64 x 8 heads, all
+// 100 11.2, 12.6; all 600 19.6, 18.5; all 1200 27.6, 26.5)
 constexpr int kWholeUnits = 28;
 
 template <int NG, bool PAIR, bool SPLIT>
@@ -247,24 +247,20 @@ __device__ __forceinline__ void finish_row(const Kv4AttnArgs &a, int b, int h, i
 // items), its own queries and softmax state.  Items that lie in one warp are
 // finished by it; the others leave partial rows, which the CTA adds up at its
 // end, and for items shared by CTAs the last CTA to arrive does, all in the
-// order of the units, so that results do not depend on the run.  (With the
-// CTA's warps on one item at a time, the two barriers and the queries' load at
-// each item cost 3.5 us: 64 ragged slots took 79 us and short slots beside long
-// ones 41.)
+// order of the units, so that results do not depend on the run.  (The CTA's
+// warps on one item at a time pay two barriers and the queries' load for each.)
 // The registers (128) leave 16 warps on an SM.  As one CTA of 16 they share fewer
-// items between CTAs than as two of 8: 128k positions 56.4 us against 59.3, 64
-// ragged slots 41.4 against 42.4, 8 KV heads at 8192 positions 10.2 against 11.6,
-// at 32768 15.4 against 16.9; 32 MHA heads at 2048 9.8 against 9.2, at 4096 11.4
-// against 11.3.
-// 64 slots at 512..4096 positions (8 x 4 heads, head_dim 128, fp32) take 40.3 us
-// (3.9 TB/s), two contexts of 100k and 128k (bf16) 56.5 us (4.7 TB/s).  With the
-// copies alone, no products, they take 34.2 and 45.2: about 23 and 39 for the
-// bytes, the rest for launch, start (lengths, queries and first chunk in turn)
-// and merges, which is all that short caches have.  What the products add is
-// bound by the unpacking, 9 instructions for 8 codes, on the integer pipe (56 to
-// 59 % busy over the launch).  No gain from: queries in wider shared
-// loads, the shift of a code word as a multiplication (64 slots 41.6 -> 43.7 us), the
-// masks of odd columns as multiplications, the next entries of the merge ahead.
+// items between CTAs than as two of 8, whose barriers and merges are cheaper:
+// 128k positions 58.0 us against 60.3, 64 ragged slots 41.5 against 42.7, 16 rows
+// of 32 heads at 6007 28.9 against 31.0, 8 KV heads at 32768 15.7 against 16.8;
+// but 32 MHA heads at 2048 10.0 against 9.3, 64 x 8 heads at 100 11.2 against 9.5.
+// 64 slots at 512..4096 positions (8 x 4 heads, head_dim 128, fp32) take 41.3 us
+// (3.8 TB/s), two contexts of 100k and 128k (bf16) 57.8 us (4.6 TB/s).  The bytes
+// alone are 23 and 39 of that; the rest is launch, start (lengths, queries and
+// first chunk in turn) and merges, which is all that short caches have, and the
+// latency of a chunk's chain from codes to sums, at four warps per scheduler
+// (issue slots 58 and 64 % busy over the launch, the integer pipe, which
+// unpacks 8 codes in 9 instructions, 45 and 50 %).
 template <int NG, bool PAIR, bool SPLIT, bool TRACK>
 __global__ void __launch_bounds__(kKv4Threads, kKv4CtasPerSm)
     k_kv4_attn(const __grid_constant__ Kv4AttnArgs a) {
@@ -620,7 +616,7 @@ __global__ void __launch_bounds__(kKv4Threads, kKv4CtasPerSm)
       // in 2^2 .. 2^15 whatever the chunks before it held (a first entry that takes
       // nearly all the weight, say).  Products keep 22 bits down to 2^-3 and lose one
       // per power of two from there.  (One reference for all chunks, that of the
-      // largest score, left 2 % of error beside such an entry.  New references by
+      // largest score, left up to 4 % of error beside such an entry.  New references by
       // every chunk's own largest scores, with the sums' factors: 64 slots 47.5 us.)
       bool off = uneven;                // some row's reference does not fit
       float xmax[RL], lmul = 1.f;
@@ -953,7 +949,7 @@ __global__ void __launch_bounds__(kKv4Threads, kKv4CtasPerSm)
 
 // weights[j] = decay * weights[j] + sum over the rows of 2^(x_ij - ref_i) / l_i: each
 // position has one owner that adds its rows in order.  Bound by latency (8 slots
-// at 512..4096, 8 x 4 heads: 4 us behind the attention's 14) and, with many rows,
+// at 512..4096, 8 x 4 heads: 4 us behind the attention's 13) and, with many rows,
 // by the scores' bytes (16 rows of 32 heads at 6007 positions, 12 MB: 6 us).
 // Each thread has four positions; PARTS groups of threads share out the rows of
 // the same positions, and the first adds up the groups' sums in order.
@@ -1079,8 +1075,8 @@ cudaError_t run_weights(const Kv4WeightArgs &a, cudaStream_t st) {
 
 cudaError_t launch_kv4_weights(const Kv4WeightArgs &a, cudaStream_t st) {
   // rows in one or four parts, tracked attention at head_dim 64, us: 64 rows, 2
-  // slots at 367 16.3, 12.4; 56 rows, 14 at 958 24.1, 18.5; 64 rows, 8 x 32768 72.0,
-  // 68.7; 24 rows, 15 x 20000 35.5, 36.4; 16 rows, 64 x 8 at 1000 42.6, 47.3
+  // slots at 367 14.7, 12.3; 56 rows, 14 at 958 22.5, 18.6; 64 rows, 8 x 32768 69.3,
+  // 69.0; 24 rows, 15 x 20000 35.1, 37.0; 16 rows, 64 x 8 at 1000 43.2, 47.9
   return a.rows < 32 ? run_weights<1>(a, st) : run_weights<4>(a, st);
 }
 
