@@ -545,6 +545,108 @@ int pnb_kvq_layer_views(const pnb_kvq *c, int32_t layer, pnb_kvq_views *out);
    PNB_E_DEVICE when any is set. */
 int pnb_kvq_check(pnb_kvq *c, int32_t *device_error);
 
+/* ------------------------------------------------------- paged KV cache
+   K and V of many sequences in pages of one pool, so that a sequence needs no
+   contiguous room and several sequences can hold the same pages (a common
+   system prompt, a document with many questions).  It stands beside the 4-bit
+   cache: one layer per call, for callers that keep their own sequences.  No
+   counterpart in the Pantheon pages.
+
+   The pool is the caller's buffer, row-major bf16,
+     [n_layer][n_page][2 (K, V)][n_kv_head][page][head_dim].
+   Entry i of a sequence lies in row i % page of the page that the sequence's
+   page table names at i / page.  Keys are held after RoPE.  What the pool's
+   other rows hold (rows behind a sequence's last entry, free pages) does not
+   matter, be it NaN or infinity; the entries of a sequence themselves are
+   finite (the rows of a call that share 128 entries of a sequence, one of which
+   holds a NaN or an infinity, may all answer NaN).
+
+   All calls are stream-ordered, allocate nothing and may be captured into a CUDA
+   graph: page tables, lengths and token counts are read on the device.  The
+   library allocates the cache's workspace in pnb_pkv_new (partial sums, about
+   40 MB; with shared_tok n_head * (head_dim + 2) * 4 bytes per token more);
+   calls on one cache share it, so at most one attention call may be in flight
+   per cache, on any stream, graphs included. */
+typedef struct {
+  int32_t n_layer, n_page, page;  /* pages per layer; entries per page: 16, 32, 64 or 128 */
+  int32_t n_head, n_kv_head;      /* n_head % n_kv_head == 0, at most 64 query heads per KV head */
+  int32_t head_dim;               /* 64 or 128 */
+  int32_t shared_tok;             /* most tokens per pnb_pkv_attention_shared call (0: none) */
+  int32_t rope_neox;              /* pnb_pkv_append: 0 turns pairs (2i, 2i + 1), 1 (i, i + head_dim / 2) */
+  int32_t rope_section[3];        /* pairs that turn by each of three position axes, in order (sum
+                                     head_dim / 2); 0, 0, 0: one axis */
+  double rope_theta;              /* pair i turns by pos * rope_theta^(-2i/head_dim); 0: no rotation */
+} pnb_pkv_config;
+typedef struct pnb_pkv pnb_pkv;
+
+/* The sequences of a call and its tokens, packed one sequence after another:
+   rows [token][head][head_dim] (the `slot` stride of a pnb_rows is not used).
+   The tokens of sequence b are start[b] .. start[b + 1] - 1, n of them, and its
+   last n entries: token t of them is entry len[b] - n + t.  Rows from
+   start[n_seq] on belong to no sequence and are left as they are.
+   Lengths, counts and page ids that are out of range reach no memory outside
+   the buffers and set PNB_DEV_ERR_RANGE. */
+typedef struct {
+  int32_t n_seq;              /* 1 .. 1024 */
+  int32_t max_page;           /* row stride of the page tables */
+  const int32_t *start_dev;   /* [n_seq + 1], not decreasing, 0 <= start <= n_tok; NULL: n_tok / n_seq tokens
+                                 each */
+  const int32_t *len_dev;     /* [n_seq] entries, this call's tokens included; 0 .. max_page * page */
+  const int32_t *pages_dev;   /* [n_seq][max_page] page ids */
+} pnb_pkv_batch;
+
+/* Bytes of a cache's pool; 0 for an invalid or unsupported config. */
+size_t pnb_pkv_bytes(const pnb_pkv_config *cfg);
+
+/* Create a cache over a caller-owned pool (128-byte aligned) on the current
+   device.  The pool is not touched. */
+int pnb_pkv_new(const pnb_pkv_config *cfg, void *pool_dev, size_t bytes, pnb_pkv **out);
+void pnb_pkv_free(pnb_pkv *c);
+
+/* Rotate and store n_tok >= 1 tokens' keys and store their values (rounded to
+   bf16), and, when q is given, write the rotated queries to q_out (which may be
+   q's own rows).  q, k and v have one dtype, q_out may have the other.
+   pos_dev: int32 [n_tok] positions, [3][n_tok] with rope_section; NULL: a
+   token's entry index, on every axis.  The angle is kept in 64-bit fixed point
+   (exact for every int32 position up to the rounding of theta's powers in
+   double), rotations are in fp32.
+   Entries that a call stores are in pages that no other sequence of the call
+   stores to.  A token whose entry is not in its page table is dropped
+   (PNB_DEV_ERR_FULL; its query is still rotated). */
+int pnb_pkv_append(pnb_pkv *c, int32_t layer, const pnb_pkv_batch *b, int32_t n_tok, const pnb_rows *k,
+                   const pnb_rows *v, const pnb_rows *q, const pnb_rows *q_out, const int32_t *pos_dev,
+                   pnb_stream stream);
+
+/* Causal attention of n_tok >= 1 query tokens over their sequences' entries
+   (whole prompts, prompt chunks, drafted tokens, single tokens, in any
+   mixture): token t of sequence b attends to entries [0, i], i = len[b] - n + t,
+   under a window (> 0) to [max(0, i - window + 1), i].
+     q    [n_tok][n_head][head_dim], already rotated
+     out  the same shape: softmax(q.k / sqrt(head_dim)) applied to V
+   A token with nothing to attend to (i < 0) answers 0.  q and out may differ in
+   dtype; out may be q's own rows when they have the same strides and dtype.
+   With fp32 on either side queries and softmax weights enter the products with
+   16 bits or more (about 2e-6 relative); with bf16 on both, prompts round the
+   weights to bf16 (about 1.7e-3, as much as the rounding of the output).
+   Results do not depend on the run: no atomic sums. */
+int pnb_pkv_attention(pnb_pkv *c, int32_t layer, const pnb_pkv_batch *b, int32_t n_tok, const pnb_rows *q,
+                      const pnb_rows *out, int32_t window, pnb_stream stream);
+
+/* The same answer where sequences share a prefix: group g is the sequences
+   group_start[g] .. group_start[g + 1] - 1 (device int32 [n_group + 1], from 0
+   to n_seq, not decreasing), whose page tables name the same pages for their
+   first prefix[g] entries (device int32 [n_group], rounded down to whole pages,
+   at most len - n of every sequence of the group).  Each group's prefix is read
+   once for all its tokens.  Every sequence has n_tok / n_seq tokens
+   (start_dev NULL).  n_tok <= shared_tok (PNB_E_INVAL). */
+int pnb_pkv_attention_shared(pnb_pkv *c, int32_t layer, const pnb_pkv_batch *b, int32_t n_group,
+                             const int32_t *group_start_dev, const int32_t *prefix_dev, int32_t n_tok,
+                             const pnb_rows *q, const pnb_rows *out, int32_t window, pnb_stream stream);
+
+/* Synchronise, read and clear the cache's device error bits (PNB_DEV_ERR_*);
+   returns PNB_E_DEVICE when any was set. */
+int pnb_pkv_check(pnb_pkv *c, int32_t *device_error);
+
 /* Diagnostics: have the step's kernels record globaltimer stamps (ns) into
    trace_dev, laid out [launch][256][8]: launch = 6 * layer + kernel kind
    (PNB_KERNEL_*), 6 * n_layer for the LM head; the CTA's linear index

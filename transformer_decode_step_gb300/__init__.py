@@ -74,6 +74,17 @@ class pnb_kvq_views(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("len", "seen", "ids", "weights")]
 
 
+class pnb_pkv_config(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in
+                ("n_layer", "n_page", "page", "n_head", "n_kv_head", "head_dim", "shared_tok", "rope_neox")] + \
+               [("rope_section", ctypes.c_int32 * 3), ("rope_theta", ctypes.c_double)]
+
+
+class pnb_pkv_batch(ctypes.Structure):
+    _fields_ = [("n_seq", ctypes.c_int32), ("max_page", ctypes.c_int32)] + \
+               [(n, ctypes.c_void_p) for n in ("start_dev", "len_dev", "pages_dev")]
+
+
 _p, _i32, _sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
 _SIGS = {
     "pnb_model_create": (_i32, [_p, _p, _p]),
@@ -116,6 +127,13 @@ _SIGS = {
     "pnb_kvq_evict": (_i32, [_p, _i32, _p, _i32, _i32, _i32, _i32, _p]),
     "pnb_kvq_layer_views": (_i32, [_p, _i32, _p]),
     "pnb_kvq_check": (_i32, [_p, _p]),
+    "pnb_pkv_bytes": (_sz, [_p]),
+    "pnb_pkv_new": (_i32, [_p, _p, _sz, _p]),
+    "pnb_pkv_free": (None, [_p]),
+    "pnb_pkv_append": (_i32, [_p, _i32, _p, _i32, _p, _p, _p, _p, _p, _p]),
+    "pnb_pkv_attention": (_i32, [_p, _i32, _p, _i32, _p, _p, _i32, _p]),
+    "pnb_pkv_attention_shared": (_i32, [_p, _i32, _p, _i32, _p, _p, _i32, _p, _p, _i32, _p]),
+    "pnb_pkv_check": (_i32, [_p, _p]),
     "pnb_strerror": (ctypes.c_char_p, [_i32]),
 }
 for _name, (_res, _args) in _SIGS.items():
@@ -358,3 +376,4 @@ class State:
 
 from .synthetic import SynthModel  # noqa: E402  (generated-weight models for tests / bench)
 from .kv4 import Kv4Cache  # noqa: E402  (the 4-bit KV cache)
+from .paged import PagedBatch, PagedKv  # noqa: E402  (the paged KV cache)

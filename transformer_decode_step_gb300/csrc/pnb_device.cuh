@@ -24,6 +24,8 @@ constexpr unsigned long long kWaitLimitNs = 1000000000ull;  // bounded waits: 1 
 // device-side error bits (mirror of PNB_DEV_ERR_*)
 constexpr int kErrToken = 1;
 constexpr int kErrTimeout = 2;
+constexpr int kErrFull = 4;
+constexpr int kErrRange = 8;
 
 // -------------------------------------------------------------- shared mem
 __device__ __forceinline__ uint32_t smem_addr(const void *p) {
@@ -141,6 +143,15 @@ __device__ __forceinline__ float2 ffma2(float2 a, float2 b, float2 c) {
       : "l"(*reinterpret_cast<unsigned long long *>(&a)),
         "l"(*reinterpret_cast<unsigned long long *>(&b)),
         "l"(*reinterpret_cast<unsigned long long *>(&c)));
+  return *reinterpret_cast<float2 *>(&d);
+}
+
+// a + b on packed pairs of fp32
+__device__ __forceinline__ float2 fadd2(float2 a, float2 b) {
+  unsigned long long d;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(d)
+      : "l"(*reinterpret_cast<unsigned long long *>(&a)), "l"(*reinterpret_cast<unsigned long long *>(&b)));
   return *reinterpret_cast<float2 *>(&d);
 }
 

@@ -256,7 +256,7 @@ __global__ void __launch_bounds__(kStepThreads) k_kv4_append_step(const __grid_c
   for (int i = tid; i < work; i += kStepThreads) {
     const int row = i / TPR, sub = i % TPR, rr = row >> 1, h = rr % a.n_kv, t = rr / a.n_kv;
     const bool live = rr < rows, is_v = row & 1;
-    const Kv4Rows &src = is_v ? a.v : a.k;
+    const DevRows &src = is_v ? a.v : a.k;
     Raw8<T> raw;
     if (live) raw.load(src.p, b * src.slot + t * src.token + h * src.head + sub * 8);
     else raw.clear();
@@ -336,7 +336,7 @@ __global__ void __launch_bounds__(kAppendThreads, sizeof(T) == 4 ? 4 : 0) k_kv4_
   const int64_t bh = (int64_t)b * a.n_kv + h;
   const bool is_v = tid >= 128;
   const int th = tid & 127, sub = th % TPR, j = sub >> 2, cc = sub & 3, r0 = th / TPR;
-  const Kv4Rows &rows = is_v ? a.v : a.k;
+  const DevRows &rows = is_v ? a.v : a.k;
   const int ch0 = rg.start / kKv4Chunk + (int)blockIdx.x * a.group;
   const int ch1 = min(ch0 + a.group, (rg.end + kKv4Chunk - 1) / kKv4Chunk);
   const T *src = static_cast<const T *>(rows.p) + b * rows.slot + h * rows.head + sub * 8;
@@ -485,7 +485,7 @@ __global__ void __launch_bounds__(256) k_kv4_read_step(const __grid_constant__ K
       q4_values(w, d, x);
     }
   }
-  const Kv4Rows &o = is_v ? a.v : a.k;
+  const DevRows &o = is_v ? a.v : a.k;
   store8<T>(o.p, b * o.slot + t * o.token + h * o.head + sub * 8, x);
 }
 
@@ -990,10 +990,10 @@ cudaError_t run_append(Kv4AppendArgs a, cudaStream_t st) {
   // (the last, many tokens of few heads, is where the rule picks the slower form)
   const int64_t values = (int64_t)a.T * a.n_kv * 32 * NG;
   if (values <= 2048 || (values <= 8192 && (int64_t)a.n_slot * a.n_kv > 1024))
-    return kv4_launch(k_kv4_append_step<NG, T>, dim3(a.n_slot), dim3(kStepThreads), (size_t)values / 2, 1, st, a);
+    return launch_pdl(k_kv4_append_step<NG, T>, dim3(a.n_slot), dim3(kStepThreads), (size_t)values / 2, 1, st, a);
   a.group = chunk_group(a.T, a.n_kv, a.n_slot, a.sms, kAppendChunks);
   const dim3 grid(chunk_groups(a.T, a.group), a.n_kv, a.n_slot);
-  return kv4_launch(k_kv4_append<NG, T>, grid, dim3(kAppendThreads), 0, 1, st, a);
+  return launch_pdl(k_kv4_append<NG, T>, grid, dim3(kAppendThreads), 0, 1, st, a);
 }
 
 template <int NG, typename T>
@@ -1003,11 +1003,11 @@ cudaError_t run_read(Kv4ReadArgs a, cudaStream_t st) {
   // 32 tokens 7.0 both)
   if (a.T <= kReadStepTokens) {
     const int64_t threads = (int64_t)a.n_slot * a.T * a.n_kv * 8 * NG;
-    return kv4_launch(k_kv4_read_step<NG, T>, dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, 1, st, a);
+    return launch_pdl(k_kv4_read_step<NG, T>, dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, 1, st, a);
   }
   a.group = chunk_group(a.T, a.n_kv, a.n_slot, a.sms, kReadChunks);
   const dim3 grid(chunk_groups(a.T, a.group), a.n_kv, a.n_slot);
-  return kv4_launch(k_kv4_read<NG, T>, grid, dim3(kReadThreads), 0, 1, st, a);
+  return launch_pdl(k_kv4_read<NG, T>, grid, dim3(kReadThreads), 0, 1, st, a);
 }
 
 template <int NG>
@@ -1024,7 +1024,7 @@ template <int NG>
 cudaError_t run_move(const Kv4EvictArgs &a, cudaStream_t st) {
   const int most = a.budget < a.src.cap ? a.budget : a.src.cap, pos = kMoveChunks * kKv4Chunk;
   const dim3 grid((most + pos - 1) / pos, a.n_kv, a.n_slot);
-  return kv4_launch(k_kv4_move<NG>, grid, dim3(kMoveThreads), 0, 1, st, a);
+  return launch_pdl(k_kv4_move<NG>, grid, dim3(kMoveThreads), 0, 1, st, a);
 }
 
 }  // namespace
@@ -1047,11 +1047,11 @@ cudaError_t launch_kv4_evict(int ng, const Kv4EvictArgs &a, cudaStream_t st) {
   while (cl * per < cap) cl *= 2;
   const dim3 grid(cl, a.n_kv, a.n_slot);
   cudaError_t e;
-  if (per == 1024) e = kv4_launch(k_kv4_select<256, 4>, grid, dim3(256), 0, cl, st, a);
-  else if (per == 2048) e = kv4_launch(k_kv4_select<256, 8>, grid, dim3(256), 0, cl, st, a);
-  else if (per == 4096) e = kv4_launch(k_kv4_select<256, 16>, grid, dim3(256), 0, cl, st, a);
-  else if (per == 16384) e = kv4_launch(k_kv4_select<1024, 16>, grid, dim3(1024), 0, cl, st, a);
-  else e = kv4_launch(k_kv4_select<1024, 32>, grid, dim3(1024), 0, cl, st, a);
+  if (per == 1024) e = launch_pdl(k_kv4_select<256, 4>, grid, dim3(256), 0, cl, st, a);
+  else if (per == 2048) e = launch_pdl(k_kv4_select<256, 8>, grid, dim3(256), 0, cl, st, a);
+  else if (per == 4096) e = launch_pdl(k_kv4_select<256, 16>, grid, dim3(256), 0, cl, st, a);
+  else if (per == 16384) e = launch_pdl(k_kv4_select<1024, 16>, grid, dim3(1024), 0, cl, st, a);
+  else e = launch_pdl(k_kv4_select<1024, 32>, grid, dim3(1024), 0, cl, st, a);
   if (e != cudaSuccess) return e;
   return ng == 4 ? run_move<4>(a, st) : ng == 2 ? run_move<2>(a, st) : run_move<1>(a, st);
 }

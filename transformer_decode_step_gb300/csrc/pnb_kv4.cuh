@@ -29,6 +29,7 @@
 
 #include "pnb.h"
 #include "pnb_device.cuh"
+#include "pnb_rows.cuh"
 
 namespace pnb {
 
@@ -41,8 +42,6 @@ constexpr int kKv4MaxRows = 64;            // tokens x heads of a group in one c
 constexpr int kKv4MaxSlots = 1024;
 constexpr int kKv4MaxCap = 1 << 20;        // positions per slot
 constexpr int kKv4MaxEvictCap = 1 << 18;   // largest cache the eviction selects from
-constexpr int kErrFull = 4;                // mirror of PNB_DEV_ERR_FULL
-constexpr int kErrRange = 8;               // mirror of PNB_DEV_ERR_RANGE
 
 __host__ __device__ constexpr int kv4_chunk_bytes(int ng) { return 1152 * ng; }
 __host__ __device__ constexpr int kv4_kscale_off(int ng) { return 512 * ng; }
@@ -66,13 +65,6 @@ __host__ __device__ constexpr int kv4_vunit(int J, int r, int c) {
 // bit position of position p's nibble in its V word; its class is (p / 2) % 4
 __host__ __device__ constexpr int kv4_vshift(int p) { return 4 * ((p >> 3) + 4 * (p & 1)); }
 
-// rows of a caller's tensor [slot][token][head][head_dim], strides in elements
-struct Kv4Rows {
-  void *p;
-  int64_t slot, token, head;
-  int32_t dtype;
-};
-
 // one layer of a cache
 struct Kv4Layer {
   uint8_t *codes;       // [n_slot][n_kv][cap / 32] chunks
@@ -84,7 +76,7 @@ struct Kv4Layer {
 
 struct Kv4AppendArgs {
   Kv4Layer l;
-  Kv4Rows k, v;
+  DevRows k, v;
   const int32_t *n_new, *start;   // [n_slot] or NULL
   int32_t n_slot, n_kv, T, sms;   // (sms: the device's SM count)
   int32_t group;                  // chunks per CTA (set by the launcher)
@@ -94,7 +86,7 @@ struct Kv4AppendArgs {
 
 struct Kv4ReadArgs {
   Kv4Layer l;
-  Kv4Rows k, v;
+  DevRows k, v;
   const int32_t *first;           // [n_slot] or NULL
   int32_t n_slot, n_kv, T, sms;   // (sms: the device's SM count)
   int32_t group;                  // chunks per CTA (set by the launcher)
@@ -103,7 +95,7 @@ struct Kv4ReadArgs {
 
 struct Kv4AttnArgs {
   Kv4Layer l;
-  Kv4Rows q, out;
+  DevRows q, out;
   int32_t n_slot, n_kv, G, T, rows;  // rows = T * G
   int32_t nrb;                    // items per KV head (set by the launcher)
   float qscale;                   // log2(e) / sqrt(head_dim)
@@ -143,33 +135,6 @@ cudaError_t launch_kv4_evict(int ng, const Kv4EvictArgs &a, cudaStream_t st);
 cudaError_t launch_kv4_reset(int32_t *len, int32_t *seen, int64_t layer_stride, int n_layer, int n_slot,
                              int slot, cudaStream_t st);
 
-// launch with programmatic dependent launch: every kernel of the cache waits
-// (griddepcontrol.wait) before its first access to global memory
-template <typename K, typename A>
-inline cudaError_t kv4_launch(K kern, dim3 grid, dim3 block, size_t smem, int cluster, cudaStream_t st,
-                              const A &a) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = grid;
-  cfg.blockDim = block;
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[2];
-  int na = 0;
-  attr[na].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[na].val.programmaticStreamSerializationAllowed = 1;
-  ++na;
-  if (cluster > 1) {
-    attr[na].id = cudaLaunchAttributeClusterDimension;
-    attr[na].val.clusterDim.x = cluster;
-    attr[na].val.clusterDim.y = 1;
-    attr[na].val.clusterDim.z = 1;
-    ++na;
-  }
-  cfg.attrs = attr;
-  cfg.numAttrs = na;
-  return cudaLaunchKernelEx(&cfg, kern, a);
-}
-
 // The code pairs of a word as fp16 pairs u - 8, exactly: nibbles 0 and 4
 // (b[0]), 1 and 5 (b[1]), 2 and 6 (b[2]), 3 and 7 (b[3]).  As published for 4-bit
 // weights: a masked nibble under the exponent of 1024 is the number 1024 + u (or
@@ -196,15 +161,6 @@ __device__ __forceinline__ void code_pairs(uint32_t w, uint32_t magic, uint32_t 
     b[2 * i + 1] = *reinterpret_cast<const uint32_t *>(&h);
     w >>= 8;
   }
-}
-
-// a + b on packed pairs of fp32
-__device__ __forceinline__ float2 fadd2(float2 a, float2 b) {
-  unsigned long long d;
-  asm("add.rn.f32x2 %0, %1, %2;"
-      : "=l"(d)
-      : "l"(*reinterpret_cast<unsigned long long *>(&a)), "l"(*reinterpret_cast<unsigned long long *>(&b)));
-  return *reinterpret_cast<float2 *>(&d);
 }
 
 // Entries of slot b as the kernels use them: a length outside [0, cap] (the

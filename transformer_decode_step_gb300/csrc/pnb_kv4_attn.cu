@@ -175,7 +175,7 @@ struct Split {
 };
 
 template <int N>
-__device__ __forceinline__ void store_row(const Kv4Rows &o, int64_t at, const float (&v)[N]) {
+__device__ __forceinline__ void store_row(const DevRows &o, int64_t at, const float (&v)[N]) {
   if (o.dtype == PNB_F32) {
     float *p = static_cast<float *>(o.p) + at;
     if constexpr (N == 4) *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
@@ -1044,7 +1044,7 @@ cudaError_t run_attn(Kv4AttnArgs a, int grid, cudaStream_t st) {
   a.nrb = (a.rows + rows - 1) / rows;
   const int smem = AttnSmem<NG, PAIR, SPLIT>::bytes(a.n_slot);
   auto kern = a.scores ? k_kv4_attn<NG, PAIR, SPLIT, true> : k_kv4_attn<NG, PAIR, SPLIT, false>;
-  return kv4_launch(kern, dim3(grid), dim3(kKv4Threads), smem, 1, st, a);
+  return launch_pdl(kern, dim3(grid), dim3(kKv4Threads), smem, 1, st, a);
 }
 
 template <int NG>
@@ -1070,7 +1070,7 @@ cudaError_t run_weights(const Kv4WeightArgs &a, cudaStream_t st) {
   const int64_t most = (int64_t)kWeightCtasPerSm * a.sms;
   const int grid = (int)(units < most ? units : most);
   const int smem = (PARTS - 1) * (kWeightThreads / PARTS) * 16 + (a.n_slot + 1) * 4;
-  return kv4_launch(k_kv4_weights<PARTS>, dim3(grid), dim3(kWeightThreads), smem, 1, st, a);
+  return launch_pdl(k_kv4_weights<PARTS>, dim3(grid), dim3(kWeightThreads), smem, 1, st, a);
 }
 
 cudaError_t launch_kv4_weights(const Kv4WeightArgs &a, cudaStream_t st) {
