@@ -38,16 +38,6 @@ constexpr int kTThreads = 192;
 constexpr int kTile = 128;          // positions per tile
 constexpr int kBox = 128 * 128;     // bytes of one 128-row x 64-column bf16 box
 
-// byte offset of (row, byte column) in a [rows][128 B] tile with 128-byte swizzle
-__device__ __forceinline__ uint32_t sw128(int row, int col_bytes) {
-  return (uint32_t)row * 128u + ((((uint32_t)col_bytes >> 4) ^ ((uint32_t)row & 7u)) << 4) +
-         ((uint32_t)col_bytes & 15u);
-}
-
-__device__ __forceinline__ void fence_async_smem() {
-  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-}
-
 __device__ __forceinline__ void epi_sync_t() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 
 __device__ __forceinline__ void cl_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
@@ -98,19 +88,6 @@ __device__ __forceinline__ bool cl_mbar_wait(uint64_t *bar, uint32_t parity) {
 // [local head][split][hd + 4] floats (O, then max and sum).
 constexpr int kMaxSplit = 8;   // portable cluster size (16-CTA clusters measured slower)
 __host__ __device__ constexpr int merge_floats(int hd) { return 16 * (hd + 4); }
-
-// descriptor of an MN-major operand tile with 128-byte swizzle: 64-element
-// atoms along N lbo bytes apart, groups of 8 K-rows 1024 bytes apart
-__device__ __forceinline__ uint64_t desc_mn_sw128(const void *tile, uint32_t lbo) {
-  const uint32_t addr = smem_addr(tile);
-  uint64_t d = 0;
-  d |= (uint64_t)((addr >> 4) & 0x3FFFu);
-  d |= (uint64_t)((lbo >> 4) & 0x3FFFu) << 16;
-  d |= (uint64_t)(1024u >> 4) << 32;
-  d |= (uint64_t)1u << 46;
-  d |= (uint64_t)2u << 61;
-  return d;
-}
 
 // head_dim 128 computes O^T = V^T P^T (M = 128 dims, V as an MN-major A
 // operand, P a 16-row K-major B operand, O^T in 16 TMEM columns: one dim per

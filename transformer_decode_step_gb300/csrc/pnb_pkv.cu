@@ -31,11 +31,6 @@ __device__ __forceinline__ void load8(const T *p, int l, float (&f)[8]) {
   }
 }
 
-__device__ __forceinline__ uint32_t pack2(float a, float b) {
-  const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
-  return *reinterpret_cast<const uint32_t *>(&v);
-}
-
 template <int HD, bool NEOX, typename T>
 __device__ __forceinline__ void store8(T *p, int l, const float (&f)[8]) {
   T *a = NEOX ? p + 4 * l : p + 8 * l, *b = NEOX ? p + HD / 2 + 4 * l : p + 8 * l + 4;
@@ -43,11 +38,11 @@ __device__ __forceinline__ void store8(T *p, int l, const float (&f)[8]) {
     *reinterpret_cast<float4 *>(a) = make_float4(f[0], f[1], f[2], f[3]);
     *reinterpret_cast<float4 *>(b) = make_float4(f[4], f[5], f[6], f[7]);
   } else if constexpr (NEOX) {
-    *reinterpret_cast<uint2 *>(a) = make_uint2(pack2(f[0], f[1]), pack2(f[2], f[3]));
-    *reinterpret_cast<uint2 *>(b) = make_uint2(pack2(f[4], f[5]), pack2(f[6], f[7]));
+    *reinterpret_cast<uint2 *>(a) = make_uint2(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]));
+    *reinterpret_cast<uint2 *>(b) = make_uint2(pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
   } else {
     *reinterpret_cast<uint4 *>(a) =
-        make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7]));
+        make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
   }
 }
 

@@ -5,8 +5,10 @@
 // a tiled bulk copy brings them as they lie.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
+#include <limits.h>
 #include <stdint.h>
 
 #include "pnb.h"
@@ -43,6 +45,29 @@ struct PkvAppendArgs {
   int32_t sms;
 };
 
+// Rows (token, query head of a KV head's group) that share their K and V are
+// attended together: the tokens of one sequence, or, over a shared prefix, those
+// of all the sequences of a group.  A block is up to kPkvBlockRows such rows, an
+// item a block with its tiles of kPkvTile entries; the flat list of all items'
+// tiles (and kPkvItemUnits more per item, for its queries and its end) is cut into
+// equal runs, one per CTA.  What a run holds of an item that others share goes to
+// the run's partial sums, which a second kernel adds up in the list's order.
+constexpr int kPkvTile = 128;
+constexpr int kPkvBlockRows = 256;
+constexpr int kPkvItemUnits = 2;
+
+// what a CTA left of an item that others share
+struct PkvPart {
+  int32_t flags;      // 1: holds something, 2: the item ends here
+  int32_t b, j, h;    // sequence (or group), block, KV head
+};
+
+// the whole pages that a group shares, as far as every query of the group sees
+// them, and its sequences' shortest and longest length
+struct PkvGroup {
+  int32_t prefix, len_min, len_max, pad;
+};
+
 struct PkvAttnArgs {
   PkvPool pool;
   PkvSeqs seqs;
@@ -50,10 +75,19 @@ struct PkvAttnArgs {
   int32_t n_head, window;
   float qscale;                         // log2(e) / sqrt(head_dim)
   int32_t *err;
+  // groups of sequences with a common prefix (NULL: none)
+  const int32_t *group_start, *prefix;
+  int32_t n_group;
+  PkvGroup *groups;                     // [n_group] workspace
+  float *row_o, *row_ml;                // [n_tok][n_head][head_dim], [..][2]: the prefix's part of each row
+  float *part_o, *part_ml;              // [2 grid][kPkvBlockRows][head_dim], [..][2]
+  PkvPart *part;                        // [2 grid]
+  int32_t grid;
 };
 
+cudaError_t prepare_pkv_kernels(int hd);
 cudaError_t launch_pkv_append(int hd, bool neox, const PkvAppendArgs &a, cudaStream_t st);
-cudaError_t launch_pkv_attn(int hd, const PkvAttnArgs &a, cudaStream_t st);
+cudaError_t launch_pkv_rows(int hd, const CUtensorMap &map, const PkvAttnArgs &a, cudaStream_t st);
 
 // Tokens of sequence b: the first one and their number, kept inside the packed
 // rows whatever `start` holds.
@@ -99,6 +133,92 @@ __device__ __forceinline__ __nv_bfloat16 *pkv_row(const PkvPool &p, const int32_
   if (id < 0 || id >= p.n_page) return nullptr;
   const int64_t row = (((int64_t)id * 2 + kv) * p.n_kv + head) << p.page_log2;
   return p.base + (row + (e & ((1 << p.page_log2) - 1))) * HD;
+}
+
+// the group of sequence s, -1 when none holds it (group starts that decrease or
+// do not reach it)
+__device__ __forceinline__ int pkv_group_of(const int32_t *start, int n_group, int s) {
+  int lo = 0, hi = n_group;
+  while (hi - lo > 1) {
+    const int m = (lo + hi) >> 1;
+    if (start[m] <= s) lo = m;
+    else hi = m;
+  }
+  return start[lo] <= s && s < start[lo + 1] ? lo : -1;
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t *>(&v);
+}
+
+// 2^x by the hardware's approximation (2 ulp; subnormal results are 0)
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// N consecutive outputs o * f
+template <int N>
+__device__ __forceinline__ void pkv_store(const DevRows &out, int64_t at, const float *o, float f) {
+  if (out.dtype == PNB_F32) {
+    float *p = static_cast<float *>(out.p) + at;
+    if constexpr (N % 4 == 0) {
+#pragma unroll
+      for (int i = 0; i < N; i += 4)
+        *reinterpret_cast<float4 *>(p + i) = make_float4(o[i] * f, o[i + 1] * f, o[i + 2] * f, o[i + 3] * f);
+    } else {
+      *reinterpret_cast<float2 *>(p) = make_float2(o[0] * f, o[1] * f);
+    }
+  } else {
+    __nv_bfloat16 *p = static_cast<__nv_bfloat16 *>(out.p) + at;
+    if constexpr (N % 8 == 0) {
+#pragma unroll
+      for (int i = 0; i < N; i += 8)
+        *reinterpret_cast<uint4 *>(p + i) =
+            make_uint4(pack_bf16(o[i] * f, o[i + 1] * f), pack_bf16(o[i + 2] * f, o[i + 3] * f),
+                       pack_bf16(o[i + 4] * f, o[i + 5] * f), pack_bf16(o[i + 6] * f, o[i + 7] * f));
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; i += 2) *reinterpret_cast<uint32_t *>(p + i) = pack_bf16(o[i] * f, o[i + 1] * f);
+    }
+  }
+}
+
+// One row's sums over entries [from, to) by the calling warp, without matrix
+// instructions: lane l answers elements l * HD / 32 ...  A page that the table does
+// not name counts as zeros.
+template <int HD>
+__device__ __noinline__ void pkv_attend_row(const PkvPool &pool, const int32_t *pages, int h, const DevRows &q,
+                                            int64_t q_at, float scale, int from, int to, float (&o)[HD / 32], float &m,
+                                            float &sum) {
+  constexpr int N = HD / 32;
+  const int lane = threadIdx.x & 31;
+  float x[N];
+  if (q.dtype == PNB_F32) load_vals<float, N>(static_cast<const float *>(q.p) + q_at + lane * N, x);
+  else load_vals<__nv_bfloat16, N>(static_cast<const __nv_bfloat16 *>(q.p) + q_at + lane * N, x);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    x[i] *= scale;
+    o[i] = 0.f;
+  }
+  m = -INFINITY;
+  sum = 0.f;
+  for (int e = from; e < to; ++e) {
+    const __nv_bfloat16 *k = pkv_row<HD>(pool, pages, e, 0, h);
+    float y[N] = {}, s = 0.f;
+    if (k) load_vals<__nv_bfloat16, N>(k + lane * N, y);
+#pragma unroll
+    for (int i = 0; i < N; ++i) s += x[i] * y[i];
+    s = warp_sum(s);
+    const float top = fmaxf(m, s), ref = top == -INFINITY ? 0.f : top, f = exp2f(m - ref), p = exp2f(s - ref);
+    if (k) load_vals<__nv_bfloat16, N>(k + ((int64_t)pool.n_kv << pool.page_log2) * HD + lane * N, y);
+#pragma unroll
+    for (int i = 0; i < N; ++i) o[i] = o[i] * f + p * y[i];
+    sum = sum * f + p;
+    m = top;
+  }
 }
 
 }  // namespace pnb

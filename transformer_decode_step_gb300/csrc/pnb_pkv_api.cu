@@ -3,9 +3,11 @@
 
 #include <cmath>
 #include <new>
+#include <vector>
 
 #include "pnb.h"
 #include "pnb_pkv.cuh"
+#include "pnb_tmap.cuh"
 
 using namespace pnb;
 
@@ -17,6 +19,10 @@ struct pnb_pkv {
   uint8_t *ws = nullptr;
   unsigned long long *freq = nullptr;
   int32_t *err = nullptr;
+  PkvGroup *groups = nullptr;
+  PkvPart *part = nullptr;
+  float *part_o = nullptr, *part_ml = nullptr, *row_o = nullptr, *row_ml = nullptr;
+  std::vector<CUtensorMap> maps;   // one per layer
 };
 
 namespace {
@@ -112,7 +118,13 @@ int attend(pnb_pkv *c, int32_t layer, const pnb_pkv_batch *b, int32_t n_tok, con
   a.window = window;
   a.qscale = (float)(1.4426950408889634 / std::sqrt((double)g.head_dim));
   a.err = c->err;
-  return launch_pkv_attn(g.head_dim, a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? PNB_OK : PNB_E_CUDA;
+  a.part = c->part;
+  a.part_o = c->part_o;
+  a.part_ml = c->part_ml;
+  a.grid = c->sms;
+  return launch_pkv_rows(g.head_dim, c->maps[layer], a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? PNB_OK
+             : PNB_E_CUDA;
 }
 
 }  // namespace
@@ -150,11 +162,28 @@ int pnb_pkv_new(const pnb_pkv_config *cfg, void *pool_dev, size_t bytes, pnb_pkv
     at += align256(n);
     return o;
   };
-  const size_t o_err = take(4), o_freq = take(sizeof(freq));
   cudaError_t e = cudaGetDevice(&k->device);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&k->sms, cudaDevAttrMultiProcessorCount, k->device);
+  if (e == cudaSuccess) e = prepare_pkv_kernels(c.head_dim);
+  bool maps = e == cudaSuccess;
+  try {
+    if (maps) k->maps.resize(c.n_layer);
+  } catch (...) {
+    delete k;
+    return PNB_E_NOMEM;
+  }
+  for (int l = 0; l < c.n_layer && maps; ++l)
+    maps = encode_map(&k->maps[l], k->pool + (size_t)l * k->layer_bytes, (int64_t)c.n_page * 2 * c.n_kv_head * c.page,
+                      c.head_dim, c.page);
+  if (e == cudaSuccess && !maps) e = cudaErrorUnknown;
+  const size_t part_rows = (size_t)2 * k->sms * kPkvBlockRows, rows = (size_t)c.shared_tok * c.n_head;
+  const size_t o_err = take(4), o_freq = take(sizeof(freq)), o_part = take(2 * (size_t)k->sms * sizeof(PkvPart));
+  const size_t zeroed = at;
+  const size_t o_groups = take(kPkvMaxSeq * sizeof(PkvGroup));
+  const size_t o_pml = take(part_rows * 8), o_po = take(part_rows * c.head_dim * 4);
+  const size_t o_rml = take(rows * 8), o_ro = take(rows * c.head_dim * 4);
   if (e == cudaSuccess) e = cudaMalloc(&k->ws, at);
-  if (e == cudaSuccess) e = clear_now(k->ws, at);
+  if (e == cudaSuccess) e = clear_now(k->ws, zeroed);
   if (e == cudaSuccess) e = cudaMemcpy(k->ws + o_freq, freq, sizeof(freq), cudaMemcpyHostToDevice);
   if (e != cudaSuccess) {
     cudaGetLastError();
@@ -164,6 +193,12 @@ int pnb_pkv_new(const pnb_pkv_config *cfg, void *pool_dev, size_t bytes, pnb_pkv
   }
   k->err = reinterpret_cast<int32_t *>(k->ws + o_err);
   k->freq = reinterpret_cast<unsigned long long *>(k->ws + o_freq);
+  k->groups = reinterpret_cast<PkvGroup *>(k->ws + o_groups);
+  k->part = reinterpret_cast<PkvPart *>(k->ws + o_part);
+  k->part_ml = reinterpret_cast<float *>(k->ws + o_pml);
+  k->part_o = reinterpret_cast<float *>(k->ws + o_po);
+  k->row_ml = reinterpret_cast<float *>(k->ws + o_rml);
+  k->row_o = reinterpret_cast<float *>(k->ws + o_ro);
   *out = k;
   return PNB_OK;
 }
