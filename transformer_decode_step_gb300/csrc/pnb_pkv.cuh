@@ -52,6 +52,10 @@ struct PkvAppendArgs {
 // tiles (and kPkvItemUnits more per item, for its queries and its end) is cut into
 // equal runs, one per CTA.  What a run holds of an item that others share goes to
 // the run's partial sums, which a second kernel adds up in the list's order.
+constexpr int kPkvBoxLog2 = 6;          // rows of a TMA box: a page's, at most 64
+// what a kernel attends to: everything, the groups' prefixes (unfinished rows into
+// row_o, row_ml), or what lies behind them, adding the prefix's part
+enum { kPkvAll = 0, kPkvPrefix = 1, kPkvOwn = 2 };
 constexpr int kPkvTile = 128;
 constexpr int kPkvBlockRows = 256;
 constexpr int kPkvItemUnits = 2;
@@ -75,7 +79,8 @@ struct PkvAttnArgs {
   int32_t n_head, window;
   float qscale;                         // log2(e) / sqrt(head_dim)
   int32_t *err;
-  // groups of sequences with a common prefix (NULL: none)
+  int32_t pass;                         // kPkvAll, kPkvPrefix, kPkvOwn
+  // groups of sequences with a common prefix
   const int32_t *group_start, *prefix;
   int32_t n_group;
   PkvGroup *groups;                     // [n_group] workspace
@@ -85,9 +90,13 @@ struct PkvAttnArgs {
   int32_t grid;
 };
 
-cudaError_t prepare_pkv_kernels(int hd);
+cudaError_t prepare_pkv_rows(int hd);
+cudaError_t prepare_pkv_step(int hd);
 cudaError_t launch_pkv_append(int hd, bool neox, const PkvAppendArgs &a, cudaStream_t st);
 cudaError_t launch_pkv_rows(int hd, const CUtensorMap &map, const PkvAttnArgs &a, cudaStream_t st);
+cudaError_t launch_pkv_step(int hd, const CUtensorMap &map, const PkvAttnArgs &a, cudaStream_t st);
+// adds up the parts that the CTAs of either left, up to `rows` rows per item
+cudaError_t launch_pkv_join(int hd, const PkvAttnArgs &a, int rows, cudaStream_t st);
 
 // Tokens of sequence b: the first one and their number, kept inside the packed
 // rows whatever `start` holds.
@@ -219,6 +228,27 @@ __device__ __noinline__ void pkv_attend_row(const PkvPool &pool, const int32_t *
     sum = sum * f + p;
     m = top;
   }
+}
+
+// what brings sums with references m and m2 to a common one
+__device__ __forceinline__ void pkv_join_factors(float m, float m2, float &f, float &f2) {
+  const float top = fmaxf(m, m2);
+  f = m == -INFINITY ? 0.f : exp2f(m - top);
+  f2 = m2 == -INFINITY ? 0.f : exp2f(m2 - top);
+}
+
+// Adds the prefix's part of a row to lane l's outputs l * N .. and its sum.
+template <int N>
+__device__ __forceinline__ void pkv_add_prefix(const PkvAttnArgs &a, int tok, int head, float *o, float &m, float &sum) {
+  const int64_t at = (int64_t)tok * a.n_head + head;
+  const float2 ml = *reinterpret_cast<const float2 *>(a.row_ml + at * 2);
+  float f, f2, x[N];
+  pkv_join_factors(m, ml.x, f, f2);
+  load_vals<float, N>(a.row_o + at * 32 * N + (threadIdx.x & 31) * N, x);
+#pragma unroll
+  for (int i = 0; i < N; ++i) o[i] = o[i] * f + x[i] * f2;
+  sum = sum * f + ml.y * f2;
+  m = fmaxf(m, ml.x);
 }
 
 }  // namespace pnb

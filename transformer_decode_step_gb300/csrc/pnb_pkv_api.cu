@@ -101,8 +101,13 @@ int check_tokens(const pnb_pkv *c, const pnb_rows *r, int n_tok, int heads, bool
   return off_pool(c, *out, n_tok, heads) ? PNB_OK : PNB_E_INVAL;
 }
 
-int attend(pnb_pkv *c, int32_t layer, const pnb_pkv_batch *b, int32_t n_tok, const pnb_rows *q, const pnb_rows *out,
-           int32_t window, pnb_stream stream) {
+// Up to this many rows (tokens x query heads of a KV head) of every sequence go
+// through the kernel for steps.
+constexpr int kStepRows = 16;
+
+int attend(pnb_pkv *c, int32_t layer, const pnb_pkv_batch *b, int32_t n_group, const int32_t *group_start,
+           const int32_t *prefix, int32_t n_tok, const pnb_rows *q, const pnb_rows *out, int32_t window,
+           pnb_stream stream) {
   const pnb_pkv_config &g = c->cfg;
   if (window < 0) return PNB_E_INVAL;
   PkvAttnArgs a{};
@@ -113,6 +118,7 @@ int attend(pnb_pkv *c, int32_t layer, const pnb_pkv_batch *b, int32_t n_tok, con
   if (!apart(a.out, a.q, n_tok, 1, g.n_head, g.head_dim, true)) return PNB_E_INVAL;
   rc = check_call(c, layer);
   if (rc != PNB_OK) return rc;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   a.pool = pool_of(c, layer);
   a.n_head = g.n_head;
   a.window = window;
@@ -122,9 +128,22 @@ int attend(pnb_pkv *c, int32_t layer, const pnb_pkv_batch *b, int32_t n_tok, con
   a.part_o = c->part_o;
   a.part_ml = c->part_ml;
   a.grid = c->sms;
-  return launch_pkv_rows(g.head_dim, c->maps[layer], a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
-             ? PNB_OK
-             : PNB_E_CUDA;
+  a.pass = kPkvAll;
+  const CUtensorMap &map = c->maps[layer];
+  if (group_start) {
+    a.group_start = group_start;
+    a.prefix = prefix;
+    a.n_group = n_group;
+    a.groups = c->groups;
+    a.row_o = c->row_o;
+    a.row_ml = c->row_ml;
+    a.pass = kPkvPrefix;
+    if (launch_pkv_rows(g.head_dim, map, a, st) != cudaSuccess) return PNB_E_CUDA;
+    a.pass = kPkvOwn;
+  }
+  const bool step = a.seqs.each > 0 && (int64_t)a.seqs.each * (g.n_head / g.n_kv_head) <= kStepRows;
+  const cudaError_t e = step ? launch_pkv_step(g.head_dim, map, a, st) : launch_pkv_rows(g.head_dim, map, a, st);
+  return e == cudaSuccess ? PNB_OK : PNB_E_CUDA;
 }
 
 }  // namespace
@@ -164,7 +183,8 @@ int pnb_pkv_new(const pnb_pkv_config *cfg, void *pool_dev, size_t bytes, pnb_pkv
   };
   cudaError_t e = cudaGetDevice(&k->device);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&k->sms, cudaDevAttrMultiProcessorCount, k->device);
-  if (e == cudaSuccess) e = prepare_pkv_kernels(c.head_dim);
+  if (e == cudaSuccess) e = prepare_pkv_rows(c.head_dim);
+  if (e == cudaSuccess) e = prepare_pkv_step(c.head_dim);
   bool maps = e == cudaSuccess;
   try {
     if (maps) k->maps.resize(c.n_layer);
@@ -174,7 +194,7 @@ int pnb_pkv_new(const pnb_pkv_config *cfg, void *pool_dev, size_t bytes, pnb_pkv
   }
   for (int l = 0; l < c.n_layer && maps; ++l)
     maps = encode_map(&k->maps[l], k->pool + (size_t)l * k->layer_bytes, (int64_t)c.n_page * 2 * c.n_kv_head * c.page,
-                      c.head_dim, c.page);
+                      c.head_dim, c.page < 1 << kPkvBoxLog2 ? c.page : 1 << kPkvBoxLog2);
   if (e == cudaSuccess && !maps) e = cudaErrorUnknown;
   const size_t part_rows = (size_t)2 * k->sms * kPkvBlockRows, rows = (size_t)c.shared_tok * c.n_head;
   const size_t o_err = take(4), o_freq = take(sizeof(freq)), o_part = take(2 * (size_t)k->sms * sizeof(PkvPart));
@@ -249,7 +269,7 @@ int pnb_pkv_append(pnb_pkv *c, int32_t layer, const pnb_pkv_batch *b, int32_t n_
 int pnb_pkv_attention(pnb_pkv *c, int32_t layer, const pnb_pkv_batch *b, int32_t n_tok, const pnb_rows *q,
                       const pnb_rows *out, int32_t window, pnb_stream stream) {
   if (!c || !b || !q || !out) return PNB_E_NULL;
-  return attend(c, layer, b, n_tok, q, out, window, stream);
+  return attend(c, layer, b, 0, nullptr, nullptr, n_tok, q, out, window, stream);
 }
 
 int pnb_pkv_attention_shared(pnb_pkv *c, int32_t layer, const pnb_pkv_batch *b, int32_t n_group,
@@ -258,7 +278,7 @@ int pnb_pkv_attention_shared(pnb_pkv *c, int32_t layer, const pnb_pkv_batch *b, 
   if (!c || !b || !group_start_dev || !prefix_dev || !q || !out) return PNB_E_NULL;
   if (!aligned4(group_start_dev) || !aligned4(prefix_dev)) return PNB_E_ALIGN;
   if (n_group < 1 || n_group > b->n_seq || b->start_dev || n_tok > c->cfg.shared_tok) return PNB_E_INVAL;
-  return attend(c, layer, b, n_tok, q, out, window, stream);
+  return attend(c, layer, b, n_group, group_start_dev, prefix_dev, n_tok, q, out, window, stream);
 }
 
 int pnb_pkv_check(pnb_pkv *c, int32_t *device_error) {

@@ -24,7 +24,7 @@
 #include <cuda_bf16.h>
 #include <math.h>
 
-#include "pnb_pkv.cuh"
+#include "pnb_pkv_sched.cuh"
 #include "pnb_tc.cuh"
 
 namespace pnb {
@@ -51,219 +51,11 @@ struct RL {
   static constexpr int SMEM = 1024 + 2 * QHALF + NU * UNIT + 1024;
 };
 
-struct RItem {
-  int b, j, h;              // sequence or group, block, KV head
-  int tok0, ntok;           // its tokens
-  int base;                 // first token's last entry (prompts)
-  int hi, lo;               // entries [lo, hi): those that some row sees
-  int hi_min, lo_max;       // entries [lo_max, hi_min): those that every row sees
-  int t0, nt;               // tiles of the whole item
-  int ta, tb;               // this CTA's tiles
-  bool ends;                // the item's end is this CTA's
-};
-
-// the j-th block of a sequence or group; false behind the last one
-__device__ __forceinline__ bool block_of(const PkvAttnArgs &a, int TB, int b, int j, RItem &it) {
-  int t0, n;
-  if (a.groups) {
-    const int gs = min(max(a.group_start[b], 0), a.seqs.n_seq), ge = min(max(a.group_start[b + 1], gs), a.seqs.n_seq);
-    t0 = gs * a.seqs.each;
-    n = (ge - gs) * a.seqs.each;
-  } else {
-    pkv_tokens(a.seqs, b, t0, n);
-  }
-  if (j * TB >= n) return false;
-  it.b = b;
-  it.j = j;
-  it.tok0 = t0 + j * TB;
-  it.ntok = min(TB, n - j * TB);
-  const int W = a.window;
-  if (a.groups) {
-    const PkvGroup g = a.groups[b];
-    it.base = 0;
-    it.hi = it.hi_min = g.prefix;
-    it.lo = W > 0 ? min(max(0, g.len_min - a.seqs.each - W + 1), g.prefix) : 0;
-    it.lo_max = W > 0 ? max(0, g.len_max - W) : 0;
-  } else {
-    it.base = pkv_len(a.seqs, a.pool.page_log2, b, a.err) - n + j * TB;
-    it.hi = max(0, it.base + it.ntok);
-    it.hi_min = it.base + 1;
-    it.lo = W > 0 ? max(0, it.base - W + 1) : 0;
-    it.lo_max = W > 0 ? max(0, it.base + it.ntok - W) : 0;
-  }
-  it.t0 = it.lo / kPkvTile;
-  it.nt = max(1, (it.hi + kPkvTile - 1) / kPkvTile - it.t0);
-  return true;
-}
-
-// a CTA's way through its run of units
-struct RWalk {
-  int h, b, j, x;       // next item, units of it that lie before the run
-  int64_t left;         // units
-  int n_b;              // sequences or groups
-
-  __device__ __forceinline__ bool next(const PkvAttnArgs &a, int TB, RItem &it) {
-    while (left > 0 && h < a.pool.n_kv) {
-      if (!block_of(a, TB, b, j, it)) {
-        j = 0;
-        if (++b == n_b) {
-          b = 0;
-          ++h;
-        }
-        continue;
-      }
-      const int units = it.nt + kPkvItemUnits;
-      const int end = (int)min((int64_t)units, x + left);
-      it.h = h;
-      it.ta = max(0, x - kPkvItemUnits);
-      it.tb = max(0, end - kPkvItemUnits);
-      it.ends = end == units;
-      left -= end - x;
-      x = end;
-      if (it.ends) {
-        ++j;
-        x = 0;
-      }
-      if (it.tb > it.ta) return true;
-    }
-    return false;
-  }
-};
-
-// The shared prefix of every group as all of its queries see it.  Every CTA writes
-// the same numbers, so each finds its own.
-__device__ void find_groups(const PkvAttnArgs &a, int *scratch) {
-  int *gmin = scratch, *gmax = scratch + a.n_group;
-  for (int g = threadIdx.x; g < a.n_group; g += kThreads) {
-    gmin[g] = INT_MAX;
-    gmax[g] = 0;
-  }
-  __syncthreads();
-  for (int s = threadIdx.x; s < a.seqs.n_seq; s += kThreads) {
-    const int g = pkv_group_of(a.group_start, a.n_group, s);
-    if (g < 0) {
-      set_error(a.err, kErrRange);
-      continue;
-    }
-    const int n = pkv_len(a.seqs, a.pool.page_log2, s, a.err);
-    atomicMin(&gmin[g], n);
-    atomicMax(&gmax[g], n);
-  }
-  __syncthreads();
-  for (int g = threadIdx.x; g < a.n_group; g += kThreads) {
-    const int p = min(max(a.prefix[g], 0), max(0, gmin[g] - a.seqs.each));
-    a.groups[g] = PkvGroup{p >> a.pool.page_log2 << a.pool.page_log2, gmin[g], gmax[g], 0};
-  }
-  __syncthreads();
-}
-
-// Where this CTA's run starts.  The blocks of one KV head are counted and their
-// units added up by all threads; heads follow one another in the list.
-__device__ void find_run(const PkvAttnArgs &a, int TB, int *scratch, RWalk *out) {
-  const int n_b = a.groups ? a.n_group : a.seqs.n_seq, tid = threadIdx.x, lane = tid & 31;
-  int *first = scratch;                                             // [n_b + 1] blocks before a sequence
-  long long *sums = reinterpret_cast<long long *>(scratch + 1026);   // [kThreads + 1]
-  for (int b = tid; b < n_b; b += kThreads) {
-    int t0, n;
-    if (a.groups) {
-      const int gs = min(max(a.group_start[b], 0), a.seqs.n_seq);
-      n = (min(max(a.group_start[b + 1], gs), a.seqs.n_seq) - gs) * a.seqs.each;
-    } else {
-      pkv_tokens(a.seqs, b, t0, n);
-    }
-    first[b + 1] = (n + TB - 1) / TB;
-  }
-  if (tid == 0) first[0] = 0;
-  __syncthreads();
-  if (tid < 32) {
-    int base = 0;
-    for (int b0 = 1; b0 <= n_b; b0 += 32) {
-      int v = b0 + lane <= n_b ? first[b0 + lane] : 0;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int u = __shfl_up_sync(0xffffffffu, v, o);
-        if (lane >= o) v += u;
-      }
-      if (b0 + lane <= n_b) first[b0 + lane] = base + v;
-      base += __shfl_sync(0xffffffffu, v, 31);
-    }
-  }
-  __syncthreads();
-  const int blocks = first[n_b];
-  const int i0 = (int)((int64_t)blocks * tid / kThreads), i1 = (int)((int64_t)blocks * (tid + 1) / kThreads);
-  // the sequence of block i0: the last one that starts at or before it
-  int b0 = 0;
-  if (i0 < i1) {
-    int lo = 0, hi = n_b;   // first[lo] <= i0 < first[hi]
-    while (hi - lo > 1) {
-      const int m = (lo + hi) >> 1;
-      if (first[m] <= i0) lo = m;
-      else hi = m;
-    }
-    b0 = lo;
-  }
-  auto walk = [&](auto &&f) {
-    int b = b0, j = i0 - first[b0];
-    for (int i = i0; i < i1; ++i) {
-      RItem it;
-      while (!block_of(a, TB, b, j, it)) {
-        ++b;
-        j = 0;
-      }
-      if (!f(b, j, it.nt + kPkvItemUnits)) return;
-      ++j;
-    }
-  };
-  long long mine = 0;
-  walk([&](int, int, int u) {
-    mine += u;
-    return true;
-  });
-  sums[tid + 1] = mine;
-  if (tid == 0) sums[0] = 0;
-  __syncthreads();
-  if (tid < 32) {
-    long long base = 0;
-    for (int k0 = 1; k0 <= kThreads; k0 += 32) {
-      long long v = sums[k0 + lane];
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long u = __shfl_up_sync(0xffffffffu, v, o);
-        if (lane >= o) v += u;
-      }
-      sums[k0 + lane] = base + v;
-      base += __shfl_sync(0xffffffffu, v, 31);
-    }
-  }
-  __syncthreads();
-  const long long per_head = sums[kThreads], total = per_head * a.pool.n_kv;
-  const int ctas = gridDim.x;
-  const long long u0 = total * blockIdx.x / ctas, u1 = total * (blockIdx.x + 1) / ctas;
-  if (u1 <= u0) {
-    if (tid == 0) *out = RWalk{0, 0, 0, 0, 0, n_b};
-  } else {
-    const int h = (int)(u0 / per_head);
-    const long long in_head = u0 - h * per_head;
-    if (in_head >= sums[tid] && in_head < sums[tid + 1]) {
-      long long at = sums[tid];
-      walk([&](int b, int j, int u) {
-        if (in_head >= at + u) {
-          at += u;
-          return true;
-        }
-        *out = RWalk{h, b, j, (int)(in_head - at), u1 - u0, n_b};
-        return false;
-      });
-    }
-  }
-  __syncthreads();
-}
-
 struct RBars {
   uint64_t full[16], empty[16], q_ready[2], s_full[2], p_ready[2], o_full[2], v_go, v_ok, drain;
   uint32_t tmem, pad;
   int bad[kBadSlots];
-  RWalk walk;
+  PkvWalk walk;
 };
 static_assert(sizeof(RBars) <= 1024, "barriers");
 
@@ -317,7 +109,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&bar.drain, 1);
     for (int i = 0; i < kBadSlots; ++i) bar.bad[i] = 0;
     fence_barrier_init();
-    bar.walk = RWalk{0, 0, 0, 0, 0, 1};
+    bar.walk = PkvWalk{0, 0, 0, 0, 0, 1};
   }
   if (warp == 9) {
     tmem_alloc(&bar.tmem, 512);
@@ -329,10 +121,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_wait();
   pdl_trigger();
   if (threadIdx.x < 2) a.part[2 * blockIdx.x + threadIdx.x].flags = 0;
-  if (a.groups) find_groups(a, reinterpret_cast<int *>(ring));
-  find_run(a, TB, reinterpret_cast<int *>(ring), &bar.walk);
-  RWalk walk = bar.walk;
-  RItem it;
+  if (a.pass == kPkvPrefix) pkv_find_groups<kThreads>(a, reinterpret_cast<int *>(ring));
+  pkv_find_run<kPkvTile, kThreads>(a, TB, reinterpret_cast<int *>(ring), &bar.walk);
+  PkvWalk walk = bar.walk;
+  PkvItem it;
   const uint32_t tmem = bar.tmem;
   const uint32_t t_s[2] = {tmem, tmem + 128}, t_o[2] = {tmem + 256, tmem + 384};
   // the ring held the schedule's sums: order them before the tiles that TMA writes
@@ -345,20 +137,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ------------------------------------------------------ K and V tiles
       bool ok = true;
       uint32_t u = 0;   // units issued
-      const int log2p = a.pool.page_log2, per_tile = kPkvTile >> log2p, page = 1 << log2p;
+      // a lane per copied box: a page's rows, at most 64 of them
+      const int log2p = a.pool.page_log2, log2b = min(log2p, kPkvBoxLog2), per_tile = kPkvTile >> log2b, box = 1 << log2b;
       const int rows_total = a.pool.n_page * 2 * a.pool.n_kv << log2p;
-      while (ok && walk.next(a, TB, it)) {
+      while (ok && walk.next<kPkvTile>(a, TB, it)) {
         // page ids are the first sequence's of a group
-        const int seq = a.groups ? min(max(a.group_start[it.b], 0), a.seqs.n_seq - 1) : it.b;
+        const int seq = a.pass == kPkvPrefix ? min(max(a.group_start[it.b], 0), a.seqs.n_seq - 1) : it.b;
         const int32_t *pages = a.seqs.pages + (int64_t)seq * a.seqs.max_page;
         auto page_id = [&](int t) {
-          const int e = (it.t0 + t) * kPkvTile + (lane << log2p);
-          return lane < per_tile && e < it.hi && e + page > it.lo ? pages[e >> log2p] : -1;
+          const int e = (it.t0 + t) * kPkvTile + (lane << log2b);
+          return lane < per_tile && e < it.hi && e + box > it.lo ? pages[e >> log2p] : -1;
         };
         int id = page_id(it.ta);
         for (int t = it.ta; t < it.tb && ok; ++t) {
-          const int e = (it.t0 + t) * kPkvTile + (lane << log2p);
-          const bool needed = lane < per_tile && e < it.hi && e + page > it.lo;
+          const int e = (it.t0 + t) * kPkvTile + (lane << log2b);
+          const bool needed = lane < per_tile && e < it.hi && e + box > it.lo;
           const bool good = id >= 0 && id < a.pool.n_page;
           if (needed && !good) set_error(a.err, kErrRange);
           const int now = id;
@@ -373,8 +166,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (lane < per_tile) {
               // rows behind the pool's end read as zero
-              const int y = needed && good ? ((now * 2 + kv) * a.pool.n_kv + it.h) << log2p : rows_total;
-              uint8_t *dst = ring + s * L::UNIT + (lane << log2p) * 128;
+              const int y = needed && good
+                                ? (((now * 2 + kv) * a.pool.n_kv + it.h) << log2p) + (e & ((1 << log2p) - 1))
+                                : rows_total;
+              uint8_t *dst = ring + s * L::UNIT + (lane << log2b) * 128;
 #pragma unroll
               for (int c = 0; c < L::NB; ++c) tma_load_2d(dst + c * L::BOX, &kvmap, c * 64, y, &bar.full[s]);
             }
@@ -414,7 +209,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               mma_bf16_ts(t_o[w], t_s[w] + part * 64 + x * 8, desc_mn_sw128(v + x * 2048, L::BOX), idesc_o,
                           !first || part > 0 || x > 0);
         };
-        while (ok && walk.next(a, TB, it)) {
+        while (ok && walk.next<kPkvTile>(a, TB, it)) {
           const int halves = it.ntok * G > 128 ? 2 : 1;
           for (int w = 0; w < halves && ok; ++w) {
             ok = mbar_wait(&bar.q_ready[w], nq[w]++ & 1) && (w || mbar_wait(&bar.full[u % NU], (u / NU) & 1));
@@ -463,7 +258,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int tid = threadIdx.x - 320;
       bool ok = true;
       uint32_t u = 0, item = 0, nv = 0;
-      while (ok && walk.next(a, TB, it)) {
+      while (ok && walk.next<kPkvTile>(a, TB, it)) {
         for (int t = it.ta; t < it.tb && ok; ++t, u += 2) {
           const int e0 = (it.t0 + t) * kPkvTile;
           if (e0 >= it.lo_max && e0 + kPkvTile <= it.hi_min) continue;
@@ -507,7 +302,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
 
     // the warp's 32 query rows of an item into shared memory
-    auto load_q = [&](const RItem &x) {
+    auto load_q = [&](const PkvItem &x) {
       constexpr int LPR = HD / 8, RPW = 32 / LPR;   // lanes per row, rows at a time
       const int l = lane % LPR, sub = lane / LPR;
       uint8_t *q = Q + w * L::QHALF;
@@ -528,8 +323,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive(&bar.q_ready[w]);
     };
     // the next item with rows for this half
-    auto next = [&](RItem &x) {
-      while (walk.next(a, TB, x)) {
+    auto next = [&](PkvItem &x) {
+      while (walk.next<kPkvTile>(a, TB, x)) {
         ++item;
         if (x.ntok * G > 128 * w) return true;
       }
@@ -542,7 +337,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool live = r < it.ntok * G;
       const int tok = it.tok0 + (live ? r / G : 0), head = it.h * G + (live ? r % G : 0);
       int lo = it.lo, hi = it.hi;
-      if (a.groups) {
+      if (a.pass == kPkvPrefix) {
         if (a.window > 0) {
           const int seq = tok / a.seqs.each;
           const int last = pkv_len(a.seqs, a.pool.page_log2, seq, a.err) - a.seqs.each + tok % a.seqs.each;
@@ -551,7 +346,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       } else {
         const int last = it.base + (tok - it.tok0);
         hi = last + 1;
-        if (a.window > 0) lo = max(0, last - a.window + 1);
+        lo = max(it.floor, a.window > 0 ? last - a.window + 1 : 0);
       }
       float m = -INFINITY, sum = 0.f;
       for (int t = it.ta; t < it.tb; ++t) {
@@ -638,7 +433,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       // the next item's queries go where this one's lay: its last S is done
       const uint32_t id = item;
-      RItem nx;
+      PkvItem nx;
       have = next(nx);
       if (have) load_q(nx);
 
@@ -651,14 +446,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool redo = *reinterpret_cast<volatile int *>(&bar.bad[(id - 1) % kBadSlots]) == (int)id;
       const bool whole = it.ta == 0 && it.ends;
       const int side = it.ta > 0 ? 0 : 1;   // of the run's two partial sums
-      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+      // the prefix's part of the row
+      float f_own = 1.f, f_pre = 0.f, all = sum;
+      const float *bo = nullptr;
+      if (whole && it.floor > 0) {
+        const int64_t at = (int64_t)tok * a.n_head + head;
+        const float2 ml = *reinterpret_cast<const float2 *>(a.row_ml + at * 2);
+        bo = a.row_o + at * HD;
+        pkv_join_factors(m, ml.x, f_own, f_pre);
+        all = sum * f_own + ml.y * f_pre;
+      }
+      const float inv = all == 0.f ? 0.f : 1.f / all;
       float *po = nullptr, *pml = nullptr;
       if (!whole) {
         const int64_t at = (int64_t)(2 * blockIdx.x + side) * kPkvBlockRows + r;
         po = a.part_o + at * HD;
         pml = a.part_ml + at * 2;
         if (r == 0) a.part[2 * blockIdx.x + side] = PkvPart{it.ends ? 3 : 1, it.b, it.j, it.h};
-      } else if (a.groups) {
+      } else if (a.pass == kPkvPrefix) {
         const int64_t at = (int64_t)tok * a.n_head + head;
         po = a.row_o + at * HD;
         pml = a.row_ml + at * 2;
@@ -676,6 +481,16 @@ __global__ void __launch_bounds__(kThreads, 1)
               *reinterpret_cast<float4 *>(po + i + k) = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
           } else if (live) {
             // a row that saw nothing has only zeros summed up
+            if (it.floor > 0) {
+#pragma unroll
+              for (int k = 0; k < 32; k += 4) {
+                const float4 x = *reinterpret_cast<const float4 *>(bo + i + k);
+                o[k] = o[k] * f_own + x.x * f_pre;
+                o[k + 1] = o[k + 1] * f_own + x.y * f_pre;
+                o[k + 2] = o[k + 2] * f_own + x.z * f_pre;
+                o[k + 3] = o[k + 3] * f_own + x.w * f_pre;
+              }
+            }
             pkv_store<32>(a.out, tok * a.out.token + head * a.out.head + i, o, inv);
           }
           __syncwarp();
@@ -683,7 +498,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (live && po) *reinterpret_cast<float2 *>(pml) = make_float2(m, sum);
       } else {
         // a NaN or an infinity among values that only some rows see: each row by itself
-        const int seq = a.groups ? min(max(a.group_start[it.b], 0), a.seqs.n_seq - 1) : it.b;
+        const int seq = a.pass == kPkvPrefix ? min(max(a.group_start[it.b], 0), a.seqs.n_seq - 1) : it.b;
         for (int k = 0; k < 32; ++k) {
           const int from = max(__shfl_sync(0xffffffffu, lo, k), (it.t0 + it.ta) * kPkvTile);
           const int to_e = min(__shfl_sync(0xffffffffu, hi, k), (it.t0 + it.tb) * kPkvTile);
@@ -700,7 +515,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; i < HD / 32; ++i) dst[lane * (HD / 32) + i] = o[i];
             if (lane == 0) *reinterpret_cast<float2 *>((uintptr_t)pml_k) = make_float2(mk, lk);
           } else {
-            const float d = to_e > from ? 1.f / lk : 0.f;
+            if (it.floor > 0) pkv_add_prefix<HD / 32>(a, tk, hd_k, o, mk, lk);
+            const float d = lk == 0.f ? 0.f : 1.f / lk;
             pkv_store<HD / 32>(a.out, tk * a.out.token + hd_k * a.out.head + lane * (HD / 32), o, d);
           }
         }
@@ -728,8 +544,8 @@ __global__ void __launch_bounds__(256) k_pkv_join(const PkvAttnArgs a) {
   const PkvPart p = a.part[2 * c0 + 1];
   if (!(p.flags & 1)) return;
   const int G = a.n_head / a.pool.n_kv, TB = kPkvBlockRows / G;
-  RItem it;
-  if (!block_of(a, TB, p.b, p.j, it)) return;
+  PkvItem it;
+  if (!pkv_block<kPkvTile>(a, TB, p.b, p.j, it)) return;
   int last = c0;   // the run that ends the item
   if (!(p.flags & 2))
     for (last = c0 + 1; last < a.grid - 1 && !(a.part[2 * last].flags & 2);) ++last;
@@ -756,7 +572,8 @@ __global__ void __launch_bounds__(256) k_pkv_join(const PkvAttnArgs a) {
       sum += f * ml.y;
     }
     const int tok = it.tok0 + r / G, head = p.h * G + r % G;
-    if (a.groups) {
+    if (it.floor > 0) pkv_add_prefix<N>(a, tok, head, o, m, sum);
+    if (a.pass == kPkvPrefix) {
       const int64_t at = (int64_t)tok * a.n_head + head;
 #pragma unroll
       for (int i = 0; i < N; ++i) a.row_o[at * HD + lane * N + i] = o[i];
@@ -779,9 +596,7 @@ cudaError_t launch_rows(const CUtensorMap &map, const PkvAttnArgs &a, cudaStream
   cfg.stream = st;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, k_pkv_rows<HD, SPLIT>, map, a);
-  if (e != cudaSuccess) return e;
-  return launch_pdl(k_pkv_join<HD>, dim3(a.grid, 8), dim3(256), 0, 1, st, a);
+  return cudaLaunchKernelEx(&cfg, k_pkv_rows<HD, SPLIT>, map, a);
 }
 
 template <int HD>
@@ -794,12 +609,20 @@ cudaError_t prepare() {
 
 }  // namespace
 
-cudaError_t prepare_pkv_kernels(int hd) { return hd == 128 ? prepare<128>() : prepare<64>(); }
+cudaError_t launch_pkv_join(int hd, const PkvAttnArgs &a, int rows, cudaStream_t st) {
+  const dim3 grid(a.grid, (rows + 31) / 32), block(256);
+  return hd == 128 ? launch_pdl(k_pkv_join<128>, grid, block, 0, 1, st, a)
+                   : launch_pdl(k_pkv_join<64>, grid, block, 0, 1, st, a);
+}
+
+cudaError_t prepare_pkv_rows(int hd) { return hd == 128 ? prepare<128>() : prepare<64>(); }
 
 cudaError_t launch_pkv_rows(int hd, const CUtensorMap &map, const PkvAttnArgs &a, cudaStream_t st) {
   const bool split = a.q.dtype == PNB_F32 || a.out.dtype == PNB_F32;
-  if (hd == 128) return split ? launch_rows<128, true>(map, a, st) : launch_rows<128, false>(map, a, st);
-  return split ? launch_rows<64, true>(map, a, st) : launch_rows<64, false>(map, a, st);
+  cudaError_t e;
+  if (hd == 128) e = split ? launch_rows<128, true>(map, a, st) : launch_rows<128, false>(map, a, st);
+  else e = split ? launch_rows<64, true>(map, a, st) : launch_rows<64, false>(map, a, st);
+  return e == cudaSuccess ? launch_pkv_join(hd, a, kPkvBlockRows, st) : e;
 }
 
 }  // namespace pnb
