@@ -13,10 +13,12 @@
 //   warp 8          K and V tiles by tiled TMA loads of a page's rows each, into a ring;
 //   warp 9          S = Q K^T (both operands in shared memory) and O += P V (P in tensor
 //                   memory), the two halves in turn, so that one half's softmax runs
-//                   beside the other's products;
-//   warps 10, 11    V rows that no row of the block sees become zero (0 x NaN is NaN), and
-//                   tiles that some rows see only in part are searched for NaN and
-//                   infinities: a block that has one is done again row by row.
+//                   beside the other's products (issued by a thread each, the halves ran
+//                   in step, softmax beside softmax: a third slower);
+//   warps 10, 11    V rows behind a sequence's last entry become zero (0 x NaN is NaN).
+// A NaN or an infinity among a sequence's own values reaches, through tiles that a block's
+// rows see only in part, rows that do not attend to it: a row whose output is not finite
+// is done again by itself where such a value lies.
 // Tensor memory (512 columns): S of both halves (128 each), O of both halves.
 //
 // fp32 on either side (SPLIT): Q and P enter as two bf16 numbers, high and low part, in
@@ -34,12 +36,24 @@ extern __shared__ __align__(1024) uint8_t r_smem[];
 
 constexpr int kThreads = 384;
 constexpr int kSoftWarps = 8;
-constexpr int kBadSlots = 8;       // items that the V search may be ahead of the softmax, and more
 constexpr float kTau = 8.f;
-// the V search waits for a tile that may be a whole item away
+// the warps that clear V wait for a tile that may be a whole item away
 constexpr unsigned long long kItemLimitNs = 10000000000ull;
-// registers per thread: 384 x 168 at launch = 256 x 216 + 128 x 72
-constexpr int kRegsSoft = 216, kRegsRest = 72;
+// registers per thread: 384 x 168 at launch = 256 x 208 + 128 x 88
+constexpr int kRegsSoft = 208, kRegsRest = 88;
+
+// a place in the ring and the parity of its turn
+template <int NU>
+struct RingAt {
+  int s = 0;
+  uint32_t turn = 0;
+  __device__ __forceinline__ void next() {
+    if (++s == NU) {
+      s = 0;
+      turn ^= 1;
+    }
+  }
+};
 
 template <int HD, bool SPLIT>
 struct RL {
@@ -54,31 +68,60 @@ struct RL {
 struct RBars {
   uint64_t full[16], empty[16], q_ready[2], s_full[2], p_ready[2], o_full[2], v_go, v_ok, drain;
   uint32_t tmem, pad;
-  int bad[kBadSlots];
   PkvWalk walk;
 };
 static_assert(sizeof(RBars) <= 1024, "barriers");
 
-// 8 elements of a query row as bf16, and with SPLIT what the rounding left
-template <bool SPLIT>
-__device__ __forceinline__ void load_q8(const DevRows &q, int64_t at, uint4 &hi, uint4 &lo) {
-  if (q.dtype == PNB_BF16) {
-    hi = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(q.p) + at);
-    lo = make_uint4(0, 0, 0, 0);
-    return;
+// S = Q K^T of one half and tile: hd / 16 products (twice with SPLIT)
+template <int HD, bool SPLIT, int I = 0>
+__device__ __forceinline__ void products_s(uint32_t d, uint64_t q, uint64_t k) {
+  typedef RL<HD, SPLIT> L;
+  constexpr int KS = HD / 16, part = I / KS, c = I % KS / 4, x = I % 4;
+  if constexpr (I < (SPLIT ? 2 : 1) * KS) {
+    mma_bf16_off<(part * L::UNIT + c * L::BOX + x * 32) / 16, (c * L::BOX + x * 32) / 16>(
+        d, q, k, idesc_bf16_f32(128, kPkvTile), I > 0);
+    products_s<HD, SPLIT, I + 1>(d, q, k);
   }
-  float f[8];
-  const float *p = static_cast<const float *>(q.p) + at;
-  load_vals<float, 4>(p, reinterpret_cast<float(&)[4]>(f[0]));
-  load_vals<float, 4>(p + 4, reinterpret_cast<float(&)[4]>(f[4]));
-  uint32_t h[4], l[4];
+}
+// O += P V: eight products of 16 entries (twice with SPLIT), V with N contiguous
+template <int HD, bool SPLIT, int I = 0>
+__device__ __forceinline__ void products_o(uint32_t d, uint32_t p, uint64_t v, bool first) {
+  constexpr int KS = kPkvTile / 16, part = I / KS, x = I % KS;
+  if constexpr (I < (SPLIT ? 2 : 1) * KS) {
+    mma_bf16_ts_off<part * 64 + x * 8, x * 2048 / 16>(d, p, v, idesc_bf16_f32(128, HD) | (1u << 16), I > 0 || !first);
+    products_o<HD, SPLIT, I + 1>(d, p, v, first);
+  }
+}
+
+// 8 elements of a query row as bf16, and what the rounding left
+__device__ __forceinline__ void split8(const float4 &a, const float4 &b, uint4 &hi, uint4 &lo) {
+  hi = make_uint4(pack_bf16(a.x, a.y), pack_bf16(a.z, a.w), pack_bf16(b.x, b.y), pack_bf16(b.z, b.w));
+  lo = make_uint4(pack_bf16(a.x - bf16lo(hi.x), a.y - bf16hi(hi.x)), pack_bf16(a.z - bf16lo(hi.y), a.w - bf16hi(hi.y)),
+                  pack_bf16(b.x - bf16lo(hi.z), b.y - bf16hi(hi.z)), pack_bf16(b.z - bf16lo(hi.w), b.w - bf16hi(hi.w)));
+}
+
+// Whether a value that some row of a block sees and another does not is NaN or infinite
+// (the calling warp; entries of tiles that the block's rows see in part).
+template <int HD>
+__device__ __noinline__ bool hidden_odd_values(const PkvAttnArgs &a, const PkvItem &it) {
+  const int lane = threadIdx.x & 31;
+  const int seq = a.pass == kPkvPrefix ? min(max(a.group_start[it.b], 0), a.seqs.n_seq - 1) : it.b;
+  const int32_t *pages = a.seqs.pages + (int64_t)seq * a.seqs.max_page;
+  const int first = it.t0 * kPkvTile, end = (it.t0 + it.nt) * kPkvTile;
+  const int lim = a.pass == kPkvPrefix ? it.hi : it.len;
+  bool bad = false;
+  for (int part = 0; part < 2; ++part) {
+    const int from = part ? max(it.hi_min, first) : first;
+    const int to = min(part ? end : min(it.lo_max, end), lim);
+    for (int e = max(from, 0); e < to; ++e) {
+      const __nv_bfloat16 *v = pkv_row<HD>(a.pool, pages, e, 1, it.h);
+      float x[HD / 32] = {};
+      if (v) load_vals<__nv_bfloat16, HD / 32>(v + lane * (HD / 32), x);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    h[i] = pack_bf16(f[2 * i], f[2 * i + 1]);
-    l[i] = pack_bf16(f[2 * i] - bf16lo(h[i]), f[2 * i + 1] - bf16hi(h[i]));
+      for (int i = 0; i < HD / 32; ++i) bad |= !(x[i] * 0.f == 0.f);
+    }
   }
-  hi = make_uint4(h[0], h[1], h[2], h[3]);
-  lo = make_uint4(l[0], l[1], l[2], l[3]);
+  return __any_sync(0xffffffffu, bad);
 }
 
 template <int HD, bool SPLIT>
@@ -107,7 +150,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&bar.v_go, 1);
     mbar_init(&bar.v_ok, 64);
     mbar_init(&bar.drain, 1);
-    for (int i = 0; i < kBadSlots; ++i) bar.bad[i] = 0;
     fence_barrier_init();
     bar.walk = PkvWalk{0, 0, 0, 0, 0, 1};
   }
@@ -126,7 +168,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   PkvWalk walk = bar.walk;
   PkvItem it;
   const uint32_t tmem = bar.tmem;
-  const uint32_t t_s[2] = {tmem, tmem + 128}, t_o[2] = {tmem + 256, tmem + 384};
   // the ring held the schedule's sums: order them before the tiles that TMA writes
   fence_async_smem();
   __syncthreads();
@@ -137,6 +178,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ------------------------------------------------------ K and V tiles
       bool ok = true;
       uint32_t u = 0;   // units issued
+      RingAt<NU> at;
       // a lane per copied box: a page's rows, at most 64 of them
       const int log2p = a.pool.page_log2, log2b = min(log2p, kPkvBoxLog2), per_tile = kPkvTile >> log2b, box = 1 << log2b;
       const int rows_total = a.pool.n_page * 2 * a.pool.n_kv << log2p;
@@ -157,9 +199,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int now = id;
           if (t + 1 < it.tb) id = page_id(t + 1);
 #pragma unroll
-          for (int kv = 0; kv < 2; ++kv, ++u) {
-            const int s = u % NU;
-            if (u >= NU && !mbar_wait(&bar.empty[s], (u / NU - 1) & 1)) ok = false;
+          for (int kv = 0; kv < 2; ++kv, ++u, at.next()) {
+            const int s = at.s;
+            if (u >= NU && !mbar_wait(&bar.empty[s], at.turn ^ 1)) ok = false;
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             if (lane == 0) mbar_arrive_expect_tx(&bar.full[s], L::UNIT);
@@ -183,111 +225,99 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     } else if (warp == 9) {
       // ----------------------------------------------------------- products
-      if (lane == 0) {
-        constexpr uint32_t idesc_s = idesc_bf16_f32(128, kPkvTile);
-        constexpr uint32_t idesc_o = idesc_bf16_f32(128, HD) | (1u << 16);   // V: N contiguous
-        bool ok = true;
-        uint32_t u = 0, nq[2] = {0, 0}, np[2] = {0, 0}, nv = 0;
-        auto issue_s = [&](int w, int s) {
-          const uint8_t *k = ring + s * L::UNIT, *q = Q + w * L::QHALF;
+      // The whole warp goes through the loops, with numbers that are the same in every lane,
+      // and one elected lane issues: descriptors then stay in uniform registers (21 cycles
+      // per product; 47 from a thread of its own, which kept the tensor pipe waiting).
+      // A descriptor each for Q, K and V at the buffers' start; what a product adds to it
+      // is known at compile time.
+      const uint64_t q0 = desc_k_sw128(Q, 0), k0 = desc_k_sw128(ring, 0), v0 = desc_mn_sw128(ring, L::BOX);
+      bool ok = true;
+      uint32_t nq[2] = {0, 0}, np[2] = {0, 0}, nv = 0;
+      RingAt<NU> at;
+      auto wait = [&](uint64_t *b, uint32_t parity) { return __all_sync(0xffffffffu, mbar_wait(b, parity)) != 0; };
+      while (ok && __all_sync(0xffffffffu, walk.next<kPkvTile>(a, TB, it))) {
+        const int halves = __shfl_sync(0xffffffffu, it.ntok * G > 128 ? 2 : 1, 0);
+        const int tiles = __shfl_sync(0xffffffffu, it.tb - it.ta, 0);
+        // tiles from this one on reach past the sequence's last entry
+        const int past = __shfl_sync(0xffffffffu, it.len / kPkvTile - it.t0 - it.ta, 0);
+        ok = wait(&bar.full[at.s], at.turn);
 #pragma unroll
-          for (int part = 0; part < (SPLIT ? 2 : 1); ++part)
+        for (int w = 0; w < 2; ++w) {
+          if (w >= halves || !ok) break;
+          ok = wait(&bar.q_ready[w], nq[w]++ & 1);
+          if (!ok) break;
+          tc_fence_after();
+          if (elect_one()) {
+            products_s<HD, SPLIT>(tmem + w * 128, q0 + w * (L::QHALF >> 4), k0 + at.s * (L::UNIT >> 4));
+            mma_commit(&bar.s_full[w]);
+            if (w == halves - 1) mma_commit(&bar.empty[at.s]);
+          }
+          __syncwarp();
+        }
+        at.next();
+        for (int t = 0; t < tiles && ok; ++t) {
+          const RingAt<NU> v = at;   // this tile's V, then the next one's K
+          at.next();
+          const bool more = t + 1 < tiles;
+          ok = wait(&bar.full[v.s], v.turn);
+          if (ok && t >= past) {
+            if (elect_one()) mbar_arrive(&bar.v_go);
+            ok = wait(&bar.v_ok, nv++ & 1);
+          }
+          if (ok && more) ok = wait(&bar.full[at.s], at.turn);
 #pragma unroll
-            for (int c = 0; c < L::NB; ++c)
-#pragma unroll
-              for (int x = 0; x < 4; ++x)
-                mma_bf16(t_s[w], desc_k_sw128(q + part * L::UNIT + c * L::BOX, x * 32),
-                         desc_k_sw128(k + c * L::BOX, x * 32), idesc_s, part > 0 || c > 0 || x > 0);
-          mma_commit(&bar.s_full[w]);
-        };
-        auto issue_o = [&](int w, int s, bool first) {
-          const uint8_t *v = ring + s * L::UNIT;
-#pragma unroll
-          for (int part = 0; part < (SPLIT ? 2 : 1); ++part)
-#pragma unroll
-            for (int x = 0; x < kPkvTile / 16; ++x)
-              mma_bf16_ts(t_o[w], t_s[w] + part * 64 + x * 8, desc_mn_sw128(v + x * 2048, L::BOX), idesc_o,
-                          !first || part > 0 || x > 0);
-        };
-        while (ok && walk.next<kPkvTile>(a, TB, it)) {
-          const int halves = it.ntok * G > 128 ? 2 : 1;
-          for (int w = 0; w < halves && ok; ++w) {
-            ok = mbar_wait(&bar.q_ready[w], nq[w]++ & 1) && (w || mbar_wait(&bar.full[u % NU], (u / NU) & 1));
+          for (int w = 0; w < 2; ++w) {
+            if (w >= halves || !ok) break;
+            ok = wait(&bar.p_ready[w], np[w]++ & 1);
             if (!ok) break;
             tc_fence_after();
-            issue_s(w, u % NU);
-          }
-          if (ok) mma_commit(&bar.empty[u % NU]);
-          ++u;
-          for (int t = it.ta; t < it.tb && ok; ++t) {
-            // u: this tile's V; u + 1: the next one's K
-            const int sv = u % NU, sk = (u + 1) % NU;
-            const bool more = t + 1 < it.tb;
-            const int e = (it.t0 + t) * kPkvTile;
-            ok = mbar_wait(&bar.full[sv], (u / NU) & 1);
-            if (ok && (e < it.lo_max || e + kPkvTile > it.hi_min)) {
-              mbar_arrive(&bar.v_go);
-              ok = mbar_wait(&bar.v_ok, nv++ & 1);
-            }
-            for (int w = 0; w < halves && ok; ++w) {
-              ok = mbar_wait(&bar.p_ready[w], np[w]++ & 1);
-              if (!ok) break;
-              tc_fence_after();
-              issue_o(w, sv, t == it.ta);
-              if (!more) mma_commit(&bar.o_full[w]);
-              if (w == halves - 1) mma_commit(&bar.empty[sv]);
+            if (elect_one()) {
+              products_o<HD, SPLIT>(tmem + 256 + w * 128, tmem + w * 128, v0 + v.s * (L::UNIT >> 4), t == 0);
               if (more) {
-                if (w == 0) ok = mbar_wait(&bar.full[sk], ((u + 1) / NU) & 1);
-                if (!ok) break;
-                issue_s(w, sk);
-                if (w == halves - 1) mma_commit(&bar.empty[sk]);
+                if (w == halves - 1) mma_commit(&bar.empty[v.s]);
+                products_s<HD, SPLIT>(tmem + w * 128, q0 + w * (L::QHALF >> 4), k0 + at.s * (L::UNIT >> 4));
+                mma_commit(&bar.s_full[w]);
+                if (w == halves - 1) mma_commit(&bar.empty[at.s]);
+              } else {
+                mma_commit(&bar.o_full[w]);
+                if (w == halves - 1) mma_commit(&bar.empty[v.s]);
               }
             }
-            u += more ? 2 : 1;
+            __syncwarp();
           }
+          if (more) at.next();
         }
-        if (!ok) {
+      }
+      if (!ok) {
+        if (elect_one()) {
           set_error(a.err, kErrTimeout);
           mma_commit(&bar.drain);   // the products in flight end before tensor memory is given back
-          mbar_wait(&bar.drain, 0);
         }
+        mbar_wait(&bar.drain, 0);
       }
       __syncwarp();
     } else {
-      // --------------------------------------------- V rows that are not seen
-      const int tid = threadIdx.x - 320;
+      // --------------------------------------------- V rows that are no entries
       bool ok = true;
-      uint32_t u = 0, item = 0, nv = 0;
+      const int tid = threadIdx.x - 320;
+      uint32_t nv = 0;
+      RingAt<NU> at;
       while (ok && walk.next<kPkvTile>(a, TB, it)) {
-        for (int t = it.ta; t < it.tb && ok; ++t, u += 2) {
+        for (int t = it.ta; t < it.tb && ok; ++t, at.next()) {
+          at.next();   // K, then V
           const int e0 = (it.t0 + t) * kPkvTile;
-          if (e0 >= it.lo_max && e0 + kPkvTile <= it.hi_min) continue;
-          const int s = (u + 1) % NU;
+          if (it.t0 + t < it.len / kPkvTile) continue;
+          const int s = at.s;
           // (the ring's own barriers would not do: this warp skips tiles, and the ring
           // may be a whole turn ahead or behind)
           ok = mbar_wait_for(&bar.v_go, nv++ & 1, kItemLimitNs);
           if (!ok) break;
-          uint8_t *v = ring + s * L::UNIT;
-          bool bad = false;
-          for (int i = tid; i < L::UNIT / 16; i += 64) {
-            const int e = e0 + ((i >> 3) & (kPkvTile - 1));
-            uint4 *p = reinterpret_cast<uint4 *>(v) + i;
-            if (e >= it.hi || e < it.lo) {
-              *p = make_uint4(0, 0, 0, 0);
-            } else {
-              const uint4 x = *p;
-              // an exponent of ones in either half of a word
-              auto odd = [](uint32_t w) {
-                return (w & 0x7f800000u) == 0x7f800000u || (w & 0x7f80u) == 0x7f80u;
-              };
-              bad |= odd(x.x) || odd(x.y) || odd(x.z) || odd(x.w);
-            }
-          }
-          if (bad) *reinterpret_cast<volatile int *>(&bar.bad[item % kBadSlots]) = (int)item + 1;
+          uint4 *v = reinterpret_cast<uint4 *>(ring + s * L::UNIT);
+          for (int i = tid; i < L::UNIT / 16; i += 64)
+            if (e0 + ((i >> 3) & (kPkvTile - 1)) >= it.len) v[i] = make_uint4(0, 0, 0, 0);
           fence_async_smem();
           mbar_arrive(&bar.v_ok);
         }
-        ++item;
       }
       if (!ok && lane == 0) set_error(a.err, kErrTimeout);
     }
@@ -296,27 +326,74 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
     const int w = warp >> 2, quad = warp & 3, r = (warp << 5) + lane;   // r: row of the block
     const uint32_t lanes = (uint32_t)(32 * quad) << 16;
-    const uint32_t ts = t_s[w] + lanes, to = t_o[w] + lanes;
+    const uint32_t ts = tmem + w * 128 + lanes, to = tmem + 256 + w * 128 + lanes;
     const float c = a.qscale;
-    uint32_t ns = 0, no = 0, item = 0;
+    // row / G as the high half of a product: exact for rows below 2^16 and G up to 64
+    const uint32_t g_inv = (uint32_t)((0x100000000ull + G - 1) / G);
+    auto div_g = [&](int row) { return G == 1 ? row : (int)__umulhi((uint32_t)row, g_inv); };
+    uint32_t ns = 0, no = 0;
     bool ok = true;
 
-    // the warp's 32 query rows of an item into shared memory
-    auto load_q = [&](const PkvItem &x) {
-      constexpr int LPR = HD / 8, RPW = 32 / LPR;   // lanes per row, rows at a time
-      const int l = lane % LPR, sub = lane / LPR;
-      uint8_t *q = Q + w * L::QHALF;
-#pragma unroll 4
-      for (int k = 0; k < 32; k += RPW) {
-        const int row = (warp << 5) + k + sub;
-        uint4 hi = make_uint4(0, 0, 0, 0), lo = hi;
-        if (row < x.ntok * G) {
-          const int tok = x.tok0 + row / G, head = x.h * G + row % G;
-          load_q8<SPLIT>(a.q, tok * a.q.token + head * a.q.head + 8 * l, hi, lo);
+    // A warp's 32 rows of a half lie in its own part of the Q buffer: queries before an
+    // item, outputs on their way to memory behind it.  LPR lanes have 8 elements each.
+    constexpr int LPR = HD / 8, RPW = 32 / LPR, QR = 32 / RPW;
+    const int ql = lane % LPR, qsub = lane / LPR;
+    uint8_t *const qmine = Q + w * L::QHALF + quad * 4096;   // 4 KB of each box
+    uint4 qh[SPLIT ? 1 : QR];
+    auto q_at = [&](const PkvItem &x, int row) {
+      const int q = div_g(row);
+      return (x.tok0 + q) * a.q.token + (x.h * G + row - q * G) * a.q.head + 8 * ql;
+    };
+    auto put = [&](int k, const uint4 &v, int part) {
+      const int row = k * RPW + qsub;
+      *reinterpret_cast<uint4 *>(qmine + part * L::UNIT + (ql >> 3) * L::BOX + sw128(row, (ql & 7) * 16)) = v;
+    };
+    // bf16 queries of the next item load while this one's outputs are on their way; rows
+    // behind the block's last one repeat it, so that all loads are on their way at once
+    auto fetch_q = [&](const PkvItem &x) {
+      if constexpr (!SPLIT) {
+        const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(a.q.p);
+        const int last = x.ntok * G - 1;
+#pragma unroll
+        for (int k = 0; k < QR; ++k)
+          qh[k] = *reinterpret_cast<const uint4 *>(src + q_at(x, min((warp << 5) + k * RPW + qsub, last)));
+      }
+    };
+    auto put_q = [&](const PkvItem &x) {
+      if constexpr (!SPLIT) {
+#pragma unroll
+        for (int k = 0; k < QR; ++k) put(k, qh[k], 0);
+      } else {
+        const int last = x.ntok * G - 1;
+        constexpr int B = 4;
+#pragma unroll 1
+        for (int k = 0; k < QR; k += B) {
+          uint4 hi[B], lo[B];
+          if (a.q.dtype == PNB_F32) {
+            float4 f[B][2];
+#pragma unroll
+            for (int i = 0; i < B; ++i) {
+              const float4 *p = reinterpret_cast<const float4 *>(
+                  static_cast<const float *>(a.q.p) + q_at(x, min((warp << 5) + (k + i) * RPW + qsub, last)));
+              f[i][0] = p[0];
+              f[i][1] = p[1];
+            }
+#pragma unroll
+            for (int i = 0; i < B; ++i) split8(f[i][0], f[i][1], hi[i], lo[i]);
+          } else {
+#pragma unroll
+            for (int i = 0; i < B; ++i) {
+              hi[i] = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.q.p) +
+                                                       q_at(x, min((warp << 5) + (k + i) * RPW + qsub, last)));
+              lo[i] = make_uint4(0, 0, 0, 0);
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < B; ++i) {
+            put(k + i, hi[i], 0);
+            put(k + i, lo[i], 1);
+          }
         }
-        uint8_t *p = q + (l >> 3) * L::BOX + sw128(row & 127, (l & 7) * 16);
-        *reinterpret_cast<uint4 *>(p) = hi;
-        if (SPLIT) *reinterpret_cast<uint4 *>(p + L::UNIT) = lo;
       }
       fence_async_smem();
       __syncwarp();
@@ -324,18 +401,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     // the next item with rows for this half
     auto next = [&](PkvItem &x) {
-      while (walk.next<kPkvTile>(a, TB, x)) {
-        ++item;
+      while (walk.next<kPkvTile>(a, TB, x))
         if (x.ntok * G > 128 * w) return true;
-      }
       return false;
     };
 
     bool have = next(it);
-    if (have) load_q(it);
+    if (have) {
+      fetch_q(it);
+      put_q(it);
+    }
     while (have && ok) {
       const bool live = r < it.ntok * G;
-      const int tok = it.tok0 + (live ? r / G : 0), head = it.h * G + (live ? r % G : 0);
+      const int rq = live ? div_g(r) : 0, tok = it.tok0 + rq, head = it.h * G + (live ? r - rq * G : 0);
       int lo = it.lo, hi = it.hi;
       if (a.pass == kPkvPrefix) {
         if (a.window > 0) {
@@ -431,19 +509,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(&bar.p_ready[w]);
       }
       if (!ok) break;
-      // the next item's queries go where this one's lay: its last S is done
-      const uint32_t id = item;
       PkvItem nx;
       have = next(nx);
-      if (have) load_q(nx);
-
+      if (have) fetch_q(nx);
       if (!mbar_wait(&bar.o_full[w], no++ & 1)) {
         ok = false;
         break;
       }
       __syncwarp();
       tc_fence_after();
-      const bool redo = *reinterpret_cast<volatile int *>(&bar.bad[(id - 1) % kBadSlots]) == (int)id;
       const bool whole = it.ta == 0 && it.ends;
       const int side = it.ta > 0 ? 0 : 1;   // of the run's two partial sums
       // the prefix's part of the row
@@ -457,47 +531,95 @@ __global__ void __launch_bounds__(kThreads, 1)
         all = sum * f_own + ml.y * f_pre;
       }
       const float inv = all == 0.f ? 0.f : 1.f / all;
-      float *po = nullptr, *pml = nullptr;
+      float *po = nullptr, *pml = nullptr, *po_base = nullptr;
+      auto qout = [&](int at) { return qmine + (at >> 12) * L::BOX + (at & 4095); };   // no row crosses 4 KB
       if (!whole) {
         const int64_t at = (int64_t)(2 * blockIdx.x + side) * kPkvBlockRows + r;
         po = a.part_o + at * HD;
+        po_base = a.part_o + (int64_t)(2 * blockIdx.x + side) * kPkvBlockRows * HD;
         pml = a.part_ml + at * 2;
         if (r == 0) a.part[2 * blockIdx.x + side] = PkvPart{it.ends ? 3 : 1, it.b, it.j, it.h};
       } else if (a.pass == kPkvPrefix) {
         const int64_t at = (int64_t)tok * a.n_head + head;
         po = a.row_o + at * HD;
+        po_base = a.row_o;
         pml = a.row_ml + at * 2;
       }
-      if (!redo) {
+      // outputs through the warp's part of the Q buffer, so that rows leave in whole lines
+      const bool f32 = po || a.out.dtype == PNB_F32;
+      const int passes = f32 && !SPLIT ? 2 : 1;   // without SPLIT there is room for 16 bits per element
+      bool redo = false, odd = false;
+      uint32_t odd_rows = 0;
+#pragma unroll 1
+      for (int pass = 0; pass < passes; ++pass) {
+        const int rows_at_once = 32 / passes;
+        const bool mine = lane / rows_at_once == pass;
+        float z = 0.f;   // NaN if an output is not finite
 #pragma unroll 1
         for (int i = 0; i < HD; i += 32) {
           float o[32];
           tmem_ld32_async(to + i, o);
           tmem_wait_ld();
           tmem_landed(o);
-          if (live && po) {
 #pragma unroll
-            for (int k = 0; k < 32; k += 4)
-              *reinterpret_cast<float4 *>(po + i + k) = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
-          } else if (live) {
-            // a row that saw nothing has only zeros summed up
-            if (it.floor > 0) {
+          for (int k = 0; k < 32; ++k) z = fmaf(o[k], 0.f, z);
+          if (bo && live) {
 #pragma unroll
-              for (int k = 0; k < 32; k += 4) {
-                const float4 x = *reinterpret_cast<const float4 *>(bo + i + k);
-                o[k] = o[k] * f_own + x.x * f_pre;
-                o[k + 1] = o[k + 1] * f_own + x.y * f_pre;
-                o[k + 2] = o[k + 2] * f_own + x.z * f_pre;
-                o[k + 3] = o[k + 3] * f_own + x.w * f_pre;
-              }
+            for (int k = 0; k < 32; k += 4) {
+              const float4 x = *reinterpret_cast<const float4 *>(bo + i + k);
+              o[k] = o[k] * f_own + x.x * f_pre;
+              o[k + 1] = o[k + 1] * f_own + x.y * f_pre;
+              o[k + 2] = o[k + 2] * f_own + x.z * f_pre;
+              o[k + 3] = o[k + 3] * f_own + x.w * f_pre;
             }
-            pkv_store<32>(a.out, tok * a.out.token + head * a.out.head + i, o, inv);
           }
-          __syncwarp();
+          // 16-byte pieces of a row, turned by the row so that lanes meet different banks
+          if (mine) {
+            uint8_t *row = qout((lane % rows_at_once) * (f32 ? HD * 4 : HD * 2));
+            const float f = po ? 1.f : inv;   // a row that saw nothing has only zeros summed up
+            if (f32) {
+#pragma unroll
+              for (int k = 0; k < 32; k += 4)
+                *reinterpret_cast<float4 *>(row + ((((i + k) >> 2) ^ (lane & 7)) << 4)) =
+                    make_float4(o[k] * f, o[k + 1] * f, o[k + 2] * f, o[k + 3] * f);
+            } else {
+#pragma unroll
+              for (int k = 0; k < 32; k += 8)
+                *reinterpret_cast<uint4 *>(row + ((((i + k) >> 3) ^ (lane & 7)) << 4)) =
+                    make_uint4(pack_bf16(o[k] * f, o[k + 1] * f), pack_bf16(o[k + 2] * f, o[k + 3] * f),
+                               pack_bf16(o[k + 4] * f, o[k + 5] * f), pack_bf16(o[k + 6] * f, o[k + 7] * f));
+            }
+          }
         }
-        if (live && po) *reinterpret_cast<float2 *>(pml) = make_float2(m, sum);
-      } else {
-        // a NaN or an infinity among values that only some rows see: each row by itself
+        if (pass == 0) {
+          odd = live && z != 0.f;
+          odd_rows = __ballot_sync(0xffffffffu, odd);
+          if (odd_rows) {
+            const PkvItem copy = it;   // (its address is taken)
+            redo = hidden_odd_values<HD>(a, copy);
+          }
+        }
+        __syncwarp();
+        const int lpr = f32 ? HD / 4 : HD / 8;   // lanes per row
+        const int l = lane % lpr;
+#pragma unroll 4
+        for (int k = lane / lpr; k < rows_at_once; k += 32 / lpr) {
+          const int src = pass * rows_at_once + k, row = (warp << 5) + src;
+          const uint4 x = *reinterpret_cast<const uint4 *>(qout(k * (f32 ? HD * 4 : HD * 2)) + ((l ^ (src & 7)) << 4));
+          const int q = div_g(row);
+          if (row >= it.ntok * G || (redo && (odd_rows >> src & 1))) continue;
+          if (po) {
+            reinterpret_cast<uint4 *>(po_base + (int64_t)(whole ? (it.tok0 + q) * a.n_head + it.h * G + row - q * G : row) * HD)[l] = x;
+          } else {
+            const int64_t at = (it.tok0 + q) * a.out.token + (it.h * G + row - q * G) * a.out.head;
+            if (f32) reinterpret_cast<uint4 *>(static_cast<float *>(a.out.p) + at)[l] = x;
+            else reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out.p) + at)[l] = x;
+          }
+        }
+        __syncwarp();
+      }
+      if (live && po && !(redo && odd)) *reinterpret_cast<float2 *>(pml) = make_float2(m, sum);
+      if (redo) {
         const int seq = a.pass == kPkvPrefix ? min(max(a.group_start[it.b], 0), a.seqs.n_seq - 1) : it.b;
         for (int k = 0; k < 32; ++k) {
           const int from = max(__shfl_sync(0xffffffffu, lo, k), (it.t0 + it.ta) * kPkvTile);
@@ -505,7 +627,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int tk = __shfl_sync(0xffffffffu, tok, k), hd_k = __shfl_sync(0xffffffffu, head, k);
           const long long po_k = __shfl_sync(0xffffffffu, (long long)(uintptr_t)po, k);
           const long long pml_k = __shfl_sync(0xffffffffu, (long long)(uintptr_t)pml, k);
-          if (!__shfl_sync(0xffffffffu, (int)live, k)) continue;
+          if (!(odd_rows >> k & 1)) continue;
           float o[HD / 32], mk, lk;
           pkv_attend_row<HD>(a.pool, a.seqs.pages + (int64_t)seq * a.seqs.max_page, it.h, a.q,
                              tk * a.q.token + hd_k * a.q.head, c, from, to_e, o, mk, lk);
@@ -516,11 +638,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) *reinterpret_cast<float2 *>((uintptr_t)pml_k) = make_float2(mk, lk);
           } else {
             if (it.floor > 0) pkv_add_prefix<HD / 32>(a, tk, hd_k, o, mk, lk);
-            const float d = lk == 0.f ? 0.f : 1.f / lk;
-            pkv_store<HD / 32>(a.out, tk * a.out.token + hd_k * a.out.head + lane * (HD / 32), o, d);
+            pkv_store<HD / 32>(a.out, tk * a.out.token + hd_k * a.out.head + lane * (HD / 32), o,
+                               lk == 0.f ? 0.f : 1.f / lk);
           }
         }
       }
+      if (have) put_q(nx);
       tc_fence_before();
       it = nx;
     }
@@ -534,10 +657,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // Adds up the parts of the items that several CTAs shared, in the list's order.  The
 // CTA whose run holds an item's first tiles has it in its second partial sum; the
-// runs behind it hold the rest in their first ones.  A warp per row.
+// runs behind it hold the rest in their first ones.  A warp takes four rows together, so
+// that the parts' loads are on their way at once.
 template <int HD>
 __global__ void __launch_bounds__(256) k_pkv_join(const PkvAttnArgs a) {
-  constexpr int N = HD / 32;
+  constexpr int N = HD / 32, R = 4;
+  __shared__ int s_last;
   const int lane = threadIdx.x & 31, c0 = blockIdx.x;
   pdl_wait();
   pdl_trigger();
@@ -546,40 +671,75 @@ __global__ void __launch_bounds__(256) k_pkv_join(const PkvAttnArgs a) {
   const int G = a.n_head / a.pool.n_kv, TB = kPkvBlockRows / G;
   PkvItem it;
   if (!pkv_block<kPkvTile>(a, TB, p.b, p.j, it)) return;
-  int last = c0;   // the run that ends the item
-  if (!(p.flags & 2))
-    for (last = c0 + 1; last < a.grid - 1 && !(a.part[2 * last].flags & 2);) ++last;
-  for (int r = blockIdx.y * 8 + (threadIdx.x >> 5); r < it.ntok * G; r += 8 * gridDim.y) {
-    float m = -INFINITY;
-    for (int k = c0; k <= last; ++k) {
-      const int slot = k == c0 ? 2 * k + 1 : 2 * k;
-      if (!(a.part[slot].flags & 1)) continue;   // (a run without units)
-      m = fmaxf(m, a.part_ml[((int64_t)slot * kPkvBlockRows + r) * 2]);
-    }
-    const float ref = m == -INFINITY ? 0.f : m;
-    float o[N] = {}, sum = 0.f;
-    for (int k = c0; k <= last; ++k) {
-      const int slot = k == c0 ? 2 * k + 1 : 2 * k;
-      if (!(a.part[slot].flags & 1)) continue;
-      const int64_t at = (int64_t)slot * kPkvBlockRows + r;
-      const float2 ml = *reinterpret_cast<const float2 *>(a.part_ml + at * 2);
-      const float f = ml.x == -INFINITY ? 0.f : exp2f(ml.x - ref);
-      float x[N];
-      load_vals<float, N>(a.part_o + at * HD + lane * N, x);
-      if (ml.x == -INFINITY && ml.y == 0.f) continue;   // a part without entries of this row
+  const int rows = it.ntok * G, r0 = (blockIdx.y * 8 + (threadIdx.x >> 5)) * R;
+  // the run that ends the item
+  if (threadIdx.x == 0) s_last = a.grid - 1;
+  __syncthreads();
+  for (int k = c0 + 1 + threadIdx.x; k < a.grid; k += blockDim.x)
+    if (a.part[2 * k].flags & 2) atomicMin(&s_last, k);
+  __syncthreads();
+  const int last = s_last;
+  if (r0 >= rows) return;
+  float m[R], sum[R], o[R][N] = {};
 #pragma unroll
-      for (int i = 0; i < N; ++i) o[i] += f * x[i];
-      sum += f * ml.y;
+  for (int i = 0; i < R; ++i) m[i] = -INFINITY;
+  // a lane per part: references first, then factors
+  for (int k0 = c0; k0 <= last; k0 += 32) {
+    const int k = k0 + lane, slot = k == c0 ? 2 * k + 1 : 2 * k;
+    const bool has = k <= last && (a.part[slot].flags & 1);   // (a run may have no units)
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+      if (has && r0 + i < rows) m[i] = fmaxf(m[i], a.part_ml[((int64_t)slot * kPkvBlockRows + r0 + i) * 2]);
+  }
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    m[i] = warp_max(m[i]);
+    sum[i] = 0.f;
+  }
+  for (int k0 = c0; k0 <= last; k0 += 32) {
+    const int k = k0 + lane, slot = k == c0 ? 2 * k + 1 : 2 * k;
+    const bool has = k <= last && (a.part[slot].flags & 1);
+    float f[R];
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      f[i] = 0.f;
+      if (has && r0 + i < rows) {
+        const float2 ml = *reinterpret_cast<const float2 *>(a.part_ml + ((int64_t)slot * kPkvBlockRows + r0 + i) * 2);
+        // a part without entries of the row counts 0, one with a NaN score as it is
+        f[i] = ml.x == -INFINITY ? (ml.y == 0.f ? 0.f : 1.f) : exp2f(ml.x - m[i]);
+        sum[i] += f[i] * ml.y;
+      }
     }
+    const uint32_t which = __ballot_sync(0xffffffffu, has);
+#pragma unroll 4
+    for (int j = 0; j < 32; ++j) {
+      if (!(which >> j & 1)) continue;
+      const int kk = k0 + j;
+      const float *src = a.part_o + ((int64_t)(kk == c0 ? 2 * kk + 1 : 2 * kk) * kPkvBlockRows + r0) * HD + lane * N;
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        float x[N] = {};
+        if (r0 + i < rows) load_vals<float, N>(src + i * HD, x);
+        const float fj = __shfl_sync(0xffffffffu, f[i], j);
+#pragma unroll
+        for (int n = 0; n < N; ++n) o[i][n] += fj * x[n];
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    const int r = r0 + i;
+    sum[i] = warp_sum(sum[i]);
+    if (r >= rows) break;
     const int tok = it.tok0 + r / G, head = p.h * G + r % G;
-    if (it.floor > 0) pkv_add_prefix<N>(a, tok, head, o, m, sum);
+    if (it.floor > 0) pkv_add_prefix<N>(a, tok, head, o[i], m[i], sum[i]);
     if (a.pass == kPkvPrefix) {
       const int64_t at = (int64_t)tok * a.n_head + head;
 #pragma unroll
-      for (int i = 0; i < N; ++i) a.row_o[at * HD + lane * N + i] = o[i];
-      if (lane == 0) *reinterpret_cast<float2 *>(a.row_ml + at * 2) = make_float2(m, sum);
+      for (int n = 0; n < N; ++n) a.row_o[at * HD + lane * N + n] = o[i][n];
+      if (lane == 0) *reinterpret_cast<float2 *>(a.row_ml + at * 2) = make_float2(m[i], sum[i]);
     } else {
-      pkv_store<N>(a.out, tok * a.out.token + head * a.out.head + lane * N, o, sum == 0.f ? 0.f : 1.f / sum);
+      pkv_store<N>(a.out, tok * a.out.token + head * a.out.head + lane * N, o[i], sum[i] == 0.f ? 0.f : 1.f / sum[i]);
     }
   }
 }

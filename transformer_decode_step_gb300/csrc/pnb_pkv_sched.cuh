@@ -14,6 +14,7 @@ struct PkvItem {
   int base;                 // first token's last entry (prompts)
   int hi, lo;               // entries [lo, hi): those that some row sees
   int hi_min, lo_max;       // entries [lo_max, hi_min): those that every row sees
+  int len;                  // the sequence's entries (the prefix's)
   int floor;                // entries below are the prefix's, another pass's
   int t0, nt;               // tiles of the whole item
   int ta, tb;               // this CTA's tiles
@@ -46,11 +47,13 @@ __device__ __forceinline__ bool pkv_block(const PkvAttnArgs &a, int TB, int b, i
   if (a.pass == kPkvPrefix) {
     const PkvGroup g = a.groups[b];
     it.base = 0;
+    it.len = INT_MAX;   // (a shared prefix is whole pages, all of them entries)
     it.hi = it.hi_min = g.prefix;
     it.lo = W > 0 ? min(max(0, g.len_min - a.seqs.each - W + 1), g.prefix) : 0;
     it.lo_max = W > 0 ? max(0, g.len_max - W) : 0;
   } else {
-    it.base = pkv_len(a.seqs, a.pool.page_log2, b, a.err) - n + j * TB;
+    it.len = pkv_len(a.seqs, a.pool.page_log2, b, a.err);
+    it.base = it.len - n + j * TB;
     it.hi = max(0, it.base + it.ntok);
     it.hi_min = it.base + 1;
     it.lo = W > 0 ? max(0, it.base - W + 1) : 0;

@@ -26,6 +26,13 @@ __device__ __forceinline__ void tma_load_2d(void *dst, const void *tmap, int x, 
 }
 
 // --------------------------------------------------------------- tcgen05
+// true in one lane of a converged warp
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
 // Allocate ncols TMEM columns (a power of two >= 32); the whole warp
 // executes it and the TMEM address lands in *dst (shared memory).
 __device__ __forceinline__ void tmem_alloc(uint32_t *dst, uint32_t ncols) {
@@ -60,23 +67,38 @@ __device__ __forceinline__ void mma_bf16(uint32_t d_tmem, uint64_t a_desc, uint6
       : "memory");
 }
 
+// The same, and with A from TMEM (its rows are lanes, two bf16 per column), with
+// descriptors as a base and what is added to it, in 16-byte units (A in TMEM: columns), so
+// that no register holds a product's own descriptor from one loop turn to the next.
+template <int A_OFF, int B_OFF>
+__device__ __forceinline__ void mma_bf16_off(uint32_t d_tmem, uint64_t a_base, uint64_t b_base, uint32_t idesc,
+                                             bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+      "add.s64 a, %1, %5;\n\tadd.s64 b, %2, %6;\n\t"
+      "setp.ne.u32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_base), "l"(b_base), "r"(idesc), "r"(accumulate ? 1u : 0u), "n"(A_OFF), "n"(B_OFF)
+      : "memory");
+}
+template <int A_OFF, int B_OFF>
+__device__ __forceinline__ void mma_bf16_ts_off(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_base, uint32_t idesc,
+                                                bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b32 a;\n\t.reg .b64 b;\n\t"
+      "add.s32 a, %1, %5;\n\tadd.s64 b, %2, %6;\n\t"
+      "setp.ne.u32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_base), "r"(idesc), "r"(accumulate ? 1u : 0u), "n"(A_OFF), "n"(B_OFF)
+      : "memory");
+}
+
 // Arrive (once) on the mbarrier when every tcgen05 operation this thread
 // issued so far has completed.
 __device__ __forceinline__ void mma_commit(uint64_t *bar) {
   asm volatile(
       "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
           smem_addr(bar))
-      : "memory");
-}
-
-// D[tmem] (+)= A[tmem] * B[smem]: A's rows are TMEM lanes, two bf16 per column.
-__device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                            bool accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate ? 1u : 0u)
       : "memory");
 }
 
