@@ -4,8 +4,9 @@
 //
 // Row i attends to entries [lo_i, hi_i).  With x_ij = q_i.k_j log2(e) / sqrt(hd) and a
 // reference r_i, p_ij = 2^(x_ij - r_i), l_i = sum_j p_ij, o_i = sum_j p_ij v_j / l_i.
-// r_i only moves when a tile's largest score passes it by 2^8, so that sums and
-// outputs are rarely rescaled; p stays below 2^8 and sums are held in fp32.
+// r_i is the largest of the first scores seen, and moves when the sum of 64 p passes
+// 2^16, so that no maximum is taken and nothing is rescaled in most tiles; sums are held
+// in fp32.
 //
 // One CTA per SM works through a run of (block, 128-entry tile) units:
 //   warps 0-3, 4-7  softmax of the block's rows 0-127 and 128-255, one row per thread:
@@ -36,7 +37,7 @@ extern __shared__ __align__(1024) uint8_t r_smem[];
 
 constexpr int kThreads = 384;
 constexpr int kSoftWarps = 8;
-constexpr float kTau = 8.f;
+constexpr float kLarge = 65536.f;   // a sum of 64 p that moves the reference
 // the warps that clear V wait for a tile that may be a whole item away
 constexpr unsigned long long kItemLimitNs = 10000000000ull;
 // registers per thread: 384 x 168 at launch = 256 x 208 + 128 x 88
@@ -66,7 +67,7 @@ struct RL {
 };
 
 struct RBars {
-  uint64_t full[16], empty[16], q_ready[2], s_full[2], p_ready[2], o_full[2], v_go, v_ok, drain;
+  uint64_t full[16], empty[16], q_ready[2], s_full[2], p_ready[2][2], pv_half[2], o_full[2], v_go, v_ok, drain;
   uint32_t tmem, pad;
   PkvWalk walk;
 };
@@ -83,13 +84,14 @@ __device__ __forceinline__ void products_s(uint32_t d, uint64_t q, uint64_t k) {
     products_s<HD, SPLIT, I + 1>(d, q, k);
   }
 }
-// O += P V: eight products of 16 entries (twice with SPLIT), V with N contiguous
-template <int HD, bool SPLIT, int I = 0>
+// O += P V of half a tile: four products of 16 entries (twice with SPLIT), V with N contiguous
+template <int HD, bool SPLIT, int HALF, int I = 0>
 __device__ __forceinline__ void products_o(uint32_t d, uint32_t p, uint64_t v, bool first) {
-  constexpr int KS = kPkvTile / 16, part = I / KS, x = I % KS;
-  if constexpr (I < (SPLIT ? 2 : 1) * KS) {
-    mma_bf16_ts_off<part * 64 + x * 8, x * 2048 / 16>(d, p, v, idesc_bf16_f32(128, HD) | (1u << 16), I > 0 || !first);
-    products_o<HD, SPLIT, I + 1>(d, p, v, first);
+  constexpr int part = I / 4, x = I % 4;
+  if constexpr (I < (SPLIT ? 8 : 4)) {
+    mma_bf16_ts_off<HALF * 64 + part * 32 + x * 8, (HALF * 4 + x) * 2048 / 16>(
+        d, p, v, idesc_bf16_f32(128, HD) | (1u << 16), I > 0 || !first);
+    products_o<HD, SPLIT, HALF, I + 1>(d, p, v, first);
   }
 }
 
@@ -144,7 +146,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bar.q_ready[i], 4);
       mbar_init(&bar.s_full[i], 1);
-      mbar_init(&bar.p_ready[i], 4);
+      mbar_init(&bar.p_ready[i][0], 4);
+      mbar_init(&bar.p_ready[i][1], 4);
+      mbar_init(&bar.pv_half[i], 1);
       mbar_init(&bar.o_full[i], 1);
     }
     mbar_init(&bar.v_go, 1);
@@ -268,11 +272,19 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int w = 0; w < 2; ++w) {
             if (w >= halves || !ok) break;
-            ok = wait(&bar.p_ready[w], np[w]++ & 1);
+            ok = wait(&bar.p_ready[w][0], np[w] & 1);
             if (!ok) break;
             tc_fence_after();
             if (elect_one()) {
-              products_o<HD, SPLIT>(tmem + 256 + w * 128, tmem + w * 128, v0 + v.s * (L::UNIT >> 4), t == 0);
+              products_o<HD, SPLIT, 0>(tmem + 256 + w * 128, tmem + w * 128, v0 + v.s * (L::UNIT >> 4), t == 0);
+              mma_commit(&bar.pv_half[w]);
+            }
+            __syncwarp();
+            ok = wait(&bar.p_ready[w][1], np[w]++ & 1);
+            if (!ok) break;
+            tc_fence_after();
+            if (elect_one()) {
+              products_o<HD, SPLIT, 1>(tmem + 256 + w * 128, tmem + w * 128, v0 + v.s * (L::UNIT >> 4), false);
               if (more) {
                 if (w == halves - 1) mma_commit(&bar.empty[v.s]);
                 products_s<HD, SPLIT>(tmem + w * 128, q0 + w * (L::QHALF >> 4), k0 + at.s * (L::UNIT >> 4));
@@ -434,79 +446,83 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
         tc_fence_after();
-        float s[128];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) tmem_ld32_async(ts + 32 * i, s + 32 * i);
-        tmem_wait_ld();
-#pragma unroll
-        for (int i = 0; i < 4; ++i) tmem_landed(s + 32 * i);
+        // The row's 128 scores in two halves: the products of the first begin beside the
+        // second one's exponentials.
         const int e = (it.t0 + t) * kPkvTile;
-        if (e < it.lo_max || e + kPkvTile > it.hi_min) {
-          // columns [from, from + n) of the tile are this row's
-          const int from = max(lo - e, 0), n = max(min(hi - e, kPkvTile) - from, 0);
-#pragma unroll
-          for (int i = 0; i < 128; ++i)
-            if ((unsigned)(i - from) >= (unsigned)n) s[i] = -INFINITY;
-        }
-        float mx[4] = {s[0], s[1], s[2], s[3]};
-#pragma unroll
-        for (int i = 4; i < 124; i += 8)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) mx[k] = fmaxf(fmaxf(mx[k], s[i + k]), s[i + k + 4]);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) mx[k] = fmaxf(mx[k], s[124 + k]);
-        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
-        const bool move = top > m + kTau;
-        if (__any_sync(0xffffffffu, move)) {
-          const float f = move ? (m == -INFINITY ? 0.f : exp2_approx(m - top)) : 1.f;
-          if (move) m = top;
-          sum *= f;
-          if (t > it.ta) {
-            // the products of the tile before are done: S of this one came behind them
+        const bool masked = e < it.lo_max || e + kPkvTile > it.hi_min;
 #pragma unroll 1
-            for (int i = 0; i < HD; i += 32) {
-              float o[32];
-              tmem_ld32_async(to + i, o);
-              tmem_wait_ld();
-              tmem_landed(o);
+        for (int h = 0; h < 2; ++h) {
+          float x[64];
 #pragma unroll
-              for (int k = 0; k < 32; ++k) o[k] *= f;
-              tmem_st32_async(to + i, reinterpret_cast<const uint32_t *>(o));
+          for (int i = 0; i < 2; ++i) tmem_ld32_async(ts + 64 * h + 32 * i, x + 32 * i);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 2; ++i) tmem_landed(x + 32 * i);
+          if (masked) {
+            // columns [from, from + n) of the 64 are this row's
+            const int e2 = e + 64 * h, from = max(lo - e2, 0), n = max(min(hi - e2, 64) - from, 0);
+#pragma unroll
+            for (int i = 0; i < 64; ++i)
+              if ((unsigned)(i - from) >= (unsigned)n) x[i] = -INFINITY;
+          }
+          // No maximum is taken while the reference does: p and its sum tell when it does not,
+          // and fp32 and bf16 hold a p far above 1 as well as one below.
+          uint32_t p[32], low[SPLIT ? 32 : 1];
+          float part = 0.f;
+          for (int again = 0;; ++again) {
+            const float ref = m == -INFINITY ? 0.f : m;   // nothing seen yet: every p is 2^-inf
+            const float2 c2 = make_float2(c, c), r2 = make_float2(-ref, -ref);
+            float2 acc[2] = {};
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              float2 y = ffma2(make_float2(x[2 * i], x[2 * i + 1]), c2, r2);
+              y.x = exp2_approx(y.x);
+              y.y = exp2_approx(y.y);
+              acc[i & 1] = fadd2(acc[i & 1], y);
+              p[i] = pack_bf16(y.x, y.y);
+              if constexpr (SPLIT) low[i] = pack_bf16(y.x - bf16lo(p[i]), y.y - bf16hi(p[i]));
+            }
+            acc[0] = fadd2(acc[0], acc[1]);
+            part = acc[0].x + acc[0].y;
+            if (again || !__any_sync(0xffffffffu, m == -INFINITY || !(part < kLarge))) break;
+            float mx[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+            for (int i = 4; i < 64; i += 4)
+#pragma unroll
+              for (int k = 0; k < 4; ++k) mx[k] = fmaxf(mx[k], x[i + k]);
+            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
+            const bool move = top > m && (m == -INFINITY || !(part < kLarge));
+            if (!__any_sync(0xffffffffu, move)) break;
+            const float f = move ? (m == -INFINITY ? 0.f : exp2_approx(m - top)) : 1.f;
+            if (move) m = top;
+            sum *= f;
+            if (t > it.ta || h) {
+              // Outputs so far go to the new reference.  The products of the tile before are
+              // done, S of this one came behind them; those of its first half end first.
+              if (h && !mbar_wait(&bar.pv_half[w], (ns - 1) & 1)) ok = false;
+              __syncwarp();
+              tc_fence_after();
+#pragma unroll 1
+              for (int i = 0; i < HD; i += 32) {
+                float o[32];
+                tmem_ld32_async(to + i, o);
+                tmem_wait_ld();
+                tmem_landed(o);
+#pragma unroll
+                for (int k = 0; k < 32; ++k) o[k] *= f;
+                tmem_st32_async(to + i, reinterpret_cast<const uint32_t *>(o));
+              }
             }
           }
+          sum += part;
+          // p over S, high parts (and low parts) of 64 entries in 32 columns each
+          tmem_st32_async(ts + 64 * h, p);
+          if constexpr (SPLIT) tmem_st32_async(ts + 64 * h + 32, low);
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar.p_ready[w][h]);
         }
-        const float ref = m == -INFINITY ? 0.f : m;   // nothing seen yet: every p is 2^-inf
-        const float2 c2 = make_float2(c, c), r2 = make_float2(-ref, -ref);
-        float2 acc[4] = {};
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          uint32_t p[32];
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            float2 x = make_float2(s[64 * half + 2 * i], s[64 * half + 2 * i + 1]);
-            x = ffma2(x, c2, r2);
-            x.x = exp2_approx(x.x);
-            x.y = exp2_approx(x.y);
-            acc[i & 3] = fadd2(acc[i & 3], x);
-            p[i] = pack_bf16(x.x, x.y);
-            if (SPLIT) {
-              s[64 * half + 2 * i] = x.x - bf16lo(p[i]);
-              s[64 * half + 2 * i + 1] = x.y - bf16hi(p[i]);
-            }
-          }
-          tmem_st32_async(ts + 32 * half, p);
-          if (SPLIT) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) p[i] = pack_bf16(s[64 * half + 2 * i], s[64 * half + 2 * i + 1]);
-            tmem_st32_async(ts + 64 + 32 * half, p);
-          }
-        }
-        acc[0] = fadd2(fadd2(acc[0], acc[1]), fadd2(acc[2], acc[3]));
-        sum += acc[0].x + acc[0].y;
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bar.p_ready[w]);
       }
       if (!ok) break;
       PkvItem nx;
