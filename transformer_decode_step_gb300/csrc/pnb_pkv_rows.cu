@@ -466,13 +466,13 @@ __global__ void __launch_bounds__(kThreads, 1)
               if ((unsigned)(i - from) >= (unsigned)n) x[i] = -INFINITY;
           }
           // No maximum is taken while the reference does: p and its sum tell when it does not,
-          // and fp32 and bf16 hold a p far above 1 as well as one below.
-          uint32_t p[32], low[SPLIT ? 32 : 1];
-          float part = 0.f;
-          for (int again = 0;; ++again) {
+          // and fp32 and bf16 hold a p far above 1 as well as one below.  p goes over S, high
+          // parts (and low parts) of 64 entries in 32 columns each.
+          auto exponentials = [&]() {
             const float ref = m == -INFINITY ? 0.f : m;   // nothing seen yet: every p is 2^-inf
             const float2 c2 = make_float2(c, c), r2 = make_float2(-ref, -ref);
             float2 acc[2] = {};
+            uint32_t p[32], low[SPLIT ? 32 : 1];
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
               float2 y = ffma2(make_float2(x[2 * i], x[2 * i + 1]), c2, r2);
@@ -482,9 +482,13 @@ __global__ void __launch_bounds__(kThreads, 1)
               p[i] = pack_bf16(y.x, y.y);
               if constexpr (SPLIT) low[i] = pack_bf16(y.x - bf16lo(p[i]), y.y - bf16hi(p[i]));
             }
+            tmem_st32_async(ts + 64 * h, p);
+            if constexpr (SPLIT) tmem_st32_async(ts + 64 * h + 32, low);
             acc[0] = fadd2(acc[0], acc[1]);
-            part = acc[0].x + acc[0].y;
-            if (again || !__any_sync(0xffffffffu, m == -INFINITY || !(part < kLarge))) break;
+            return acc[0].x + acc[0].y;
+          };
+          float part = exponentials();
+          if (__any_sync(0xffffffffu, m == -INFINITY || !(part < kLarge))) {
             float mx[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
             for (int i = 4; i < 64; i += 4)
@@ -492,32 +496,31 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int k = 0; k < 4; ++k) mx[k] = fmaxf(mx[k], x[i + k]);
             const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
             const bool move = top > m && (m == -INFINITY || !(part < kLarge));
-            if (!__any_sync(0xffffffffu, move)) break;
-            const float f = move ? (m == -INFINITY ? 0.f : exp2_approx(m - top)) : 1.f;
-            if (move) m = top;
-            sum *= f;
-            if (t > it.ta || h) {
-              // Outputs so far go to the new reference.  The products of the tile before are
-              // done, S of this one came behind them; those of its first half end first.
-              if (h && !mbar_wait(&bar.pv_half[w], (ns - 1) & 1)) ok = false;
-              __syncwarp();
-              tc_fence_after();
+            if (__any_sync(0xffffffffu, move)) {
+              const float f = move ? (m == -INFINITY ? 0.f : exp2_approx(m - top)) : 1.f;
+              if (move) m = top;
+              sum *= f;
+              if (t > it.ta || h) {
+                // Outputs so far go to the new reference.  The products of the tile before are
+                // done, S of this one came behind them; those of its first half end first.
+                if (h && !mbar_wait(&bar.pv_half[w], (ns - 1) & 1)) ok = false;
+                __syncwarp();
+                tc_fence_after();
 #pragma unroll 1
-              for (int i = 0; i < HD; i += 32) {
-                float o[32];
-                tmem_ld32_async(to + i, o);
-                tmem_wait_ld();
-                tmem_landed(o);
+                for (int i = 0; i < HD; i += 32) {
+                  float o[32];
+                  tmem_ld32_async(to + i, o);
+                  tmem_wait_ld();
+                  tmem_landed(o);
 #pragma unroll
-                for (int k = 0; k < 32; ++k) o[k] *= f;
-                tmem_st32_async(to + i, reinterpret_cast<const uint32_t *>(o));
+                  for (int k = 0; k < 32; ++k) o[k] *= f;
+                  tmem_st32_async(to + i, reinterpret_cast<const uint32_t *>(o));
+                }
               }
+              part = exponentials();
             }
           }
           sum += part;
-          // p over S, high parts (and low parts) of 64 entries in 32 columns each
-          tmem_st32_async(ts + 64 * h, p);
-          if constexpr (SPLIT) tmem_st32_async(ts + 64 * h + 32, low);
           tmem_wait_st();
           tc_fence_before();
           __syncwarp();
