@@ -49,7 +49,7 @@ struct PkvAppendArgs {
 // attended together: the tokens of one sequence, or, over a shared prefix, those
 // of all the sequences of a group.  A block is up to kPkvBlockRows such rows, an
 // item a block with its tiles of kPkvTile entries; the flat list of all items'
-// tiles (and kPkvItemUnits more per item, for its queries and its end) is cut into
+// tiles (and a few units more per item, for its queries and its end) is cut into
 // equal runs, one per CTA.  What a run holds of an item that others share goes to
 // the run's partial sums, which a second kernel adds up in the list's order.
 constexpr int kPkvBoxLog2 = 6;          // rows of a TMA box: a page's, at most 64
@@ -58,7 +58,6 @@ constexpr int kPkvBoxLog2 = 6;          // rows of a TMA box: a page's, at most 
 enum { kPkvAll = 0, kPkvPrefix = 1, kPkvOwn = 2 };
 constexpr int kPkvTile = 128;
 constexpr int kPkvBlockRows = 256;
-constexpr int kPkvItemUnits = 2;
 
 // what a CTA left of an item that others share
 struct PkvPart {
@@ -88,6 +87,7 @@ struct PkvAttnArgs {
   float *part_o, *part_ml;              // [2 grid][kPkvBlockRows][head_dim], [..][2]
   PkvPart *part;                        // [2 grid]
   int32_t grid;
+  int32_t item_units;                   // what an item costs beside its tiles, in tiles (set by the launchers)
 };
 
 cudaError_t prepare_pkv_rows(int hd);

@@ -7,7 +7,6 @@
 namespace pnb {
 
 constexpr int kPkvMinRun = 4;      // units that a CTA starts for
-
 struct PkvItem {
   int b, j, h;              // sequence or group, block, KV head
   int tok0, ntok;           // its tokens
@@ -88,11 +87,11 @@ struct PkvWalk {
         }
         continue;
       }
-      const int units = it.nt + kPkvItemUnits;
+      const int units = it.nt + a.item_units;
       const int end = (int)min((int64_t)units, x + left);
       it.h = h;
-      it.ta = max(0, x - kPkvItemUnits);
-      it.tb = max(0, end - kPkvItemUnits);
+      it.ta = max(0, x - a.item_units);
+      it.tb = max(0, end - a.item_units);
       it.ends = end == units;
       left -= end - x;
       x = end;
@@ -183,7 +182,7 @@ __device__ __forceinline__ void pkv_find_run(const PkvAttnArgs &a, int TB, int *
         ++b;
         j = 0;
       }
-      if (!f(b, j, it.nt + kPkvItemUnits)) return;
+      if (!f(b, j, it.nt + a.item_units)) return;
       ++j;
     }
   };

@@ -375,7 +375,9 @@ cudaError_t prepare_pkv_step(int hd) {
   return hd == 128 ? prepare<128, 2>() : prepare<64, 2>();
 }
 
-cudaError_t launch_pkv_step(int hd, const CUtensorMap &map, const PkvAttnArgs &a, cudaStream_t st) {
+cudaError_t launch_pkv_step(int hd, const CUtensorMap &map, const PkvAttnArgs &args, cudaStream_t st) {
+  PkvAttnArgs a = args;
+  a.item_units = 4;
   const int rows = a.seqs.each * (a.n_head / a.pool.n_kv);
   cudaError_t e;
   if (hd == 128) e = rows <= 8 ? launch_step<128, 1>(map, a, st) : launch_step<128, 2>(map, a, st);
