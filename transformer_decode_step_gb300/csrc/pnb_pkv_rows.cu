@@ -69,7 +69,6 @@ struct RL {
 struct RBars {
   uint64_t full[16], empty[16], q_ready[2], s_full[2], p_ready[2][2], pv_half[2], o_full[2], v_go, v_ok, drain;
   uint32_t tmem, pad;
-  PkvWalk walk;
 };
 static_assert(sizeof(RBars) <= 1024, "barriers");
 
@@ -110,11 +109,10 @@ __device__ __noinline__ bool hidden_odd_values(const PkvAttnArgs &a, const PkvIt
   const int seq = a.pass == kPkvPrefix ? min(max(a.group_start[it.b], 0), a.seqs.n_seq - 1) : it.b;
   const int32_t *pages = a.seqs.pages + (int64_t)seq * a.seqs.max_page;
   const int first = it.t0 * kPkvTile, end = (it.t0 + it.nt) * kPkvTile;
-  const int lim = a.pass == kPkvPrefix ? it.hi : it.len;
   bool bad = false;
   for (int part = 0; part < 2; ++part) {
     const int from = part ? max(it.hi_min, first) : first;
-    const int to = min(part ? end : min(it.lo_max, end), lim);
+    const int to = min(part ? end : min(it.lo_max, end), it.len);
     for (int e = max(from, 0); e < to; ++e) {
       const __nv_bfloat16 *v = pkv_row<HD>(a.pool, pages, e, 1, it.h);
       float x[HD / 32] = {};
@@ -155,7 +153,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&bar.v_ok, 64);
     mbar_init(&bar.drain, 1);
     fence_barrier_init();
-    bar.walk = PkvWalk{0, 0, 0, 0, 0, 1};
   }
   if (warp == 9) {
     tmem_alloc(&bar.tmem, 512);
@@ -168,8 +165,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_trigger();
   if (threadIdx.x < 2) a.part[2 * blockIdx.x + threadIdx.x].flags = 0;
   if (a.pass == kPkvPrefix) pkv_find_groups<kThreads>(a, reinterpret_cast<int *>(ring));
-  pkv_find_run<kPkvTile, kThreads>(a, TB, reinterpret_cast<int *>(ring), &bar.walk);
-  PkvWalk walk = bar.walk;
+  PkvWalk walk = pkv_find_run<kPkvTile, kThreads>(a, TB, reinterpret_cast<long long *>(ring));
   PkvItem it;
   const uint32_t tmem = bar.tmem;
   // the ring held the schedule's sums: order them before the tiles that TMA writes
@@ -242,8 +238,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       while (ok && __all_sync(0xffffffffu, walk.next<kPkvTile>(a, TB, it))) {
         const int halves = __shfl_sync(0xffffffffu, it.ntok * G > 128 ? 2 : 1, 0);
         const int tiles = __shfl_sync(0xffffffffu, it.tb - it.ta, 0);
-        // tiles from this one on reach past the sequence's last entry
-        const int past = __shfl_sync(0xffffffffu, it.len / kPkvTile - it.t0 - it.ta, 0);
+        // tiles from this one on reach behind the sequence's last entry (a prefix is whole pages, and
+        // what lies behind in its last tile reads as zero)
+        const int past = __shfl_sync(0xffffffffu, a.pass == kPkvPrefix ? INT_MAX : it.len / kPkvTile - it.t0 - it.ta, 0);
         ok = wait(&bar.full[at.s], at.turn);
 #pragma unroll
         for (int w = 0; w < 2; ++w) {
@@ -318,7 +315,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int t = it.ta; t < it.tb && ok; ++t, at.next()) {
           at.next();   // K, then V
           const int e0 = (it.t0 + t) * kPkvTile;
-          if (it.t0 + t < it.len / kPkvTile) continue;
+          if (it.t0 + t < it.len / kPkvTile || a.pass == kPkvPrefix) continue;
           const int s = at.s;
           // (the ring's own barriers would not do: this warp skips tiles, and the ring
           // may be a whole turn ahead or behind)
@@ -377,7 +374,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int k = 0; k < QR; ++k) put(k, qh[k], 0);
       } else {
         const int last = x.ntok * G - 1;
-        constexpr int B = 4;
+        constexpr int B = QR < 8 ? QR : 8;
 #pragma unroll 1
         for (int k = 0; k < QR; k += B) {
           uint4 hi[B], lo[B];
@@ -688,8 +685,9 @@ __global__ void __launch_bounds__(256) k_pkv_join(const PkvAttnArgs a) {
   const PkvPart p = a.part[2 * c0 + 1];
   if (!(p.flags & 1)) return;
   const int G = a.n_head / a.pool.n_kv, TB = kPkvBlockRows / G;
+  const PkvSeq seq = pkv_seq(a, p.b);
   PkvItem it;
-  if (!pkv_block<kPkvTile>(a, TB, p.b, p.j, it)) return;
+  pkv_block<kPkvTile>(a, seq, TB, p.b, p.j, it);
   const int rows = it.ntok * G, r0 = (blockIdx.y * 8 + (threadIdx.x >> 5)) * R;
   // the run that ends the item
   if (threadIdx.x == 0) s_last = a.grid - 1;
@@ -730,18 +728,25 @@ __global__ void __launch_bounds__(256) k_pkv_join(const PkvAttnArgs a) {
       }
     }
     const uint32_t which = __ballot_sync(0xffffffffu, has);
-#pragma unroll 4
-    for (int j = 0; j < 32; ++j) {
-      if (!(which >> j & 1)) continue;
-      const int kk = k0 + j;
-      const float *src = a.part_o + ((int64_t)(kk == c0 ? 2 * kk + 1 : 2 * kk) * kPkvBlockRows + r0) * HD + lane * N;
+    // four parts' rows on their way together
+    for (int j = 0; j <= last - k0 && j < 32; j += 4) {
+      float x[4][R][N];
 #pragma unroll
-      for (int i = 0; i < R; ++i) {
-        float x[N] = {};
-        if (r0 + i < rows) load_vals<float, N>(src + i * HD, x);
-        const float fj = __shfl_sync(0xffffffffu, f[i], j);
+      for (int u = 0; u < 4; ++u) {
+        const int kk = min(k0 + j + u, last), from = kk == c0 ? 2 * kk + 1 : 2 * kk;
+        const float *src = a.part_o + ((int64_t)from * kPkvBlockRows + r0) * HD + lane * N;
 #pragma unroll
-        for (int n = 0; n < N; ++n) o[i][n] += fj * x[n];
+        for (int i = 0; i < R; ++i) load_vals<float, N>(src + i * HD, x[u][i]);
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        if (j + u > 31 || !(which >> (j + u) & 1)) continue;
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+          const float fj = __shfl_sync(0xffffffffu, f[i], j + u);
+#pragma unroll
+          for (int n = 0; n < N; ++n) o[i][n] += fj * x[u][i][n];
+        }
       }
     }
   }

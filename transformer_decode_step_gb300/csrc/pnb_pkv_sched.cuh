@@ -1,5 +1,10 @@
 // pnb_pkv_sched.cuh - the list of work of the paged cache's attention kernels: blocks of
 // rows, their tiles of entries, and each CTA's run through them.
+//
+// The list holds, sequence by sequence (or group by group), the blocks in order, and each
+// block once per KV head.  A block's units are its tiles and what its start and end cost;
+// a sequence's units have a closed form, so that a CTA finds its run with one load per
+// sequence, a prefix sum over the sequences, and a search within one of them.
 #pragma once
 
 #include "pnb_pkv.cuh"
@@ -7,86 +12,156 @@
 namespace pnb {
 
 constexpr int kPkvMinRun = 4;      // units that a CTA starts for
+
+// a sequence, or in the prefix's pass a group
+struct PkvSeq {
+  int t0, n;                // its tokens
+  int len;                  // its entries (the prefix's whole pages)
+  int floor;                // entries below are the prefix's, another pass's
+  int lo, lo_max;           // prefix: entries that some row, and that every row sees, start here
+};
+
 struct PkvItem {
   int b, j, h;              // sequence or group, block, KV head
   int tok0, ntok;           // its tokens
-  int base;                 // first token's last entry (prompts)
+  int base;                 // first token's last entry (not the prefix's pass)
   int hi, lo;               // entries [lo, hi): those that some row sees
   int hi_min, lo_max;       // entries [lo_max, hi_min): those that every row sees
-  int len;                  // the sequence's entries (the prefix's)
-  int floor;                // entries below are the prefix's, another pass's
+  int len, floor;           // of its sequence
   int t0, nt;               // tiles of the whole item
   int ta, tb;               // this CTA's tiles
   bool ends;                // the item's end is this CTA's
 };
 
-// tokens of a sequence, or of a group's sequences in the prefix's pass
-__device__ __forceinline__ void pkv_members(const PkvAttnArgs &a, int b, int &t0, int &n) {
+__device__ __forceinline__ PkvSeq pkv_seq(const PkvAttnArgs &a, int b) {
+  PkvSeq s{};
+  const int W = a.window;
   if (a.pass == kPkvPrefix) {
     const int gs = min(max(a.group_start[b], 0), a.seqs.n_seq), ge = min(max(a.group_start[b + 1], gs), a.seqs.n_seq);
-    t0 = gs * a.seqs.each;
-    n = (ge - gs) * a.seqs.each;
-  } else {
-    pkv_tokens(a.seqs, b, t0, n);
-  }
-}
-
-// the j-th block of a sequence or group; false behind the last one
-template <int TILE>
-__device__ __forceinline__ bool pkv_block(const PkvAttnArgs &a, int TB, int b, int j, PkvItem &it) {
-  int t0, n;
-  pkv_members(a, b, t0, n);
-  if (j * TB >= n) return false;
-  it.b = b;
-  it.j = j;
-  it.tok0 = t0 + j * TB;
-  it.ntok = min(TB, n - j * TB);
-  const int W = a.window;
-  it.floor = 0;
-  if (a.pass == kPkvPrefix) {
+    s.t0 = gs * a.seqs.each;
+    s.n = (ge - gs) * a.seqs.each;
     const PkvGroup g = a.groups[b];
-    it.base = 0;
-    it.len = INT_MAX;   // (a shared prefix is whole pages, all of them entries)
-    it.hi = it.hi_min = g.prefix;
-    it.lo = W > 0 ? min(max(0, g.len_min - a.seqs.each - W + 1), g.prefix) : 0;
-    it.lo_max = W > 0 ? max(0, g.len_max - W) : 0;
+    s.len = g.prefix;
+    s.lo = W > 0 ? min(max(0, g.len_min - a.seqs.each - W + 1), g.prefix) : 0;
+    s.lo_max = W > 0 ? max(0, g.len_max - W) : 0;
   } else {
-    it.len = pkv_len(a.seqs, a.pool.page_log2, b, a.err);
-    it.base = it.len - n + j * TB;
-    it.hi = max(0, it.base + it.ntok);
-    it.hi_min = it.base + 1;
-    it.lo = W > 0 ? max(0, it.base - W + 1) : 0;
-    it.lo_max = W > 0 ? max(0, it.base + it.ntok - W) : 0;
+    pkv_tokens(a.seqs, b, s.t0, s.n);
+    s.len = pkv_len(a.seqs, a.pool.page_log2, b, a.err);
     if (a.pass == kPkvOwn) {
       const int g = pkv_group_of(a.group_start, a.n_group, b);
-      const int p = g < 0 ? 0 : a.groups[g].prefix;
-      it.lo = min(max(it.lo, p), it.hi);
-      it.lo_max = max(it.lo_max, p);
-      it.floor = p;
+      s.floor = g < 0 ? 0 : min(a.groups[g].prefix, max(s.len - s.n, 0));
     }
+  }
+  return s;
+}
+
+// a sequence's j-th block (j * TB < n)
+template <int TILE>
+__device__ __forceinline__ void pkv_block(const PkvAttnArgs &a, const PkvSeq &s, int TB, int b, int j, PkvItem &it) {
+  const int W = a.window;
+  it.b = b;
+  it.j = j;
+  it.tok0 = s.t0 + j * TB;
+  it.ntok = min(TB, s.n - j * TB);
+  it.len = s.len;
+  it.floor = s.floor;
+  if (a.pass == kPkvPrefix) {
+    it.base = 0;
+    it.hi = it.hi_min = s.len;
+    it.lo = s.lo;
+    it.lo_max = s.lo_max;
+  } else {
+    it.base = s.len - s.n + j * TB;
+    it.hi = max(0, it.base + it.ntok);
+    it.hi_min = it.base + 1;
+    it.lo = max(s.floor, W > 0 ? it.base - W + 1 : 0);
+    it.lo_max = max(s.floor, W > 0 ? it.base + it.ntok - W : 0);
   }
   it.t0 = it.lo / TILE;
   it.nt = max(1, (it.hi + TILE - 1) / TILE - it.t0);
-  return true;
+}
+
+// sum of floor((a i + b) / m) for i = 0 .. n - 1 (the steps of Euclid's algorithm on a and
+// m); a n + b below 2^32 once a and b are below m
+__device__ __forceinline__ long long floor_sum(uint32_t n, uint32_t m, uint32_t a, uint32_t b) {
+  unsigned long long sum = 0;
+  while (n > 0) {
+    if (a >= m) {
+      sum += (unsigned long long)n * (n - 1) / 2 * (a / m);
+      a %= m;
+    }
+    if (b >= m) {
+      sum += (unsigned long long)n * (b / m);
+      b %= m;
+    }
+    const uint32_t y = a * n + b;
+    if (y < m) break;
+    n = y / m;
+    b = y % m;
+    const uint32_t t = m;
+    m = a;
+    a = t;
+  }
+  return (long long)sum;
+}
+
+__device__ __forceinline__ int pkv_blocks(const PkvSeq &s, int TB) { return (s.n + TB - 1) / TB; }
+
+// units of a sequence's first J blocks, per KV head
+template <int TILE>
+__device__ __forceinline__ long long pkv_units(const PkvAttnArgs &a, const PkvSeq &s, int TB, int J) {
+  if (J <= 0) return 0;
+  PkvItem it;
+  if (a.pass == kPkvPrefix) {
+    pkv_block<TILE>(a, s, TB, 0, 0, it);
+    return (long long)J * (it.nt + a.item_units);
+  }
+  // the last block may have fewer tokens
+  long long sum = 0;
+  int K = J;
+  if (J == pkv_blocks(s, TB)) {
+    pkv_block<TILE>(a, s, TB, 0, J - 1, it);
+    sum = it.nt;
+    --K;
+  }
+  if (K > 0) {
+    const int base = s.len - s.n;
+    // blocks z .. K - 1 end behind entry base + (j + 1) TB; those before see nothing: a tile each
+    const int z = base < 0 ? min(K, -base / TB) : 0;
+    sum += z;
+    if (K > z) sum += floor_sum(K - z, TILE, TB, base + (z + 1) * TB + TILE - 1);
+    // first entries: the floor, and from block y on the window's
+    int y = K;
+    if (a.window > 0) {
+      const int d = s.floor + a.window - 1 - base;   // base + j TB - window + 1 > floor
+      y = d < 0 ? z : min(K, max(z, d / TB + 1));
+    }
+    sum -= (long long)(y - z) * (s.floor / TILE);
+    if (K > y) sum -= floor_sum(K - y, TILE, TB, base + y * TB - a.window + 1);
+  }
+  return sum + (long long)J * a.item_units;
 }
 
 // a CTA's way through its run of units
 struct PkvWalk {
-  int h, b, j, x;       // next item, units of it that lie before the run
-  int64_t left;         // units
+  int b, j, h, x;       // next item, units of it that lie before the run
   int n_b;              // sequences or groups
+  int64_t left;         // units
+  PkvSeq seq;           // sequence b
 
   template <int TILE>
   __device__ __forceinline__ bool next(const PkvAttnArgs &a, int TB, PkvItem &it) {
-    while (left > 0 && h < a.pool.n_kv) {
-      if (!pkv_block<TILE>(a, TB, b, j, it)) {
-        j = 0;
-        if (++b == n_b) {
-          b = 0;
-          ++h;
-        }
-        continue;
+    while (left > 0) {
+      if (h == a.pool.n_kv) {
+        h = 0;
+        ++j;
       }
+      while (j * TB >= seq.n) {
+        if (++b >= n_b) return false;
+        j = 0;
+        seq = pkv_seq(a, b);
+      }
+      pkv_block<TILE>(a, seq, TB, b, j, it);
       const int units = it.nt + a.item_units;
       const int end = (int)min((int64_t)units, x + left);
       it.h = h;
@@ -96,7 +171,7 @@ struct PkvWalk {
       left -= end - x;
       x = end;
       if (it.ends) {
-        ++j;
+        ++h;
         x = 0;
       }
       if (it.tb > it.ta) return true;
@@ -116,12 +191,12 @@ __device__ __forceinline__ void pkv_find_groups(const PkvAttnArgs &a, int *scrat
   }
   __syncthreads();
   for (int s = threadIdx.x; s < a.seqs.n_seq; s += THREADS) {
+    const int n = pkv_len(a.seqs, a.pool.page_log2, s, a.err);
     const int g = pkv_group_of(a.group_start, a.n_group, s);
     if (g < 0) {
       set_error(a.err, kErrRange);
       continue;
     }
-    const int n = pkv_len(a.seqs, a.pool.page_log2, s, a.err);
     atomicMin(&gmin[g], n);
     atomicMax(&gmax[g], n);
   }
@@ -133,103 +208,79 @@ __device__ __forceinline__ void pkv_find_groups(const PkvAttnArgs &a, int *scrat
   __syncthreads();
 }
 
-// Where this CTA's run starts.  The blocks of one KV head are counted and their
-// units added up by all threads; heads follow one another in the list.
+// Where this CTA's run starts (every warp answers for itself).  scratch: 64 numbers.
 template <int TILE, int THREADS>
-__device__ __forceinline__ void pkv_find_run(const PkvAttnArgs &a, int TB, int *scratch, PkvWalk *out) {
-  const int n_b = a.pass == kPkvPrefix ? a.n_group : a.seqs.n_seq, tid = threadIdx.x, lane = tid & 31;
-  int *first = scratch;                                             // [n_b + 1] blocks before a sequence
-  long long *sums = reinterpret_cast<long long *>(scratch + 1026);   // [THREADS + 1]
-  for (int b = tid; b < n_b; b += THREADS) {
-    int t0, n;
-    pkv_members(a, b, t0, n);
-    first[b + 1] = (n + TB - 1) / TB;
-  }
-  if (tid == 0) first[0] = 0;
-  __syncthreads();
-  if (tid < 32) {
-    int base = 0;
-    for (int b0 = 1; b0 <= n_b; b0 += 32) {
-      int v = b0 + lane <= n_b ? first[b0 + lane] : 0;
+__device__ __forceinline__ PkvWalk pkv_find_run(const PkvAttnArgs &a, int TB, long long *scratch) {
+  constexpr int WARPS = THREADS / 32, PASSES = (kPkvMaxSeq + THREADS - 1) / THREADS;
+  static_assert(WARPS <= 32, "warps");
+  const int n_b = a.pass == kPkvPrefix ? a.n_group : a.seqs.n_seq;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  long long before[PASSES], units[PASSES], total = 0;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int u = __shfl_up_sync(0xffffffffu, v, o);
-        if (lane >= o) v += u;
-      }
-      if (b0 + lane <= n_b) first[b0 + lane] = base + v;
-      base += __shfl_sync(0xffffffffu, v, 31);
+  for (int k = 0; k < PASSES; ++k) {
+    before[k] = units[k] = 0;
+    if (k * THREADS >= n_b) continue;   // (the same for all threads)
+    const int b = k * THREADS + tid;
+    if (b < n_b) {
+      const PkvSeq s = pkv_seq(a, b);
+      units[k] = pkv_units<TILE>(a, s, TB, pkv_blocks(s, TB));
     }
-  }
-  __syncthreads();
-  const int blocks = first[n_b];
-  const int i0 = (int)((int64_t)blocks * tid / THREADS), i1 = (int)((int64_t)blocks * (tid + 1) / THREADS);
-  // the sequence of block i0: the last one that starts at or before it
-  int b0 = 0;
-  if (i0 < i1) {
-    int lo = 0, hi = n_b;   // first[lo] <= i0 < first[hi]
-    while (hi - lo > 1) {
-      const int m = (lo + hi) >> 1;
-      if (first[m] <= i0) lo = m;
-      else hi = m;
-    }
-    b0 = lo;
-  }
-  auto walk = [&](auto &&f) {
-    int b = b0, j = i0 - first[b0];
-    for (int i = i0; i < i1; ++i) {
-      PkvItem it;
-      while (!pkv_block<TILE>(a, TB, b, j, it)) {
-        ++b;
-        j = 0;
-      }
-      if (!f(b, j, it.nt + a.item_units)) return;
-      ++j;
-    }
-  };
-  long long mine = 0;
-  walk([&](int, int, int u) {
-    mine += u;
-    return true;
-  });
-  sums[tid + 1] = mine;
-  if (tid == 0) sums[0] = 0;
-  __syncthreads();
-  if (tid < 32) {
-    long long base = 0;
-    for (int k0 = 1; k0 <= THREADS; k0 += 32) {
-      long long v = sums[k0 + lane];
+    long long v = units[k];
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long u = __shfl_up_sync(0xffffffffu, v, o);
-        if (lane >= o) v += u;
-      }
-      sums[k0 + lane] = base + v;
-      base += __shfl_sync(0xffffffffu, v, 31);
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long u = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += u;
     }
+    __syncthreads();
+    if (lane == 31) scratch[warp] = v;
+    __syncthreads();
+    long long w = lane < WARPS ? scratch[lane] : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long u = __shfl_up_sync(0xffffffffu, w, o);
+      if (lane >= o) w += u;
+    }
+    const long long all = __shfl_sync(0xffffffffu, w, 31);
+    const long long warps_before = warp ? __shfl_sync(0xffffffffu, w, warp - 1) : 0;
+    before[k] = total + warps_before + v - units[k];
+    total += all;
   }
-  __syncthreads();
-  const long long per_head = sums[THREADS], total = per_head * a.pool.n_kv;
   // as many CTAs as get a run of a few units each
-  const long long ctas = max(1ll, min((long long)gridDim.x, total / kPkvMinRun));
-  const long long c = min((long long)blockIdx.x, ctas), u0 = total * c / ctas, u1 = total * min(c + 1, ctas) / ctas;
-  if (u1 <= u0) {
-    if (tid == 0) *out = PkvWalk{0, 0, 0, 0, 0, n_b};
-  } else {
-    const int h = (int)(u0 / per_head);
-    const long long in_head = u0 - h * per_head;
-    if (in_head >= sums[tid] && in_head < sums[tid + 1]) {
-      long long at = sums[tid];
-      walk([&](int b, int j, int u) {
-        if (in_head >= at + u) {
-          at += u;
-          return true;
-        }
-        *out = PkvWalk{h, b, j, (int)(in_head - at), u1 - u0, n_b};
-        return false;
-      });
+  const int n_kv = a.pool.n_kv;
+  const long long list = total * n_kv, ctas = max(1ll, min((long long)gridDim.x, list / kPkvMinRun));
+  const long long c = min((long long)blockIdx.x, ctas), u0 = list * c / ctas, u1 = list * min(c + 1, ctas) / ctas;
+  PkvWalk r{};
+  r.n_b = n_b;
+  if (u1 <= u0) return r;
+  const long long at = u0 / n_kv;   // in units of one KV head: which sequence, which block
+#pragma unroll
+  for (int k = 0; k < PASSES; ++k)
+    if (at >= before[k] && at < before[k] + units[k]) {
+      scratch[40] = k * THREADS + tid;
+      scratch[41] = before[k];
     }
-  }
   __syncthreads();
+  r.b = (int)scratch[40];
+  r.seq = pkv_seq(a, r.b);
+  const long long in_seq = at - scratch[41];
+  // the last block j with units(j) <= in_seq: 32 candidates at a time
+  int lo = 0, hi = pkv_blocks(r.seq, TB);
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 31) / 32, j = lo + lane * step;
+    const bool in = j < hi && pkv_units<TILE>(a, r.seq, TB, j) <= in_seq;
+    const int k = 31 - __clz(__ballot_sync(0xffffffffu, in));
+    lo += k * step;
+    hi = min(hi, lo + step);
+  }
+  r.j = lo;
+  PkvItem it;
+  pkv_block<TILE>(a, r.seq, TB, r.b, lo, it);
+  // units of the block before the run, over its KV heads
+  const long long rest = u0 - (scratch[41] + pkv_units<TILE>(a, r.seq, TB, lo)) * n_kv;
+  r.h = (int)(rest / (it.nt + a.item_units));
+  r.x = (int)(rest % (it.nt + a.item_units));
+  r.left = u1 - u0;
+  return r;
 }
 
 }  // namespace pnb

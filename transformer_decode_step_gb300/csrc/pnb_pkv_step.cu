@@ -44,7 +44,6 @@ struct SL {
 
 struct SBars {
   uint64_t full[8], empty[8];
-  PkvWalk walk;
   float2 ml[kWarps][16];
   int bad;
 };
@@ -101,15 +100,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&bar.empty[i], kWarps / 2);
     }
     fence_barrier_init();
-    bar.walk = PkvWalk{0, 0, 0, 0, 0, 1};
     bar.bad = 0;
   }
   __syncthreads();
   pdl_wait();
   pdl_trigger();
   if (threadIdx.x < 2) a.part[2 * blockIdx.x + threadIdx.x].flags = 0;
-  pkv_find_run<kChunk, kThreads>(a, a.seqs.each, reinterpret_cast<int *>(ring), &bar.walk);
-  PkvWalk walk = bar.walk;
+  PkvWalk walk = pkv_find_run<kChunk, kThreads>(a, a.seqs.each, reinterpret_cast<long long *>(ring));
   PkvItem it;
   fence_async_smem();   // the ring held the schedule's sums
   __syncthreads();
