@@ -87,6 +87,7 @@ struct PkvAttnArgs {
   float *part_o, *part_ml;              // [2 grid][kPkvBlockRows][head_dim], [..][2]
   PkvPart *part;                        // [2 grid]
   int32_t grid;
+  int32_t heads_inner;                  // the list's order (set by the launchers)
   int32_t item_units;                   // what an item costs beside its tiles, in tiles (set by the launchers)
 };
 

@@ -808,6 +808,7 @@ cudaError_t launch_pkv_rows(int hd, const CUtensorMap &map, const PkvAttnArgs &a
   // 1538 us; 16 packed prompts 325, 298, 291, 298; fp32, whose tiles take twice as long, 872, 848,
   // 869, 872.
   a.item_units = split ? 4 : 6;
+  a.heads_inner = a.pass == kPkvAll;
   cudaError_t e;
   if (hd == 128) e = split ? launch_rows<128, true>(map, a, st) : launch_rows<128, false>(map, a, st);
   else e = split ? launch_rows<64, true>(map, a, st) : launch_rows<64, false>(map, a, st);
