@@ -15,69 +15,93 @@ namespace pnb {
 namespace {
 
 constexpr int kWarps = 8;
-constexpr int kUnroll = 4;      // rows on their way per lane group
+constexpr int kMaxPairs = 64;
 
-// 8 elements of a row: 8 l .. 8 l + 7, or, half-split, 4 l .. 4 l + 3 of each half
+// A lane's part of a row: E elements (8 l ..), or, half-split, E / 2 of each half, as 16-byte
+// loads where the type allows: 8 elements, and 16 of bf16 half-split rows.
+template <bool NEOX, typename T>
+constexpr int kElems = NEOX && sizeof(T) == 2 ? 16 : 8;
+
 template <int HD, bool NEOX, typename T>
-__device__ __forceinline__ void load8(const T *p, int l, float (&f)[8]) {
-  if constexpr (NEOX) {
-    load_vals<T, 4>(p + 4 * l, reinterpret_cast<float(&)[4]>(f[0]));
-    load_vals<T, 4>(p + HD / 2 + 4 * l, reinterpret_cast<float(&)[4]>(f[4]));
-  } else if constexpr (sizeof(T) == 2) {
-    load_vals<T, 8>(p + 8 * l, f);
-  } else {
-    load_vals<T, 4>(p + 8 * l, reinterpret_cast<float(&)[4]>(f[0]));
-    load_vals<T, 4>(p + 8 * l + 4, reinterpret_cast<float(&)[4]>(f[4]));
+__device__ __forceinline__ void load_part(const T *p, int l, float (&f)[kElems<NEOX, T>]) {
+  constexpr int E = kElems<NEOX, T>, V = sizeof(T) == 2 ? 8 : 4;   // elements of a 16-byte load
+#pragma unroll
+  for (int i = 0; i < E; i += V) {
+    const T *from = !NEOX ? p + E * l + i : i < E / 2 ? p + E / 2 * l + i : p + HD / 2 + E / 2 * l + i - E / 2;
+    load_vals<T, V>(from, reinterpret_cast<float(&)[V]>(f[i]));
   }
 }
 
-template <int HD, bool NEOX, typename T>
-__device__ __forceinline__ void store8(T *p, int l, const float (&f)[8]) {
-  T *a = NEOX ? p + 4 * l : p + 8 * l, *b = NEOX ? p + HD / 2 + 4 * l : p + 8 * l + 4;
-  if constexpr (sizeof(T) == 4) {
-    *reinterpret_cast<float4 *>(a) = make_float4(f[0], f[1], f[2], f[3]);
-    *reinterpret_cast<float4 *>(b) = make_float4(f[4], f[5], f[6], f[7]);
-  } else if constexpr (NEOX) {
-    *reinterpret_cast<uint2 *>(a) = make_uint2(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]));
-    *reinterpret_cast<uint2 *>(b) = make_uint2(pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
-  } else {
-    *reinterpret_cast<uint4 *>(a) =
-        make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
+// the same part of a row of type T, computed as E elements
+template <int HD, bool NEOX, int E, typename T>
+__device__ __forceinline__ void store_part(T *p, int l, const float (&f)[E]) {
+  constexpr int V = sizeof(T) == 4 ? 4 : NEOX && E == 8 ? 4 : 8;
+#pragma unroll
+  for (int i = 0; i < E; i += V) {
+    T *to = !NEOX ? p + E * l + i : i < E / 2 ? p + E / 2 * l + i : p + HD / 2 + E / 2 * l + i - E / 2;
+    if constexpr (sizeof(T) == 4)
+      *reinterpret_cast<float4 *>(to) = make_float4(f[i], f[i + 1], f[i + 2], f[i + 3]);
+    else if constexpr (V == 4)
+      *reinterpret_cast<uint2 *>(to) = make_uint2(pack_bf16(f[i], f[i + 1]), pack_bf16(f[i + 2], f[i + 3]));
+    else
+      *reinterpret_cast<uint4 *>(to) = make_uint4(pack_bf16(f[i], f[i + 1]), pack_bf16(f[i + 2], f[i + 3]),
+                                                  pack_bf16(f[i + 4], f[i + 5]), pack_bf16(f[i + 6], f[i + 7]));
   }
 }
 
+// a.wpt warps (1, 2, 4 or 8) take a token: they compute its cosines and sines once, in
+// shared memory, while its first rows load
 template <int HD, bool NEOX, typename T, typename TQ>
 __global__ void __launch_bounds__(kWarps * 32) k_pkv_append(const PkvAppendArgs a) {
-  constexpr int LPR = HD / 8, RPW = 32 / LPR;   // lanes per row, rows per warp
+  constexpr int E = kElems<NEOX, T>, LPR = HD / E, RPW = 32 / LPR;   // lanes per row, rows per warp
+  constexpr int U = sizeof(T) == 2 && E == 8 ? 6 : 3;                // rows on their way per lane
+  __shared__ float2 turns[kWarps][kMaxPairs];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int tok = blockIdx.x * (kWarps / a.wpt) + warp / a.wpt;
+  const int tok = blockIdx.x * (kWarps / a.wpt) + warp / a.wpt, rank = warp % a.wpt;
   pdl_wait();
-  if (tok >= a.seqs.n_tok) return;
-  const int b = pkv_seq_of(a.seqs, tok);
-  if (b < 0) return;
-  int t0, n;
-  pkv_tokens(a.seqs, b, t0, n);
-  if (tok < t0 || tok - t0 >= n) {   // `start` decreases
+  const int b = tok < a.seqs.n_tok ? pkv_seq_of(a.seqs, tok) : -1;
+  int t0 = 0, n = 0;
+  if (b >= 0) pkv_tokens(a.seqs, b, t0, n);
+  bool live = b >= 0;
+  if (live && (tok < t0 || tok - t0 >= n)) {   // `start` decreases
     set_error(a.err, kErrRange);
-    return;
+    live = false;
   }
-  const int64_t e64 = (int64_t)a.seqs.len[b] - n + (tok - t0);   // the token's entry
+  const int64_t e64 = live ? (int64_t)a.seqs.len[b] - n + (tok - t0) : 0;   // the token's entry
   const int e = (int)e64;
-  const int l = lane % LPR, sub = lane / LPR, rank = warp % a.wpt;
 
-  float cs[4], sn[4];
+  const int l = lane % LPR, sub = lane / LPR;
+  const int nq = a.q.p ? a.n_head : 0, nkv = a.pool.n_kv, rows = nq + 2 * nkv, step = a.wpt * RPW;
+  const T *q = static_cast<const T *>(a.q.p) + tok * a.q.token;
+  const T *k = static_cast<const T *>(a.k.p) + tok * a.k.token;
+  const T *v = static_cast<const T *>(a.v.p) + tok * a.v.token;
+  float x[U][E];
+  auto load = [&](int r0) {
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int i = 4 * l + j;
-    cs[j] = 1.f;
-    sn[j] = 0.f;
-    if (a.freq) {
+    for (int u = 0; u < U; ++u) {
+      const int r = r0 + u * step;
+      if (r >= rows) break;
+      const T *p = r < nq ? q + r * a.q.head : r < nq + nkv ? k + (r - nq) * a.k.head : v + (r - nq - nkv) * a.v.head;
+      load_part<HD, NEOX, T>(p, l, x[u]);
+    }
+  };
+  int r0 = rank * RPW + sub;
+  if (live) load(r0);
+
+  float2 *mine = turns[warp / a.wpt * a.wpt];
+  if (live && a.freq) {
+    for (int i = rank * 32 + lane; i < HD / 2; i += a.wpt * 32) {
       const int axis = (i >= a.sec0) + (i >= a.sec1);
       const int p = a.pos ? a.pos[(int64_t)axis * a.seqs.n_tok + tok] : e;
       const long long turn = (long long)((unsigned long long)(long long)p * a.freq[i]);
-      sincospif(__ll2float_rn(turn) * 0x1p-63f, &sn[j], &cs[j]);
+      float sn, cs;
+      sincospif(__ll2float_rn(turn) * 0x1p-63f, &sn, &cs);
+      mine[i] = make_float2(cs, sn);
     }
   }
+  if (a.wpt > 1) __syncthreads();
+  else __syncwarp();
+  if (!live) return;
 
   __nv_bfloat16 *page = nullptr;   // the entry's K row of KV head 0
   if (e64 < 0 || e64 >= (int64_t)a.seqs.max_page << a.pool.page_log2) {
@@ -87,39 +111,30 @@ __global__ void __launch_bounds__(kWarps * 32) k_pkv_append(const PkvAppendArgs 
     if (!page && lane == 0 && rank == 0) set_error(a.err, kErrRange);
   }
   const int64_t head_step = (int64_t)HD << a.pool.page_log2;
-
-  const int nq = a.q.p ? a.n_head : 0, nkv = a.pool.n_kv, rows = nq + 2 * nkv;
-  const T *q = static_cast<const T *>(a.q.p) + tok * a.q.token;
-  const T *k = static_cast<const T *>(a.k.p) + tok * a.k.token;
-  const T *v = static_cast<const T *>(a.v.p) + tok * a.v.token;
+  float2 cs[E / 2];
+#pragma unroll
+  for (int j = 0; j < E / 2; ++j) cs[j] = a.freq ? mine[E / 2 * l + j] : make_float2(1.f, 0.f);
   TQ *q_out = static_cast<TQ *>(a.q_out.p) + tok * a.q_out.token;
-  const int step = a.wpt * RPW;
-  for (int r0 = rank * RPW + sub; r0 < rows; r0 += step * kUnroll) {
-    float x[kUnroll][8];
+  while (r0 < rows) {
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int r = r0 + u * step;
-      if (r >= rows) break;
-      const T *p = r < nq ? q + r * a.q.head : r < nq + nkv ? k + (r - nq) * a.k.head : v + (r - nq - nkv) * a.v.head;
-      load8<HD, NEOX>(p, l, x[u]);
-    }
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
+    for (int u = 0; u < U; ++u) {
       const int r = r0 + u * step;
       if (r >= rows) break;
       if (r < nq + nkv && a.freq) {
-        float(&f)[8] = x[u];
+        float(&f)[E] = x[u];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          float &y = f[NEOX ? j : 2 * j], &z = f[NEOX ? 4 + j : 2 * j + 1];
+        for (int j = 0; j < E / 2; ++j) {
+          float &y = f[NEOX ? j : 2 * j], &z = f[NEOX ? E / 2 + j : 2 * j + 1];
           const float y0 = y, z0 = z;
-          y = y0 * cs[j] - z0 * sn[j];
-          z = y0 * sn[j] + z0 * cs[j];
+          y = y0 * cs[j].x - z0 * cs[j].y;
+          z = y0 * cs[j].y + z0 * cs[j].x;
         }
       }
-      if (r < nq) store8<HD, NEOX>(q_out + r * a.q_out.head, l, x[u]);
-      else if (page) store8<HD, NEOX>(page + (r - nq) * head_step, l, x[u]);   // V lies n_kv heads behind K
+      if (r < nq) store_part<HD, NEOX, E, TQ>(q_out + r * a.q_out.head, l, x[u]);
+      else if (page) store_part<HD, NEOX, E, __nv_bfloat16>(page + (r - nq) * head_step, l, x[u]);   // V lies n_kv heads behind K
     }
+    r0 += step * U;
+    if (r0 < rows) load(r0);
   }
 }
 

@@ -27,6 +27,8 @@
 #include <cuda_bf16.h>
 #include <math.h>
 
+#include <type_traits>
+
 #include "pnb_pkv_sched.cuh"
 #include "pnb_tc.cuh"
 
@@ -349,41 +351,40 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int ql = lane % LPR, qsub = lane / LPR;
     uint8_t *const qmine = Q + w * L::QHALF + quad * 4096;   // 4 KB of each box
     uint4 qh[SPLIT ? 1 : QR];
-    auto q_at = [&](const PkvItem &x, int row) {
-      const int q = div_g(row);
-      return (x.tok0 + q) * a.q.token + (x.h * G + row - q * G) * a.q.head + 8 * ql;
-    };
+    // A lane finds its own row's address; the lanes that move the row get it from there.
+    auto of_lane = [&](long long v, int from) { return __shfl_sync(0xffffffffu, v, from); };
     auto put = [&](int k, const uint4 &v, int part) {
       const int row = k * RPW + qsub;
       *reinterpret_cast<uint4 *>(qmine + part * L::UNIT + (ql >> 3) * L::BOX + sw128(row, (ql & 7) * 16)) = v;
     };
+    const bool q32 = a.q.dtype == PNB_F32;
+    long long q_row = 0;
     // bf16 queries of the next item load while this one's outputs are on their way; rows
     // behind the block's last one repeat it, so that all loads are on their way at once
     auto fetch_q = [&](const PkvItem &x) {
+      const int row = min(r, x.ntok * G - 1), q = div_g(row);
+      const int64_t at = (x.tok0 + q) * a.q.token + (x.h * G + row - q * G) * a.q.head;
+      q_row = (long long)(uintptr_t)a.q.p + at * (q32 ? 4 : 2);
       if constexpr (!SPLIT) {
-        const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(a.q.p);
-        const int last = x.ntok * G - 1;
 #pragma unroll
         for (int k = 0; k < QR; ++k)
-          qh[k] = *reinterpret_cast<const uint4 *>(src + q_at(x, min((warp << 5) + k * RPW + qsub, last)));
+          qh[k] = reinterpret_cast<const uint4 *>((uintptr_t)of_lane(q_row, k * RPW + qsub))[ql];
       }
     };
-    auto put_q = [&](const PkvItem &x) {
+    auto put_q = [&]() {
       if constexpr (!SPLIT) {
 #pragma unroll
         for (int k = 0; k < QR; ++k) put(k, qh[k], 0);
       } else {
-        const int last = x.ntok * G - 1;
         constexpr int B = QR < 8 ? QR : 8;
 #pragma unroll 1
         for (int k = 0; k < QR; k += B) {
           uint4 hi[B], lo[B];
-          if (a.q.dtype == PNB_F32) {
+          if (q32) {
             float4 f[B][2];
 #pragma unroll
             for (int i = 0; i < B; ++i) {
-              const float4 *p = reinterpret_cast<const float4 *>(
-                  static_cast<const float *>(a.q.p) + q_at(x, min((warp << 5) + (k + i) * RPW + qsub, last)));
+              const float4 *p = reinterpret_cast<const float4 *>((uintptr_t)of_lane(q_row, (k + i) * RPW + qsub)) + 2 * ql;
               f[i][0] = p[0];
               f[i][1] = p[1];
             }
@@ -392,8 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           } else {
 #pragma unroll
             for (int i = 0; i < B; ++i) {
-              hi[i] = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.q.p) +
-                                                       q_at(x, min((warp << 5) + (k + i) * RPW + qsub, last)));
+              hi[i] = reinterpret_cast<const uint4 *>((uintptr_t)of_lane(q_row, (k + i) * RPW + qsub))[ql];
               lo[i] = make_uint4(0, 0, 0, 0);
             }
           }
@@ -418,7 +418,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool have = next(it);
     if (have) {
       fetch_q(it);
-      put_q(it);
+      put_q();
     }
     while (have && ok) {
       const bool live = r < it.ntok * G;
@@ -547,93 +547,95 @@ __global__ void __launch_bounds__(kThreads, 1)
         all = sum * f_own + ml.y * f_pre;
       }
       const float inv = all == 0.f ? 0.f : 1.f / all;
-      float *po = nullptr, *pml = nullptr, *po_base = nullptr;
-      auto qout = [&](int at) { return qmine + (at >> 12) * L::BOX + (at & 4095); };   // no row crosses 4 KB
+      // where the row goes: the answer, or, unfinished, its sums
+      float *po = nullptr, *pml = nullptr;
       if (!whole) {
         const int64_t at = (int64_t)(2 * blockIdx.x + side) * kPkvBlockRows + r;
         po = a.part_o + at * HD;
-        po_base = a.part_o + (int64_t)(2 * blockIdx.x + side) * kPkvBlockRows * HD;
         pml = a.part_ml + at * 2;
         if (r == 0) a.part[2 * blockIdx.x + side] = PkvPart{it.ends ? 3 : 1, it.b, it.j, it.h};
       } else if (a.pass == kPkvPrefix) {
         const int64_t at = (int64_t)tok * a.n_head + head;
         po = a.row_o + at * HD;
-        po_base = a.row_o;
         pml = a.row_ml + at * 2;
       }
-      // outputs through the warp's part of the Q buffer, so that rows leave in whole lines
-      const bool f32 = po || a.out.dtype == PNB_F32;
-      const int passes = f32 && !SPLIT ? 2 : 1;   // without SPLIT there is room for 16 bits per element
+      const bool out32 = a.out.dtype == PNB_F32;
+      const long long to_row = po ? (long long)(uintptr_t)po
+                                  : (long long)(uintptr_t)a.out.p +
+                                        (tok * a.out.token + head * a.out.head) * (out32 ? 4 : 2);
       bool redo = false, odd = false;
       uint32_t odd_rows = 0;
+      // Outputs go through the warp's part of the Q buffer, so that rows leave in whole lines:
+      // 16-byte pieces of a row, turned by the row so that lanes meet different banks.
+      auto emit = [&](auto wide) {
+        constexpr bool F32 = decltype(wide)::value;
+        constexpr int PASSES = F32 && !SPLIT ? 2 : 1;   // without SPLIT there is room for 16 bits per element
+        constexpr int ROWS = 32 / PASSES, BYTES = F32 ? HD * 4 : HD * 2, PIECES = BYTES / 16, STEP = 32 / PIECES;
+        auto piece = [&](int row, int i, int turn) {
+          const int at = row * BYTES + ((i ^ (turn & 7)) << 4);
+          return reinterpret_cast<uint4 *>(qmine + (at >> 12) * L::BOX + (at & 4095));   // no row crosses 4 KB
+        };
+        const float f = po ? 1.f : inv;   // a row that saw nothing has only zeros summed up
 #pragma unroll 1
-      for (int pass = 0; pass < passes; ++pass) {
-        const int rows_at_once = 32 / passes;
-        const bool mine = lane / rows_at_once == pass;
-        float z = 0.f;   // NaN if an output is not finite
+        for (int pass = 0; pass < PASSES; ++pass) {
+          const bool mine = lane / ROWS == pass;
+          float z = 0.f;   // NaN if an output is not finite
 #pragma unroll 1
-        for (int i = 0; i < HD; i += 32) {
-          float o[32];
-          tmem_ld32_async(to + i, o);
-          tmem_wait_ld();
-          tmem_landed(o);
+          for (int i = 0; i < HD; i += 32) {
+            float o[32];
+            tmem_ld32_async(to + i, o);
+            tmem_wait_ld();
+            tmem_landed(o);
 #pragma unroll
-          for (int k = 0; k < 32; ++k) z = fmaf(o[k], 0.f, z);
-          if (bo && live) {
+            for (int k = 0; k < 32; ++k) z = fmaf(o[k], 0.f, z);
+            if (bo && live) {
 #pragma unroll
-            for (int k = 0; k < 32; k += 4) {
-              const float4 x = *reinterpret_cast<const float4 *>(bo + i + k);
-              o[k] = o[k] * f_own + x.x * f_pre;
-              o[k + 1] = o[k + 1] * f_own + x.y * f_pre;
-              o[k + 2] = o[k + 2] * f_own + x.z * f_pre;
-              o[k + 3] = o[k + 3] * f_own + x.w * f_pre;
+              for (int k = 0; k < 32; k += 4) {
+                const float4 x = *reinterpret_cast<const float4 *>(bo + i + k);
+                o[k] = o[k] * f_own + x.x * f_pre;
+                o[k + 1] = o[k + 1] * f_own + x.y * f_pre;
+                o[k + 2] = o[k + 2] * f_own + x.z * f_pre;
+                o[k + 3] = o[k + 3] * f_own + x.w * f_pre;
+              }
+            }
+            if (mine) {
+              if constexpr (F32) {
+#pragma unroll
+                for (int k = 0; k < 32; k += 4)
+                  *piece(lane % ROWS, (i + k) >> 2, lane) =
+                      make_uint4(__float_as_uint(o[k] * f), __float_as_uint(o[k + 1] * f),
+                                 __float_as_uint(o[k + 2] * f), __float_as_uint(o[k + 3] * f));
+              } else {
+#pragma unroll
+                for (int k = 0; k < 32; k += 8)
+                  *piece(lane, (i + k) >> 3, lane) =
+                      make_uint4(pack_bf16(o[k] * f, o[k + 1] * f), pack_bf16(o[k + 2] * f, o[k + 3] * f),
+                                 pack_bf16(o[k + 4] * f, o[k + 5] * f), pack_bf16(o[k + 6] * f, o[k + 7] * f));
+              }
+            }
+            __syncwarp();
+          }
+          if (pass == 0) {
+            odd = live && z != 0.f;
+            odd_rows = __ballot_sync(0xffffffffu, odd);
+            if (odd_rows) {
+              const PkvItem copy = it;   // (its address is taken)
+              redo = hidden_odd_values<HD>(a, copy);
             }
           }
-          // 16-byte pieces of a row, turned by the row so that lanes meet different banks
-          if (mine) {
-            uint8_t *row = qout((lane % rows_at_once) * (f32 ? HD * 4 : HD * 2));
-            const float f = po ? 1.f : inv;   // a row that saw nothing has only zeros summed up
-            if (f32) {
-#pragma unroll
-              for (int k = 0; k < 32; k += 4)
-                *reinterpret_cast<float4 *>(row + ((((i + k) >> 2) ^ (lane & 7)) << 4)) =
-                    make_float4(o[k] * f, o[k + 1] * f, o[k + 2] * f, o[k + 3] * f);
-            } else {
-#pragma unroll
-              for (int k = 0; k < 32; k += 8)
-                *reinterpret_cast<uint4 *>(row + ((((i + k) >> 3) ^ (lane & 7)) << 4)) =
-                    make_uint4(pack_bf16(o[k] * f, o[k + 1] * f), pack_bf16(o[k + 2] * f, o[k + 3] * f),
-                               pack_bf16(o[k + 4] * f, o[k + 5] * f), pack_bf16(o[k + 6] * f, o[k + 7] * f));
-            }
-          }
-        }
-        if (pass == 0) {
-          odd = live && z != 0.f;
-          odd_rows = __ballot_sync(0xffffffffu, odd);
-          if (odd_rows) {
-            const PkvItem copy = it;   // (its address is taken)
-            redo = hidden_odd_values<HD>(a, copy);
-          }
-        }
-        __syncwarp();
-        const int lpr = f32 ? HD / 4 : HD / 8;   // lanes per row
-        const int l = lane % lpr;
+          const uint32_t store = __ballot_sync(0xffffffffu, live && !(redo && odd));
 #pragma unroll 4
-        for (int k = lane / lpr; k < rows_at_once; k += 32 / lpr) {
-          const int src = pass * rows_at_once + k, row = (warp << 5) + src;
-          const uint4 x = *reinterpret_cast<const uint4 *>(qout(k * (f32 ? HD * 4 : HD * 2)) + ((l ^ (src & 7)) << 4));
-          const int q = div_g(row);
-          if (row >= it.ntok * G || (redo && (odd_rows >> src & 1))) continue;
-          if (po) {
-            reinterpret_cast<uint4 *>(po_base + (int64_t)(whole ? (it.tok0 + q) * a.n_head + it.h * G + row - q * G : row) * HD)[l] = x;
-          } else {
-            const int64_t at = (it.tok0 + q) * a.out.token + (it.h * G + row - q * G) * a.out.head;
-            if (f32) reinterpret_cast<uint4 *>(static_cast<float *>(a.out.p) + at)[l] = x;
-            else reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out.p) + at)[l] = x;
+          for (int k = 0; k < ROWS; k += STEP) {
+            const int at = k + lane / PIECES, src = pass * ROWS + at;
+            const uint4 x = *piece(at, lane % PIECES, src);
+            uint4 *dst = reinterpret_cast<uint4 *>((uintptr_t)of_lane(to_row, src)) + lane % PIECES;
+            if (store >> src & 1) *dst = x;
           }
+          __syncwarp();
         }
-        __syncwarp();
-      }
+      };
+      if (po || out32) emit(std::true_type());
+      else emit(std::false_type());
       if (live && po && !(redo && odd)) *reinterpret_cast<float2 *>(pml) = make_float2(m, sum);
       if (redo) {
         const int seq = a.pass == kPkvPrefix ? min(max(a.group_start[it.b], 0), a.seqs.n_seq - 1) : it.b;
@@ -659,7 +661,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      if (have) put_q(nx);
+      if (have) put_q();
       tc_fence_before();
       it = nx;
     }
