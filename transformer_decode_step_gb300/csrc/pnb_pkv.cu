@@ -16,6 +16,10 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kMaxPairs = 64;
+// Loads on their way come from many warps rather than from many rows per lane: an 8k MHA
+// prompt (half-split, bf16) with 1, 2, 3 rows per lane takes 68, 73, 96 us, and with 2, 4, 5, 6
+// CTAs per SM 92, 68, 78, 108 (the registers of the last do not hold the rows).
+constexpr int kCtasPerSm = 4;
 
 // A lane's part of a row: E elements (8 l ..), or, half-split, E / 2 of each half, as 16-byte
 // loads where the type allows: 8 elements, and 16 of bf16 half-split rows.
@@ -52,23 +56,54 @@ __device__ __forceinline__ void store_part(T *p, int l, const float (&f)[E]) {
 // a.wpt warps (1, 2, 4 or 8) take a token: they compute its cosines and sines once, in
 // shared memory, while its first rows load
 template <int HD, bool NEOX, typename T, typename TQ>
-__global__ void __launch_bounds__(kWarps * 32) k_pkv_append(const PkvAppendArgs a) {
+__global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) k_pkv_append(const PkvAppendArgs a) {
   constexpr int E = kElems<NEOX, T>, LPR = HD / E, RPW = 32 / LPR;   // lanes per row, rows per warp
-  constexpr int U = sizeof(T) == 2 && E == 8 ? 6 : 3;                // rows on their way per lane
+  constexpr int U = E == 16 ? 1 : sizeof(T) == 2 ? 4 : 2;                // rows on their way per lane
   __shared__ float2 turns[kWarps][kMaxPairs];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int tok = blockIdx.x * (kWarps / a.wpt) + warp / a.wpt, rank = warp % a.wpt;
   pdl_wait();
-  const int b = tok < a.seqs.n_tok ? pkv_seq_of(a.seqs, tok) : -1;
-  int t0 = 0, n = 0;
-  if (b >= 0) pkv_tokens(a.seqs, b, t0, n);
+  // the lane's pairs turn by positions that are there, or by the token's entry
+  constexpr int PAIRS = HD / 2 / 32;   // per lane, at one warp per token
+  int pos[PAIRS] = {};
+  if (a.pos && a.freq && tok < a.seqs.n_tok)
+#pragma unroll
+    for (int j = 0; j < PAIRS; ++j) {
+      const int i = (rank + j * a.wpt) * 32 + lane;
+      if (i < HD / 2) pos[j] = a.pos[(int64_t)((i >= a.sec0) + (i >= a.sec1)) * a.seqs.n_tok + tok];
+    }
+  int b, t0, n, len = 0;
+  if (tok >= a.seqs.n_tok) {
+    b = -1;
+  } else if (a.seqs.start && a.seqs.n_seq <= 32) {
+    // all sequences' starts and lengths in one trip to memory, a lane each
+    const int at = min(lane, a.seqs.n_seq - 1);
+    const int from = a.seqs.start[at], to = a.seqs.start[at + 1], held = a.seqs.len[at];
+    b = __popc(__ballot_sync(0xffffffffu, lane < a.seqs.n_seq && to <= tok));
+    const int src = min(b, a.seqs.n_seq - 1);
+    t0 = min(max(__shfl_sync(0xffffffffu, from, src), 0), a.seqs.n_tok);
+    n = max(min(__shfl_sync(0xffffffffu, to, src), a.seqs.n_tok) - t0, 0);
+    len = __shfl_sync(0xffffffffu, held, src);
+    if (b >= a.seqs.n_seq) b = -1;
+  } else {
+    b = pkv_seq_of(a.seqs, tok);
+    if (b >= 0) {
+      pkv_tokens(a.seqs, b, t0, n);
+      len = a.seqs.len[b];
+    }
+  }
   bool live = b >= 0;
   if (live && (tok < t0 || tok - t0 >= n)) {   // `start` decreases
     set_error(a.err, kErrRange);
     live = false;
   }
-  const int64_t e64 = live ? (int64_t)a.seqs.len[b] - n + (tok - t0) : 0;   // the token's entry
+  const int64_t e64 = live ? (int64_t)len - n + (tok - t0) : 0;   // the token's entry
   const int e = (int)e64;
+
+  const bool held = live && e64 >= 0 && e64 < (int64_t)a.seqs.max_page << a.pool.page_log2;
+  // the entry's K row of KV head 0
+  __nv_bfloat16 *const page =
+      held ? pkv_row<HD>(a.pool, a.seqs.pages + (int64_t)b * a.seqs.max_page, e, 0, 0) : nullptr;
 
   const int l = lane % LPR, sub = lane / LPR;
   const int nq = a.q.p ? a.n_head : 0, nkv = a.pool.n_kv, rows = nq + 2 * nkv, step = a.wpt * RPW;
@@ -90,9 +125,11 @@ __global__ void __launch_bounds__(kWarps * 32) k_pkv_append(const PkvAppendArgs 
 
   float2 *mine = turns[warp / a.wpt * a.wpt];
   if (live && a.freq) {
-    for (int i = rank * 32 + lane; i < HD / 2; i += a.wpt * 32) {
-      const int axis = (i >= a.sec0) + (i >= a.sec1);
-      const int p = a.pos ? a.pos[(int64_t)axis * a.seqs.n_tok + tok] : e;
+#pragma unroll
+    for (int j = 0; j < PAIRS; ++j) {
+      const int i = (rank + j * a.wpt) * 32 + lane;
+      if (i >= HD / 2) break;
+      const int p = a.pos ? pos[j] : e;
       const long long turn = (long long)((unsigned long long)(long long)p * a.freq[i]);
       float sn, cs;
       sincospif(__ll2float_rn(turn) * 0x1p-63f, &sn, &cs);
@@ -103,13 +140,7 @@ __global__ void __launch_bounds__(kWarps * 32) k_pkv_append(const PkvAppendArgs 
   else __syncwarp();
   if (!live) return;
 
-  __nv_bfloat16 *page = nullptr;   // the entry's K row of KV head 0
-  if (e64 < 0 || e64 >= (int64_t)a.seqs.max_page << a.pool.page_log2) {
-    if (lane == 0 && rank == 0) set_error(a.err, kErrFull);
-  } else {
-    page = pkv_row<HD>(a.pool, a.seqs.pages + (int64_t)b * a.seqs.max_page, e, 0, 0);
-    if (!page && lane == 0 && rank == 0) set_error(a.err, kErrRange);
-  }
+  if (!page && lane == 0 && rank == 0) set_error(a.err, held ? kErrRange : kErrFull);
   const int64_t head_step = (int64_t)HD << a.pool.page_log2;
   float2 cs[E / 2];
 #pragma unroll
