@@ -374,17 +374,24 @@ SHARED = [
 ]
 
 
+def _wide(n_seq, n_kv, hd, page):
+    """Page tables wide enough for the prefix to be attended once per group (small batches go
+    sequence by sequence)."""
+    return -(-(1 << 29) // (n_seq * page * n_kv * hd * 4))
+
+
 @pytest.mark.parametrize("dtype,out_dtype", [("bf16", "bf16"), ("fp32", "fp32"), ("bf16", "fp32")])
 @pytest.mark.parametrize("groups,own,T,n_kv,G,hd,page", SHARED)
 @pytest.mark.parametrize("window", [0, 100])
-def test_shared(groups, own, T, n_kv, G, hd, page, window, dtype, out_dtype):
+@pytest.mark.parametrize("wide", [True, False])
+def test_shared(groups, own, T, n_kv, G, hd, page, wide, window, dtype, out_dtype):
     pre = [0] * len(own)
     for seqs, p in groups:
         for b in seqs:
             pre[b] = p
     lens = [p + o + T for p, o in zip(pre, own)]
     c = Case(lens, n_kv, G, hd, page, seed=21, new=[T] * len(own), prefix=[(s, p // page * page) for s, p in groups],
-             shared_tok=len(own) * T)
+             shared_tok=len(own) * T, max_page=_wide(len(own), n_kv, hd, page) if wide else None)
     q = c.queries(dtype)
     out = torch.full(q.shape, 7.0, dtype=DT[out_dtype], device="cuda")
     start = torch.tensor([s[0] for s, _ in groups] + [len(own)], dtype=torch.int32, device="cuda")
@@ -395,7 +402,8 @@ def test_shared(groups, own, T, n_kv, G, hd, page, window, dtype, out_dtype):
 
 def test_shared_prefix_that_covers_whole_sequences():
     # the prefix reaches past some sequences' queries: what a row does not see stays unseen
-    c = Case([200, 200, 210], 2, 2, 64, 16, seed=22, new=[4, 4, 4], prefix=[([0, 1, 2], 192)], shared_tok=12)
+    c = Case([200, 200, 210], 2, 2, 64, 16, seed=22, new=[4, 4, 4], prefix=[([0, 1, 2], 192)], shared_tok=12,
+             max_page=_wide(3, 2, 64, 16))
     q = c.queries("fp32")
     out = torch.full_like(q, 7.0)
     start = torch.tensor([0, 3], dtype=torch.int32, device="cuda")
@@ -407,7 +415,7 @@ def test_shared_prefix_that_covers_whole_sequences():
 
 def test_shared_pages_written_by_the_step_itself():
     # drafted tokens of a single sequence inside its "prefix"
-    c = Case([64], 1, 2, 64, 16, seed=23, new=[8], shared_tok=8)
+    c = Case([64], 1, 2, 64, 16, seed=23, new=[8], shared_tok=8, max_page=_wide(1, 1, 64, 16))
     q = c.queries("fp32")
     out = torch.full_like(q, 7.0)
     one = torch.tensor([0, 1], dtype=torch.int32, device="cuda")
@@ -426,10 +434,10 @@ def test_serving_run(dtype):
     kv.buf.fill_(255)   # NaN
     gen = torch.Generator(device="cuda")
     gen.manual_seed(31)
-    table = torch.zeros((B, 12), dtype=torch.int32)
+    table = torch.zeros((B, _wide(B, n_kv, hd, page)), dtype=torch.int32)
     table[:, :5] = torch.tensor([7, 3, 60, 21, 9])
     for b in range(B):
-        table[b, 5:] = 22 + 7 * b + torch.arange(7)
+        table[b, 5:12] = 22 + 7 * b + torch.arange(7)
     table = table.cuda()
     held = [[[[], []] for _ in range(B)] for _ in range(layers)]
 
@@ -487,7 +495,8 @@ def test_serving_run(dtype):
 
 
 def test_captured_calls_follow_the_device_tensors():
-    c = Case([300, 77], 2, 4, 128, 32, seed=41, new=[5, 5], prefix=[([0, 1], 64)], shared_tok=10)
+    c = Case([300, 77], 2, 4, 128, 32, seed=41, new=[5, 5], prefix=[([0, 1], 64)], shared_tok=10,
+             max_page=_wide(2, 2, 128, 32))
     q = c.queries("bf16")
     out, out2 = torch.zeros_like(q), torch.zeros_like(q)
     start = torch.tensor([0, 2], dtype=torch.int32, device="cuda")
@@ -598,7 +607,7 @@ def test_offsets_past_32_bits():
 
 
 def test_nonsense_in_device_tensors_is_reported():
-    c = Case([100, 40], 2, 2, 64, 16, seed=61, new=[3, 3], shared_tok=6)
+    c = Case([100, 40], 2, 2, 64, 16, seed=61, new=[3, 3], shared_tok=6, max_page=_wide(2, 2, 64, 16))
     q = c.queries("fp32")
     out = torch.zeros_like(q)
     start = torch.tensor([0, 2], dtype=torch.int32, device="cuda")

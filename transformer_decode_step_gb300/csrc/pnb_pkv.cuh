@@ -53,10 +53,11 @@ struct PkvAppendArgs {
 // equal runs, one per CTA.  What a run holds of an item that others share goes to
 // the run's partial sums, which a second kernel adds up in the list's order.
 constexpr int kPkvBoxLog2 = 6;          // rows of a TMA box: a page's, at most 64
-// what a kernel attends to: everything, the groups' prefixes (unfinished rows into
-// row_o, row_ml), or what lies behind them, adding the prefix's part
+// what a kernel attends to: everything, the groups' prefixes, or what lies behind them;
+// the rows of the last two are unfinished, and a kernel behind both adds them up
 enum { kPkvAll = 0, kPkvPrefix = 1, kPkvOwn = 2 };
-constexpr int kPkvTile = 128;
+constexpr int kPkvTile = 128;          // of the prompts' kernel
+constexpr int kPkvChunk = 64;          // of the steps' kernel
 constexpr int kPkvBlockRows = 256;
 
 // what a CTA left of an item that others share
@@ -83,12 +84,16 @@ struct PkvAttnArgs {
   const int32_t *group_start, *prefix;
   int32_t n_group;
   PkvGroup *groups;                     // [n_group] workspace
-  float *row_o, *row_ml;                // [n_tok][n_head][head_dim], [..][2]: the prefix's part of each row
+  // unfinished rows, sums and (reference, their weights' sum): of whole items, of the prefix's
+  // and of the own pass [n_tok][n_head][head_dim], [..][2], and of what items share, per CTA
+  float *row_o[2], *row_ml[2];
   float *part_o, *part_ml;              // [2 grid][kPkvBlockRows][head_dim], [..][2]
   PkvPart *part;                        // [2 grid]
   int32_t grid;
   int32_t heads_inner;                  // the list's order (set by the launchers)
-  int32_t item_units;                   // what an item costs beside its tiles, in tiles (set by the launchers)
+  // what an item costs beside its tiles, in tiles, and a tile's time on an SM; the same of the
+  // pass beside this one, and its tiles' entries (set by the launchers)
+  int32_t item_units, unit_ns, other_item_units, other_ns, other_tile;
 };
 
 cudaError_t prepare_pkv_rows(int hd);
@@ -96,8 +101,13 @@ cudaError_t prepare_pkv_step(int hd);
 cudaError_t launch_pkv_append(int hd, bool neox, const PkvAppendArgs &a, cudaStream_t st);
 cudaError_t launch_pkv_rows(int hd, const CUtensorMap &map, const PkvAttnArgs &a, cudaStream_t st);
 cudaError_t launch_pkv_step(int hd, const CUtensorMap &map, const PkvAttnArgs &a, cudaStream_t st);
-// adds up the parts that the CTAs of either left, up to `rows` rows per item
+// adds up the parts that the CTAs left, up to `rows` rows per item, and with a.pass not kPkvAll
+// the parts of both passes and then the passes
 cudaError_t launch_pkv_join(int hd, const PkvAttnArgs &a, int rows, cudaStream_t st);
+// a tile's time, and what an item costs beside its tiles
+void pkv_rows_cost(int hd, bool split, int *unit_ns, int *item_units);
+void pkv_step_cost(int hd, int *unit_ns, int *item_units);
+inline bool pkv_split(const PkvAttnArgs &a) { return a.q.dtype == PNB_F32 || a.out.dtype == PNB_F32; }
 
 // Tokens of sequence b: the first one and their number, kept inside the packed
 // rows whatever `start` holds.
@@ -236,20 +246,6 @@ __device__ __forceinline__ void pkv_join_factors(float m, float m2, float &f, fl
   const float top = fmaxf(m, m2);
   f = m == -INFINITY ? 0.f : exp2f(m - top);
   f2 = m2 == -INFINITY ? 0.f : exp2f(m2 - top);
-}
-
-// Adds the prefix's part of a row to lane l's outputs l * N .. and its sum.
-template <int N>
-__device__ __forceinline__ void pkv_add_prefix(const PkvAttnArgs &a, int tok, int head, float *o, float &m, float &sum) {
-  const int64_t at = (int64_t)tok * a.n_head + head;
-  const float2 ml = *reinterpret_cast<const float2 *>(a.row_ml + at * 2);
-  float f, f2, x[N];
-  pkv_join_factors(m, ml.x, f, f2);
-  load_vals<float, N>(a.row_o + at * 32 * N + (threadIdx.x & 31) * N, x);
-#pragma unroll
-  for (int i = 0; i < N; ++i) o[i] = o[i] * f + x[i] * f2;
-  sum = sum * f + ml.y * f2;
-  m = fmaxf(m, ml.x);
 }
 
 }  // namespace pnb

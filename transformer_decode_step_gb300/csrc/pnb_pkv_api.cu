@@ -10,6 +10,9 @@
 #include "pnb_tmap.cuh"
 
 using namespace pnb;
+#ifndef DIRECT_MB
+#define DIRECT_MB 200
+#endif
 
 struct pnb_pkv {
   pnb_pkv_config cfg;
@@ -21,7 +24,7 @@ struct pnb_pkv {
   int32_t *err = nullptr;
   PkvGroup *groups = nullptr;
   PkvPart *part = nullptr;
-  float *part_o = nullptr, *part_ml = nullptr, *row_o = nullptr, *row_ml = nullptr;
+  float *part_o = nullptr, *part_ml = nullptr, *row_o[2] = {}, *row_ml[2] = {};
   std::vector<CUtensorMap> maps;   // one per layer
 };
 
@@ -104,6 +107,9 @@ int check_tokens(const pnb_pkv *c, const pnb_rows *r, int n_tok, int heads, bool
 // Up to this many rows (tokens x query heads of a KV head) of every sequence go
 // through the kernel for steps.
 constexpr int kStepRows = 16;
+// A batch whose page tables name no more than this goes sequence by sequence, shared prefix or
+// not: the pages that sequences share come from L2.
+constexpr int64_t kDirectBytes = (int64_t)DIRECT_MB << 20;
 
 int attend(pnb_pkv *c, int32_t layer, const pnb_pkv_batch *b, int32_t n_group, const int32_t *group_start,
            const int32_t *prefix, int32_t n_tok, const pnb_rows *q, const pnb_rows *out, int32_t window,
@@ -130,19 +136,40 @@ int attend(pnb_pkv *c, int32_t layer, const pnb_pkv_batch *b, int32_t n_group, c
   a.grid = c->sms;
   a.pass = kPkvAll;
   const CUtensorMap &map = c->maps[layer];
-  if (group_start) {
+  const int group = g.n_head / g.n_kv_head;
+  const bool step = a.seqs.each > 0 && (int64_t)a.seqs.each * group <= kStepRows;
+  const int64_t held = (int64_t)b->n_seq * b->max_page * g.page * g.n_kv_head * g.head_dim * 4;
+  cudaError_t e = cudaSuccess;
+  if (group_start && held > kDirectBytes) {
     a.group_start = group_start;
     a.prefix = prefix;
     a.n_group = n_group;
     a.groups = c->groups;
-    a.row_o = c->row_o;
-    a.row_ml = c->row_ml;
+    for (int i = 0; i < 2; ++i) {
+      a.row_o[i] = c->row_o[i];
+      a.row_ml[i] = c->row_ml[i];
+    }
+    // the prefix's pass, and beside it, with partial sums of its own, the other
+    PkvAttnArgs p = a, o = a;
+    p.pass = kPkvPrefix;
+    o.pass = kPkvOwn;
+    if (step) pkv_step_cost(g.head_dim, &p.other_ns, &p.other_item_units);
+    else pkv_rows_cost(g.head_dim, pkv_split(a), &p.other_ns, &p.other_item_units);
+    p.other_tile = step ? kPkvChunk : kPkvTile;
+    pkv_rows_cost(g.head_dim, pkv_split(a), &o.other_ns, &o.other_item_units);
+    o.other_tile = kPkvTile;
+    o.part += 2 * c->sms;
+    o.part_o += (size_t)2 * c->sms * kPkvBlockRows * g.head_dim;
+    o.part_ml += (size_t)2 * c->sms * kPkvBlockRows * 2;
+    e = launch_pkv_rows(g.head_dim, map, p, st);
+    if (e == cudaSuccess)
+      e = step ? launch_pkv_step(g.head_dim, map, o, st) : launch_pkv_rows(g.head_dim, map, o, st);
     a.pass = kPkvPrefix;
-    if (launch_pkv_rows(g.head_dim, map, a, st) != cudaSuccess) return PNB_E_CUDA;
-    a.pass = kPkvOwn;
+  } else {
+    e = step ? launch_pkv_step(g.head_dim, map, a, st) : launch_pkv_rows(g.head_dim, map, a, st);
   }
-  const bool step = a.seqs.each > 0 && (int64_t)a.seqs.each * (g.n_head / g.n_kv_head) <= kStepRows;
-  const cudaError_t e = step ? launch_pkv_step(g.head_dim, map, a, st) : launch_pkv_rows(g.head_dim, map, a, st);
+  if (e == cudaSuccess)
+    e = launch_pkv_join(g.head_dim, a, step && a.pass == kPkvAll ? a.seqs.each * group : kPkvBlockRows, st);
   return e == cudaSuccess ? PNB_OK : PNB_E_CUDA;
 }
 
@@ -196,12 +223,15 @@ int pnb_pkv_new(const pnb_pkv_config *cfg, void *pool_dev, size_t bytes, pnb_pkv
     maps = encode_map(&k->maps[l], k->pool + (size_t)l * k->layer_bytes, (int64_t)c.n_page * 2 * c.n_kv_head * c.page,
                       c.head_dim, c.page < 1 << kPkvBoxLog2 ? c.page : 1 << kPkvBoxLog2);
   if (e == cudaSuccess && !maps) e = cudaErrorUnknown;
-  const size_t part_rows = (size_t)2 * k->sms * kPkvBlockRows, rows = (size_t)c.shared_tok * c.n_head;
-  const size_t o_err = take(4), o_freq = take(sizeof(freq)), o_part = take(2 * (size_t)k->sms * sizeof(PkvPart));
+  // two partial sums per CTA, for either of the passes over a shared prefix
+  const size_t parts = (size_t)2 * k->sms * (c.shared_tok ? 2 : 1), part_rows = parts * kPkvBlockRows;
+  const size_t rows = (size_t)c.shared_tok * c.n_head;
+  const size_t o_err = take(4), o_freq = take(sizeof(freq)), o_part = take(parts * sizeof(PkvPart));
   const size_t zeroed = at;
   const size_t o_groups = take(kPkvMaxSeq * sizeof(PkvGroup));
   const size_t o_pml = take(part_rows * 8), o_po = take(part_rows * c.head_dim * 4);
   const size_t o_rml = take(rows * 8), o_ro = take(rows * c.head_dim * 4);
+  const size_t o_rml2 = take(rows * 8), o_ro2 = take(rows * c.head_dim * 4);
   if (e == cudaSuccess) e = cudaMalloc(&k->ws, at);
   if (e == cudaSuccess) e = clear_now(k->ws, zeroed);
   if (e == cudaSuccess) e = cudaMemcpy(k->ws + o_freq, freq, sizeof(freq), cudaMemcpyHostToDevice);
@@ -217,8 +247,10 @@ int pnb_pkv_new(const pnb_pkv_config *cfg, void *pool_dev, size_t bytes, pnb_pkv
   k->part = reinterpret_cast<PkvPart *>(k->ws + o_part);
   k->part_ml = reinterpret_cast<float *>(k->ws + o_pml);
   k->part_o = reinterpret_cast<float *>(k->ws + o_po);
-  k->row_ml = reinterpret_cast<float *>(k->ws + o_rml);
-  k->row_o = reinterpret_cast<float *>(k->ws + o_ro);
+  k->row_ml[0] = reinterpret_cast<float *>(k->ws + o_rml);
+  k->row_o[0] = reinterpret_cast<float *>(k->ws + o_ro);
+  k->row_ml[1] = reinterpret_cast<float *>(k->ws + o_rml2);
+  k->row_o[1] = reinterpret_cast<float *>(k->ws + o_ro2);
   *out = k;
   return PNB_OK;
 }

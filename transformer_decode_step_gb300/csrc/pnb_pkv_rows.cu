@@ -163,10 +163,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  pdl_wait();
+  // The own pass runs beside the prefix's, which let it start behind its own wait: the call's
+  // inputs are there, and it waits for the prefix's end only at its own.
+  if (a.pass != kPkvOwn) pdl_wait();
   pdl_trigger();
   if (threadIdx.x < 2) a.part[2 * blockIdx.x + threadIdx.x].flags = 0;
-  if (a.pass == kPkvPrefix) pkv_find_groups<kThreads>(a, reinterpret_cast<int *>(ring));
+  if (a.pass != kPkvAll) pkv_find_groups<kThreads>(a, reinterpret_cast<int *>(ring));
   PkvWalk walk = pkv_find_run<kPkvTile, kThreads>(a, TB, reinterpret_cast<long long *>(ring));
   PkvItem it;
   const uint32_t tmem = bar.tmem;
@@ -536,17 +538,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       const bool whole = it.ta == 0 && it.ends;
       const int side = it.ta > 0 ? 0 : 1;   // of the run's two partial sums
-      // the prefix's part of the row
-      float f_own = 1.f, f_pre = 0.f, all = sum;
-      const float *bo = nullptr;
-      if (whole && it.floor > 0) {
-        const int64_t at = (int64_t)tok * a.n_head + head;
-        const float2 ml = *reinterpret_cast<const float2 *>(a.row_ml + at * 2);
-        bo = a.row_o + at * HD;
-        pkv_join_factors(m, ml.x, f_own, f_pre);
-        all = sum * f_own + ml.y * f_pre;
-      }
-      const float inv = all == 0.f ? 0.f : 1.f / all;
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
       // where the row goes: the answer, or, unfinished, its sums
       float *po = nullptr, *pml = nullptr;
       if (!whole) {
@@ -554,10 +546,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         po = a.part_o + at * HD;
         pml = a.part_ml + at * 2;
         if (r == 0) a.part[2 * blockIdx.x + side] = PkvPart{it.ends ? 3 : 1, it.b, it.j, it.h};
-      } else if (a.pass == kPkvPrefix) {
+      } else if (a.pass != kPkvAll) {
         const int64_t at = (int64_t)tok * a.n_head + head;
-        po = a.row_o + at * HD;
-        pml = a.row_ml + at * 2;
+        po = a.row_o[a.pass - 1] + at * HD;
+        pml = a.row_ml[a.pass - 1] + at * 2;
       }
       const bool out32 = a.out.dtype == PNB_F32;
       const long long to_row = po ? (long long)(uintptr_t)po
@@ -588,16 +580,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_landed(o);
 #pragma unroll
             for (int k = 0; k < 32; ++k) z = fmaf(o[k], 0.f, z);
-            if (bo && live) {
-#pragma unroll
-              for (int k = 0; k < 32; k += 4) {
-                const float4 x = *reinterpret_cast<const float4 *>(bo + i + k);
-                o[k] = o[k] * f_own + x.x * f_pre;
-                o[k + 1] = o[k + 1] * f_own + x.y * f_pre;
-                o[k + 2] = o[k + 2] * f_own + x.z * f_pre;
-                o[k + 3] = o[k + 3] * f_own + x.w * f_pre;
-              }
-            }
             if (mine) {
               if constexpr (F32) {
 #pragma unroll
@@ -655,7 +637,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; i < HD / 32; ++i) dst[lane * (HD / 32) + i] = o[i];
             if (lane == 0) *reinterpret_cast<float2 *>((uintptr_t)pml_k) = make_float2(mk, lk);
           } else {
-            if (it.floor > 0) pkv_add_prefix<HD / 32>(a, tk, hd_k, o, mk, lk);
             pkv_store<HD / 32>(a.out, tk * a.out.token + hd_k * a.out.head + lane * (HD / 32), o,
                                lk == 0.f ? 0.f : 1.f / lk);
           }
@@ -671,25 +652,33 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   if (warp == 9) tmem_dealloc(tmem, 512);
+  if (a.pass == kPkvOwn) pdl_wait();
 }
 
 // Adds up the parts of the items that several CTAs shared, in the list's order.  The
 // CTA whose run holds an item's first tiles has it in its second partial sum; the
 // runs behind it hold the rest in their first ones.  A warp takes four rows together, so
-// that the parts' loads are on their way at once.
+// that the parts' loads are on their way at once.  blockIdx.z: the prefix's and the own pass.
 template <int HD>
-__global__ void __launch_bounds__(256) k_pkv_join(const PkvAttnArgs a) {
+__global__ void __launch_bounds__(256) k_pkv_join(const PkvAttnArgs args) {
   constexpr int N = HD / 32, R = 4;
   __shared__ int s_last;
+  PkvAttnArgs a = args;
   const int lane = threadIdx.x & 31, c0 = blockIdx.x;
   pdl_wait();
   pdl_trigger();
+  if (args.pass != kPkvAll) {
+    a.pass = kPkvPrefix + blockIdx.z;
+    a.part += (size_t)blockIdx.z * 2 * a.grid;
+    a.part_o += (size_t)blockIdx.z * 2 * a.grid * kPkvBlockRows * HD;
+    a.part_ml += (size_t)blockIdx.z * 2 * a.grid * kPkvBlockRows * 2;
+  }
   const PkvPart p = a.part[2 * c0 + 1];
   if (!(p.flags & 1)) return;
   const int G = a.n_head / a.pool.n_kv, TB = kPkvBlockRows / G;
-  const PkvSeq seq = pkv_seq(a, p.b);
+  const PkvSeq seq = pkv_seq(a, a.pass, p.b);
   PkvItem it;
-  pkv_block<kPkvTile>(a, seq, TB, p.b, p.j, it);
+  pkv_block<kPkvTile>(a, a.pass, seq, TB, p.b, p.j, it);
   const int rows = it.ntok * G, r0 = (blockIdx.y * 8 + (threadIdx.x >> 5)) * R;
   // the run that ends the item
   if (threadIdx.x == 0) s_last = a.grid - 1;
@@ -758,16 +747,46 @@ __global__ void __launch_bounds__(256) k_pkv_join(const PkvAttnArgs a) {
     sum[i] = warp_sum(sum[i]);
     if (r >= rows) break;
     const int tok = it.tok0 + r / G, head = p.h * G + r % G;
-    if (it.floor > 0) pkv_add_prefix<N>(a, tok, head, o[i], m[i], sum[i]);
-    if (a.pass == kPkvPrefix) {
+    if (a.pass != kPkvAll) {
       const int64_t at = (int64_t)tok * a.n_head + head;
 #pragma unroll
-      for (int n = 0; n < N; ++n) a.row_o[at * HD + lane * N + n] = o[i][n];
-      if (lane == 0) *reinterpret_cast<float2 *>(a.row_ml + at * 2) = make_float2(m[i], sum[i]);
+      for (int n = 0; n < N; ++n) a.row_o[a.pass - 1][at * HD + lane * N + n] = o[i][n];
+      if (lane == 0) *reinterpret_cast<float2 *>(a.row_ml[a.pass - 1] + at * 2) = make_float2(m[i], sum[i]);
     } else {
       pkv_store<N>(a.out, tok * a.out.token + head * a.out.head + lane * N, o[i], sum[i] == 0.f ? 0.f : 1.f / sum[i]);
     }
   }
+}
+
+// Adds the two passes' parts of every row, a warp each.
+template <int HD>
+__global__ void __launch_bounds__(256) k_pkv_finish(const PkvAttnArgs a) {
+  constexpr int N = HD / 32;
+  const int lane = threadIdx.x & 31;
+  const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  pdl_wait();
+  if (row >= (int64_t)a.seqs.n_tok * a.n_head) return;
+  const int tok = (int)(row / a.n_head), head = (int)(row - (int64_t)tok * a.n_head);
+  float2 ml[2];
+  float x[2][N];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    ml[i] = *reinterpret_cast<const float2 *>(a.row_ml[i] + row * 2);
+    load_vals<float, N>(a.row_o[i] + row * HD + lane * N, x[i]);
+  }
+  // a sequence that no group holds has no prefix
+  const int g = pkv_group_of(a.group_start, a.n_group, tok / a.seqs.each);
+  if (g < 0 || a.groups[g].prefix == 0) {
+    ml[0] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[0][i] = 0.f;
+  }
+  float f0, f1, o[N];
+  pkv_join_factors(ml[0].x, ml[1].x, f0, f1);
+  const float sum = ml[0].y * f0 + ml[1].y * f1;
+#pragma unroll
+  for (int i = 0; i < N; ++i) o[i] = x[0][i] * f0 + x[1][i] * f1;
+  pkv_store<N>(a.out, tok * a.out.token + head * a.out.head + lane * N, o, sum == 0.f ? 0.f : 1.f / sum);
 }
 
 template <int HD, bool SPLIT>
@@ -796,25 +815,33 @@ cudaError_t prepare() {
 }  // namespace
 
 cudaError_t launch_pkv_join(int hd, const PkvAttnArgs &a, int rows, cudaStream_t st) {
-  const dim3 grid(a.grid, (rows + 31) / 32), block(256);
-  return hd == 128 ? launch_pdl(k_pkv_join<128>, grid, block, 0, 1, st, a)
-                   : launch_pdl(k_pkv_join<64>, grid, block, 0, 1, st, a);
+  const bool two = a.pass != kPkvAll;
+  const dim3 grid(a.grid, (rows + 31) / 32, two ? 2 : 1), block(256);
+  cudaError_t e = hd == 128 ? launch_pdl(k_pkv_join<128>, grid, block, 0, 1, st, a)
+                            : launch_pdl(k_pkv_join<64>, grid, block, 0, 1, st, a);
+  if (e != cudaSuccess || !two) return e;
+  const dim3 all((unsigned)(((int64_t)a.seqs.n_tok * a.n_head + 7) / 8));
+  return hd == 128 ? launch_pdl(k_pkv_finish<128>, all, block, 0, 1, st, a)
+                   : launch_pdl(k_pkv_finish<64>, all, block, 0, 1, st, a);
+}
+
+// An item's start and end against a tile's time.  16k prompt at 2, 4, 6, 8 units: 1625, 1544, 1523,
+// 1538 us; 16 packed prompts 325, 298, 291, 298; fp32, whose tiles take twice as long, 872, 848,
+// 869, 872.
+void pkv_rows_cost(int hd, bool split, int *unit_ns, int *item_units) {
+  *unit_ns = (split ? 2400 : 1500) * (hd == 128 ? 2 : 1) / 2;
+  *item_units = split ? 4 : 6;
 }
 
 cudaError_t prepare_pkv_rows(int hd) { return hd == 128 ? prepare<128>() : prepare<64>(); }
 
 cudaError_t launch_pkv_rows(int hd, const CUtensorMap &map, const PkvAttnArgs &args, cudaStream_t st) {
   PkvAttnArgs a = args;
-  const bool split = a.q.dtype == PNB_F32 || a.out.dtype == PNB_F32;
-  // An item's start and end against a tile's time.  16k prompt at 2, 4, 6, 8 units: 1625, 1544, 1523,
-  // 1538 us; 16 packed prompts 325, 298, 291, 298; fp32, whose tiles take twice as long, 872, 848,
-  // 869, 872.
-  a.item_units = split ? 4 : 6;
+  const bool split = pkv_split(a);
+  pkv_rows_cost(hd, split, &a.unit_ns, &a.item_units);
   a.heads_inner = a.pass == kPkvAll;
-  cudaError_t e;
-  if (hd == 128) e = split ? launch_rows<128, true>(map, a, st) : launch_rows<128, false>(map, a, st);
-  else e = split ? launch_rows<64, true>(map, a, st) : launch_rows<64, false>(map, a, st);
-  return e == cudaSuccess ? launch_pkv_join(hd, a, kPkvBlockRows, st) : e;
+  if (hd == 128) return split ? launch_rows<128, true>(map, a, st) : launch_rows<128, false>(map, a, st);
+  return split ? launch_rows<64, true>(map, a, st) : launch_rows<64, false>(map, a, st);
 }
 
 }  // namespace pnb

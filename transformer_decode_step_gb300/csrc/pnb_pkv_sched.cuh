@@ -1,6 +1,10 @@
 // pnb_pkv_sched.cuh - the list of work of the paged cache's attention kernels: blocks of
 // rows, their tiles of entries, and each CTA's run through them.
 //
+// Over a shared prefix two lists are worked through at once, the groups' prefixes and what
+// the sequences have of their own: each gets CTAs by its share of the work, and the two
+// kernels run side by side on their SMs (one bound by products, one by bytes).
+//
 // The list holds the sequences (or groups) and their blocks in order, once per KV head: the
 // heads innermost for prompts, so that the CTAs that read the same entries for different
 // blocks read them at about the same time (512 tokens on a 60k context, whose K and V do
@@ -37,10 +41,10 @@ struct PkvItem {
   bool ends;                // the item's end is this CTA's
 };
 
-__device__ __forceinline__ PkvSeq pkv_seq(const PkvAttnArgs &a, int b) {
+__device__ __forceinline__ PkvSeq pkv_seq(const PkvAttnArgs &a, int pass, int b) {
   PkvSeq s{};
   const int W = a.window;
-  if (a.pass == kPkvPrefix) {
+  if (pass == kPkvPrefix) {
     const int gs = min(max(a.group_start[b], 0), a.seqs.n_seq), ge = min(max(a.group_start[b + 1], gs), a.seqs.n_seq);
     s.t0 = gs * a.seqs.each;
     s.n = (ge - gs) * a.seqs.each;
@@ -51,7 +55,7 @@ __device__ __forceinline__ PkvSeq pkv_seq(const PkvAttnArgs &a, int b) {
   } else {
     pkv_tokens(a.seqs, b, s.t0, s.n);
     s.len = pkv_len(a.seqs, a.pool.page_log2, b, a.err);
-    if (a.pass == kPkvOwn) {
+    if (pass == kPkvOwn) {
       const int g = pkv_group_of(a.group_start, a.n_group, b);
       s.floor = g < 0 ? 0 : min(a.groups[g].prefix, max(s.len - s.n, 0));
     }
@@ -61,7 +65,8 @@ __device__ __forceinline__ PkvSeq pkv_seq(const PkvAttnArgs &a, int b) {
 
 // a sequence's j-th block (j * TB < n)
 template <int TILE>
-__device__ __forceinline__ void pkv_block(const PkvAttnArgs &a, const PkvSeq &s, int TB, int b, int j, PkvItem &it) {
+__device__ __forceinline__ void pkv_block(const PkvAttnArgs &a, int pass, const PkvSeq &s, int TB, int b, int j,
+                                          PkvItem &it) {
   const int W = a.window;
   it.b = b;
   it.j = j;
@@ -69,7 +74,7 @@ __device__ __forceinline__ void pkv_block(const PkvAttnArgs &a, const PkvSeq &s,
   it.ntok = min(TB, s.n - j * TB);
   it.len = s.len;
   it.floor = s.floor;
-  if (a.pass == kPkvPrefix) {
+  if (pass == kPkvPrefix) {
     it.base = 0;
     it.hi = it.hi_min = s.len;
     it.lo = s.lo;
@@ -111,20 +116,20 @@ __device__ __forceinline__ long long floor_sum(uint32_t n, uint32_t m, uint32_t 
 
 __device__ __forceinline__ int pkv_blocks(const PkvSeq &s, int TB) { return (s.n + TB - 1) / TB; }
 
-// units of a sequence's first J blocks, per KV head
+// units of a sequence's first J blocks, per KV head; `each` of them for an item's start and end
 template <int TILE>
-__device__ __forceinline__ long long pkv_units(const PkvAttnArgs &a, const PkvSeq &s, int TB, int J) {
+__device__ __forceinline__ long long pkv_units(const PkvAttnArgs &a, int pass, int each, const PkvSeq &s, int TB, int J) {
   if (J <= 0) return 0;
   PkvItem it;
-  if (a.pass == kPkvPrefix) {
-    pkv_block<TILE>(a, s, TB, 0, 0, it);
-    return (long long)J * (it.nt + a.item_units);
+  if (pass == kPkvPrefix) {
+    pkv_block<TILE>(a, pass, s, TB, 0, 0, it);
+    return (long long)J * (it.nt + each);
   }
   // the last block may have fewer tokens
   long long sum = 0;
   int K = J;
   if (J == pkv_blocks(s, TB)) {
-    pkv_block<TILE>(a, s, TB, 0, J - 1, it);
+    pkv_block<TILE>(a, pass, s, TB, 0, J - 1, it);
     sum = it.nt;
     --K;
   }
@@ -143,7 +148,7 @@ __device__ __forceinline__ long long pkv_units(const PkvAttnArgs &a, const PkvSe
     sum -= (long long)(y - z) * (s.floor / TILE);
     if (K > y) sum -= floor_sum(K - y, TILE, TB, base + y * TB - a.window + 1);
   }
-  return sum + (long long)J * a.item_units;
+  return sum + (long long)J * each;
 }
 
 // a CTA's way through its run of units
@@ -166,9 +171,9 @@ struct PkvWalk {
           b = 0;
           if (a.heads_inner || ++h == a.pool.n_kv) return false;
         }
-        seq = pkv_seq(a, b);
+        seq = pkv_seq(a, a.pass, b);
       }
-      pkv_block<TILE>(a, seq, TB, b, j, it);
+      pkv_block<TILE>(a, a.pass, seq, TB, b, j, it);
       const int units = it.nt + a.item_units;
       const int end = (int)min((int64_t)units, x + left);
       it.h = h;
@@ -216,13 +221,50 @@ __device__ __forceinline__ void pkv_find_groups(const PkvAttnArgs &a, int *scrat
   __syncthreads();
 }
 
+// Inclusive prefix sum over the CTA's threads; `all` gets their sum.  scratch: 32 numbers.
+template <int THREADS>
+__device__ __forceinline__ long long pkv_scan(long long v, long long *scratch, long long &all) {
+  constexpr int WARPS = THREADS / 32;
+  static_assert(WARPS <= 32, "warps");
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long u = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += u;
+  }
+  __syncthreads();
+  if (lane == 31) scratch[warp] = v;
+  __syncthreads();
+  long long w = lane < WARPS ? scratch[lane] : 0;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long u = __shfl_up_sync(0xffffffffu, w, o);
+    if (lane >= o) w += u;
+  }
+  all = __shfl_sync(0xffffffffu, w, 31);
+  return v + (warp ? __shfl_sync(0xffffffffu, w, warp - 1) : 0);
+}
+
+// The work of the pass that runs beside this one, in nanoseconds of an SM.
+template <int THREADS>
+__device__ __forceinline__ long long pkv_other_work(const PkvAttnArgs &a, long long *scratch) {
+  const int pass = a.pass == kPkvPrefix ? kPkvOwn : kPkvPrefix, n = pass == kPkvPrefix ? a.n_group : a.seqs.n_seq;
+  long long mine = 0, all;
+  for (int b = threadIdx.x; b < n; b += THREADS) {
+    const PkvSeq s = pkv_seq(a, pass, b);
+    const int TB = a.other_tile == kPkvTile ? kPkvBlockRows / (a.n_head / a.pool.n_kv) : a.seqs.each;
+    mine += a.other_tile == kPkvTile ? pkv_units<kPkvTile>(a, pass, a.other_item_units, s, TB, pkv_blocks(s, TB))
+                                     : pkv_units<kPkvChunk>(a, pass, a.other_item_units, s, TB, pkv_blocks(s, TB));
+  }
+  pkv_scan<THREADS>(mine, scratch, all);
+  return all * a.other_ns;
+}
+
 // Where this CTA's run starts (every warp answers for itself).  scratch: 64 numbers.
 template <int TILE, int THREADS>
 __device__ __forceinline__ PkvWalk pkv_find_run(const PkvAttnArgs &a, int TB, long long *scratch) {
-  constexpr int WARPS = THREADS / 32, PASSES = (kPkvMaxSeq + THREADS - 1) / THREADS;
-  static_assert(WARPS <= 32, "warps");
-  const int n_b = a.pass == kPkvPrefix ? a.n_group : a.seqs.n_seq;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  constexpr int PASSES = (kPkvMaxSeq + THREADS - 1) / THREADS;
+  const int n_b = a.pass == kPkvPrefix ? a.n_group : a.seqs.n_seq, tid = threadIdx.x, lane = tid & 31;
   long long before[PASSES], units[PASSES], total = 0;
 #pragma unroll
   for (int k = 0; k < PASSES; ++k) {
@@ -230,32 +272,25 @@ __device__ __forceinline__ PkvWalk pkv_find_run(const PkvAttnArgs &a, int TB, lo
     if (k * THREADS >= n_b) continue;   // (the same for all threads)
     const int b = k * THREADS + tid;
     if (b < n_b) {
-      const PkvSeq s = pkv_seq(a, b);
-      units[k] = pkv_units<TILE>(a, s, TB, pkv_blocks(s, TB));
+      const PkvSeq s = pkv_seq(a, a.pass, b);
+      units[k] = pkv_units<TILE>(a, a.pass, a.item_units, s, TB, pkv_blocks(s, TB));
     }
-    long long v = units[k];
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long u = __shfl_up_sync(0xffffffffu, v, o);
-      if (lane >= o) v += u;
-    }
-    __syncthreads();
-    if (lane == 31) scratch[warp] = v;
-    __syncthreads();
-    long long w = lane < WARPS ? scratch[lane] : 0;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long u = __shfl_up_sync(0xffffffffu, w, o);
-      if (lane >= o) w += u;
-    }
-    const long long all = __shfl_sync(0xffffffffu, w, 31);
-    const long long warps_before = warp ? __shfl_sync(0xffffffffu, w, warp - 1) : 0;
-    before[k] = total + warps_before + v - units[k];
+    long long all;
+    before[k] = total + pkv_scan<THREADS>(units[k], scratch, all) - units[k];
     total += all;
   }
-  // as many CTAs as get a run of a few units each
+  // as many CTAs as get a run of a few units each, and this pass's share of them
   const int n_kv = a.pool.n_kv;
-  const long long list = total * n_kv, ctas = max(1ll, min((long long)gridDim.x, list / kPkvMinRun));
+  const long long list = total * n_kv;
+  long long ctas = gridDim.x;
+  if (a.pass != kPkvAll) {
+    const long long here = total * a.unit_ns, there = pkv_other_work<THREADS>(a, scratch);
+    // (the prefix's pass rounds down and the other one up)
+    const long long prefix = a.pass == kPkvPrefix ? here : there;
+    ctas = max(1ll, min(ctas - 1, ctas * prefix / max(here + there, 1ll)));
+    if (a.pass == kPkvOwn) ctas = gridDim.x - ctas;
+  }
+  ctas = max(1ll, min(ctas, list / kPkvMinRun));
   const long long c = min((long long)blockIdx.x, ctas), u0 = list * c / ctas, u1 = list * min(c + 1, ctas) / ctas;
   PkvWalk r{};
   r.n_b = n_b;
@@ -271,22 +306,22 @@ __device__ __forceinline__ PkvWalk pkv_find_run(const PkvAttnArgs &a, int TB, lo
     }
   __syncthreads();
   r.b = (int)scratch[40];
-  r.seq = pkv_seq(a, r.b);
+  r.seq = pkv_seq(a, a.pass, r.b);
   const long long in_seq = at - scratch[41];
   // the last block j with units(j) <= in_seq: 32 candidates at a time
   int lo = 0, hi = pkv_blocks(r.seq, TB);
   while (hi - lo > 1) {
     const int step = (hi - lo + 31) / 32, j = lo + lane * step;
-    const bool in = j < hi && pkv_units<TILE>(a, r.seq, TB, j) <= in_seq;
+    const bool in = j < hi && pkv_units<TILE>(a, a.pass, a.item_units, r.seq, TB, j) <= in_seq;
     const int k = 31 - __clz(__ballot_sync(0xffffffffu, in));
     lo += k * step;
     hi = min(hi, lo + step);
   }
   r.j = lo;
-  const long long block = pkv_units<TILE>(a, r.seq, TB, lo);
+  const long long block = pkv_units<TILE>(a, a.pass, a.item_units, r.seq, TB, lo);
   if (a.heads_inner) {
     PkvItem it;
-    pkv_block<TILE>(a, r.seq, TB, r.b, lo, it);
+    pkv_block<TILE>(a, a.pass, r.seq, TB, r.b, lo, it);
     const long long rest = u0 - (scratch[41] + block) * n_kv;   // of the block, over its heads
     r.h = (int)(rest / (it.nt + a.item_units));
     r.x = (int)(rest % (it.nt + a.item_units));

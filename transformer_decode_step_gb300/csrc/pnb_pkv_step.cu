@@ -26,7 +26,7 @@ extern __shared__ __align__(1024) uint8_t s_smem[];
 
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32 + 32;
-constexpr int kChunk = 64;
+constexpr int kChunk = kPkvChunk;
 constexpr float kTau = 8.f;
 
 template <int HD, int RB>
@@ -103,9 +103,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     bar.bad = 0;
   }
   __syncthreads();
-  pdl_wait();
+  // The own pass runs beside the prefix's, which let it start behind its own wait: the call's
+  // inputs are there, and it waits for the prefix's end only at its own.
+  if (a.pass != kPkvOwn) pdl_wait();
   pdl_trigger();
   if (threadIdx.x < 2) a.part[2 * blockIdx.x + threadIdx.x].flags = 0;
+  if (a.pass == kPkvOwn) pkv_find_groups<kThreads>(a, reinterpret_cast<int *>(ring));
   PkvWalk walk = pkv_find_run<kChunk, kThreads>(a, a.seqs.each, reinterpret_cast<long long *>(ring));
   PkvItem it;
   fence_async_smem();   // the ring held the schedule's sums
@@ -330,18 +333,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                            tok * a.q.token + head * a.q.head, a.qscale, from, min(last + 1, (it.t0 + it.tb) * kChunk), x,
                            mr, sr);
       }
-      if (whole) {
-        if (it.floor > 0) pkv_add_prefix<N>(a, tok, head, x, mr, sr);
+      if (whole && a.pass == kPkvAll) {
         pkv_store<N>(a.out, tok * a.out.token + head * a.out.head + lane * N, x, sr == 0.f ? 0.f : 1.f / sr);
       } else {
-        const int64_t at = (int64_t)(2 * blockIdx.x + side) * kPkvBlockRows + r;
+        const int64_t at =
+            whole ? (int64_t)tok * a.n_head + head : (int64_t)(2 * blockIdx.x + side) * kPkvBlockRows + r;
+        float *po = whole ? a.row_o[1] : a.part_o, *pml = whole ? a.row_ml[1] : a.part_ml;
 #pragma unroll
-        for (int i = 0; i < N; ++i) a.part_o[at * HD + lane * N + i] = x[i];
-        if (lane == 0) *reinterpret_cast<float2 *>(a.part_ml + at * 2) = make_float2(mr, sr);
+        for (int i = 0; i < N; ++i) po[at * HD + lane * N + i] = x[i];
+        if (lane == 0) *reinterpret_cast<float2 *>(pml + at * 2) = make_float2(mr, sr);
       }
     }
     consumer_sync<kWarps * 32>();
   }
+  if (a.pass == kPkvOwn) pdl_wait();
 }
 
 template <int HD, int RB>
@@ -372,14 +377,18 @@ cudaError_t prepare_pkv_step(int hd) {
   return hd == 128 ? prepare<128, 2>() : prepare<64, 2>();
 }
 
+// a chunk at the GPU's copy rate, shared out over its SMs
+void pkv_step_cost(int hd, int *unit_ns, int *item_units) {
+  *unit_ns = hd == 128 ? 800 : 400;
+  *item_units = 4;
+}
+
 cudaError_t launch_pkv_step(int hd, const CUtensorMap &map, const PkvAttnArgs &args, cudaStream_t st) {
   PkvAttnArgs a = args;
-  a.item_units = 4;
+  pkv_step_cost(hd, &a.unit_ns, &a.item_units);
   const int rows = a.seqs.each * (a.n_head / a.pool.n_kv);
-  cudaError_t e;
-  if (hd == 128) e = rows <= 8 ? launch_step<128, 1>(map, a, st) : launch_step<128, 2>(map, a, st);
-  else e = rows <= 8 ? launch_step<64, 1>(map, a, st) : launch_step<64, 2>(map, a, st);
-  return e == cudaSuccess ? launch_pkv_join(hd, a, rows, st) : e;
+  if (hd == 128) return rows <= 8 ? launch_step<128, 1>(map, a, st) : launch_step<128, 2>(map, a, st);
+  return rows <= 8 ? launch_step<64, 1>(map, a, st) : launch_step<64, 2>(map, a, st);
 }
 
 }  // namespace pnb
