@@ -19,6 +19,7 @@ namespace pnb {
 
 constexpr int kPkvMaxSeq = 1024;
 constexpr int kPkvMaxGroup = 64;       // query heads per KV head
+constexpr int kPkvMaxCtas = 512;       // most CTAs of an attention kernel
 
 // one layer of a pool
 struct PkvPool {

@@ -169,7 +169,7 @@ int attend(pnb_pkv *c, int32_t layer, const pnb_pkv_batch *b, int32_t n_group, c
     e = step ? launch_pkv_step(g.head_dim, map, a, st) : launch_pkv_rows(g.head_dim, map, a, st);
   }
   if (e == cudaSuccess)
-    e = launch_pkv_join(g.head_dim, a, step && a.pass == kPkvAll ? a.seqs.each * group : kPkvBlockRows, st);
+    e = launch_pkv_join(g.head_dim, a, step ? a.seqs.each * group : kPkvBlockRows, st);
   return e == cudaSuccess ? PNB_OK : PNB_E_CUDA;
 }
 
@@ -212,6 +212,7 @@ int pnb_pkv_new(const pnb_pkv_config *cfg, void *pool_dev, size_t bytes, pnb_pkv
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&k->sms, cudaDevAttrMultiProcessorCount, k->device);
   if (e == cudaSuccess) e = prepare_pkv_rows(c.head_dim);
   if (e == cudaSuccess) e = prepare_pkv_step(c.head_dim);
+  k->sms = k->sms < kPkvMaxCtas ? k->sms : kPkvMaxCtas;
   bool maps = e == cudaSuccess;
   try {
     if (maps) k->maps.resize(c.n_layer);

@@ -128,7 +128,7 @@ __device__ __noinline__ bool hidden_odd_values(const PkvAttnArgs &a, const PkvIt
 
 template <int HD, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
-    k_pkv_rows(const __grid_constant__ CUtensorMap kvmap, const PkvAttnArgs a) {
+    k_pkv_rows(const __grid_constant__ CUtensorMap kvmap, const __grid_constant__ PkvAttnArgs a) {
   typedef RL<HD, SPLIT> L;
   constexpr int NU = L::NU;
   static_assert(NU <= 16 && NU >= 2, "ring");
@@ -655,46 +655,36 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (a.pass == kPkvOwn) pdl_wait();
 }
 
-// Adds up the parts of the items that several CTAs shared, in the list's order.  The
-// CTA whose run holds an item's first tiles has it in its second partial sum; the
-// runs behind it hold the rest in their first ones.  A warp takes four rows together, so
-// that the parts' loads are on their way at once.  blockIdx.z: the prefix's and the own pass.
+// rows r0 .. r0 + 3 of the item whose first tiles CTA c0 had
 template <int HD>
-__global__ void __launch_bounds__(256) k_pkv_join(const PkvAttnArgs args) {
+__device__ __forceinline__ void join_rows(const PkvAttnArgs &a, int pass, int c0, int r0, const uint8_t *first,
+                                          const uint8_t *second) {
   constexpr int N = HD / 32, R = 4;
-  __shared__ int s_last;
-  PkvAttnArgs a = args;
-  const int lane = threadIdx.x & 31, c0 = blockIdx.x;
-  pdl_wait();
-  pdl_trigger();
-  if (args.pass != kPkvAll) {
-    a.pass = kPkvPrefix + blockIdx.z;
-    a.part += (size_t)blockIdx.z * 2 * a.grid;
-    a.part_o += (size_t)blockIdx.z * 2 * a.grid * kPkvBlockRows * HD;
-    a.part_ml += (size_t)blockIdx.z * 2 * a.grid * kPkvBlockRows * 2;
-  }
+  const int lane = threadIdx.x & 31;
   const PkvPart p = a.part[2 * c0 + 1];
-  if (!(p.flags & 1)) return;
-  const int G = a.n_head / a.pool.n_kv, TB = kPkvBlockRows / G;
-  const PkvSeq seq = pkv_seq(a, a.pass, p.b);
+  const int G = a.n_head / a.pool.n_kv, TB = kPkvBlockRows / G, h = p.h;
+  const PkvSeq seq = pkv_seq(a, pass, p.b);
   PkvItem it;
-  pkv_block<kPkvTile>(a, a.pass, seq, TB, p.b, p.j, it);
-  const int rows = it.ntok * G, r0 = (blockIdx.y * 8 + (threadIdx.x >> 5)) * R;
-  // the run that ends the item
-  if (threadIdx.x == 0) s_last = a.grid - 1;
-  __syncthreads();
-  for (int k = c0 + 1 + threadIdx.x; k < a.grid; k += blockDim.x)
-    if (a.part[2 * k].flags & 2) atomicMin(&s_last, k);
-  __syncthreads();
-  const int last = s_last;
+  pkv_block<kPkvTile>(a, pass, seq, TB, p.b, p.j, it);
+  const int rows = it.ntok * G;
   if (r0 >= rows) return;
+  // the run that ends the item
+  const int end = (c0 / a.grid + 1) * a.grid;
+  int last = end - 1;
+  for (int k0 = c0 + 1; k0 < end; k0 += 32) {
+    const uint32_t ends = __ballot_sync(0xffffffffu, k0 + lane < end && (first[k0 + lane] & 2));
+    if (ends) {
+      last = k0 + __ffs(ends) - 1;
+      break;
+    }
+  }
   float m[R], sum[R], o[R][N] = {};
 #pragma unroll
   for (int i = 0; i < R; ++i) m[i] = -INFINITY;
   // a lane per part: references first, then factors
   for (int k0 = c0; k0 <= last; k0 += 32) {
     const int k = k0 + lane, slot = k == c0 ? 2 * k + 1 : 2 * k;
-    const bool has = k <= last && (a.part[slot].flags & 1);   // (a run may have no units)
+    const bool has = k <= last && ((k == c0 ? second[k] : first[k]) & 1);   // (a run may have no units)
 #pragma unroll
     for (int i = 0; i < R; ++i)
       if (has && r0 + i < rows) m[i] = fmaxf(m[i], a.part_ml[((int64_t)slot * kPkvBlockRows + r0 + i) * 2]);
@@ -706,7 +696,7 @@ __global__ void __launch_bounds__(256) k_pkv_join(const PkvAttnArgs args) {
   }
   for (int k0 = c0; k0 <= last; k0 += 32) {
     const int k = k0 + lane, slot = k == c0 ? 2 * k + 1 : 2 * k;
-    const bool has = k <= last && (a.part[slot].flags & 1);
+    const bool has = k <= last && ((k == c0 ? second[k] : first[k]) & 1);
     float f[R];
 #pragma unroll
     for (int i = 0; i < R; ++i) {
@@ -746,21 +736,65 @@ __global__ void __launch_bounds__(256) k_pkv_join(const PkvAttnArgs args) {
     const int r = r0 + i;
     sum[i] = warp_sum(sum[i]);
     if (r >= rows) break;
-    const int tok = it.tok0 + r / G, head = p.h * G + r % G;
-    if (a.pass != kPkvAll) {
+    const int tok = it.tok0 + r / G, head = h * G + r % G;
+    if (pass != kPkvAll) {
       const int64_t at = (int64_t)tok * a.n_head + head;
 #pragma unroll
-      for (int n = 0; n < N; ++n) a.row_o[a.pass - 1][at * HD + lane * N + n] = o[i][n];
-      if (lane == 0) *reinterpret_cast<float2 *>(a.row_ml[a.pass - 1] + at * 2) = make_float2(m[i], sum[i]);
+      for (int n = 0; n < N; ++n) a.row_o[pass - 1][at * HD + lane * N + n] = o[i][n];
+      if (lane == 0) *reinterpret_cast<float2 *>(a.row_ml[pass - 1] + at * 2) = make_float2(m[i], sum[i]);
     } else {
       pkv_store<N>(a.out, tok * a.out.token + head * a.out.head + lane * N, o[i], sum[i] == 0.f ? 0.f : 1.f / sum[i]);
     }
   }
 }
 
+// Adds up the parts of the items that several CTAs shared, in the list's order.  The
+// CTA whose run holds an item's first tiles has it in its second partial sum; the
+// runs behind it hold the rest in their first ones.  A warp takes four rows together, so
+// that the parts' loads are on their way at once.  Over a shared prefix the parts of both
+// passes are there, the own pass's CTAs behind the prefix's.  Blocks share out the items
+// that have something to add: chunks of 32 rows, chunks[pass] of them per item.
+template <int HD>
+__global__ void __launch_bounds__(256)
+    k_pkv_join(const __grid_constant__ PkvAttnArgs a, const int chunks0, const int chunks1) {
+  constexpr int R = 4, MAX = 2 * kPkvMaxCtas;
+  __shared__ uint8_t first[MAX], second[MAX];   // flags of the CTAs' partial sums
+  __shared__ uint16_t leaders[MAX];
+  __shared__ int n_leaders[2];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int passes = a.pass == kPkvAll ? 1 : 2, n = passes * a.grid;
+  pdl_wait();
+  pdl_trigger();
+  for (int k = threadIdx.x; k < n; k += 256) {
+    first[k] = (uint8_t)a.part[2 * k].flags;
+    second[k] = (uint8_t)a.part[2 * k + 1].flags;
+  }
+  __syncthreads();
+  if (warp == 0) {
+    int at = 0;
+    for (int k0 = 0; k0 < n; k0 += 32) {
+      const int k = k0 + lane;
+      const uint32_t is = __ballot_sync(0xffffffffu, k < n && (second[k] & 1));
+      if (is >> lane & 1) leaders[at + __popc(is & ((1u << lane) - 1))] = (uint16_t)k;
+      const uint32_t early = __ballot_sync(0xffffffffu, k < a.grid);
+      if (lane == 0 && k0 < a.grid) n_leaders[0] = at + __popc(is & early);
+      at += __popc(is);
+    }
+    if (lane == 0) n_leaders[1] = at;
+  }
+  __syncthreads();
+  const int items0 = n_leaders[0], work0 = items0 * chunks0, work = work0 + (n_leaders[1] - items0) * chunks1;
+  for (int i = blockIdx.x; i < work; i += gridDim.x) {
+    const int own = i >= work0, chunks = own ? chunks1 : chunks0, at = own ? i - work0 : i;
+    const int c0 = leaders[own * items0 + at / chunks], r0 = ((at % chunks) * 8 + warp) * R;
+    const int pass = a.pass == kPkvAll ? kPkvAll : kPkvPrefix + own;
+    join_rows<HD>(a, pass, c0, r0, first, second);
+  }
+}
+
 // Adds the two passes' parts of every row, a warp each.
 template <int HD>
-__global__ void __launch_bounds__(256) k_pkv_finish(const PkvAttnArgs a) {
+__global__ void __launch_bounds__(256) k_pkv_finish(const __grid_constant__ PkvAttnArgs a) {
   constexpr int N = HD / 32;
   const int lane = threadIdx.x & 31;
   const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
@@ -816,9 +850,18 @@ cudaError_t prepare() {
 
 cudaError_t launch_pkv_join(int hd, const PkvAttnArgs &a, int rows, cudaStream_t st) {
   const bool two = a.pass != kPkvAll;
-  const dim3 grid(a.grid, (rows + 31) / 32, two ? 2 : 1), block(256);
-  cudaError_t e = hd == 128 ? launch_pdl(k_pkv_join<128>, grid, block, 0, 1, st, a)
-                            : launch_pdl(k_pkv_join<64>, grid, block, 0, 1, st, a);
+  const dim3 block(256);
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(2 * a.grid);
+  cfg.blockDim = block;
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  const int chunks0 = (two ? kPkvBlockRows : rows) / 32, chunks1 = (rows + 31) / 32;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, hd == 128 ? k_pkv_join<128> : k_pkv_join<64>, a, two ? chunks0 : chunks1, chunks1);
   if (e != cudaSuccess || !two) return e;
   const dim3 all((unsigned)(((int64_t)a.seqs.n_tok * a.n_head + 7) / 8));
   return hd == 128 ? launch_pdl(k_pkv_finish<128>, all, block, 0, 1, st, a)
@@ -829,7 +872,7 @@ cudaError_t launch_pkv_join(int hd, const PkvAttnArgs &a, int rows, cudaStream_t
 // 1538 us; 16 packed prompts 325, 298, 291, 298; fp32, whose tiles take twice as long, 872, 848,
 // 869, 872.
 void pkv_rows_cost(int hd, bool split, int *unit_ns, int *item_units) {
-  *unit_ns = (split ? 2400 : 1500) * (hd == 128 ? 2 : 1) / 2;
+  *unit_ns = (split ? 4000 : 1800) * (hd == 128 ? 2 : 1) / 2;
   *item_units = split ? 4 : 6;
 }
 

@@ -82,7 +82,7 @@ __device__ __forceinline__ void load_q2(const DevRows &q, int64_t at, uint32_t &
 
 template <int HD, int RB>
 __global__ void __launch_bounds__(kThreads, 1)
-    k_pkv_step(const __grid_constant__ CUtensorMap kvmap, const PkvAttnArgs a) {
+    k_pkv_step(const __grid_constant__ CUtensorMap kvmap, const __grid_constant__ PkvAttnArgs a) {
   typedef SL<HD, RB> L;
   constexpr int NS = L::NS, KS = HD / 16, NT = HD / 8;
   static_assert(NS >= 2 && L::SMEM <= 232448, "ring");
@@ -379,7 +379,7 @@ cudaError_t prepare_pkv_step(int hd) {
 
 // a chunk at the GPU's copy rate, shared out over its SMs
 void pkv_step_cost(int hd, int *unit_ns, int *item_units) {
-  *unit_ns = hd == 128 ? 800 : 400;
+  *unit_ns = hd == 128 ? 700 : 350;
   *item_units = 4;
 }
 
