@@ -75,8 +75,9 @@ enum {
 enum {
   PNB_DEV_ERR_TOKEN = 1,   /* a token from device memory was out of range; id 0 was used */
   PNB_DEV_ERR_TIMEOUT = 2, /* a bounded wait inside a kernel expired; results are invalid */
-  PNB_DEV_ERR_FULL = 4,    /* pnb_kvq_append: rows past the cache's capacity were not stored */
-  PNB_DEV_ERR_RANGE = 8    /* pnb_kvq_append: a start or count from device memory was out of range */
+  PNB_DEV_ERR_FULL = 4,    /* pnb_kvq_append, pnb_pkv_append: rows past the capacity were not stored */
+  PNB_DEV_ERR_RANGE = 8    /* pnb_kvq_append: a start or count from device memory was out of range;
+                              pnb_pkv_*: a length, count, group or page id was */
 };
 
 /* Model dimensions: the config fields of the pages ("Engine Architecture",
@@ -557,16 +558,17 @@ int pnb_kvq_check(pnb_kvq *c, int32_t *device_error);
    Entry i of a sequence lies in row i % page of the page that the sequence's
    page table names at i / page.  Keys are held after RoPE.  What the pool's
    other rows hold (rows behind a sequence's last entry, free pages) does not
-   matter, be it NaN or infinity; the entries of a sequence themselves are
-   finite (the rows of a call that share 128 entries of a sequence, one of which
-   holds a NaN or an infinity, may all answer NaN).
+   matter, be it NaN or infinity, and one among a sequence's own entries reaches
+   the tokens that attend to it and no others.
 
    All calls are stream-ordered, allocate nothing and may be captured into a CUDA
    graph: page tables, lengths and token counts are read on the device.  The
-   library allocates the cache's workspace in pnb_pkv_new (partial sums, about
-   40 MB; with shared_tok n_head * (head_dim + 2) * 4 bytes per token more);
-   calls on one cache share it, so at most one attention call may be in flight
-   per cache, on any stream, graphs included. */
+   library allocates the cache's workspace in pnb_pkv_new (partial sums, 512
+   rows of head_dim fp32 per SM, about 40 MB; with shared_tok as much again and
+   n_head * (head_dim + 2) * 8 bytes per token); calls on one cache share it, so
+   at most one attention call may be in flight per cache, on any stream, graphs
+   included.  Errors found on the device (PNB_DEV_ERR_FULL, _RANGE, _TIMEOUT)
+   set bits that pnb_pkv_check reads. */
 typedef struct {
   int32_t n_layer, n_page, page;  /* pages per layer; entries per page: 16, 32, 64 or 128 */
   int32_t n_head, n_kv_head;      /* n_head % n_kv_head == 0, at most 64 query heads per KV head */
@@ -636,9 +638,11 @@ int pnb_pkv_attention(pnb_pkv *c, int32_t layer, const pnb_pkv_batch *b, int32_t
    group_start[g] .. group_start[g + 1] - 1 (device int32 [n_group + 1], from 0
    to n_seq, not decreasing), whose page tables name the same pages for their
    first prefix[g] entries (device int32 [n_group], rounded down to whole pages,
-   at most len - n of every sequence of the group).  Each group's prefix is read
-   once for all its tokens.  Every sequence has n_tok / n_seq tokens
-   (start_dev NULL).  n_tok <= shared_tok (PNB_E_INVAL). */
+   at most len - n of every sequence of the group: what is said beyond that is
+   cut off).  Each group's prefix is read once for all its tokens; batches whose
+   page tables have room for less than 256 MB of K and V go sequence by sequence,
+   which is faster for them.  Every sequence has n_tok / n_seq tokens (start_dev
+   NULL).  n_tok <= shared_tok (PNB_E_INVAL). */
 int pnb_pkv_attention_shared(pnb_pkv *c, int32_t layer, const pnb_pkv_batch *b, int32_t n_group,
                              const int32_t *group_start_dev, const int32_t *prefix_dev, int32_t n_tok,
                              const pnb_rows *q, const pnb_rows *out, int32_t window, pnb_stream stream);

@@ -10,9 +10,6 @@
 #include "pnb_tmap.cuh"
 
 using namespace pnb;
-#ifndef DIRECT_MB
-#define DIRECT_MB 200
-#endif
 
 struct pnb_pkv {
   pnb_pkv_config cfg;
@@ -105,11 +102,13 @@ int check_tokens(const pnb_pkv *c, const pnb_rows *r, int n_tok, int heads, bool
 }
 
 // Up to this many rows (tokens x query heads of a KV head) of every sequence go
-// through the kernel for steps.
+// through the kernel for steps (its registers hold 16).
 constexpr int kStepRows = 16;
-// A batch whose page tables name no more than this goes sequence by sequence, shared prefix or
-// not: the pages that sequences share come from L2.
-constexpr int64_t kDirectBytes = (int64_t)DIRECT_MB << 20;
+// A batch whose page tables have room for no more than this goes sequence by sequence, shared
+// prefix or not: the pages that sequences share come from L2, at some 11 TB/s, and one kernel
+// and its join take less than two passes.  Single tokens of 32 / 8 heads, head_dim 128, tables
+// of 10, 75, 151, 285, 302, 2416 MB: 15, 21, 29, 41, 45, 224 us against 32, 33, 37, 37, 42, 89.
+constexpr int64_t kDirectBytes = (int64_t)256 << 20;
 
 int attend(pnb_pkv *c, int32_t layer, const pnb_pkv_batch *b, int32_t n_group, const int32_t *group_start,
            const int32_t *prefix, int32_t n_tok, const pnb_rows *q, const pnb_rows *out, int32_t window,

@@ -765,11 +765,13 @@ __global__ void __launch_bounds__(256)
   const int passes = a.pass == kPkvAll ? 1 : 2, n = passes * a.grid;
   pdl_wait();
   pdl_trigger();
+  int any = 0;
   for (int k = threadIdx.x; k < n; k += 256) {
     first[k] = (uint8_t)a.part[2 * k].flags;
     second[k] = (uint8_t)a.part[2 * k + 1].flags;
+    any |= second[k] & 1;
   }
-  __syncthreads();
+  if (!__syncthreads_or(any)) return;
   if (warp == 0) {
     int at = 0;
     for (int k0 = 0; k0 < n; k0 += 32) {

@@ -117,9 +117,8 @@ __device__ __forceinline__ long long floor_sum(uint32_t n, uint32_t m, uint32_t 
 __device__ __forceinline__ int pkv_blocks(const PkvSeq &s, int TB) { return (s.n + TB - 1) / TB; }
 
 // units of a sequence's first J blocks, per KV head; `each` of them for an item's start and end
-// (not inlined: a kernel's start is bound by fetching its instructions)
 template <int TILE>
-__device__ __noinline__ long long pkv_units(const PkvAttnArgs &a, int pass, int each, const PkvSeq &s, int TB, int J) {
+__device__ __forceinline__ long long pkv_units(const PkvAttnArgs &a, int pass, int each, const PkvSeq &s, int TB, int J) {
   if (J <= 0) return 0;
   PkvItem it;
   if (pass == kPkvPrefix) {
