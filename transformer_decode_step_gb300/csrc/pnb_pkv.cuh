@@ -59,7 +59,9 @@ constexpr int kPkvBoxLog2 = 6;          // rows of a TMA box: a page's, at most 
 enum { kPkvAll = 0, kPkvPrefix = 1, kPkvOwn = 2 };
 constexpr int kPkvTile = 128;          // of the prompts' kernel
 constexpr int kPkvChunk = 64;          // of the steps' kernel
-constexpr int kPkvBlockRows = 256;
+constexpr int kPkvBlockRows = 256;     // at most; see pkv_block_rows
+// rows of a block of the prompts' kernel
+__host__ __device__ constexpr int pkv_block_rows(int hd, bool split) { return split && hd == 128 ? 128 : 256; }
 
 // what a CTA left of an item that others share
 struct PkvPart {
@@ -91,6 +93,7 @@ struct PkvAttnArgs {
   float *part_o, *part_ml;              // [2 grid][kPkvBlockRows][head_dim], [..][2]
   PkvPart *part;                        // [2 grid]
   int32_t grid;
+  int32_t block_rows;
   int32_t heads_inner;                  // the list's order (set by the launchers)
   // what an item costs beside its tiles, in tiles, and a tile's time on an SM; the same of the
   // pass beside this one, and its tiles' entries (set by the launchers)

@@ -133,6 +133,7 @@ int attend(pnb_pkv *c, int32_t layer, const pnb_pkv_batch *b, int32_t n_group, c
   a.part_o = c->part_o;
   a.part_ml = c->part_ml;
   a.grid = c->sms;
+  a.block_rows = pkv_block_rows(g.head_dim, pkv_split(a));
   a.pass = kPkvAll;
   const CUtensorMap &map = c->maps[layer];
   const int group = g.n_head / g.n_kv_head;

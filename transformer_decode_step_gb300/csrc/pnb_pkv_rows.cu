@@ -20,10 +20,13 @@
 // A NaN or an infinity among a sequence's own values reaches, through tiles that a block's
 // rows see only in part, rows that do not attend to it: a row whose output is not finite
 // is done again by itself where such a value lies.
-// Tensor memory (512 columns): S of both halves (128 each), O of both halves.
+// Tensor memory (512 columns): S of both halves (128 each), O of both halves, with SPLIT
+// beside each half's O the sum over the tiles before.
 //
-// fp32 on either side (SPLIT): Q and P enter as two bf16 numbers, high and low part, in
-// twice the products.
+// fp32 on either side (SPLIT): Q enters as three bf16 numbers (24 bits: a score's error is
+// its weight's relative one, and with two of them 60k entries with scores of some tens came
+// out 5e-5 off), P as two, in 5/2 times the products.  At head_dim 128 a block is then
+// 128 rows, whose softmax has nothing to run beside.
 #include <cuda_bf16.h>
 #include <math.h>
 
@@ -58,14 +61,23 @@ struct RingAt {
   }
 };
 
+// With SPLIT the products' sums start anew every so many tiles, and are added up outside: the
+// matrix unit cuts off what it adds, always towards zero, and over 475 tiles outputs came out
+// 5e-5 too small.
+constexpr int kFold = 4;
+
 template <int HD, bool SPLIT>
 struct RL {
   static constexpr int NB = HD / 64;                        // 64-column boxes of a row
   static constexpr int BOX = kPkvTile * 128;                // bytes of a 128-row box
   static constexpr int UNIT = NB * BOX;                     // a K or V tile
-  static constexpr int QHALF = UNIT * (SPLIT ? 2 : 1);      // Q of 128 rows (high, then low parts)
-  static constexpr int NU = (229376 - 2 * QHALF) / UNIT;    // ring units
-  static constexpr int SMEM = 1024 + 2 * QHALF + NU * UNIT + 1024;
+  // fp32 on either side: queries of three bf16 parts, for which one half of rows leaves room at
+  // head_dim 128
+  static constexpr int HALVES = pkv_block_rows(HD, SPLIT) / 128;
+  static constexpr int PARTS = SPLIT ? 3 : 1;
+  static constexpr int QHALF = UNIT * PARTS;                // Q of 128 rows, part by part
+  static constexpr int NU = (229376 - HALVES * QHALF) / UNIT;   // ring units
+  static constexpr int SMEM = 1024 + HALVES * QHALF + NU * UNIT + 1024;
 };
 
 struct RBars {
@@ -74,12 +86,12 @@ struct RBars {
 };
 static_assert(sizeof(RBars) <= 1024, "barriers");
 
-// S = Q K^T of one half and tile: hd / 16 products (twice with SPLIT)
+// S = Q K^T of one half and tile: hd / 16 products (three times with SPLIT)
 template <int HD, bool SPLIT, int I = 0>
 __device__ __forceinline__ void products_s(uint32_t d, uint64_t q, uint64_t k) {
   typedef RL<HD, SPLIT> L;
   constexpr int KS = HD / 16, part = I / KS, c = I % KS / 4, x = I % 4;
-  if constexpr (I < (SPLIT ? 2 : 1) * KS) {
+  if constexpr (I < L::PARTS * KS) {
     mma_bf16_off<(part * L::UNIT + c * L::BOX + x * 32) / 16, (c * L::BOX + x * 32) / 16>(
         d, q, k, idesc_bf16_f32(128, kPkvTile), I > 0);
     products_s<HD, SPLIT, I + 1>(d, q, k);
@@ -96,11 +108,20 @@ __device__ __forceinline__ void products_o(uint32_t d, uint32_t p, uint64_t v, b
   }
 }
 
-// 8 elements of a query row as bf16, and what the rounding left
-__device__ __forceinline__ void split8(const float4 &a, const float4 &b, uint4 &hi, uint4 &lo) {
-  hi = make_uint4(pack_bf16(a.x, a.y), pack_bf16(a.z, a.w), pack_bf16(b.x, b.y), pack_bf16(b.z, b.w));
-  lo = make_uint4(pack_bf16(a.x - bf16lo(hi.x), a.y - bf16hi(hi.x)), pack_bf16(a.z - bf16lo(hi.y), a.w - bf16hi(hi.y)),
-                  pack_bf16(b.x - bf16lo(hi.z), b.y - bf16hi(hi.z)), pack_bf16(b.z - bf16lo(hi.w), b.w - bf16hi(hi.w)));
+// 8 elements of a query row as three bf16 parts each, what a rounding leaves in the next
+__device__ __forceinline__ void split8(const float4 &a, const float4 &b, uint4 (&part)[3]) {
+  float f[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+  for (int p = 0; p < 3; ++p) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      w[i] = pack_bf16(f[2 * i], f[2 * i + 1]);
+      f[2 * i] -= bf16lo(w[i]);
+      f[2 * i + 1] -= bf16hi(w[i]);
+    }
+    part[p] = make_uint4(w[0], w[1], w[2], w[3]);
+  }
 }
 
 // Whether a value that some row of a block sees and another does not is NaN or infinite
@@ -133,10 +154,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr int NU = L::NU;
   static_assert(NU <= 16 && NU >= 2, "ring");
   uint8_t *sm = r_smem + ((1024u - (smem_addr(r_smem) & 1023u)) & 1023u);
-  uint8_t *Q = sm, *ring = sm + 2 * L::QHALF;
+  uint8_t *Q = sm, *ring = sm + L::HALVES * L::QHALF;
   RBars &bar = *reinterpret_cast<RBars *>(ring + NU * L::UNIT);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int G = a.n_head / a.pool.n_kv, TB = kPkvBlockRows / G;
+  const int G = a.n_head / a.pool.n_kv, TB = a.block_rows / G;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < NU; ++i) {
@@ -277,7 +298,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!ok) break;
             tc_fence_after();
             if (elect_one()) {
-              products_o<HD, SPLIT, 0>(tmem + 256 + w * 128, tmem + w * 128, v0 + v.s * (L::UNIT >> 4), t == 0);
+              products_o<HD, SPLIT, 0>(tmem + 256 + w * 128, tmem + w * 128, v0 + v.s * (L::UNIT >> 4),
+                                      SPLIT ? t % kFold == 0 : t == 0);
               mma_commit(&bar.pv_half[w]);
             }
             __syncwarp();
@@ -381,7 +403,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr int B = QR < 8 ? QR : 8;
 #pragma unroll 1
         for (int k = 0; k < QR; k += B) {
-          uint4 hi[B], lo[B];
           if (q32) {
             float4 f[B][2];
 #pragma unroll
@@ -391,18 +412,23 @@ __global__ void __launch_bounds__(kThreads, 1)
               f[i][1] = p[1];
             }
 #pragma unroll
-            for (int i = 0; i < B; ++i) split8(f[i][0], f[i][1], hi[i], lo[i]);
+            for (int i = 0; i < B; ++i) {
+              uint4 part[3];
+              split8(f[i][0], f[i][1], part);
+#pragma unroll
+              for (int p = 0; p < 3; ++p) put(k + i, part[p], p);
+            }
           } else {
+            uint4 hi[B];
+#pragma unroll
+            for (int i = 0; i < B; ++i)
+              hi[i] = reinterpret_cast<const uint4 *>((uintptr_t)of_lane(q_row, (k + i) * RPW + qsub))[ql];
 #pragma unroll
             for (int i = 0; i < B; ++i) {
-              hi[i] = reinterpret_cast<const uint4 *>((uintptr_t)of_lane(q_row, (k + i) * RPW + qsub))[ql];
-              lo[i] = make_uint4(0, 0, 0, 0);
+              put(k + i, hi[i], 0);
+              put(k + i, make_uint4(0, 0, 0, 0), 1);
+              put(k + i, make_uint4(0, 0, 0, 0), 2);
             }
-          }
-#pragma unroll
-          for (int i = 0; i < B; ++i) {
-            put(k + i, hi[i], 0);
-            put(k + i, lo[i], 1);
           }
         }
       }
@@ -445,6 +471,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
         tc_fence_after();
+        if (SPLIT && t > it.ta && (t - it.ta) % kFold == 0) {
+          // the products of the tiles so far are done: S of this one came behind them
+#pragma unroll 1
+          for (int i = 0; i < HD; i += 32) {
+            float o[32], all[32];
+            tmem_ld32_async(to + i, o);
+            tmem_ld32_async(to + HD + i, all);
+            tmem_wait_ld();
+            tmem_landed(o);
+            tmem_landed(all);
+#pragma unroll
+            for (int k = 0; k < 32; ++k) all[k] = t - it.ta == kFold ? o[k] : all[k] + o[k];
+            tmem_st32_async(to + HD + i, reinterpret_cast<const uint32_t *>(all));
+          }
+        }
         // The row's 128 scores in two halves: the products of the first begin beside the
         // second one's exponentials.
         const int e = (it.t0 + t) * kPkvTile;
@@ -506,8 +547,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 tc_fence_after();
 #pragma unroll 1
-                for (int i = 0; i < HD; i += 32) {
+                for (int i = 0; i < (SPLIT && t - it.ta >= kFold ? 2 * HD : HD); i += 32) {
                   float o[32];
+                  tmem_wait_st();
                   tmem_ld32_async(to + i, o);
                   tmem_wait_ld();
                   tmem_landed(o);
@@ -578,6 +620,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_ld32_async(to + i, o);
             tmem_wait_ld();
             tmem_landed(o);
+            if (SPLIT && it.tb - it.ta > kFold) {
+              float all[32];
+              tmem_ld32_async(to + HD + i, all);
+              tmem_wait_ld();
+              tmem_landed(all);
+#pragma unroll
+              for (int k = 0; k < 32; ++k) o[k] += all[k];
+            }
 #pragma unroll
             for (int k = 0; k < 32; ++k) z = fmaf(o[k], 0.f, z);
             if (mine) {
@@ -662,7 +712,7 @@ __device__ __forceinline__ void join_rows(const PkvAttnArgs &a, int pass, int c0
   constexpr int N = HD / 32, R = 4;
   const int lane = threadIdx.x & 31;
   const PkvPart p = a.part[2 * c0 + 1];
-  const int G = a.n_head / a.pool.n_kv, TB = kPkvBlockRows / G, h = p.h;
+  const int G = a.n_head / a.pool.n_kv, TB = a.block_rows / G, h = p.h;
   const PkvSeq seq = pkv_seq(a, pass, p.b);
   PkvItem it;
   pkv_block<kPkvTile>(a, pass, seq, TB, p.b, p.j, it);

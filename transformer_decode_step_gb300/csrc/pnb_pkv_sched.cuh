@@ -252,7 +252,7 @@ __device__ __forceinline__ long long pkv_other_work(const PkvAttnArgs &a, long l
   long long mine = 0, all;
   for (int b = threadIdx.x; b < n; b += THREADS) {
     const PkvSeq s = pkv_seq(a, pass, b);
-    const int TB = a.other_tile == kPkvTile ? kPkvBlockRows / (a.n_head / a.pool.n_kv) : a.seqs.each;
+    const int TB = a.other_tile == kPkvTile ? a.block_rows / (a.n_head / a.pool.n_kv) : a.seqs.each;
     mine += a.other_tile == kPkvTile ? pkv_units<kPkvTile>(a, pass, a.other_item_units, s, TB, pkv_blocks(s, TB))
                                      : pkv_units<kPkvChunk>(a, pass, a.other_item_units, s, TB, pkv_blocks(s, TB));
   }

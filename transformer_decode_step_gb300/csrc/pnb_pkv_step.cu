@@ -5,7 +5,8 @@
 // instructions m16n8k16 take rows 0-7 of A as the rows' bf16 high parts and rows 8-15 as
 // their low parts, of the queries in S = Q K^T and of the softmax weights in O = P V: the
 // 16 rows that the instruction has anyway give 16 bits of both operands, and a lane
-// holds a row's high and low sums side by side.  tcgen05's 128 rows would be empty but
+// holds a row's high and low sums side by side.  (fp32 queries' third parts take a second
+// instruction.)  tcgen05's 128 rows would be empty but
 // for these.
 //
 // One CTA per SM, eight compute warps and one that loads.  The list of all (sequence, KV
@@ -68,15 +69,17 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// two neighbouring elements of a query row: high parts, low parts
-__device__ __forceinline__ void load_q2(const DevRows &q, int64_t at, uint32_t &hi, uint32_t &lo) {
+// two neighbouring elements of a query row: high parts, low parts and the rest
+__device__ __forceinline__ void load_q2(const DevRows &q, int64_t at, uint32_t &hi, uint32_t &lo, uint32_t &rest) {
   if (q.dtype == PNB_BF16) {
     hi = *reinterpret_cast<const uint32_t *>(static_cast<const __nv_bfloat16 *>(q.p) + at);
-    lo = 0;
+    lo = rest = 0;
   } else {
     const float2 f = *reinterpret_cast<const float2 *>(static_cast<const float *>(q.p) + at);
     hi = pack_bf16(f.x, f.y);
-    lo = pack_bf16(f.x - bf16lo(hi), f.y - bf16hi(hi));
+    const float x = f.x - bf16lo(hi), y = f.y - bf16hi(hi);
+    lo = pack_bf16(x, y);
+    rest = pack_bf16(x - bf16lo(lo), y - bf16hi(lo));
   }
 }
 
@@ -162,13 +165,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const int half = warp >> 2, p0 = (warp & 3) * 16;   // this warp's entries of a chunk
   const int g = lane >> 2, c = lane & 3;
+  const bool q32 = a.q.dtype == PNB_F32;
   uint32_t u = 0, item = 0;
   bool ok = true;
   while (walk.next<kChunk>(a, a.seqs.each, it)) {
     ++item;
     const int rows = it.ntok * G;
     // queries as A operands, and the entries that each row sees
-    uint32_t aq[RB][KS][4];
+    uint32_t aq[RB][KS][4], ar[RB][KS][2];
     int lo[RB], hi[RB];
 #pragma unroll
     for (int b = 0; b < RB; ++b) {
@@ -177,8 +181,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int64_t at = tok * a.q.token + head * a.q.head + 2 * c;
 #pragma unroll
       for (int k = 0; k < KS; ++k) {
-        load_q2(a.q, at + 16 * k, aq[b][k][0], aq[b][k][1]);
-        load_q2(a.q, at + 16 * k + 8, aq[b][k][2], aq[b][k][3]);
+        load_q2(a.q, at + 16 * k, aq[b][k][0], aq[b][k][1], ar[b][k][0]);
+        load_q2(a.q, at + 16 * k + 8, aq[b][k][2], aq[b][k][3], ar[b][k][1]);
       }
       const int last = it.base + rr / G;
       hi[b] = last + 1;
@@ -218,6 +222,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int b = 0; b < RB; ++b) {
           mma16816(sc[b][0], aq[b][k], kb[0], kb[1]);
           mma16816(sc[b][1], aq[b][k], kb[2], kb[3]);
+          if (q32) {
+            const uint32_t rest[4] = {ar[b][k][0], 0, ar[b][k][1], 0};
+            mma16816(sc[b][0], rest, kb[0], kb[1]);
+            mma16816(sc[b][1], rest, kb[2], kb[3]);
+          }
         }
       }
       if (masked) {
