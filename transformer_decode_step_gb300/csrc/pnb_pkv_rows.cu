@@ -23,10 +23,9 @@
 // Tensor memory (512 columns): S of both halves (128 each), O of both halves, with SPLIT
 // beside each half's O the sum over the tiles before.
 //
-// fp32 on either side (SPLIT): Q enters as three bf16 numbers (24 bits: a score's error is
-// its weight's relative one, and with two of them 60k entries with scores of some tens came
-// out 5e-5 off), P as two, in 5/2 times the products.  At head_dim 128 a block is then
-// 128 rows, whose softmax has nothing to run beside.
+// fp32 on either side (SPLIT): Q enters as three bf16 numbers (24 bits: a score's error is its
+// weight's relative one), P as two, in 5/2 times the products.  At head_dim 128 there is room for
+// the queries of 128 rows: warps 4-7 idle, and S of two tiles takes both halves' columns.
 #include <cuda_bf16.h>
 #include <math.h>
 
@@ -257,7 +256,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // is known at compile time.
       const uint64_t q0 = desc_k_sw128(Q, 0), k0 = desc_k_sw128(ring, 0), v0 = desc_mn_sw128(ring, L::BOX);
       bool ok = true;
-      uint32_t nq[2] = {0, 0}, np[2] = {0, 0}, nv = 0;
+      uint32_t nq[2] = {0, 0}, np[2] = {0, 0}, nv = 0, n_s = 0;
       RingAt<NU> at;
       auto wait = [&](uint64_t *b, uint32_t parity) { return __all_sync(0xffffffffu, mbar_wait(b, parity)) != 0; };
       while (ok && __all_sync(0xffffffffu, walk.next<kPkvTile>(a, TB, it))) {
@@ -266,6 +265,61 @@ __global__ void __launch_bounds__(kThreads, 1)
         // tiles from this one on reach behind the sequence's last entry (a prefix is whole pages, and
         // what lies behind in its last tile reads as zero)
         const int past = __shfl_sync(0xffffffffu, a.pass == kPkvPrefix ? INT_MAX : it.len / kPkvTile - it.t0 - it.ta, 0);
+        if constexpr (L::HALVES == 1) {
+          // One half: S of the next two tiles lies in tensor memory before a tile's p is there, so
+          // that the softmax goes from tile to tile and the products run beside it.
+          RingAt<NU> k = at, v = at;   // a tile's K and V lie side by side in the ring
+          v.next();
+          auto issue_s = [&]() {
+            ok = wait(&bar.full[k.s], k.turn);
+            if (!ok) return;
+            tc_fence_after();
+            if (elect_one()) {
+              products_s<HD, SPLIT>(tmem + (n_s & 1) * 128, q0, k0 + k.s * (L::UNIT >> 4));
+              mma_commit(&bar.s_full[n_s & 1]);
+              mma_commit(&bar.empty[k.s]);
+            }
+            __syncwarp();
+            ++n_s;
+            k.next();
+            k.next();
+          };
+          ok = wait(&bar.q_ready[0], nq[0]++ & 1);
+          if (ok) issue_s();
+          if (ok && tiles > 1) issue_s();
+          for (int t = 0; t < tiles && ok; ++t) {
+            ok = wait(&bar.full[v.s], v.turn);
+            if (ok && t >= past) {
+              if (elect_one()) mbar_arrive(&bar.v_go);
+              ok = wait(&bar.v_ok, nv++ & 1);
+            }
+            // (a p_ready for each of the two S: a warp may be a tile ahead of the others)
+            const uint32_t i = np[0] & 1, turn = np[0]++ >> 1 & 1, p = tmem + i * 128;
+            if (ok) ok = wait(&bar.p_ready[i][0], turn);
+            if (!ok) break;
+            tc_fence_after();
+            if (elect_one()) {
+              products_o<HD, SPLIT, 0>(tmem + 256, p, v0 + v.s * (L::UNIT >> 4), t % kFold == 0);
+              mma_commit(&bar.pv_half[0]);
+            }
+            __syncwarp();
+            ok = wait(&bar.p_ready[i][1], turn);
+            if (!ok) break;
+            tc_fence_after();
+            if (elect_one()) {
+              products_o<HD, SPLIT, 1>(tmem + 256, p, v0 + v.s * (L::UNIT >> 4), false);
+              mma_commit(&bar.pv_half[1]);   // (of the whole tile)
+              mma_commit(&bar.empty[v.s]);
+              if (t + 1 == tiles) mma_commit(&bar.o_full[0]);
+            }
+            __syncwarp();
+            v.next();
+            v.next();
+            if (t + 2 < tiles) issue_s();
+          }
+          at = k;
+          continue;
+        }
         ok = wait(&bar.full[at.s], at.turn);
 #pragma unroll
         for (int w = 0; w < 2; ++w) {
@@ -361,7 +415,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
     const int w = warp >> 2, quad = warp & 3, r = (warp << 5) + lane;   // r: row of the block
     const uint32_t lanes = (uint32_t)(32 * quad) << 16;
-    const uint32_t ts = tmem + w * 128 + lanes, to = tmem + 256 + w * 128 + lanes;
+    constexpr bool ALONE = L::HALVES == 1;   // S of consecutive tiles in either half's columns
+    const uint32_t ts0 = tmem + w * 128 + lanes, to = tmem + 256 + w * 128 + lanes;
     const float c = a.qscale;
     // row / G as the high half of a product: exact for rows below 2^16 and G up to 64
     const uint32_t g_inv = (uint32_t)((0x100000000ull + G - 1) / G);
@@ -465,27 +520,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       float m = -INFINITY, sum = 0.f;
       for (int t = it.ta; t < it.tb; ++t) {
-        if (!mbar_wait(&bar.s_full[w], ns++ & 1)) {
+        const uint32_t ts = ts0 + (ALONE ? (ns & 1) * 128 : 0);
+        if (!mbar_wait(&bar.s_full[ALONE ? ns & 1 : w], (ALONE ? ns >> 1 : ns) & 1)) {
           ok = false;
           break;
         }
+        ++ns;
         __syncwarp();
         tc_fence_after();
-        if (SPLIT && t > it.ta && (t - it.ta) % kFold == 0) {
-          // the products of the tiles so far are done: S of this one came behind them
-#pragma unroll 1
-          for (int i = 0; i < HD; i += 32) {
-            float o[32], all[32];
-            tmem_ld32_async(to + i, o);
-            tmem_ld32_async(to + HD + i, all);
-            tmem_wait_ld();
-            tmem_landed(o);
-            tmem_landed(all);
-#pragma unroll
-            for (int k = 0; k < 32; ++k) all[k] = t - it.ta == kFold ? o[k] : all[k] + o[k];
-            tmem_st32_async(to + HD + i, reinterpret_cast<const uint32_t *>(all));
-          }
-        }
         // The row's 128 scores in two halves: the products of the first begin beside the
         // second one's exponentials.
         const int e = (it.t0 + t) * kPkvTile;
@@ -544,6 +586,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // Outputs so far go to the new reference.  The products of the tile before are
                 // done, S of this one came behind them; those of its first half end first.
                 if (h && !mbar_wait(&bar.pv_half[w], (ns - 1) & 1)) ok = false;
+                if (ALONE && !h && !mbar_wait(&bar.pv_half[1], ns & 1)) ok = false;
                 __syncwarp();
                 tc_fence_after();
 #pragma unroll 1
@@ -562,10 +605,29 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           sum += part;
+          if (SPLIT && h == 0 && t > it.ta && (t - it.ta) % kFold == 0) {
+            // the products of the tiles so far (done: S of this one came behind them) go to the
+            // sum, and this tile's start anew
+            if (ALONE && !mbar_wait(&bar.pv_half[1], ns & 1)) ok = false;
+            __syncwarp();
+            tc_fence_after();
+#pragma unroll 1
+            for (int i = 0; i < HD; i += 32) {
+              float o[32], all[32];
+              tmem_ld32_async(to + i, o);
+              tmem_ld32_async(to + HD + i, all);
+              tmem_wait_ld();
+              tmem_landed(o);
+              tmem_landed(all);
+#pragma unroll
+              for (int k = 0; k < 32; ++k) all[k] = t - it.ta == kFold ? o[k] : all[k] + o[k];
+              tmem_st32_async(to + HD + i, reinterpret_cast<const uint32_t *>(all));
+            }
+          }
           tmem_wait_st();
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&bar.p_ready[w][h]);
+          if (lane == 0) mbar_arrive(&bar.p_ready[ALONE ? (ns - 1) & 1 : w][h]);
         }
       }
       if (!ok) break;
