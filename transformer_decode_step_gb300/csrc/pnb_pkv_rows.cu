@@ -24,8 +24,18 @@
 // beside each half's O the sum over the tiles before.
 //
 // fp32 on either side (SPLIT): Q enters as three bf16 numbers (24 bits: a score's error is its
-// weight's relative one), P as two, in 5/2 times the products.  At head_dim 128 there is room for
-// the queries of 128 rows: warps 4-7 idle, and S of two tiles takes both halves' columns.
+// weight's relative one), P as two (16 bits and the sign: 2^-18 of a weight at most), in 5/2
+// times the products.  At head_dim 128 that leaves room for the queries of 128 rows: warps 4-7
+// idle, S of two tiles takes both halves' columns, and the products of S run ahead of the softmax
+// (8k prompt under a window of 4096: 1468 us one tile at a time, 1146 so).
+//
+// Bound by the tensor rate and, beside it, by the softmax: a tile's S and O take 2048 cycles for
+// the two halves at head_dim 128, the exponentials, conversions and sums of 64 scores 367 cycles
+// of a scheduler (654 for two warps).  A 16k prompt (32 / 8 heads, head_dim 128, bf16) takes
+// 1575 us, 1.40 PFLOP/s or 71 % of cuBLAS's bf16 rate on the same part; 512 tokens behind 60k
+// entries 371 us, 69 %; DRAM is idle (2 %), K and V come from L2 (94 %).
+// Not kept: two threads per row (16 softmax warps meet at a barrier per tile: 2078 against 1661),
+// an issuing thread per half (2145), a warp that serves whichever half is ready (2077).
 #include <cuda_bf16.h>
 #include <math.h>
 
@@ -85,11 +95,12 @@ struct RBars {
 };
 static_assert(sizeof(RBars) <= 1024, "barriers");
 
-// S = Q K^T of one half and tile: hd / 16 products (three times with SPLIT)
+// S = Q K^T of one half and tile: hd / 16 products (three times with SPLIT, the smallest part
+// first: a product cuts off what it adds to a large sum, and to a small one next to nothing)
 template <int HD, bool SPLIT, int I = 0>
 __device__ __forceinline__ void products_s(uint32_t d, uint64_t q, uint64_t k) {
   typedef RL<HD, SPLIT> L;
-  constexpr int KS = HD / 16, part = I / KS, c = I % KS / 4, x = I % 4;
+  constexpr int KS = HD / 16, part = L::PARTS - 1 - I / KS, c = I % KS / 4, x = I % 4;
   if constexpr (I < L::PARTS * KS) {
     mma_bf16_off<(part * L::UNIT + c * L::BOX + x * 32) / 16, (c * L::BOX + x * 32) / 16>(
         d, q, k, idesc_bf16_f32(128, kPkvTile), I > 0);
@@ -982,11 +993,12 @@ cudaError_t launch_pkv_join(int hd, const PkvAttnArgs &a, int rows, cudaStream_t
                    : launch_pdl(k_pkv_finish<64>, all, block, 0, 1, st, a);
 }
 
-// An item's start and end against a tile's time.  16k prompt at 2, 4, 6, 8 units: 1625, 1544, 1523,
-// 1538 us; 16 packed prompts 325, 298, 291, 298; fp32, whose tiles take twice as long, 872, 848,
-// 869, 872.
+// A tile's time, for the shares of a prefix's and the own pass, and an item's start and end against
+// it.  16k prompt at 2, 4, 6, 8 units: 1625, 1544, 1523, 1538 us; 16 packed prompts 325, 298, 291,
+// 298; fp32, whose tiles take twice as long, 872, 848, 869, 872.  64 slots behind a shared 8k prefix
+// with fp32 at 2600, 3200, 4000 ns: 100, 103, 114 us.
 void pkv_rows_cost(int hd, bool split, int *unit_ns, int *item_units) {
-  *unit_ns = (split ? 4000 : 1800) * (hd == 128 ? 2 : 1) / 2;
+  *unit_ns = hd == 128 ? (split ? 2600 : 1800) : (split ? 2000 : 900);
   *item_units = split ? 4 : 6;
 }
 
