@@ -102,8 +102,12 @@ int check_tokens(const pnb_pkv *c, const pnb_rows *r, int n_tok, int heads, bool
 }
 
 // Up to this many rows (tokens x query heads of a KV head) of every sequence go
-// through the kernel for steps (its registers hold 16).
-constexpr int kStepRows = 16;
+// through the kernel for steps (its registers hold 16).  At head_dim 128 a second block of 8
+// rows costs it more than the tcgen05 kernel's empty rows do: 16 rows over 64 sequences of 4096,
+// 64 of 300, 8 of 1000, 1 of 32768, 1 of 200, in bf16: 421, 88, 49, 86, 29 us against 236, 68,
+// 45, 59, 31; in fp32 430, 92, 49, 88, 33 against 287, 90, 53, 72, 37; at head_dim 64 in bf16
+// 166, 47, 30, 41, 18 against 184, 55, 39, 49, 27.
+constexpr int kStepRows = 16, kStepRows128 = 8;
 // A batch whose page tables have room for no more than this goes sequence by sequence, shared
 // prefix or not: the pages that sequences share come from L2, at some 11 TB/s, and one kernel
 // and its join take less than two passes.  Single tokens of 32 / 8 heads, head_dim 128, tables
@@ -137,7 +141,7 @@ int attend(pnb_pkv *c, int32_t layer, const pnb_pkv_batch *b, int32_t n_group, c
   a.pass = kPkvAll;
   const CUtensorMap &map = c->maps[layer];
   const int group = g.n_head / g.n_kv_head;
-  const bool step = a.seqs.each > 0 && (int64_t)a.seqs.each * group <= kStepRows;
+  const bool step = a.seqs.each > 0 && (int64_t)a.seqs.each * group <= (g.head_dim == 128 ? kStepRows128 : kStepRows);
   const int64_t held = (int64_t)b->n_seq * b->max_page * g.page * g.n_kv_head * g.head_dim * 4;
   cudaError_t e = cudaSuccess;
   if (group_start && held > kDirectBytes) {

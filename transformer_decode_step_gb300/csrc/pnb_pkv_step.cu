@@ -1,7 +1,8 @@
 // pnb_pkv_step.cu - attention of a few rows per sequence and KV head (single tokens,
 // a few drafted ones) over the paged KV cache.  Bound by the bytes of K and V.
 //
-// A row is one (token, query head); up to 8 RB rows share a KV head's entries.  Warp
+// A row is one (token, query head); up to 8 RB rows share a KV head's entries (RB 2 at
+// head_dim 64 only: at 128 the tcgen05 kernel is faster from 9 rows on).  Warp
 // instructions m16n8k16 take rows 0-7 of A as the rows' bf16 high parts and rows 8-15 as
 // their low parts, of the queries in S = Q K^T and of the softmax weights in O = P V: the
 // 16 rows that the instruction has anyway give 16 bits of both operands, and a lane
@@ -14,6 +15,10 @@
 // by TMA into a ring; four warps take 16 of its entries each, the other four the next
 // chunk.  Every warp keeps its own reference, sums and outputs; they meet at an item's
 // end in shared memory, and those of items that CTAs share in the join kernel.
+//
+// Single tokens of 64 sequences of 4096 entries (32 / 8 heads, head_dim 128, 1.07 GB, L2
+// cold) take 195 us, 5.5 TB/s; 8 of 32768 188 us, 5.7; one of 32768 51 us, 2.6: bytes, and
+// for few of them the start (schedule, lengths, page ids and first chunk in turn) and the join.
 #include <cuda_bf16.h>
 #include <math.h>
 
@@ -382,8 +387,8 @@ cudaError_t prepare() {
 
 cudaError_t prepare_pkv_step(int hd) {
   cudaError_t e = hd == 128 ? prepare<128, 1>() : prepare<64, 1>();
-  if (e != cudaSuccess) return e;
-  return hd == 128 ? prepare<128, 2>() : prepare<64, 2>();
+  if (e != cudaSuccess || hd == 128) return e;
+  return prepare<64, 2>();
 }
 
 // a chunk at the GPU's copy rate, shared out over its SMs
@@ -396,7 +401,7 @@ cudaError_t launch_pkv_step(int hd, const CUtensorMap &map, const PkvAttnArgs &a
   PkvAttnArgs a = args;
   pkv_step_cost(hd, &a.unit_ns, &a.item_units);
   const int rows = a.seqs.each * (a.n_head / a.pool.n_kv);
-  if (hd == 128) return rows <= 8 ? launch_step<128, 1>(map, a, st) : launch_step<128, 2>(map, a, st);
+  if (hd == 128) return launch_step<128, 1>(map, a, st);
   return rows <= 8 ? launch_step<64, 1>(map, a, st) : launch_step<64, 2>(map, a, st);
 }
 
