@@ -104,8 +104,8 @@ int check_tokens(const pnb_pkv *c, const pnb_rows *r, int n_tok, int heads, bool
 // Up to this many rows (tokens x query heads of a KV head) of every sequence go
 // through the kernel for steps (its registers hold 16).  At head_dim 128 a second block of 8
 // rows costs it more than the tcgen05 kernel's empty rows do: 16 rows over 64 sequences of 4096,
-// 64 of 300, 8 of 1000, 1 of 32768, 1 of 200, in bf16: 421, 88, 49, 86, 29 us against 236, 68,
-// 45, 59, 31; in fp32 430, 92, 49, 88, 33 against 287, 90, 53, 72, 37; at head_dim 64 in bf16
+// 64 of 300, 8 of 1000, 1 of 32768, 1 of 200, in bf16: 421, 88, 49, 86, 29 us against 223, 65,
+// 45, 59, 27; in fp32 430, 92, 49, 88, 33 against 287, 90, 53, 72, 37; at head_dim 64 in bf16
 // 166, 47, 30, 41, 18 against 184, 55, 39, 49, 27.
 constexpr int kStepRows = 16, kStepRows128 = 8;
 // A batch whose page tables have room for no more than this goes sequence by sequence, shared

@@ -27,7 +27,8 @@
 // weight's relative one), P as two (16 bits and the sign: 2^-18 of a weight at most), in 5/2
 // times the products.  At head_dim 128 that leaves room for the queries of 128 rows: warps 4-7
 // idle, S of two tiles takes both halves' columns, and the products of S run ahead of the softmax
-// (two prompts up to 8191 under a window of 4096: 1468 us one tile at a time, 1146 so).
+// (two prompts up to 8191 under a window of 4096: 1468 us one tile at a time, 1146 so).  With ONE
+// the same is done for calls whose blocks all have at most 128 rows.
 //
 // Bound by the tensor rate and, beside it, by the softmax: a tile's S and O take 2048 cycles for
 // the two halves at head_dim 128, the exponentials, conversions and sums of 64 scores 367 cycles
@@ -75,14 +76,15 @@ struct RingAt {
 // 5e-5 too small.
 constexpr int kFold = 4;
 
-template <int HD, bool SPLIT>
+template <int HD, bool SPLIT, bool ONE>
 struct RL {
   static constexpr int NB = HD / 64;                        // 64-column boxes of a row
   static constexpr int BOX = kPkvTile * 128;                // bytes of a 128-row box
   static constexpr int UNIT = NB * BOX;                     // a K or V tile
   // fp32 on either side: queries of three bf16 parts, for which one half of rows leaves room at
   // head_dim 128
-  static constexpr int HALVES = pkv_block_rows(HD, SPLIT) / 128;
+  // (ONE: no block of the call has more)
+  static constexpr int HALVES = ONE ? 1 : pkv_block_rows(HD, SPLIT) / 128;
   static constexpr int PARTS = SPLIT ? 3 : 1;
   static constexpr int QHALF = UNIT * PARTS;                // Q of 128 rows, part by part
   static constexpr int NU = (229376 - HALVES * QHALF) / UNIT;   // ring units
@@ -99,7 +101,7 @@ static_assert(sizeof(RBars) <= 1024, "barriers");
 // first: a product cuts off what it adds to a large sum, and to a small one next to nothing)
 template <int HD, bool SPLIT, int I = 0>
 __device__ __forceinline__ void products_s(uint32_t d, uint64_t q, uint64_t k) {
-  typedef RL<HD, SPLIT> L;
+  typedef RL<HD, SPLIT, true> L;   // (the same for both)
   constexpr int KS = HD / 16, part = L::PARTS - 1 - I / KS, c = I % KS / 4, x = I % 4;
   if constexpr (I < L::PARTS * KS) {
     mma_bf16_off<(part * L::UNIT + c * L::BOX + x * 32) / 16, (c * L::BOX + x * 32) / 16>(
@@ -157,10 +159,10 @@ __device__ __noinline__ bool hidden_odd_values(const PkvAttnArgs &a, const PkvIt
   return __any_sync(0xffffffffu, bad);
 }
 
-template <int HD, bool SPLIT>
+template <int HD, bool SPLIT, bool ONE>
 __global__ void __launch_bounds__(kThreads, 1)
     k_pkv_rows(const __grid_constant__ CUtensorMap kvmap, const __grid_constant__ PkvAttnArgs a) {
-  typedef RL<HD, SPLIT> L;
+  typedef RL<HD, SPLIT, ONE> L;
   constexpr int NU = L::NU;
   static_assert(NU <= 16 && NU >= 2, "ring");
   uint8_t *sm = r_smem + ((1024u - (smem_addr(r_smem) & 1023u)) & 1023u);
@@ -310,7 +312,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!ok) break;
             tc_fence_after();
             if (elect_one()) {
-              products_o<HD, SPLIT, 0>(tmem + 256, p, v0 + v.s * (L::UNIT >> 4), t % kFold == 0);
+              products_o<HD, SPLIT, 0>(tmem + 256, p, v0 + v.s * (L::UNIT >> 4), SPLIT ? t % kFold == 0 : t == 0);
               mma_commit(&bar.pv_half[0]);
             }
             __syncwarp();
@@ -948,7 +950,7 @@ __global__ void __launch_bounds__(256) k_pkv_finish(const __grid_constant__ PkvA
   pkv_store<N>(a.out, tok * a.out.token + head * a.out.head + lane * N, o, sum == 0.f ? 0.f : 1.f / sum);
 }
 
-template <int HD, bool SPLIT>
+template <int HD, bool SPLIT, bool ONE>
 cudaError_t launch_rows(const CUtensorMap &map, const PkvAttnArgs &a, cudaStream_t st) {
   cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute attr;
@@ -956,19 +958,29 @@ cudaError_t launch_rows(const CUtensorMap &map, const PkvAttnArgs &a, cudaStream
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.gridDim = dim3(a.grid);
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = RL<HD, SPLIT>::SMEM;
+  cfg.dynamicSmemBytes = RL<HD, SPLIT, ONE>::SMEM;
   cfg.stream = st;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_pkv_rows<HD, SPLIT>, map, a);
+  return cudaLaunchKernelEx(&cfg, k_pkv_rows<HD, SPLIT, ONE>, map, a);
 }
 
-template <int HD>
+template <int HD, bool SPLIT>
+cudaError_t launch_halves(bool one, const CUtensorMap &map, const PkvAttnArgs &a, cudaStream_t st) {
+  if constexpr (pkv_block_rows(HD, SPLIT) > 128)
+    if (!one) return launch_rows<HD, SPLIT, false>(map, a, st);
+  return launch_rows<HD, SPLIT, true>(map, a, st);
+}
+
+template <int HD, bool SPLIT>
 cudaError_t prepare() {
-  cudaError_t e = cudaFuncSetAttribute(k_pkv_rows<HD, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       RL<HD, false>::SMEM);
-  if (e != cudaSuccess) return e;
-  return cudaFuncSetAttribute(k_pkv_rows<HD, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, RL<HD, true>::SMEM);
+  const cudaError_t e = cudaFuncSetAttribute(
+      k_pkv_rows<HD, SPLIT, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, RL<HD, SPLIT, true>::SMEM);
+  if constexpr (pkv_block_rows(HD, SPLIT) > 128)
+    if (e == cudaSuccess)
+      return cudaFuncSetAttribute(k_pkv_rows<HD, SPLIT, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                  RL<HD, SPLIT, false>::SMEM);
+  return e;
 }
 
 }  // namespace
@@ -1002,15 +1014,25 @@ void pkv_rows_cost(int hd, bool split, int *unit_ns, int *item_units) {
   *item_units = split ? 4 : 6;
 }
 
-cudaError_t prepare_pkv_rows(int hd) { return hd == 128 ? prepare<128>() : prepare<64>(); }
+cudaError_t prepare_pkv_rows(int hd) {
+  const cudaError_t e = hd == 128 ? prepare<128, false>() : prepare<64, false>();
+  if (e != cudaSuccess) return e;
+  return hd == 128 ? prepare<128, true>() : prepare<64, true>();
+}
 
 cudaError_t launch_pkv_rows(int hd, const CUtensorMap &map, const PkvAttnArgs &args, cudaStream_t st) {
   PkvAttnArgs a = args;
   const bool split = pkv_split(a);
   pkv_rows_cost(hd, split, &a.unit_ns, &a.item_units);
   a.heads_inner = a.pass == kPkvAll;
-  if (hd == 128) return split ? launch_rows<128, true>(map, a, st) : launch_rows<128, false>(map, a, st);
-  return split ? launch_rows<64, true>(map, a, st) : launch_rows<64, false>(map, a, st);
+  // No block has more than a half's rows: the kernel of one half, S running ahead.  16 rows over
+  // 64 sequences of 4096 (head_dim 128, bf16) 223 against 238 us, 80 over 16 of 3000 86 against 92;
+  // 32 rows over 64 of 4096 at head_dim 64 in bf16 166 against 184, in fp32 217 against 258.  Beside
+  // a prefix's pass it gains nothing (32 slots of 12 rows behind 30000 entries 118 against 110).
+  const int64_t tokens = a.seqs.each ? a.seqs.each : a.seqs.n_tok;
+  const bool one = a.pass == kPkvAll && tokens * (a.n_head / a.pool.n_kv) <= 128;
+  if (hd == 128) return split ? launch_halves<128, true>(one, map, a, st) : launch_halves<128, false>(one, map, a, st);
+  return split ? launch_halves<64, true>(one, map, a, st) : launch_halves<64, false>(one, map, a, st);
 }
 
 }  // namespace pnb
