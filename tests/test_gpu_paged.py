@@ -321,6 +321,20 @@ def test_attention_large_and_growing_scores(dtype, new):
     c.run(dtype, scale=3.0, ragged=len(new) > 1)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("T,G,hd", [(32, 4, 128), (5, 4, 128), (128, 1, 64), (40, 3, 64), (9, 1, 128)])
+@pytest.mark.parametrize("window", [0, 30, 100, 500])
+def test_blocks_of_few_rows(T, G, hd, window, dtype):
+    # windows begin at every place within a tile, and references move in some warps and not in others
+    lens = [700 + 37 * i for i in range(12)]
+    c = Case(lens, 2, G, hd, 32, seed=17, new=[T] * len(lens))
+    for b, n in enumerate(lens):
+        k = c.entries[b][0]
+        k.copy_((k.float() * torch.linspace(0.01, 4, n, device="cuda")[:, None, None]).to(torch.bfloat16))
+        c.store(b)
+    c.run(dtype, window=window, scale=2.0, ragged=False)
+
+
 @pytest.mark.parametrize("T", [1, 3, 40])
 def test_more_tokens_than_entries_answer_zero(T):
     c = Case([2, 0, 200], 2, 2, 64, 16, seed=17, new=[T] * 3)
