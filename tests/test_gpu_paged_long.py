@@ -1,0 +1,136 @@
+"""The paged KV cache's attention in the steady state of its kernels, against 64 bits.
+
+A CTA takes the parts of the work that lie side by side, and small calls are spread over all of them.
+These calls are large enough that a CTA goes through dozens of 128-entry tiles of one block: the
+rings and the buffers of scores turn over many times, and with fp32 the sums start anew again and again.
+
+Sequences of a case name the same pages, so that a small pool makes much work; queries are each
+sequence's own.
+"""
+import math
+
+import pytest
+import torch
+
+import transformer_decode_step_gb300 as pnb
+
+pytestmark = pytest.mark.gpu
+
+DT = {"fp32": torch.float32, "bf16": torch.bfloat16}
+U = 2.0 ** -8
+
+
+class Same:
+    """``B`` sequences of T tokens on the same L entries."""
+
+    def __init__(self, L, B, T, n_kv, G, hd, page, seed, **kw):
+        self.L, self.B, self.T, self.n_kv, self.G, self.H, self.hd = L, B, T, n_kv, G, n_kv * G, hd
+        self.gen = torch.Generator(device="cuda")
+        self.gen.manual_seed(seed)
+        n_page = -(-L // page)
+        self.kv = pnb.PagedKv(n_layer=1, n_head=self.H, n_kv_head=n_kv, head_dim=hd, n_page=n_page + 1, page=page, **kw)
+        self.order = torch.randperm(n_page, generator=self.gen, device="cuda")
+        self.table = self.order.to(torch.int32).expand(B, -1).contiguous()
+        self.lens = torch.full((B,), L, dtype=torch.int32, device="cuda")
+        self.page = page
+        self.k = torch.randn((L, n_kv, hd), generator=self.gen, device="cuda").to(torch.bfloat16)
+        self.v = torch.randn((L, n_kv, hd), generator=self.gen, device="cuda").to(torch.bfloat16)
+
+    def store(self):
+        pool = self.kv.pages(0)
+        pool.fill_(float("nan"))
+        e = torch.arange(self.L, device="cuda")
+        for s, x in enumerate((self.k, self.v)):
+            pool[self.order[e // self.page], s, :, e % self.page] = x
+        return self.kv.batch(self.lens, self.table)
+
+    def queries(self, dtype, scale=1.0):
+        q = torch.randn((self.B * self.T, self.H, self.hd), generator=self.gen, device="cuda") * scale
+        return q.to(DT[dtype])
+
+    def want(self, q, seqs, window=0):
+        """Answers of some sequences in 64 bits, [len(seqs)][T][H][hd]; the largest |score|."""
+        n_kv, G, T, L = self.n_kv, self.G, self.T, self.L
+        q = q.view(self.B, T, n_kv, G, self.hd)
+        i = torch.arange(L - T, L, device="cuda")[:, None]
+        j = torch.arange(L, device="cuda")
+        see = (j <= i) & ((j > i - window) if window else torch.ones_like(j <= i))
+        out, most = [], 0.0
+        for b in seqs:
+            heads = []
+            for h in range(n_kv):
+                s = torch.einsum("tgd,md->tgm", q[b, :, h].double(), self.k[:, h].double()) / math.sqrt(self.hd)
+                most = max(most, float(s.abs().max()))
+                p = torch.softmax(s.masked_fill(~see[:, None], -math.inf), -1)
+                heads.append(torch.einsum("tgm,md->tgd", p, self.v[:, h].double()))
+            out.append(torch.stack(heads, 1).flatten(1, 2))
+        return torch.stack(out), most
+
+
+def _stairs(c, gen, chance, first, second, step):
+    """Keys that move the references of the warps (32 rows of a block each) at places of their own: element w
+    of a key, which rows of warp w look at, rises by ``step`` at an entry of a tile's first half (with
+    ``first``) or its second one, in ``chance`` of the tiles.  Values have mean 1, so that what is
+    lost of a sum shows."""
+    tiles = c.L // 128
+    for w in range(4):
+        at = []
+        for t in range(1, tiles):
+            for half in ([0] if first else []) + ([1] if second else []):
+                if torch.rand((), generator=gen).item() < chance:
+                    at.append(t * 128 + half * 64 + int(torch.randint(0, 64, (), generator=gen)))
+        rise = torch.zeros(c.L)
+        rise[at] = step
+        c.k[:, :, w] = torch.cumsum(rise, 0).to(torch.bfloat16).cuda()[:, None]
+    c.v.copy_((c.v.float() * 0.25 + 1.0).to(torch.bfloat16))
+
+
+def _looking(c, q):
+    """Rows look at their warp's element of the keys, every third row at none of them."""
+    q = q.view(c.B, c.T, c.n_kv, c.G, c.hd)
+    q[..., :4] = 0
+    row = (torch.arange(c.T)[:, None] * c.G + torch.arange(c.G)).cuda()
+    for w in range(4):
+        q[:, :, :, :, w] = ((row // 32 % 4 == w) & (row % 3 != 0)).to(q.dtype)[None, :, None] * math.sqrt(c.hd)
+    return q.view(c.B * c.T, c.H, c.hd)
+
+
+def _moving(dtype, hd, T, G, chance, first, second, B=40, window=0, L=5000):
+    c = Same(L, B, T, 8, G, hd, 64, seed=5)
+    gen = torch.Generator()
+    gen.manual_seed(7)
+    _stairs(c, gen, chance, first, second, 14.0)      # 14 of a score: 2^20 of a weight
+    batch = c.store()
+    q = _looking(c, c.queries(dtype))
+    out = torch.full(q.shape, 7.0, dtype=q.dtype, device="cuda")
+    c.kv.attention(0, batch, q, out, window=window)
+    again = torch.empty_like(out)
+    for _ in range(30):
+        again.fill_(7.0)
+        c.kv.attention(0, batch, q, again, window=window)
+        assert torch.equal(out, again)
+    assert c.kv.device_error() == 0
+    seqs = list(range(0, B, 3))
+    want, most = c.want(q, seqs, window)
+    # Scores: at most hd / 16 * 3 additions, each cut off by 2^-23 of what it adds up, which is at most the largest
+    # element (one product makes the score) and the others' random sums, below 2 * most + 64; weights: that
+    # and 2^-17 (fp32) or 2^-9 (bf16); the mean's numerator and denominator: twice that, times values below 3.  Queries of
+    # bf16 are exact, those of fp32 are held in 24 bits.  The output's own rounding: 2^-8 of 3 with bf16.
+    score = (2 * most + 64) * (hd // 16 * 3 + 1) * 2.0 ** -23
+    tol = 2 * 3 * (score + (2.0 ** -17 if dtype == "fp32" else U)) + (0 if dtype == "fp32" else U * 3)
+    got = out.view(B, T, c.H, hd)[seqs].double()
+    assert float((got - want).abs().max()) <= tol
+
+
+# blocks of at most 128 rows: scores of the next tiles are there before the products of the last
+ONE_HALF = [("fp32", 128, 32, 4), ("bf16", 128, 32, 4), ("fp32", 64, 32, 4), ("bf16", 64, 32, 4), ("fp32", 128, 64, 5)]
+
+
+@pytest.mark.parametrize("dtype,hd,T,G", ONE_HALF)
+@pytest.mark.parametrize("chance,first,second", [(0.3, True, True), (1.0, True, False), (1.0, False, True), (0.06, True, True)])
+def test_references_that_move_beside_other_warps_products(dtype, hd, T, G, chance, first, second):
+    # A warp rescales its sums in the first half of a tile while others do so in the second half of the one
+    # before it or behind it; all runs answer with the same bits.  (With a step in every tile the sequences
+    # are shorter, so that scores stay within what the tolerance can tell apart.)
+    L = 5000 if chance < 1.0 else 2600
+    _moving(dtype, hd, T, G, chance, first, second, L=L, B=40 if chance < 1.0 else 64)

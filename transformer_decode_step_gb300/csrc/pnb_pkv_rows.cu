@@ -596,10 +596,12 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (move) m = top;
               sum *= f;
               if (t > it.ta || h) {
-                // Outputs so far go to the new reference.  The products of the tile before are
-                // done, S of this one came behind them; those of its first half end first.
+                // Outputs so far go to the new reference.  The products of the tile before end
+                // first: with two halves S of this tile came behind them; with one it did not, and they
+                // may wait for another warp's p yet.  Those of this tile's first half end next (only
+                // then: a phase further back has the same parity, and would pass for this one).
+                if (ALONE && t > it.ta && !mbar_wait(&bar.pv_half[1], ns & 1)) ok = false;
                 if (h && !mbar_wait(&bar.pv_half[w], (ns - 1) & 1)) ok = false;
-                if (ALONE && !h && !mbar_wait(&bar.pv_half[1], ns & 1)) ok = false;
                 __syncwarp();
                 tc_fence_after();
 #pragma unroll 1
