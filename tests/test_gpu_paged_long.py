@@ -134,3 +134,10 @@ def test_references_that_move_beside_other_warps_products(dtype, hd, T, G, chanc
     # are shorter, so that scores stay within what the tolerance can tell apart.)
     L = 5000 if chance < 1.0 else 2600
     _moving(dtype, hd, T, G, chance, first, second, L=L, B=40 if chance < 1.0 else 64)
+
+
+@pytest.mark.parametrize("T,G,hd", [(64, 4, 64), (100, 4, 64), (37, 3, 128)])
+def test_sums_that_start_anew_where_a_reference_moves(T, G, hd):
+    # fp32: the reference moves in the first half of every tile, those among them that add the sums up
+    _moving("fp32", hd, T, G, 1.0, True, False, L=2600, B=64)
+    _moving("fp32", hd, T, G, 0.5, True, False, L=5000)

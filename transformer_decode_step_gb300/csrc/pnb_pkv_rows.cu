@@ -616,6 +616,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                   tmem_st32_async(to + i, reinterpret_cast<const uint32_t *>(o));
                 }
               }
+              // p goes over p, and below a sum that starts anew is read back
+              tmem_wait_st();
               part = exponentials();
             }
           }
