@@ -130,7 +130,8 @@ int attend(pnb_pkv *c, int32_t layer, const pnb_pkv_batch *b, int32_t n_group, c
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   a.pool = pool_of(c, layer);
   a.n_head = g.n_head;
-  a.window = window;
+  // a window that reaches past the page tables is none
+  a.window = window < (int64_t)b->max_page * g.page ? window : 0;
   a.qscale = (float)(1.4426950408889634 / std::sqrt((double)g.head_dim));
   a.err = c->err;
   a.part = c->part;

@@ -527,7 +527,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           lo = max(0, last - a.window + 1);
         }
       } else {
-        const int last = it.base + (tok - it.tok0);
+        const int last = max(it.base + (tok - it.tok0), -1);
         hi = last + 1;
         lo = max(it.floor, a.window > 0 ? last - a.window + 1 : 0);
       }

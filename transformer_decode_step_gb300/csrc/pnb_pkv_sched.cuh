@@ -83,8 +83,9 @@ __device__ __forceinline__ void pkv_block(const PkvAttnArgs &a, int pass, const 
     it.base = s.len - s.n + j * TB;
     it.hi = max(0, it.base + it.ntok);
     it.hi_min = it.base + 1;
-    it.lo = max(s.floor, W > 0 ? it.base - W + 1 : 0);
-    it.lo_max = max(s.floor, W > 0 ? it.base + it.ntok - W : 0);
+    // (before entry 0 a window starts at no entry either: what may be far below 0 is left out)
+    it.lo = max(s.floor, W > 0 ? max(it.base, 0) - W + 1 : 0);
+    it.lo_max = max(s.floor, W > 0 ? max(it.base + it.ntok, 0) - W : 0);
   }
   it.t0 = it.lo / TILE;
   it.nt = max(1, (it.hi + TILE - 1) / TILE - it.t0);
@@ -142,8 +143,8 @@ __device__ __forceinline__ long long pkv_units(const PkvAttnArgs &a, int pass, i
     // first entries: the floor, and from block y on the window's
     int y = K;
     if (a.window > 0) {
-      const int d = s.floor + a.window - 1 - base;   // base + j TB - window + 1 > floor
-      y = d < 0 ? z : min(K, max(z, d / TB + 1));
+      const int64_t d = (int64_t)s.floor + a.window - 1 - base;   // base + j TB - window + 1 > floor
+      y = d < 0 ? z : (int)min((int64_t)K, max((int64_t)z, d / TB + 1));
     }
     sum -= (long long)(y - z) * (s.floor / TILE);
     if (K > y) sum -= floor_sum(K - y, TILE, TB, base + y * TB - a.window + 1);
