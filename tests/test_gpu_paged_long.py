@@ -141,3 +141,36 @@ def test_sums_that_start_anew_where_a_reference_moves(T, G, hd):
     # fp32: the reference moves in the first half of every tile, those among them that add the sums up
     _moving("fp32", hd, T, G, 1.0, True, False, L=2600, B=64)
     _moving("fp32", hd, T, G, 0.5, True, False, L=5000)
+
+
+@pytest.mark.parametrize("L,T,hidden", [(400000, 64, 24), (2000000, 64, 24), (2000000, 2, 1)])
+def test_a_hidden_nan_in_a_long_context_reaches_nobody_else(L, T, hidden):
+    # One sequence of 304 has a NaN among its values that its first tokens do not see; the CTA that has its
+    # entries has other sequences' behind them.
+    B, G, hd, page = 304, 4, 64, 128
+    L += 77
+    c = Same(L, B, T, 1, G, hd, page, seed=9)
+    batch = c.store()
+    victim, bad = 150, L - T + hidden
+    pool, own = c.kv.pages(0), c.kv.cfg.n_page - 1
+    pool[own] = pool[c.table[0, -1].long()]
+    pool[own, 1, :, bad % page, 5] = float("nan")
+    assert bad // page == c.table.shape[1] - 1
+    c.table[victim, -1] = own
+    q = torch.randn((1, T * G, hd), generator=c.gen, device="cuda").to(torch.bfloat16).expand(B, -1, -1)
+    q = q.reshape(B * T, G, hd).contiguous()
+    out = torch.full_like(q, 7.0)
+    c.kv.attention(0, batch, q, out)
+    torch.cuda.synchronize()
+    assert c.kv.device_error() == 0
+    want, A = c.want(q, [0])
+    # scores: 8 sums of 16 products, cut off by 2^-23 of at most twice the largest; weights by that and 2^-8 for
+    # their rounding, numerator and denominator alike; answers by 2^-8 of what they are
+    v = c.v
+    c.v = v.abs()
+    tol = 2 * (2 * A * 8 * 2.0 ** -23 + U) * float(c.want(q, [0])[0].max()) + U * float(want.abs().max())
+    c.v = v
+    got = out.view(B, T, G, hd).double()
+    assert bool(torch.isnan(got[victim, hidden:, :, 5]).all())
+    got[victim, hidden:, :, 5] = want[0, hidden:, :, 5]
+    assert float((got - want).abs().max()) <= tol

@@ -65,6 +65,12 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t *bar, uint32_t parity) {
   return ok != 0;
 }
 
+// its low half: times up to four seconds apart
+__device__ __forceinline__ uint32_t global_ns_lo() {
+  uint32_t t;
+  asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
+  return t;
+}
 __device__ __forceinline__ unsigned long long global_ns() {
   unsigned long long t;
   asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
@@ -102,6 +108,37 @@ __device__ __forceinline__ bool mbar_wait_for(uint64_t *bar, uint32_t parity,
 // The kernels' bounded wait: gives up after about kWaitLimitNs.
 __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity) {
   return mbar_wait_for(bar, parity, kWaitLimitNs);
+}
+
+// A wait behind other warps' work of any length: gives up when `work`, a number in shared memory
+// that those who work change as they go, has stood still for about kWaitLimitNs.
+__device__ __forceinline__ bool mbar_wait_working(uint64_t *bar, uint32_t parity, const uint32_t *work) {
+  if (mbar_try_wait(bar, parity)) return true;
+  uint32_t t0 = 0, seen = ~0u;   // (the clock is first looked at when the wait has become long)
+  for (uint32_t it = 1;; ++it) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((it & 255u) == 0u) {
+      const uint32_t now = global_ns_lo(), at = *reinterpret_cast<const volatile uint32_t *>(work);
+      if (at != seen) {
+        seen = at;
+        t0 = now;
+        it = 0;
+      } else if (now - t0 > (uint32_t)kWaitLimitNs || it > (1u << 26)) {
+        return false;
+      }
+    }
+  }
+}
+
+// The wait of one whose work all others wait for, and that is to look at little else: gives up
+// when one of them has, and has set `stop` in shared memory (or after 2^32 polls).
+__device__ __forceinline__ bool mbar_wait_unless(uint64_t *bar, uint32_t parity, const uint32_t *stop) {
+  if (mbar_try_wait(bar, parity)) return true;
+  for (uint32_t it = 1; it; ++it) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((it & 255u) == 0u && *reinterpret_cast<const volatile uint32_t *>(stop)) return false;
+  }
+  return false;
 }
 
 // 1-D bulk copy global -> shared, completion counted on an mbarrier (TMA).

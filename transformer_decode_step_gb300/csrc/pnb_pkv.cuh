@@ -210,39 +210,88 @@ __device__ __forceinline__ void pkv_store(const DevRows &out, int64_t at, const 
   }
 }
 
-// One row's sums over entries [from, to) by the calling warp, without matrix
-// instructions: lane l answers elements l * HD / 32 ...  A page that the table does
-// not name counts as zeros.
+// Sums of R rows over entries [from, to) of each, by the calling warp, without matrix
+// instructions: lanes take an entry each for the scores and HD / 32 elements each (l * HD / 32 ..)
+// for the outputs.  A page that the table does not name counts as zeros, and what a row
+// does not see is no part of its sums, whatever it holds.  *work changes every 32 entries.
+template <int HD, int R>
+__device__ __forceinline__ void pkv_attend_rows(const PkvPool &pool, const int32_t *pages, int h, const DevRows &q,
+                                             const int64_t (&q_at)[R], float scale, const int (&from)[R],
+                                             const int (&to)[R], float (&o)[R][HD / 32], float (&m)[R], float (&sum)[R],
+                                             uint32_t *work) {
+  constexpr int N = HD / 32;
+  const int lane = threadIdx.x & 31;
+  int begin = INT_MAX, end = 0;
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    if (from[r] < to[r]) {
+      begin = min(begin, from[r]);
+      end = max(end, to[r]);
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) o[r][i] = 0.f;
+    m[r] = -INFINITY;
+    sum[r] = 0.f;
+  }
+  for (int e0 = begin; e0 < end; e0 += 32) {
+    const int e = e0 + lane;
+    const __nv_bfloat16 *k = e < end ? pkv_row<HD>(pool, pages, e, 0, h) : nullptr;
+    float s[R] = {};
+    if (k) {
+#pragma unroll 4
+      for (int i = 0; i < HD; i += 4) {
+        float y[4];
+        load_vals<__nv_bfloat16, 4>(k + i, y);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          float x[4];
+          if (q.dtype == PNB_F32) load_vals<float, 4>(static_cast<const float *>(q.p) + q_at[r] + i, x);
+          else load_vals<__nv_bfloat16, 4>(static_cast<const __nv_bfloat16 *>(q.p) + q_at[r] + i, x);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) s[r] = fmaf(x[c], y[c], s[r]);
+        }
+      }
+    }
+    float p[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const float x = e >= from[r] && e < to[r] ? s[r] * scale : -INFINITY;
+      const float top = fmaxf(m[r], warp_max(x)), ref = top == -INFINITY ? 0.f : top, f = exp2f(m[r] - ref);
+      p[r] = exp2f(x - ref);
+      sum[r] = sum[r] * f + warp_sum(p[r]);
+#pragma unroll
+      for (int i = 0; i < N; ++i) o[r][i] *= f;
+      m[r] = top;
+    }
+    const long long v = (long long)(uintptr_t)(k ? k + ((int64_t)pool.n_kv << pool.page_log2) * HD : nullptr);
+#pragma unroll 4
+    for (int j = 0; j < 32; ++j) {
+      const long long at = __shfl_sync(0xffffffffu, v, j);
+      float y[N] = {};
+      if (at) load_vals<__nv_bfloat16, N>(reinterpret_cast<const __nv_bfloat16 *>((uintptr_t)at) + lane * N, y);
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const float f = __shfl_sync(0xffffffffu, p[r], j);
+        const bool sees = e0 + j >= from[r] && e0 + j < to[r];
+#pragma unroll
+        for (int i = 0; i < N; ++i) o[r][i] = sees ? fmaf(f, y[i], o[r][i]) : o[r][i];
+      }
+    }
+    if (lane == 0) atomicAdd(work, 1u);
+  }
+}
+
+// the same for one row, by a call
 template <int HD>
 __device__ __noinline__ void pkv_attend_row(const PkvPool &pool, const int32_t *pages, int h, const DevRows &q,
                                             int64_t q_at, float scale, int from, int to, float (&o)[HD / 32], float &m,
-                                            float &sum) {
-  constexpr int N = HD / 32;
-  const int lane = threadIdx.x & 31;
-  float x[N];
-  if (q.dtype == PNB_F32) load_vals<float, N>(static_cast<const float *>(q.p) + q_at + lane * N, x);
-  else load_vals<__nv_bfloat16, N>(static_cast<const __nv_bfloat16 *>(q.p) + q_at + lane * N, x);
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    x[i] *= scale;
-    o[i] = 0.f;
-  }
-  m = -INFINITY;
-  sum = 0.f;
-  for (int e = from; e < to; ++e) {
-    const __nv_bfloat16 *k = pkv_row<HD>(pool, pages, e, 0, h);
-    float y[N] = {}, s = 0.f;
-    if (k) load_vals<__nv_bfloat16, N>(k + lane * N, y);
-#pragma unroll
-    for (int i = 0; i < N; ++i) s += x[i] * y[i];
-    s = warp_sum(s);
-    const float top = fmaxf(m, s), ref = top == -INFINITY ? 0.f : top, f = exp2f(m - ref), p = exp2f(s - ref);
-    if (k) load_vals<__nv_bfloat16, N>(k + ((int64_t)pool.n_kv << pool.page_log2) * HD + lane * N, y);
-#pragma unroll
-    for (int i = 0; i < N; ++i) o[i] = o[i] * f + p * y[i];
-    sum = sum * f + p;
-    m = top;
-  }
+                                            float &sum, uint32_t *work) {
+  const int64_t at[1] = {q_at};
+  const int f[1] = {from}, t[1] = {to};
+  float ms[1], sums[1];
+  pkv_attend_rows<HD, 1>(pool, pages, h, q, at, scale, f, t, reinterpret_cast<float(&)[1][HD / 32]>(o), ms, sums, work);
+  m = ms[0];
+  sum = sums[0];
 }
 
 // what brings sums with references m and m2 to a common one

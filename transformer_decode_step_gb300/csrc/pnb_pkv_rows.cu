@@ -53,8 +53,6 @@ extern __shared__ __align__(1024) uint8_t r_smem[];
 constexpr int kThreads = 384;
 constexpr int kSoftWarps = 8;
 constexpr float kLarge = 65536.f;   // a sum of 64 p that moves the reference
-// the warps that clear V wait for a tile that may be a whole item away
-constexpr unsigned long long kItemLimitNs = 10000000000ull;
 // registers per thread: 384 x 168 at launch = 256 x 208 + 128 x 88
 constexpr int kRegsSoft = 208, kRegsRest = 88;
 
@@ -93,7 +91,9 @@ struct RL {
 
 struct RBars {
   uint64_t full[16], empty[16], q_ready[2], s_full[2], p_ready[2][2], pv_half[2], o_full[2], v_go, v_ok, drain;
-  uint32_t tmem, pad;
+  uint32_t tmem;
+  uint32_t work;   // changes with every tile that is loaded, and with rows done again
+  uint32_t stop;   // a warp gave up
 };
 static_assert(sizeof(RBars) <= 1024, "barriers");
 
@@ -137,9 +137,9 @@ __device__ __forceinline__ void split8(const float4 &a, const float4 &b, uint4 (
 }
 
 // Whether a value that some row of a block sees and another does not is NaN or infinite
-// (the calling warp; entries of tiles that the block's rows see in part).
+// (the calling warp, a lane per entry; entries of tiles that the block's rows see in part).
 template <int HD>
-__device__ __noinline__ bool hidden_odd_values(const PkvAttnArgs &a, const PkvItem &it) {
+__device__ __noinline__ bool hidden_odd_values(const PkvAttnArgs &a, const PkvItem &it, uint32_t *work) {
   const int lane = threadIdx.x & 31;
   const int seq = a.pass == kPkvPrefix ? min(max(a.group_start[it.b], 0), a.seqs.n_seq - 1) : it.b;
   const int32_t *pages = a.seqs.pages + (int64_t)seq * a.seqs.max_page;
@@ -148,15 +148,62 @@ __device__ __noinline__ bool hidden_odd_values(const PkvAttnArgs &a, const PkvIt
   for (int part = 0; part < 2; ++part) {
     const int from = part ? max(it.hi_min, first) : first;
     const int to = min(part ? end : min(it.lo_max, end), it.len);
-    for (int e = max(from, 0); e < to; ++e) {
-      const __nv_bfloat16 *v = pkv_row<HD>(a.pool, pages, e, 1, it.h);
-      float x[HD / 32] = {};
-      if (v) load_vals<__nv_bfloat16, HD / 32>(v + lane * (HD / 32), x);
+    for (int e0 = max(from, 0); e0 < to; e0 += 32) {
+      const __nv_bfloat16 *v = e0 + lane < to ? pkv_row<HD>(a.pool, pages, e0 + lane, 1, it.h) : nullptr;
+#pragma unroll 4
+      for (int i = 0; i < HD && v; i += 4) {
+        float x[4];
+        load_vals<__nv_bfloat16, 4>(v + i, x);
 #pragma unroll
-      for (int i = 0; i < HD / 32; ++i) bad |= !(x[i] * 0.f == 0.f);
+        for (int c = 0; c < 4; ++c) bad |= !(x[c] * 0.f == 0.f);
+      }
+      if (lane == 0) atomicAdd(work, 1u);
     }
   }
   return __any_sync(0xffffffffu, bad);
+}
+
+// Does rows of a warp (bits of `rows`, a lane's row each) again by themselves: entries [lo, hi) of
+// this CTA's tiles.  Sums go to po and pml, or where these are NULL answers to their place.
+// An item's 256 rows over 400k entries (head_dim 64) take 0.8 s, over 2M 4.5 s: bound by latency, for
+// a mishap.  The pipeline's waits count this as work.
+template <int HD>
+__device__ __noinline__ void repair_rows(const PkvAttnArgs &a, const PkvItem &it, uint32_t rows, int lo, int hi, int tok,
+                                         int head, float *po, float *pml, uint32_t *work) {
+  constexpr int R = 4, N = HD / 32;   // four rows at a time share the loads of K and V
+  const int lane = threadIdx.x & 31;
+  const int seq = a.pass == kPkvPrefix ? min(max(a.group_start[it.b], 0), a.seqs.n_seq - 1) : it.b;
+  const int first = (it.t0 + it.ta) * kPkvTile, end = (it.t0 + it.tb) * kPkvTile;
+  while (rows) {
+    int64_t q_at[R];
+    int from[R], to[R], src[R];
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      src[i] = rows ? __ffs(rows) - 1 : -1;
+      rows &= rows - 1;   // (0 stays 0)
+      const int k = max(src[i], 0);
+      from[i] = max(__shfl_sync(0xffffffffu, lo, k), first);
+      to[i] = src[i] < 0 ? 0 : min(__shfl_sync(0xffffffffu, hi, k), end);
+      q_at[i] = __shfl_sync(0xffffffffu, tok, k) * a.q.token + __shfl_sync(0xffffffffu, head, k) * a.q.head;
+    }
+    float o[R][N], m[R], sum[R];
+    pkv_attend_rows<HD, R>(a.pool, a.seqs.pages + (int64_t)seq * a.seqs.max_page, it.h, a.q, q_at, a.qscale, from, to, o, m,
+                           sum, work);
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      if (src[i] < 0) break;
+      float *dst = reinterpret_cast<float *>((uintptr_t)__shfl_sync(0xffffffffu, (long long)(uintptr_t)po, src[i]));
+      float *ml = reinterpret_cast<float *>((uintptr_t)__shfl_sync(0xffffffffu, (long long)(uintptr_t)pml, src[i]));
+      const int t = __shfl_sync(0xffffffffu, tok, src[i]), hd = __shfl_sync(0xffffffffu, head, src[i]);
+      if (dst) {
+#pragma unroll
+        for (int n = 0; n < N; ++n) dst[lane * N + n] = o[i][n];
+        if (lane == 0) *reinterpret_cast<float2 *>(ml) = make_float2(m[i], sum[i]);
+      } else {
+        pkv_store<N>(a.out, t * a.out.token + hd * a.out.head + lane * N, o[i], sum[i] == 0.f ? 0.f : 1.f / sum[i]);
+      }
+    }
+  }
 }
 
 template <int HD, bool SPLIT, bool ONE>
@@ -171,7 +218,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int G = a.n_head / a.pool.n_kv, TB = a.block_rows / G;
 
+  // Waits behind other warps' tiles, items and repairs, of any number and length, go by the work that
+  // is done meanwhile.  The products' warp, for which the others wait, only looks whether one of them
+  // gave up (with the others' wait 16 packed prompts took 311 to 316 us against 305, so 307 to 311).
+  auto working = [&](uint64_t *b, uint32_t parity) { return mbar_wait_working(b, parity, &bar.work); };
+  auto give_up = [&]() {
+    set_error(a.err, kErrTimeout);
+    *reinterpret_cast<volatile uint32_t *>(&bar.stop) = 1;
+  };
+
   if (threadIdx.x == 0) {
+    bar.work = bar.stop = 0;
     for (int i = 0; i < NU; ++i) {
       mbar_init(&bar.full[i], 1);
       mbar_init(&bar.empty[i], 1);
@@ -238,10 +295,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int kv = 0; kv < 2; ++kv, ++u, at.next()) {
             const int s = at.s;
-            if (u >= NU && !mbar_wait(&bar.empty[s], at.turn ^ 1)) ok = false;
+            if (u >= NU && !working(&bar.empty[s], at.turn ^ 1)) ok = false;
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
-            if (lane == 0) mbar_arrive_expect_tx(&bar.full[s], L::UNIT);
+            if (lane == 0) {
+              *reinterpret_cast<volatile uint32_t *>(&bar.work) = u;
+              mbar_arrive_expect_tx(&bar.full[s], L::UNIT);
+            }
             __syncwarp();
             if (lane < per_tile) {
               // rows behind the pool's end read as zero
@@ -256,7 +316,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (!ok) {
-        if (lane == 0) set_error(a.err, kErrTimeout);
+        if (lane == 0) give_up();
         // what is still on its way lands before the CTA ends
         for (uint32_t i = u > NU ? u - NU : 0; i < u; ++i) mbar_wait(&bar.full[i % NU], (i / NU) & 1);
       }
@@ -271,7 +331,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       uint32_t nq[2] = {0, 0}, np[2] = {0, 0}, nv = 0, n_s = 0;
       RingAt<NU> at;
-      auto wait = [&](uint64_t *b, uint32_t parity) { return __all_sync(0xffffffffu, mbar_wait(b, parity)) != 0; };
+      auto wait = [&](uint64_t *b, uint32_t parity) { return __all_sync(0xffffffffu, mbar_wait_unless(b, parity, &bar.stop)) != 0; };
       while (ok && __all_sync(0xffffffffu, walk.next<kPkvTile>(a, TB, it))) {
         const int halves = __shfl_sync(0xffffffffu, it.ntok * G > 128 ? 2 : 1, 0);
         const int tiles = __shfl_sync(0xffffffffu, it.tb - it.ta, 0);
@@ -392,7 +452,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) {
         if (elect_one()) {
-          set_error(a.err, kErrTimeout);
+          give_up();
           mma_commit(&bar.drain);   // the products in flight end before tensor memory is given back
         }
         mbar_wait(&bar.drain, 0);
@@ -412,7 +472,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int s = at.s;
           // (the ring's own barriers would not do: this warp skips tiles, and the ring
           // may be a whole turn ahead or behind)
-          ok = mbar_wait_for(&bar.v_go, nv++ & 1, kItemLimitNs);
+          ok = working(&bar.v_go, nv++ & 1);
           if (!ok) break;
           uint4 *v = reinterpret_cast<uint4 *>(ring + s * L::UNIT);
           for (int i = tid; i < L::UNIT / 16; i += 64)
@@ -421,7 +481,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive(&bar.v_ok);
         }
       }
-      if (!ok && lane == 0) set_error(a.err, kErrTimeout);
+      if (!ok && lane == 0) give_up();
     }
   } else {
     // ------------------------------------------------------------- softmax
@@ -534,7 +594,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       float m = -INFINITY, sum = 0.f;
       for (int t = it.ta; t < it.tb; ++t) {
         const uint32_t ts = ts0 + (ALONE ? (ns & 1) * 128 : 0);
-        if (!mbar_wait(&bar.s_full[ALONE ? ns & 1 : w], (ALONE ? ns >> 1 : ns) & 1)) {
+        if (!working(&bar.s_full[ALONE ? ns & 1 : w], (ALONE ? ns >> 1 : ns) & 1)) {
           ok = false;
           break;
         }
@@ -600,8 +660,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // first: with two halves S of this tile came behind them; with one it did not, and they
                 // may wait for another warp's p yet.  Those of this tile's first half end next (only
                 // then: a phase further back has the same parity, and would pass for this one).
-                if (ALONE && t > it.ta && !mbar_wait(&bar.pv_half[1], ns & 1)) ok = false;
-                if (h && !mbar_wait(&bar.pv_half[w], (ns - 1) & 1)) ok = false;
+                if (ALONE && t > it.ta && !working(&bar.pv_half[1], ns & 1)) ok = false;
+                if (h && !working(&bar.pv_half[w], (ns - 1) & 1)) ok = false;
                 __syncwarp();
                 tc_fence_after();
 #pragma unroll 1
@@ -625,7 +685,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (SPLIT && h == 0 && t > it.ta && (t - it.ta) % kFold == 0) {
             // the products of the tiles so far (done: S of this one came behind them) go to the
             // sum, and this tile's start anew
-            if (ALONE && !mbar_wait(&bar.pv_half[1], ns & 1)) ok = false;
+            if (ALONE && !working(&bar.pv_half[1], ns & 1)) ok = false;
             __syncwarp();
             tc_fence_after();
 #pragma unroll 1
@@ -651,7 +711,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       PkvItem nx;
       have = next(nx);
       if (have) fetch_q(nx);
-      if (!mbar_wait(&bar.o_full[w], no++ & 1)) {
+      if (!working(&bar.o_full[w], no++ & 1)) {
         ok = false;
         break;
       }
@@ -731,7 +791,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             odd_rows = __ballot_sync(0xffffffffu, odd);
             if (odd_rows) {
               const PkvItem copy = it;   // (its address is taken)
-              redo = hidden_odd_values<HD>(a, copy);
+              redo = hidden_odd_values<HD>(a, copy, &bar.work);
             }
           }
           const uint32_t store = __ballot_sync(0xffffffffu, live && !(redo && odd));
@@ -749,33 +809,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       else emit(std::false_type());
       if (live && po && !(redo && odd)) *reinterpret_cast<float2 *>(pml) = make_float2(m, sum);
       if (redo) {
-        const int seq = a.pass == kPkvPrefix ? min(max(a.group_start[it.b], 0), a.seqs.n_seq - 1) : it.b;
-        for (int k = 0; k < 32; ++k) {
-          const int from = max(__shfl_sync(0xffffffffu, lo, k), (it.t0 + it.ta) * kPkvTile);
-          const int to_e = min(__shfl_sync(0xffffffffu, hi, k), (it.t0 + it.tb) * kPkvTile);
-          const int tk = __shfl_sync(0xffffffffu, tok, k), hd_k = __shfl_sync(0xffffffffu, head, k);
-          const long long po_k = __shfl_sync(0xffffffffu, (long long)(uintptr_t)po, k);
-          const long long pml_k = __shfl_sync(0xffffffffu, (long long)(uintptr_t)pml, k);
-          if (!(odd_rows >> k & 1)) continue;
-          float o[HD / 32], mk, lk;
-          pkv_attend_row<HD>(a.pool, a.seqs.pages + (int64_t)seq * a.seqs.max_page, it.h, a.q,
-                             tk * a.q.token + hd_k * a.q.head, c, from, to_e, o, mk, lk);
-          if (po_k) {
-            float *dst = reinterpret_cast<float *>((uintptr_t)po_k);
-#pragma unroll
-            for (int i = 0; i < HD / 32; ++i) dst[lane * (HD / 32) + i] = o[i];
-            if (lane == 0) *reinterpret_cast<float2 *>((uintptr_t)pml_k) = make_float2(mk, lk);
-          } else {
-            pkv_store<HD / 32>(a.out, tk * a.out.token + hd_k * a.out.head + lane * (HD / 32), o,
-                               lk == 0.f ? 0.f : 1.f / lk);
-          }
-        }
+        const PkvItem copy = it;
+        repair_rows<HD>(a, copy, odd_rows, lo, hi, tok, head, po, pml, &bar.work);
       }
       if (have) put_q();
       tc_fence_before();
       it = nx;
     }
-    if (!ok && lane == 0) set_error(a.err, kErrTimeout);
+    if (!ok && lane == 0) give_up();
   }
   tc_fence_before();
   __syncthreads();

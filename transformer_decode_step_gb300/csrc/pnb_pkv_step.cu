@@ -52,6 +52,7 @@ struct SBars {
   uint64_t full[8], empty[8];
   float2 ml[kWarps][16];
   int bad;
+  uint32_t work;   // changes with rows done again
 };
 
 __device__ __forceinline__ void ldmatrix4(uint32_t addr, uint32_t (&r)[4]) {
@@ -109,6 +110,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     fence_barrier_init();
     bar.bad = 0;
+    bar.work = 0;
   }
   __syncthreads();
   // The own pass runs beside the prefix's, which let it start behind its own wait: the call's
@@ -143,7 +145,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int now = id;
         if (t + 1 < it.tb) id = page_id(t + 1);
         const int s = u % NS;
-        if (u >= NS && !mbar_wait(&bar.empty[s], (u / NS - 1) & 1)) ok = false;
+        if (u >= NS && !mbar_wait_working(&bar.empty[s], (u / NS - 1) & 1, &bar.work)) ok = false;
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         if (lane == 0) mbar_arrive_expect_tx(&bar.full[s], L::STAGE);
@@ -236,7 +238,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (masked) {
         // V rows that no row sees become zero (0 x NaN is NaN), the others are searched
-        // for NaN and infinities
+        // for NaN and infinities (a single token's rows all see the same)
         bool bad = false;
         for (int i = lane; i < 16 * HD / 8; i += 32) {
           const int pos = (i >> 3) & 15;
@@ -249,7 +251,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             bad |= odd(x.x) || odd(x.y) || odd(x.z) || odd(x.w);
           }
         }
-        if (bad) *reinterpret_cast<volatile int *>(&bar.bad) = (int)item;
+        if (bad && it.ntok > 1) *reinterpret_cast<volatile int *>(&bar.bad) = (int)item;
         fence_async_smem();
         __syncwarp();
       }
@@ -345,7 +347,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int from = max(max(it.floor, a.window > 0 ? last - a.window + 1 : 0), (it.t0 + it.ta) * kChunk);
         pkv_attend_row<HD>(a.pool, a.seqs.pages + (int64_t)it.b * a.seqs.max_page, it.h, a.q,
                            tok * a.q.token + head * a.q.head, a.qscale, from, min(last + 1, (it.t0 + it.tb) * kChunk), x,
-                           mr, sr);
+                           mr, sr, &bar.work);
       }
       if (whole && a.pass == kPkvAll) {
         pkv_store<N>(a.out, tok * a.out.token + head * a.out.head + lane * N, x, sr == 0.f ? 0.f : 1.f / sr);
