@@ -77,7 +77,7 @@ enum {
   PNB_DEV_ERR_TIMEOUT = 2, /* a bounded wait inside a kernel expired; results are invalid */
   PNB_DEV_ERR_FULL = 4,    /* pnb_kvq_append, pnb_pkv_append: rows past the capacity were not stored */
   PNB_DEV_ERR_RANGE = 8    /* pnb_kvq_append: a start or count from device memory was out of range;
-                              pnb_pkv_*: a length, count, group or page id was */
+                              pnb_pkv_*: a length, start, group, prefix or page id was */
 };
 
 /* Model dimensions: the config fields of the pages ("Engine Architecture",
@@ -584,10 +584,11 @@ typedef struct pnb_pkv pnb_pkv;
 /* The sequences of a call and its tokens, packed one sequence after another:
    rows [token][head][head_dim] (the `slot` stride of a pnb_rows is not used).
    The tokens of sequence b are start[b] .. start[b + 1] - 1, n of them, and its
-   last n entries: token t of them is entry len[b] - n + t.  Rows from
-   start[n_seq] on belong to no sequence and are left as they are.
-   Lengths, counts and page ids that are out of range reach no memory outside
-   the buffers and set PNB_DEV_ERR_RANGE. */
+   last n entries: token t of them is entry len[b] - n + t.  Rows before
+   start[0] and from start[n_seq] on belong to no sequence and are left as they
+   are.  Lengths, starts, groups, prefixes and page ids that are out of range
+   reach no memory outside the buffers and set PNB_DEV_ERR_RANGE (tokens that
+   pnb_pkv_append cannot store for their sequence's length: PNB_DEV_ERR_FULL). */
 typedef struct {
   int32_t n_seq;              /* 1 .. 1024 */
   int32_t max_page;           /* row stride of the page tables */
@@ -643,8 +644,9 @@ int pnb_pkv_attention(pnb_pkv *c, int32_t layer, const pnb_pkv_batch *b, int32_t
    at most len - n of every sequence of the group: what is said beyond that is
    cut off).  Each group's prefix is read once for all its tokens; batches whose
    page tables have room for less than 256 MB of K and V go sequence by sequence,
-   which is faster for them.  Every sequence has n_tok / n_seq tokens (start_dev
-   NULL).  n_tok <= shared_tok (PNB_E_INVAL). */
+   which is faster for them (and do not look at groups and prefixes).  Every
+   sequence has n_tok / n_seq tokens (start_dev NULL).  n_tok <= shared_tok
+   (PNB_E_INVAL). */
 int pnb_pkv_attention_shared(pnb_pkv *c, int32_t layer, const pnb_pkv_batch *b, int32_t n_group,
                              const int32_t *group_start_dev, const int32_t *prefix_dev, int32_t n_tok,
                              const pnb_rows *q, const pnb_rows *out, int32_t window, pnb_stream stream);

@@ -54,3 +54,79 @@ def test_wide_windows_over_a_shared_prefix(T, window):
     out = torch.full_like(q, 7.0)
     c.kv.attention_shared(0, c.batch(False), _ints(0, 3, 4, 5), _ints(640, 0, 0), q, out, window=window)
     _answers(c, q, out, window)
+
+
+# ------------------------------------------------- what the device's arrays hold
+@pytest.mark.parametrize("n_seq", [3, 40, 700])
+def test_starts_that_are_out_of_range_are_reported(n_seq):
+    c = Case([20 + i % 7 for i in range(n_seq)], 2, 2, 64, 16, seed=83, new=[2] * n_seq)
+    n = 2 * n_seq
+    q = c.queries("fp32")
+    out = torch.zeros_like(q)
+    k = torch.zeros((n, 2, 64), device="cuda")
+    good = c.start_t.clone()
+    b = c.batch()
+
+    def bits(at, value):
+        c.start_t.copy_(good)
+        if at is not None:
+            c.start_t[at] = value
+        c.kv.attention(0, b, q, out)
+        e = c.kv.device_error()
+        c.kv.append(0, b, k, k)
+        assert c.kv.device_error() & ~pnb.PNB_DEV_ERR_FULL == e & ~pnb.PNB_DEV_ERR_FULL
+        return e
+
+    assert bits(None, 0) == 0
+    for at in (0, 1, n_seq // 2, n_seq):
+        assert bits(at, -1) == pnb.PNB_DEV_ERR_RANGE
+        assert bits(at, n + 1) == pnb.PNB_DEV_ERR_RANGE
+    assert bits(1, 5) == pnb.PNB_DEV_ERR_RANGE            # decreases behind it
+    assert bits(n_seq, n - 3) == pnb.PNB_DEV_ERR_RANGE
+    # equal starts and starts behind the first row are none
+    assert bits(1, 0) == 0 and bits(0, 1) == 0 and bits(n_seq, n - 1) == 0
+
+
+def test_rows_before_the_first_sequence_are_left():
+    c = Case([30, 40], 2, 2, 64, 16, seed=84, new=[5, 6])
+    q = c.queries("fp32", tail=4)
+    c.start_t.copy_(_ints(2, 7, 13))
+    b = c.batch()
+    out = torch.full_like(q, 7.0)
+    c.kv.attention(0, b, q, out)
+    assert bool((out[:2] == 7).all()) and bool((out[13:] == 7).all())
+    c.check(out[2:13], q[2:13])
+    k = torch.randn((15, 2, 64), generator=c.gen, device="cuda")
+    rot = torch.full_like(q, 7.0)
+    before = c.kv.pages(0).clone()
+    c.kv.append(0, b, k, k, q=q, q_out=rot)
+    assert bool((rot[:2] == 7).all()) and bool((rot[13:] == 7).all()) and not bool((rot[2:13] == 7).any())
+    e = torch.cat([torch.arange(25, 30), torch.arange(34, 40)]).cuda()
+    ids = c.table.long()[torch.tensor([0] * 5 + [1] * 6, device="cuda"), e // 16]
+    assert torch.equal(c.kv.pages(0)[ids, 1, :, e % 16], k[2:13].to(torch.bfloat16))
+    keep = torch.ones(before.shape[0], 16, dtype=torch.bool, device="cuda")
+    keep[ids, e % 16] = False
+    x, y = (t.view(torch.int16).permute(0, 3, 1, 2, 4)[keep] for t in (c.kv.pages(0), before))
+    assert torch.equal(x, y)
+    assert c.kv.device_error() == 0
+
+
+@pytest.mark.parametrize("wide", [True, False])
+@pytest.mark.parametrize("T", [1, 20])
+def test_groups_that_are_out_of_range_are_reported(T, wide):
+    c = Case([100 + T] * 4, 2, 4, 64, 16, seed=85, new=[T] * 4, prefix=[([0, 1], 64), ([2, 3], 64)], shared_tok=4 * T,
+             max_page=_wide(4, 2, 64, 16) if wide else None)
+    q = c.queries("fp32")
+    out = torch.zeros_like(q)
+    start, prefix = _ints(0, 2, 4), _ints(64, 64)
+    for s, p, bad in (((0, 2, 4), (64, 64), False), ((0, 2, 4), (0, 64), False), ((0, 0, 4), (64, 0), False),
+                      ((0, 2, 4), (64, -1), True), ((0, 5, 4), (64, 64), True), ((1, 2, 4), (64, 64), True),
+                      ((0, 2, 3), (64, 64), True), ((0, 3, 2), (64, 64), True), ((-1, 2, 4), (64, 64), True),
+                      ((0, 2, 5), (64, 64), True)):
+        start.copy_(_ints(*s))
+        prefix.copy_(_ints(*p))
+        c.kv.attention_shared(0, c.batch(False), start, prefix, q, out)
+        if bad and wide:
+            assert c.kv.device_error() == pnb.PNB_DEV_ERR_RANGE, (s, p)
+        else:     # (small batches do not look at groups)
+            c.check(out, q)

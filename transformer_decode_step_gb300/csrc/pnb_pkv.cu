@@ -96,11 +96,11 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) k_pkv_append(const Pk
       len = a.seqs.len[b];
     }
   }
-  bool live = b >= 0;
-  if (live && (tok < t0 || tok - t0 >= n)) {   // `start` decreases
+  // (tokens before the first sequence are no one's, as are any that a `start` that decreases leaves out)
+  const bool live = b >= 0 && tok >= t0 && tok - t0 < n;
+  if (blockIdx.x == 0 && a.seqs.start &&
+      pkv_bad_starts(a.seqs.start, a.seqs.n_seq, -1, -1, a.seqs.n_tok, threadIdx.x, kWarps * 32))
     set_error(a.err, kErrRange);
-    live = false;
-  }
   const int64_t e64 = live ? (int64_t)len - n + (tok - t0) : 0;   // the token's entry
   const int e = (int)e64;
 

@@ -125,6 +125,17 @@ __device__ __forceinline__ void pkv_tokens(const PkvSeqs &s, int b, int &t0, int
   }
 }
 
+// Whether the calling threads (thread i of n) find starts that are out of range or decrease,
+// from `first` (-1: from anywhere) to `last` (-1: to anywhere) in 0 .. most.
+__device__ __forceinline__ bool pkv_bad_starts(const int32_t *start, int count, int first, int last, int most, int i, int n) {
+  bool bad = false;
+  for (; i <= count; i += n) {
+    const int at = start[i], before = i ? start[i - 1] : 0;
+    bad |= at < before || at > most || (i == 0 && first >= 0 && at != first) || (i == count && last >= 0 && at != last);
+  }
+  return bad;
+}
+
 // entries of sequence b, no more than its page table names
 __device__ __forceinline__ int pkv_len(const PkvSeqs &s, int page_log2, int b, int32_t *err) {
   const int n = s.len[b], most = (int)min((int64_t)s.max_page << page_log2, (int64_t)0x7fffffff);

@@ -482,6 +482,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (!ok && lane == 0) give_up();
+      // Starts, groups and prefixes that are out of range are reported by a warp of the last CTA that
+      // has nothing else to do (in the join kernel or in the schedule this took small calls 0.5 us).
+      if (warp == 11 && blockIdx.x == gridDim.x - 1) {
+        bool bad = false;
+        if (a.seqs.start) bad = pkv_bad_starts(a.seqs.start, a.seqs.n_seq, -1, -1, a.seqs.n_tok, lane, 32);
+        if (a.pass == kPkvPrefix) {
+          bad |= pkv_bad_starts(a.group_start, a.n_group, 0, a.seqs.n_seq, a.seqs.n_seq, lane, 32);
+          for (int g = lane; g < a.n_group; g += 32) bad |= a.prefix[g] < 0;
+        }
+        if (bad) set_error(a.err, kErrRange);
+      }
     }
   } else {
     // ------------------------------------------------------------- softmax
