@@ -8,7 +8,7 @@ import pytest
 import torch
 
 import transformer_decode_step_gb300 as pnb
-from test_gpu_paged import Case, _wide
+from test_gpu_paged import DT, U, Case, _near_rotated, _rotate64, _wide
 
 pytestmark = pytest.mark.gpu
 
@@ -130,3 +130,28 @@ def test_groups_that_are_out_of_range_are_reported(T, wide):
             assert c.kv.device_error() == pnb.PNB_DEV_ERR_RANGE, (s, p)
         else:     # (small batches do not look at groups)
             c.check(out, q)
+
+
+# ------------------------------------------------------------------ append
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("n", [1, 23])
+def test_append_in_place_of_a_projection_head_by_head(n, dtype):
+    # [token][head][q, k, v]: the queries' rows lie between the keys' and the values'
+    hd, H = 64, 3
+    c = Case([n + 5], H, 1, hd, 32, seed=86, new=[n], rope_theta=10000.0, rope_neox=True)
+    x = torch.randn((n, H, 3, hd), generator=c.gen, device="cuda").to(DT[dtype])
+    keep = x.clone()
+    q, k, v = x.unbind(2)
+    c.kv.append(0, c.batch(), k, v, q=q)
+    at = torch.arange(5, n + 5, device="cuda")[None]
+    _near_rotated(q, _rotate64(keep[:, :, 0], at, 10000.0, True, [hd // 2]), keep[:, :, 0], 0.0 if dtype == "fp32" else U)
+    assert torch.equal(x[:, :, 1:], keep[:, :, 1:])
+    e = torch.arange(5, n + 5, device="cuda")
+    ids = c.table.long()[0, e // 32]
+    _near_rotated(c.kv.pages(0)[ids, 0, :, e % 32], _rotate64(keep[:, :, 1], at, 10000.0, True, [hd // 2]), keep[:, :, 1], U)
+    assert torch.equal(c.kv.pages(0)[ids, 1, :, e % 32], keep[:, :, 2].to(torch.bfloat16))
+    for q_out in (k, v):
+        with pytest.raises(pnb.PnbError) as err:
+            c.kv.append(0, c.batch(), k, v, q=q, q_out=q_out)
+        assert err.value.code == -1
+    assert c.kv.device_error() == 0

@@ -284,9 +284,12 @@ int pnb_pkv_append(pnb_pkv *c, int32_t layer, const pnb_pkv_batch *b, int32_t n_
   if (q) {
     // the rotated queries lie over no other rows of the call but q's own
     if (!apart(a.q_out, a.q, n_tok, 1, g.n_head, g.head_dim, true)) return PNB_E_INVAL;
-    if (!rows_apart(a.q_out, g.n_head, a.k, g.n_kv_head, n_tok, g.head_dim) ||
-        !rows_apart(a.q_out, g.n_head, a.v, g.n_kv_head, n_tok, g.head_dim))
-      return PNB_E_INVAL;
+    // (k and v of as many heads may also lie between q's heads)
+    auto clear = [&](const DevRows &r) {
+      return rows_apart(a.q_out, g.n_head, r, g.n_kv_head, n_tok, g.head_dim) ||
+             (g.n_head == g.n_kv_head && apart(a.q_out, r, n_tok, 1, g.n_head, g.head_dim, false));
+    };
+    if (!clear(a.k) || !clear(a.v)) return PNB_E_INVAL;
   }
   rc = check_call(c, layer);
   if (rc != PNB_OK) return rc;
