@@ -629,8 +629,9 @@ int pnb_pkv_append(pnb_pkv *c, int32_t layer, const pnb_pkv_batch *b, int32_t n_
    A token with nothing to attend to (i < 0) answers 0.  q and out may differ in
    dtype; out may be q's own rows when they have the same strides and dtype.
    With fp32 on either side queries enter the products with 24 bits and softmax
-   weights with 16 (1e-6 to 4e-6 of the outputs, rms, up to 60k entries); with
-   bf16 on both, all but calls of at most 8 rows (tokens of a sequence x query
+   weights with 16 (1e-6 to 4e-6 of the outputs, rms); with bf16 on both, sums
+   may come out up to 3e-4 of their size too small, however long they are, and
+   all but calls of at most 8 rows (tokens of a sequence x query
    heads of a KV head; 16 at head_dim 64) round the weights to bf16 (2.1e-3 to
    2.4e-3, where the output's own rounding is 1.7e-3).
    Results do not depend on the run: no atomic sums. */

@@ -174,3 +174,38 @@ def test_a_hidden_nan_in_a_long_context_reaches_nobody_else(L, T, hidden):
     assert bool(torch.isnan(got[victim, hidden:, :, 5]).all())
     got[victim, hidden:, :, 5] = want[0, hidden:, :, 5]
     assert float((got - want).abs().max()) <= tol
+
+
+@pytest.mark.parametrize("hd,T,dtype", [(64, 64, "bf16"), (128, 64, "bf16"), (64, 32, "bf16"), (128, 32, "bf16"),
+                                        (64, 2, "fp32"), (128, 2, "fp32"), (64, 4, "fp32"), (128, 32, "fp32")])
+def test_sums_over_a_million_entries_are_not_cut_off(hd, T, dtype):
+    # All entries have the same values, so that they are the answer: the matrix units cut off what they add to a sum,
+    # and with sums that go on and on answers came out 4e-3 (bf16) and 3e-4 (fp32, few rows) too small.
+    c = Same(131072, 160, T, 1, 4, hd, 128, seed=3)
+    c.v = (1.0 + torch.rand((1, 1, hd), generator=c.gen, device="cuda")).to(torch.bfloat16).expand_as(c.v).contiguous()
+    c.store()
+    table = c.table.repeat(1, 8)
+    batch = c.kv.batch(torch.full((160,), 8 * c.L, dtype=torch.int32, device="cuda"), table)
+    q = c.queries(dtype)
+    out = torch.full_like(q, 7.0)
+    c.kv.attention(0, batch, q, out)
+    assert c.kv.device_error() == 0
+    want = c.v[:1].double()
+    if dtype == "bf16":
+        # below a quarter of bf16's half step: at most 512 tiles' 8 additions at 2^-23 each, and the weights' roundings, which
+        # differ from entry to entry (2^-9 / sqrt(2^20))
+        assert torch.equal(out, c.v[:1].expand_as(out))
+    else:
+        # At most 64 additions of the matrix units between new starts are cut off by 2^-23 of a sum that is half there on
+        # the average: 64 x 2^-24.  The sums of weights (2^14 additions, one per 64 entries) and of outputs (2^11) are rounded
+        # either way, by at most 2^-24 of a sum that grows evenly: a deviation of 2^-24 sqrt(n / 9), taken six times for the
+        # thousands of rows, 256 and 90 x 2^-24.  Weights' roundings of 2^-17, over 2^20 entries: 2^-27.
+        assert float((out.double() / want - 1).abs().max()) <= (64 + 256 + 90 + 1) * 2.0 ** -24
+
+
+@pytest.mark.parametrize("dtype,hd,T,L,chance", [("bf16", 64, 64, 90000, 0.02), ("bf16", 128, 64, 90000, 0.02),
+                                                 ("bf16", 64, 32, 150000, 0.01), ("bf16", 128, 32, 150000, 0.01),
+                                                 ("bf16", 128, 2, 20000, 0.1), ("fp32", 128, 2, 20000, 0.1),
+                                                 ("fp32", 64, 4, 20000, 0.1)])
+def test_references_that_move_over_long_sums(dtype, hd, T, L, chance):
+    _moving(dtype, hd, T, 4, chance, True, True, L=L)

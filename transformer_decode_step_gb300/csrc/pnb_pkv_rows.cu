@@ -73,6 +73,11 @@ struct RingAt {
 // matrix unit cuts off what it adds, always towards zero, and over 475 tiles outputs came out
 // 5e-5 too small.
 constexpr int kFold = 4;
+// Without SPLIT, where bf16's own roundings are of 2e-3, only every so many tiles (64k entries: 2.6e-4
+// at most; without, values of mean 1 came out 4e-3 too small over 1M entries and 7e-2 over 16M).
+// The sum over the tiles before then lies in the CTA's partial sums, in global memory: tensor
+// memory has no columns left.
+constexpr int kFoldLong = 512;
 
 template <int HD, bool SPLIT, bool ONE>
 struct RL {
@@ -133,6 +138,32 @@ __device__ __forceinline__ void split8(const float4 &a, const float4 &b, uint4 (
       f[2 * i + 1] -= bf16hi(w[i]);
     }
     part[p] = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
+// Adds a row's outputs in tensor memory to its sum in global memory (with `first`, sets it).
+template <int HD>
+__device__ __noinline__ void fold_long(uint32_t to, float *all, bool first) {
+#pragma unroll 1
+  for (int i = 0; i < HD; i += 32) {
+    float o[32];
+    tmem_ld32_async(to + i, o);
+    tmem_wait_ld();
+    tmem_landed(o);
+#pragma unroll
+    for (int k = 0; k < 32; k += 4) {
+      float4 *p = reinterpret_cast<float4 *>(all + i + k);
+      const float4 x = first ? make_float4(0.f, 0.f, 0.f, 0.f) : *p;
+      *p = make_float4(x.x + o[k], x.y + o[k + 1], x.z + o[k + 2], x.w + o[k + 3]);
+    }
+  }
+}
+template <int HD>
+__device__ __noinline__ void scale_long(float *all, float f) {
+#pragma unroll 1
+  for (int i = 0; i < HD; i += 4) {
+    float4 *p = reinterpret_cast<float4 *>(all + i);
+    *p = make_float4(p->x * f, p->y * f, p->z * f, p->w * f);
   }
 }
 
@@ -372,7 +403,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!ok) break;
             tc_fence_after();
             if (elect_one()) {
-              products_o<HD, SPLIT, 0>(tmem + 256, p, v0 + v.s * (L::UNIT >> 4), SPLIT ? t % kFold == 0 : t == 0);
+              products_o<HD, SPLIT, 0>(tmem + 256, p, v0 + v.s * (L::UNIT >> 4), t % (SPLIT ? kFold : kFoldLong) == 0);
               mma_commit(&bar.pv_half[0]);
             }
             __syncwarp();
@@ -426,7 +457,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after();
             if (elect_one()) {
               products_o<HD, SPLIT, 0>(tmem + 256 + w * 128, tmem + w * 128, v0 + v.s * (L::UNIT >> 4),
-                                      SPLIT ? t % kFold == 0 : t == 0);
+                                      t % (SPLIT ? kFold : kFoldLong) == 0);
               mma_commit(&bar.pv_half[w]);
             }
             __syncwarp();
@@ -603,120 +634,138 @@ __global__ void __launch_bounds__(kThreads, 1)
         lo = max(it.floor, a.window > 0 ? last - a.window + 1 : 0);
       }
       float m = -INFINITY, sum = 0.f;
-      for (int t = it.ta; t < it.tb; ++t) {
-        const uint32_t ts = ts0 + (ALONE ? (ns & 1) * 128 : 0);
-        if (!working(&bar.s_full[ALONE ? ns & 1 : w], (ALONE ? ns >> 1 : ns) & 1)) {
-          ok = false;
-          break;
-        }
-        ++ns;
-        __syncwarp();
-        tc_fence_after();
-        // The row's 128 scores in two halves: the products of the first begin beside the
-        // second one's exponentials.
-        const int e = (it.t0 + t) * kPkvTile;
-        const bool masked = e < it.lo_max || e + kPkvTile > it.hi_min;
-#pragma unroll 1
-        for (int h = 0; h < 2; ++h) {
-          float x[64];
-#pragma unroll
-          for (int i = 0; i < 2; ++i) tmem_ld32_async(ts + 64 * h + 32 * i, x + 32 * i);
-          tmem_wait_ld();
-#pragma unroll
-          for (int i = 0; i < 2; ++i) tmem_landed(x + 32 * i);
-          if (masked) {
-            // columns [from, from + n) of the 64 are this row's
-            const int e2 = e + 64 * h, from = max(lo - e2, 0), n = max(min(hi - e2, 64) - from, 0);
-#pragma unroll
-            for (int i = 0; i < 64; ++i)
-              if ((unsigned)(i - from) >= (unsigned)n) x[i] = -INFINITY;
-          }
-          // No maximum is taken while the reference does: p and its sum tell when it does not,
-          // and fp32 and bf16 hold a p far above 1 as well as one below.  p goes over S, high
-          // parts (and low parts) of 64 entries in 32 columns each.
-          auto exponentials = [&]() {
-            const float ref = m == -INFINITY ? 0.f : m;   // nothing seen yet: every p is 2^-inf
-            const float2 c2 = make_float2(c, c), r2 = make_float2(-ref, -ref);
-            float2 acc[2] = {};
-            uint32_t p[32], low[SPLIT ? 32 : 1];
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              float2 y = ffma2(make_float2(x[2 * i], x[2 * i + 1]), c2, r2);
-              y.x = exp2_approx(y.x);
-              y.y = exp2_approx(y.y);
-              acc[i & 1] = fadd2(acc[i & 1], y);
-              p[i] = pack_bf16(y.x, y.y);
-              if constexpr (SPLIT) low[i] = pack_bf16(y.x - bf16lo(p[i]), y.y - bf16hi(p[i]));
-            }
-            tmem_st32_async(ts + 64 * h, p);
-            if constexpr (SPLIT) tmem_st32_async(ts + 64 * h + 32, low);
-            acc[0] = fadd2(acc[0], acc[1]);
-            return acc[0].x + acc[0].y;
-          };
-          float part = exponentials();
-          if (__any_sync(0xffffffffu, m == -INFINITY || !(part < kLarge))) {
-            float mx[4] = {x[0], x[1], x[2], x[3]};
-#pragma unroll
-            for (int i = 4; i < 64; i += 4)
-#pragma unroll
-              for (int k = 0; k < 4; ++k) mx[k] = fmaxf(mx[k], x[i + k]);
-            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
-            const bool move = top > m && (m == -INFINITY || !(part < kLarge));
-            if (__any_sync(0xffffffffu, move)) {
-              const float f = move ? (m == -INFINITY ? 0.f : exp2_approx(m - top)) : 1.f;
-              if (move) m = top;
-              sum *= f;
-              if (t > it.ta || h) {
-                // Outputs so far go to the new reference.  The products of the tile before end
-                // first: with two halves S of this tile came behind them; with one it did not, and they
-                // may wait for another warp's p yet.  Those of this tile's first half end next (only
-                // then: a phase further back has the same parity, and would pass for this one).
-                if (ALONE && t > it.ta && !working(&bar.pv_half[1], ns & 1)) ok = false;
-                if (h && !working(&bar.pv_half[w], (ns - 1) & 1)) ok = false;
-                __syncwarp();
-                tc_fence_after();
-#pragma unroll 1
-                for (int i = 0; i < (SPLIT && t - it.ta >= kFold ? 2 * HD : HD); i += 32) {
-                  float o[32];
-                  tmem_wait_st();
-                  tmem_ld32_async(to + i, o);
-                  tmem_wait_ld();
-                  tmem_landed(o);
-#pragma unroll
-                  for (int k = 0; k < 32; ++k) o[k] *= f;
-                  tmem_st32_async(to + i, reinterpret_cast<const uint32_t *>(o));
-                }
-              }
-              // p goes over p, and below a sum that starts anew is read back
-              tmem_wait_st();
-              part = exponentials();
-            }
-          }
-          sum += part;
-          if (SPLIT && h == 0 && t > it.ta && (t - it.ta) % kFold == 0) {
-            // the products of the tiles so far (done: S of this one came behind them) go to the
-            // sum, and this tile's start anew
-            if (ALONE && !working(&bar.pv_half[1], ns & 1)) ok = false;
-            __syncwarp();
-            tc_fence_after();
-#pragma unroll 1
-            for (int i = 0; i < HD; i += 32) {
-              float o[32], all[32];
-              tmem_ld32_async(to + i, o);
-              tmem_ld32_async(to + HD + i, all);
-              tmem_wait_ld();
-              tmem_landed(o);
-              tmem_landed(all);
-#pragma unroll
-              for (int k = 0; k < 32; ++k) all[k] = t - it.ta == kFold ? o[k] : all[k] + o[k];
-              tmem_st32_async(to + HD + i, reinterpret_cast<const uint32_t *>(all));
-            }
-          }
-          tmem_wait_st();
-          tc_fence_before();
+      for (int t0 = it.ta; t0 < it.tb && ok; t0 += kFoldLong) {
+        if (!SPLIT && t0 > it.ta) {
+          // The products of the tiles so far go to the sum: with two halves they end before S of the next
+          // tile is there, with one they are waited for.
+          if (!working(&bar.s_full[ALONE ? ns & 1 : w], (ALONE ? ns >> 1 : ns) & 1)) ok = false;
+          if (ALONE && !working(&bar.pv_half[1], (ns - 1) & 1)) ok = false;
+          if (!ok) break;
           __syncwarp();
-          if (lane == 0) mbar_arrive(&bar.p_ready[ALONE ? (ns - 1) & 1 : w][h]);
+          tc_fence_after();
+          fold_long<HD>(to, a.part_o + ((int64_t)(2 * blockIdx.x + (it.ta > 0 ? 0 : 1)) * kPkvBlockRows + r) * HD,
+                        t0 - it.ta == kFoldLong);
+          tc_fence_before();
         }
+        const int t1 = SPLIT ? it.tb : min(it.tb, t0 + kFoldLong);
+        for (int t = t0; t < t1; ++t) {
+          const uint32_t ts = ts0 + (ALONE ? (ns & 1) * 128 : 0);
+          if (!working(&bar.s_full[ALONE ? ns & 1 : w], (ALONE ? ns >> 1 : ns) & 1)) {
+            ok = false;
+            break;
+          }
+          ++ns;
+          __syncwarp();
+          tc_fence_after();
+          // The row's 128 scores in two halves: the products of the first begin beside the
+          // second one's exponentials.
+          const int e = (it.t0 + t) * kPkvTile;
+          const bool masked = e < it.lo_max || e + kPkvTile > it.hi_min;
+#pragma unroll 1
+          for (int h = 0; h < 2; ++h) {
+            float x[64];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) tmem_ld32_async(ts + 64 * h + 32 * i, x + 32 * i);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 2; ++i) tmem_landed(x + 32 * i);
+            if (masked) {
+              // columns [from, from + n) of the 64 are this row's
+              const int e2 = e + 64 * h, from = max(lo - e2, 0), n = max(min(hi - e2, 64) - from, 0);
+#pragma unroll
+              for (int i = 0; i < 64; ++i)
+                if ((unsigned)(i - from) >= (unsigned)n) x[i] = -INFINITY;
+            }
+            // No maximum is taken while the reference does: p and its sum tell when it does not,
+            // and fp32 and bf16 hold a p far above 1 as well as one below.  p goes over S, high
+            // parts (and low parts) of 64 entries in 32 columns each.
+            auto exponentials = [&]() {
+              const float ref = m == -INFINITY ? 0.f : m;   // nothing seen yet: every p is 2^-inf
+              const float2 c2 = make_float2(c, c), r2 = make_float2(-ref, -ref);
+              float2 acc[2] = {};
+              uint32_t p[32], low[SPLIT ? 32 : 1];
+#pragma unroll
+              for (int i = 0; i < 32; ++i) {
+                float2 y = ffma2(make_float2(x[2 * i], x[2 * i + 1]), c2, r2);
+                y.x = exp2_approx(y.x);
+                y.y = exp2_approx(y.y);
+                acc[i & 1] = fadd2(acc[i & 1], y);
+                p[i] = pack_bf16(y.x, y.y);
+                if constexpr (SPLIT) low[i] = pack_bf16(y.x - bf16lo(p[i]), y.y - bf16hi(p[i]));
+              }
+              tmem_st32_async(ts + 64 * h, p);
+              if constexpr (SPLIT) tmem_st32_async(ts + 64 * h + 32, low);
+              acc[0] = fadd2(acc[0], acc[1]);
+              return acc[0].x + acc[0].y;
+            };
+            float part = exponentials();
+            if (__any_sync(0xffffffffu, m == -INFINITY || !(part < kLarge))) {
+              float mx[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+              for (int i = 4; i < 64; i += 4)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) mx[k] = fmaxf(mx[k], x[i + k]);
+              const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
+              const bool move = top > m && (m == -INFINITY || !(part < kLarge));
+              if (__any_sync(0xffffffffu, move)) {
+                const float f = move ? (m == -INFINITY ? 0.f : exp2_approx(m - top)) : 1.f;
+                if (move) m = top;
+                sum *= f;
+                if (!SPLIT && t - it.ta >= kFoldLong && move)
+                  scale_long<HD>(a.part_o + ((int64_t)(2 * blockIdx.x + (it.ta > 0 ? 0 : 1)) * kPkvBlockRows + r) * HD, f);
+                if (t > it.ta || h) {
+                  // Outputs so far go to the new reference.  The products of the tile before end
+                  // first: with two halves S of this tile came behind them; with one it did not, and they
+                  // may wait for another warp's p yet.  Those of this tile's first half end next (only
+                  // then: a phase further back has the same parity, and would pass for this one).
+                  if (ALONE && t > it.ta && !working(&bar.pv_half[1], ns & 1)) ok = false;
+                  if (h && !working(&bar.pv_half[w], (ns - 1) & 1)) ok = false;
+                  __syncwarp();
+                  tc_fence_after();
+#pragma unroll 1
+                  for (int i = 0; i < (SPLIT && t - it.ta >= kFold ? 2 * HD : HD); i += 32) {
+                    float o[32];
+                    tmem_wait_st();
+                    tmem_ld32_async(to + i, o);
+                    tmem_wait_ld();
+                    tmem_landed(o);
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) o[k] *= f;
+                    tmem_st32_async(to + i, reinterpret_cast<const uint32_t *>(o));
+                  }
+                }
+                // p goes over p, and below a sum that starts anew is read back
+                tmem_wait_st();
+                part = exponentials();
+              }
+            }
+            sum += part;
+            if (SPLIT && h == 0 && t > it.ta && (t - it.ta) % kFold == 0) {
+              // the products of the tiles so far (done: S of this one came behind them) go to the
+              // sum, and this tile's start anew
+              if (ALONE && !working(&bar.pv_half[1], ns & 1)) ok = false;
+              __syncwarp();
+              tc_fence_after();
+#pragma unroll 1
+              for (int i = 0; i < HD; i += 32) {
+                float o[32], all[32];
+                tmem_ld32_async(to + i, o);
+                tmem_ld32_async(to + HD + i, all);
+                tmem_wait_ld();
+                tmem_landed(o);
+                tmem_landed(all);
+#pragma unroll
+                for (int k = 0; k < 32; ++k) all[k] = t - it.ta == kFold ? o[k] : all[k] + o[k];
+                tmem_st32_async(to + HD + i, reinterpret_cast<const uint32_t *>(all));
+              }
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar.p_ready[ALONE ? (ns - 1) & 1 : w][h]);
+          }
+        }
+        if (SPLIT) break;   // (whose sums start anew beside the softmax)
       }
       if (!ok) break;
       PkvItem nx;
@@ -777,6 +826,17 @@ __global__ void __launch_bounds__(kThreads, 1)
               tmem_landed(all);
 #pragma unroll
               for (int k = 0; k < 32; ++k) o[k] += all[k];
+            }
+            if (!SPLIT && it.tb - it.ta > kFoldLong) {
+              const float *all = a.part_o + ((int64_t)(2 * blockIdx.x + side) * kPkvBlockRows + r) * HD + i;
+#pragma unroll
+              for (int k = 0; k < 32; k += 4) {
+                const float4 x = *reinterpret_cast<const float4 *>(all + k);
+                o[k] += x.x;
+                o[k + 1] += x.y;
+                o[k + 2] += x.z;
+                o[k + 3] += x.w;
+              }
             }
 #pragma unroll
             for (int k = 0; k < 32; ++k) z = fmaf(o[k], 0.f, z);

@@ -34,6 +34,14 @@ constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32 + 32;
 constexpr int kChunk = kPkvChunk;
 constexpr float kTau = 8.f;
+// The matrix instructions cut off what they add, always towards zero: without new starts values of mean 1
+// came out 1.4e-5 too small over 64k entries and 8e-3 over 16M.  With LONG, in items of more chunks
+// than this, outputs go to fp32 sums in shared memory every so many chunks, half of them a warp's
+// (1.4e-6 at any length).  It is there for page tables with room for so many entries of a sequence, from
+// where on the cut is above 4e-6 (bf16: 5e-5): 8 of 32768 take 173 us with it and 172 without, but 64
+// slots behind a shared 8k prefix 105 against 98, for registers.
+constexpr int kFoldChunks = 128;
+constexpr int64_t kLongF32 = 16384, kLongBf16 = 262144;
 
 template <int HD, int RB>
 struct SL {
@@ -89,7 +97,7 @@ __device__ __forceinline__ void load_q2(const DevRows &q, int64_t at, uint32_t &
   }
 }
 
-template <int HD, int RB>
+template <int HD, int RB, bool LONG>
 __global__ void __launch_bounds__(kThreads, 1)
     k_pkv_step(const __grid_constant__ CUtensorMap kvmap, const __grid_constant__ PkvAttnArgs a) {
   typedef SL<HD, RB> L;
@@ -202,6 +210,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       sum[b] = 0.f;
     }
 
+    // this lane's places of the warp's sums, where they meet at the end
+    auto place = [&](int b, int n) {
+      return reinterpret_cast<float2 *>(merge + ((warp * RB + b) * 8 + g) * L::LD + 2 * c + n * 8);
+    };
+    const bool folds = LONG && it.tb - it.ta > kFoldChunks;
+    if (folds) {
+#pragma unroll 1
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int b = 0; b < RB; ++b) *place(b, n) = make_float2(0.f, 0.f);
+    }
+
     for (int t = it.ta; t < it.tb; ++t, ++u) {
       if ((u & 1) != half) continue;
       const int s = u % NS;
@@ -279,6 +299,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int n = 0; n < NT; ++n)
 #pragma unroll
               for (int i = 0; i < 4; ++i) o[b][n][i] *= f;
+            if (folds) {
+#pragma unroll 1
+              for (int n = 0; n < NT; ++n) *place(b, n) = make_float2(place(b, n)->x * f, place(b, n)->y * f);
+            }
           }
         }
         const float ref = m[b] == -INFINITY ? 0.f : m[b];
@@ -305,6 +329,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar.empty[s]);
+      if (folds && ((t - it.ta) | 1) % kFoldChunks == kFoldChunks - 1) {   // (one of two chunks is the warp's)
+#pragma unroll
+        for (int b = 0; b < RB; ++b)
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            const float2 all = *place(b, n);
+            *place(b, n) = make_float2(all.x + (o[b][n][0] + o[b][n][2]), all.y + (o[b][n][1] + o[b][n][3]));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[b][n][i] = 0.f;
+          }
+      }
     }
 
     // the warps' parts of the item meet
@@ -313,10 +348,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       sum[b] += __shfl_xor_sync(0xffffffffu, sum[b], 1);
       sum[b] += __shfl_xor_sync(0xffffffffu, sum[b], 2);
       if (c == 0) bar.ml[warp][b * 8 + g] = make_float2(m[b], sum[b]);
-      float *p = merge + ((warp * RB + b) * 8 + g) * L::LD + 2 * c;
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
-        *reinterpret_cast<float2 *>(p + n * 8) = make_float2(o[b][n][0] + o[b][n][2], o[b][n][1] + o[b][n][3]);
+      for (int n = 0; n < NT; ++n) {
+        const float2 all = folds ? *place(b, n) : make_float2(0.f, 0.f);
+        *place(b, n) = make_float2(all.x + (o[b][n][0] + o[b][n][2]), all.y + (o[b][n][1] + o[b][n][3]));
+      }
     }
     consumer_sync<kWarps * 32>();
     const bool redo = *reinterpret_cast<volatile int *>(&bar.bad) == (int)item;
@@ -365,7 +401,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (a.pass == kPkvOwn) pdl_wait();
 }
 
-template <int HD, int RB>
+template <int HD, int RB, bool LONG>
 cudaError_t launch_step(const CUtensorMap &map, const PkvAttnArgs &a, cudaStream_t st) {
   cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute attr;
@@ -377,12 +413,22 @@ cudaError_t launch_step(const CUtensorMap &map, const PkvAttnArgs &a, cudaStream
   cfg.stream = st;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_pkv_step<HD, RB>, map, a);
+  return cudaLaunchKernelEx(&cfg, k_pkv_step<HD, RB, LONG>, map, a);
+}
+
+template <int HD, int RB>
+cudaError_t launch_step(const CUtensorMap &map, const PkvAttnArgs &a, cudaStream_t st) {
+  const int64_t room = (int64_t)a.seqs.max_page << a.pool.page_log2;
+  return room > (a.out.dtype == PNB_F32 ? kLongF32 : kLongBf16) ? launch_step<HD, RB, true>(map, a, st)
+                                                                 : launch_step<HD, RB, false>(map, a, st);
 }
 
 template <int HD, int RB>
 cudaError_t prepare() {
-  return cudaFuncSetAttribute(k_pkv_step<HD, RB>, cudaFuncAttributeMaxDynamicSharedMemorySize, SL<HD, RB>::SMEM);
+  const cudaError_t e =
+      cudaFuncSetAttribute(k_pkv_step<HD, RB, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, SL<HD, RB>::SMEM);
+  if (e != cudaSuccess) return e;
+  return cudaFuncSetAttribute(k_pkv_step<HD, RB, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, SL<HD, RB>::SMEM);
 }
 
 }  // namespace
