@@ -155,3 +155,34 @@ def test_append_in_place_of_a_projection_head_by_head(n, dtype):
             c.kv.append(0, c.batch(), k, v, q=q, q_out=q_out)
         assert err.value.code == -1
     assert c.kv.device_error() == 0
+
+
+# ------------------------------------------------ values that only some rows see
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("hd,G,T", [(64, 4, 40), (128, 4, 40), (128, 4, 2), (64, 2, 3), (128, 1, 70)])
+@pytest.mark.parametrize("value", [float("nan"), float("-inf")])
+@pytest.mark.parametrize("bad", [3, 590, 660, 671])
+def test_hidden_values_over_a_shared_prefix(bad, value, hd, G, T, dtype):
+    # windows of 100: only the first sequences see the last of the prefix's 672 entries
+    lens = [672 + T, 676 + T, 700 + T, 768 + T, 1000]
+    c = Case(lens, 2, G, hd, 32, seed=87, new=[T] * 5, prefix=[(list(range(5)), 672)], shared_tok=5 * T,
+             max_page=_wide(5, 2, hd, 32))
+    for b in range(5):
+        c.entries[b][1][bad, :, 7] = value
+        c.store(b)
+    q = c.queries(dtype)
+    out = torch.full_like(q, 7.0)
+    for window in (0, 100):
+        c.kv.attention_shared(0, c.batch(False), _ints(0, 5), _ints(672), q, out, window=window)
+        sees = torch.cat([(bad <= i) & ((bad > i - window) if window else torch.ones_like(i, dtype=torch.bool))
+                          for i in (torch.arange(m - T, m, device="cuda") for m in lens)])
+        assert not bool(torch.isfinite(out[sees][:, :, 7]).any())
+        clean = Case.__new__(Case)
+        clean.__dict__.update(c.__dict__)
+        clean.entries = [tuple(torch.where(torch.isfinite(x), x, torch.zeros_like(x)) for x in e) for e in c.entries]
+        got = out.clone()
+        got[sees] = clean.want(q, window)[0][sees].to(out.dtype)
+        clean.check(got, q, window)
+        others = out[sees].clone()       # the value's own element is all that it reaches
+        others[:, :, 7] = 0
+        assert bool(torch.isfinite(others).all())

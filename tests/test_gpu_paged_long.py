@@ -209,3 +209,26 @@ def test_sums_over_a_million_entries_are_not_cut_off(hd, T, dtype):
                                                  ("fp32", 64, 4, 20000, 0.1)])
 def test_references_that_move_over_long_sums(dtype, hd, T, L, chance):
     _moving(dtype, hd, T, 4, chance, True, True, L=L)
+
+
+@pytest.mark.parametrize("scale", [1.0, 3.0])
+@pytest.mark.parametrize("L", [300, 5000, 40000])
+@pytest.mark.parametrize("hd,T,G", [(64, 64, 4), (64, 32, 4), (128, 64, 4), (128, 32, 4), (64, 4, 4), (64, 2, 4), (128, 2, 4)])
+def test_precision_of_fp32(hd, T, G, L, scale):
+    # Errors' rms against the answers'.  Weights are two bf16 numbers: the second holds what the first's rounding leaves, evenly
+    # spread up to 2^-8, with a rounding evenly spread up to 2^-8 of that: 2^-16 / 3.  Sums of at most 64 additions, each
+    # cut off by 2^-23 of a sum that is half there on the average: 32 x 2^-24 of the weighted mean, whose size they share.
+    # Scores, of size `scale`: 24 additions, cut off by 2^-24 on the average (queries' 24 bits are below that).
+    # All three are of random sign and independent.
+    c = Same(L, 40, T, 8, G, hd, 64, seed=21)
+    batch = c.store()
+    q = c.queries("fp32", scale)
+    seqs = [0, 17, 39]
+    for qq in (q, q.to(torch.bfloat16)):
+        out = torch.full(q.shape, 7.0, device="cuda")
+        c.kv.attention(0, batch, qq, out)
+        assert c.kv.device_error() == 0
+        want, _ = c.want(qq, seqs)
+        err = out.view(c.B, T, c.H, hd)[seqs].double() - want
+        rel = float(err.square().mean().sqrt() / want.square().mean().sqrt())
+        assert rel <= math.sqrt((2.0 ** -16 / 3) ** 2 + (32 * 2.0 ** -24) ** 2 + (24 * 2.0 ** -24 * scale) ** 2), rel
