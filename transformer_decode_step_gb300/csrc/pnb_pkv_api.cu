@@ -104,14 +104,15 @@ int check_tokens(const pnb_pkv *c, const pnb_rows *r, int n_tok, int heads, bool
 // Up to this many rows (tokens x query heads of a KV head) of every sequence go
 // through the kernel for steps (its registers hold 16).  At head_dim 128 a second block of 8
 // rows costs it more than the tcgen05 kernel's empty rows do: 16 rows over 64 sequences of 4096,
-// 64 of 300, 8 of 1000, 1 of 32768, 1 of 200, in bf16: 421, 88, 49, 86, 29 us against 223, 65,
-// 45, 59, 27; in fp32 430, 92, 49, 88, 33 against 287, 90, 53, 72, 37; at head_dim 64 in bf16
-// 166, 47, 30, 41, 18 against 184, 55, 39, 49, 27.
+// 64 of 300, 8 of 1000, 1 of 32768, 1 of 200, in bf16, cold L2: 421, 88, 49, 86, 29 us against 227, 72,
+// 43, 61, 33; in fp32 430, 92, 49, 88, 33 against 291, 90, 53, 74, 37; at head_dim 64 in bf16
+// 166, 47, 31, 41, 21 against 162, 57, 39, 49, 29, in fp32 178, 53, 35, 45, 23 against 215, 74, 47, 57, 35.
 constexpr int kStepRows = 16, kStepRows128 = 8;
 // A batch whose page tables have room for no more than this goes sequence by sequence, shared
 // prefix or not: the pages that sequences share come from L2, at some 11 TB/s, and one kernel
-// and its join take less than two passes.  Single tokens of 32 / 8 heads, head_dim 128, tables
-// of 10, 75, 151, 285, 302, 2416 MB: 15, 21, 29, 41, 45, 224 us against 32, 33, 37, 37, 42, 89.
+// and its join take less than two passes.  Single tokens of 32 / 8 heads, head_dim 128, bf16, cold L2,
+// tables of 10, 75, 151, 285, 302, 2416 MB: 25, 37, 46, 59, 68, 285 us against 44, 50, 52, 52, 67, 99.
+// The host knows the tables' room, not the lengths: a batch of few entries in wide tables takes the second.
 constexpr int64_t kDirectBytes = (int64_t)256 << 20;
 
 int attend(pnb_pkv *c, int32_t layer, const pnb_pkv_batch *b, int32_t n_group, const int32_t *group_start,

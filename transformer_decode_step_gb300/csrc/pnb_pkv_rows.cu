@@ -24,7 +24,7 @@
 // beside each half's O the sum over the tiles before.
 //
 // fp32 on either side (SPLIT): Q enters as three bf16 numbers (24 bits: a score's error is its
-// weight's relative one), P as two (16 bits and the sign: 2^-18 of a weight at most), in 5/2
+// weight's relative one), P as two (16 bits: 2^-17 of a weight at most), in 5/2
 // times the products.  At head_dim 128 that leaves room for the queries of 128 rows: warps 4-7
 // idle, S of two tiles takes both halves' columns, and the products of S run ahead of the softmax
 // (two prompts up to 8191 under a window of 4096: 1468 us one tile at a time, 1146 so).  With ONE
@@ -1121,13 +1121,16 @@ cudaError_t launch_pkv_join(int hd, const PkvAttnArgs &a, int rows, cudaStream_t
                    : launch_pdl(k_pkv_finish<64>, all, block, 0, 1, st, a);
 }
 
-// A tile's time, for the shares of a prefix's and the own pass, and an item's start and end against
-// it.  16k prompt at 2, 4, 6, 8 units: 1625, 1544, 1523, 1538 us; 16 packed prompts 325, 298, 291,
-// 298; fp32, whose tiles take twice as long, 872, 848, 869, 872.  64 slots behind a shared 8k prefix
-// with fp32 at 2600, 3200, 4000 ns: 100, 103, 114 us.
+// A tile's time, for the shares of a prefix's and the own pass (against pkv_step_cost's), and an item's
+// start and end against a tile.  64 slots of up to 1024 entries behind a shared prefix, us at
+//   1200, 1500, 1800, 2200, 2600 ns: 8k, head_dim 128: fp32 110, 104, 95, 98, 104; bf16 96, 84, 86, 88, 90;
+//                                    16k, head_dim 64: fp32 84, 80, 77, 75, 76; bf16 65, 63, 67, 69, 73.
+// 3, 4, 6, 8 units per item: 16k prompt 1677, 1522, 1556, 1560; 16 packed prompts 317, 300, 311, 330, in
+// fp32 692, 642, 656, 693, at head_dim 64 227, 224, 234, 247 and in fp32 351, 345, 365, 386; two prompts under a
+// window, fp32, 1287, 1139, 1141, 1165.
 void pkv_rows_cost(int hd, bool split, int *unit_ns, int *item_units) {
-  *unit_ns = hd == 128 ? (split ? 2600 : 1800) : (split ? 2000 : 900);
-  *item_units = split ? 4 : 6;
+  *unit_ns = hd == 128 ? (split ? 1800 : 1500) : (split ? 2000 : 1500);
+  *item_units = 4;
 }
 
 cudaError_t prepare_pkv_rows(int hd) {
@@ -1142,9 +1145,9 @@ cudaError_t launch_pkv_rows(int hd, const CUtensorMap &map, const PkvAttnArgs &a
   pkv_rows_cost(hd, split, &a.unit_ns, &a.item_units);
   a.heads_inner = a.pass == kPkvAll;
   // No block has more than a half's rows: the kernel of one half, S running ahead.  16 rows over
-  // 64 sequences of 4096 (head_dim 128, bf16) 223 against 238 us, 80 over 16 of 3000 86 against 92;
-  // 32 rows over 64 of 4096 at head_dim 64 in bf16 166 against 184, in fp32 217 against 258.  Beside
-  // a prefix's pass it gains nothing (32 slots of 12 rows behind 30000 entries 118 against 110).
+  // 64 sequences of 4096 (head_dim 128, bf16, cold L2) 227 against 243 us, 80 over 16 of 3000 92 against
+  // 100; 32 rows over 64 of 4096 at head_dim 64 in bf16 164 against 182, in fp32 215 against 258.  Beside
+  // a prefix's pass it loses (32 slots of 12 rows behind 30000 entries 132 against 114).
   const int64_t tokens = a.seqs.each ? a.seqs.each : a.seqs.n_tok;
   const bool one = a.pass == kPkvAll && tokens * (a.n_head / a.pool.n_kv) <= 128;
   if (hd == 128) return split ? launch_halves<128, true>(one, map, a, st) : launch_halves<128, false>(one, map, a, st);

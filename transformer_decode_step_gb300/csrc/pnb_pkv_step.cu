@@ -17,7 +17,7 @@
 // end in shared memory, and those of items that CTAs share in the join kernel.
 //
 // Single tokens of 64 sequences of 4096 entries (32 / 8 heads, head_dim 128, 1.07 GB, L2
-// cold) take 195 us, 5.5 TB/s; 8 of 32768 188 us, 5.7; one of 32768 51 us, 2.6: bytes, and
+// cold) take 194 us, 5.5 TB/s; 8 of 32768 188 us, 5.7; one of 32768 53 us, 2.5: bytes, and
 // for few of them the start (schedule, lengths, page ids and first chunk in turn) and the join.
 #include <cuda_bf16.h>
 #include <math.h>
@@ -439,7 +439,9 @@ cudaError_t prepare_pkv_step(int hd) {
   return prepare<64, 2>();
 }
 
-// a chunk at the GPU's copy rate, shared out over its SMs
+// A chunk at the GPU's copy rate, shared out over its SMs.  64 slots behind a shared prefix (as at
+// pkv_rows_cost) at 350, 500, 700, 1000 ns: head_dim 128 fp32 115, 104, 95, 108, bf16 94, 86, 84, 102; head_dim 64
+// fp32 75, 86, 90, 100, bf16 63, 71, 74, 86.
 void pkv_step_cost(int hd, int *unit_ns, int *item_units) {
   *unit_ns = hd == 128 ? 700 : 350;
   *item_units = 4;
