@@ -631,9 +631,11 @@ int pnb_pkv_append(pnb_pkv *c, int32_t layer, const pnb_pkv_batch *b, int32_t n_
    With fp32 on either side queries enter the products with 24 bits and softmax
    weights with 16 (1e-6 to 4e-6 of the outputs, rms); with bf16 on both, sums
    may come out up to 3e-4 of their size too small, however long they are, and
-   all but calls of at most 8 rows (tokens of a sequence x query
-   heads of a KV head; 16 at head_dim 64) round the weights to bf16 (2.1e-3 to
-   2.4e-3, where the output's own rounding is 1.7e-3).
+   all but calls of at most 8 rows (tokens of a sequence x query heads of a KV
+   head; 16 at head_dim 64) round the weights to bf16 (2.1e-3 to 2.4e-3, where
+   the output's own rounding is 1.7e-3).  Scores may be of any finite size.
+   Weights are divided by their sum at the end: values above 1e28 can overflow.
+   An infinity among the values reaches its tokens as infinity or as NaN.
    Results do not depend on the run: no atomic sums. */
 int pnb_pkv_attention(pnb_pkv *c, int32_t layer, const pnb_pkv_batch *b, int32_t n_tok, const pnb_rows *q,
                       const pnb_rows *out, int32_t window, pnb_stream stream);

@@ -186,3 +186,41 @@ def test_hidden_values_over_a_shared_prefix(bad, value, hd, G, T, dtype):
         others = out[sees].clone()       # the value's own element is all that it reaches
         others[:, :, 7] = 0
         assert bool(torch.isfinite(others).all())
+
+
+# ------------------------------------------------------------------ scores
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("hd,T,G", [(128, 40, 4), (64, 80, 4), (64, 20, 4), (128, 90, 1), (128, 1, 4), (64, 3, 4)])
+@pytest.mark.parametrize("size", [6, 8, 9, 10, 12, 16, 24, 32])
+def test_answers_at_any_finite_scores(size, hd, T, G, dtype):
+    # Scores of 10^size apart by as much: an entry has all of a row's weight.  Where two are near enough to be told
+    # apart by less than the products' rounding (hd + 3 of 2^-24 of the sum of their sizes, in either), either may.
+    c = Case([900, 333], 2, G, hd, 32, seed=88, new=[T, T])
+    for negative in (False, True):
+        q = c.queries(dtype, 10.0 ** size)
+        if negative:      # all scores far below 0
+            for b in range(2):
+                c.entries[b][0].copy_(c.entries[b][0].abs())
+                c.store(b)
+            q = -q.abs()
+        out = torch.full_like(q, 7.0)
+        c.kv.attention(0, c.batch(False), q, out)
+        assert bool(torch.isfinite(out).all())
+        for b in range(2):
+            k, v = (x.double().transpose(0, 1) for x in c.entries[b])
+            rows = q[c.starts[b]:c.starts[b + 1]].double().unflatten(1, (2, G))
+            s = torch.einsum("tkgd,kmd->tkgm", rows, k) / math.sqrt(hd)
+            near = torch.einsum("tkgd,kmd->tkgm", rows.abs(), k.abs()) / math.sqrt(hd) * (hd + 3) * 2.0 ** -23
+            m = c.lens[b]
+            see = torch.arange(m, device="cuda") <= torch.arange(m - T, m, device="cuda")[:, None]
+            s = s.masked_fill(~see[:, None, None], -math.inf)
+            first, at = s.max(-1, keepdim=True)
+            # (30: what is left of e^-30 of a weight is below every rounding)
+            clear = ((s + near + 30 < first - near.gather(-1, at)).sum(-1) == m - 1)
+            want = torch.gather(v[None, :, None].expand(T, -1, G, -1, -1), 3, at[..., None].expand(-1, -1, -1, 1, hd))[..., 0, :]
+            got = out[c.starts[b]:c.starts[b + 1]].double().unflatten(1, (2, G))
+            assert float(clear.double().mean()) > 0.5
+            # the weight is off by bf16's half step, or 2^-16 with a second number, and the answer is rounded
+            tol = 2.0 ** -15 if dtype == "fp32" else 2 * U
+            assert float(((got - want).abs() * clear[..., None]).max()) <= tol * float(v.abs().max())
+    assert c.kv.device_error() == 0

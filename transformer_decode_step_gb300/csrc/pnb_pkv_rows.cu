@@ -19,7 +19,7 @@
 //   warps 10, 11    V rows behind a sequence's last entry become zero (0 x NaN is NaN).
 // A NaN or an infinity among a sequence's own values reaches, through tiles that a block's
 // rows see only in part, rows that do not attend to it: a row whose output is not finite
-// is done again by itself where such a value lies.
+// is done again by itself where such a value lies, and so is one of scores above 2^26.
 // Tensor memory (512 columns): S of both halves (128 each), O of both halves, with SPLIT
 // beside each half's O the sum over the tiles before.
 //
@@ -53,6 +53,9 @@ extern __shared__ __align__(1024) uint8_t r_smem[];
 constexpr int kThreads = 384;
 constexpr int kSoftWarps = 8;
 constexpr float kLarge = 65536.f;   // a sum of 64 p that moves the reference
+// A reference that is rounded by many powers of two puts p, exact products less the reference,
+// out of any range: such rows are done again by themselves.
+constexpr float kFar = 67108864.f;
 // registers per thread: 384 x 168 at launch = 256 x 208 + 128 x 88
 constexpr int kRegsSoft = 208, kRegsRest = 88;
 
@@ -634,6 +637,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         lo = max(it.floor, a.window > 0 ? last - a.window + 1 : 0);
       }
       float m = -INFINITY, sum = 0.f;
+      bool far = false;
       for (int t0 = it.ta; t0 < it.tb && ok; t0 += kFoldLong) {
         if (!SPLIT && t0 > it.ta) {
           // The products of the tiles so far go to the sum: with two halves they end before S of the next
@@ -710,6 +714,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (__any_sync(0xffffffffu, move)) {
                 const float f = move ? (m == -INFINITY ? 0.f : exp2_approx(m - top)) : 1.f;
                 if (move) m = top;
+                far |= move && fabsf(top) >= kFar;
                 sum *= f;
                 if (!SPLIT && t - it.ta >= kFoldLong && move)
                   scale_long<HD>(a.part_o + ((int64_t)(2 * blockIdx.x + (it.ta > 0 ? 0 : 1)) * kPkvBlockRows + r) * HD, f);
@@ -858,11 +863,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
           }
           if (pass == 0) {
-            odd = live && z != 0.f;
+            odd = live && (z != 0.f || far);
             odd_rows = __ballot_sync(0xffffffffu, odd);
             if (odd_rows) {
               const PkvItem copy = it;   // (its address is taken)
-              redo = hidden_odd_values<HD>(a, copy, &bar.work);
+              redo = __any_sync(0xffffffffu, far) || hidden_odd_values<HD>(a, copy, &bar.work);
             }
           }
           const uint32_t store = __ballot_sync(0xffffffffu, live && !(redo && odd));
