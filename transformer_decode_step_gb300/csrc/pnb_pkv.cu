@@ -8,7 +8,7 @@
 // at most 2^-24 of the turn, whatever the position.  Bound by bytes: each row is
 // read and written once.
 //
-// An 8k MHA prompt (32 heads, head_dim 128, bf16, 403 MB) takes 68 us, 5.9 TB/s (88 % of a
+// An 8k MHA prompt (32 heads, head_dim 128, bf16, 403 MB) takes 68.5 us, 5.9 TB/s (88 % of a
 // plain copy), its warps waiting for loads; 64 single tokens 11 us with the host's part, 7
 // without: lengths, starts and page ids, then rows, in turn.
 #include <cuda_bf16.h>

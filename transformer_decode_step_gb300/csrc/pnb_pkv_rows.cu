@@ -27,14 +27,15 @@
 // weight's relative one), P as two (16 bits: 2^-17 of a weight at most), in 5/2
 // times the products.  At head_dim 128 that leaves room for the queries of 128 rows: warps 4-7
 // idle, S of two tiles takes both halves' columns, and the products of S run ahead of the softmax
-// (two prompts up to 8191 under a window of 4096: 1468 us one tile at a time, 1146 so).  With ONE
+// (two prompts up to 8191 under a window of 4096: 1468 us one tile at a time, 1149 so).  With ONE
 // the same is done for calls whose blocks all have at most 128 rows.
 //
-// Bound by the tensor rate and, beside it, by the softmax: a tile's S and O take 2048 cycles for
-// the two halves at head_dim 128, the exponentials, conversions and sums of 64 scores 367 cycles
-// of a scheduler (654 for two warps).  A 16k prompt (32 / 8 heads, head_dim 128, bf16) takes
-// 1558 us, 1.41 PFLOP/s or 71 % of cuBLAS's bf16 rate on the same part; 512 tokens behind 60k
-// entries 369 us, 69 %; DRAM is idle (2 to 12 %), K and V come from L2.
+// Bound by the hand-over between softmax and products: a tile's S and O take 2048 cycles for the two
+// halves at head_dim 128, the exponentials, conversions and sums of 64 scores 367 cycles of a
+// scheduler, 654 with both halves' warps on it, so that 128 scores of one half (1308) outlast the
+// other's products (1024).  A 16k prompt (32 / 8 heads, head_dim 128, bf16) takes 1565 us, 1.41 PFLOP/s
+// or 72 % of cuBLAS's bf16 rate on the same part; 512 tokens behind 60k entries 372 us, 70 %; DRAM is
+// idle (2 to 12 %), K and V come from L2.
 // Not kept: two threads per row (16 softmax warps meet at a barrier per tile: 2078 against 1661),
 // an issuing thread per half (2145), a warp that serves whichever half is ready (2077).
 #include <cuda_bf16.h>
