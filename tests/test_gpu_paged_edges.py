@@ -224,3 +224,35 @@ def test_answers_at_any_finite_scores(size, hd, T, G, dtype):
             tol = 2.0 ** -15 if dtype == "fp32" else 2 * U
             assert float(((got - want).abs() * clear[..., None]).max()) <= tol * float(v.abs().max())
     assert c.kv.device_error() == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("hd,G,T,L", [(64, 4, 90, 300), (128, 4, 90, 300), (128, 2, 3, 700), (128, 4, 30, 5000)])
+def test_rows_done_again_in_place(hd, G, T, L, dtype):
+    # answers over the queries, where rows have a value that others of their tile do not see, or scores beyond any range
+    c = Case([L, 40], 2, G, hd, 32, seed=89, new=[T, T], n_layer=2)
+    c.kv.pages(1).copy_(c.kv.pages(0))
+    q = c.queries(dtype)
+    q[1::7] *= 1e12
+    for b in range(2):
+        c.entries[b][1][c.lens[b] - 2, :, 3] = float("nan")
+        c.store(b)
+    apart = torch.full_like(q, 7.0)
+    c.kv.attention(0, c.batch(), q, apart)
+    over = q.clone()
+    c.kv.attention(0, c.batch(), over, over)
+    assert torch.equal(apart.view(torch.int32 if dtype == "fp32" else torch.int16),
+                       over.view(torch.int32 if dtype == "fp32" else torch.int16))
+    # without the NaN, what does not attend to it is the same
+    clean = torch.full_like(q, 7.0)
+    c.kv.attention(1, c.batch(), q, clean)
+    assert bool(torch.isfinite(clean).all())
+    for b in range(2):
+        rows = slice(c.starts[b], c.starts[b + 1] - 2)
+        near = (apart[rows].double() - clean[rows].double()).abs()
+        # (the same roundings as in test_gpu_paged.py, twice: weights' and answers')
+        V = float(torch.nan_to_num(c.entries[b][1].float()).abs().max())
+        calm = torch.arange(c.starts[b], c.starts[b + 1] - 2, device="cuda") % 7 != 1
+        assert float(near[calm].max()) <= 2 * 2 * (2 * U if dtype == "bf16" else 2.0 ** -15) * V
+        assert bool(torch.isnan(apart[c.starts[b + 1] - 2:c.starts[b + 1], :, 3]).all())
+    assert c.kv.device_error() == 0
